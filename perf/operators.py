@@ -255,7 +255,7 @@ def _plain_scan(s):
     h = _prefix(carry, b)
     out = {"h": h.to(dt), "h_last": h[:, -1].clone()}
     if case["train"]:
-        dh = s["dh"].float()
+        dh = s["dh"].float().clone()
         dh[:, -1] += s["dh_last"]
         # total gradient of h_t: dh_t + carry_(t+1) times that of h_(t+1)
         after = torch.cat((carry[:, 1:], torch.zeros_like(carry[:, :1])), 1)
@@ -292,13 +292,14 @@ def _plain_product(s):
     z = (s["a"].float() @ s["w"]) * s["row_scale"][:, None] * s["col_scale"]
     if case["bias"]:
         z = z + s["bias"]
-    y, slope = _plain_act(z, case["act"])
+    y, _ = _plain_act(z, case["act"])
     if case["residual"]:
         y = y + s["residual"].float()
     out = {"out": y.to(dt)}
     if case["train"]:
-        dz = s["dy"].float() * slope
+        # the gradient is taken at the saved pre-activation, in the type it is kept in
         out["pre"] = z.to(dt)
+        dz = s["dy"].float() * _plain_act(out["pre"].float(), case["act"])[1]
         out["dz"] = dz.to(dt)
         if case["bias"]:
             out["dbias"] = dz.sum(0)
@@ -414,33 +415,36 @@ def _exact_scan(s):
     return out
 
 
+def _exact_act(z, act):
+    """act(z) and its derivative."""
+    zero = torch.zeros_like(z)
+    if act == "none":
+        return z, zero + 1
+    if act == "relu":
+        return torch.maximum(z, zero), torch.where(z > 0, 1.0, zero)
+    if act == "relu2":
+        return torch.maximum(z, zero) ** 2, 2 * torch.maximum(z, zero)
+    if act == "silu":
+        sg = 1 / (1 + torch.exp(-z))
+        return z * sg, sg + z * sg * (1 - sg)
+    # 0.5 (1 + tanh u) = 1 / (1 + exp(-2 u))
+    k = 2 * math.sqrt(2 / math.pi)
+    sg = 1 / (1 + torch.exp(-k * (z + 0.044715 * z ** 3)))
+    return z * sg, sg + z * sg * (1 - sg) * k * (1 + 0.134145 * z ** 2)
+
+
 def _exact_product(s):
     case = s["case"]
     z = torch.matmul(s["a"].double(), s["w"].double())
     z = z * s["row_scale"].double()[:, None] * s["col_scale"].double()[None, :]
     if case["bias"]:
         z += s["bias"].double()
-    act = case["act"]
-    zero = torch.zeros_like(z)
-    if act == "none":
-        y, slope = z, zero + 1
-    elif act == "relu":
-        y, slope = torch.maximum(z, zero), torch.where(z > 0, 1.0, zero)
-    elif act == "relu2":
-        y, slope = torch.maximum(z, zero) ** 2, 2 * torch.maximum(z, zero)
-    elif act == "silu":
-        sg = 1 / (1 + torch.exp(-z))
-        y, slope = z * sg, sg + z * sg * (1 - sg)
-    else:
-        # 0.5 (1 + tanh u) = 1 / (1 + exp(-2 u))
-        k = 2 * math.sqrt(2 / math.pi)
-        sg = 1 / (1 + torch.exp(-k * (z + 0.044715 * z ** 3)))
-        y, slope = z * sg, sg + z * sg * (1 - sg) * k * (1 + 0.134145 * z ** 2)
+    y = _exact_act(z, case["act"])[0]
     if case["residual"]:
         y = y + s["residual"].double()
     out = {"out": y}
     if case["train"]:
-        dz = s["dy"].double() * slope
+        dz = s["dy"].double() * _exact_act(z.to(DTYPES[case["dtype"]]).double(), case["act"])[1]
         out["pre"], out["dz"] = z, dz
         if case["bias"]:
             out["dbias"] = dz.sum(0)
