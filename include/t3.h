@@ -265,6 +265,142 @@ int t3_gemm_bwd_dw_scaled_noalloc(const int8_t* A, const int8_t* dY, void* dW, i
                                   int64_t N, int64_t K, const float* row_scale,
                                   const float* col_scale, int out_kind, t3_stream_t stream);
 
+/*
+ * ---------------------------------------------------------------------------
+ * The operators around the products of a ternary layer: the norm that feeds
+ * them, the recurrence between them, and the product with its epilogue.  The
+ * pages have no counterpart; each formula stands with its declaration.
+ *
+ * Element types of activations (`dtype`): T3_OUT_F32 (float) or T3_OUT_BF16.
+ * Gains, biases, scales, statistics and states are float.  Arithmetic is
+ * float, with one rounding per output element.  Results do not change from call
+ * to call (no atomics; sums are added in a fixed order).
+ *
+ * A matrix [rows][cols] with a stride `ld*` (in elements) has its row r at
+ * base + r * ld*; an output's stride is at least its columns, an input's may be
+ * anything from 0 up.  Without a stride a matrix is dense.  Rows whose base
+ * and stride are multiples of 16 bytes go fastest; any others are taken too.
+ * Outputs must not overlap inputs or each other except where a call says so.
+ * All of these calls are asynchronous on `stream`, take device pointers
+ * and allocate nothing.
+ */
+
+/*
+ * t3_rmsnorm_quant -- residual add, root-mean-square norm and int8 rows, one
+ * pass over each row:
+ *   s = x + residual, rounded to `dtype` (s = x when residual is NULL),
+ *   rstd[r] = 1 / sqrt(mean_c(s^2) + eps),   y = s * rstd[r] * gamma[c],
+ *   row_scale[r] = max_c |y| / 127,
+ *   q = rint(u * (127 / max_c |u|)) with u = s * gamma (a float product), ties
+ *   to even, clamped to [-127, 127]; y / row_scale up to rounding.
+ * q [rows][cols] (dense) and row_scale are what the products take.  gamma [cols]
+ * NULL stands for ones.  sum_out (stride lds) receives s, the residual stream, and may be
+ * x's or residual's buffer with the same stride; rstd is kept for the
+ * gradient; either may be NULL.  A row of zeros gives q = 0 and row_scale = 0.  A row
+ * with an element of u that is not finite, or whose squares overflow a float
+ * sum, gets row_scale = NaN and q = 0, so that whatever is computed from it shows it.
+ * T3_EINVAL: negative sizes or strides, lds < cols, a null x, q or row_scale
+ * with a non-empty shape, eps not a positive finite float, an unknown dtype.
+ * rows = 0 is a no-op; cols = 0 writes row_scale = 0 and rstd = 1 / sqrt(eps).
+ */
+int t3_rmsnorm_quant(const void* x, int64_t ldx, const void* residual, int64_t ldr,
+                     const float* gamma, float eps, int8_t* q, float* row_scale, float* rstd,
+                     void* sum_out, int64_t lds, int64_t rows, int64_t cols, int dtype,
+                     t3_stream_t stream);
+
+/*
+ * t3_rmsnorm_bwd -- the gradient of t3_rmsnorm_quant with the rounding to int8
+ * passed straight through.  dy is the gradient of y, dsum (may be NULL) that of s
+ * itself (the residual stream):
+ *   n = dy * gamma,
+ *   dx = rstd * (n - s * rstd^2 * mean_c(n * s)) + dsum,
+ *   dgamma[c] = sum_r dy * s * rstd          (skipped when dgamma is NULL).
+ * dx is the gradient of x and of residual alike.  s and rstd are the forward's.
+ * dx may be dy's or dsum's buffer with the same stride.  workspace:
+ * DEVICE floats, at least t3_colsum_workspace(rows, cols) of them, needed
+ * (not zeroed) when dgamma is given.  rows = 0 writes dgamma = 0.
+ */
+int t3_rmsnorm_bwd(const void* dy, int64_t lddy, const void* s, int64_t lds, const float* rstd,
+                   const float* gamma, const void* dsum, int64_t lddsum, void* dx, int64_t lddx,
+                   float* dgamma, int64_t rows, int64_t cols, int dtype, float* workspace,
+                   t3_stream_t stream);
+
+/* Floats of workspace the column sums over [rows][cols] need (0 for empty or
+ * invalid sizes); the same on every device. */
+int64_t t3_colsum_workspace(int64_t rows, int64_t cols);
+
+/*
+ * t3_gated_scan_fwd -- the gated linear recurrence of `batch` sequences of
+ * `length` tokens and `width` channels, element by element:
+ *   a_t = sigmoid(gate_t),   h_t = a_t * h'_{t-1} + (1 - a_t) * cand_t,
+ *   h'_{t-1} = h_{t-1}, or 0 where resets[b][t] is not 0 (a document starts);
+ *   h_{-1} = h0 (NULL: zeros).
+ * gate, cand, h: token t of sequence b is row b * length + t of a matrix with
+ * `width` columns and the given stride.  h0, h_last float [batch][width]; resets
+ * uint8 [batch][length] or NULL.  h_last (may be NULL, may be h0's buffer) receives the
+ * float state after the last token, so single tokens (length = 1) advance
+ * a state in place.  A token whose 1 - a_t is exactly 0 (gate = +inf, or one
+ * beyond the float range of sigmoid) leaves the state as it is whatever cand
+ * holds, NaN included.  length = 0 copies h0 to h_last.
+ * T3_EINVAL: negative sizes or strides, sizes above 2^31 - 1, ldh < width, a
+ * null gate, cand or h with a non-empty shape, an unknown dtype.
+ */
+int t3_gated_scan_fwd(const void* gate, int64_t ldg, const void* cand, int64_t ldc,
+                      const float* h0, const uint8_t* resets, void* h, int64_t ldh, float* h_last,
+                      int64_t batch, int64_t length, int64_t width, int dtype, t3_stream_t stream);
+
+/*
+ * t3_gated_scan_bwd -- the gradient of t3_gated_scan_fwd.  dh is the gradient
+ * of h, dh_last (may be NULL) that of h_last; h is the forward's output:
+ *   G_t = dh_t + a_{t+1} G_{t+1} (without the second term where t + 1 resets;
+ *         dh_last joins at the last token),
+ *   dcand_t = (1 - a_t) G_t,  dgate_t = G_t (h'_{t-1} - cand_t) a_t (1 - a_t),
+ *   dh0 = a_0 G_0 (0 where token 0 resets; dh0 may be NULL).
+ * dgate and dcand take strides as gate and cand do; a gate whose sigmoid is
+ * exactly 0 or 1 gets dgate = 0.  length = 0 copies dh_last (or zeros) to dh0.
+ */
+int t3_gated_scan_bwd(const void* gate, int64_t ldg, const void* cand, int64_t ldc, const void* h,
+                      int64_t ldh, const void* dh, int64_t lddh, const float* h0,
+                      const uint8_t* resets, const float* dh_last, void* dgate, int64_t lddg,
+                      void* dcand, int64_t lddc, float* dh0, int64_t batch, int64_t length,
+                      int64_t width, int dtype, t3_stream_t stream);
+
+/* Activations: T3_ACT_RELU2 is max(z, 0)^2, T3_ACT_SILU z sigmoid(z), T3_ACT_GELU
+ * the tanh form z (1 + tanh(sqrt(2/pi) (z + 0.044715 z^3))) / 2. */
+enum { T3_ACT_NONE = 0, T3_ACT_RELU = 1, T3_ACT_RELU2 = 2, T3_ACT_SILU = 3, T3_ACT_GELU = 4 };
+
+/*
+ * t3_gemm_fwd_act -- the forward product with the rest of a layer in its
+ * epilogue.  For the exact int32 x = A . W of t3_gemm_fwd:
+ *   z = (x * row_scale[m]) * col_scale[n] + bias[n],
+ *   C = act(z) + residual,   pre = z.
+ * row_scale [M], col_scale [N], bias [N] (float), residual [M][N] and pre
+ * [M][N] (the output's type) may each be NULL: ones, ones, zeros, zeros, not
+ * written.  pre is what t3_act_bwd takes.  out_kind: T3_OUT_F32 or T3_OUT_BF16.  K = 0
+ * takes x = 0.  workspace: DEVICE int32 [M][N], as in t3_gemm_fwd_scaled:
+ * needed for T3_OUT_BF16 where the product cannot end in this epilogue (M > 32
+ * with operands or outputs whose rows are not 16-byte aligned, K > 65536, or a
+ * small product); a caller without one gets T3_EINVAL there.  Sizes and
+ * overflow rules are those of t3_gemm_fwd_scaled.
+ */
+int t3_gemm_fwd_act(const int8_t* A, const uint8_t* Wp, void* C, int64_t M, int64_t N, int64_t K,
+                    const float* row_scale, const float* col_scale, const float* bias, int act,
+                    const void* residual, void* pre, int out_kind, int32_t* workspace,
+                    t3_stream_t stream);
+
+/*
+ * t3_act_bwd -- the gradient of that epilogue: for dy, the gradient of C, and
+ * z, the forward's pre, both dense [rows][cols] of `dtype`:
+ *   dz = dy * act'(z),   dbias[c] = sum_r dz   (before dz is rounded).
+ * dz (may be dy's buffer) or dbias may be NULL; z may be NULL for T3_ACT_NONE.
+ * dz is what t3_quantize_rows_bf16 and the backward products take; the
+ * residual's gradient is dy itself.  workspace: at least
+ * t3_colsum_workspace(rows, cols) floats when dbias is given.  rows = 0
+ * writes dbias = 0.
+ */
+int t3_act_bwd(const void* dy, const void* z, int act, void* dz, float* dbias, int64_t rows,
+               int64_t cols, int dtype, float* workspace, t3_stream_t stream);
+
 /* A static, human-readable name for a status code (never NULL). */
 const char* t3_status_string(int status);
 

@@ -16,6 +16,12 @@ Function names follow the C ABI:
   t3_dequant_i32(x, kind, row_scale, col_scale, out=None)   scaled float/bf16 output
   t3_gemm_fwd_scaled / t3_gemm_bwd_dx_scaled / t3_gemm_bwd_dw_scaled
                                            the products with that output
+  t3_rmsnorm_quant(x, gamma, residual)     residual add, norm, int8 rows with scales
+  t3_rmsnorm_bwd(dy, s, rstd, gamma)       its gradient
+  t3_gated_scan_fwd(gate, cand, h0)        the gated linear recurrence (sequences, tokens)
+  t3_gated_scan_bwd(gate, cand, h, dh)     its gradient
+  t3_gemm_fwd_act(A, Wp, bias=, act=)      the forward with bias, activation, residual
+  t3_act_bwd(dy, z, act)                   that epilogue's gradient
 """
 from __future__ import annotations
 
@@ -32,6 +38,7 @@ HEADER = os.path.join(os.path.dirname(_PKG), "include", "t3.h")
 
 T3_OK, T3_EINVAL, T3_EVALUE, T3_EOVERFLOW, T3_ECUDA, T3_ETIMEOUT, T3_EDEVICE = 0, -1, -2, -3, -4, -5, -6
 T3_OUT_F32, T3_OUT_BF16, T3_OUT_F32_ADD = 0, 1, 2
+T3_ACT_NONE, T3_ACT_RELU, T3_ACT_RELU2, T3_ACT_SILU, T3_ACT_GELU = 0, 1, 2, 3, 4
 
 _lock = threading.Lock()
 _lib = None
@@ -88,6 +95,20 @@ def load():
         lib.t3_selftest_wait_timeout.restype = ctypes.c_int
         lib.t3_set_small_product_limit.argtypes = [i64]
         lib.t3_set_small_product_limit.restype = i64
+        i32 = ctypes.c_int
+        for name, types in (
+                ("t3_rmsnorm_quant", [p, i64, p, i64, p, ctypes.c_float, p, p, p, p, i64, i64, i64, i32, p]),
+                ("t3_rmsnorm_bwd", [p, i64, p, i64, p, p, p, i64, p, i64, p, i64, i64, i32, p, p]),
+                ("t3_gated_scan_fwd", [p, i64, p, i64, p, p, p, i64, p, i64, i64, i64, i32, p]),
+                ("t3_gated_scan_bwd", [p, i64, p, i64, p, i64, p, i64, p, p, p, p, i64, p, i64, p,
+                                       i64, i64, i64, i32, p]),
+                ("t3_gemm_fwd_act", [p, p, p, i64, i64, i64, p, p, p, i32, p, p, i32, p, p]),
+                ("t3_act_bwd", [p, p, i32, p, p, i64, i64, i32, p, p])):
+            f = getattr(lib, name)
+            f.argtypes = types
+            f.restype = ctypes.c_int
+        lib.t3_colsum_workspace.argtypes = [i64, i64]
+        lib.t3_colsum_workspace.restype = i64
         lib.t3_version.argtypes = []
         lib.t3_version.restype = ctypes.c_int
         _lib = lib
@@ -400,6 +421,259 @@ def t3_gemm_bwd_dw_scaled_noalloc(A, dY, row_scale=None, col_scale=None, kind=T3
         rc = load().t3_gemm_bwd_dw_scaled_noalloc(*args)
     _check(rc, "t3_gemm_bwd_dw_scaled_noalloc")
     return dW
+
+
+# ------------------------------------------- norm, recurrence, epilogue ---
+
+def _dtype_of(t, name):
+    """The element type's code (T3_OUT_F32 or T3_OUT_BF16) of an activation tensor."""
+    torch = _torch()
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    if t.dtype == torch.bfloat16:
+        return T3_OUT_BF16
+    if t.dtype == torch.float32:
+        return T3_OUT_F32
+    raise TypeError(f"{name} must be bfloat16 or float32, got {t.dtype}")
+
+
+def _rows(t, like, shape, name, out=False):
+    """(address, row stride) of a tensor [..., cols] whose rows are evenly
+    spaced: `shape` is what it must be, `like` gives dtype and device.  None
+    gives (None, 0)."""
+    if t is None:
+        return None, 0
+    if t.dtype != like.dtype or t.device != like.device:
+        raise TypeError(f"{name} must be a {like.dtype} tensor on {like.device}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+    if t.numel() == 0:
+        return None, shape[-1]
+    st = t.stride()
+    if shape[-1] > 1 and st[-1] != 1:
+        raise ValueError(f"{name}: the elements of a row must be adjacent")
+    if len(shape) == 3:  # [batch][length][width]: one stride serves both
+        ld = st[1] if shape[1] > 1 else st[0]
+        if shape[0] > 1 and shape[1] > 1 and st[0] != shape[1] * ld:
+            raise ValueError(f"{name}: sequences must be evenly spaced (stride {st[0]}, not {shape[1] * ld})")
+        if shape[0] == 1 and shape[1] == 1:
+            ld = shape[-1]
+    else:
+        ld = st[0] if shape[0] > 1 else shape[-1]
+    if out and ld < shape[-1]:
+        raise ValueError(f"{name}: output rows must not overlap")
+    return t.data_ptr(), ld
+
+
+def _dense(t, dtype, like, shape, name):
+    """Address of a contiguous tensor on like's device; None gives None."""
+    if t is None:
+        return None
+    if t.dtype != dtype or t.device != like.device:
+        raise TypeError(f"{name} must be a {dtype} tensor on {like.device}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr() if t.numel() else None
+
+
+def _launch(name, like, stream, *args):
+    """Calls the library on like's device, with its current stream unless one is given."""
+    torch = _torch()
+    s = (stream if stream is not None else torch.cuda.current_stream(like.device)).cuda_stream
+    fn = getattr(load() if _lib is None else _lib, name)
+    if like.device.index == torch.cuda.current_device():
+        rc = fn(*args, s)
+    else:
+        with torch.cuda.device(like.device):
+            rc = fn(*args, s)
+    if rc != T3_OK:
+        raise T3Error(rc, name)
+
+
+def _workspace(workspace, rows, cols, like):
+    n = (load() if _lib is None else _lib).t3_colsum_workspace(rows, cols)
+    torch = _torch()
+    if workspace is None:
+        return torch.empty(n, dtype=torch.float32, device=like.device)
+    if workspace.dtype != torch.float32 or workspace.device != like.device or not workspace.is_contiguous():
+        raise TypeError(f"workspace must be a contiguous float32 tensor on {like.device}")
+    if workspace.numel() < n:
+        raise ValueError(f"workspace needs {n} floats, has {workspace.numel()}")
+    return workspace
+
+
+def t3_rmsnorm_quant(x, gamma=None, residual=None, eps=1e-5, q=None, row_scale=None, rstd=None,
+                     sum_out=None, stream=None):
+    """(q, row_scale, rstd, s): s = x + residual in x's type, normalized by its
+    root mean square, times gamma, as int8 rows with one scale each; rstd and s
+    are what t3_rmsnorm_bwd takes (see include/t3.h).  x [rows][cols] bfloat16
+    or float32, rows evenly spaced; gamma float32 [cols].  s is x itself
+    without a residual and without sum_out; sum_out may be x or residual."""
+    torch = _torch()
+    dtype = _dtype_of(x, "x")
+    if x.dim() != 2:
+        raise TypeError("x must be 2-D [rows][cols]")
+    shape = x.shape
+    rows, cols = shape
+    if q is None:
+        q = torch.empty(shape, dtype=torch.int8, device=x.device)
+    if row_scale is None:
+        row_scale = torch.empty(rows, dtype=torch.float32, device=x.device)
+    if rstd is None:
+        rstd = torch.empty(rows, dtype=torch.float32, device=x.device)
+    if sum_out is None and residual is not None:
+        sum_out = torch.empty(shape, dtype=x.dtype, device=x.device)
+    px, ldx = _rows(x, x, shape, "x")
+    pr, ldr = _rows(residual, x, shape, "residual")
+    ps, lds = _rows(sum_out, x, shape, "sum_out", out=True)
+    _launch("t3_rmsnorm_quant", x, stream, px, ldx, pr, ldr,
+            _dense(gamma, torch.float32, x, (cols,), "gamma"), eps,
+            _dense(q, torch.int8, x, shape, "q"),
+            _dense(row_scale, torch.float32, x, (rows,), "row_scale"),
+            _dense(rstd, torch.float32, x, (rows,), "rstd"), ps, lds, rows, cols, dtype)
+    return q, row_scale, rstd, x if sum_out is None else sum_out
+
+
+def t3_rmsnorm_bwd(dy, s, rstd, gamma=None, dsum=None, dx=None, dgamma=None, workspace=None, stream=None):
+    """(dx, dgamma): the gradient of t3_rmsnorm_quant for dy, the gradient of
+    the normalized rows, and dsum, that of s itself; s and rstd are the
+    forward's.  dgamma is None without gamma.  dx may be dy or dsum."""
+    torch = _torch()
+    dtype = _dtype_of(dy, "dy")
+    if dy.dim() != 2:
+        raise TypeError("dy must be 2-D [rows][cols]")
+    shape = dy.shape
+    rows, cols = shape
+    if dx is None:
+        dx = torch.empty(shape, dtype=dy.dtype, device=dy.device)
+    if dgamma is None and gamma is not None:
+        dgamma = torch.empty(cols, dtype=torch.float32, device=dy.device)
+    ws = None if dgamma is None else _workspace(workspace, rows, cols, dy)
+    pdy, lddy = _rows(dy, dy, shape, "dy")
+    ps, lds = _rows(s, dy, shape, "s")
+    pd, ldd = _rows(dsum, dy, shape, "dsum")
+    px, ldx = _rows(dx, dy, shape, "dx", out=True)
+    _launch("t3_rmsnorm_bwd", dy, stream, pdy, lddy, ps, lds,
+            _dense(rstd, torch.float32, dy, (rows,), "rstd"),
+            _dense(gamma, torch.float32, dy, (cols,), "gamma"), pd, ldd, px, ldx,
+            _dense(dgamma, torch.float32, dy, (cols,), "dgamma"), rows, cols, dtype,
+            None if ws is None else ws.data_ptr())
+    return dx, dgamma
+
+
+def t3_gated_scan_fwd(gate, cand, h0=None, resets=None, h=None, h_last=None, stream=None):
+    """(h, h_last): h_t = a_t h_(t-1) + (1 - a_t) cand_t with a_t =
+    sigmoid(gate_t) over [batch][length][width], from the float state h0
+    [batch][width] (None: zeros); resets uint8 [batch][length] marks tokens
+    that start from zero.  gate and cand may be slices of one wider tensor.
+    h_last (float32 [batch][width]) may be h0: the state advances in place."""
+    torch = _torch()
+    dtype = _dtype_of(gate, "gate")
+    if gate.dim() != 3:
+        raise TypeError("gate must be 3-D [batch][length][width]")
+    shape = gate.shape
+    batch, length, width = shape
+    if h is None:
+        h = torch.empty(shape, dtype=gate.dtype, device=gate.device)
+    if h_last is None:
+        h_last = torch.empty((batch, width), dtype=torch.float32, device=gate.device)
+    pg, ldg = _rows(gate, gate, shape, "gate")
+    pc, ldc = _rows(cand, gate, shape, "cand")
+    ph, ldh = _rows(h, gate, shape, "h", out=True)
+    _launch("t3_gated_scan_fwd", gate, stream, pg, ldg, pc, ldc,
+            _dense(h0, torch.float32, gate, (batch, width), "h0"),
+            _dense(resets, torch.uint8, gate, (batch, length), "resets"), ph, ldh,
+            _dense(h_last, torch.float32, gate, (batch, width), "h_last"), batch, length, width, dtype)
+    return h, h_last
+
+
+def t3_gated_scan_bwd(gate, cand, h, dh, h0=None, resets=None, dh_last=None, dgate=None, dcand=None,
+                      dh0=None, stream=None):
+    """(dgate, dcand, dh0): the gradient of t3_gated_scan_fwd for dh, the
+    gradient of h, and dh_last (float32 [batch][width] or None), that of
+    h_last; h is the forward's output."""
+    torch = _torch()
+    dtype = _dtype_of(gate, "gate")
+    if gate.dim() != 3:
+        raise TypeError("gate must be 3-D [batch][length][width]")
+    shape = gate.shape
+    batch, length, width = shape
+    if dgate is None:
+        dgate = torch.empty(shape, dtype=gate.dtype, device=gate.device)
+    if dcand is None:
+        dcand = torch.empty(shape, dtype=gate.dtype, device=gate.device)
+    if dh0 is None:
+        dh0 = torch.empty((batch, width), dtype=torch.float32, device=gate.device)
+    pg, ldg = _rows(gate, gate, shape, "gate")
+    pc, ldc = _rows(cand, gate, shape, "cand")
+    ph, ldh = _rows(h, gate, shape, "h")
+    pd, ldd = _rows(dh, gate, shape, "dh")
+    pdg, lddg = _rows(dgate, gate, shape, "dgate", out=True)
+    pdc, lddc = _rows(dcand, gate, shape, "dcand", out=True)
+    f32 = torch.float32
+    _launch("t3_gated_scan_bwd", gate, stream, pg, ldg, pc, ldc, ph, ldh, pd, ldd,
+            _dense(h0, f32, gate, (batch, width), "h0"),
+            _dense(resets, torch.uint8, gate, (batch, length), "resets"),
+            _dense(dh_last, f32, gate, (batch, width), "dh_last"), pdg, lddg, pdc, lddc,
+            _dense(dh0, f32, gate, (batch, width), "dh0"), batch, length, width, dtype)
+    return dgate, dcand, dh0
+
+
+def t3_gemm_fwd_act(A, Wp, K=None, row_scale=None, col_scale=None, bias=None, act=T3_ACT_NONE,
+                    residual=None, kind=T3_OUT_F32, C=None, pre=None, workspace=None, stream=None):
+    """C = act(z) + residual with z = A . W scaled per row and column plus
+    bias; `pre`, when given, receives z for t3_act_bwd.  kind: T3_OUT_F32 or
+    T3_OUT_BF16, the type of C, residual and pre [M][N].  workspace: int32
+    [M][N], allocated when the call may need one and none is given."""
+    torch = _torch()
+    M, Ka = A.shape
+    K = Ka if K is None else K
+    if Ka != K:
+        raise ValueError("A must be [M][K]")
+    if Wp.dim() != 2 or Wp.shape[1] != (K + 3) // 4:
+        raise ValueError("Wp must be [N][ceil(K/4)]")
+    if not A.is_cuda:
+        raise TypeError("A must be a CUDA tensor")
+    if kind not in (T3_OUT_F32, T3_OUT_BF16):
+        raise ValueError(f"unknown output kind {kind}")
+    N = Wp.shape[0]
+    dtype = torch.bfloat16 if kind == T3_OUT_BF16 else torch.float32
+    if C is None:
+        C = torch.empty((M, N), dtype=dtype, device=A.device)
+    if workspace is None and kind == T3_OUT_BF16:
+        workspace = torch.empty((M, N), dtype=torch.int32, device=A.device)
+    f32 = torch.float32
+    _launch("t3_gemm_fwd_act", A, stream, _dense(A, torch.int8, A, (M, K), "A"),
+            _dense(Wp, torch.uint8, A, (N, (K + 3) // 4), "Wp"), _dense(C, dtype, A, (M, N), "C"), M, N, K,
+            _dense(row_scale, f32, A, (M,), "row_scale"), _dense(col_scale, f32, A, (N,), "col_scale"),
+            _dense(bias, f32, A, (N,), "bias"), act, _dense(residual, dtype, A, (M, N), "residual"),
+            _dense(pre, dtype, A, (M, N), "pre"), kind,
+            _dense(workspace, torch.int32, A, (M, N), "workspace"))
+    return C
+
+
+def t3_act_bwd(dy, z, act, dz=None, dbias=None, workspace=None, stream=None):
+    """(dz, dbias): dz = dy * act'(z) and, into dbias when one is given
+    (float32 [cols]), its column sums; z is t3_gemm_fwd_act's pre.  dz may be
+    dy."""
+    torch = _torch()
+    dtype = _dtype_of(dy, "dy")
+    if dy.dim() != 2:
+        raise TypeError("dy must be 2-D [rows][cols]")
+    shape = dy.shape
+    rows, cols = shape
+    if z is None and act != T3_ACT_NONE:
+        raise ValueError("z is needed for this activation")
+    if dz is None:
+        dz = torch.empty(shape, dtype=dy.dtype, device=dy.device)
+    ws = None if dbias is None else _workspace(workspace, rows, cols, dy)
+    _launch("t3_act_bwd", dy, stream, _dense(dy, dy.dtype, dy, shape, "dy"),
+            _dense(z, dy.dtype, dy, shape, "z"), act, _dense(dz, dy.dtype, dy, shape, "dz"),
+            _dense(dbias, torch.float32, dy, (cols,), "dbias"), rows, cols, dtype,
+            None if ws is None else ws.data_ptr())
+    return dz, dbias
 
 
 def t3_last_device_error(stream=None):

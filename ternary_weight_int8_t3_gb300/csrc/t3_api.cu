@@ -368,6 +368,12 @@ bool bad_dims(int64_t M, int64_t N, int64_t K) {
   return M < 0 || N < 0 || K < 0 || M > kMaxDim || N > kMaxDim || K > kMaxDim;
 }
 
+// Activations' element types are the output kinds that store them.
+bool valid_dtype(int dtype) { return dtype == T3_OUT_F32 || dtype == T3_OUT_BF16; }
+bool valid_act(int act) { return act >= T3_ACT_NONE && act <= T3_ACT_GELU; }
+// Row strides so large that a row's offset in bytes could pass 63 bits.
+bool bad_ld(int64_t ld) { return ld < 0 || ld > kMaxDim; }
+
 // Empty reduction: the output is all zeros.
 int zero_fill(int32_t* out, int64_t rows, int64_t cols, cudaStream_t s) {
   if (!out) return T3_EINVAL;
@@ -543,6 +549,109 @@ int t3_gemm_bwd_dw_scaled(const int8_t* A, const int8_t* dY, void* dW, int64_t M
   return scaled_two_pass(
       [&](int32_t* x) { return t3_gemm_bwd_dw(A, dY, x, M, N, K, stream); }, dW, K, N, row_scale,
       col_scale, out_kind, workspace, stream);
+}
+
+int64_t t3_colsum_workspace(int64_t rows, int64_t cols) {
+  if (rows <= 0 || cols <= 0 || rows > kMaxDim || cols > kMaxDim) return 0;
+  return std::min<int64_t>(rows, kMaxColParts) * cols;
+}
+
+int t3_rmsnorm_quant(const void* x, int64_t ldx, const void* residual, int64_t ldr,
+                     const float* gamma, float eps, int8_t* q, float* row_scale, float* rstd,
+                     void* sum_out, int64_t lds, int64_t rows, int64_t cols, int dtype,
+                     t3_stream_t stream) {
+  if (bad_dims(rows, cols, 0) || !valid_dtype(dtype) || bad_ld(ldx) || (residual && bad_ld(ldr)) ||
+      (sum_out && (bad_ld(lds) || lds < cols)) || !(eps > 0.0f) || !(eps <= 3.4028234e38f))
+    return T3_EINVAL;
+  if (rows == 0) return T3_OK;
+  if (!row_scale || (cols > 0 && (!x || !q))) return T3_EINVAL;
+  const DeviceInfo* dev = nullptr;
+  const int st = device_info(&dev);
+  if (st != T3_OK) return st;
+  return launch_norm_fwd(x, ldx, residual, ldr, gamma, eps, q, row_scale, rstd, sum_out, lds, rows, cols,
+                         dtype, dev->sms, stream);
+}
+
+int t3_rmsnorm_bwd(const void* dy, int64_t lddy, const void* s, int64_t lds, const float* rstd,
+                   const float* gamma, const void* dsum, int64_t lddsum, void* dx, int64_t lddx,
+                   float* dgamma, int64_t rows, int64_t cols, int dtype, float* workspace,
+                   t3_stream_t stream) {
+  if (bad_dims(rows, cols, 0) || !valid_dtype(dtype) || bad_ld(lddy) || bad_ld(lds) ||
+      (dsum && bad_ld(lddsum)) || bad_ld(lddx) || (rows > 1 && lddx < cols))
+    return T3_EINVAL;
+  if (cols == 0) return T3_OK;
+  if (rows == 0) return dgamma ? zero_fill(reinterpret_cast<int32_t*>(dgamma), 1, cols, stream) : T3_OK;
+  if (!dy || !s || !rstd || !dx || (dgamma && !workspace)) return T3_EINVAL;
+  const DeviceInfo* dev = nullptr;
+  const int st = device_info(&dev);
+  if (st != T3_OK) return st;
+  return launch_norm_bwd(dy, lddy, s, lds, rstd, gamma, dsum, lddsum, dx, lddx, dgamma, rows, cols, dtype,
+                         workspace, dev->sms, stream);
+}
+
+int t3_gated_scan_fwd(const void* gate, int64_t ldg, const void* cand, int64_t ldc,
+                      const float* h0, const uint8_t* resets, void* h, int64_t ldh, float* h_last,
+                      int64_t batch, int64_t length, int64_t width, int dtype, t3_stream_t stream) {
+  if (bad_dims(batch, length, width) || !valid_dtype(dtype) || bad_ld(ldg) || bad_ld(ldc) || bad_ld(ldh) ||
+      ldh < width)
+    return T3_EINVAL;
+  if (batch == 0 || width == 0) return T3_OK;
+  if (length > 0 && (!gate || !cand || !h)) return T3_EINVAL;
+  if (length == 0 && !h_last) return T3_OK;
+  const DeviceInfo* dev = nullptr;
+  const int st = device_info(&dev);
+  if (st != T3_OK) return st;
+  return launch_scan_fwd(gate, ldg, cand, ldc, h0, resets, h, ldh, h_last, batch, length, width, dtype,
+                         dev->sms, stream);
+}
+
+int t3_gated_scan_bwd(const void* gate, int64_t ldg, const void* cand, int64_t ldc, const void* h,
+                      int64_t ldh, const void* dh, int64_t lddh, const float* h0,
+                      const uint8_t* resets, const float* dh_last, void* dgate, int64_t lddg,
+                      void* dcand, int64_t lddc, float* dh0, int64_t batch, int64_t length,
+                      int64_t width, int dtype, t3_stream_t stream) {
+  if (bad_dims(batch, length, width) || !valid_dtype(dtype) || bad_ld(ldg) || bad_ld(ldc) || bad_ld(ldh) ||
+      bad_ld(lddh) || bad_ld(lddg) || bad_ld(lddc) || lddg < width || lddc < width)
+    return T3_EINVAL;
+  if (batch == 0 || width == 0) return T3_OK;
+  if (length > 0 && (!gate || !cand || !h || !dh || !dgate || !dcand)) return T3_EINVAL;
+  if (length == 0 && !dh0) return T3_OK;
+  const DeviceInfo* dev = nullptr;
+  const int st = device_info(&dev);
+  if (st != T3_OK) return st;
+  return launch_scan_bwd(gate, ldg, cand, ldc, h, ldh, dh, lddh, h0, resets, dh_last, dgate, lddg, dcand, lddc,
+                         dh0, batch, length, width, dtype, dev->sms, stream);
+}
+
+int t3_gemm_fwd_act(const int8_t* A, const uint8_t* Wp, void* C, int64_t M, int64_t N, int64_t K,
+                    const float* row_scale, const float* col_scale, const float* bias, int act,
+                    const void* residual, void* pre, int out_kind, int32_t* workspace,
+                    t3_stream_t stream) {
+  if (bad_dims(M, N, K) || !valid_dtype(out_kind) || !valid_act(act)) return T3_EINVAL;
+  if (M == 0 || N == 0) return T3_OK;
+  if (!C || (K > 0 && (!A || !Wp)) || C == residual || C == pre) return T3_EINVAL;
+  if (K > kMaxTernaryReduction) return T3_EOVERFLOW;
+  const EpilogueArgs e{row_scale, col_scale, bias, residual, pre, act};
+  int32_t* x = workspace ? workspace : (out_kind == T3_OUT_F32 ? static_cast<int32_t*>(C) : nullptr);
+  if (!x) return T3_EINVAL;
+  int st = t3_gemm_fwd(A, Wp, x, M, N, K, stream);
+  if (st != T3_OK) return st;
+  const DeviceInfo* dev = nullptr;
+  st = device_info(&dev);
+  if (st != T3_OK) return st;
+  return launch_epilogue(x, C, e, M, N, out_kind, dev->sms, stream);
+}
+
+int t3_act_bwd(const void* dy, const void* z, int act, void* dz, float* dbias, int64_t rows,
+               int64_t cols, int dtype, float* workspace, t3_stream_t stream) {
+  if (bad_dims(rows, cols, 0) || !valid_dtype(dtype) || !valid_act(act)) return T3_EINVAL;
+  if (cols == 0 || (!dz && !dbias)) return T3_OK;
+  if (rows == 0) return dbias ? zero_fill(reinterpret_cast<int32_t*>(dbias), 1, cols, stream) : T3_OK;
+  if (!dy || (act != T3_ACT_NONE && !z) || (dbias && !workspace)) return T3_EINVAL;
+  const DeviceInfo* dev = nullptr;
+  const int st = device_info(&dev);
+  if (st != T3_OK) return st;
+  return launch_act_bwd(dy, z, act, dz, dbias, rows, cols, dtype, workspace, dev->sms, stream);
 }
 
 int64_t t3_set_small_product_limit(int64_t macs) {

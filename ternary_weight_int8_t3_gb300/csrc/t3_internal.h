@@ -78,4 +78,47 @@ int launch_small(int op, const int8_t* x, const int8_t* y, const uint8_t* wp, in
 int launch_skinny_fwd(const int8_t* A, const uint8_t* Wp, int32_t* C, int64_t M, int64_t N,
                       int64_t K, int sms, int* err, cudaStream_t s);
 
+// Partial rows of the column sums (norm and epilogue gradients): at most so
+// many, so that a workspace's size does not depend on the device.
+constexpr int kMaxColParts = 608;
+
+// out[c] = the sum of partial[0 .. parts)[c], added in a fixed order, on `s`.
+int launch_col_finish(const float* partial, int parts, int64_t cols, float* out, cudaStream_t s);
+
+// Residual add, root-mean-square norm, int8 rows with a scale each, and its
+// gradient (t3_norm.cu); dtype T3_OUT_F32 or T3_OUT_BF16.
+int launch_norm_fwd(const void* x, int64_t ldx, const void* residual, int64_t ldr, const float* gamma,
+                    float eps, int8_t* q, float* row_scale, float* rstd, void* sum_out, int64_t lds,
+                    int64_t rows, int64_t cols, int dtype, int sms, cudaStream_t s);
+int launch_norm_bwd(const void* dy, int64_t lddy, const void* x, int64_t lds, const float* rstd,
+                    const float* gamma, const void* dsum, int64_t lddsum, void* dx, int64_t lddx,
+                    float* dgamma, int64_t rows, int64_t cols, int dtype, float* workspace, int sms,
+                    cudaStream_t s);
+
+// The gated recurrence over sequences and its gradient (t3_scan.cu).
+int launch_scan_fwd(const void* gate, int64_t ldg, const void* cand, int64_t ldc, const float* h0,
+                    const uint8_t* resets, void* h, int64_t ldh, float* h_last, int64_t batch,
+                    int64_t length, int64_t width, int dtype, int sms, cudaStream_t s);
+int launch_scan_bwd(const void* gate, int64_t ldg, const void* cand, int64_t ldc, const void* h,
+                    int64_t ldh, const void* dh, int64_t lddh, const float* h0, const uint8_t* resets,
+                    const float* dh_last, void* dgate, int64_t lddg, void* dcand, int64_t lddc,
+                    float* dh0, int64_t batch, int64_t length, int64_t width, int dtype, int sms,
+                    cudaStream_t s);
+
+// What follows a product: z = (x row_scale) col_scale + bias, pre = z,
+// out = act(z) + residual (t3_epilogue.cu); x may be out's buffer for
+// T3_OUT_F32.
+struct EpilogueArgs {
+  const float *row_scale, *col_scale, *bias;
+  const void* residual;
+  void* pre;
+  int act;
+};
+int launch_epilogue(const int32_t* x, void* out, const EpilogueArgs& e, int64_t rows, int64_t cols,
+                    int kind, int sms, cudaStream_t s);
+
+// dz = dy act'(z) and its column sums.
+int launch_act_bwd(const void* dy, const void* z, int act, void* dz, float* dbias, int64_t rows,
+                   int64_t cols, int dtype, float* workspace, int sms, cudaStream_t s);
+
 }  // namespace t3
