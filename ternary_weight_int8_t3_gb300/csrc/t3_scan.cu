@@ -31,6 +31,8 @@
 // Everything is read once and written once, in a fixed order: the result does
 // not change from call to call.  Sequences of a few tokens take one thread per
 // channel pair and no exchange.
+#include <atomic>
+
 #include "t3_vec.cuh"
 
 namespace t3 {
@@ -61,7 +63,6 @@ struct BwdArgs {
   void *dgate, *dcand;
   float* dh0;
   int64_t length, width, tiles;
-  int64_t channels;
 };
 
 __device__ __forceinline__ uint32_t cluster_rank() {
@@ -77,14 +78,15 @@ __device__ __forceinline__ uint32_t cluster_size() {
 __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
-// Stores two floats at `p` in the shared memory of CTA `rank` of the cluster.
-__device__ __forceinline__ void store_peer(float2* p, uint32_t rank, float a, float b) {
+// Stores v at `p` in the shared memory of CTA `rank` of the cluster.
+__device__ __forceinline__ void store_peer(float4* p, int rank, const float4& v) {
   uint32_t r;
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(smem_addr(p)), "r"(rank));
-  asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(r), "f"(a), "f"(b) : "memory");
+  asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(r), "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w)
+               : "memory");
 }
 
-// k = sigmoid(-f) and, where asked for, k (1 - k).
+// k = sigmoid(-f).
 __device__ __forceinline__ float take_of(float f) { return logistic(f).neg; }
 
 // One step of the state.
@@ -105,134 +107,225 @@ __device__ __forceinline__ void compose(float R, float H, float& a, float& b) {
   a = fmaf(R, 1.0f - a, a);
 }
 
-// The maps of a CTA's warps and of the cluster's CTAs.
-template <int CPL>
+// The maps of a CTA's warps and of the cluster's CTAs, two channels an entry
+// (R0, H0, R1, H1), in two copies used in turn: a copy is written again only
+// after a barrier that everyone who read it has passed.
+template <int LPR>
 struct Maps {
-  float2 warp[2][kWarps][32 * CPL];      // this CTA's warps
-  float2 cta[2][kMaxCluster][32 * CPL];  // the cluster's CTAs
+  float4 warp[2][kWarps][LPR];
+  float4 cta[2][kMaxCluster][LPR];
 };
 
-// Hands this warp's maps (R, H) to the cluster, applies the maps of all warps
-// before this one (after it when kReverse) to `carry` and returns that state in `in`; carry
-// becomes the state past the whole cluster's steps.
-template <int CPL, bool kReverse>
-__device__ __forceinline__ void exchange(Maps<CPL>& m, int phase, const float (&R)[CPL], const float (&H)[CPL],
-                                         float (&carry)[CPL], float (&in)[CPL]) {
+// Where the rows of a warp lie: LPR lanes (two channels each) share a row of the
+// tile, and the 32 / LPR groups of lanes take consecutive runs of steps.  Each
+// lane has the map (R, H) of its own run.  The call applies all the maps that
+// come before (after, for kReverse) this lane's run to `carry`, the state in front
+// of the whole cluster's steps, and returns that state in `in`; carry becomes
+// the state past all of them.
+template <int LPR, bool kReverse>
+__device__ __forceinline__ void exchange(Maps<LPR>& m, int phase, int size, int rank, const float (&R)[2],
+                                         const float (&H)[2], float (&carry)[2], float (&in)[2]) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int rank = static_cast<int>(cluster_rank()), size = static_cast<int>(cluster_size());
+  const int col = lane % LPR;
+  // over the groups of this warp: the map before this lane's run, and of all
+  float gr[2] = {}, gh[2] = {}, tr[2], th[2];
 #pragma unroll
-  for (int j = 0; j < CPL; ++j) m.warp[phase][warp][lane * CPL + j] = make_float2(R[j], H[j]);
-  __syncthreads();
-  if (size > 1) {
-    if (warp == 0) {
-#pragma unroll
-      for (int j = 0; j < CPL; ++j) {
-        float a = 0.0f, h = 0.0f;
-#pragma unroll
-        for (int i = 0; i < kWarps; ++i) {
-          const float2 w = m.warp[phase][kReverse ? kWarps - 1 - i : i][lane * CPL + j];
-          compose(w.x, w.y, a, h);
-        }
-        for (int r = 0; r < size; ++r) store_peer(&m.cta[phase][rank][lane * CPL + j], r, a, h);
+  for (int j = 0; j < 2; ++j) {
+    tr[j] = R[j];
+    th[j] = H[j];
+    if constexpr (LPR == 16) {
+      const float r2 = __shfl_xor_sync(0xffffffffu, R[j], 16), h2 = __shfl_xor_sync(0xffffffffu, H[j], 16);
+      if ((lane >= 16) != kReverse) {  // the other group comes first
+        gr[j] = r2;
+        gh[j] = h2;
+        tr[j] = r2;
+        th[j] = h2;
+        compose(R[j], H[j], tr[j], th[j]);
+      } else {
+        compose(r2, h2, tr[j], th[j]);
       }
     }
+  }
+  if (lane < LPR) m.warp[phase][warp][col] = make_float4(tr[0], th[0], tr[1], th[1]);
+  __syncthreads();
+  // over the warps: the map before this warp, and of the CTA
+  float pr[2] = {}, ph[2] = {}, ar[2] = {}, ah[2] = {};
+#pragma unroll
+  for (int i = 0; i < kWarps; ++i) {
+    const int w = kReverse ? kWarps - 1 - i : i;
+    if (w == warp) {
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        pr[j] = ar[j];
+        ph[j] = ah[j];
+      }
+    }
+    const float4 e = m.warp[phase][w][col];
+    compose(e.x, e.y, ar[0], ah[0]);
+    compose(e.z, e.w, ar[1], ah[1]);
+  }
+  float first[2] = {carry[0], carry[1]};  // the state in front of this CTA
+  if (size > 1) {
+    if (warp < size && lane < LPR)
+      store_peer(&m.cta[phase][rank][col], warp, make_float4(ar[0], ah[0], ar[1], ah[1]));
     cluster_sync();
+    for (int i = 0; i < size; ++i) {
+      const int r = kReverse ? size - 1 - i : i;
+      if (r == rank) {
+        first[0] = carry[0];
+        first[1] = carry[1];
+      }
+      const float4 e = m.cta[phase][r][col];
+      carry[0] = apply(e.x, e.y, carry[0]);
+      carry[1] = apply(e.z, e.w, carry[1]);
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < 2; ++j) carry[j] = apply(ar[j], ah[j], carry[j]);
   }
 #pragma unroll
-  for (int j = 0; j < CPL; ++j) {
-    float h = carry[j], mine = h;
-    if (size > 1) {
-      for (int i = 0; i < size; ++i) {
-        const int r = kReverse ? size - 1 - i : i;
-        if (r == rank) mine = h;
-        const float2 w = m.cta[phase][r][lane * CPL + j];
-        h = apply(w.x, w.y, h);
-      }
-      carry[j] = h;
-      h = mine;
-    }
+  for (int j = 0; j < 2; ++j) in[j] = apply(gr[j], gh[j], apply(pr[j], ph[j], first[j]));
+}
+
+// One stage of a warp's operands in shared memory: NA arrays, each the warp's
+// 32 / LPR * S rows of 2 * LPR channels, copied asynchronously in pieces of CH
+// bytes.  Rows and channels outside the sequence are filled with zeros.
+template <class T, int LPR, int S, int NA>
+struct Slab {
+  static constexpr int kRow = 2 * LPR * static_cast<int>(sizeof(T));
+  static constexpr int kRows = 32 / LPR * S;
+  static constexpr int kBytes = kRow * kRows;
+  uint8_t a[NA][kBytes];
+};
+
+template <int CH>
+__device__ __forceinline__ void copy_async(uint8_t* dst, const void* src, bool valid) {
+  const int n = valid ? CH : 0;
+  if constexpr (CH == 2)  // rows of 2-byte elements on odd boundaries: a plain copy
+    *reinterpret_cast<uint16_t*>(dst) = valid ? *static_cast<const uint16_t*>(src) : 0;
+  else if constexpr (CH == 16)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_addr(dst)), "l"(src), "r"(n) : "memory");
+  else
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(smem_addr(dst)), "l"(src), "r"(n) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copy_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// Rows t0 .. of one array (row t at base + t * ld, its first channel ch0 of
+// `width`) into a slab; rows outside [0, length) become zeros.
+template <class T, int LPR, int S, int CH>
+__device__ __forceinline__ void load_rows(uint8_t* slab, const T* base, int64_t ld, int64_t t0, int64_t length,
+                                          int64_t ch0, int64_t width, int lane) {
+  constexpr int kRow = 2 * LPR * static_cast<int>(sizeof(T));
+  constexpr int kPieces = (32 / LPR * S) * kRow / CH;
+  static_assert(kPieces % 32 == 0, "whole rounds of pieces");
 #pragma unroll
-    for (int i = 0; i < kWarps; ++i) {
-      const int w = kReverse ? kWarps - 1 - i : i;
-      if (w == warp) in[j] = h;
-      const float2 v = m.warp[phase][w][lane * CPL + j];
-      h = apply(v.x, v.y, h);
-    }
-    if (size == 1) carry[j] = h;
+  for (int i = 0; i < kPieces / 32; ++i) {
+    const int off = (i * 32 + lane) * CH;
+    const int row = off / kRow;
+    const int c = off % kRow / static_cast<int>(sizeof(T));
+    const int64_t t = t0 + row;
+    const bool ok = t >= 0 && t < length && ch0 + c < width;
+    copy_async<CH>(slab + off, ok ? base + t * ld + c : base, ok);
   }
 }
 
-template <class T, int CPL, int S>
+template <class T>
+__device__ __forceinline__ void read_pair(const uint8_t* slab, int row, int rowbytes, int col, float (&f)[2]) {
+  to_float(load<T, 2>(reinterpret_cast<const T*>(slab + row * rowbytes) + 2 * col), f);
+}
+
+// Two channels to memory: one store where pairs are aligned, else one each.
+template <class T, bool kPair>
+__device__ __forceinline__ void write_pair(T* p, const float (&f)[2], bool second) {
+  if constexpr (kPair) {
+    store<T, 2>(p, from_float(f, T()));
+  } else {
+    const float lo[1] = {f[0]}, hi[1] = {f[1]};
+    store<T, 1>(p, from_float(lo, T()));
+    if (second) store<T, 1>(p + 1, from_float(hi, T()));
+  }
+}
+
+// CH: bytes a copy; kPair: outputs are aligned to pairs (else element stores).
+template <class T, int LPR, int S, int CH, bool kPair>
 __global__ void __launch_bounds__(32 * kWarps) scan_fwd_kernel(const FwdArgs p) {
-  __shared__ Maps<CPL> maps;
+  using Stage = Slab<T, LPR, S, 2>;
+  extern __shared__ __align__(16) uint8_t smem[];
+  __shared__ Maps<LPR> maps;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int col = lane % LPR, group = lane / LPR;
   const int size = static_cast<int>(cluster_size()), rank = static_cast<int>(cluster_rank());
   const int64_t tile = blockIdx.x / size;
-  const int64_t b = tile / p.tiles, ch = (tile - b * p.tiles) * (32 * CPL) + lane * CPL;
-  const bool live = ch < p.width;
-  const T* gate = static_cast<const T*>(p.gate) + b * p.length * p.ldg + ch;
-  const T* cand = static_cast<const T*>(p.cand) + b * p.length * p.ldc + ch;
+  const int64_t b = tile / p.tiles, ch0 = (tile - b * p.tiles) * (2 * LPR), ch = ch0 + 2 * col;
+  const bool live = ch < p.width, second = ch + 1 < p.width;
+  const T* gate = static_cast<const T*>(p.gate) + b * p.length * p.ldg + ch0;
+  const T* cand = static_cast<const T*>(p.cand) + b * p.length * p.ldc + ch0;
   T* out = static_cast<T*>(p.h) + b * p.length * p.ldh + ch;
-  float carry[CPL] = {};
+  Stage* stages = reinterpret_cast<Stage*>(smem) + warp * 2;  // this warp's two
+  float carry[2] = {};
   launch_dependents();
   grid_dependency_wait();
+  const int64_t span = static_cast<int64_t>(size) * kWarps * Stage::kRows;
+  const int64_t mine = (rank * kWarps + warp) * Stage::kRows;  // this warp's rows in a span
+  auto issue = [&](int64_t base, int st) {
+    load_rows<T, LPR, S, CH>(stages[st].a[0], gate, p.ldg, base + mine, p.length, ch0, p.width, lane);
+    load_rows<T, LPR, S, CH>(stages[st].a[1], cand, p.ldc, base + mine, p.length, ch0, p.width, lane);
+    copy_commit();
+  };
+  issue(0, 0);
   if (p.h0 && live) {  // plain loads: h_last may be the same array
-#pragma unroll
-    for (int j = 0; j < CPL; ++j) carry[j] = p.h0[b * p.width + ch + j];
+    carry[0] = p.h0[b * p.width + ch];
+    if (second) carry[1] = p.h0[b * p.width + ch + 1];
   }
   if (size > 1) cluster_sync();  // the peers run before anything is stored to them
   int phase = 0;
-  for (int64_t base = 0; base < p.length; base += static_cast<int64_t>(size) * kWarps * S, phase ^= 1) {
-    const int64_t t0 = base + (rank * kWarps + warp) * S;
+  for (int64_t base = 0; base < p.length; base += span, phase ^= 1) {
+    issue(base + span, phase ^ 1);  // past the end: zeros
+    const uint32_t resets = reset_bits(p.resets, b * p.length, base + mine, p.length, Stage::kRows, lane) >> (group * S);
+    copy_wait<1>();
+    __syncwarp();
+    const uint8_t* sf = stages[phase].a[0];
+    const uint8_t* sc = stages[phase].a[1];
+    const int64_t t0 = base + mine + group * S;
     const int n = p.length - t0 < S ? static_cast<int>(p.length - t0) : S;  // steps here (may be negative)
-    Raw<T, CPL> f[S], c[S];
+    float k[S][2], c[2], R[2] = {}, H[2] = {}, h[2];
 #pragma unroll
     for (int i = 0; i < S; ++i) {
-      f[i] = zero<T, CPL>();
-      c[i] = zero<T, CPL>();
-      if (live && i < n) {
-        f[i] = load<T, CPL>(gate + (t0 + i) * p.ldg);
-        c[i] = load<T, CPL>(cand + (t0 + i) * p.ldc);
-      }
-    }
-    const uint32_t resets = reset_bits(p.resets, b * p.length, t0, p.length, S, lane);
-    float k[S][CPL], cv[CPL], R[CPL], H[CPL], h[CPL];
+      read_pair<T>(sf, group * S + i, Stage::kRow, col, k[i]);
+      read_pair<T>(sc, group * S + i, Stage::kRow, col, c);
 #pragma unroll
-    for (int j = 0; j < CPL; ++j) {
-      R[j] = 0.0f;
-      H[j] = 0.0f;
-    }
-#pragma unroll
-    for (int i = 0; i < S; ++i) {
-      to_float(f[i], k[i]);
-      to_float(c[i], cv);
-#pragma unroll
-      for (int j = 0; j < CPL; ++j) {
+      for (int j = 0; j < 2; ++j) {
         k[i][j] = i < n ? take_of(k[i][j]) : 0.0f;
         if (resets >> i & 1) {
           R[j] = 1.0f;
           H[j] = 0.0f;
         }
         R[j] = fmaf(k[i][j], 1.0f - R[j], R[j]);
-        H[j] = step(H[j], k[i][j], k[i][j] == 0.0f ? 0.0f : cv[j]);
+        H[j] = step(H[j], k[i][j], k[i][j] == 0.0f ? 0.0f : c[j]);
       }
     }
-    exchange<CPL, false>(maps, phase, R, H, carry, h);
+    exchange<LPR, false>(maps, phase, size, rank, R, H, carry, h);
 #pragma unroll
     for (int i = 0; i < S; ++i) {
-      to_float(c[i], cv);
+      read_pair<T>(sc, group * S + i, Stage::kRow, col, c);
 #pragma unroll
-      for (int j = 0; j < CPL; ++j) {
+      for (int j = 0; j < 2; ++j) {
         if (resets >> i & 1) h[j] = 0.0f;
-        h[j] = step(h[j], k[i][j], k[i][j] == 0.0f ? 0.0f : cv[j]);
+        h[j] = step(h[j], k[i][j], k[i][j] == 0.0f ? 0.0f : c[j]);
       }
-      if (live && i < n) store<T, CPL>(out + (t0 + i) * p.ldh, from_float(h, T()));
+      if (live && i < n) write_pair<T, kPair>(out + (t0 + i) * p.ldh, h, second);
     }
+    __syncwarp();  // this stage is read: the next round copies into it
   }
+  copy_wait<0>();
   // the carried state is past the last step; every CTA has read h0 by now
-  if (p.h_last && live && rank == 0 && warp == 0) {
-#pragma unroll
-    for (int j = 0; j < CPL; ++j) p.h_last[b * p.width + ch + j] = carry[j];
+  if (p.h_last && live && rank == 0 && warp == 0 && group == 0) {
+    p.h_last[b * p.width + ch] = carry[0];
+    if (second) p.h_last[b * p.width + ch + 1] = carry[1];
   }
 }
 
@@ -270,150 +363,213 @@ __global__ void __launch_bounds__(128) scan_fwd_short_kernel(const FwdArgs p) {
   }
 }
 
-template <class T, int CPL, int S>
+template <class T, int LPR, int S, int CH, bool kPair>
 __global__ void __launch_bounds__(32 * kWarps) scan_bwd_kernel(const BwdArgs p) {
-  __shared__ Maps<CPL> maps;
+  using Stage = Slab<T, LPR, S, 4>;
+  extern __shared__ __align__(16) uint8_t smem[];
+  __shared__ Maps<LPR> maps;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int col = lane % LPR, group = lane / LPR;
   const int size = static_cast<int>(cluster_size()), rank = static_cast<int>(cluster_rank());
   const int64_t tile = blockIdx.x / size;
-  const int64_t b = tile / p.tiles, ch = (tile - b * p.tiles) * (32 * CPL) + lane * CPL;
-  const bool live = ch < p.width;
+  const int64_t b = tile / p.tiles, ch0 = (tile - b * p.tiles) * (2 * LPR), ch = ch0 + 2 * col;
+  const bool live = ch < p.width, second = ch + 1 < p.width;
   const int64_t row0 = b * p.length;
-  const T* gate = static_cast<const T*>(p.gate) + row0 * p.ldg + ch;
-  const T* cand = static_cast<const T*>(p.cand) + row0 * p.ldc + ch;
-  const T* hs = static_cast<const T*>(p.h) + row0 * p.ldh + ch;
-  const T* dh = static_cast<const T*>(p.dh) + row0 * p.lddh + ch;
+  const T* gate = static_cast<const T*>(p.gate) + row0 * p.ldg + ch0;
+  const T* cand = static_cast<const T*>(p.cand) + row0 * p.ldc + ch0;
+  const T* hs = static_cast<const T*>(p.h) + row0 * p.ldh + ch0;
+  const T* dh = static_cast<const T*>(p.dh) + row0 * p.lddh + ch0;
   T* dgate = static_cast<T*>(p.dgate) + row0 * p.lddg + ch;
   T* dcand = static_cast<T*>(p.dcand) + row0 * p.lddc + ch;
-  float carry[CPL] = {}, first[CPL] = {};
+  Stage* stages = reinterpret_cast<Stage*>(smem) + warp * 2;
+  float carry[2] = {}, start[2] = {};
   launch_dependents();
   grid_dependency_wait();
+  const int64_t span = static_cast<int64_t>(size) * kWarps * Stage::kRows;
+  const int64_t mine = (rank * kWarps + warp) * Stage::kRows;
+  auto issue = [&](int64_t base, int st) {  // rows in front of the sequence: zeros
+    const int64_t t = base + mine;
+    load_rows<T, LPR, S, CH>(stages[st].a[0], gate, p.ldg, t, p.length, ch0, p.width, lane);
+    load_rows<T, LPR, S, CH>(stages[st].a[1], cand, p.ldc, t, p.length, ch0, p.width, lane);
+    load_rows<T, LPR, S, CH>(stages[st].a[2], dh, p.lddh, t, p.length, ch0, p.width, lane);
+    load_rows<T, LPR, S, CH>(stages[st].a[3], hs, p.ldh, t - 1, p.length, ch0, p.width, lane);
+    copy_commit();
+  };
+  const int64_t last = p.length > 0 ? (p.length - 1) / span * span : 0;
+  issue(last, 0);
   if (live) {
-    if (p.dh_last) load_floats<CPL>(p.dh_last + b * p.width + ch, carry);
-    if (p.h0) load_floats<CPL>(p.h0 + b * p.width + ch, first);
+    const int64_t at = b * p.width + ch;
+    if (p.dh_last) {
+      carry[0] = p.dh_last[at];
+      if (second) carry[1] = p.dh_last[at + 1];
+    }
+    if (p.h0) {
+      start[0] = p.h0[at];
+      if (second) start[1] = p.h0[at + 1];
+    }
   }
   if (size > 1) cluster_sync();  // the peers run before anything is stored to them
-  const int64_t span = static_cast<int64_t>(size) * kWarps * S;
   int phase = 0;
-  for (int64_t base = (p.length - 1) / span * span; base >= 0; base -= span, phase ^= 1) {
-    const int64_t t0 = base + (rank * kWarps + warp) * S;
+  for (int64_t base = last; base >= 0; base -= span, phase ^= 1) {
+    issue(base - span, phase ^ 1);
+    const uint32_t resets = reset_bits(p.resets, row0, base + mine, p.length, Stage::kRows, lane) >> (group * S);
+    copy_wait<1>();
+    __syncwarp();
+    const Stage& st = stages[phase];
+    const int64_t t0 = base + mine + group * S;
     const int n = p.length - t0 < S ? static_cast<int>(p.length - t0) : S;
-    Raw<T, CPL> f[S], c[S], hp[S], d[S];
-#pragma unroll
-    for (int i = 0; i < S; ++i) {
-      f[i] = zero<T, CPL>();
-      c[i] = zero<T, CPL>();
-      hp[i] = zero<T, CPL>();
-      d[i] = zero<T, CPL>();
-      if (live && i < n) {
-        f[i] = load<T, CPL>(gate + (t0 + i) * p.ldg);
-        c[i] = load<T, CPL>(cand + (t0 + i) * p.ldc);
-        d[i] = load<T, CPL>(dh + (t0 + i) * p.lddh);
-        if (t0 + i > 0) hp[i] = load<T, CPL>(hs + (t0 + i - 1) * p.ldh);
-      }
-    }
-    const uint32_t resets = reset_bits(p.resets, row0, t0, p.length, S, lane);
-    float R[CPL], Q[CPL], v[CPL], fv[CPL], cv[CPL], dv[CPL], hv[CPL];
-#pragma unroll
-    for (int j = 0; j < CPL; ++j) {
-      R[j] = 0.0f;
-      Q[j] = 0.0f;
-    }
-    // the map of (1 - k_{t1}) G_{t1} at the end of these steps to the same at their start
+    float k[S][2], slope[S][2], R[2] = {}, Q[2] = {}, v[2], x[2], y[2], z[2];
+    // the map of (1 - k) G past these steps to the same in front of them
 #pragma unroll
     for (int i = S - 1; i >= 0; --i) {
-      to_float(f[i], fv);
-      to_float(d[i], dv);
+      read_pair<T>(st.a[0], group * S + i, Stage::kRow, col, x);
+      read_pair<T>(st.a[2], group * S + i, Stage::kRow, col, y);
 #pragma unroll
-      for (int j = 0; j < CPL; ++j) {
-        const float k = i < n ? take_of(fv[j]) : 0.0f;
-        const float g = dv[j] + Q[j];
-        R[j] = fmaf(k, 1.0f - R[j], R[j]);
-        Q[j] = fmaf(-k, g, g);
+      for (int j = 0; j < 2; ++j) {
+        const Logistic s = logistic(x[j]);
+        k[i][j] = i < n ? s.neg : 0.0f;
+        slope[i][j] = s.slope;
+        const float g = y[j] + Q[j];
+        R[j] = fmaf(k[i][j], 1.0f - R[j], R[j]);
+        Q[j] = fmaf(-k[i][j], g, g);
         if (resets >> i & 1) {
           R[j] = 1.0f;
           Q[j] = 0.0f;
         }
       }
     }
-    exchange<CPL, true>(maps, phase, R, Q, carry, v);
+    exchange<LPR, true>(maps, phase, size, rank, R, Q, carry, v);
 #pragma unroll
     for (int i = S - 1; i >= 0; --i) {
-      to_float(f[i], fv);
-      to_float(c[i], cv);
-      to_float(d[i], dv);
-      to_float(hp[i], hv);
-      float df[CPL], dc[CPL];
+      read_pair<T>(st.a[1], group * S + i, Stage::kRow, col, x);
+      read_pair<T>(st.a[2], group * S + i, Stage::kRow, col, y);
+      read_pair<T>(st.a[3], group * S + i, Stage::kRow, col, z);
+      const bool reset = resets >> i & 1;
+      float df[2], dc[2];
 #pragma unroll
-      for (int j = 0; j < CPL; ++j) {
-        const Logistic s = logistic(fv[j]);
-        const float k = i < n ? s.neg : 0.0f;
-        const float g = dv[j] + v[j];
-        const bool reset = resets >> i & 1;
-        const float before = reset ? 0.0f : (t0 + i == 0 ? first[j] : hv[j]);
-        dc[j] = k * g;
-        df[j] = s.slope == 0.0f ? 0.0f : g * s.slope * (before - cv[j]);
-        v[j] = reset ? 0.0f : fmaf(-k, g, g);
+      for (int j = 0; j < 2; ++j) {
+        const float g = y[j] + v[j];
+        const float before = reset ? 0.0f : (t0 + i == 0 ? start[j] : z[j]);
+        dc[j] = k[i][j] * g;
+        df[j] = slope[i][j] == 0.0f ? 0.0f : g * slope[i][j] * (before - x[j]);
+        v[j] = reset ? 0.0f : fmaf(-k[i][j], g, g);
       }
       if (live && i < n) {
-        store<T, CPL>(dgate + (t0 + i) * p.lddg, from_float(df, T()));
-        store<T, CPL>(dcand + (t0 + i) * p.lddc, from_float(dc, T()));
+        write_pair<T, kPair>(dgate + (t0 + i) * p.lddg, df, second);
+        write_pair<T, kPair>(dcand + (t0 + i) * p.lddc, dc, second);
       }
     }
+    __syncwarp();  // this stage is read: the next round copies into it
   }
-  if (p.dh0 && live && rank == 0 && warp == 0) {
-#pragma unroll
-    for (int j = 0; j < CPL; ++j) p.dh0[b * p.width + ch + j] = carry[j];
+  copy_wait<0>();
+  if (p.dh0 && live && rank == 0 && warp == 0 && group == 0) {
+    p.dh0[b * p.width + ch] = carry[0];
+    if (second) p.dh0[b * p.width + ch + 1] = carry[1];
   }
 }
 
-// CTAs in a cluster: enough that the grid has about four CTAs an SM (the
-// registers hold that many), none of them without steps.
-int cluster_for(int64_t tiles, int64_t length, int steps, int sms) {
+// CTAs in a cluster: enough that the grid has about two CTAs an SM, none of
+// them without steps.
+int cluster_for(int64_t tiles, int64_t length, int rows, int sms) {
   int c = 1;
-  while (c < kMaxCluster && tiles * c < 4ll * sms && length > static_cast<int64_t>(c) * kWarps * steps) c *= 2;
+  while (c < kMaxCluster && tiles * c < 2ll * sms && length > static_cast<int64_t>(c) * kWarps * rows) c *= 2;
   return c;
 }
 
 constexpr int64_t kShort = 8;  // tokens up to which a sequence is not split
-constexpr int kFwdSteps = 16, kBwdSteps = 8;
+// Steps a lane holds: the operands of a stage are 2 KB an array and warp
+// forward, 1 KB backward.
+template <class T> constexpr int kFwdSteps = 32 / sizeof(T);
+template <class T> constexpr int kBwdSteps = 16 / sizeof(T);
 
-template <class T, int CPL>
-int fwd(FwdArgs p, int64_t batch, int sms, cudaStream_t s) {
-  if (p.length <= kShort) {
-    const int64_t n = p.channels / CPL;
-    return launch(scan_fwd_short_kernel<T, CPL>, (n + 127) / 128, 128, 0, s, 1, p);
+// Dynamic shared memory of `Fn`, set once per device.
+template <auto Fn>
+int allow_smem(int bytes) {
+  static std::atomic<bool> done[64];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return T3_ECUDA;
+  if (dev < 0 || dev >= 64) return T3_EDEVICE;
+  if (!done[dev].load(std::memory_order_acquire)) {
+    if (cudaFuncSetAttribute(Fn, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess) return T3_ECUDA;
+    done[dev].store(true, std::memory_order_release);
   }
-  p.tiles = (p.width + 32 * CPL - 1) / (32 * CPL);
-  const int64_t tiles = batch * p.tiles;
-  const int c = cluster_for(tiles, p.length, kFwdSteps, sms);
-  return launch(scan_fwd_kernel<T, CPL, kFwdSteps>, tiles * c, 32 * kWarps, 0, s, c, p);
+  return T3_OK;
 }
 
-template <class T, int CPL>
-int bwd(BwdArgs p, int64_t batch, int sms, cudaStream_t s) {
-  p.tiles = (p.width + 32 * CPL - 1) / (32 * CPL);
-  const int64_t tiles = batch * p.tiles;
-  const int c = cluster_for(tiles, p.length, kBwdSteps, sms);
-  return launch(scan_bwd_kernel<T, CPL, kBwdSteps>, tiles * c, 32 * kWarps, 0, s, c, p);
+template <class T, int LPR, int CH, bool kPair>
+int run_fwd(FwdArgs p, int64_t batch, int sms, cudaStream_t s) {
+  constexpr int S = kFwdSteps<T>;
+  constexpr int smem = 2 * kWarps * sizeof(Slab<T, LPR, S, 2>);
+  const int st = allow_smem<scan_fwd_kernel<T, LPR, S, CH, kPair>>(smem);
+  if (st != T3_OK) return st;
+  p.tiles = (p.width + 2 * LPR - 1) / (2 * LPR);
+  const int c = cluster_for(batch * p.tiles, p.length, 32 / LPR * S, sms);
+  return launch(scan_fwd_kernel<T, LPR, S, CH, kPair>, batch * p.tiles * c, 32 * kWarps, smem, s, c, p);
+}
+
+template <class T, int LPR, int CH, bool kPair>
+int run_bwd(BwdArgs p, int64_t batch, int sms, cudaStream_t s) {
+  constexpr int S = kBwdSteps<T>;
+  constexpr int smem = 2 * kWarps * sizeof(Slab<T, LPR, S, 4>);
+  const int st = allow_smem<scan_bwd_kernel<T, LPR, S, CH, kPair>>(smem);
+  if (st != T3_OK) return st;
+  p.tiles = (p.width + 2 * LPR - 1) / (2 * LPR);
+  const int c = cluster_for(batch * p.tiles, p.length, 32 / LPR * S, sms);
+  return launch(scan_bwd_kernel<T, LPR, S, CH, kPair>, batch * p.tiles * c, 32 * kWarps, smem, s, c, p);
+}
+
+// Tiles of 64 channels, or of 32 where those would leave the GPU short of
+// CTAs even in the largest clusters.
+bool narrow(int64_t batch, int64_t width, int sms) {
+  return batch * ((width + 63) / 64) * kMaxCluster < 2ll * sms;
+}
+
+// CH 16: rows of whole 16-byte pieces; otherwise pieces of 4 bytes, or of one
+// element where rows of 2-byte elements start on odd boundaries.
+template <class T, int LPR>
+int fwd(const FwdArgs& p, int64_t batch, int ch, bool pair, int sms, cudaStream_t s) {
+  if (ch == 16) return run_fwd<T, LPR, 16, true>(p, batch, sms, s);
+  if (sizeof(T) == 4 || ch == 4)
+    return pair ? run_fwd<T, LPR, 4, true>(p, batch, sms, s) : run_fwd<T, LPR, 4, false>(p, batch, sms, s);
+  return run_fwd<T, LPR, sizeof(T) == 4 ? 4 : 2, false>(p, batch, sms, s);
+}
+
+template <class T, int LPR>
+int bwd(const BwdArgs& p, int64_t batch, int ch, bool pair, int sms, cudaStream_t s) {
+  if (ch == 16) return run_bwd<T, LPR, 16, true>(p, batch, sms, s);
+  if (sizeof(T) == 4 || ch == 4)
+    return pair ? run_bwd<T, LPR, 4, true>(p, batch, sms, s) : run_bwd<T, LPR, 4, false>(p, batch, sms, s);
+  return run_bwd<T, LPR, sizeof(T) == 4 ? 4 : 2, false>(p, batch, sms, s);
+}
+
+// Whether every row of `width` elements at `p` with stride ld starts and ends
+// on a boundary of `bytes`.
+bool rows_on(const void* p, int64_t ld, int64_t width, int es, int bytes) {
+  return aligned(p, bytes) && ld * es % bytes == 0 && width * es % bytes == 0;
 }
 
 }  // namespace sc
-
-namespace {
-// Rows of pairs: every row starts on a boundary of two elements.
-bool pair_rows(const void* p, int64_t ld, int es) { return ld % 2 == 0 && vec::aligned(p, 2 * es); }
-}  // namespace
 
 int launch_scan_fwd(const void* gate, int64_t ldg, const void* cand, int64_t ldc, const float* h0,
                     const uint8_t* resets, void* h, int64_t ldh, float* h_last, int64_t batch,
                     int64_t length, int64_t width, int dtype, int sms, cudaStream_t s) {
   const sc::FwdArgs p{gate, cand, ldg, ldc, ldh, h0, resets, h, h_last, length, width, 0, batch * width};
   const int es = dtype == T3_OUT_BF16 ? 2 : 4;
-  const bool pairs = width % 2 == 0 && pair_rows(gate, ldg, es) && pair_rows(cand, ldc, es) && pair_rows(h, ldh, es);
+  auto on = [&](int n) { return sc::rows_on(gate, ldg, width, es, n) && sc::rows_on(cand, ldc, width, es, n); };
+  const bool pair = sc::rows_on(h, ldh, width, es, 2 * es);
+  if (length <= sc::kShort) {
+    const bool two = pair && on(2 * es);
+    const int64_t n = p.channels / (two ? 2 : 1);
+    auto fn = dtype == T3_OUT_BF16
+                  ? (two ? sc::scan_fwd_short_kernel<vec::bf16, 2> : sc::scan_fwd_short_kernel<vec::bf16, 1>)
+                  : (two ? sc::scan_fwd_short_kernel<float, 2> : sc::scan_fwd_short_kernel<float, 1>);
+    return vec::launch(fn, (n + 127) / 128, 128, 0, s, 1, p);
+  }
+  const int ch = pair && on(16) ? 16 : on(4) ? 4 : 2;
+  const bool nar = sc::narrow(batch, width, sms);
   if (dtype == T3_OUT_BF16)
-    return pairs ? sc::fwd<vec::bf16, 2>(p, batch, sms, s) : sc::fwd<vec::bf16, 1>(p, batch, sms, s);
-  return pairs ? sc::fwd<float, 2>(p, batch, sms, s) : sc::fwd<float, 1>(p, batch, sms, s);
+    return nar ? sc::fwd<vec::bf16, 16>(p, batch, ch, pair, sms, s) : sc::fwd<vec::bf16, 32>(p, batch, ch, pair, sms, s);
+  return nar ? sc::fwd<float, 16>(p, batch, ch, pair, sms, s) : sc::fwd<float, 32>(p, batch, ch, pair, sms, s);
 }
 
 int launch_scan_bwd(const void* gate, int64_t ldg, const void* cand, int64_t ldc, const void* h,
@@ -422,14 +578,18 @@ int launch_scan_bwd(const void* gate, int64_t ldg, const void* cand, int64_t ldc
                     float* dh0, int64_t batch, int64_t length, int64_t width, int dtype, int sms,
                     cudaStream_t s) {
   const sc::BwdArgs p{gate, cand, h, dh, ldg, ldc, ldh, lddh, lddg, lddc, h0, resets, dh_last,
-                      dgate, dcand, dh0, length, width, 0, batch * width};
+                      dgate, dcand, dh0, length, width, 0};
   const int es = dtype == T3_OUT_BF16 ? 2 : 4;
-  const bool pairs = width % 2 == 0 && pair_rows(gate, ldg, es) && pair_rows(cand, ldc, es) &&
-                     pair_rows(h, ldh, es) && pair_rows(dh, lddh, es) && pair_rows(dgate, lddg, es) &&
-                     pair_rows(dcand, lddc, es);
+  auto on = [&](int n) {
+    return sc::rows_on(gate, ldg, width, es, n) && sc::rows_on(cand, ldc, width, es, n) &&
+           sc::rows_on(h, ldh, width, es, n) && sc::rows_on(dh, lddh, width, es, n);
+  };
+  const bool pair = sc::rows_on(dgate, lddg, width, es, 2 * es) && sc::rows_on(dcand, lddc, width, es, 2 * es);
+  const int ch = pair && on(16) ? 16 : on(4) ? 4 : 2;
+  const bool nar = sc::narrow(batch, width, sms);
   if (dtype == T3_OUT_BF16)
-    return pairs ? sc::bwd<vec::bf16, 2>(p, batch, sms, s) : sc::bwd<vec::bf16, 1>(p, batch, sms, s);
-  return pairs ? sc::bwd<float, 2>(p, batch, sms, s) : sc::bwd<float, 1>(p, batch, sms, s);
+    return nar ? sc::bwd<vec::bf16, 16>(p, batch, ch, pair, sms, s) : sc::bwd<vec::bf16, 32>(p, batch, ch, pair, sms, s);
+  return nar ? sc::bwd<float, 16>(p, batch, ch, pair, sms, s) : sc::bwd<float, 32>(p, batch, ch, pair, sms, s);
 }
 
 }  // namespace t3

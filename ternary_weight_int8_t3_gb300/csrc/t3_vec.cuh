@@ -167,9 +167,12 @@ __device__ __forceinline__ float warp_max_nan(float v) {
 struct Logistic {
   float pos, neg, slope;  // sigmoid(z), sigmoid(-z), their product
 };
+// exp2 and the reciprocal are the hardware's approximations (2 ulp and 1 ulp),
+// results below the float range flushed to 0.
 __device__ __forceinline__ Logistic logistic(float z) {
-  const float e = __expf(-fabsf(z));
-  const float r = __fdividef(1.0f, 1.0f + e);
+  float e, r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(-1.4426950408889634f * fabsf(z)));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + e));
   const float er = e * r;
   Logistic s;
   s.pos = z >= 0.0f ? r : er;
