@@ -24,8 +24,8 @@
 //     S steps in registers, a warp 64 channels, a CTA of 8 warps 8 S
 //     consecutive steps, and a cluster of up to 8 CTAs 64 S consecutive steps;
 //   * each warp composes its S steps, the CTA's maps meet in shared memory, the
-//     cluster's in every CTA's shared memory (stores to the peers, one cluster
-//     barrier), each warp applies the maps before it to the carried state and
+//     cluster's in every CTA's shared memory (asynchronous stores that complete on
+//     the receiver's barrier, so that nobody waits for its own output stores), each warp applies the maps before it to the carried state and
 //     runs its S steps again from registers, this time with the true state;
 //   * the cluster walks along the sequence; every thread carries the state.
 // Everything is read once and written once, in a fixed order: the result does
@@ -42,6 +42,7 @@ using namespace vec;
 
 constexpr int kWarps = 8;
 constexpr int kMaxCluster = 8;
+constexpr int kPerSm = 3;  // CTAs that share an SM: 64 KB of stages and at most 80 registers a thread
 
 struct FwdArgs {
   const void *gate, *cand;
@@ -52,6 +53,7 @@ struct FwdArgs {
   float* h_last;
   int64_t length, width, tiles;
   int64_t channels;  // batch * width (short sequences)
+  int* err;
 };
 
 struct BwdArgs {
@@ -63,6 +65,7 @@ struct BwdArgs {
   void *dgate, *dcand;
   float* dh0;
   int64_t length, width, tiles;
+  int* err;
 };
 
 __device__ __forceinline__ uint32_t cluster_rank() {
@@ -75,15 +78,50 @@ __device__ __forceinline__ uint32_t cluster_size() {
   asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
   return r;
 }
-__device__ __forceinline__ void cluster_sync() {
-  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+// All threads of the cluster arrive; nothing is ordered by it (a release here
+// would wait for every output store in flight).
+__device__ __forceinline__ void cluster_meet() {
+  asm volatile("barrier.cluster.arrive.relaxed.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
 }
-// Stores v at `p` in the shared memory of CTA `rank` of the cluster.
-__device__ __forceinline__ void store_peer(float4* p, int rank, const float4& v) {
+// The address in CTA `rank` of the cluster of a shared variable of this one.
+__device__ __forceinline__ uint32_t peer(const void* p, int rank) {
   uint32_t r;
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(smem_addr(p)), "r"(rank));
-  asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(r), "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w)
-               : "memory");
+  return r;
+}
+
+// Where a CTA waits for its cluster's maps; `failed` once a wait ran out, after which no wait
+// is made and the results are not valid (the error word says so).
+struct Waits {
+  int* err;
+  volatile int* abort_flag;
+  bool failed;
+};
+constexpr int kWaitCode = (11 << 8) | 7;
+
+// Waits for a phase of `bar` that peers complete with st.async; bounded like
+// mbar_wait, with the acquire at cluster scope.
+__device__ __forceinline__ void wait_peers(uint64_t* bar, uint32_t parity, Waits& w) {
+  if (w.failed) return;
+  uint64_t t0 = 0;
+  for (uint32_t spin = 0;; ++spin) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(smem_addr(bar)), "r"(parity), "r"(1000000u)
+        : "memory");
+    if (ok) return;
+    if (spin == 0) t0 = global_timer_ns();
+    if (*w.abort_flag || global_timer_ns() - t0 > kWaitLimitNs) {
+      atomicCAS(w.err, 0, kWaitCode);
+      *w.abort_flag = 1;
+      w.failed = true;
+      return;
+    }
+  }
 }
 
 // k = sigmoid(-f).
@@ -108,13 +146,31 @@ __device__ __forceinline__ void compose(float R, float H, float& a, float& b) {
 }
 
 // The maps of a CTA's warps and of the cluster's CTAs, two channels an entry
-// (R0, H0, R1, H1), in two copies used in turn: a copy is written again only
-// after a barrier that everyone who read it has passed.
+// (R0, H0, R1, H1), in two copies used in turn; the cluster's [2][CTAs][LPR]
+// lie behind the operands' stages in dynamic shared memory.  A copy is free again two
+// rounds later: a CTA sends its maps of the round in between only after its
+// warps have met (__syncthreads) behind their reads of the first, and nobody
+// sends for the third without having received that.
 template <int LPR>
 struct Maps {
   float4 warp[2][kWarps][LPR];
-  float4 cta[2][kMaxCluster][LPR];
+  uint64_t full[2];  // a round's maps of all the cluster's CTAs have arrived
+  int aborted;
 };
+
+// Sets the barriers up; every thread of the cluster calls it.
+template <int LPR>
+__device__ __forceinline__ void open_maps(Maps<LPR>& m, int size) {
+  if (size == 1) return;
+  if (threadIdx.x == 0) {
+    mbar_init(&m.full[0], 1);
+    mbar_init(&m.full[1], 1);
+    m.aborted = 0;
+    fence_mbarrier_init();
+  }
+  __syncthreads();
+  cluster_meet();  // the peers run, with their barriers, before anything is sent to them
+}
 
 // Where the rows of a warp lie: LPR lanes (two channels each) share a row of the
 // tile, and the 32 / LPR groups of lanes take consecutive runs of steps.  Each
@@ -123,10 +179,10 @@ struct Maps {
 // of the whole cluster's steps, and returns that state in `in`; carry becomes
 // the state past all of them.
 template <int LPR, bool kReverse>
-__device__ __forceinline__ void exchange(Maps<LPR>& m, int phase, int size, int rank, const float (&R)[2],
+__device__ __forceinline__ void exchange(Maps<LPR>& m, float4* cta, int round, int size, int rank, Waits& waits, const float (&R)[2],
                                          const float (&H)[2], float (&carry)[2], float (&in)[2]) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int col = lane % LPR;
+  const int col = lane % LPR, phase = round & 1;
   // over the groups of this warp: the map before this lane's run, and of all
   float gr[2] = {}, gh[2] = {}, tr[2], th[2];
 #pragma unroll
@@ -166,16 +222,18 @@ __device__ __forceinline__ void exchange(Maps<LPR>& m, int phase, int size, int 
   }
   float first[2] = {carry[0], carry[1]};  // the state in front of this CTA
   if (size > 1) {
-    if (warp < size && lane < LPR)
-      store_peer(&m.cta[phase][rank][col], warp, make_float4(ar[0], ah[0], ar[1], ah[1]));
-    cluster_sync();
+    if (threadIdx.x == 0) mbar_arrive_expect_tx(&m.full[phase], size * LPR * 16);
+    if (warp < size && lane < LPR)  // warp w sends to CTA w
+      st_async_v4(peer(cta + (phase * size + rank) * LPR + col, warp), __float_as_uint(ar[0]), __float_as_uint(ah[0]),
+                  __float_as_uint(ar[1]), __float_as_uint(ah[1]), peer(&m.full[phase], warp));
+    wait_peers(&m.full[phase], (round >> 1) & 1, waits);
     for (int i = 0; i < size; ++i) {
       const int r = kReverse ? size - 1 - i : i;
       if (r == rank) {
         first[0] = carry[0];
         first[1] = carry[1];
       }
-      const float4 e = m.cta[phase][r][col];
+      const float4 e = cta[(phase * size + r) * LPR + col];
       carry[0] = apply(e.x, e.y, carry[0]);
       carry[1] = apply(e.z, e.w, carry[1]);
     }
@@ -252,7 +310,7 @@ __device__ __forceinline__ void write_pair(T* p, const float (&f)[2], bool secon
 
 // CH: bytes a copy; kPair: outputs are aligned to pairs (else element stores).
 template <class T, int LPR, int S, int CH, bool kPair>
-__global__ void __launch_bounds__(32 * kWarps) scan_fwd_kernel(const FwdArgs p) {
+__global__ void __launch_bounds__(32 * kWarps, kPerSm) scan_fwd_kernel(const FwdArgs p) {
   using Stage = Slab<T, LPR, S, 2>;
   extern __shared__ __align__(16) uint8_t smem[];
   __shared__ Maps<LPR> maps;
@@ -266,6 +324,7 @@ __global__ void __launch_bounds__(32 * kWarps) scan_fwd_kernel(const FwdArgs p) 
   const T* cand = static_cast<const T*>(p.cand) + b * p.length * p.ldc + ch0;
   T* out = static_cast<T*>(p.h) + b * p.length * p.ldh + ch;
   Stage* stages = reinterpret_cast<Stage*>(smem) + warp * 2;  // this warp's two
+  float4* cta_maps = reinterpret_cast<float4*>(smem + 2 * kWarps * sizeof(Stage));
   float carry[2] = {};
   launch_dependents();
   grid_dependency_wait();
@@ -281,9 +340,11 @@ __global__ void __launch_bounds__(32 * kWarps) scan_fwd_kernel(const FwdArgs p) 
     carry[0] = p.h0[b * p.width + ch];
     if (second) carry[1] = p.h0[b * p.width + ch + 1];
   }
-  if (size > 1) cluster_sync();  // the peers run before anything is stored to them
-  int phase = 0;
-  for (int64_t base = 0; base < p.length; base += span, phase ^= 1) {
+  open_maps(maps, size);
+  Waits waits{p.err, &maps.aborted, false};
+  int round = 0;
+  for (int64_t base = 0; base < p.length; base += span, ++round) {
+    const int phase = round & 1;
     issue(base + span, phase ^ 1);  // past the end: zeros
     const uint32_t resets = reset_bits(p.resets, b * p.length, base + mine, p.length, Stage::kRows, lane) >> (group * S);
     copy_wait<1>();
@@ -292,36 +353,70 @@ __global__ void __launch_bounds__(32 * kWarps) scan_fwd_kernel(const FwdArgs p) 
     const uint8_t* sc = stages[phase].a[1];
     const int64_t t0 = base + mine + group * S;
     const int n = p.length - t0 < S ? static_cast<int>(p.length - t0) : S;  // steps here (may be negative)
-    float k[S][2], c[2], R[2] = {}, H[2] = {}, h[2];
+    // Steps at the sequence's end, resets and tokens that are masked out (k = 0)
+    // take the careful form; the others skip its selects.
+    float k[S][2], c[2], R[2] = {}, H[2] = {}, h[2], least = 1.0f;
+    bool careful = n < S || resets != 0;
+    if (!careful) {
 #pragma unroll
-    for (int i = 0; i < S; ++i) {
-      read_pair<T>(sf, group * S + i, Stage::kRow, col, k[i]);
-      read_pair<T>(sc, group * S + i, Stage::kRow, col, c);
+      for (int i = 0; i < S; ++i) {
+        read_pair<T>(sf, group * S + i, Stage::kRow, col, k[i]);
+        read_pair<T>(sc, group * S + i, Stage::kRow, col, c);
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        k[i][j] = i < n ? take_of(k[i][j]) : 0.0f;
-        if (resets >> i & 1) {
-          R[j] = 1.0f;
-          H[j] = 0.0f;
+        for (int j = 0; j < 2; ++j) {
+          k[i][j] = take_of(k[i][j]);
+          least = fminf(least, k[i][j]);
+          R[j] = fmaf(k[i][j], 1.0f - R[j], R[j]);
+          H[j] = step(H[j], k[i][j], c[j]);
         }
-        R[j] = fmaf(k[i][j], 1.0f - R[j], R[j]);
-        H[j] = step(H[j], k[i][j], k[i][j] == 0.0f ? 0.0f : c[j]);
+      }
+      careful = least == 0.0f;
+    }
+    if (careful) {
+#pragma unroll
+      for (int j = 0; j < 2; ++j) R[j] = H[j] = 0.0f;
+#pragma unroll
+      for (int i = 0; i < S; ++i) {
+        read_pair<T>(sf, group * S + i, Stage::kRow, col, k[i]);
+        read_pair<T>(sc, group * S + i, Stage::kRow, col, c);
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          k[i][j] = i < n ? take_of(k[i][j]) : 0.0f;
+          if (resets >> i & 1) {
+            R[j] = 1.0f;
+            H[j] = 0.0f;
+          }
+          R[j] = fmaf(k[i][j], 1.0f - R[j], R[j]);
+          H[j] = step(H[j], k[i][j], k[i][j] == 0.0f ? 0.0f : c[j]);
+        }
       }
     }
-    exchange<LPR, false>(maps, phase, size, rank, R, H, carry, h);
+    exchange<LPR, false>(maps, cta_maps, round, size, rank, waits, R, H, carry, h);
+    T* o = out + t0 * p.ldh;
+    if (!careful) {
 #pragma unroll
-    for (int i = 0; i < S; ++i) {
-      read_pair<T>(sc, group * S + i, Stage::kRow, col, c);
+      for (int i = 0; i < S; ++i, o += p.ldh) {
+        read_pair<T>(sc, group * S + i, Stage::kRow, col, c);
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        if (resets >> i & 1) h[j] = 0.0f;
-        h[j] = step(h[j], k[i][j], k[i][j] == 0.0f ? 0.0f : c[j]);
+        for (int j = 0; j < 2; ++j) h[j] = step(h[j], k[i][j], c[j]);
+        if (live) write_pair<T, kPair>(o, h, second);
       }
-      if (live && i < n) write_pair<T, kPair>(out + (t0 + i) * p.ldh, h, second);
+    } else {
+#pragma unroll
+      for (int i = 0; i < S; ++i, o += p.ldh) {
+        read_pair<T>(sc, group * S + i, Stage::kRow, col, c);
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          if (resets >> i & 1) h[j] = 0.0f;
+          h[j] = step(h[j], k[i][j], k[i][j] == 0.0f ? 0.0f : c[j]);
+        }
+        if (live && i < n) write_pair<T, kPair>(o, h, second);
+      }
     }
     __syncwarp();  // this stage is read: the next round copies into it
   }
   copy_wait<0>();
+  if (size > 1) cluster_meet();  // nothing is on its way to a CTA that has left
   // the carried state is past the last step; every CTA has read h0 by now
   if (p.h_last && live && rank == 0 && warp == 0 && group == 0) {
     p.h_last[b * p.width + ch] = carry[0];
@@ -364,7 +459,7 @@ __global__ void __launch_bounds__(128) scan_fwd_short_kernel(const FwdArgs p) {
 }
 
 template <class T, int LPR, int S, int CH, bool kPair>
-__global__ void __launch_bounds__(32 * kWarps) scan_bwd_kernel(const BwdArgs p) {
+__global__ void __launch_bounds__(32 * kWarps, kPerSm) scan_bwd_kernel(const BwdArgs p) {
   using Stage = Slab<T, LPR, S, 4>;
   extern __shared__ __align__(16) uint8_t smem[];
   __shared__ Maps<LPR> maps;
@@ -382,6 +477,7 @@ __global__ void __launch_bounds__(32 * kWarps) scan_bwd_kernel(const BwdArgs p) 
   T* dgate = static_cast<T*>(p.dgate) + row0 * p.lddg + ch;
   T* dcand = static_cast<T*>(p.dcand) + row0 * p.lddc + ch;
   Stage* stages = reinterpret_cast<Stage*>(smem) + warp * 2;
+  float4* cta_maps = reinterpret_cast<float4*>(smem + 2 * kWarps * sizeof(Stage));
   float carry[2] = {}, start[2] = {};
   launch_dependents();
   grid_dependency_wait();
@@ -408,9 +504,11 @@ __global__ void __launch_bounds__(32 * kWarps) scan_bwd_kernel(const BwdArgs p) 
       if (second) start[1] = p.h0[at + 1];
     }
   }
-  if (size > 1) cluster_sync();  // the peers run before anything is stored to them
-  int phase = 0;
-  for (int64_t base = last; base >= 0; base -= span, phase ^= 1) {
+  open_maps(maps, size);
+  Waits waits{p.err, &maps.aborted, false};
+  int round = 0;
+  for (int64_t base = last; base >= 0; base -= span, ++round) {
+    const int phase = round & 1;
     issue(base - span, phase ^ 1);
     const uint32_t resets = reset_bits(p.resets, row0, base + mine, p.length, Stage::kRows, lane) >> (group * S);
     copy_wait<1>();
@@ -438,7 +536,7 @@ __global__ void __launch_bounds__(32 * kWarps) scan_bwd_kernel(const BwdArgs p) 
         }
       }
     }
-    exchange<LPR, true>(maps, phase, size, rank, R, Q, carry, v);
+    exchange<LPR, true>(maps, cta_maps, round, size, rank, waits, R, Q, carry, v);
 #pragma unroll
     for (int i = S - 1; i >= 0; --i) {
       read_pair<T>(st.a[1], group * S + i, Stage::kRow, col, x);
@@ -462,18 +560,21 @@ __global__ void __launch_bounds__(32 * kWarps) scan_bwd_kernel(const BwdArgs p) 
     __syncwarp();  // this stage is read: the next round copies into it
   }
   copy_wait<0>();
+  if (size > 1) cluster_meet();  // nothing is on its way to a CTA that has left
   if (p.dh0 && live && rank == 0 && warp == 0 && group == 0) {
     p.dh0[b * p.width + ch] = carry[0];
     if (second) p.dh0[b * p.width + ch + 1] = carry[1];
   }
 }
 
-// CTAs in a cluster: enough that the grid has about two CTAs an SM, none of
-// them without steps.
+// CTAs in a cluster: as many as leave all clusters resident at once, none of
+// them without steps.  (A second wave costs as much as the first, and a
+// cluster that waits for room holds up its sequences from the start.)
 int cluster_for(int64_t tiles, int64_t length, int rows, int sms) {
-  int c = 1;
-  while (c < kMaxCluster && tiles * c < 2ll * sms && length > static_cast<int64_t>(c) * kWarps * rows) c *= 2;
-  return c;
+  const int64_t room = static_cast<int64_t>(kPerSm) * sms / tiles;
+  const int64_t most = (length + kWarps * rows - 1) / (kWarps * rows);
+  const int64_t c = room < most ? room : most;
+  return static_cast<int>(c < 1 ? 1 : c > kMaxCluster ? kMaxCluster : c);
 }
 
 constexpr int64_t kShort = 8;  // tokens up to which a sequence is not split
@@ -499,23 +600,23 @@ int allow_smem(int bytes) {
 template <class T, int LPR, int CH, bool kPair>
 int run_fwd(FwdArgs p, int64_t batch, int sms, cudaStream_t s) {
   constexpr int S = kFwdSteps<T>;
-  constexpr int smem = 2 * kWarps * sizeof(Slab<T, LPR, S, 2>);
-  const int st = allow_smem<scan_fwd_kernel<T, LPR, S, CH, kPair>>(smem);
+  constexpr int smem = 2 * kWarps * sizeof(Slab<T, LPR, S, 2>), per_cta = 2 * LPR * sizeof(float4);
+  const int st = allow_smem<scan_fwd_kernel<T, LPR, S, CH, kPair>>(smem + kMaxCluster * per_cta);
   if (st != T3_OK) return st;
   p.tiles = (p.width + 2 * LPR - 1) / (2 * LPR);
   const int c = cluster_for(batch * p.tiles, p.length, 32 / LPR * S, sms);
-  return launch(scan_fwd_kernel<T, LPR, S, CH, kPair>, batch * p.tiles * c, 32 * kWarps, smem, s, c, p);
+  return launch(scan_fwd_kernel<T, LPR, S, CH, kPair>, batch * p.tiles * c, 32 * kWarps, smem + (c > 1 ? c * per_cta : 0), s, c, p);
 }
 
 template <class T, int LPR, int CH, bool kPair>
 int run_bwd(BwdArgs p, int64_t batch, int sms, cudaStream_t s) {
   constexpr int S = kBwdSteps<T>;
-  constexpr int smem = 2 * kWarps * sizeof(Slab<T, LPR, S, 4>);
-  const int st = allow_smem<scan_bwd_kernel<T, LPR, S, CH, kPair>>(smem);
+  constexpr int smem = 2 * kWarps * sizeof(Slab<T, LPR, S, 4>), per_cta = 2 * LPR * sizeof(float4);
+  const int st = allow_smem<scan_bwd_kernel<T, LPR, S, CH, kPair>>(smem + kMaxCluster * per_cta);
   if (st != T3_OK) return st;
   p.tiles = (p.width + 2 * LPR - 1) / (2 * LPR);
   const int c = cluster_for(batch * p.tiles, p.length, 32 / LPR * S, sms);
-  return launch(scan_bwd_kernel<T, LPR, S, CH, kPair>, batch * p.tiles * c, 32 * kWarps, smem, s, c, p);
+  return launch(scan_bwd_kernel<T, LPR, S, CH, kPair>, batch * p.tiles * c, 32 * kWarps, smem + (c > 1 ? c * per_cta : 0), s, c, p);
 }
 
 // Tiles of 64 channels, or of 32 where those would leave the GPU short of
@@ -552,8 +653,8 @@ bool rows_on(const void* p, int64_t ld, int64_t width, int es, int bytes) {
 
 int launch_scan_fwd(const void* gate, int64_t ldg, const void* cand, int64_t ldc, const float* h0,
                     const uint8_t* resets, void* h, int64_t ldh, float* h_last, int64_t batch,
-                    int64_t length, int64_t width, int dtype, int sms, cudaStream_t s) {
-  const sc::FwdArgs p{gate, cand, ldg, ldc, ldh, h0, resets, h, h_last, length, width, 0, batch * width};
+                    int64_t length, int64_t width, int dtype, int sms, int* err, cudaStream_t s) {
+  const sc::FwdArgs p{gate, cand, ldg, ldc, ldh, h0, resets, h, h_last, length, width, 0, batch * width, err};
   const int es = dtype == T3_OUT_BF16 ? 2 : 4;
   auto on = [&](int n) { return sc::rows_on(gate, ldg, width, es, n) && sc::rows_on(cand, ldc, width, es, n); };
   const bool pair = sc::rows_on(h, ldh, width, es, 2 * es);
@@ -576,9 +677,9 @@ int launch_scan_bwd(const void* gate, int64_t ldg, const void* cand, int64_t ldc
                     int64_t ldh, const void* dh, int64_t lddh, const float* h0, const uint8_t* resets,
                     const float* dh_last, void* dgate, int64_t lddg, void* dcand, int64_t lddc,
                     float* dh0, int64_t batch, int64_t length, int64_t width, int dtype, int sms,
-                    cudaStream_t s) {
+                    int* err, cudaStream_t s) {
   const sc::BwdArgs p{gate, cand, h, dh, ldg, ldc, ldh, lddh, lddg, lddc, h0, resets, dh_last,
-                      dgate, dcand, dh0, length, width, 0};
+                      dgate, dcand, dh0, length, width, 0, err};
   const int es = dtype == T3_OUT_BF16 ? 2 : 4;
   auto on = [&](int n) {
     return sc::rows_on(gate, ldg, width, es, n) && sc::rows_on(cand, ldc, width, es, n) &&
