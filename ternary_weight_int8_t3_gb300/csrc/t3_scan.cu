@@ -42,7 +42,10 @@ using namespace vec;
 
 constexpr int kWarps = 8;
 constexpr int kMaxCluster = 8;
-constexpr int kPerSm = 3;  // CTAs that share an SM: 64 KB of stages and at most 80 registers a thread
+// CTAs that share an SM.  Both hold 64 KB of stages a CTA; the backward's 16
+// values of k and of its slope a thread spill at the 80 registers that three
+// CTAs leave (8 x 2048 x 3456: 117 us with three, 112 us with two).
+constexpr int kFwdPerSm = 3, kBwdPerSm = 2;
 
 struct FwdArgs {
   const void *gate, *cand;
@@ -124,8 +127,27 @@ __device__ __forceinline__ void wait_peers(uint64_t* bar, uint32_t parity, Waits
   }
 }
 
-// k = sigmoid(-f).
-__device__ __forceinline__ float take_of(float f) { return logistic(f).neg; }
+// k = sigmoid(-f) = 1 / (1 + e) with e = exp(f), 0 once e is infinite.  Both ways
+// from zero it keeps its relative precision.
+__device__ __forceinline__ float exp_approx(float f) {
+  float e;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(1.4426950408889634f * f));
+  return e;
+}
+__device__ __forceinline__ float rcp_approx(float x) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+__device__ __forceinline__ float take_of(float f) { return rcp_approx(1.0f + exp_approx(f)); }
+// The same with k (1 - k) = e k^2: e is held below infinity, so that it is 0 where k is.
+__device__ __forceinline__ float take_of(float f, float& slope) {
+  float e = exp_approx(f);
+  asm("min.NaN.f32 %0, %0, %1;" : "+f"(e) : "f"(3.402823466e38f));
+  const float k = rcp_approx(1.0f + e);
+  slope = e * k * k;
+  return k;
+}
 
 // One step of the state.
 __device__ __forceinline__ float step(float h, float k, float c) { return fmaf(k, c - h, h); }
@@ -145,15 +167,16 @@ __device__ __forceinline__ void compose(float R, float H, float& a, float& b) {
   a = fmaf(R, 1.0f - a, a);
 }
 
-// The maps of a CTA's warps and of the cluster's CTAs, two channels an entry
-// (R0, H0, R1, H1), in two copies used in turn; the cluster's [2][CTAs][LPR]
-// lie behind the operands' stages in dynamic shared memory.  A copy is free again two
-// rounds later: a CTA sends its maps of the round in between only after its
-// warps have met (__syncthreads) behind their reads of the first, and nobody
-// sends for the third without having received that.
+// What a CTA's warps exchange, two channels an entry: their maps (R0, H0, R1,
+// H1) and the states in front of their steps.  The cluster's maps, [2][CTAs][LPR] in
+// two copies used in turn, lie behind the operands' stages in dynamic shared
+// memory.  A copy is free again two rounds later: a CTA sends its map of the
+// round in between only behind its reads of the first, and nobody sends for the
+// third without having received that.
 template <int LPR>
 struct Maps {
-  float4 warp[2][kWarps][LPR];
+  float4 map[kWarps][LPR];
+  float2 state[kWarps][LPR];
   uint64_t full[2];  // a round's maps of all the cluster's CTAs have arrived
   int aborted;
 };
@@ -172,15 +195,17 @@ __device__ __forceinline__ void open_maps(Maps<LPR>& m, int size) {
   cluster_meet();  // the peers run, with their barriers, before anything is sent to them
 }
 
-// Where the rows of a warp lie: LPR lanes (two channels each) share a row of the
-// tile, and the 32 / LPR groups of lanes take consecutive runs of steps.  Each
-// lane has the map (R, H) of its own run.  The call applies all the maps that
-// come before (after, for kReverse) this lane's run to `carry`, the state in front
-// of the whole cluster's steps, and returns that state in `in`; carry becomes
-// the state past all of them.
+// LPR lanes (two channels each) share a row of the tile, and the 32 / LPR groups
+// of lanes take consecutive runs of steps; each lane has the map (R, H) of its
+// run.  Returns in `in` the state in front of (behind, for kReverse) this lane's run.
+// `carry`, kept by warp 0, is the state in front of the whole cluster's steps and
+// becomes the state past them.  Warp 0 composes the CTA's maps, trades them
+// with the cluster and steps the state from warp to warp; the others only hand
+// their map in and take their state out.
 template <int LPR, bool kReverse>
-__device__ __forceinline__ void exchange(Maps<LPR>& m, float4* cta, int round, int size, int rank, Waits& waits, const float (&R)[2],
-                                         const float (&H)[2], float (&carry)[2], float (&in)[2]) {
+__device__ __forceinline__ void exchange(Maps<LPR>& m, float4* cta, int round, int size, int rank, Waits& waits,
+                                         const float (&R)[2], const float (&H)[2], float (&carry)[2],
+                                         float (&in)[2]) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int col = lane % LPR, phase = round & 1;
   // over the groups of this warp: the map before this lane's run, and of all
@@ -202,47 +227,54 @@ __device__ __forceinline__ void exchange(Maps<LPR>& m, float4* cta, int round, i
       }
     }
   }
-  if (lane < LPR) m.warp[phase][warp][col] = make_float4(tr[0], th[0], tr[1], th[1]);
+  if (lane < LPR) m.map[warp][col] = make_float4(tr[0], th[0], tr[1], th[1]);
   __syncthreads();
-  // over the warps: the map before this warp, and of the CTA
-  float pr[2] = {}, ph[2] = {}, ar[2] = {}, ah[2] = {};
+  if (warp == 0) {
+    float4 e[kWarps];
 #pragma unroll
-  for (int i = 0; i < kWarps; ++i) {
-    const int w = kReverse ? kWarps - 1 - i : i;
-    if (w == warp) {
+    for (int i = 0; i < kWarps; ++i) e[i] = m.map[kReverse ? kWarps - 1 - i : i][col];
+    float s[2] = {carry[0], carry[1]};  // the state in front of this CTA
+    if (size > 1) {
+      float ar[2] = {}, ah[2] = {};
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        pr[j] = ar[j];
-        ph[j] = ah[j];
+      for (int i = 0; i < kWarps; ++i) {
+        compose(e[i].x, e[i].y, ar[0], ah[0]);
+        compose(e[i].z, e[i].w, ar[1], ah[1]);
+      }
+      if (lane == 0) mbar_arrive_expect_tx(&m.full[phase], size * LPR * 16);
+      float4* slot = cta + (phase * size + rank) * LPR + col;
+      if (lane < LPR)
+        for (int r = 0; r < size; ++r)
+          st_async_v4(peer(slot, r), __float_as_uint(ar[0]), __float_as_uint(ah[0]), __float_as_uint(ar[1]),
+                      __float_as_uint(ah[1]), peer(&m.full[phase], r));
+      __syncwarp();
+      wait_peers(&m.full[phase], (round >> 1) & 1, waits);
+      for (int i = 0; i < size; ++i) {
+        const int r = kReverse ? size - 1 - i : i;
+        if (r == rank) {
+          s[0] = carry[0];
+          s[1] = carry[1];
+        }
+        const float4 c = cta[(phase * size + r) * LPR + col];
+        carry[0] = apply(c.x, c.y, carry[0]);
+        carry[1] = apply(c.z, c.w, carry[1]);
       }
     }
-    const float4 e = m.warp[phase][w][col];
-    compose(e.x, e.y, ar[0], ah[0]);
-    compose(e.z, e.w, ar[1], ah[1]);
-  }
-  float first[2] = {carry[0], carry[1]};  // the state in front of this CTA
-  if (size > 1) {
-    if (threadIdx.x == 0) mbar_arrive_expect_tx(&m.full[phase], size * LPR * 16);
-    if (warp < size && lane < LPR)  // warp w sends to CTA w
-      st_async_v4(peer(cta + (phase * size + rank) * LPR + col, warp), __float_as_uint(ar[0]), __float_as_uint(ah[0]),
-                  __float_as_uint(ar[1]), __float_as_uint(ah[1]), peer(&m.full[phase], warp));
-    wait_peers(&m.full[phase], (round >> 1) & 1, waits);
-    for (int i = 0; i < size; ++i) {
-      const int r = kReverse ? size - 1 - i : i;
-      if (r == rank) {
-        first[0] = carry[0];
-        first[1] = carry[1];
-      }
-      const float4 e = cta[(phase * size + r) * LPR + col];
-      carry[0] = apply(e.x, e.y, carry[0]);
-      carry[1] = apply(e.z, e.w, carry[1]);
+#pragma unroll
+    for (int i = 0; i < kWarps; ++i) {
+      if (lane < LPR) m.state[kReverse ? kWarps - 1 - i : i][col] = make_float2(s[0], s[1]);
+      s[0] = apply(e[i].x, e[i].y, s[0]);
+      s[1] = apply(e[i].z, e[i].w, s[1]);
     }
-  } else {
-#pragma unroll
-    for (int j = 0; j < 2; ++j) carry[j] = apply(ar[j], ah[j], carry[j]);
+    if (size == 1) {
+      carry[0] = s[0];
+      carry[1] = s[1];
+    }
   }
-#pragma unroll
-  for (int j = 0; j < 2; ++j) in[j] = apply(gr[j], gh[j], apply(pr[j], ph[j], first[j]));
+  __syncthreads();
+  const float2 v = m.state[warp][col];
+  in[0] = apply(gr[0], gh[0], v.x);
+  in[1] = apply(gr[1], gh[1], v.y);
 }
 
 // One stage of a warp's operands in shared memory: NA arrays, each the warp's
@@ -280,14 +312,18 @@ __device__ __forceinline__ void load_rows(uint8_t* slab, const T* base, int64_t 
   constexpr int kRow = 2 * LPR * static_cast<int>(sizeof(T));
   constexpr int kPieces = (32 / LPR * S) * kRow / CH;
   static_assert(kPieces % 32 == 0, "whole rounds of pieces");
+  constexpr int kEach = 32 * CH >= kRow ? 32 * CH / kRow : 1;  // rows a round of the warp's copies covers
+  constexpr int kPer = 32 * CH >= kRow ? 1 : kRow / (32 * CH);  // rounds a row takes
+  const int row = lane * CH / kRow, c = lane * CH % kRow / static_cast<int>(sizeof(T));
+  const T* src = base + (t0 + row) * ld + c;
+  uint8_t* dst = slab + lane * CH;
 #pragma unroll
-  for (int i = 0; i < kPieces / 32; ++i) {
-    const int off = (i * 32 + lane) * CH;
-    const int row = off / kRow;
-    const int c = off % kRow / static_cast<int>(sizeof(T));
-    const int64_t t = t0 + row;
-    const bool ok = t >= 0 && t < length && ch0 + c < width;
-    copy_async<CH>(slab + off, ok ? base + t * ld + c : base, ok);
+  for (int i = 0; i < kPieces / 32; ++i, dst += 32 * CH) {
+    const int64_t t = t0 + row + i / kPer * kEach;
+    const int at = i % kPer * (32 * CH / static_cast<int>(sizeof(T)));  // channels along the row
+    const bool ok = t >= 0 && t < length && ch0 + c + at < width;
+    copy_async<CH>(dst, ok ? src + at : base, ok);
+    if (i % kPer == kPer - 1) src += kEach * ld;
   }
 }
 
@@ -310,7 +346,7 @@ __device__ __forceinline__ void write_pair(T* p, const float (&f)[2], bool secon
 
 // CH: bytes a copy; kPair: outputs are aligned to pairs (else element stores).
 template <class T, int LPR, int S, int CH, bool kPair>
-__global__ void __launch_bounds__(32 * kWarps, kPerSm) scan_fwd_kernel(const FwdArgs p) {
+__global__ void __launch_bounds__(32 * kWarps, kFwdPerSm) scan_fwd_kernel(const FwdArgs p) {
   using Stage = Slab<T, LPR, S, 2>;
   extern __shared__ __align__(16) uint8_t smem[];
   __shared__ Maps<LPR> maps;
@@ -353,9 +389,9 @@ __global__ void __launch_bounds__(32 * kWarps, kPerSm) scan_fwd_kernel(const Fwd
     const uint8_t* sc = stages[phase].a[1];
     const int64_t t0 = base + mine + group * S;
     const int n = p.length - t0 < S ? static_cast<int>(p.length - t0) : S;  // steps here (may be negative)
-    // Steps at the sequence's end, resets and tokens that are masked out (k = 0)
-    // take the careful form; the others skip its selects.
-    float k[S][2], c[2], R[2] = {}, H[2] = {}, h[2], least = 1.0f;
+    // Steps at the sequence's end, resets, and masked tokens (k = 0) whose
+    // candidate is not finite, which would show in H, take the careful form.
+    float k[S][2], c[2], R[2] = {}, H[2] = {}, h[2];
     bool careful = n < S || resets != 0;
     if (!careful) {
 #pragma unroll
@@ -365,12 +401,11 @@ __global__ void __launch_bounds__(32 * kWarps, kPerSm) scan_fwd_kernel(const Fwd
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
           k[i][j] = take_of(k[i][j]);
-          least = fminf(least, k[i][j]);
           R[j] = fmaf(k[i][j], 1.0f - R[j], R[j]);
           H[j] = step(H[j], k[i][j], c[j]);
         }
       }
-      careful = least == 0.0f;
+      careful = !(fabsf(H[0]) + fabsf(H[1]) < __int_as_float(0x7f800000));
     }
     if (careful) {
 #pragma unroll
@@ -459,7 +494,7 @@ __global__ void __launch_bounds__(128) scan_fwd_short_kernel(const FwdArgs p) {
 }
 
 template <class T, int LPR, int S, int CH, bool kPair>
-__global__ void __launch_bounds__(32 * kWarps, kPerSm) scan_bwd_kernel(const BwdArgs p) {
+__global__ void __launch_bounds__(32 * kWarps, kBwdPerSm) scan_bwd_kernel(const BwdArgs p) {
   using Stage = Slab<T, LPR, S, 4>;
   extern __shared__ __align__(16) uint8_t smem[];
   __shared__ Maps<LPR> maps;
@@ -517,44 +552,61 @@ __global__ void __launch_bounds__(32 * kWarps, kPerSm) scan_bwd_kernel(const Bwd
     const int64_t t0 = base + mine + group * S;
     const int n = p.length - t0 < S ? static_cast<int>(p.length - t0) : S;
     float k[S][2], slope[S][2], R[2] = {}, Q[2] = {}, v[2], x[2], y[2], z[2];
+    const bool careful = n < S || resets != 0 || t0 == 0;  // ends, resets
     // the map of (1 - k) G past these steps to the same in front of them
+    if (!careful) {
 #pragma unroll
-    for (int i = S - 1; i >= 0; --i) {
-      read_pair<T>(st.a[0], group * S + i, Stage::kRow, col, x);
-      read_pair<T>(st.a[2], group * S + i, Stage::kRow, col, y);
+      for (int i = S - 1; i >= 0; --i) {
+        read_pair<T>(st.a[0], group * S + i, Stage::kRow, col, x);
+        read_pair<T>(st.a[2], group * S + i, Stage::kRow, col, y);
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const Logistic s = logistic(x[j]);
-        k[i][j] = i < n ? s.neg : 0.0f;
-        slope[i][j] = s.slope;
-        const float g = y[j] + Q[j];
-        R[j] = fmaf(k[i][j], 1.0f - R[j], R[j]);
-        Q[j] = fmaf(-k[i][j], g, g);
-        if (resets >> i & 1) {
-          R[j] = 1.0f;
-          Q[j] = 0.0f;
+        for (int j = 0; j < 2; ++j) {
+          k[i][j] = take_of(x[j], slope[i][j]);
+          const float g = y[j] + Q[j];
+          R[j] = fmaf(k[i][j], 1.0f - R[j], R[j]);
+          Q[j] = fmaf(-k[i][j], g, g);
+        }
+      }
+    } else {
+#pragma unroll
+      for (int i = S - 1; i >= 0; --i) {
+        read_pair<T>(st.a[0], group * S + i, Stage::kRow, col, x);
+        read_pair<T>(st.a[2], group * S + i, Stage::kRow, col, y);
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const float t = take_of(x[j], slope[i][j]);
+          k[i][j] = i < n ? t : 0.0f;
+          const float g = y[j] + Q[j];
+          R[j] = fmaf(k[i][j], 1.0f - R[j], R[j]);
+          Q[j] = fmaf(-k[i][j], g, g);
+          if (resets >> i & 1) {
+            R[j] = 1.0f;
+            Q[j] = 0.0f;
+          }
         }
       }
     }
     exchange<LPR, true>(maps, cta_maps, round, size, rank, waits, R, Q, carry, v);
+    T* og = dgate + (t0 + S - 1) * p.lddg;
+    T* oc = dcand + (t0 + S - 1) * p.lddc;
 #pragma unroll
-    for (int i = S - 1; i >= 0; --i) {
+    for (int i = S - 1; i >= 0; --i, og -= p.lddg, oc -= p.lddc) {
       read_pair<T>(st.a[1], group * S + i, Stage::kRow, col, x);
       read_pair<T>(st.a[2], group * S + i, Stage::kRow, col, y);
       read_pair<T>(st.a[3], group * S + i, Stage::kRow, col, z);
-      const bool reset = resets >> i & 1;
+      const bool reset = careful && (resets >> i & 1);
       float df[2], dc[2];
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
         const float g = y[j] + v[j];
-        const float before = reset ? 0.0f : (t0 + i == 0 ? start[j] : z[j]);
+        if (careful) z[j] = reset ? 0.0f : (t0 + i == 0 ? start[j] : z[j]);
         dc[j] = k[i][j] * g;
-        df[j] = slope[i][j] == 0.0f ? 0.0f : g * slope[i][j] * (before - x[j]);
+        df[j] = slope[i][j] == 0.0f ? 0.0f : g * slope[i][j] * (z[j] - x[j]);
         v[j] = reset ? 0.0f : fmaf(-k[i][j], g, g);
       }
-      if (live && i < n) {
-        write_pair<T, kPair>(dgate + (t0 + i) * p.lddg, df, second);
-        write_pair<T, kPair>(dcand + (t0 + i) * p.lddc, dc, second);
+      if (live && (!careful || i < n)) {
+        write_pair<T, kPair>(og, df, second);
+        write_pair<T, kPair>(oc, dc, second);
       }
     }
     __syncwarp();  // this stage is read: the next round copies into it
@@ -570,8 +622,8 @@ __global__ void __launch_bounds__(32 * kWarps, kPerSm) scan_bwd_kernel(const Bwd
 // CTAs in a cluster: as many as leave all clusters resident at once, none of
 // them without steps.  (A second wave costs as much as the first, and a
 // cluster that waits for room holds up its sequences from the start.)
-int cluster_for(int64_t tiles, int64_t length, int rows, int sms) {
-  const int64_t room = static_cast<int64_t>(kPerSm) * sms / tiles;
+int cluster_for(int64_t tiles, int64_t length, int rows, int slots) {
+  const int64_t room = slots / tiles;
   const int64_t most = (length + kWarps * rows - 1) / (kWarps * rows);
   const int64_t c = room < most ? room : most;
   return static_cast<int>(c < 1 ? 1 : c > kMaxCluster ? kMaxCluster : c);
@@ -604,7 +656,7 @@ int run_fwd(FwdArgs p, int64_t batch, int sms, cudaStream_t s) {
   const int st = allow_smem<scan_fwd_kernel<T, LPR, S, CH, kPair>>(smem + kMaxCluster * per_cta);
   if (st != T3_OK) return st;
   p.tiles = (p.width + 2 * LPR - 1) / (2 * LPR);
-  const int c = cluster_for(batch * p.tiles, p.length, 32 / LPR * S, sms);
+  const int c = cluster_for(batch * p.tiles, p.length, 32 / LPR * S, kFwdPerSm * sms);
   return launch(scan_fwd_kernel<T, LPR, S, CH, kPair>, batch * p.tiles * c, 32 * kWarps, smem + (c > 1 ? c * per_cta : 0), s, c, p);
 }
 
@@ -615,7 +667,7 @@ int run_bwd(BwdArgs p, int64_t batch, int sms, cudaStream_t s) {
   const int st = allow_smem<scan_bwd_kernel<T, LPR, S, CH, kPair>>(smem + kMaxCluster * per_cta);
   if (st != T3_OK) return st;
   p.tiles = (p.width + 2 * LPR - 1) / (2 * LPR);
-  const int c = cluster_for(batch * p.tiles, p.length, 32 / LPR * S, sms);
+  const int c = cluster_for(batch * p.tiles, p.length, 32 / LPR * S, kBwdPerSm * sms);
   return launch(scan_bwd_kernel<T, LPR, S, CH, kPair>, batch * p.tiles * c, 32 * kWarps, smem + (c > 1 ? c * per_cta : 0), s, c, p);
 }
 
