@@ -377,11 +377,14 @@ enum { T3_ACT_NONE = 0, T3_ACT_RELU = 1, T3_ACT_RELU2 = 2, T3_ACT_SILU = 3, T3_A
  * row_scale [M], col_scale [N], bias [N] (float), residual [M][N] and pre
  * [M][N] (the output's type) may each be NULL: ones, ones, zeros, zeros, not
  * written.  pre is what t3_act_bwd takes.  out_kind: T3_OUT_F32 or T3_OUT_BF16.  K = 0
- * takes x = 0.  workspace: DEVICE int32 [M][N], as in t3_gemm_fwd_scaled:
- * needed for T3_OUT_BF16 where the product cannot end in this epilogue (M > 32
- * with operands or outputs whose rows are not 16-byte aligned, K > 65536, or a
- * small product); a caller without one gets T3_EINVAL there.  Sizes and
- * overflow rules are those of t3_gemm_fwd_scaled.
+ * takes x = 0.  residual and pre must not be C's buffer (T3_EINVAL).  One
+ * kernel does it all for one or two rows (and up to eight when Wp is at most 4
+ * MB), and for M > 32 where A, Wp, C, residual and pre have rows of whole 16-
+ * byte pieces on 16-byte boundaries, K <= 65536 and the product is not one of
+ * the small ones that t3_gemm_fwd runs on the CUDA cores.  Otherwise the int32
+ * product is taken first, into `workspace` (DEVICE int32 [M][N]) or, for
+ * T3_OUT_F32 without one, into C; T3_OUT_BF16 returns T3_EINVAL there without
+ * a workspace.  Sizes and overflow rules are those of t3_gemm_fwd_scaled.
  */
 int t3_gemm_fwd_act(const int8_t* A, const uint8_t* Wp, void* C, int64_t M, int64_t N, int64_t K,
                     const float* row_scale, const float* col_scale, const float* bias, int act,

@@ -90,7 +90,10 @@ bool make_u16_map_tiled(CUtensorMap* map, const void* base, int64_t rows, int64_
 // Output tensor map of the pair pipeline for output kind `kind` (tc2::kOutI32
 // or a T3_OUT_* kind): boxes of 32 columns x 128 rows; int32 and float rows
 // in the 128-byte swizzle, bf16 rows (64 bytes) unswizzled.
-bool make_out_map(CUtensorMap* map, const void* base, int64_t rows, int64_t cols, int kind) {
+// per_warp: boxes of 32 x 32 as a layer's epilogue takes them, bf16 rows in the
+// 64-byte swizzle (no int32 there).
+bool make_out_map(CUtensorMap* map, const void* base, int64_t rows, int64_t cols, int kind,
+                  bool per_warp = false) {
   if (kind == tc2::kOutI32) return make_i32_map_tiled(map, base, rows, cols, 128, 32, true);
   std::memset(map, 0, sizeof(*map));
   const int64_t esize = (kind == T3_OUT_BF16) ? 2 : 4;
@@ -99,12 +102,14 @@ bool make_out_map(CUtensorMap* map, const void* base, int64_t rows, int64_t cols
   if (!fn) return false;
   cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
   cuuint64_t strides[1] = {static_cast<cuuint64_t>(cols * esize)};
-  cuuint32_t box[2] = {32, 128};
+  cuuint32_t box[2] = {32, per_warp ? 32u : 128u};
   cuuint32_t estr[2] = {1, 1};
   CUresult r = fn(map,
                   kind == T3_OUT_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32,
                   2, const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                  kind == T3_OUT_BF16 ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B,
+                  kind != T3_OUT_BF16 ? CU_TENSOR_MAP_SWIZZLE_128B
+                  : per_warp          ? CU_TENSOR_MAP_SWIZZLE_64B
+                                      : CU_TENSOR_MAP_SWIZZLE_NONE,
                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   if (r != CUDA_SUCCESS) std::memset(map, 0, sizeof(*map));
   return r == CUDA_SUCCESS;
@@ -186,7 +191,7 @@ __global__ void wait_selftest_kernel(int* err, uint64_t limit_ns) {
 template <int OP>
 int run_tc2(const int8_t* act, const uint8_t* Wp, void* out, int64_t M, int64_t N, int64_t K,
             cudaStream_t stream, int out_kind = tc2::kOutI32, const float* row_scale = nullptr,
-            const float* col_scale = nullptr) {
+            const float* col_scale = nullptr, const EpilogueArgs* epi = nullptr) {
   const DeviceInfo* dev = nullptr;
   int st = device_info(&dev);
   if (st != T3_OK) return st;
@@ -201,8 +206,17 @@ int run_tc2(const int8_t* act, const uint8_t* Wp, void* out, int64_t M, int64_t 
   const bool w_ok = (OP == kOpFwd)
                         ? make_u8_map_tiled(&mw, Wp, N, KB, KB, tc2::BNH, tc2::BK / 4)
                         : make_u8_map_tiled(&mw, Wp, N, KB, KB, tc2::BK, tc2::BN / 4);
-  const bool out_ok = make_out_map(&mo, out, M, out_cols, out_kind);
+  const bool out_ok = make_out_map(&mo, out, M, out_cols, out_kind, epi != nullptr);
   if (!out_ok && out_kind != tc2::kOutI32) return T3_EINVAL;  // scaled output needs bulk stores
+  // a layer's epilogue also wants TMA operands, and maps of the pre-activation
+  // and the residual
+  tc2::ActMaps more;
+  if (epi) {
+    if (!a_ok || !w_ok) return T3_EINVAL;
+    more.pre = more.res = mo;  // unused copies: any initialised map
+    if (epi->pre && !make_out_map(&more.pre, epi->pre, M, out_cols, out_kind, true)) return T3_EINVAL;
+    if (epi->residual && !make_out_map(&more.res, epi->residual, M, out_cols, out_kind, true)) return T3_EINVAL;
+  }
   if (!a_ok) ma = w_ok ? mw : mo;  // unused copies: any initialised map
   if (!w_ok) mw = ma;
   if (out_kind != tc2::kOutI32 && ceil_div(act_cols, tc2::BK) > tc2::kChunkStages) return T3_EINVAL;
@@ -269,6 +283,11 @@ int run_tc2(const int8_t* act, const uint8_t* Wp, void* out, int64_t M, int64_t 
   }
   const int64_t pairs = split ? max_pairs : std::min(num_tiles, max_pairs);
   const int grid = static_cast<int>(2 * pairs);
+  if (epi) {
+    p.mode = tc2::kModeAct;
+    p.epi = *epi;
+    return launch_tc2_fwd_act(p, ma, mw, mo, more, grid, stream);
+  }
   return (OP == kOpFwd) ? launch_tc2_fwd(p, ma, mw, mo, grid, stream)
                         : launch_tc2_dx(p, ma, mw, mo, grid, stream);
 }
@@ -356,6 +375,13 @@ bool word_rows(const void* base, int64_t len) {
   return len % 4 == 0 && reinterpret_cast<uintptr_t>(base) % 4 == 0;
 }
 
+// Forwards of few rows that run on the CUDA cores: one or two rows, or up to
+// eight over few weights (measured: they beat the tensor cores there; the
+// tensor cores win from four rows at N = K = 8192).
+bool gemv_rows(int64_t M, int64_t N, int64_t K) {
+  return M <= 2 || (M <= kGemvM && N * ((K + 3) / 4) <= kGemvSmallBytes);
+}
+
 int run_small(int op, const int8_t* x, const int8_t* y, const uint8_t* wp, int32_t* out, int64_t M,
               int64_t N, int64_t K, cudaStream_t stream) {
   const DeviceInfo* dev = nullptr;
@@ -425,10 +451,7 @@ int t3_gemm_fwd(const int8_t* A, const uint8_t* Wp, int32_t* C, int64_t M, int64
     const DeviceInfo* dev = nullptr;
     int st = device_info(&dev);
     if (st != T3_OK) return st;
-    // the CUDA-core path: one or two rows, or up to eight over few weights
-    // (measured: it beats the tensor cores there; the tensor cores win from
-    // four rows at N = K = 8192)
-    if (M <= 2 || (M <= kGemvM && N * ((K + 3) / 4) <= kGemvSmallBytes)) {
+    if (gemv_rows(M, N, K)) {
       st = launch_gemv_fwd(A, Wp, C, M, N, K, dev->sms, stream);
       if (st != T3_EINVAL) return st;
     }
@@ -632,12 +655,21 @@ int t3_gemm_fwd_act(const int8_t* A, const uint8_t* Wp, void* C, int64_t M, int6
   if (!C || (K > 0 && (!A || !Wp)) || C == residual || C == pre) return T3_EINVAL;
   if (K > kMaxTernaryReduction) return T3_EOVERFLOW;
   const EpilogueArgs e{row_scale, col_scale, bias, residual, pre, act};
+  const DeviceInfo* dev = nullptr;
+  int st = device_info(&dev);
+  if (st != T3_OK) return st;
+  // the routes of t3_gemm_fwd; those that can end in this epilogue do
+  if (K > 0 && M <= kGemvM && gemv_rows(M, N, K)) {
+    st = launch_gemv_fwd_act(A, Wp, C, e, out_kind, M, N, K, dev->sms, stream);
+    if (st != T3_EINVAL) return st;
+  }
+  if (K > 0 && M > kSmallM && !small_product(M, N, K, word_rows(A, K) && word_rows(Wp, (K + 3) / 4))) {
+    st = run_tc2<kOpFwd>(A, Wp, C, M, N, K, stream, out_kind, row_scale, col_scale, &e);
+    if (st != T3_EINVAL) return st;
+  }
   int32_t* x = workspace ? workspace : (out_kind == T3_OUT_F32 ? static_cast<int32_t*>(C) : nullptr);
   if (!x) return T3_EINVAL;
-  int st = t3_gemm_fwd(A, Wp, x, M, N, K, stream);
-  if (st != T3_OK) return st;
-  const DeviceInfo* dev = nullptr;
-  st = device_info(&dev);
+  st = t3_gemm_fwd(A, Wp, x, M, N, K, stream);
   if (st != T3_OK) return st;
   return launch_epilogue(x, C, e, M, N, out_kind, dev->sms, stream);
 }

@@ -28,6 +28,8 @@
 // Launch: a programmatic dependent of whatever precedes it on the stream; it
 // reads A and Wp and writes C only after griddepcontrol.wait, and before the
 // wait asks its share of 16-byte aligned packed rows into L2.
+#include <cuda_bf16.h>
+
 #include <atomic>
 #include <cstdint>
 
@@ -53,14 +55,54 @@ __device__ __forceinline__ void decode16_s8(uint32_t x, uint32_t (&w)[4]) {
   w[3] = prmt(kWeightTable, 0u, od >> 16);
 }
 
+// Where a sum goes: the int32 output, or through a layer's epilogue into f32 or
+// bf16.  `ahead(m, n)` loads what the epilogue of C[m][n] needs before the sum
+// is taken, so that those loads are not on the end of the kernel.
+struct OutI32 {
+  int32_t* C;
+  struct Ahead {};
+  __device__ __forceinline__ Ahead ahead(int64_t, int64_t, int64_t) const { return {}; }
+  __device__ __forceinline__ void put(int64_t at, int32_t acc, const Ahead&) const { C[at] = acc; }
+};
+
+template <class T>
+struct OutAct {
+  T* C;
+  EpilogueArgs e;
+  struct Ahead {
+    float rs, cs, bias, res;
+  };
+  static __device__ __forceinline__ float value(const float* p) { return __ldg(p); }
+  static __device__ __forceinline__ float value(const __nv_bfloat16* p) { return __bfloat162float(*p); }
+  __device__ __forceinline__ Ahead ahead(int64_t m, int64_t n, int64_t N) const {
+    return {e.row_scale ? __ldg(e.row_scale + m) : 1.0f, e.col_scale ? __ldg(e.col_scale + n) : 1.0f,
+            e.bias ? __ldg(e.bias + n) : 0.0f,
+            e.residual ? value(static_cast<const T*>(e.residual) + m * N + n) : 0.0f};
+  }
+  static __device__ __forceinline__ void write(float* p, float y) { *p = y; }
+  static __device__ __forceinline__ void write(__nv_bfloat16* p, float y) { *p = __float2bfloat16_rn(y); }
+  __device__ __forceinline__ void put(int64_t at, int32_t acc, const Ahead& a) const {
+    float y = __fadd_rn(__fmul_rn(__fmul_rn(__int2float_rn(acc), a.rs), a.cs), a.bias);
+    if (e.pre) write(static_cast<T*>(e.pre) + at, y);
+    switch (e.act) {
+      case T3_ACT_RELU: y = vec::act<T3_ACT_RELU>(y); break;
+      case T3_ACT_RELU2: y = vec::act<T3_ACT_RELU2>(y); break;
+      case T3_ACT_SILU: y = vec::act<T3_ACT_SILU>(y); break;
+      case T3_ACT_GELU: y = vec::act<T3_ACT_GELU>(y); break;
+      default: break;
+    }
+    write(C + at, y + a.res);
+  }
+};
+
 // Each warp takes R weight rows at a time, so that one read of A's copy from
 // shared memory serves R rows.  kVec: packed rows of a multiple of 16 bytes
 // at a 16-byte aligned base (16-byte loads); else the chunks are assembled
 // from single bytes.
-template <int MR, bool kVec>
+template <int MR, bool kVec, class Out>
 __global__ void __launch_bounds__(32 * kWarps, 1)
     gemv_kernel(const int8_t* __restrict__ A, const uint8_t* __restrict__ Wp,
-                int32_t* __restrict__ C, int M, int N, int K, int64_t KB, int groups) {
+                const Out out, int M, int N, int K, int64_t KB, int groups) {
   constexpr int R = MR <= 4 ? 4 : 2;
   // A's copy, [MR][4][chunks]: entry (m, q, j) holds the 16 activations of
   // 16-k group 4 j + q in the decode's order, so that consecutive lanes (chunks
@@ -118,6 +160,8 @@ __global__ void __launch_bounds__(32 * kWarps, 1)
     for (int r = 0; r < R; ++r)
 #pragma unroll
       for (int m = 0; m < MR; ++m) acc[r][m] = 0;
+    typename Out::Ahead ahead{};
+    if (lane < R * MR && lane % MR < M && n0 + lane / MR < ne) ahead = out.ahead(lane % MR, n0 + lane / MR, N);
 #pragma unroll 2
     for (int64_t j = lane; j < chunks; j += 32) {
       uint32_t c[R][4];
@@ -172,24 +216,24 @@ __global__ void __launch_bounds__(32 * kWarps, 1)
 #pragma unroll
       for (int m = 0; m < MR; ++m)
         if (lane == r * MR + m && m < M && n0 + r < ne)
-          C[static_cast<int64_t>(m) * N + n0 + r] = acc[r][m];
+          out.put(static_cast<int64_t>(m) * N + n0 + r, acc[r][m], ahead);
   }
 }
 
-template <int MR>
+template <int MR, class Out>
 int set_attrs() {
-  return (cudaFuncSetAttribute(gemv_kernel<MR, true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+  return (cudaFuncSetAttribute(gemv_kernel<MR, true, Out>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                static_cast<int>(kMaxSmem)) == cudaSuccess &&
-          cudaFuncSetAttribute(gemv_kernel<MR, false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+          cudaFuncSetAttribute(gemv_kernel<MR, false, Out>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                static_cast<int>(kMaxSmem)) == cudaSuccess)
              ? T3_OK
              : T3_ECUDA;
 }
 
-template <int MR>
-int launch_mr(const int8_t* A, const uint8_t* Wp, int32_t* C, int M, int N, int K, int64_t KB,
+template <int MR, class Out>
+int launch_mr(const int8_t* A, const uint8_t* Wp, const Out& out, int M, int N, int K, int64_t KB,
               int groups, int64_t smem, int grid, bool vec, cudaStream_t s) {
-  auto fn = vec ? gemv_kernel<MR, true> : gemv_kernel<MR, false>;
+  auto fn = vec ? gemv_kernel<MR, true, Out> : gemv_kernel<MR, false, Out>;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
@@ -200,28 +244,27 @@ int launch_mr(const int8_t* A, const uint8_t* Wp, int32_t* C, int M, int N, int 
   cfg.stream = s;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  if (cudaLaunchKernelEx(&cfg, fn, A, Wp, C, M, N, K, KB, groups) != cudaSuccess) return T3_ECUDA;
+  if (cudaLaunchKernelEx(&cfg, fn, A, Wp, out, M, N, K, KB, groups) != cudaSuccess) return T3_ECUDA;
   return cudaGetLastError() == cudaSuccess ? T3_OK : T3_ECUDA;
 }
 
-}  // namespace gv
-
-int launch_gemv_fwd(const int8_t* A, const uint8_t* Wp, int32_t* C, int64_t M, int64_t N,
-                    int64_t K, int sms, cudaStream_t s) {
+template <class Out>
+int launch_any(const int8_t* A, const uint8_t* Wp, const Out& out, int64_t M, int64_t N, int64_t K, int sms,
+               cudaStream_t s) {
   const int64_t KB = (K + 3) / 4;
   // 16-k groups, padded to whole 16-byte chunks of codes (64 k)
   const int64_t groups = (K + 63) / 64 * 4;
   const int mr = M <= 1 ? 1 : M <= 2 ? 2 : M <= 4 ? 4 : 8;
   const int64_t smem = static_cast<int64_t>(mr) * groups * 16;
-  if (M < 1 || M > 8 || smem > gv::kMaxSmem || N > 2147483647LL) return T3_EINVAL;
+  if (M < 1 || M > 8 || smem > kMaxSmem || N > 2147483647LL) return T3_EINVAL;
   const bool vec = (KB % 16 == 0) && (reinterpret_cast<uintptr_t>(Wp) % 16 == 0);
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return T3_ECUDA;
   static std::atomic<bool> attr_done[64];
   if (dev < 0 || dev >= 64) return T3_EDEVICE;
   if (!attr_done[dev].load(std::memory_order_acquire)) {
-    if (gv::set_attrs<1>() != T3_OK || gv::set_attrs<2>() != T3_OK || gv::set_attrs<4>() != T3_OK ||
-        gv::set_attrs<8>() != T3_OK)
+    if (set_attrs<1, Out>() != T3_OK || set_attrs<2, Out>() != T3_OK || set_attrs<4, Out>() != T3_OK ||
+        set_attrs<8, Out>() != T3_OK)
       return T3_ECUDA;
     attr_done[dev].store(true, std::memory_order_release);
   }
@@ -231,11 +274,25 @@ int launch_gemv_fwd(const int8_t* A, const uint8_t* Wp, int32_t* C, int64_t M, i
   const int m = static_cast<int>(M), n = static_cast<int>(N), k = static_cast<int>(K);
   const int gr = static_cast<int>(groups);
   switch (mr) {
-    case 1: return gv::launch_mr<1>(A, Wp, C, m, n, k, KB, gr, smem, grid, vec, s);
-    case 2: return gv::launch_mr<2>(A, Wp, C, m, n, k, KB, gr, smem, grid, vec, s);
-    case 4: return gv::launch_mr<4>(A, Wp, C, m, n, k, KB, gr, smem, grid, vec, s);
-    default: return gv::launch_mr<8>(A, Wp, C, m, n, k, KB, gr, smem, grid, vec, s);
+    case 1: return launch_mr<1>(A, Wp, out, m, n, k, KB, gr, smem, grid, vec, s);
+    case 2: return launch_mr<2>(A, Wp, out, m, n, k, KB, gr, smem, grid, vec, s);
+    case 4: return launch_mr<4>(A, Wp, out, m, n, k, KB, gr, smem, grid, vec, s);
+    default: return launch_mr<8>(A, Wp, out, m, n, k, KB, gr, smem, grid, vec, s);
   }
+}
+
+}  // namespace gv
+
+int launch_gemv_fwd(const int8_t* A, const uint8_t* Wp, int32_t* C, int64_t M, int64_t N,
+                    int64_t K, int sms, cudaStream_t s) {
+  return gv::launch_any(A, Wp, gv::OutI32{C}, M, N, K, sms, s);
+}
+
+int launch_gemv_fwd_act(const int8_t* A, const uint8_t* Wp, void* C, const EpilogueArgs& e, int kind,
+                        int64_t M, int64_t N, int64_t K, int sms, cudaStream_t s) {
+  if (kind == T3_OUT_BF16)
+    return gv::launch_any(A, Wp, gv::OutAct<__nv_bfloat16>{static_cast<__nv_bfloat16*>(C), e}, M, N, K, sms, s);
+  return gv::launch_any(A, Wp, gv::OutAct<float>{static_cast<float*>(C), e}, M, N, K, sms, s);
 }
 
 }  // namespace t3

@@ -3,6 +3,7 @@
 #include <cstdint>
 #include <cuda.h>
 #include <cuda_runtime.h>
+#include "t3_act.cuh"
 #include "t3_common.cuh"
 #include "t3_tc2.cuh"
 #include "t3_tc2_dw.cuh"
@@ -33,6 +34,12 @@ int prepare_tc2_dx();
 // (tc2::kModeBf16; p.row_inv holds the rows' inverse scales).
 int launch_tc2_fwd_bf16(const tc2::Params& p, const CUtensorMap& ma, const CUtensorMap& mw,
                         const CUtensorMap& mo, int grid, cudaStream_t s);
+
+// The forward with the whole epilogue of a layer (tc2::kModeAct; p.epi, out_kind
+// f32 or bf16): operands by TMA, whole tiles, one exact chunk, bulk stores; `more`
+// describes p.epi.pre and p.epi.residual where those are set.
+int launch_tc2_fwd_act(const tc2::Params& p, const CUtensorMap& ma, const CUtensorMap& mw,
+                       const CUtensorMap& mo, const tc2::ActMaps& more, int grid, cudaStream_t s);
 
 // Zeroes out[0, n) on `s` as a programmatic dependent of the work before it:
 // it waits for that work to complete, then lets the next grid launch early.
@@ -66,6 +73,9 @@ int launch_dequant(const int32_t* x, void* out, int64_t rows, int64_t cols, cons
 // launched, when A's copy would not fit its shared-memory budget.
 int launch_gemv_fwd(const int8_t* A, const uint8_t* Wp, int32_t* C, int64_t M, int64_t N,
                     int64_t K, int sms, cudaStream_t s);
+// The same with the epilogue in the kernel that ends each sum.
+int launch_gemv_fwd_act(const int8_t* A, const uint8_t* Wp, void* C, const EpilogueArgs& e, int kind,
+                        int64_t M, int64_t N, int64_t K, int sms, cudaStream_t s);
 
 // The three products on the CUDA cores for small problems, any alignment
 // (t3_small.cu): op 1 C = A.W (x = A, wp = Wp), 2 dX = dY.Wᵀ (x = dY, wp = Wp),
@@ -105,15 +115,8 @@ int launch_scan_bwd(const void* gate, int64_t ldg, const void* cand, int64_t ldc
                     float* dh0, int64_t batch, int64_t length, int64_t width, int dtype, int sms,
                     int* err, cudaStream_t s);
 
-// What follows a product: z = (x row_scale) col_scale + bias, pre = z,
-// out = act(z) + residual (t3_epilogue.cu); x may be out's buffer for
-// T3_OUT_F32.
-struct EpilogueArgs {
-  const float *row_scale, *col_scale, *bias;
-  const void* residual;
-  void* pre;
-  int act;
-};
+// What follows a product (EpilogueArgs) on its int32 result (t3_epilogue.cu);
+// x may be out's buffer for T3_OUT_F32.
 int launch_epilogue(const int32_t* x, void* out, const EpilogueArgs& e, int64_t rows, int64_t cols,
                     int kind, int sms, cudaStream_t s);
 

@@ -35,6 +35,7 @@
 #include <cstdint>
 
 #include "t3.h"
+#include "t3_act.cuh"
 #include "t3_common.cuh"
 
 namespace t3 {
@@ -85,6 +86,12 @@ template <int OP, int kActBytes = 1> struct Layout {
   static constexpr int n_bars = 2 * RAW_STAGES + 3 * OP_STAGES + 2 * ACC_BUFS + 1;
   static constexpr int off_misc = off_bar + 8 * n_bars;
   static constexpr int smem_alloc = off_misc + 16 + 1024;
+  // kModeAct only: a tile's biases, read as 16-byte vectors like the scales
+  static constexpr int off_bias = (off_misc + 16 + 15) / 16 * 16;
+  static constexpr int off_stage2 = (off_bias + BN * 4 + 1023) / 1024 * 1024;
+  static constexpr int off_res_bar = off_stage2 + 2 * stage_out;  // a barrier per epilogue warp and slot
+  static constexpr int smem_alloc_act = off_res_bar + 8 * 4 * 8 + 1024;
+  static_assert(off_cs % 16 == 0 && off_bias % 16 == 0, "vectors of scales and biases");
 };
 static_assert(4 * 33 * 32 * 4 <= 2 * Layout<kOpFwd>::stage_out,
               "the unaligned-output epilogue's row blocks fit the staging buffers");
@@ -125,6 +132,8 @@ struct Params {
   int dp_tiles;
   // kModeBf16: the inverse row scales 127 / amax of the bf16 activations
   const float* row_inv;
+  // kModeAct: what the epilogue adds to the scales
+  EpilogueArgs epi;
   int* err;
 };
 
@@ -182,17 +191,15 @@ constexpr int kModeTma = 0, kModeWGlobal = 1, kModeAGlobal = 2;
 // The forward with bf16 activations quantized in the converters (both
 // operands by TMA, whole tiles, int32 output).
 constexpr int kModeBf16 = 3;
+// The forward with a layer's whole epilogue: scales, bias, activation, residual,
+// and the pre-activation as a second output (both operands by TMA, whole
+// tiles, f32 or bf16 output).  An instantiation of its own, so that the others
+// keep their registers.
+constexpr int kModeAct = 4;
 
-// Scaled epilogue: y = ((float)x * rs) * cs per element, each product rounded
-// to nearest (no contraction); x is the accumulator, an exact integer in f32
-// when the reduction is one chunk.  Stages float (128-byte-swizzled rows of
-// 32 words, like the int32 path) or bf16 ([128][64 B], unswizzled).
-// cs: this block's 32 column scales, staged in shared memory.
-__device__ __forceinline__ void stage_scaled(uint8_t* buf, int srow, const uint32_t (&v)[32],
-                                             float rs, const float* cs, int kind) {
-  float y[32];
-#pragma unroll
-  for (int e = 0; e < 32; ++e) y[e] = __fmul_rn(__fmul_rn(__uint_as_float(v[e]), rs), cs[e]);
+// Stages 32 floats of row `srow` for a bulk store: float (128-byte-swizzled rows
+// of 32 words, like the int32 path) or bf16 ([128][64 B], unswizzled).
+__device__ __forceinline__ void stage_floats(uint8_t* buf, int srow, const float (&y)[32], int kind) {
   if (kind == T3_OUT_BF16) {
 #pragma unroll
     for (int g = 0; g < 4; ++g) {
@@ -210,6 +217,107 @@ __device__ __forceinline__ void stage_scaled(uint8_t* buf, int srow, const uint3
       sts128(buf + tc::sw128(srow, c), __float_as_uint(y[4 * c]), __float_as_uint(y[4 * c + 1]),
              __float_as_uint(y[4 * c + 2]), __float_as_uint(y[4 * c + 3]));
   }
+}
+
+// Scaled epilogue: y = ((float)x * rs) * cs per element, each product rounded
+// to nearest (no contraction); x is the accumulator, an exact integer in f32
+// when the reduction is one chunk.
+// cs: this block's 32 column scales, staged in shared memory.
+__device__ __forceinline__ void stage_scaled(uint8_t* buf, int srow, const uint32_t (&v)[32],
+                                             float rs, const float* cs, int kind) {
+  float y[32];
+#pragma unroll
+  for (int e = 0; e < 32; ++e) y[e] = __fmul_rn(__fmul_rn(__uint_as_float(v[e]), rs), cs[e]);
+  stage_floats(buf, srow, y, kind);
+}
+
+// The epilogue's values of one row and 32 columns.  bias: this block's 32
+// biases in shared memory, like cs; zeros where there are none.
+__device__ __forceinline__ void scale_bias(float (&y)[32], const uint32_t (&v)[32], float rs, const float* cs,
+                                           const float* bias) {
+#pragma unroll
+  for (int g = 0; g < 8; ++g) {
+    const float4 c = *reinterpret_cast<const float4*>(cs + 4 * g), b = *reinterpret_cast<const float4*>(bias + 4 * g);
+    y[4 * g] = __fadd_rn(__fmul_rn(__fmul_rn(__uint_as_float(v[4 * g]), rs), c.x), b.x);
+    y[4 * g + 1] = __fadd_rn(__fmul_rn(__fmul_rn(__uint_as_float(v[4 * g + 1]), rs), c.y), b.y);
+    y[4 * g + 2] = __fadd_rn(__fmul_rn(__fmul_rn(__uint_as_float(v[4 * g + 2]), rs), c.z), b.z);
+    y[4 * g + 3] = __fadd_rn(__fmul_rn(__fmul_rn(__uint_as_float(v[4 * g + 3]), rs), c.w), b.w);
+  }
+}
+
+template <int ACT>
+__device__ __forceinline__ void act_row(float (&y)[32]) {
+#pragma unroll
+  for (int e = 0; e < 32; ++e) y[e] = vec::act<ACT>(y[e]);
+}
+
+__device__ __forceinline__ void act_row_any(float (&y)[32], int act) {
+  switch (act) {
+    case T3_ACT_RELU: return act_row<T3_ACT_RELU>(y);
+    case T3_ACT_RELU2: return act_row<T3_ACT_RELU2>(y);
+    case T3_ACT_SILU: return act_row<T3_ACT_SILU>(y);
+    case T3_ACT_GELU: return act_row<T3_ACT_GELU>(y);
+    default: return;
+  }
+}
+
+// A warp's 32 x 32 block in its slot: rows of 32 floats in the 128-byte swizzle,
+// or of 32 bf16 in the 64-byte one (16-byte piece g of row r at g ^ (r / 2) % 4), so
+// that a lane's accesses to its own row meet no bank conflicts.
+__device__ __forceinline__ uint8_t* act_piece(uint8_t* slot, int lane, int g, bool bf16) {
+  return slot + (bf16 ? lane * 64 + ((g ^ (lane >> 1)) & 3) * 16 : tc::sw128(lane, g));
+}
+
+__device__ __forceinline__ void add_slot(float (&y)[32], uint8_t* slot, int lane, bool bf16) {
+  if (bf16) {
+#pragma unroll
+    for (int g = 0; g < 4; ++g) {
+      const uint4 r = *reinterpret_cast<const uint4*>(act_piece(slot, lane, g, true));
+      const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        y[8 * g + 2 * j] += __uint_as_float(w[j] << 16);
+        y[8 * g + 2 * j + 1] += __uint_as_float(w[j] & 0xFFFF0000u);
+      }
+    }
+  } else {
+#pragma unroll
+    for (int g = 0; g < 8; ++g) {
+      const float4 r = *reinterpret_cast<const float4*>(act_piece(slot, lane, g, false));
+      y[4 * g] += r.x;
+      y[4 * g + 1] += r.y;
+      y[4 * g + 2] += r.z;
+      y[4 * g + 3] += r.w;
+    }
+  }
+}
+
+__device__ __forceinline__ void stage_slot(uint8_t* slot, int lane, const float (&y)[32], bool bf16) {
+  if (bf16) {
+#pragma unroll
+    for (int g = 0; g < 4; ++g) {
+      uint32_t w[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const __nv_bfloat162 b = __floats2bfloat162_rn(y[8 * g + 2 * j], y[8 * g + 2 * j + 1]);
+        w[j] = *reinterpret_cast<const uint32_t*>(&b);
+      }
+      sts128(act_piece(slot, lane, g, true), w[0], w[1], w[2], w[3]);
+    }
+  } else {
+#pragma unroll
+    for (int g = 0; g < 8; ++g)
+      sts128(act_piece(slot, lane, g, false), __float_as_uint(y[4 * g]), __float_as_uint(y[4 * g + 1]),
+             __float_as_uint(y[4 * g + 2]), __float_as_uint(y[4 * g + 3]));
+  }
+}
+
+// At most `pending` (0 to 3) of this thread's bulk stores still read shared memory.
+__device__ __forceinline__ void bulk_wait_read_upto(int pending) {
+  if (pending >= 3) return bulk_wait_group_read<3>();
+  if (pending == 2) return bulk_wait_group_read<2>();
+  if (pending == 1) return bulk_wait_group_read<1>();
+  bulk_wait_group_read<0>();
 }
 
 // ---------------------------------------------------------------- cluster
@@ -638,14 +746,36 @@ __device__ __forceinline__ int64_t pair_stage_count(const Params& p, int pair, i
 
 // ------------------------------------------------------------------ kernel
 
+// kModeAct: a warp's part of the staging buffers: two slots of 32 rows of 32
+// floats, or four of bf16.
+constexpr int kWarpStage = 2 * 32 * 32 * 4;
+static_assert(4 * kWarpStage <= 2 * Layout<kOpFwd>::stage_out, "four warps' slots fit the staging buffers");
+
+// kModeAct's further maps: the pre-activation's and the residual's.
+struct NoMap {};
+struct ActMaps {
+  CUtensorMap pre, res;
+};
+template <int kMode> struct MoreMapsOf { using type = NoMap; };
+template <> struct MoreMapsOf<kModeAct> { using type = ActMaps; };
+template <int kMode> using MoreMaps = typename MoreMapsOf<kMode>::type;
+
 // kSplit: the split schedule (operands by TMA only); without it every pair
 // takes whole tiles and the loops below reduce to plain tile loops.
+// Epilogue warps and threads of an instantiation: a layer's epilogue has about
+// three times the instructions of the others, and takes twice the warps.
+__host__ __device__ constexpr int epi_warps(int mode) { return mode == kModeAct ? 8 : 4; }
+__host__ __device__ constexpr int threads(int mode) { return 32 * (kConvWarps + 2 + epi_warps(mode)); }
+static_assert(threads(kModeTma) == kThreads, "four epilogue warps elsewhere");
+
 template <int OP, int kMode, bool kSplit>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads(kMode), 1)
     tc2_kernel(const Params p, const __grid_constant__ CUtensorMap map_a,
                const __grid_constant__ CUtensorMap map_w,
-               const __grid_constant__ CUtensorMap map_out) {
+               const __grid_constant__ CUtensorMap map_out,
+               const __grid_constant__ MoreMaps<kMode> more) {
   static_assert(!kSplit || kMode == kModeTma, "the split schedule takes TMA operands");
+  static_assert(kMode != kModeAct || (OP == kOpFwd && !kSplit), "the layer epilogue: forward, whole tiles");
   static_assert(kMode != kModeBf16 || (OP == kOpFwd && !kSplit), "bf16 activations: forward, whole tiles");
   using L = Layout<OP, kMode == kModeBf16 ? 2 : 1>;
   extern __shared__ uint8_t smem_raw[];
@@ -679,7 +809,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       // without weight TMA only the activation warps read the raw stages
       // the warps that read the raw stages release them
       const int readers = (p.a_tma ? kActWarps : 0) + (p.w_tma ? kWWarps : 0);
-      mbar_init(&raw_empty[s], (kMode == kModeTma || kMode == kModeBf16) ? kConvWarps
+      mbar_init(&raw_empty[s], (kMode == kModeTma || kMode == kModeBf16 || kMode == kModeAct) ? kConvWarps
                                : kMode == kModeWGlobal ? kActWarps
                                : (readers > 0 ? readers : 1));
     }
@@ -690,9 +820,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     }
     for (int s = 0; s < ACC_BUFS; ++s) {
       mbar_init(&acc_full[s], 1);
-      mbar_init(&acc_empty[s], 8);
+      mbar_init(&acc_empty[s], 2 * epi_warps(kMode));
     }
     mbar_init(drain_bar, 1);
+    if (kMode == kModeAct)
+      for (int s = 0; s < 8 * 4; ++s) mbar_init(reinterpret_cast<uint64_t*>(smem + L::off_res_bar) + s, 1);
     *abort_flag = 0;
     fence_mbarrier_init();
   }
@@ -983,6 +1115,39 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     uint32_t ab = 0, aph = 0, slab = 0;
     bool ok = true;
     if (p.use_tma_out && epi_tid == 0) prefetch_tensormap(&map_out);
+    constexpr int kEpiThreads = 32 * epi_warps(kMode);
+    // kModeAct: warps 4 to 7 of the epilogue take the tile's upper 96 columns
+    const int half = kMode == kModeAct ? (warp - kEpiWarp0) >> 2 : 0;
+    const int cb0 = half * (BN / 64), cb1 = kMode == kModeAct ? cb0 + BN / 64 : BN / 32;
+    // kModeAct: the biases' tile, and this warp's ring of slots.  Each output of
+    // a block (the pre-activation, where one is wanted, then C) takes the next
+    // slot; the residual of a block is loaded into its slot of C, added there and
+    // overwritten by the sum.
+    float* bias_tile = reinterpret_cast<float*>(smem + L::off_bias);
+    uint8_t* ring = (half ? smem + L::off_stage2 : stage_out) + q * kWarpStage;
+    uint64_t* res_bar = reinterpret_cast<uint64_t*>(smem + L::off_res_bar) + (half * 4 + q) * 4;
+    const bool bf16_out = p.out_kind == T3_OUT_BF16;
+    const int nslots = bf16_out ? 4 : 2, slot_bytes = kWarpStage / nslots;
+    const int uses = kMode == kModeAct && p.epi.pre ? 2 : 1;  // slots a block takes
+    const bool has_res = kMode == kModeAct && p.epi.residual;
+    // room to load a tile's three residual blocks at once, or one block early
+    const bool res_all = nslots == 4 && uses == 1, res_ahead = !res_all && nslots >= 2 * uses;
+    uint32_t use = 0, res_par = 0;
+    bool res_ok = true;
+    auto fetch = [&](uint32_t n, int col, int row, int pending) {  // the residual into the slot of use n
+      if constexpr (kMode == kModeAct) {
+        if (lane == 0) {
+          const int s = static_cast<int>(n) & (nslots - 1);
+          bulk_wait_read_upto(pending);
+          mbar_arrive_expect_tx(&res_bar[s], slot_bytes);
+          tma_load_2d(ring + s * slot_bytes, &more.res, &res_bar[s], col, row);
+        }
+      }
+    };
+    if constexpr (kMode == kModeAct) {
+      if (epi_tid == 0 && p.epi.pre) prefetch_tensormap(&more.pre);
+      if (epi_tid == 0 && p.epi.residual) prefetch_tensormap(&more.res);
+    }
     // split schedule: the zeroing grid launched just before has finished
     // before the first output write
     if (kSplit) grid_dependency_wait();
@@ -1002,11 +1167,24 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       const int64_t row = static_cast<int64_t>(row0) + srow;
       const float rs =
           (p.out_kind != kOutI32 && p.row_scale && row < p.out_rows) ? __ldg(p.row_scale + row) : 1.0f;
+      // kModeAct: the residual's first block or all, while the product is still
+      // computed
+      int fetched = 0;
+      if (has_res)
+        for (int cb = cb0; cb < (res_all ? cb1 : cb0 + 1); ++cb, ++fetched) {
+          if (static_cast<int64_t>(tcol) * BN + cb * 32 >= p.out_cols) break;
+          fetch(use + fetched + uses - 1, tcol * BN + cb * 32, row0 + q * 32, nslots - uses - fetched);
+        }
       for (int64_t c0 = kb0, c1; c0 < kb1; c0 = c1) {
         c1 = kSplit ? chunk_end(static_cast<int>(c0), static_cast<int>(kb1))
                     : ((kb1 < c0 + kChunkStages) ? kb1 : c0 + kChunkStages);
         ok = mbar_wait(&acc_full[ab], aph, abort_flag, p.err, code_base | 4);
-        ok = named_bar_and(kEpiBarrier, 128, __all_sync(0xffffffffu, ok));
+        ok = named_bar_and(kEpiBarrier, kEpiThreads, __all_sync(0xffffffffu, ok && res_ok));
+        if (!ok)  // giving up: the copies in flight land before this CTA leaves
+          for (int i = 0; i < fetched; ++i) {
+            const int s = static_cast<int>(use + i + uses - 1) & (nslots - 1);
+            mbar_wait(&res_bar[s], (res_par >> s) & 1u, abort_flag, p.err, code_base | 4);
+          }
         if (!ok) break;
         tc_fence_after();
         // a whole tile's first chunk is stored; its later chunks, and every
@@ -1017,20 +1195,53 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         if (p.out_kind != kOutI32) {
           // the tile's column scales, once (the barrier above ends the previous
           // tile's reads of them)
-          for (int j = epi_tid; j < BN; j += 128) {
+          for (int j = epi_tid; j < BN; j += kEpiThreads) {
             const int64_t col = static_cast<int64_t>(tcol) * BN + j;
             cs_tile[j] = p.col_scale ? (col < p.out_cols ? __ldg(p.col_scale + col) : 0.0f) : 1.0f;
+            if (kMode == kModeAct)
+              bias_tile[j] = p.epi.bias && col < p.out_cols ? __ldg(p.epi.bias + col) : 0.0f;
           }
-          named_bar_sync(kEpiBarrier, 128);
+          named_bar_sync(kEpiBarrier, kEpiThreads);
         }
-        for (int cb = 0; cb < BN / 32; ++cb) {
+        for (int cb = cb0; cb < cb1; ++cb) {
           const int64_t col0 = static_cast<int64_t>(tcol) * BN + cb * 32;
           if (col0 >= p.out_cols) break;
           uint32_t v[32];
           tmem_ld_block<OP>(
               tmem_base + (static_cast<uint32_t>(q * 32) << 16) + kAccCol + ab * BN + cb * 32, v);
           tmem_wait_ld();
-          if (p.use_tma_out) {
+          if constexpr (kMode == kModeAct) {
+            // each warp stages and stores its own 32 rows: no barrier between
+            // them within a tile
+            const int row_w = row0 + q * 32, col = static_cast<int>(col0);
+            if (has_res) {
+              if (!res_all && !res_ahead && cb > cb0) fetch(use + uses - 1, col, row_w, nslots - uses);
+              if (res_ahead && cb + 1 < cb1 && col0 + 32 < p.out_cols)
+                fetch(use + 2 * uses - 1, col + 32, row_w, nslots - 2 * uses);
+            }
+            float y[32];
+            scale_bias(y, v, rs, cs_tile + cb * 32, bias_tile + cb * 32);
+            for (int pass = 2 - uses; pass < 2; ++pass, ++use) {
+              const int s = static_cast<int>(use) & (nslots - 1);
+              uint8_t* slot = ring + s * slot_bytes;
+              if (pass == 1) act_row_any(y, p.epi.act);
+              if (pass == 1 && has_res) {
+                if (res_ok) res_ok = mbar_wait(&res_bar[s], (res_par >> s) & 1u, abort_flag, p.err, code_base | 4);
+                res_par ^= 1u << s;
+                add_slot(y, slot, lane, bf16_out);
+              } else {
+                if (lane == 0) bulk_wait_read_upto(nslots - 1);
+                __syncwarp();
+              }
+              stage_slot(slot, lane, y, bf16_out);
+              fence_proxy_async_smem();
+              __syncwarp();
+              if (lane == 0) {
+                if (row_w < p.out_rows) tma_store_2d(pass ? &map_out : &more.pre, slot, col, row_w);
+                bulk_commit_group();
+              }
+            }
+          } else if (p.use_tma_out) {
             uint8_t* buf = stage_out + (slab & 1) * L::stage_out;
             if (epi_tid == 0) bulk_wait_group_read<1>();
             named_bar_sync(kEpiBarrier, 128);
@@ -1071,7 +1282,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         if (++ab == ACC_BUFS) { ab = 0; aph ^= 1u; }
       }
     }
-    if (p.use_tma_out && epi_tid == 0) bulk_wait_group<0>();
+    if (kMode == kModeAct ? lane == 0 : p.use_tma_out && epi_tid == 0) bulk_wait_group<0>();
   }
 
   tc_fence_before();

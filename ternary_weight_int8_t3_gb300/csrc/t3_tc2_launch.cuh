@@ -53,17 +53,17 @@ int launch_tc2_op(const tc2::Params& p, const CUtensorMap& ma, const CUtensorMap
   cfg.numAttrs = 1;
   if (p.dp_tiles < p.tiles_r * p.tiles_c) {
     if (p.mode != tc2::kModeTma) return T3_EINVAL;  // the split schedule takes TMA operands
-    if (cudaLaunchKernelEx(&cfg, tc2::tc2_kernel<OP, tc2::kModeTma, true>, p, ma, mw, mo) !=
+    if (cudaLaunchKernelEx(&cfg, tc2::tc2_kernel<OP, tc2::kModeTma, true>, p, ma, mw, mo, tc2::NoMap{}) !=
         cudaSuccess)
       return T3_ECUDA;
     return cudaGetLastError() == cudaSuccess ? T3_OK : T3_ECUDA;
   }
   if (p.mode == tc2::kModeTma)
-    tc2::tc2_kernel<OP, tc2::kModeTma, false><<<grid, tc2::kThreads, kSmem, s>>>(p, ma, mw, mo);
+    tc2::tc2_kernel<OP, tc2::kModeTma, false><<<grid, tc2::kThreads, kSmem, s>>>(p, ma, mw, mo, tc2::NoMap{});
   else if (p.mode == tc2::kModeWGlobal)
-    tc2::tc2_kernel<OP, tc2::kModeWGlobal, false><<<grid, tc2::kThreads, kSmem, s>>>(p, ma, mw, mo);
+    tc2::tc2_kernel<OP, tc2::kModeWGlobal, false><<<grid, tc2::kThreads, kSmem, s>>>(p, ma, mw, mo, tc2::NoMap{});
   else
-    tc2::tc2_kernel<OP, tc2::kModeAGlobal, false><<<grid, tc2::kThreads, kSmem, s>>>(p, ma, mw, mo);
+    tc2::tc2_kernel<OP, tc2::kModeAGlobal, false><<<grid, tc2::kThreads, kSmem, s>>>(p, ma, mw, mo, tc2::NoMap{});
   return cudaGetLastError() == cudaSuccess ? T3_OK : T3_ECUDA;
 }
 

@@ -1,6 +1,6 @@
 // t3_vec.cuh -- what the row, sequence and epilogue kernels share: element
-// types (float, bf16) loaded and stored as vectors of floats, the activations
-// and their derivatives, reductions over a warp, and the launch that lets a
+// types (float, bf16) loaded and stored as vectors of floats, reductions over a
+// warp, and the launch that lets a
 // kernel's set-up overlap the end of the work before it.
 #pragma once
 #include <cuda_bf16.h>
@@ -8,6 +8,7 @@
 #include <cstdint>
 
 #include "t3.h"
+#include "t3_act.cuh"
 #include "t3_internal.h"
 
 namespace t3 {
@@ -157,60 +158,6 @@ __device__ __forceinline__ float warp_max_nan(float v) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) v = max_nan(v, __shfl_xor_sync(0xffffffffu, v, o));
   return v;
-}
-
-// The logistic function from one exponential that cannot overflow, with
-// e = exp(-|z|) and r = 1 / (1 + e):
-//   sigmoid(z) = r for z >= 0 and e r below, sigmoid(-z) the other one,
-//   sigmoid(z) sigmoid(-z) = e r r;
-// each keeps its relative precision however far z is from zero.
-struct Logistic {
-  float pos, neg, slope;  // sigmoid(z), sigmoid(-z), their product
-};
-// exp2 and the reciprocal are the hardware's approximations (2 ulp and 1 ulp),
-// results below the float range flushed to 0.
-__device__ __forceinline__ Logistic logistic(float z) {
-  float e, r;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(-1.4426950408889634f * fabsf(z)));
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + e));
-  const float er = e * r;
-  Logistic s;
-  s.pos = z >= 0.0f ? r : er;
-  s.neg = z >= 0.0f ? er : r;
-  s.slope = er * r;
-  return s;
-}
-
-// Activation ACT of z, and its derivative.  GELU is the tanh form written as
-// z sigmoid(2 u) with u = sqrt(2 / pi) (z + 0.044715 z^3), since
-// (1 + tanh u) / 2 = sigmoid(2 u).
-constexpr float kGeluC = 1.5957691216057308f;  // 2 sqrt(2 / pi)
-constexpr float kGeluA = 0.044715f;
-
-template <int ACT>
-__device__ __forceinline__ float act(float z) {
-  if constexpr (ACT == T3_ACT_RELU) return z < 0.0f ? 0.0f : z;
-  if constexpr (ACT == T3_ACT_RELU2) return z < 0.0f ? 0.0f : z * z;
-  if constexpr (ACT == T3_ACT_SILU) return z * logistic(z).pos;
-  if constexpr (ACT == T3_ACT_GELU) return z * logistic(kGeluC * (z + kGeluA * z * z * z)).pos;
-  return z;
-}
-
-template <int ACT>
-__device__ __forceinline__ float act_slope(float z) {
-  if constexpr (ACT == T3_ACT_RELU) return z > 0.0f ? 1.0f : (z <= 0.0f ? 0.0f : z);
-  if constexpr (ACT == T3_ACT_RELU2) return z < 0.0f ? 0.0f : 2.0f * z;
-  if constexpr (ACT == T3_ACT_SILU) {
-    const Logistic s = logistic(z);
-    return s.slope == 0.0f ? s.pos : fmaf(z, s.slope, s.pos);  // far out: no infinity times zero
-  }
-  if constexpr (ACT == T3_ACT_GELU) {
-    const float z2 = z * z;
-    const Logistic s = logistic(kGeluC * z * fmaf(kGeluA, z2, 1.0f));
-    return s.slope == 0.0f ? s.pos
-                           : fmaf(z * s.slope, kGeluC * fmaf(3.0f * kGeluA, z2, 1.0f), s.pos);
-  }
-  return 1.0f;
 }
 
 // Launches `fn` as a programmatic dependent of the work before it on `s`: the
