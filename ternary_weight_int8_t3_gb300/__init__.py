@@ -150,9 +150,15 @@ def t3_pack_ternary(w) -> np.ndarray:
 
 # ----------------------------------------------------------------- device ---
 
+_torch_module = None
+
+
 def _torch():
-    import torch
-    return torch
+    global _torch_module
+    if _torch_module is None:
+        import torch
+        _torch_module = torch
+    return _torch_module
 
 
 def _dev_ptr(t, dtype, name):
@@ -425,80 +431,104 @@ def t3_gemm_bwd_dw_scaled_noalloc(A, dY, row_scale=None, col_scale=None, kind=T3
 
 # ------------------------------------------- norm, recurrence, epilogue ---
 
+# These calls may run once per token of a serving loop, on a few kilobytes: the
+# checks below read each tensor property once and build nothing.
+
 def _dtype_of(t, name):
     """The element type's code (T3_OUT_F32 or T3_OUT_BF16) of an activation tensor."""
     torch = _torch()
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA tensor")
-    if t.dtype == torch.bfloat16:
+    if t.dtype is torch.bfloat16:
         return T3_OUT_BF16
-    if t.dtype == torch.float32:
+    if t.dtype is torch.float32:
         return T3_OUT_F32
     raise TypeError(f"{name} must be bfloat16 or float32, got {t.dtype}")
 
 
-def _rows(t, like, shape, name, out=False):
-    """(address, row stride) of a tensor [..., cols] whose rows are evenly
-    spaced: `shape` is what it must be, `like` gives dtype and device.  None
-    gives (None, 0)."""
+def _rows(t, dtype, dev, shape, name, out=False):
+    """(address, row stride) of a tensor [..., cols] on device number `dev`
+    whose rows are evenly spaced; None gives (None, 0)."""
     if t is None:
         return None, 0
-    if t.dtype != like.dtype or t.device != like.device:
-        raise TypeError(f"{name} must be a {like.dtype} tensor on {like.device}")
+    if t.dtype is not dtype or t.get_device() != dev:
+        raise TypeError(f"{name} must be a {dtype} tensor on device {dev}")
     if t.shape != shape:
         raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
-    if t.numel() == 0:
-        return None, shape[-1]
     st = t.stride()
-    if shape[-1] > 1 and st[-1] != 1:
+    cols = shape[-1]
+    if st[-1] != 1 and cols > 1 and t.numel():
         raise ValueError(f"{name}: the elements of a row must be adjacent")
-    if len(shape) == 3:  # [batch][length][width]: one stride serves both
-        ld = st[1] if shape[1] > 1 else st[0]
-        if shape[0] > 1 and shape[1] > 1 and st[0] != shape[1] * ld:
-            raise ValueError(f"{name}: sequences must be evenly spaced (stride {st[0]}, not {shape[1] * ld})")
-        if shape[0] == 1 and shape[1] == 1:
-            ld = shape[-1]
-    else:
-        ld = st[0] if shape[0] > 1 else shape[-1]
-    if out and ld < shape[-1]:
-        raise ValueError(f"{name}: output rows must not overlap")
+    if len(shape) == 2:
+        ld = st[0] if shape[0] > 1 else cols
+    else:  # [batch][length][width]: one stride serves both
+        batch, length = shape[0], shape[1]
+        ld = st[1] if length > 1 else st[0] if batch > 1 else cols
+        if batch > 1 and length > 1 and st[0] != length * ld and cols:
+            raise ValueError(f"{name}: sequences must be evenly spaced (stride {st[0]}, not {length * ld})")
+    if ld < cols:
+        if not t.numel():
+            ld = cols
+        elif out:
+            raise ValueError(f"{name}: output rows must not overlap")
     return t.data_ptr(), ld
 
 
-def _dense(t, dtype, like, shape, name):
-    """Address of a contiguous tensor on like's device; None gives None."""
+def _dense(t, dtype, dev, shape, name):
+    """Address of a contiguous tensor on device number `dev`; None gives None."""
     if t is None:
         return None
-    if t.dtype != dtype or t.device != like.device:
-        raise TypeError(f"{name} must be a {dtype} tensor on {like.device}")
+    if t.dtype is not dtype or t.get_device() != dev:
+        raise TypeError(f"{name} must be a {dtype} tensor on device {dev}")
     if t.shape != shape:
         raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
-    return t.data_ptr() if t.numel() else None
+    return t.data_ptr()
 
 
-def _launch(name, like, stream, *args):
-    """Calls the library on like's device, with its current stream unless one is given."""
-    torch = _torch()
-    s = (stream if stream is not None else torch.cuda.current_stream(like.device)).cuda_stream
-    fn = getattr(load() if _lib is None else _lib, name)
-    if like.device.index == torch.cuda.current_device():
+_fns = {}
+_raw_stream = None
+
+
+def _launch(name, dev, stream, *args):
+    """Calls the library on device number `dev`, on its current stream unless one is given."""
+    global _raw_stream
+    fn = _fns.get(name)
+    if fn is None:
+        fn = _fns[name] = getattr(load(), name)
+        # the current stream's handle without a Stream object around it
+        _raw_stream = getattr(_torch()._C, "_cuda_getCurrentRawStream",
+                              lambda d: _torch().cuda.current_stream(d).cuda_stream)
+    s = _raw_stream(dev) if stream is None else stream.cuda_stream
+    cuda = _torch().cuda
+    if dev == cuda.current_device():
         rc = fn(*args, s)
     else:
-        with torch.cuda.device(like.device):
+        with cuda.device(dev):
             rc = fn(*args, s)
     if rc != T3_OK:
         raise T3Error(rc, name)
 
 
-def _workspace(workspace, rows, cols, like):
-    n = (load() if _lib is None else _lib).t3_colsum_workspace(rows, cols)
+def _empty(shape, dtype, dev, stream):
+    """An output or workspace for a call on `stream` (None: the current one):
+    allocated on that stream, so that memory another stream still uses is not
+    handed out, nor this memory to another stream while the call is running."""
+    torch = _torch()
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=dev)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=dev)
+
+
+def _workspace(workspace, rows, cols, dev, stream):
+    n = load().t3_colsum_workspace(rows, cols)
     torch = _torch()
     if workspace is None:
-        return torch.empty(n, dtype=torch.float32, device=like.device)
-    if workspace.dtype != torch.float32 or workspace.device != like.device or not workspace.is_contiguous():
-        raise TypeError(f"workspace must be a contiguous float32 tensor on {like.device}")
+        return _empty(n, torch.float32, dev, stream)
+    if workspace.dtype is not torch.float32 or workspace.get_device() != dev or not workspace.is_contiguous():
+        raise TypeError(f"workspace must be a contiguous float32 tensor on device {dev}")
     if workspace.numel() < n:
         raise ValueError(f"workspace needs {n} floats, has {workspace.numel()}")
     return workspace
@@ -515,24 +545,22 @@ def t3_rmsnorm_quant(x, gamma=None, residual=None, eps=1e-5, q=None, row_scale=N
     dtype = _dtype_of(x, "x")
     if x.dim() != 2:
         raise TypeError("x must be 2-D [rows][cols]")
-    shape = x.shape
+    shape, xt, dev, f32 = x.shape, x.dtype, x.get_device(), torch.float32
     rows, cols = shape
     if q is None:
-        q = torch.empty(shape, dtype=torch.int8, device=x.device)
+        q = _empty(shape, torch.int8, dev, stream)
     if row_scale is None:
-        row_scale = torch.empty(rows, dtype=torch.float32, device=x.device)
+        row_scale = _empty(rows, f32, dev, stream)
     if rstd is None:
-        rstd = torch.empty(rows, dtype=torch.float32, device=x.device)
+        rstd = _empty(rows, f32, dev, stream)
     if sum_out is None and residual is not None:
-        sum_out = torch.empty(shape, dtype=x.dtype, device=x.device)
-    px, ldx = _rows(x, x, shape, "x")
-    pr, ldr = _rows(residual, x, shape, "residual")
-    ps, lds = _rows(sum_out, x, shape, "sum_out", out=True)
-    _launch("t3_rmsnorm_quant", x, stream, px, ldx, pr, ldr,
-            _dense(gamma, torch.float32, x, (cols,), "gamma"), eps,
-            _dense(q, torch.int8, x, shape, "q"),
-            _dense(row_scale, torch.float32, x, (rows,), "row_scale"),
-            _dense(rstd, torch.float32, x, (rows,), "rstd"), ps, lds, rows, cols, dtype)
+        sum_out = _empty(shape, xt, dev, stream)
+    px, ldx = _rows(x, xt, dev, shape, "x")
+    pr, ldr = _rows(residual, xt, dev, shape, "residual")
+    ps, lds = _rows(sum_out, xt, dev, shape, "sum_out", out=True)
+    _launch("t3_rmsnorm_quant", dev, stream, px, ldx, pr, ldr, _dense(gamma, f32, dev, (cols,), "gamma"), eps,
+            _dense(q, torch.int8, dev, shape, "q"), _dense(row_scale, f32, dev, (rows,), "row_scale"),
+            _dense(rstd, f32, dev, (rows,), "rstd"), ps, lds, rows, cols, dtype)
     return q, row_scale, rstd, x if sum_out is None else sum_out
 
 
@@ -544,22 +572,20 @@ def t3_rmsnorm_bwd(dy, s, rstd, gamma=None, dsum=None, dx=None, dgamma=None, wor
     dtype = _dtype_of(dy, "dy")
     if dy.dim() != 2:
         raise TypeError("dy must be 2-D [rows][cols]")
-    shape = dy.shape
+    shape, xt, dev, f32 = dy.shape, dy.dtype, dy.get_device(), torch.float32
     rows, cols = shape
     if dx is None:
-        dx = torch.empty(shape, dtype=dy.dtype, device=dy.device)
+        dx = _empty(shape, xt, dev, stream)
     if dgamma is None and gamma is not None:
-        dgamma = torch.empty(cols, dtype=torch.float32, device=dy.device)
-    ws = None if dgamma is None else _workspace(workspace, rows, cols, dy)
-    pdy, lddy = _rows(dy, dy, shape, "dy")
-    ps, lds = _rows(s, dy, shape, "s")
-    pd, ldd = _rows(dsum, dy, shape, "dsum")
-    px, ldx = _rows(dx, dy, shape, "dx", out=True)
-    _launch("t3_rmsnorm_bwd", dy, stream, pdy, lddy, ps, lds,
-            _dense(rstd, torch.float32, dy, (rows,), "rstd"),
-            _dense(gamma, torch.float32, dy, (cols,), "gamma"), pd, ldd, px, ldx,
-            _dense(dgamma, torch.float32, dy, (cols,), "dgamma"), rows, cols, dtype,
-            None if ws is None else ws.data_ptr())
+        dgamma = _empty(cols, f32, dev, stream)
+    ws = None if dgamma is None else _workspace(workspace, rows, cols, dev, stream)
+    pdy, lddy = _rows(dy, xt, dev, shape, "dy")
+    ps, lds = _rows(s, xt, dev, shape, "s")
+    pd, ldd = _rows(dsum, xt, dev, shape, "dsum")
+    px, ldx = _rows(dx, xt, dev, shape, "dx", out=True)
+    _launch("t3_rmsnorm_bwd", dev, stream, pdy, lddy, ps, lds, _dense(rstd, f32, dev, (rows,), "rstd"),
+            _dense(gamma, f32, dev, (cols,), "gamma"), pd, ldd, px, ldx,
+            _dense(dgamma, f32, dev, (cols,), "dgamma"), rows, cols, dtype, None if ws is None else ws.data_ptr())
     return dx, dgamma
 
 
@@ -573,19 +599,18 @@ def t3_gated_scan_fwd(gate, cand, h0=None, resets=None, h=None, h_last=None, str
     dtype = _dtype_of(gate, "gate")
     if gate.dim() != 3:
         raise TypeError("gate must be 3-D [batch][length][width]")
-    shape = gate.shape
+    shape, xt, dev, f32 = gate.shape, gate.dtype, gate.get_device(), torch.float32
     batch, length, width = shape
     if h is None:
-        h = torch.empty(shape, dtype=gate.dtype, device=gate.device)
+        h = _empty(shape, xt, dev, stream)
     if h_last is None:
-        h_last = torch.empty((batch, width), dtype=torch.float32, device=gate.device)
-    pg, ldg = _rows(gate, gate, shape, "gate")
-    pc, ldc = _rows(cand, gate, shape, "cand")
-    ph, ldh = _rows(h, gate, shape, "h", out=True)
-    _launch("t3_gated_scan_fwd", gate, stream, pg, ldg, pc, ldc,
-            _dense(h0, torch.float32, gate, (batch, width), "h0"),
-            _dense(resets, torch.uint8, gate, (batch, length), "resets"), ph, ldh,
-            _dense(h_last, torch.float32, gate, (batch, width), "h_last"), batch, length, width, dtype)
+        h_last = _empty((batch, width), f32, dev, stream)
+    pg, ldg = _rows(gate, xt, dev, shape, "gate")
+    pc, ldc = _rows(cand, xt, dev, shape, "cand")
+    ph, ldh = _rows(h, xt, dev, shape, "h", out=True)
+    _launch("t3_gated_scan_fwd", dev, stream, pg, ldg, pc, ldc, _dense(h0, f32, dev, (batch, width), "h0"),
+            _dense(resets, torch.uint8, dev, (batch, length), "resets"), ph, ldh,
+            _dense(h_last, f32, dev, (batch, width), "h_last"), batch, length, width, dtype)
     return h, h_last
 
 
@@ -598,26 +623,25 @@ def t3_gated_scan_bwd(gate, cand, h, dh, h0=None, resets=None, dh_last=None, dga
     dtype = _dtype_of(gate, "gate")
     if gate.dim() != 3:
         raise TypeError("gate must be 3-D [batch][length][width]")
-    shape = gate.shape
+    shape, xt, dev, f32 = gate.shape, gate.dtype, gate.get_device(), torch.float32
     batch, length, width = shape
     if dgate is None:
-        dgate = torch.empty(shape, dtype=gate.dtype, device=gate.device)
+        dgate = _empty(shape, xt, dev, stream)
     if dcand is None:
-        dcand = torch.empty(shape, dtype=gate.dtype, device=gate.device)
+        dcand = _empty(shape, xt, dev, stream)
     if dh0 is None:
-        dh0 = torch.empty((batch, width), dtype=torch.float32, device=gate.device)
-    pg, ldg = _rows(gate, gate, shape, "gate")
-    pc, ldc = _rows(cand, gate, shape, "cand")
-    ph, ldh = _rows(h, gate, shape, "h")
-    pd, ldd = _rows(dh, gate, shape, "dh")
-    pdg, lddg = _rows(dgate, gate, shape, "dgate", out=True)
-    pdc, lddc = _rows(dcand, gate, shape, "dcand", out=True)
-    f32 = torch.float32
-    _launch("t3_gated_scan_bwd", gate, stream, pg, ldg, pc, ldc, ph, ldh, pd, ldd,
-            _dense(h0, f32, gate, (batch, width), "h0"),
-            _dense(resets, torch.uint8, gate, (batch, length), "resets"),
-            _dense(dh_last, f32, gate, (batch, width), "dh_last"), pdg, lddg, pdc, lddc,
-            _dense(dh0, f32, gate, (batch, width), "dh0"), batch, length, width, dtype)
+        dh0 = _empty((batch, width), f32, dev, stream)
+    pg, ldg = _rows(gate, xt, dev, shape, "gate")
+    pc, ldc = _rows(cand, xt, dev, shape, "cand")
+    ph, ldh = _rows(h, xt, dev, shape, "h")
+    pd, ldd = _rows(dh, xt, dev, shape, "dh")
+    pdg, lddg = _rows(dgate, xt, dev, shape, "dgate", out=True)
+    pdc, lddc = _rows(dcand, xt, dev, shape, "dcand", out=True)
+    _launch("t3_gated_scan_bwd", dev, stream, pg, ldg, pc, ldc, ph, ldh, pd, ldd,
+            _dense(h0, f32, dev, (batch, width), "h0"),
+            _dense(resets, torch.uint8, dev, (batch, length), "resets"),
+            _dense(dh_last, f32, dev, (batch, width), "dh_last"), pdg, lddg, pdc, lddc,
+            _dense(dh0, f32, dev, (batch, width), "dh0"), batch, length, width, dtype)
     return dgate, dcand, dh0
 
 
@@ -628,29 +652,26 @@ def t3_gemm_fwd_act(A, Wp, K=None, row_scale=None, col_scale=None, bias=None, ac
     T3_OUT_BF16, the type of C, residual and pre [M][N].  workspace: int32
     [M][N], allocated when the call may need one and none is given."""
     torch = _torch()
+    if not isinstance(A, torch.Tensor) or not A.is_cuda or A.dim() != 2 or Wp.dim() != 2:
+        raise TypeError("A and Wp must be 2-D CUDA tensors")
     M, Ka = A.shape
+    N, KB = Wp.shape
     K = Ka if K is None else K
-    if Ka != K:
-        raise ValueError("A must be [M][K]")
-    if Wp.dim() != 2 or Wp.shape[1] != (K + 3) // 4:
-        raise ValueError("Wp must be [N][ceil(K/4)]")
-    if not A.is_cuda:
-        raise TypeError("A must be a CUDA tensor")
+    if Ka != K or KB != (K + 3) // 4:
+        raise ValueError("A must be [M][K] and Wp [N][ceil(K/4)]")
     if kind not in (T3_OUT_F32, T3_OUT_BF16):
         raise ValueError(f"unknown output kind {kind}")
-    N = Wp.shape[0]
-    dtype = torch.bfloat16 if kind == T3_OUT_BF16 else torch.float32
+    dev, f32, shape = A.get_device(), torch.float32, (M, N)
+    dtype = torch.bfloat16 if kind == T3_OUT_BF16 else f32
     if C is None:
-        C = torch.empty((M, N), dtype=dtype, device=A.device)
+        C = _empty(shape, dtype, dev, stream)
     if workspace is None and kind == T3_OUT_BF16:
-        workspace = torch.empty((M, N), dtype=torch.int32, device=A.device)
-    f32 = torch.float32
-    _launch("t3_gemm_fwd_act", A, stream, _dense(A, torch.int8, A, (M, K), "A"),
-            _dense(Wp, torch.uint8, A, (N, (K + 3) // 4), "Wp"), _dense(C, dtype, A, (M, N), "C"), M, N, K,
-            _dense(row_scale, f32, A, (M,), "row_scale"), _dense(col_scale, f32, A, (N,), "col_scale"),
-            _dense(bias, f32, A, (N,), "bias"), act, _dense(residual, dtype, A, (M, N), "residual"),
-            _dense(pre, dtype, A, (M, N), "pre"), kind,
-            _dense(workspace, torch.int32, A, (M, N), "workspace"))
+        workspace = _empty(shape, torch.int32, dev, stream)
+    _launch("t3_gemm_fwd_act", dev, stream, _dense(A, torch.int8, dev, (M, K), "A"),
+            _dense(Wp, torch.uint8, dev, (N, KB), "Wp"), _dense(C, dtype, dev, shape, "C"), M, N, K,
+            _dense(row_scale, f32, dev, (M,), "row_scale"), _dense(col_scale, f32, dev, (N,), "col_scale"),
+            _dense(bias, f32, dev, (N,), "bias"), act, _dense(residual, dtype, dev, shape, "residual"),
+            _dense(pre, dtype, dev, shape, "pre"), kind, _dense(workspace, torch.int32, dev, shape, "workspace"))
     return C
 
 
@@ -662,16 +683,15 @@ def t3_act_bwd(dy, z, act, dz=None, dbias=None, workspace=None, stream=None):
     dtype = _dtype_of(dy, "dy")
     if dy.dim() != 2:
         raise TypeError("dy must be 2-D [rows][cols]")
-    shape = dy.shape
+    shape, xt, dev = dy.shape, dy.dtype, dy.get_device()
     rows, cols = shape
     if z is None and act != T3_ACT_NONE:
         raise ValueError("z is needed for this activation")
     if dz is None:
-        dz = torch.empty(shape, dtype=dy.dtype, device=dy.device)
-    ws = None if dbias is None else _workspace(workspace, rows, cols, dy)
-    _launch("t3_act_bwd", dy, stream, _dense(dy, dy.dtype, dy, shape, "dy"),
-            _dense(z, dy.dtype, dy, shape, "z"), act, _dense(dz, dy.dtype, dy, shape, "dz"),
-            _dense(dbias, torch.float32, dy, (cols,), "dbias"), rows, cols, dtype,
+        dz = _empty(shape, xt, dev, stream)
+    ws = None if dbias is None else _workspace(workspace, rows, cols, dev, stream)
+    _launch("t3_act_bwd", dev, stream, _dense(dy, xt, dev, shape, "dy"), _dense(z, xt, dev, shape, "z"), act,
+            _dense(dz, xt, dev, shape, "dz"), _dense(dbias, torch.float32, dev, (cols,), "dbias"), rows, cols, dtype,
             None if ws is None else ws.data_ptr())
     return dz, dbias
 

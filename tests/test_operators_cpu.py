@@ -125,21 +125,25 @@ def test_binding_rejects_cpu_tensors_and_types():
 
 
 def test_row_strides_of_the_binding():
-    """_rows on CPU tensors: what counts as evenly spaced rows."""
+    """_rows on CPU tensors (device -1): what counts as evenly spaced rows."""
     torch = pytest.importorskip("torch")
-    x = torch.zeros((2, 3, 8))
+
+    def rows(t, shape, **kw):
+        return t3._rows(t, torch.float32, -1, shape, "t", **kw)
     both = torch.zeros((2, 3, 16))
-    assert t3._rows(both[..., 8:], x, x.shape, "c") == (both.data_ptr() + 32, 16)
-    assert t3._rows(torch.zeros((4, 8))[::2], torch.zeros(1), (2, 8), "x")[1] == 16
-    wide = torch.zeros((3, 3, 8))[::2]
-    with pytest.raises(ValueError):
-        t3._rows(wide, x, x.shape, "gap between sequences")
-    with pytest.raises(ValueError):
-        t3._rows(torch.zeros((8, 4)).t(), torch.zeros(1), (4, 8), "columns not adjacent")
-    with pytest.raises(ValueError):
-        t3._rows(torch.zeros((1, 8)).expand(4, 8), torch.zeros(1), (4, 8), "overlapping output", out=True)
-    assert t3._rows(torch.zeros((1, 8)).expand(4, 8), torch.zeros(1), (4, 8), "broadcast input")[1] == 0
-    assert t3._rows(torch.zeros((2, 1, 16))[..., :8], torch.zeros(1), (2, 1, 8), "token")[1] == 16
+    assert rows(both[..., 8:], (2, 3, 8)) == (both.data_ptr() + 32, 16)
+    assert rows(torch.zeros((4, 8))[::2], (2, 8))[1] == 16
+    with pytest.raises(ValueError):  # a gap between sequences
+        rows(torch.zeros((3, 3, 8))[::2], (2, 3, 8))
+    with pytest.raises(ValueError):  # columns not adjacent
+        rows(torch.zeros((8, 4)).t(), (4, 8))
+    with pytest.raises(ValueError):  # overlapping output
+        rows(torch.zeros((1, 8)).expand(4, 8), (4, 8), out=True)
+    assert rows(torch.zeros((1, 8)).expand(4, 8), (4, 8))[1] == 0
+    assert rows(torch.zeros((2, 1, 16))[..., :8], (2, 1, 8))[1] == 16
+    assert rows(torch.zeros((2, 0, 8)), (2, 0, 8), out=True)[1] >= 8
+    with pytest.raises(TypeError):
+        rows(both.double(), (2, 3, 16))
 
 
 # ------------------------------------------- gradients against differences ---
