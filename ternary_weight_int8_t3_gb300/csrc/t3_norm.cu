@@ -13,22 +13,28 @@
 // n = dy gamma:
 //   dx = rstd (n - s rstd^2 mean(n s)) + dsum,   dgamma = sum over rows of dy s rstd
 //
-// What bounds it: memory.  A row is read once, kept in registers between the
-// reductions and the output, and written once.  Rows of up to 1024 elements
-// (512 floats) take one warp, longer ones a CTA whose threads each hold one, two
-// or four 16-byte vectors; rows that 16-byte vectors cannot address (odd
-// widths, strides or bases) go element by element; rows longer than the
-// registers hold are read twice.  dgamma: each CTA of a persistent grid holds
-// its columns' sums in registers over all its rows, writes one partial row,
-// and a second small kernel adds the partial rows in a fixed order.
+// What bounds it: memory.  A row is read once and written once:
+//   * many rows: a persistent grid whose CTAs take rows in turn, each row copied
+//     ahead into a ring of shared-memory stages by one bulk copy an array, so
+//     that the loads in flight do not depend on registers or warps; the
+//     threads read it from there for the reductions and again for the output.
+//     Rows that do not start on 16 bytes (odd widths or strides) are copied
+//     with the aligned bytes around them, which belong to the matrix too, and read
+//     element by element;
+//   * few rows (a serving step): a CTA a row, every thread with as few elements
+//     in registers as 1024 threads allow, loaded directly;
+//   * rows longer than either holds are read twice.
+// dgamma: each CTA holds its columns' sums in registers over all its rows,
+// writes one partial row, and a second small kernel adds the partial rows in
+// a fixed order.
+#include <atomic>
+
 #include "t3_vec.cuh"
 
 namespace t3 {
 namespace nm {
 
 using namespace vec;
-
-constexpr int kWarpRows = 8;  // rows per CTA where a warp takes a row
 
 // Threads a CTA may have when each holds EPT elements of a row: up to 16384
 // elements a row forward (one float an element is kept) and 8192 backward (the
@@ -45,6 +51,7 @@ struct FwdArgs {
   float *row_scale, *rstd;
   void* sum_out;
   int64_t rows, cols;
+  int* err;
 };
 
 struct BwdArgs {
@@ -54,6 +61,7 @@ struct BwdArgs {
   void* dx;
   float* partial;  // [gridDim.x][cols], null without dgamma
   int64_t rows, cols;
+  int* err;
 };
 
 __device__ __forceinline__ int quant(float u, float inv) {
@@ -61,23 +69,31 @@ __device__ __forceinline__ int quant(float u, float inv) {
   return q > 127 ? 127 : (q < -127 ? -127 : q);
 }
 
-// A row's two results from its reductions.  Elements that are not finite, or
-// whose squares overflow the sum, make the row's scale NaN and its codes 0.
-struct RowScale {
-  float rstd, scale, inv;
-};
-__device__ __forceinline__ RowScale row_scale_of(float ssq, float amax, float eps, int64_t cols) {
-  RowScale o;
-  o.rstd = __fdiv_rn(1.0f, __fsqrt_rn(cols > 0 ? __fdiv_rn(ssq, static_cast<float>(cols)) + eps : eps));
+// 127 / max|u|, or 0 for a row of zeros or one that is not finite: an element
+// of u is not, or the squares overflow their sum.
+__device__ __forceinline__ float inverse_of(float ssq, float amax) {
   const bool finite = ssq < __int_as_float(0x7f800000) && amax < __int_as_float(0x7f800000);
-  if (!finite) {
-    o.scale = __int_as_float(0x7fffffff);
-    o.inv = 0.0f;
-  } else {
-    o.scale = __fdiv_rn(__fmul_rn(amax, o.rstd), 127.0f);
-    o.inv = amax > 0.0f ? __fdiv_rn(127.0f, amax) : 0.0f;
-  }
-  return o;
+  return finite && amax > 0.0f ? __fdiv_rn(127.0f, amax) : 0.0f;
+}
+
+// One thread: the row's scale (NaN where it is not finite) and rstd.
+__device__ __forceinline__ void put_scales(const FwdArgs& p, int64_t row, float ssq, float amax) {
+  const float rstd =
+      __fdiv_rn(1.0f, __fsqrt_rn(p.cols > 0 ? __fdiv_rn(ssq, static_cast<float>(p.cols)) + p.eps : p.eps));
+  const bool finite = ssq < __int_as_float(0x7f800000) && amax < __int_as_float(0x7f800000);
+  p.row_scale[row] = finite ? __fdiv_rn(__fmul_rn(amax, rstd), 127.0f) : __int_as_float(0x7fffffff);
+  if (p.rstd) p.rstd[row] = rstd;
+}
+
+// Four codes of four floats u * inv that lie in [-127, 127]: adding 1.5 * 2^23
+// rounds to the nearest integer, ties to even, into the low bits.
+__device__ __forceinline__ uint32_t quant4(float a, float b, float c, float d, float inv) {
+  constexpr float kMagic = 12582912.0f;
+  const uint32_t x = __float_as_uint(__fadd_rn(__fmul_rn(a, inv), kMagic));
+  const uint32_t y = __float_as_uint(__fadd_rn(__fmul_rn(b, inv), kMagic));
+  const uint32_t z = __float_as_uint(__fadd_rn(__fmul_rn(c, inv), kMagic));
+  const uint32_t w = __float_as_uint(__fadd_rn(__fmul_rn(d, inv), kMagic));
+  return prmt(prmt(x, y, 0x0040u), prmt(z, w, 0x0040u), 0x5410u);
 }
 
 // Sum of `a` and NaN-keeping maximum of `b` over the CTA's threads; `sm` holds
@@ -93,85 +109,107 @@ __device__ __forceinline__ void cta_reduce(float& a, float& b, float* sm) {
     sm[32 + warp] = b;
   }
   __syncthreads();
+  if (warps <= 4) {  // reading them all beats five more shuffles of each
+    a = sm[0];
+    b = sm[32];
+    for (int i = 1; i < warps; ++i) {
+      a += sm[i];
+      b = max_nan(b, sm[32 + i]);
+    }
+    return;
+  }
   a = warp_sum(lane < warps ? sm[lane] : 0.0f);
   b = warp_max_nan(lane < warps ? sm[32 + lane] : 0.0f);
 }
 
-template <class T, int VEC, int NV, bool kWarp>
-__global__ void __launch_bounds__(kWarp ? 32 * kWarpRows : fwd_threads(NV * VEC)) norm_fwd_kernel(const FwdArgs p) {
+template <class T, int VEC, int NV>
+__global__ void __launch_bounds__(fwd_threads(NV * VEC)) norm_fwd_kernel(const FwdArgs p) {
   __shared__ float sm[2][64];
-  const int lanes = kWarp ? 32 : blockDim.x;
-  const int tid = kWarp ? (threadIdx.x & 31) : threadIdx.x;
-  const int per = kWarp ? kWarpRows : 1;
-  const int64_t step = static_cast<int64_t>(gridDim.x) * per;
-  int phase = 0;
+  const int lanes = blockDim.x, cols = static_cast<int>(p.cols);
   launch_dependents();
   grid_dependency_wait();
-  for (int64_t row = static_cast<int64_t>(blockIdx.x) * per + (kWarp ? threadIdx.x >> 5 : 0); row < p.rows;
-       row += step, phase ^= 1) {
+  // this thread's columns: their gains, and the next row's operands, which are on
+  // their way while this row is reduced and written
+  float g[NV][VEC];
+  Raw<T, VEC> xr[NV], rr[NV];
+  auto fetch = [&](int64_t row) {
     const T* x = static_cast<const T*>(p.x) + row * p.ldx;
     const T* r = static_cast<const T*>(p.residual) + row * p.ldr;
-    T* so = static_cast<T*>(p.sum_out) + row * p.lds;
-    Raw<T, VEC> xr[NV], rr[NV];
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
-      const int k = (v * lanes + tid) * VEC;
+      const int k = (v * lanes + threadIdx.x) * VEC;
       xr[v] = zero<T, VEC>();
       rr[v] = zero<T, VEC>();
-      if (k < p.cols) {
+      if (k < cols && row < p.rows) {
         xr[v] = load<T, VEC>(x + k);
         if (p.residual) rr[v] = load<T, VEC>(r + k);
       }
     }
-    float u[NV][VEC];
-    float ssq = 0.0f, amax = 0.0f;
+  };
+  fetch(blockIdx.x);
+#pragma unroll
+  for (int v = 0; v < NV; ++v) {
+    const int k = (v * lanes + threadIdx.x) * VEC;
+#pragma unroll
+    for (int j = 0; j < VEC; ++j) g[v][j] = 1.0f;
+    if (p.gamma && k < cols) load_floats<VEC>(p.gamma + k, g[v]);
+  }
+  int phase = 0;
+  for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x, phase ^= 1) {
+    T* so = static_cast<T*>(p.sum_out) + row * p.lds;
+    float u[NV][VEC], ssq = 0.0f, amax = 0.0f;
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
-      const int k = (v * lanes + tid) * VEC;
-      float s[VEC], g[VEC];
+      const int k = (v * lanes + threadIdx.x) * VEC;
+      float s[VEC], t[VEC];
       to_float(xr[v], s);
       if (p.residual) {
-        to_float(rr[v], g);
+        to_float(rr[v], t);
 #pragma unroll
-        for (int j = 0; j < VEC; ++j) s[j] = round_to(s[j] + g[j], T());
+        for (int j = 0; j < VEC; ++j) s[j] += t[j];
       }
-      if (k < p.cols) {
-        if (p.sum_out) store<T, VEC>(so + k, from_float(s, T()));
-        if (p.gamma) load_floats<VEC>(p.gamma + k, g);
-      }
+      const Raw<T, VEC> w = from_float(s, T());
+      to_float(w, s);
+      if (p.sum_out && k < cols) store<T, VEC>(so + k, w);
 #pragma unroll
       for (int j = 0; j < VEC; ++j) {
         ssq = fmaf(s[j], s[j], ssq);
-        u[v][j] = p.gamma && k < p.cols ? __fmul_rn(s[j], g[j]) : s[j];
+        u[v][j] = __fmul_rn(s[j], g[v][j]);
         amax = max_nan(amax, fabsf(u[v][j]));
       }
     }
-    if constexpr (kWarp) {
-      ssq = warp_sum(ssq);
-      amax = warp_max_nan(amax);
-    } else {
-      cta_reduce(ssq, amax, sm[phase]);
-    }
-    const RowScale o = row_scale_of(ssq, amax, p.eps, p.cols);
-    if (tid == 0) {
-      p.row_scale[row] = o.scale;
-      if (p.rstd) p.rstd[row] = o.rstd;
-    }
+    fetch(row + gridDim.x);
+    cta_reduce(ssq, amax, sm[phase]);
+    const float inv = inverse_of(ssq, amax);
+    if (threadIdx.x == 0) put_scales(p, row, ssq, amax);
     int8_t* q = p.q + row * p.cols;
+    // u * inv within [-127, 127]: not for rows that are not finite (codes 0) nor
+    // for maxima so small that 127 / max overflows
+    const bool plain = inv > 0.0f && inv < __int_as_float(0x7f800000);
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
-      const int k = (v * lanes + tid) * VEC;
-      if (k >= p.cols) break;
-      uint32_t w[(VEC + 3) / 4] = {};
+      const int k = (v * lanes + threadIdx.x) * VEC;
+      if (k >= cols) break;
+      if constexpr (VEC == 1) {
+        q[k] = static_cast<int8_t>(quant(u[v][0], inv));
+      } else {
+        uint32_t w[VEC / 4];
 #pragma unroll
-      for (int j = 0; j < VEC; ++j)
-        w[j / 4] |= static_cast<uint32_t>(quant(u[v][j], o.inv) & 0xFF) << (8 * (j & 3));
-      if constexpr (VEC == 8)
-        *reinterpret_cast<uint2*>(q + k) = make_uint2(w[0], w[1]);
-      else if constexpr (VEC == 4)
-        *reinterpret_cast<uint32_t*>(q + k) = w[0];
-      else
-        q[k] = static_cast<int8_t>(w[0]);
+        for (int j = 0; j < VEC / 4; ++j) {
+          if (plain) {
+            w[j] = quant4(u[v][4 * j], u[v][4 * j + 1], u[v][4 * j + 2], u[v][4 * j + 3], inv);
+          } else {
+            w[j] = 0;
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              w[j] |= static_cast<uint32_t>(quant(u[v][4 * j + i], inv) & 0xFF) << (8 * i);
+          }
+        }
+        if constexpr (VEC == 8)
+          *reinterpret_cast<uint2*>(q + k) = make_uint2(w[0], w[1]);
+        else
+          *reinterpret_cast<uint32_t*>(q + k) = w[0];
+      }
     }
   }
 }
@@ -203,11 +241,8 @@ __global__ void __launch_bounds__(1024) norm_fwd_long_kernel(const FwdArgs p) {
       amax = max_nan(amax, fabsf(p.gamma ? __fmul_rn(s[0], __ldg(p.gamma + k)) : s[0]));
     }
     cta_reduce(ssq, amax, sm[phase]);
-    const RowScale o = row_scale_of(ssq, amax, p.eps, p.cols);
-    if (threadIdx.x == 0) {
-      p.row_scale[row] = o.scale;
-      if (p.rstd) p.rstd[row] = o.rstd;
-    }
+    const float inv = inverse_of(ssq, amax);
+    if (threadIdx.x == 0) put_scales(p, row, ssq, amax);
     for (int64_t k = threadIdx.x; k < p.cols; k += blockDim.x) {
       float s[1];
       if (p.sum_out)
@@ -215,20 +250,15 @@ __global__ void __launch_bounds__(1024) norm_fwd_long_kernel(const FwdArgs p) {
       else
         s[0] = sum_at(k);
       p.q[row * p.cols + k] =
-          static_cast<int8_t>(quant(p.gamma ? __fmul_rn(s[0], __ldg(p.gamma + k)) : s[0], o.inv));
+          static_cast<int8_t>(quant(p.gamma ? __fmul_rn(s[0], __ldg(p.gamma + k)) : s[0], inv));
     }
   }
 }
 
-template <class T, int VEC, int NV, bool kWarp>
-__global__ void __launch_bounds__(kWarp ? 32 * kWarpRows : bwd_threads(NV * VEC)) norm_bwd_kernel(const BwdArgs p) {
+template <class T, int VEC, int NV>
+__global__ void __launch_bounds__(bwd_threads(NV * VEC)) norm_bwd_kernel(const BwdArgs p) {
   __shared__ float sm[2][64];
-  extern __shared__ float sums[];  // kWarp: [cols], the CTA's column sums
-  const int lanes = kWarp ? 32 : blockDim.x;
-  const int tid = kWarp ? (threadIdx.x & 31) : threadIdx.x;
-  const int warp = threadIdx.x >> 5;
-  const int per = kWarp ? kWarpRows : 1;
-  const int64_t step = static_cast<int64_t>(gridDim.x) * per;
+  const int lanes = blockDim.x, tid = threadIdx.x;
   int phase = 0;
   float g[NV][VEC], acc[NV][VEC];
   launch_dependents();
@@ -244,8 +274,7 @@ __global__ void __launch_bounds__(kWarp ? 32 * kWarpRows : bwd_threads(NV * VEC)
     if (p.gamma && k < p.cols) load_floats<VEC>(p.gamma + k, g[v]);
   }
   const float inv_cols = 1.0f / static_cast<float>(p.cols);
-  for (int64_t row = static_cast<int64_t>(blockIdx.x) * per + (kWarp ? warp : 0); row < p.rows;
-       row += step, phase ^= 1) {
+  for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x, phase ^= 1) {
     const T* dy = static_cast<const T*>(p.dy) + row * p.lddy;
     const T* sp = static_cast<const T*>(p.s) + row * p.lds;
     const T* ds = static_cast<const T*>(p.dsum) + row * p.lddsum;
@@ -275,10 +304,7 @@ __global__ void __launch_bounds__(kWarp ? 32 * kWarpRows : bwd_threads(NV * VEC)
         acc[v][j] = fmaf(a[j], s[j] * rstd, acc[v][j]);
       }
     }
-    if constexpr (kWarp)
-      dot = warp_sum(dot);
-    else
-      cta_reduce(dot, unused, sm[phase]);
+    cta_reduce(dot, unused, sm[phase]);
     // rstd s bounded by sqrt(cols) / |s|: scale before squaring
     const float c = rstd * (dot * rstd * inv_cols);
     T* dx = static_cast<T*>(p.dx) + row * p.lddx;
@@ -297,29 +323,12 @@ __global__ void __launch_bounds__(kWarp ? 32 * kWarpRows : bwd_threads(NV * VEC)
   }
   if (!p.partial) return;
   float* out = p.partial + static_cast<int64_t>(blockIdx.x) * p.cols;
-  if constexpr (kWarp) {
-    // the CTA's warps add their sums in turn, in a fixed order
-    for (int w = 0; w < kWarpRows; ++w) {
-      if (warp == w) {
 #pragma unroll
-        for (int v = 0; v < NV; ++v) {
-          const int k = (v * lanes + tid) * VEC;
+  for (int v = 0; v < NV; ++v) {
+    const int k = (v * lanes + tid) * VEC;
 #pragma unroll
-          for (int j = 0; j < VEC; ++j)
-            if (k + j < p.cols) sums[k + j] = (w ? sums[k + j] : 0.0f) + acc[v][j];
-        }
-      }
-      __syncthreads();
-    }
-    for (int64_t k = threadIdx.x; k < p.cols; k += blockDim.x) out[k] = sums[k];
-  } else {
-#pragma unroll
-    for (int v = 0; v < NV; ++v) {
-      const int k = (v * lanes + tid) * VEC;
-#pragma unroll
-      for (int j = 0; j < VEC; ++j)
-        if (k + j < p.cols) out[k + j] = acc[v][j];
-    }
+    for (int j = 0; j < VEC; ++j)
+      if (k + j < p.cols) out[k + j] = acc[v][j];
   }
 }
 
@@ -385,90 +394,334 @@ __global__ void __launch_bounds__(256) norm_dgamma_kernel(const BwdArgs p, int p
   }
 }
 
-// How a row of `units` vectors is dealt to threads.  Many rows (two an SM or
-// more): a warp a row up to MAXNV vectors a lane, else the fewest vectors a
-// thread that leave the CTA at 256 threads, so that several CTAs an SM overlap
-// their barriers.  Few rows: the fewest vectors a thread that fit a CTA, for
-// the shortest time to one row.
-struct Shape {
-  bool warp;
-  int nv, threads;
+// ------------------------------------------------- many rows: a ring of rows
+
+constexpr int kMaxStages = 4;
+constexpr int kWaitCode = (12 << 8) | 7;
+// Bytes of a ring: up to four stages within kRingBytes (two CTAs an SM), two
+// stages of the longest rows within kRingMost.
+constexpr int64_t kRingBytes = 100 * 1024, kRingMost = 200 * 1024;
+
+// One array of rows in the ring.  kAligned: rows of whole 16-byte pieces on
+// 16-byte boundaries.  Any other row is copied from the boundary at or before it
+// to the one at or behind its end; where those bytes are not all the matrix's
+// own (its first and last row, when the matrix starts or ends elsewhere), the
+// threads copy the row themselves.
+template <class T, bool kAligned>
+struct Rows {
+  const T* base;
+  int64_t ld, rows;
+  int cols;
+  __device__ __forceinline__ uint64_t addr(int64_t row) const { return reinterpret_cast<uint64_t>(base + row * ld); }
+  __device__ __forceinline__ int shift(int64_t row) const { return kAligned ? 0 : static_cast<int>(addr(row) & 15); }
+  __device__ __forceinline__ uint32_t bytes(int64_t row) const {
+    return (static_cast<uint32_t>(shift(row) + cols * static_cast<int>(sizeof(T))) + 15u) & ~15u;
+  }
+  __device__ __forceinline__ bool bulk(int64_t row) const {
+    if (kAligned) return true;
+    const uint64_t a = addr(row) - shift(row), end = reinterpret_cast<uint64_t>(base + (rows - 1) * ld + cols);
+    return a >= reinterpret_cast<uint64_t>(base) && a + bytes(row) <= end;
+  }
 };
 
-template <int VEC, int MAXNV>
-bool pick(int64_t units, int64_t rows, int sms, int (*max_threads)(int), Shape& s) {
-  const bool many = rows >= 2 * static_cast<int64_t>(sms);
-  s.warp = many && units <= 32 * MAXNV;
-  if (s.warp) {
-    s.nv = units <= 32 * (MAXNV / 4) ? MAXNV / 4 : units <= 32 * (MAXNV / 2) ? MAXNV / 2 : MAXNV;
-    s.threads = 32 * kWarpRows;
+__device__ __forceinline__ void bulk_load(void* dst, uint64_t src, uint32_t bytes, uint64_t* bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                   smem_addr(dst)),
+               "l"(src), "r"(bytes), "r"(smem_addr(bar))
+               : "memory");
+}
+
+// A CTA's ring over NA arrays: rows blockIdx.x, + gridDim.x, ... take the stages
+// in turn, each array `pitch` bytes from the last.
+template <class T, int NA, bool kAligned>
+struct Ring {
+  Rows<T, kAligned> a[NA];
+  bool on[NA];  // arrays that are there
+  uint8_t* smem;
+  uint64_t* full;
+  int stages, pitch;
+  int* err;
+  volatile int* abort_flag;
+  bool failed;
+  int stage;        // of the row at hand
+  uint32_t parity;  // of its barrier
+
+  __device__ __forceinline__ uint8_t* at(int st, int i) const { return smem + (st * NA + i) * pitch; }
+  // One thread: the copies of a row into stage st.
+  __device__ __forceinline__ void issue(int st, int64_t row) {
+    uint32_t total = 0;
+#pragma unroll
+    for (int i = 0; i < NA; ++i)
+      if (on[i] && a[i].bulk(row)) total += a[i].bytes(row);
+    mbar_arrive_expect_tx(&full[st], total);
+#pragma unroll
+    for (int i = 0; i < NA; ++i)
+      if (on[i] && a[i].bulk(row)) bulk_load(at(st, i), a[i].addr(row) - a[i].shift(row), a[i].bytes(row), &full[st]);
+  }
+  // One thread, before the first row: all stages but one.
+  __device__ __forceinline__ void start(int64_t first, int64_t each) {
+    for (int i = 0; i < stages - 1; ++i)
+      if (first + i * each < a[0].rows) issue(i, first + i * each);
+  }
+  // One thread, at the top of a row: the row stages - 1 turns on goes where the
+  // last one was, which all threads have left.
+  __device__ __forceinline__ void ahead(int64_t row, int64_t each) {
+    const int64_t r = row + (stages - 1) * each;
+    if (r < a[0].rows) issue(stage == 0 ? stages - 1 : stage - 1, r);
+  }
+  // All threads: the row is in its stage.
+  __device__ __forceinline__ void wait(int64_t row) {
+    if (!failed) failed = !mbar_wait(&full[stage], parity, abort_flag, err, kWaitCode);
+    if (kAligned) return;
+    bool direct = false;
+#pragma unroll
+    for (int i = 0; i < NA; ++i)
+      if (on[i] && !a[i].bulk(row)) {
+        direct = true;
+        T* dst = reinterpret_cast<T*>(at(stage, i) + a[i].shift(row));
+        const T* src = a[i].base + row * a[i].ld;
+        for (int k = threadIdx.x; k < a[i].cols; k += blockDim.x) dst[k] = src[k];
+      }
+    if (direct) __syncthreads();
+  }
+  __device__ __forceinline__ T* row(int64_t r, int i) const {
+    return reinterpret_cast<T*>(at(stage, i) + a[i].shift(r));
+  }
+  // All threads, behind a barrier (of the warp or the CTA) after wait(): whether
+  // any of them gave up.  Then the copies in flight get one more, short, wait.
+  __device__ __forceinline__ bool given_up() {
+    __syncwarp();
+    if (!*abort_flag) return false;
+    for (int i = 0; i < stages; ++i)
+      mbar_wait(&full[(stage + i) % stages], stage + i < stages ? parity : parity ^ 1u, abort_flag, err, kWaitCode);
     return true;
   }
-  for (int pass = many ? 0 : 1; pass < 2; ++pass)
-    for (s.nv = MAXNV / 4; s.nv <= MAXNV; s.nv *= 2) {
-      const int64_t t = (units + s.nv - 1) / s.nv;
-      if (t <= (pass ? max_threads(s.nv * VEC) : 256)) {
-        s.threads = t > 0 ? static_cast<int>((t + 31) / 32 * 32) : 32;
-        return true;
+  // All threads, behind their last access to the stage.
+  __device__ __forceinline__ void leave() {
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // before the next bulk copy into it
+    __syncthreads();
+    if (++stage == stages) {
+      stage = 0;
+      parity ^= 1u;
+    }
+  }
+};
+
+// Shared memory of a ring: the barriers and the abort flag, then the stages.
+constexpr int kRingHead = 64;
+
+template <class T, int NA, bool kAligned>
+__device__ __forceinline__ void open_ring(Ring<T, NA, kAligned>& r, uint8_t* smem, int stages, int pitch, int* err) {
+  r.full = reinterpret_cast<uint64_t*>(smem);
+  int* flag = reinterpret_cast<int*>(smem + 8 * kMaxStages);
+  r.abort_flag = flag;
+  r.smem = smem + kRingHead;
+  r.stages = stages;
+  r.pitch = pitch;
+  r.err = err;
+  r.failed = false;
+  r.stage = 0;
+  r.parity = 0;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < stages; ++i) mbar_init(&r.full[i], 1);
+    *flag = 0;
+    fence_mbarrier_init();
+    fence_proxy_async_smem();
+  }
+  __syncthreads();
+}
+
+template <class T, int VEC, int NV>
+__global__ void __launch_bounds__(512) norm_bwd_ring_kernel(const BwdArgs p, int stages, int pitch) {
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ float sm[2][64];
+  const int cols = static_cast<int>(p.cols);
+  Ring<T, 3, (VEC > 1)> ring;
+  ring.a[0] = {static_cast<const T*>(p.dy), p.lddy, p.rows, cols};
+  ring.a[1] = {static_cast<const T*>(p.s), p.lds, p.rows, cols};
+  ring.a[2] = {static_cast<const T*>(p.dsum), p.lddsum, p.rows, cols};
+  ring.on[0] = ring.on[1] = true;
+  ring.on[2] = p.dsum != nullptr;
+  open_ring(ring, smem, stages, pitch, p.err);
+  launch_dependents();
+  grid_dependency_wait();
+  const int64_t first = blockIdx.x, each = gridDim.x;
+  if (threadIdx.x == 0) ring.start(first, each);
+  float g[NV][VEC], acc[NV][VEC];
+#pragma unroll
+  for (int v = 0; v < NV; ++v) {
+    const int k = (v * blockDim.x + threadIdx.x) * VEC;
+#pragma unroll
+    for (int j = 0; j < VEC; ++j) {
+      g[v][j] = 1.0f;
+      acc[v][j] = 0.0f;
+    }
+    if (p.gamma && k < cols) load_floats<VEC>(p.gamma + k, g[v]);
+  }
+  const float inv_cols = 1.0f / static_cast<float>(p.cols);
+  float next_rstd = first < p.rows ? p.rstd[first] : 0.0f;
+  int phase = 0;
+  for (int64_t row = first; row < p.rows; row += each, phase ^= 1) {
+    if (threadIdx.x == 0) ring.ahead(row, each);
+    const float rstd = next_rstd;
+    if (row + each < p.rows) next_rstd = p.rstd[row + each];
+    ring.wait(row);
+    const T* dy = ring.row(row, 0);
+    const T* sp = ring.row(row, 1);
+    const T* ds = ring.row(row, 2);
+    float dot = 0.0f, unused = 0.0f;
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+      const int k = (v * blockDim.x + threadIdx.x) * VEC;
+      if (k >= cols) break;
+      float a[VEC], s[VEC];
+      to_float(load<T, VEC>(dy + k), a);
+      to_float(load<T, VEC>(sp + k), s);
+#pragma unroll
+      for (int j = 0; j < VEC; ++j) {
+        dot = fmaf(a[j] * g[v][j], s[j], dot);
+        acc[v][j] = fmaf(a[j], s[j] * rstd, acc[v][j]);
       }
     }
-  return false;
+    cta_reduce(dot, unused, sm[phase]);
+    if (ring.given_up()) return;
+    const float c = rstd * (dot * rstd * inv_cols);
+    T* dx = static_cast<T*>(p.dx) + row * p.lddx;
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+      const int k = (v * blockDim.x + threadIdx.x) * VEC;
+      if (k >= cols) break;
+      float a[VEC], s[VEC], d[VEC] = {};
+      to_float(load<T, VEC>(dy + k), a);
+      to_float(load<T, VEC>(sp + k), s);
+      if (p.dsum) to_float(load<T, VEC>(ds + k), d);
+#pragma unroll
+      for (int j = 0; j < VEC; ++j) d[j] = fmaf(rstd, fmaf(-c, s[j], a[j] * g[v][j]), d[j]);
+      store<T, VEC>(dx + k, from_float(d, T()));
+    }
+    ring.leave();
+  }
+  if (!p.partial) return;
+  float* out = p.partial + static_cast<int64_t>(blockIdx.x) * p.cols;
+#pragma unroll
+  for (int v = 0; v < NV; ++v) {
+    const int k = (v * blockDim.x + threadIdx.x) * VEC;
+#pragma unroll
+    for (int j = 0; j < VEC; ++j)
+      if (k + j < cols) out[k + j] = acc[v][j];
+  }
 }
 
-template <class T, int VEC, int NV>
-int fwd_nv(const FwdArgs& p, const Shape& sh, int sms, cudaStream_t s) {
-  const int64_t per = sh.warp ? kWarpRows : 1;
-  int64_t grid = (p.rows + per - 1) / per;
-  const int64_t cap = static_cast<int64_t>(sms) * (2048 / sh.threads) * 4;
-  if (grid > cap) grid = cap;
-  return sh.warp ? launch(norm_fwd_kernel<T, VEC, NV, true>, grid, sh.threads, 0, s, 1, p)
-                 : launch(norm_fwd_kernel<T, VEC, NV, false>, grid, sh.threads, 0, s, 1, p);
+// ----------------------------------------------------------------- routing
+
+// A ring's launch: threads of about `ept` elements each, as many stages as fit
+// (up to four), the CTAs that fit the device, at most `max_grid`.
+struct RingShape {
+  int threads, stages, pitch;
+  int64_t grid;
+  size_t smem;
+};
+
+bool ring_shape(int64_t rows, int64_t cols, int esize, int arrays, int ept, int regs, int sms, int64_t max_grid,
+                RingShape& r) {
+  if (rows < 2 * static_cast<int64_t>(sms) || cols == 0) return false;  // few rows: registers, one CTA a row
+  const int64_t t = ((cols + ept - 1) / ept + 31) / 32 * 32;
+  if (t > 512) return false;
+  r.threads = static_cast<int>(t);
+  r.pitch = static_cast<int>((cols * esize + 15) / 16 * 16 + 16);
+  const int64_t stage = static_cast<int64_t>(arrays) * r.pitch;
+  int64_t stages = kRingBytes / stage;
+  if (stages > kMaxStages) stages = kMaxStages;
+  if (stages < 2) stages = 2;
+  if (kRingHead + stages * stage > kRingMost) return false;
+  r.stages = static_cast<int>(stages);
+  r.smem = static_cast<size_t>(kRingHead + stages * stage);
+  // resident CTAs: by shared memory (with 1.5 KB beside the ring), registers, and 24 an SM
+  int64_t per_sm = (227 * 1024) / static_cast<int64_t>(r.smem + 1536);
+  const int64_t by_regs = 65536 / (regs * t);
+  if (per_sm > by_regs) per_sm = by_regs;
+  if (per_sm > 24) per_sm = 24;
+  if (per_sm < 1) per_sm = 1;
+  r.grid = per_sm * sms;
+  if (r.grid > rows) r.grid = rows;
+  if (r.grid > max_grid) r.grid = max_grid;
+  return true;
 }
 
+// Dynamic shared memory of `Fn`, set once per device.
+template <auto Fn>
+int allow_smem() {
+  static std::atomic<bool> done[64];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return T3_ECUDA;
+  if (dev < 0 || dev >= 64) return T3_EDEVICE;
+  if (!done[dev].load(std::memory_order_acquire)) {
+    if (cudaFuncSetAttribute(Fn, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kRingMost)) !=
+        cudaSuccess)
+      return T3_ECUDA;
+    done[dev].store(true, std::memory_order_release);
+  }
+  return T3_OK;
+}
+
+// The fewest vectors a thread (MAXNV / 4, / 2 or MAXNV) that make at least
+// `least` elements and fit a CTA.
+template <int VEC, int MAXNV>
+int pick(int64_t units, int least, int (*max_threads)(int), int* threads) {
+  for (int nv = MAXNV / 4; nv <= MAXNV; nv *= 2) {
+    if (nv * VEC < least && nv < MAXNV) continue;
+    const int64_t t = (units + nv - 1) / nv;
+    if (t <= max_threads(nv * VEC)) {
+      *threads = t > 0 ? static_cast<int>((t + 31) / 32 * 32) : 32;
+      return nv;
+    }
+  }
+  return 0;
+}
+
+// Forward: few rows take the fewest elements a thread, many rows 16 or more.
 template <class T, int VEC, int MAXNV>
 int fwd_vec(const FwdArgs& p, int sms, cudaStream_t s) {
-  Shape sh;
-  if (!pick<VEC, MAXNV>((p.cols + VEC - 1) / VEC, p.rows, sms, fwd_threads, sh)) {
-    const int64_t grid = p.rows < 4 * sms ? p.rows : 4 * sms;
-    return launch(norm_fwd_long_kernel<T>, grid, 1024, 0, s, 1, p);
-  }
-  if (sh.nv == MAXNV / 4) return fwd_nv<T, VEC, MAXNV / 4>(p, sh, sms, s);
-  if (sh.nv == MAXNV / 2) return fwd_nv<T, VEC, MAXNV / 2>(p, sh, sms, s);
-  return fwd_nv<T, VEC, MAXNV>(p, sh, sms, s);
-}
-
-template <class T, int VEC, int NV>
-int bwd_nv(const BwdArgs& p, const Shape& sh, int sms, int max_parts, int* parts, cudaStream_t s) {
-  const int64_t per = sh.warp ? kWarpRows : 1;
-  int64_t grid = (p.rows + per - 1) / per;
-  int64_t cap = static_cast<int64_t>(sms) * 3;
-  if (cap > max_parts) cap = max_parts;
-  if (grid > cap) grid = cap;
-  *parts = static_cast<int>(grid);
-  const size_t smem = sh.warp ? static_cast<size_t>(p.cols) * 4 : 0;
-  return sh.warp ? launch(norm_bwd_kernel<T, VEC, NV, true>, grid, sh.threads, smem, s, 1, p)
-                 : launch(norm_bwd_kernel<T, VEC, NV, false>, grid, sh.threads, 0, s, 1, p);
+  const bool many = p.rows >= 2 * static_cast<int64_t>(sms);
+  int threads = 0;
+  const int nv = pick<VEC, MAXNV>((p.cols + VEC - 1) / VEC, many ? 16 : 1, fwd_threads, &threads);
+  // one wave of resident CTAs (64 registers a thread)
+  int64_t grid = static_cast<int64_t>(sms) * (threads > 512 ? 1 : 1024 / (threads > 0 ? threads : 1024));
+  if (nv == 0) grid = 2ll * sms;
+  if (grid > p.rows) grid = p.rows;
+  if (nv == MAXNV / 4) return launch(norm_fwd_kernel<T, VEC, MAXNV / 4>, grid, threads, 0, s, 1, p);
+  if (nv == MAXNV / 2) return launch(norm_fwd_kernel<T, VEC, MAXNV / 2>, grid, threads, 0, s, 1, p);
+  if (nv == MAXNV) return launch(norm_fwd_kernel<T, VEC, MAXNV>, grid, threads, 0, s, 1, p);
+  return launch(norm_fwd_long_kernel<T>, grid, 1024, 0, s, 1, p);
 }
 
 template <class T, int VEC, int MAXNV>
-int bwd_vec(const BwdArgs& p, int sms, int max_parts, int* parts, cudaStream_t s) {
-  Shape sh;
-  if (!pick<VEC, MAXNV>((p.cols + VEC - 1) / VEC, p.rows, sms, bwd_threads, sh)) {
-    if (p.partial) {
-      const int64_t tiles = (p.cols + 31) / 32;
-      int64_t n = (p.rows + 7) / 8;
-      if (n > 16) n = 16;
-      if (n > max_parts) n = max_parts;
-      *parts = static_cast<int>(n);
-      const int st = launch(norm_dgamma_kernel<T>, tiles * n, 256, 0, s, 1, p, *parts);
-      if (st != T3_OK) return st;
-    }
-    const int64_t grid = p.rows < 4 * sms ? p.rows : 4 * sms;
-    return launch(norm_bwd_long_kernel<T>, grid, 1024, 0, s, 1, p);
+int bwd_vec(const BwdArgs& p, int sms, int* parts, cudaStream_t s) {
+  RingShape r;
+  constexpr int NV = 16 / VEC;  // 16 elements a thread
+  if (ring_shape(p.rows, p.cols, sizeof(T), 3, 16, VEC > 1 ? 96 : 128, sms, kMaxColParts, r)) {
+    const int st = allow_smem<norm_bwd_ring_kernel<T, VEC, NV>>();
+    if (st != T3_OK) return st;
+    *parts = static_cast<int>(r.grid);
+    return launch(norm_bwd_ring_kernel<T, VEC, NV>, r.grid, r.threads, r.smem, s, 1, p, r.stages, r.pitch);
   }
-  if (sh.nv == MAXNV / 4) return bwd_nv<T, VEC, MAXNV / 4>(p, sh, sms, max_parts, parts, s);
-  if (sh.nv == MAXNV / 2) return bwd_nv<T, VEC, MAXNV / 2>(p, sh, sms, max_parts, parts, s);
-  return bwd_nv<T, VEC, MAXNV>(p, sh, sms, max_parts, parts, s);
+  int threads = 0;
+  const int nv = pick<VEC, MAXNV>((p.cols + VEC - 1) / VEC, 1, bwd_threads, &threads);
+  int64_t grid = p.rows < 2 * sms ? p.rows : 2 * sms;
+  if (nv) {
+    *parts = static_cast<int>(grid);
+    if (nv == MAXNV / 4) return launch(norm_bwd_kernel<T, VEC, MAXNV / 4>, grid, threads, 0, s, 1, p);
+    if (nv == MAXNV / 2) return launch(norm_bwd_kernel<T, VEC, MAXNV / 2>, grid, threads, 0, s, 1, p);
+    return launch(norm_bwd_kernel<T, VEC, MAXNV>, grid, threads, 0, s, 1, p);
+  }
+  if (p.partial) {
+    const int64_t tiles = (p.cols + 31) / 32;
+    const int64_t n = (p.rows + 7) / 8 < 16 ? (p.rows + 7) / 8 : 16;
+    *parts = static_cast<int>(n);
+    const int st = launch(norm_dgamma_kernel<T>, tiles * n, 256, 0, s, 1, p, *parts);
+    if (st != T3_OK) return st;
+  }
+  return launch(norm_bwd_long_kernel<T>, grid, 1024, 0, s, 1, p);
 }
 
 bool vec_rows(const void* p, int64_t ld, int esize) {
@@ -479,8 +732,8 @@ bool vec_rows(const void* p, int64_t ld, int esize) {
 
 int launch_norm_fwd(const void* x, int64_t ldx, const void* residual, int64_t ldr, const float* gamma,
                     float eps, int8_t* q, float* row_scale, float* rstd, void* sum_out, int64_t lds,
-                    int64_t rows, int64_t cols, int dtype, int sms, cudaStream_t s) {
-  const nm::FwdArgs p{x, residual, ldx, ldr, lds, gamma, eps, q, row_scale, rstd, sum_out, rows, cols};
+                    int64_t rows, int64_t cols, int dtype, int sms, int* err, cudaStream_t s) {
+  const nm::FwdArgs p{x, residual, ldx, ldr, lds, gamma, eps, q, row_scale, rstd, sum_out, rows, cols, err};
   const int es = dtype == T3_OUT_BF16 ? 2 : 4, v = 16 / es;
   const bool vec = cols % v == 0 && nm::vec_rows(x, ldx, es) && nm::vec_rows(residual, ldr, es) &&
                    nm::vec_rows(sum_out, lds, es) && vec::aligned(q, v) &&
@@ -493,20 +746,20 @@ int launch_norm_fwd(const void* x, int64_t ldx, const void* residual, int64_t ld
 int launch_norm_bwd(const void* dy, int64_t lddy, const void* x, int64_t lds, const float* rstd,
                     const float* gamma, const void* dsum, int64_t lddsum, void* dx, int64_t lddx,
                     float* dgamma, int64_t rows, int64_t cols, int dtype, float* workspace, int sms,
-                    cudaStream_t s) {
+                    int* err, cudaStream_t s) {
   const nm::BwdArgs p{dy, x, dsum, lddy, lds, lddsum, lddx, rstd, gamma, dx, dgamma ? workspace : nullptr,
-                      rows, cols};
+                      rows, cols, err};
   const int es = dtype == T3_OUT_BF16 ? 2 : 4, v = 16 / es;
   const bool vec = cols % v == 0 && nm::vec_rows(dy, lddy, es) && nm::vec_rows(x, lds, es) &&
                    nm::vec_rows(dsum, lddsum, es) && nm::vec_rows(dx, lddx, es) &&
                    (!gamma || vec::aligned(gamma, 16));
   int parts = 0, st;
   if (dtype == T3_OUT_BF16)
-    st = vec ? nm::bwd_vec<vec::bf16, 8, 4>(p, sms, kMaxColParts, &parts, s)
-             : nm::bwd_vec<vec::bf16, 1, 32>(p, sms, kMaxColParts, &parts, s);
+    st = vec ? nm::bwd_vec<vec::bf16, 8, 4>(p, sms, &parts, s)
+             : nm::bwd_vec<vec::bf16, 1, 32>(p, sms, &parts, s);
   else
-    st = vec ? nm::bwd_vec<float, 4, 4>(p, sms, kMaxColParts, &parts, s)
-             : nm::bwd_vec<float, 1, 32>(p, sms, kMaxColParts, &parts, s);
+    st = vec ? nm::bwd_vec<float, 4, 4>(p, sms, &parts, s)
+             : nm::bwd_vec<float, 1, 32>(p, sms, &parts, s);
   if (st != T3_OK || !dgamma) return st;
   return launch_col_finish(workspace, parts, cols, dgamma, s);
 }
