@@ -417,9 +417,9 @@ const char* t3_status_string(int status);
  * value.  *detail, when not NULL, receives the recorded code (0 if none):
  * bits 0-7 the role (1 producer, 2 converter, 3 MMA issuer, 4 epilogue,
  * 5 pair forwarder gave up; 6 an input value was invalid; 7 a CTA gave up
- * waiting for its cluster or its rows), bits 8-15 the kernel (4 small-M fwd;
+ * waiting for its cluster), bits 8-15 the kernel (4 small-M fwd;
  * 5 fwd, 6 dX, 7 dW on CTA pairs; 9 the device packer; 10 the wait self-test
- * below; 11 the gated recurrence; 12 the norm).
+ * below; 11 the gated recurrence).
  */
 int t3_last_device_error(t3_stream_t stream, int32_t* detail);
 

@@ -592,7 +592,7 @@ int t3_rmsnorm_quant(const void* x, int64_t ldx, const void* residual, int64_t l
   const int st = device_info(&dev);
   if (st != T3_OK) return st;
   return launch_norm_fwd(x, ldx, residual, ldr, gamma, eps, q, row_scale, rstd, sum_out, lds, rows, cols,
-                         dtype, dev->sms, dev->err_word, stream);
+                         dtype, dev->sms, stream);
 }
 
 int t3_rmsnorm_bwd(const void* dy, int64_t lddy, const void* s, int64_t lds, const float* rstd,
@@ -609,7 +609,7 @@ int t3_rmsnorm_bwd(const void* dy, int64_t lddy, const void* s, int64_t lds, con
   const int st = device_info(&dev);
   if (st != T3_OK) return st;
   return launch_norm_bwd(dy, lddy, s, lds, rstd, gamma, dsum, lddsum, dx, lddx, dgamma, rows, cols, dtype,
-                         workspace, dev->sms, dev->err_word, stream);
+                         workspace, dev->sms, stream);
 }
 
 int t3_gated_scan_fwd(const void* gate, int64_t ldg, const void* cand, int64_t ldc,

@@ -90,7 +90,7 @@ int launch_skinny_fwd(const int8_t* A, const uint8_t* Wp, int32_t* C, int64_t M,
 
 // Partial rows of the column sums (norm and epilogue gradients): at most so
 // many, so that a workspace's size does not depend on the device.
-constexpr int kMaxColParts = 608;
+constexpr int kMaxColParts = 1216;
 
 // out[c] = the sum of partial[0 .. parts)[c], added in a fixed order, on `s`.
 int launch_col_finish(const float* partial, int parts, int64_t cols, float* out, cudaStream_t s);
@@ -99,11 +99,11 @@ int launch_col_finish(const float* partial, int parts, int64_t cols, float* out,
 // gradient (t3_norm.cu); dtype T3_OUT_F32 or T3_OUT_BF16.
 int launch_norm_fwd(const void* x, int64_t ldx, const void* residual, int64_t ldr, const float* gamma,
                     float eps, int8_t* q, float* row_scale, float* rstd, void* sum_out, int64_t lds,
-                    int64_t rows, int64_t cols, int dtype, int sms, int* err, cudaStream_t s);
+                    int64_t rows, int64_t cols, int dtype, int sms, cudaStream_t s);
 int launch_norm_bwd(const void* dy, int64_t lddy, const void* x, int64_t lds, const float* rstd,
                     const float* gamma, const void* dsum, int64_t lddsum, void* dx, int64_t lddx,
                     float* dgamma, int64_t rows, int64_t cols, int dtype, float* workspace, int sms,
-                    int* err, cudaStream_t s);
+                    cudaStream_t s);
 
 // The gated recurrence over sequences and its gradient (t3_scan.cu).
 int launch_scan_fwd(const void* gate, int64_t ldg, const void* cand, int64_t ldc, const float* h0,

@@ -13,22 +13,17 @@
 // n = dy gamma:
 //   dx = rstd (n - s rstd^2 mean(n s)) + dsum,   dgamma = sum over rows of dy s rstd
 //
-// What bounds it: memory.  A row is read once and written once:
-//   * many rows: a persistent grid whose CTAs take rows in turn, each row copied
-//     ahead into a ring of shared-memory stages by one bulk copy an array, so
-//     that the loads in flight do not depend on registers or warps; the
-//     threads read it from there for the reductions and again for the output.
-//     Rows that do not start on 16 bytes (odd widths or strides) are copied
-//     with the aligned bytes around them, which belong to the matrix too, and read
-//     element by element;
-//   * few rows (a serving step): a CTA a row, every thread with as few elements
-//     in registers as 1024 threads allow, loaded directly;
-//   * rows longer than either holds are read twice.
-// dgamma: each CTA holds its columns' sums in registers over all its rows,
-// writes one partial row, and a second small kernel adds the partial rows in
-// a fixed order.
-#include <atomic>
-
+// What bounds it: memory.  A row is read once and written once.  A persistent
+// grid of one wave takes rows in turn; a thread's columns are the same in every
+// row, so their gains (and, backward, their sums of dgamma) stay in registers, and the
+// next row's operands are loaded while this one is reduced and written.  Many
+// rows take 16 elements a thread forward and 8 backward (8 and 8 where rows
+// are not 16-byte vectors and go element by element), few rows as few as 1024 threads
+// allow, for the shortest time to one row; rows longer than the registers
+// hold are read twice.  Backward, narrow rows share a CTA in groups of warps that
+// meet at barriers of their own.  dgamma: each CTA adds its groups' sums in turn,
+// writes one partial row, and a second small kernel adds the partial rows in a
+// fixed order.
 #include "t3_vec.cuh"
 
 namespace t3 {
@@ -51,7 +46,6 @@ struct FwdArgs {
   float *row_scale, *rstd;
   void* sum_out;
   int64_t rows, cols;
-  int* err;
 };
 
 struct BwdArgs {
@@ -61,7 +55,7 @@ struct BwdArgs {
   void* dx;
   float* partial;  // [gridDim.x][cols], null without dgamma
   int64_t rows, cols;
-  int* err;
+  int groups;      // row groups a CTA (norm_bwd_kernel)
 };
 
 __device__ __forceinline__ int quant(float u, float inv) {
@@ -120,6 +114,22 @@ __device__ __forceinline__ void cta_reduce(float& a, float& b, float* sm) {
   }
   a = warp_sum(lane < warps ? sm[lane] : 0.0f);
   b = warp_max_nan(lane < warps ? sm[32 + lane] : 0.0f);
+}
+
+// The sum of `a` over a group of `warps` warps, which meets at barrier `bar`;
+// `sm` holds a float for each of its warps and alternates from call to call.
+__device__ __forceinline__ float group_sum(float a, float* sm, int warp, int warps, int bar) {
+  const int lane = threadIdx.x & 31;
+  a = warp_sum(a);
+  if (warps == 1) return a;
+  if (lane == 0) sm[warp] = a;
+  named_bar_sync(bar, 32 * warps);
+  if (warps <= 4) {
+    a = sm[0];
+    for (int i = 1; i < warps; ++i) a += sm[i];
+    return a;
+  }
+  return warp_sum(lane < warps ? sm[lane] : 0.0f);
 }
 
 template <class T, int VEC, int NV>
@@ -255,80 +265,106 @@ __global__ void __launch_bounds__(1024) norm_fwd_long_kernel(const FwdArgs p) {
   }
 }
 
-template <class T, int VEC, int NV>
-__global__ void __launch_bounds__(bwd_threads(NV * VEC)) norm_bwd_kernel(const BwdArgs p) {
-  __shared__ float sm[2][64];
-  const int lanes = blockDim.x, tid = threadIdx.x;
-  int phase = 0;
-  float g[NV][VEC], acc[NV][VEC];
+// kOne: the CTA is one group; else it has p.groups of them in 256 threads.
+template <class T, int VEC, int NV, bool kOne>
+__global__ void __launch_bounds__(kOne ? bwd_threads(NV * VEC) : 256, kOne ? 1 : 3) norm_bwd_kernel(const BwdArgs p) {
+  __shared__ float sm[2][32];
+  extern __shared__ float sums[];  // [cols], with more than one group
+  const int groups = kOne ? 1 : p.groups;
+  const int lanes = blockDim.x / groups, cols = static_cast<int>(p.cols);
+  const int group = kOne ? 0 : threadIdx.x / lanes, t = threadIdx.x - group * lanes, warps = lanes >> 5;
+  const int64_t each = static_cast<int64_t>(gridDim.x) * groups;
   launch_dependents();
   grid_dependency_wait();
-#pragma unroll
-  for (int v = 0; v < NV; ++v) {
-    const int k = (v * lanes + tid) * VEC;
-#pragma unroll
-    for (int j = 0; j < VEC; ++j) {
-      g[v][j] = 1.0f;
-      acc[v][j] = 0.0f;
-    }
-    if (p.gamma && k < p.cols) load_floats<VEC>(p.gamma + k, g[v]);
-  }
-  const float inv_cols = 1.0f / static_cast<float>(p.cols);
-  for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x, phase ^= 1) {
+  // this thread's columns: gains, sums, and the next row's operands
+  float g[NV][VEC], acc[NV][VEC], next_rstd = 0.0f;
+  Raw<T, VEC> dyr[NV], sr[NV], dr[NV];
+  auto fetch = [&](int64_t row) {
     const T* dy = static_cast<const T*>(p.dy) + row * p.lddy;
     const T* sp = static_cast<const T*>(p.s) + row * p.lds;
     const T* ds = static_cast<const T*>(p.dsum) + row * p.lddsum;
-    Raw<T, VEC> dyr[NV], sr[NV], dr[NV];
+    if (row < p.rows) next_rstd = p.rstd[row];
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
-      const int k = (v * lanes + tid) * VEC;
+      const int k = (v * lanes + t) * VEC;
       dyr[v] = zero<T, VEC>();
       sr[v] = zero<T, VEC>();
       dr[v] = zero<T, VEC>();
-      if (k < p.cols) {
+      if (k < cols && row < p.rows) {
         dyr[v] = load<T, VEC>(dy + k);
         sr[v] = load<T, VEC>(sp + k);
         if (p.dsum) dr[v] = load<T, VEC>(ds + k);
       }
     }
-    const float rstd = p.rstd[row];
-    float dot = 0.0f, unused = 0.0f;
+  };
+  const int64_t first = static_cast<int64_t>(blockIdx.x) * groups + group;
+  fetch(first);
+#pragma unroll
+  for (int v = 0; v < NV; ++v) {
+    const int k = (v * lanes + t) * VEC;
+#pragma unroll
+    for (int j = 0; j < VEC; ++j) {
+      g[v][j] = 1.0f;
+      acc[v][j] = 0.0f;
+    }
+    if (p.gamma && k < cols) load_floats<VEC>(p.gamma + k, g[v]);
+  }
+  const float inv_cols = 1.0f / static_cast<float>(p.cols);
+  int phase = 0;
+  for (int64_t row = first; row < p.rows; row += each, phase ^= 1) {
+    const float rstd = next_rstd;
+    float n[NV][VEC], s[NV][VEC], dot = 0.0f;
+    Raw<T, VEC> d[NV];
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
-      float a[VEC], s[VEC];
-      to_float(dyr[v], a);
-      to_float(sr[v], s);
+      to_float(dyr[v], n[v]);
+      to_float(sr[v], s[v]);
+      d[v] = dr[v];
 #pragma unroll
       for (int j = 0; j < VEC; ++j) {
-        dot = fmaf(a[j] * g[v][j], s[j], dot);
-        acc[v][j] = fmaf(a[j], s[j] * rstd, acc[v][j]);
+        s[v][j] *= rstd;
+        acc[v][j] = fmaf(n[v][j], s[v][j], acc[v][j]);
+        n[v][j] *= g[v][j];
+        dot = fmaf(n[v][j], s[v][j], dot);
       }
     }
-    cta_reduce(dot, unused, sm[phase]);
-    // rstd s bounded by sqrt(cols) / |s|: scale before squaring
-    const float c = rstd * (dot * rstd * inv_cols);
+    fetch(row + each);
+    dot = group_sum(dot, sm[phase] + group * warps, t >> 5, warps, 1 + group);
+    const float c = dot * inv_cols;
     T* dx = static_cast<T*>(p.dx) + row * p.lddx;
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
-      const int k = (v * lanes + tid) * VEC;
-      if (k >= p.cols) break;
-      float a[VEC], s[VEC], d[VEC];
-      to_float(dyr[v], a);
-      to_float(sr[v], s);
-      to_float(dr[v], d);
+      const int k = (v * lanes + t) * VEC;
+      if (k >= cols) break;
+      float y[VEC];
+      to_float(d[v], y);
 #pragma unroll
-      for (int j = 0; j < VEC; ++j) d[j] = fmaf(rstd, fmaf(-c, s[j], a[j] * g[v][j]), d[j]);
-      store<T, VEC>(dx + k, from_float(d, T()));
+      for (int j = 0; j < VEC; ++j) y[j] = fmaf(rstd, fmaf(-c, s[v][j], n[v][j]), y[j]);
+      store<T, VEC>(dx + k, from_float(y, T()));
     }
   }
   if (!p.partial) return;
   float* out = p.partial + static_cast<int64_t>(blockIdx.x) * p.cols;
+  // the groups add their sums in turn; the last one writes
+  for (int i = 0; i < groups - 1; ++i) {
+    if (group == i) {
+#pragma unroll
+      for (int v = 0; v < NV; ++v) {
+        const int k = (v * lanes + t) * VEC;
+#pragma unroll
+        for (int j = 0; j < VEC; ++j)
+          if (k + j < cols) sums[k + j] = (i ? sums[k + j] : 0.0f) + acc[v][j];
+      }
+    }
+    __syncthreads();
+  }
+  if (group != groups - 1) return;
 #pragma unroll
   for (int v = 0; v < NV; ++v) {
-    const int k = (v * lanes + tid) * VEC;
+    const int k = (v * lanes + t) * VEC;
 #pragma unroll
     for (int j = 0; j < VEC; ++j)
-      if (k + j < p.cols) out[k + j] = acc[v][j];
+      if (k + j < cols) out[k + j] = (groups > 1 ? sums[k + j] : 0.0f) + acc[v][j];
   }
 }
 
@@ -346,14 +382,17 @@ __global__ void __launch_bounds__(1024) norm_bwd_long_kernel(const BwdArgs p) {
     const T* ds = static_cast<const T*>(p.dsum) + row * p.lddsum;
     T* dx = static_cast<T*>(p.dx) + row * p.lddx;
     const float rstd = p.rstd[row];
-    float dot = 0.0f, unused = 0.0f;
+    float dot = 0.0f;
     for (int64_t k = threadIdx.x; k < p.cols; k += blockDim.x) {
       float a[1], s[1];
       to_float(load<T, 1>(dy + k), a);
       to_float(load<T, 1>(sp + k), s);
       dot = fmaf(p.gamma ? a[0] * __ldg(p.gamma + k) : a[0], s[0], dot);
     }
-    cta_reduce(dot, unused, sm[phase]);
+    {
+      float unused = 0.0f;
+      cta_reduce(dot, unused, sm[phase]);
+    }
     const float c = rstd * (dot * rstd / static_cast<float>(p.cols));
     for (int64_t k = threadIdx.x; k < p.cols; k += blockDim.x) {
       float a[1], s[1], d[1] = {0.0f};
@@ -394,275 +433,7 @@ __global__ void __launch_bounds__(256) norm_dgamma_kernel(const BwdArgs p, int p
   }
 }
 
-// ------------------------------------------------- many rows: a ring of rows
-
-constexpr int kMaxStages = 4;
-constexpr int kWaitCode = (12 << 8) | 7;
-// Bytes of a ring: up to four stages within kRingBytes (two CTAs an SM), two
-// stages of the longest rows within kRingMost.
-constexpr int64_t kRingBytes = 100 * 1024, kRingMost = 200 * 1024;
-
-// One array of rows in the ring.  kAligned: rows of whole 16-byte pieces on
-// 16-byte boundaries.  Any other row is copied from the boundary at or before it
-// to the one at or behind its end; where those bytes are not all the matrix's
-// own (its first and last row, when the matrix starts or ends elsewhere), the
-// threads copy the row themselves.
-template <class T, bool kAligned>
-struct Rows {
-  const T* base;
-  int64_t ld, rows;
-  int cols;
-  __device__ __forceinline__ uint64_t addr(int64_t row) const { return reinterpret_cast<uint64_t>(base + row * ld); }
-  __device__ __forceinline__ int shift(int64_t row) const { return kAligned ? 0 : static_cast<int>(addr(row) & 15); }
-  __device__ __forceinline__ uint32_t bytes(int64_t row) const {
-    return (static_cast<uint32_t>(shift(row) + cols * static_cast<int>(sizeof(T))) + 15u) & ~15u;
-  }
-  __device__ __forceinline__ bool bulk(int64_t row) const {
-    if (kAligned) return true;
-    const uint64_t a = addr(row) - shift(row), end = reinterpret_cast<uint64_t>(base + (rows - 1) * ld + cols);
-    return a >= reinterpret_cast<uint64_t>(base) && a + bytes(row) <= end;
-  }
-};
-
-__device__ __forceinline__ void bulk_load(void* dst, uint64_t src, uint32_t bytes, uint64_t* bar) {
-  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
-                   smem_addr(dst)),
-               "l"(src), "r"(bytes), "r"(smem_addr(bar))
-               : "memory");
-}
-
-// A CTA's ring over NA arrays: rows blockIdx.x, + gridDim.x, ... take the stages
-// in turn, each array `pitch` bytes from the last.
-template <class T, int NA, bool kAligned>
-struct Ring {
-  Rows<T, kAligned> a[NA];
-  bool on[NA];  // arrays that are there
-  uint8_t* smem;
-  uint64_t* full;
-  int stages, pitch;
-  int* err;
-  volatile int* abort_flag;
-  bool failed;
-  int stage;        // of the row at hand
-  uint32_t parity;  // of its barrier
-
-  __device__ __forceinline__ uint8_t* at(int st, int i) const { return smem + (st * NA + i) * pitch; }
-  // One thread: the copies of a row into stage st.
-  __device__ __forceinline__ void issue(int st, int64_t row) {
-    uint32_t total = 0;
-#pragma unroll
-    for (int i = 0; i < NA; ++i)
-      if (on[i] && a[i].bulk(row)) total += a[i].bytes(row);
-    mbar_arrive_expect_tx(&full[st], total);
-#pragma unroll
-    for (int i = 0; i < NA; ++i)
-      if (on[i] && a[i].bulk(row)) bulk_load(at(st, i), a[i].addr(row) - a[i].shift(row), a[i].bytes(row), &full[st]);
-  }
-  // One thread, before the first row: all stages but one.
-  __device__ __forceinline__ void start(int64_t first, int64_t each) {
-    for (int i = 0; i < stages - 1; ++i)
-      if (first + i * each < a[0].rows) issue(i, first + i * each);
-  }
-  // One thread, at the top of a row: the row stages - 1 turns on goes where the
-  // last one was, which all threads have left.
-  __device__ __forceinline__ void ahead(int64_t row, int64_t each) {
-    const int64_t r = row + (stages - 1) * each;
-    if (r < a[0].rows) issue(stage == 0 ? stages - 1 : stage - 1, r);
-  }
-  // All threads: the row is in its stage.
-  __device__ __forceinline__ void wait(int64_t row) {
-    if (!failed) failed = !mbar_wait(&full[stage], parity, abort_flag, err, kWaitCode);
-    if (kAligned) return;
-    bool direct = false;
-#pragma unroll
-    for (int i = 0; i < NA; ++i)
-      if (on[i] && !a[i].bulk(row)) {
-        direct = true;
-        T* dst = reinterpret_cast<T*>(at(stage, i) + a[i].shift(row));
-        const T* src = a[i].base + row * a[i].ld;
-        for (int k = threadIdx.x; k < a[i].cols; k += blockDim.x) dst[k] = src[k];
-      }
-    if (direct) __syncthreads();
-  }
-  __device__ __forceinline__ T* row(int64_t r, int i) const {
-    return reinterpret_cast<T*>(at(stage, i) + a[i].shift(r));
-  }
-  // All threads, behind a barrier (of the warp or the CTA) after wait(): whether
-  // any of them gave up.  Then the copies in flight get one more, short, wait.
-  __device__ __forceinline__ bool given_up() {
-    __syncwarp();
-    if (!*abort_flag) return false;
-    for (int i = 0; i < stages; ++i)
-      mbar_wait(&full[(stage + i) % stages], stage + i < stages ? parity : parity ^ 1u, abort_flag, err, kWaitCode);
-    return true;
-  }
-  // All threads, behind their last access to the stage.
-  __device__ __forceinline__ void leave() {
-    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // before the next bulk copy into it
-    __syncthreads();
-    if (++stage == stages) {
-      stage = 0;
-      parity ^= 1u;
-    }
-  }
-};
-
-// Shared memory of a ring: the barriers and the abort flag, then the stages.
-constexpr int kRingHead = 64;
-
-template <class T, int NA, bool kAligned>
-__device__ __forceinline__ void open_ring(Ring<T, NA, kAligned>& r, uint8_t* smem, int stages, int pitch, int* err) {
-  r.full = reinterpret_cast<uint64_t*>(smem);
-  int* flag = reinterpret_cast<int*>(smem + 8 * kMaxStages);
-  r.abort_flag = flag;
-  r.smem = smem + kRingHead;
-  r.stages = stages;
-  r.pitch = pitch;
-  r.err = err;
-  r.failed = false;
-  r.stage = 0;
-  r.parity = 0;
-  if (threadIdx.x == 0) {
-    for (int i = 0; i < stages; ++i) mbar_init(&r.full[i], 1);
-    *flag = 0;
-    fence_mbarrier_init();
-    fence_proxy_async_smem();
-  }
-  __syncthreads();
-}
-
-template <class T, int VEC, int NV>
-__global__ void __launch_bounds__(512) norm_bwd_ring_kernel(const BwdArgs p, int stages, int pitch) {
-  extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ float sm[2][64];
-  const int cols = static_cast<int>(p.cols);
-  Ring<T, 3, (VEC > 1)> ring;
-  ring.a[0] = {static_cast<const T*>(p.dy), p.lddy, p.rows, cols};
-  ring.a[1] = {static_cast<const T*>(p.s), p.lds, p.rows, cols};
-  ring.a[2] = {static_cast<const T*>(p.dsum), p.lddsum, p.rows, cols};
-  ring.on[0] = ring.on[1] = true;
-  ring.on[2] = p.dsum != nullptr;
-  open_ring(ring, smem, stages, pitch, p.err);
-  launch_dependents();
-  grid_dependency_wait();
-  const int64_t first = blockIdx.x, each = gridDim.x;
-  if (threadIdx.x == 0) ring.start(first, each);
-  float g[NV][VEC], acc[NV][VEC];
-#pragma unroll
-  for (int v = 0; v < NV; ++v) {
-    const int k = (v * blockDim.x + threadIdx.x) * VEC;
-#pragma unroll
-    for (int j = 0; j < VEC; ++j) {
-      g[v][j] = 1.0f;
-      acc[v][j] = 0.0f;
-    }
-    if (p.gamma && k < cols) load_floats<VEC>(p.gamma + k, g[v]);
-  }
-  const float inv_cols = 1.0f / static_cast<float>(p.cols);
-  float next_rstd = first < p.rows ? p.rstd[first] : 0.0f;
-  int phase = 0;
-  for (int64_t row = first; row < p.rows; row += each, phase ^= 1) {
-    if (threadIdx.x == 0) ring.ahead(row, each);
-    const float rstd = next_rstd;
-    if (row + each < p.rows) next_rstd = p.rstd[row + each];
-    ring.wait(row);
-    const T* dy = ring.row(row, 0);
-    const T* sp = ring.row(row, 1);
-    const T* ds = ring.row(row, 2);
-    float dot = 0.0f, unused = 0.0f;
-#pragma unroll
-    for (int v = 0; v < NV; ++v) {
-      const int k = (v * blockDim.x + threadIdx.x) * VEC;
-      if (k >= cols) break;
-      float a[VEC], s[VEC];
-      to_float(load<T, VEC>(dy + k), a);
-      to_float(load<T, VEC>(sp + k), s);
-#pragma unroll
-      for (int j = 0; j < VEC; ++j) {
-        dot = fmaf(a[j] * g[v][j], s[j], dot);
-        acc[v][j] = fmaf(a[j], s[j] * rstd, acc[v][j]);
-      }
-    }
-    cta_reduce(dot, unused, sm[phase]);
-    if (ring.given_up()) return;
-    const float c = rstd * (dot * rstd * inv_cols);
-    T* dx = static_cast<T*>(p.dx) + row * p.lddx;
-#pragma unroll
-    for (int v = 0; v < NV; ++v) {
-      const int k = (v * blockDim.x + threadIdx.x) * VEC;
-      if (k >= cols) break;
-      float a[VEC], s[VEC], d[VEC] = {};
-      to_float(load<T, VEC>(dy + k), a);
-      to_float(load<T, VEC>(sp + k), s);
-      if (p.dsum) to_float(load<T, VEC>(ds + k), d);
-#pragma unroll
-      for (int j = 0; j < VEC; ++j) d[j] = fmaf(rstd, fmaf(-c, s[j], a[j] * g[v][j]), d[j]);
-      store<T, VEC>(dx + k, from_float(d, T()));
-    }
-    ring.leave();
-  }
-  if (!p.partial) return;
-  float* out = p.partial + static_cast<int64_t>(blockIdx.x) * p.cols;
-#pragma unroll
-  for (int v = 0; v < NV; ++v) {
-    const int k = (v * blockDim.x + threadIdx.x) * VEC;
-#pragma unroll
-    for (int j = 0; j < VEC; ++j)
-      if (k + j < cols) out[k + j] = acc[v][j];
-  }
-}
-
 // ----------------------------------------------------------------- routing
-
-// A ring's launch: threads of about `ept` elements each, as many stages as fit
-// (up to four), the CTAs that fit the device, at most `max_grid`.
-struct RingShape {
-  int threads, stages, pitch;
-  int64_t grid;
-  size_t smem;
-};
-
-bool ring_shape(int64_t rows, int64_t cols, int esize, int arrays, int ept, int regs, int sms, int64_t max_grid,
-                RingShape& r) {
-  if (rows < 2 * static_cast<int64_t>(sms) || cols == 0) return false;  // few rows: registers, one CTA a row
-  const int64_t t = ((cols + ept - 1) / ept + 31) / 32 * 32;
-  if (t > 512) return false;
-  r.threads = static_cast<int>(t);
-  r.pitch = static_cast<int>((cols * esize + 15) / 16 * 16 + 16);
-  const int64_t stage = static_cast<int64_t>(arrays) * r.pitch;
-  int64_t stages = kRingBytes / stage;
-  if (stages > kMaxStages) stages = kMaxStages;
-  if (stages < 2) stages = 2;
-  if (kRingHead + stages * stage > kRingMost) return false;
-  r.stages = static_cast<int>(stages);
-  r.smem = static_cast<size_t>(kRingHead + stages * stage);
-  // resident CTAs: by shared memory (with 1.5 KB beside the ring), registers, and 24 an SM
-  int64_t per_sm = (227 * 1024) / static_cast<int64_t>(r.smem + 1536);
-  const int64_t by_regs = 65536 / (regs * t);
-  if (per_sm > by_regs) per_sm = by_regs;
-  if (per_sm > 24) per_sm = 24;
-  if (per_sm < 1) per_sm = 1;
-  r.grid = per_sm * sms;
-  if (r.grid > rows) r.grid = rows;
-  if (r.grid > max_grid) r.grid = max_grid;
-  return true;
-}
-
-// Dynamic shared memory of `Fn`, set once per device.
-template <auto Fn>
-int allow_smem() {
-  static std::atomic<bool> done[64];
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess) return T3_ECUDA;
-  if (dev < 0 || dev >= 64) return T3_EDEVICE;
-  if (!done[dev].load(std::memory_order_acquire)) {
-    if (cudaFuncSetAttribute(Fn, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kRingMost)) !=
-        cudaSuccess)
-      return T3_ECUDA;
-    done[dev].store(true, std::memory_order_release);
-  }
-  return T3_OK;
-}
 
 // The fewest vectors a thread (MAXNV / 4, / 2 or MAXNV) that make at least
 // `least` elements and fit a CTA.
@@ -684,7 +455,7 @@ template <class T, int VEC, int MAXNV>
 int fwd_vec(const FwdArgs& p, int sms, cudaStream_t s) {
   const bool many = p.rows >= 2 * static_cast<int64_t>(sms);
   int threads = 0;
-  const int nv = pick<VEC, MAXNV>((p.cols + VEC - 1) / VEC, many ? 16 : 1, fwd_threads, &threads);
+  const int nv = pick<VEC, MAXNV>((p.cols + VEC - 1) / VEC, many ? (VEC > 1 ? 16 : 8) : 1, fwd_threads, &threads);
   // one wave of resident CTAs (64 registers a thread)
   int64_t grid = static_cast<int64_t>(sms) * (threads > 512 ? 1 : 1024 / (threads > 0 ? threads : 1024));
   if (nv == 0) grid = 2ll * sms;
@@ -695,24 +466,32 @@ int fwd_vec(const FwdArgs& p, int sms, cudaStream_t s) {
   return launch(norm_fwd_long_kernel<T>, grid, 1024, 0, s, 1, p);
 }
 
+// Backward: many rows take 8 elements a thread (more only where the row would not
+// fit a CTA).
 template <class T, int VEC, int MAXNV>
-int bwd_vec(const BwdArgs& p, int sms, int* parts, cudaStream_t s) {
-  RingShape r;
-  constexpr int NV = 16 / VEC;  // 16 elements a thread
-  if (ring_shape(p.rows, p.cols, sizeof(T), 3, 16, VEC > 1 ? 96 : 128, sms, kMaxColParts, r)) {
-    const int st = allow_smem<norm_bwd_ring_kernel<T, VEC, NV>>();
-    if (st != T3_OK) return st;
-    *parts = static_cast<int>(r.grid);
-    return launch(norm_bwd_ring_kernel<T, VEC, NV>, r.grid, r.threads, r.smem, s, 1, p, r.stages, r.pitch);
-  }
+int bwd_vec(BwdArgs p, int sms, int* parts, cudaStream_t s) {
+  const bool many = p.rows >= 2 * static_cast<int64_t>(sms);
   int threads = 0;
-  const int nv = pick<VEC, MAXNV>((p.cols + VEC - 1) / VEC, 1, bwd_threads, &threads);
-  int64_t grid = p.rows < 2 * sms ? p.rows : 2 * sms;
+  const int nv = pick<VEC, MAXNV>((p.cols + VEC - 1) / VEC, many ? 8 : 1, bwd_threads, &threads);
+  int64_t grid = 2ll * sms;
   if (nv) {
+    // narrow rows: two groups or more in 256 threads, three such CTAs an SM;
+    // else a CTA a row, as many as the registers hold
+    p.groups = many && nv * VEC == 8 ? 256 / threads : 1;
+    if (p.groups < 1) p.groups = 1;
+    const bool one = p.groups == 1;
+    const int room = (one ? bwd_threads(nv * VEC) : 768) / (threads * p.groups);
+    grid = static_cast<int64_t>(sms) * room;
+    const int64_t need = (p.rows + p.groups - 1) / p.groups;
+    if (grid > need) grid = need;
+    if (grid > kMaxColParts) grid = kMaxColParts;
     *parts = static_cast<int>(grid);
-    if (nv == MAXNV / 4) return launch(norm_bwd_kernel<T, VEC, MAXNV / 4>, grid, threads, 0, s, 1, p);
-    if (nv == MAXNV / 2) return launch(norm_bwd_kernel<T, VEC, MAXNV / 2>, grid, threads, 0, s, 1, p);
-    return launch(norm_bwd_kernel<T, VEC, MAXNV>, grid, threads, 0, s, 1, p);
+    if (!one)
+      return launch(norm_bwd_kernel<T, VEC, 8 / VEC, false>, grid, threads * p.groups,
+                    static_cast<size_t>(p.cols) * sizeof(float), s, 1, p);
+    if (nv == MAXNV / 4) return launch(norm_bwd_kernel<T, VEC, MAXNV / 4, true>, grid, threads, 0, s, 1, p);
+    if (nv == MAXNV / 2) return launch(norm_bwd_kernel<T, VEC, MAXNV / 2, true>, grid, threads, 0, s, 1, p);
+    return launch(norm_bwd_kernel<T, VEC, MAXNV, true>, grid, threads, 0, s, 1, p);
   }
   if (p.partial) {
     const int64_t tiles = (p.cols + 31) / 32;
@@ -721,6 +500,7 @@ int bwd_vec(const BwdArgs& p, int sms, int* parts, cudaStream_t s) {
     const int st = launch(norm_dgamma_kernel<T>, tiles * n, 256, 0, s, 1, p, *parts);
     if (st != T3_OK) return st;
   }
+  if (grid > p.rows) grid = p.rows;
   return launch(norm_bwd_long_kernel<T>, grid, 1024, 0, s, 1, p);
 }
 
@@ -732,8 +512,8 @@ bool vec_rows(const void* p, int64_t ld, int esize) {
 
 int launch_norm_fwd(const void* x, int64_t ldx, const void* residual, int64_t ldr, const float* gamma,
                     float eps, int8_t* q, float* row_scale, float* rstd, void* sum_out, int64_t lds,
-                    int64_t rows, int64_t cols, int dtype, int sms, int* err, cudaStream_t s) {
-  const nm::FwdArgs p{x, residual, ldx, ldr, lds, gamma, eps, q, row_scale, rstd, sum_out, rows, cols, err};
+                    int64_t rows, int64_t cols, int dtype, int sms, cudaStream_t s) {
+  const nm::FwdArgs p{x, residual, ldx, ldr, lds, gamma, eps, q, row_scale, rstd, sum_out, rows, cols};
   const int es = dtype == T3_OUT_BF16 ? 2 : 4, v = 16 / es;
   const bool vec = cols % v == 0 && nm::vec_rows(x, ldx, es) && nm::vec_rows(residual, ldr, es) &&
                    nm::vec_rows(sum_out, lds, es) && vec::aligned(q, v) &&
@@ -746,9 +526,9 @@ int launch_norm_fwd(const void* x, int64_t ldx, const void* residual, int64_t ld
 int launch_norm_bwd(const void* dy, int64_t lddy, const void* x, int64_t lds, const float* rstd,
                     const float* gamma, const void* dsum, int64_t lddsum, void* dx, int64_t lddx,
                     float* dgamma, int64_t rows, int64_t cols, int dtype, float* workspace, int sms,
-                    int* err, cudaStream_t s) {
+                    cudaStream_t s) {
   const nm::BwdArgs p{dy, x, dsum, lddy, lds, lddsum, lddx, rstd, gamma, dx, dgamma ? workspace : nullptr,
-                      rows, cols, err};
+                      rows, cols};
   const int es = dtype == T3_OUT_BF16 ? 2 : 4, v = 16 / es;
   const bool vec = cols % v == 0 && nm::vec_rows(dy, lddy, es) && nm::vec_rows(x, lds, es) &&
                    nm::vec_rows(dsum, lddsum, es) && nm::vec_rows(dx, lddx, es) &&
