@@ -625,7 +625,7 @@ int t3_gated_scan_fwd(const void* gate, int64_t ldg, const void* cand, int64_t l
   const int st = device_info(&dev);
   if (st != T3_OK) return st;
   return launch_scan_fwd(gate, ldg, cand, ldc, h0, resets, h, ldh, h_last, batch, length, width, dtype,
-                         dev->sms, dev->err_word, stream);
+                         dev->err_word, stream);
 }
 
 int t3_gated_scan_bwd(const void* gate, int64_t ldg, const void* cand, int64_t ldc, const void* h,
@@ -643,7 +643,7 @@ int t3_gated_scan_bwd(const void* gate, int64_t ldg, const void* cand, int64_t l
   const int st = device_info(&dev);
   if (st != T3_OK) return st;
   return launch_scan_bwd(gate, ldg, cand, ldc, h, ldh, dh, lddh, h0, resets, dh_last, dgate, lddg, dcand, lddc,
-                         dh0, batch, length, width, dtype, dev->sms, dev->err_word, stream);
+                         dh0, batch, length, width, dtype, dev->err_word, stream);
 }
 
 int t3_gemm_fwd_act(const int8_t* A, const uint8_t* Wp, void* C, int64_t M, int64_t N, int64_t K,

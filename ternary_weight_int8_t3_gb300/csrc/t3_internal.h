@@ -108,12 +108,12 @@ int launch_norm_bwd(const void* dy, int64_t lddy, const void* x, int64_t lds, co
 // The gated recurrence over sequences and its gradient (t3_scan.cu).
 int launch_scan_fwd(const void* gate, int64_t ldg, const void* cand, int64_t ldc, const float* h0,
                     const uint8_t* resets, void* h, int64_t ldh, float* h_last, int64_t batch,
-                    int64_t length, int64_t width, int dtype, int sms, int* err, cudaStream_t s);
+                    int64_t length, int64_t width, int dtype, int* err, cudaStream_t s);
 int launch_scan_bwd(const void* gate, int64_t ldg, const void* cand, int64_t ldc, const void* h,
                     int64_t ldh, const void* dh, int64_t lddh, const float* h0, const uint8_t* resets,
                     const float* dh_last, void* dgate, int64_t lddg, void* dcand, int64_t lddc,
-                    float* dh0, int64_t batch, int64_t length, int64_t width, int dtype, int sms,
-                    int* err, cudaStream_t s);
+                    float* dh0, int64_t batch, int64_t length, int64_t width, int dtype, int* err,
+                    cudaStream_t s);
 
 // What follows a product (EpilogueArgs) on its int32 result (t3_epilogue.cu);
 // x may be out's buffer for T3_OUT_F32.

@@ -32,6 +32,7 @@
 // not change from call to call.  Sequences of a few tokens take one thread per
 // channel pair and no exchange.
 #include <atomic>
+#include <type_traits>
 
 #include "t3_vec.cuh"
 
@@ -42,10 +43,11 @@ using namespace vec;
 
 constexpr int kWarps = 8;
 constexpr int kMaxCluster = 8;
-// CTAs that share an SM.  Both hold 64 KB of stages a CTA; the backward's 16
-// values of k and of its slope a thread spill at the 80 registers that three
-// CTAs leave (8 x 2048 x 3456: 117 us with three, 112 us with two).
-constexpr int kFwdPerSm = 3, kBwdPerSm = 2;
+// CTAs that share an SM.  Their 64 KB of stages would let three; but the 16
+// steps a lane holds spill at the 80 registers that leaves, and two balance better over
+// the SMs (8 x 2048 x 3456 forward: 61 us with three, 55 with two; backward
+// 127 and 118).
+constexpr int kPerSm = 2;
 
 struct FwdArgs {
   const void *gate, *cand;
@@ -128,10 +130,11 @@ __device__ __forceinline__ void wait_peers(uint64_t* bar, uint32_t parity, Waits
 }
 
 // k = sigmoid(-f) = 1 / (1 + e) with e = exp(f), 0 once e is infinite.  Both ways
-// from zero it keeps its relative precision.
-__device__ __forceinline__ float exp_approx(float f) {
+// from zero it keeps its relative precision.  With e held below infinity,
+// k (1 - k) = e k^2 is 0 where k is.
+__device__ __forceinline__ float ex2_approx(float x) {
   float e;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(1.4426950408889634f * f));
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(x));
   return e;
 }
 __device__ __forceinline__ float rcp_approx(float x) {
@@ -139,18 +142,35 @@ __device__ __forceinline__ float rcp_approx(float x) {
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
   return r;
 }
-__device__ __forceinline__ float take_of(float f) { return rcp_approx(1.0f + exp_approx(f)); }
-// The same with k (1 - k) = e k^2: e is held below infinity, so that it is 0 where k is.
-__device__ __forceinline__ float take_of(float f, float& slope) {
-  float e = exp_approx(f);
+__device__ __forceinline__ float below_inf(float e) {
   asm("min.NaN.f32 %0, %0, %1;" : "+f"(e) : "f"(3.402823466e38f));
-  const float k = rcp_approx(1.0f + e);
-  slope = e * k * k;
-  return k;
+  return e;
 }
+__device__ __forceinline__ float take_of(float f) { return rcp_approx(1.0f + ex2_approx(1.4426950408889634f * f)); }
 
 // One step of the state.
 __device__ __forceinline__ float step(float h, float k, float c) { return fmaf(k, c - h, h); }
+
+// Two channels at once: a packed instruction takes the place of two.
+__device__ __forceinline__ float2 sub2(float2 a, float2 b) { return __ffma2_rn(b, make_float2(-1.0f, -1.0f), a); }
+__device__ __forceinline__ float2 step2(float2 h, float2 k, float2 c) { return __ffma2_rn(k, sub2(c, h), h); }
+// R of a step after R: R + k (1 - R).
+__device__ __forceinline__ float2 join2(float2 R, float2 k) {
+  return __ffma2_rn(k, sub2(make_float2(1.0f, 1.0f), R), R);
+}
+__device__ __forceinline__ float2 take2(float2 f) {
+  const float2 x = __fmul2_rn(f, make_float2(1.4426950408889634f, 1.4426950408889634f));
+  const float2 e = __fadd2_rn(make_float2(ex2_approx(x.x), ex2_approx(x.y)), make_float2(1.0f, 1.0f));
+  return make_float2(rcp_approx(e.x), rcp_approx(e.y));
+}
+__device__ __forceinline__ float2 take2(float2 f, float2& slope) {
+  const float2 x = __fmul2_rn(f, make_float2(1.4426950408889634f, 1.4426950408889634f));
+  const float2 e = make_float2(below_inf(ex2_approx(x.x)), below_inf(ex2_approx(x.y)));
+  const float2 d = __fadd2_rn(e, make_float2(1.0f, 1.0f));
+  const float2 k = make_float2(rcp_approx(d.x), rcp_approx(d.y));
+  slope = __fmul2_rn(__fmul2_rn(e, k), k);
+  return k;
+}
 
 // Bit i of the result: whether a reset stands at step t0 + i (i < n <= 32).
 __device__ __forceinline__ uint32_t reset_bits(const uint8_t* resets, int64_t at, int64_t t0, int64_t length,
@@ -183,8 +203,7 @@ struct Maps {
 
 // Sets the barriers up; every thread of the cluster calls it.
 template <int LPR>
-__device__ __forceinline__ void open_maps(Maps<LPR>& m, int size) {
-  if (size == 1) return;
+__device__ __forceinline__ void open_maps(Maps<LPR>& m) {
   if (threadIdx.x == 0) {
     mbar_init(&m.full[0], 1);
     mbar_init(&m.full[1], 1);
@@ -197,15 +216,15 @@ __device__ __forceinline__ void open_maps(Maps<LPR>& m, int size) {
 
 // LPR lanes (two channels each) share a row of the tile, and the 32 / LPR groups
 // of lanes take consecutive runs of steps; each lane has the map (R, H) of its
-// run.  Returns in `in` the state in front of (behind, for kReverse) this lane's run.
+// run.  Returns the state in front of (behind, for kReverse) this lane's run.
 // `carry`, kept by warp 0, is the state in front of the whole cluster's steps and
 // becomes the state past them.  Warp 0 composes the CTA's maps, trades them
 // with the cluster and steps the state from warp to warp; the others only hand
 // their map in and take their state out.
 template <int LPR, bool kReverse>
-__device__ __forceinline__ void exchange(Maps<LPR>& m, float4* cta, int round, int size, int rank, Waits& waits,
-                                         const float (&R)[2], const float (&H)[2], float (&carry)[2],
-                                         float (&in)[2]) {
+__device__ __forceinline__ float2 exchange(Maps<LPR>& m, float4* cta, int round, int size, int rank, Waits& waits,
+                                           float2 R2, float2 H2, float (&carry)[2]) {
+  const float R[2] = {R2.x, R2.y}, H[2] = {H2.x, H2.y};
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int col = lane % LPR, phase = round & 1;
   // over the groups of this warp: the map before this lane's run, and of all
@@ -242,22 +261,29 @@ __device__ __forceinline__ void exchange(Maps<LPR>& m, float4* cta, int round, i
         compose(e[i].z, e[i].w, ar[1], ah[1]);
       }
       if (lane == 0) mbar_arrive_expect_tx(&m.full[phase], size * LPR * 16);
-      float4* slot = cta + (phase * size + rank) * LPR + col;
-      if (lane < LPR)
-        for (int r = 0; r < size; ++r)
-          st_async_v4(peer(slot, r), __float_as_uint(ar[0]), __float_as_uint(ah[0]), __float_as_uint(ar[1]),
-                      __float_as_uint(ah[1]), peer(&m.full[phase], r));
+      float4* slots = cta + phase * size * LPR + col;
+      if (lane < LPR) {
+#pragma unroll
+        for (int r = 0; r < kMaxCluster; ++r)
+          if (r < size)
+            st_async_v4(peer(slots + rank * LPR, r), __float_as_uint(ar[0]), __float_as_uint(ah[0]),
+                        __float_as_uint(ar[1]), __float_as_uint(ah[1]), peer(&m.full[phase], r));
+      }
       __syncwarp();
       wait_peers(&m.full[phase], (round >> 1) & 1, waits);
-      for (int i = 0; i < size; ++i) {
-        const int r = kReverse ? size - 1 - i : i;
-        if (r == rank) {
+      float4 c[kMaxCluster];
+#pragma unroll
+      for (int i = 0; i < kMaxCluster; ++i)
+        if (i < size) c[i] = slots[(kReverse ? size - 1 - i : i) * LPR];
+#pragma unroll
+      for (int i = 0; i < kMaxCluster; ++i) {
+        if (i >= size) break;
+        if ((kReverse ? size - 1 - i : i) == rank) {
           s[0] = carry[0];
           s[1] = carry[1];
         }
-        const float4 c = cta[(phase * size + r) * LPR + col];
-        carry[0] = apply(c.x, c.y, carry[0]);
-        carry[1] = apply(c.z, c.w, carry[1]);
+        carry[0] = apply(c[i].x, c[i].y, carry[0]);
+        carry[1] = apply(c[i].z, c[i].w, carry[1]);
       }
     }
 #pragma unroll
@@ -273,8 +299,12 @@ __device__ __forceinline__ void exchange(Maps<LPR>& m, float4* cta, int round, i
   }
   __syncthreads();
   const float2 v = m.state[warp][col];
-  in[0] = apply(gr[0], gh[0], v.x);
-  in[1] = apply(gr[1], gh[1], v.y);
+  return make_float2(apply(gr[0], gh[0], v.x), apply(gr[1], gh[1], v.y));
+}
+
+// v where the candidate or gradient of a taken token counts: 0 for k = 0.
+__device__ __forceinline__ float2 masked2(float2 k, float2 v) {
+  return make_float2(k.x == 0.0f ? 0.0f : v.x, k.y == 0.0f ? 0.0f : v.y);
 }
 
 // One stage of a warp's operands in shared memory: NA arrays, each the warp's
@@ -328,13 +358,16 @@ __device__ __forceinline__ void load_rows(uint8_t* slab, const T* base, int64_t 
 }
 
 template <class T>
-__device__ __forceinline__ void read_pair(const uint8_t* slab, int row, int rowbytes, int col, float (&f)[2]) {
+__device__ __forceinline__ float2 read_pair(const uint8_t* slab, int row, int rowbytes, int col) {
+  float f[2];
   to_float(load<T, 2>(reinterpret_cast<const T*>(slab + row * rowbytes) + 2 * col), f);
+  return make_float2(f[0], f[1]);
 }
 
 // Two channels to memory: one store where pairs are aligned, else one each.
 template <class T, bool kPair>
-__device__ __forceinline__ void write_pair(T* p, const float (&f)[2], bool second) {
+__device__ __forceinline__ void write_pair(T* p, float2 v, bool second) {
+  const float f[2] = {v.x, v.y};
   if constexpr (kPair) {
     store<T, 2>(p, from_float(f, T()));
   } else {
@@ -344,9 +377,10 @@ __device__ __forceinline__ void write_pair(T* p, const float (&f)[2], bool secon
   }
 }
 
-// CH: bytes a copy; kPair: outputs are aligned to pairs (else element stores).
-template <class T, int LPR, int S, int CH, bool kPair>
-__global__ void __launch_bounds__(32 * kWarps, kFwdPerSm) scan_fwd_kernel(const FwdArgs p) {
+// CH: bytes a copy (16: outputs are aligned to pairs too, else they go element by
+// element).  A launch without a cluster (size 1) executes no cluster instruction.
+template <class T, int LPR, int S, int CH>
+__global__ void __launch_bounds__(32 * kWarps, kPerSm) scan_fwd_kernel(const FwdArgs p) {
   using Stage = Slab<T, LPR, S, 2>;
   extern __shared__ __align__(16) uint8_t smem[];
   __shared__ Maps<LPR> maps;
@@ -376,12 +410,15 @@ __global__ void __launch_bounds__(32 * kWarps, kFwdPerSm) scan_fwd_kernel(const 
     carry[0] = p.h0[b * p.width + ch];
     if (second) carry[1] = p.h0[b * p.width + ch + 1];
   }
-  open_maps(maps, size);
+  if (size > 1) open_maps(maps);
   Waits waits{p.err, &maps.aborted, false};
   int round = 0;
   for (int64_t base = 0; base < p.length; base += span, ++round) {
     const int phase = round & 1;
-    issue(base + span, phase ^ 1);  // past the end: zeros
+    if (base + span < p.length)
+      issue(base + span, phase ^ 1);
+    else
+      copy_commit();  // an empty group, so that waiting for all but one still means this stage
     const uint32_t resets = reset_bits(p.resets, b * p.length, base + mine, p.length, Stage::kRows, lane) >> (group * S);
     copy_wait<1>();
     __syncwarp();
@@ -391,61 +428,45 @@ __global__ void __launch_bounds__(32 * kWarps, kFwdPerSm) scan_fwd_kernel(const 
     const int n = p.length - t0 < S ? static_cast<int>(p.length - t0) : S;  // steps here (may be negative)
     // Steps at the sequence's end, resets, and masked tokens (k = 0) whose
     // candidate is not finite, which would show in H, take the careful form.
-    float k[S][2], c[2], R[2] = {}, H[2] = {}, h[2];
+    const float2 none = make_float2(0.0f, 0.0f), all = make_float2(1.0f, 1.0f);
+    float2 k[S], R = none, H = none, h;
     bool careful = n < S || resets != 0;
     if (!careful) {
 #pragma unroll
       for (int i = 0; i < S; ++i) {
-        read_pair<T>(sf, group * S + i, Stage::kRow, col, k[i]);
-        read_pair<T>(sc, group * S + i, Stage::kRow, col, c);
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          k[i][j] = take_of(k[i][j]);
-          R[j] = fmaf(k[i][j], 1.0f - R[j], R[j]);
-          H[j] = step(H[j], k[i][j], c[j]);
-        }
+        k[i] = take2(read_pair<T>(sf, group * S + i, Stage::kRow, col));
+        R = join2(R, k[i]);
+        H = step2(H, k[i], read_pair<T>(sc, group * S + i, Stage::kRow, col));
       }
-      careful = !(fabsf(H[0]) + fabsf(H[1]) < __int_as_float(0x7f800000));
+      careful = !(fabsf(H.x) + fabsf(H.y) < __int_as_float(0x7f800000));
     }
     if (careful) {
-#pragma unroll
-      for (int j = 0; j < 2; ++j) R[j] = H[j] = 0.0f;
+      R = H = none;
 #pragma unroll
       for (int i = 0; i < S; ++i) {
-        read_pair<T>(sf, group * S + i, Stage::kRow, col, k[i]);
-        read_pair<T>(sc, group * S + i, Stage::kRow, col, c);
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          k[i][j] = i < n ? take_of(k[i][j]) : 0.0f;
-          if (resets >> i & 1) {
-            R[j] = 1.0f;
-            H[j] = 0.0f;
-          }
-          R[j] = fmaf(k[i][j], 1.0f - R[j], R[j]);
-          H[j] = step(H[j], k[i][j], k[i][j] == 0.0f ? 0.0f : c[j]);
+        k[i] = i < n ? take2(read_pair<T>(sf, group * S + i, Stage::kRow, col)) : none;
+        if (resets >> i & 1) {
+          R = all;
+          H = none;
         }
+        R = join2(R, k[i]);
+        H = step2(H, k[i], masked2(k[i], read_pair<T>(sc, group * S + i, Stage::kRow, col)));
       }
     }
-    exchange<LPR, false>(maps, cta_maps, round, size, rank, waits, R, H, carry, h);
+    h = exchange<LPR, false>(maps, cta_maps, round, size, rank, waits, R, H, carry);
     T* o = out + t0 * p.ldh;
     if (!careful) {
 #pragma unroll
       for (int i = 0; i < S; ++i, o += p.ldh) {
-        read_pair<T>(sc, group * S + i, Stage::kRow, col, c);
-#pragma unroll
-        for (int j = 0; j < 2; ++j) h[j] = step(h[j], k[i][j], c[j]);
-        if (live) write_pair<T, kPair>(o, h, second);
+        h = step2(h, k[i], read_pair<T>(sc, group * S + i, Stage::kRow, col));
+        if (live) write_pair<T, (CH == 16)>(o, h, second);
       }
     } else {
 #pragma unroll
       for (int i = 0; i < S; ++i, o += p.ldh) {
-        read_pair<T>(sc, group * S + i, Stage::kRow, col, c);
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          if (resets >> i & 1) h[j] = 0.0f;
-          h[j] = step(h[j], k[i][j], k[i][j] == 0.0f ? 0.0f : c[j]);
-        }
-        if (live && i < n) write_pair<T, kPair>(o, h, second);
+        if (resets >> i & 1) h = none;
+        h = step2(h, k[i], masked2(k[i], read_pair<T>(sc, group * S + i, Stage::kRow, col)));
+        if (live && i < n) write_pair<T, (CH == 16)>(o, h, second);
       }
     }
     __syncwarp();  // this stage is read: the next round copies into it
@@ -493,8 +514,8 @@ __global__ void __launch_bounds__(128) scan_fwd_short_kernel(const FwdArgs p) {
   }
 }
 
-template <class T, int LPR, int S, int CH, bool kPair>
-__global__ void __launch_bounds__(32 * kWarps, kBwdPerSm) scan_bwd_kernel(const BwdArgs p) {
+template <class T, int LPR, int S, int CH>
+__global__ void __launch_bounds__(32 * kWarps, kPerSm) scan_bwd_kernel(const BwdArgs p) {
   using Stage = Slab<T, LPR, S, 4>;
   extern __shared__ __align__(16) uint8_t smem[];
   __shared__ Maps<LPR> maps;
@@ -539,76 +560,68 @@ __global__ void __launch_bounds__(32 * kWarps, kBwdPerSm) scan_bwd_kernel(const 
       if (second) start[1] = p.h0[at + 1];
     }
   }
-  open_maps(maps, size);
+  if (size > 1) open_maps(maps);
   Waits waits{p.err, &maps.aborted, false};
   int round = 0;
   for (int64_t base = last; base >= 0; base -= span, ++round) {
     const int phase = round & 1;
-    issue(base - span, phase ^ 1);
+    if (base > 0)
+      issue(base - span, phase ^ 1);
+    else
+      copy_commit();  // an empty group, so that waiting for all but one still means this stage
     const uint32_t resets = reset_bits(p.resets, row0, base + mine, p.length, Stage::kRows, lane) >> (group * S);
     copy_wait<1>();
     __syncwarp();
     const Stage& st = stages[phase];
     const int64_t t0 = base + mine + group * S;
     const int n = p.length - t0 < S ? static_cast<int>(p.length - t0) : S;
-    float k[S][2], slope[S][2], R[2] = {}, Q[2] = {}, v[2], x[2], y[2], z[2];
+    const float2 none = make_float2(0.0f, 0.0f), all = make_float2(1.0f, 1.0f);
+    float2 k[S], slope[S], R = none, Q = none, v;
     const bool careful = n < S || resets != 0 || t0 == 0;  // ends, resets
     // the map of (1 - k) G past these steps to the same in front of them
-    if (!careful) {
+    auto fold = [&](auto slow) {
 #pragma unroll
       for (int i = S - 1; i >= 0; --i) {
-        read_pair<T>(st.a[0], group * S + i, Stage::kRow, col, x);
-        read_pair<T>(st.a[2], group * S + i, Stage::kRow, col, y);
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          k[i][j] = take_of(x[j], slope[i][j]);
-          const float g = y[j] + Q[j];
-          R[j] = fmaf(k[i][j], 1.0f - R[j], R[j]);
-          Q[j] = fmaf(-k[i][j], g, g);
+        k[i] = take2(read_pair<T>(st.a[0], group * S + i, Stage::kRow, col), slope[i]);
+        if (slow.value && i >= n) k[i] = none;
+        const float2 g = __fadd2_rn(read_pair<T>(st.a[2], group * S + i, Stage::kRow, col), Q);
+        R = join2(R, k[i]);
+        Q = sub2(g, __fmul2_rn(k[i], g));
+        if (slow.value && (resets >> i & 1)) {
+          R = all;
+          Q = none;
         }
       }
-    } else {
+    };
+    if (careful)
+      fold(std::true_type());
+    else
+      fold(std::false_type());
+    v = exchange<LPR, true>(maps, cta_maps, round, size, rank, waits, R, Q, carry);
+    auto put = [&](auto slow) {
+      T* og = dgate + (t0 + S - 1) * p.lddg;
+      T* oc = dcand + (t0 + S - 1) * p.lddc;
 #pragma unroll
-      for (int i = S - 1; i >= 0; --i) {
-        read_pair<T>(st.a[0], group * S + i, Stage::kRow, col, x);
-        read_pair<T>(st.a[2], group * S + i, Stage::kRow, col, y);
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          const float t = take_of(x[j], slope[i][j]);
-          k[i][j] = i < n ? t : 0.0f;
-          const float g = y[j] + Q[j];
-          R[j] = fmaf(k[i][j], 1.0f - R[j], R[j]);
-          Q[j] = fmaf(-k[i][j], g, g);
-          if (resets >> i & 1) {
-            R[j] = 1.0f;
-            Q[j] = 0.0f;
-          }
+      for (int i = S - 1; i >= 0; --i, og -= p.lddg, oc -= p.lddc) {
+        const float2 g = __fadd2_rn(read_pair<T>(st.a[2], group * S + i, Stage::kRow, col), v);
+        float2 before = read_pair<T>(st.a[3], group * S + i, Stage::kRow, col);
+        const bool reset = slow.value && (resets >> i & 1);
+        if (slow.value && t0 + i == 0) before = make_float2(start[0], start[1]);
+        if (reset) before = none;
+        const float2 dc = __fmul2_rn(k[i], g);
+        const float2 diff = sub2(before, read_pair<T>(st.a[1], group * S + i, Stage::kRow, col));
+        const float2 df = masked2(slope[i], __fmul2_rn(__fmul2_rn(g, slope[i]), diff));
+        v = reset ? none : sub2(g, dc);
+        if (live && (!slow.value || i < n)) {
+          write_pair<T, (CH == 16)>(og, df, second);
+          write_pair<T, (CH == 16)>(oc, dc, second);
         }
       }
-    }
-    exchange<LPR, true>(maps, cta_maps, round, size, rank, waits, R, Q, carry, v);
-    T* og = dgate + (t0 + S - 1) * p.lddg;
-    T* oc = dcand + (t0 + S - 1) * p.lddc;
-#pragma unroll
-    for (int i = S - 1; i >= 0; --i, og -= p.lddg, oc -= p.lddc) {
-      read_pair<T>(st.a[1], group * S + i, Stage::kRow, col, x);
-      read_pair<T>(st.a[2], group * S + i, Stage::kRow, col, y);
-      read_pair<T>(st.a[3], group * S + i, Stage::kRow, col, z);
-      const bool reset = careful && (resets >> i & 1);
-      float df[2], dc[2];
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const float g = y[j] + v[j];
-        if (careful) z[j] = reset ? 0.0f : (t0 + i == 0 ? start[j] : z[j]);
-        dc[j] = k[i][j] * g;
-        df[j] = slope[i][j] == 0.0f ? 0.0f : g * slope[i][j] * (z[j] - x[j]);
-        v[j] = reset ? 0.0f : fmaf(-k[i][j], g, g);
-      }
-      if (live && (!careful || i < n)) {
-        write_pair<T, kPair>(og, df, second);
-        write_pair<T, kPair>(oc, dc, second);
-      }
-    }
+    };
+    if (careful)
+      put(std::true_type());
+    else
+      put(std::false_type());
     __syncwarp();  // this stage is read: the next round copies into it
   }
   copy_wait<0>();
@@ -617,16 +630,6 @@ __global__ void __launch_bounds__(32 * kWarps, kBwdPerSm) scan_bwd_kernel(const 
     p.dh0[b * p.width + ch] = carry[0];
     if (second) p.dh0[b * p.width + ch + 1] = carry[1];
   }
-}
-
-// CTAs in a cluster: as many as leave all clusters resident at once, none of
-// them without steps.  (A second wave costs as much as the first, and a
-// cluster that waits for room holds up its sequences from the start.)
-int cluster_for(int64_t tiles, int64_t length, int rows, int slots) {
-  const int64_t room = slots / tiles;
-  const int64_t most = (length + kWarps * rows - 1) / (kWarps * rows);
-  const int64_t c = room < most ? room : most;
-  return static_cast<int>(c < 1 ? 1 : c > kMaxCluster ? kMaxCluster : c);
 }
 
 constexpr int64_t kShort = 8;  // tokens up to which a sequence is not split
@@ -649,50 +652,119 @@ int allow_smem(int bytes) {
   return T3_OK;
 }
 
-template <class T, int LPR, int CH, bool kPair>
-int run_fwd(FwdArgs p, int64_t batch, int sms, cudaStream_t s) {
-  constexpr int S = kFwdSteps<T>;
-  constexpr int smem = 2 * kWarps * sizeof(Slab<T, LPR, S, 2>), per_cta = 2 * LPR * sizeof(float4);
-  const int st = allow_smem<scan_fwd_kernel<T, LPR, S, CH, kPair>>(smem + kMaxCluster * per_cta);
-  if (st != T3_OK) return st;
-  p.tiles = (p.width + 2 * LPR - 1) / (2 * LPR);
-  const int c = cluster_for(batch * p.tiles, p.length, 32 / LPR * S, kFwdPerSm * sms);
-  return launch(scan_fwd_kernel<T, LPR, S, CH, kPair>, batch * p.tiles * c, 32 * kWarps, smem + (c > 1 ? c * per_cta : 0), s, c, p);
+// How many clusters of c CTAs of `Fn` are resident at once (cached per device).
+template <auto Fn>
+int max_clusters(int c, size_t smem) {
+  static std::atomic<int> cache[64][kMaxCluster + 1];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
+  int n = cache[dev][c].load(std::memory_order_acquire);
+  if (n > 0) return n;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = static_cast<unsigned>(c);
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(c), 1, 1);
+  cfg.blockDim = dim3(32 * kWarps, 1, 1);
+  cfg.dynamicSmemBytes = smem;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (cudaOccupancyMaxActiveClusters(&n, Fn, &cfg) != cudaSuccess || n < 1) return 0;
+  cache[dev][c].store(n, std::memory_order_release);
+  return n;
 }
 
-template <class T, int LPR, int CH, bool kPair>
-int run_bwd(BwdArgs p, int64_t batch, int sms, cudaStream_t s) {
-  constexpr int S = kBwdSteps<T>;
-  constexpr int smem = 2 * kWarps * sizeof(Slab<T, LPR, S, 4>), per_cta = 2 * LPR * sizeof(float4);
-  const int st = allow_smem<scan_bwd_kernel<T, LPR, S, CH, kPair>>(smem + kMaxCluster * per_cta);
-  if (st != T3_OK) return st;
-  p.tiles = (p.width + 2 * LPR - 1) / (2 * LPR);
-  const int c = cluster_for(batch * p.tiles, p.length, 32 / LPR * S, kBwdPerSm * sms);
-  return launch(scan_bwd_kernel<T, LPR, S, CH, kPair>, batch * p.tiles * c, 32 * kWarps, smem + (c > 1 ? c * per_cta : 0), s, c, p);
+// Rows of 32 channels fetch half as much with each access: they have to win by
+// this factor.
+constexpr double kNarrowGain = 1.2;
+
+// A launch: CTAs a cluster, and its estimated time in rounds of one CTA.  All
+// clusters of a wave walk their sequences side by side, `rows` steps a CTA and
+// round; a round that ends in an exchange across the cluster takes about 1.4
+// times one that does not.
+struct Plan {
+  int cluster;
+  double cost;
+};
+
+template <auto Fn>
+Plan plan(int64_t tiles, int64_t length, int rows, int smem, int per_cta) {
+  Plan best{0, 0.0};
+  for (int c = 1; c <= kMaxCluster; ++c) {
+    if (c > 1 && (c - 1) * static_cast<int64_t>(rows) >= length) break;  // CTAs without steps
+    const int n = max_clusters<Fn>(c, smem + (c > 1 ? c * per_cta : 0));
+    if (n < 1) continue;
+    const int64_t full = tiles / n, left = tiles % n, rounds = (length + c * rows - 1) / (c * rows);
+    // a last wave that is not full has the SMs more to itself
+    const double waves = static_cast<double>(full) + (left ? 0.5 + 0.5 * left / n : 0.0);
+    const double cost = waves * rounds * (c > 1 ? 1.4 : 1.0);
+    if (best.cluster == 0 || cost < best.cost) best = {c, cost};
+  }
+  return best;
 }
 
-// Tiles of 64 channels, or of 32 where those would leave the GPU short of
-// CTAs even in the largest clusters.
-bool narrow(int64_t batch, int64_t width, int sms) {
-  return batch * ((width + 63) / 64) * kMaxCluster < 2ll * sms;
+template <class T, int CH>
+struct Fwd {
+  template <int LPR> struct Kernel;
+};
+template <class T, int CH>
+struct Bwd {
+  template <int LPR> struct Kernel;
+};
+template <class T, int CH>
+template <int LPR>
+struct Fwd<T, CH>::Kernel {
+  static constexpr int S = kFwdSteps<T>, rows = kWarps * (32 / LPR) * S;
+  static constexpr int smem = 2 * kWarps * sizeof(Slab<T, LPR, S, 2>), per_cta = 2 * LPR * sizeof(float4);
+  static constexpr auto fn = scan_fwd_kernel<T, LPR, S, CH>;
+};
+template <class T, int CH>
+template <int LPR>
+struct Bwd<T, CH>::Kernel {
+  static constexpr int S = kBwdSteps<T>, rows = kWarps * (32 / LPR) * S;
+  static constexpr int smem = 2 * kWarps * sizeof(Slab<T, LPR, S, 4>), per_cta = 2 * LPR * sizeof(float4);
+  static constexpr auto fn = scan_bwd_kernel<T, LPR, S, CH>;
+};
+
+template <class K, int LPR, class Args>
+int run_plan(Args p, int64_t batch, int cluster, cudaStream_t s) {
+  p.tiles = (p.width + 2 * LPR - 1) / (2 * LPR);
+  return launch(K::fn, batch * p.tiles * cluster, 32 * kWarps, K::smem + (cluster > 1 ? cluster * K::per_cta : 0), s,
+                cluster, p);
+}
+
+// Tiles of 64 channels, or of 32 where that is estimated to be faster: few
+// channels leave the GPU short of CTAs.
+template <template <int> class K, class Args>
+int run(const Args& p, int64_t batch, cudaStream_t s) {
+  using Wide = K<32>;
+  using Narrow = K<16>;
+  int st = allow_smem<Wide::fn>(Wide::smem + kMaxCluster * Wide::per_cta);
+  if (st == T3_OK) st = allow_smem<Narrow::fn>(Narrow::smem + kMaxCluster * Narrow::per_cta);
+  if (st != T3_OK) return st;
+  const Plan w = plan<Wide::fn>(batch * ((p.width + 63) / 64), p.length, Wide::rows, Wide::smem, Wide::per_cta);
+  const Plan n = plan<Narrow::fn>(batch * ((p.width + 31) / 32), p.length, Narrow::rows, Narrow::smem, Narrow::per_cta);
+  if (w.cluster == 0 && n.cluster == 0) return T3_ECUDA;
+  if (n.cluster == 0 || (w.cluster > 0 && w.cost <= kNarrowGain * n.cost)) return run_plan<Wide, 32>(p, batch, w.cluster, s);
+  return run_plan<Narrow, 16>(p, batch, n.cluster, s);
 }
 
 // CH 16: rows of whole 16-byte pieces; otherwise pieces of 4 bytes, or of one
 // element where rows of 2-byte elements start on odd boundaries.
-template <class T, int LPR>
-int fwd(const FwdArgs& p, int64_t batch, int ch, bool pair, int sms, cudaStream_t s) {
-  if (ch == 16) return run_fwd<T, LPR, 16, true>(p, batch, sms, s);
-  if (sizeof(T) == 4 || ch == 4)
-    return pair ? run_fwd<T, LPR, 4, true>(p, batch, sms, s) : run_fwd<T, LPR, 4, false>(p, batch, sms, s);
-  return run_fwd<T, LPR, sizeof(T) == 4 ? 4 : 2, false>(p, batch, sms, s);
+template <class T>
+int fwd(const FwdArgs& p, int64_t batch, int ch, cudaStream_t s) {
+  if (ch == 16) return run<Fwd<T, 16>::template Kernel>(p, batch, s);
+  if (sizeof(T) == 4 || ch == 4) return run<Fwd<T, 4>::template Kernel>(p, batch, s);
+  return run<Fwd<T, sizeof(T) == 4 ? 4 : 2>::template Kernel>(p, batch, s);
 }
 
-template <class T, int LPR>
-int bwd(const BwdArgs& p, int64_t batch, int ch, bool pair, int sms, cudaStream_t s) {
-  if (ch == 16) return run_bwd<T, LPR, 16, true>(p, batch, sms, s);
-  if (sizeof(T) == 4 || ch == 4)
-    return pair ? run_bwd<T, LPR, 4, true>(p, batch, sms, s) : run_bwd<T, LPR, 4, false>(p, batch, sms, s);
-  return run_bwd<T, LPR, sizeof(T) == 4 ? 4 : 2, false>(p, batch, sms, s);
+template <class T>
+int bwd(const BwdArgs& p, int64_t batch, int ch, cudaStream_t s) {
+  if (ch == 16) return run<Bwd<T, 16>::template Kernel>(p, batch, s);
+  if (sizeof(T) == 4 || ch == 4) return run<Bwd<T, 4>::template Kernel>(p, batch, s);
+  return run<Bwd<T, sizeof(T) == 4 ? 4 : 2>::template Kernel>(p, batch, s);
 }
 
 // Whether every row of `width` elements at `p` with stride ld starts and ends
@@ -705,7 +777,7 @@ bool rows_on(const void* p, int64_t ld, int64_t width, int es, int bytes) {
 
 int launch_scan_fwd(const void* gate, int64_t ldg, const void* cand, int64_t ldc, const float* h0,
                     const uint8_t* resets, void* h, int64_t ldh, float* h_last, int64_t batch,
-                    int64_t length, int64_t width, int dtype, int sms, int* err, cudaStream_t s) {
+                    int64_t length, int64_t width, int dtype, int* err, cudaStream_t s) {
   const sc::FwdArgs p{gate, cand, ldg, ldc, ldh, h0, resets, h, h_last, length, width, 0, batch * width, err};
   const int es = dtype == T3_OUT_BF16 ? 2 : 4;
   auto on = [&](int n) { return sc::rows_on(gate, ldg, width, es, n) && sc::rows_on(cand, ldc, width, es, n); };
@@ -719,17 +791,14 @@ int launch_scan_fwd(const void* gate, int64_t ldg, const void* cand, int64_t ldc
     return vec::launch(fn, (n + 127) / 128, 128, 0, s, 1, p);
   }
   const int ch = pair && on(16) ? 16 : on(4) ? 4 : 2;
-  const bool nar = sc::narrow(batch, width, sms);
-  if (dtype == T3_OUT_BF16)
-    return nar ? sc::fwd<vec::bf16, 16>(p, batch, ch, pair, sms, s) : sc::fwd<vec::bf16, 32>(p, batch, ch, pair, sms, s);
-  return nar ? sc::fwd<float, 16>(p, batch, ch, pair, sms, s) : sc::fwd<float, 32>(p, batch, ch, pair, sms, s);
+  return dtype == T3_OUT_BF16 ? sc::fwd<vec::bf16>(p, batch, ch, s) : sc::fwd<float>(p, batch, ch, s);
 }
 
 int launch_scan_bwd(const void* gate, int64_t ldg, const void* cand, int64_t ldc, const void* h,
                     int64_t ldh, const void* dh, int64_t lddh, const float* h0, const uint8_t* resets,
                     const float* dh_last, void* dgate, int64_t lddg, void* dcand, int64_t lddc,
-                    float* dh0, int64_t batch, int64_t length, int64_t width, int dtype, int sms,
-                    int* err, cudaStream_t s) {
+                    float* dh0, int64_t batch, int64_t length, int64_t width, int dtype, int* err,
+                    cudaStream_t s) {
   const sc::BwdArgs p{gate, cand, h, dh, ldg, ldc, ldh, lddh, lddg, lddc, h0, resets, dh_last,
                       dgate, dcand, dh0, length, width, 0, err};
   const int es = dtype == T3_OUT_BF16 ? 2 : 4;
@@ -739,10 +808,7 @@ int launch_scan_bwd(const void* gate, int64_t ldg, const void* cand, int64_t ldc
   };
   const bool pair = sc::rows_on(dgate, lddg, width, es, 2 * es) && sc::rows_on(dcand, lddc, width, es, 2 * es);
   const int ch = pair && on(16) ? 16 : on(4) ? 4 : 2;
-  const bool nar = sc::narrow(batch, width, sms);
-  if (dtype == T3_OUT_BF16)
-    return nar ? sc::bwd<vec::bf16, 16>(p, batch, ch, pair, sms, s) : sc::bwd<vec::bf16, 32>(p, batch, ch, pair, sms, s);
-  return nar ? sc::bwd<float, 16>(p, batch, ch, pair, sms, s) : sc::bwd<float, 32>(p, batch, ch, pair, sms, s);
+  return dtype == T3_OUT_BF16 ? sc::bwd<vec::bf16>(p, batch, ch, s) : sc::bwd<float>(p, batch, ch, s);
 }
 
 }  // namespace t3
