@@ -174,8 +174,9 @@ int epilogue_act(const Args& p, int sms, cudaStream_t s) {
 template <class T, int VEC>
 int act_bwd_act(BwdArgs p, int act, int sms, int* parts, cudaStream_t s) {
   const int64_t tiles = (p.cols + 32 * VEC - 1) / (32 * VEC);
-  // about four CTAs an SM, each with at least one round of rows a warp
-  int64_t n = (4ll * sms + tiles - 1) / tiles;
+  // at most four CTAs an SM (one wave: a few CTAs more would double the time),
+  // each with at least one round of rows a warp
+  int64_t n = 4ll * sms / tiles > 1 ? 4ll * sms / tiles : 1;
   const int64_t most = (p.rows + 8 * kUnroll - 1) / (8 * kUnroll);
   if (n > most) n = most;
   if (n > kMaxColParts) n = kMaxColParts;
