@@ -314,7 +314,10 @@ template <class T, int LPR, int S, int NA>
 struct Slab {
   static constexpr int kRow = 2 * LPR * static_cast<int>(sizeof(T));
   static constexpr int kRows = 32 / LPR * S;
-  static constexpr int kBytes = kRow * kRows;
+  // the second group's rows lie one row further on, so that both groups' reads
+  // of a step meet all banks once
+  static constexpr int kSkip = LPR == 16 ? kRow : 0;
+  static constexpr int kBytes = kRow * kRows + kSkip;
   uint8_t a[NA][kBytes];
 };
 
@@ -346,10 +349,11 @@ __device__ __forceinline__ void load_rows(uint8_t* slab, const T* base, int64_t 
   constexpr int kPer = 32 * CH >= kRow ? 1 : kRow / (32 * CH);  // rounds a row takes
   const int row = lane * CH / kRow, c = lane * CH % kRow / static_cast<int>(sizeof(T));
   const T* src = base + (t0 + row) * ld + c;
-  uint8_t* dst = slab + lane * CH;
 #pragma unroll
-  for (int i = 0; i < kPieces / 32; ++i, dst += 32 * CH) {
-    const int64_t t = t0 + row + i / kPer * kEach;
+  for (int i = 0; i < kPieces / 32; ++i) {
+    const int r = row + i / kPer * kEach;
+    uint8_t* dst = slab + (i * 32 + lane) * CH + (r >= S ? kRow : 0);  // r >= S: the second group
+    const int64_t t = t0 + r;
     const int at = i % kPer * (32 * CH / static_cast<int>(sizeof(T)));  // channels along the row
     const bool ok = t >= 0 && t < length && ch0 + c + at < width;
     copy_async<CH>(dst, ok ? src + at : base, ok);
@@ -357,6 +361,7 @@ __device__ __forceinline__ void load_rows(uint8_t* slab, const T* base, int64_t 
   }
 }
 
+// This lane's pair of a row; `slab` is where its group's rows begin.
 template <class T>
 __device__ __forceinline__ float2 read_pair(const uint8_t* slab, int row, int rowbytes, int col) {
   float f[2];
@@ -422,8 +427,8 @@ __global__ void __launch_bounds__(32 * kWarps, kPerSm) scan_fwd_kernel(const Fwd
     const uint32_t resets = reset_bits(p.resets, b * p.length, base + mine, p.length, Stage::kRows, lane) >> (group * S);
     copy_wait<1>();
     __syncwarp();
-    const uint8_t* sf = stages[phase].a[0];
-    const uint8_t* sc = stages[phase].a[1];
+    const uint8_t* sf = stages[phase].a[0] + group * (S * Stage::kRow + Stage::kSkip);
+    const uint8_t* sc = stages[phase].a[1] + group * (S * Stage::kRow + Stage::kSkip);
     const int64_t t0 = base + mine + group * S;
     const int n = p.length - t0 < S ? static_cast<int>(p.length - t0) : S;  // steps here (may be negative)
     // Steps at the sequence's end, resets, and masked tokens (k = 0) whose
@@ -434,9 +439,9 @@ __global__ void __launch_bounds__(32 * kWarps, kPerSm) scan_fwd_kernel(const Fwd
     if (!careful) {
 #pragma unroll
       for (int i = 0; i < S; ++i) {
-        k[i] = take2(read_pair<T>(sf, group * S + i, Stage::kRow, col));
+        k[i] = take2(read_pair<T>(sf, i, Stage::kRow, col));
         R = join2(R, k[i]);
-        H = step2(H, k[i], read_pair<T>(sc, group * S + i, Stage::kRow, col));
+        H = step2(H, k[i], read_pair<T>(sc, i, Stage::kRow, col));
       }
       careful = !(fabsf(H.x) + fabsf(H.y) < __int_as_float(0x7f800000));
     }
@@ -444,13 +449,13 @@ __global__ void __launch_bounds__(32 * kWarps, kPerSm) scan_fwd_kernel(const Fwd
       R = H = none;
 #pragma unroll
       for (int i = 0; i < S; ++i) {
-        k[i] = i < n ? take2(read_pair<T>(sf, group * S + i, Stage::kRow, col)) : none;
+        k[i] = i < n ? take2(read_pair<T>(sf, i, Stage::kRow, col)) : none;
         if (resets >> i & 1) {
           R = all;
           H = none;
         }
         R = join2(R, k[i]);
-        H = step2(H, k[i], masked2(k[i], read_pair<T>(sc, group * S + i, Stage::kRow, col)));
+        H = step2(H, k[i], masked2(k[i], read_pair<T>(sc, i, Stage::kRow, col)));
       }
     }
     h = exchange<LPR, false>(maps, cta_maps, round, size, rank, waits, R, H, carry);
@@ -458,14 +463,14 @@ __global__ void __launch_bounds__(32 * kWarps, kPerSm) scan_fwd_kernel(const Fwd
     if (!careful) {
 #pragma unroll
       for (int i = 0; i < S; ++i, o += p.ldh) {
-        h = step2(h, k[i], read_pair<T>(sc, group * S + i, Stage::kRow, col));
+        h = step2(h, k[i], read_pair<T>(sc, i, Stage::kRow, col));
         if (live) write_pair<T, (CH == 16)>(o, h, second);
       }
     } else {
 #pragma unroll
       for (int i = 0; i < S; ++i, o += p.ldh) {
         if (resets >> i & 1) h = none;
-        h = step2(h, k[i], masked2(k[i], read_pair<T>(sc, group * S + i, Stage::kRow, col)));
+        h = step2(h, k[i], masked2(k[i], read_pair<T>(sc, i, Stage::kRow, col)));
         if (live && i < n) write_pair<T, (CH == 16)>(o, h, second);
       }
     }
@@ -573,6 +578,7 @@ __global__ void __launch_bounds__(32 * kWarps, kPerSm) scan_bwd_kernel(const Bwd
     copy_wait<1>();
     __syncwarp();
     const Stage& st = stages[phase];
+    const int at = group * (S * Stage::kRow + Stage::kSkip);
     const int64_t t0 = base + mine + group * S;
     const int n = p.length - t0 < S ? static_cast<int>(p.length - t0) : S;
     const float2 none = make_float2(0.0f, 0.0f), all = make_float2(1.0f, 1.0f);
@@ -582,9 +588,9 @@ __global__ void __launch_bounds__(32 * kWarps, kPerSm) scan_bwd_kernel(const Bwd
     auto fold = [&](auto slow) {
 #pragma unroll
       for (int i = S - 1; i >= 0; --i) {
-        k[i] = take2(read_pair<T>(st.a[0], group * S + i, Stage::kRow, col), slope[i]);
+        k[i] = take2(read_pair<T>(st.a[0] + at, i, Stage::kRow, col), slope[i]);
         if (slow.value && i >= n) k[i] = none;
-        const float2 g = __fadd2_rn(read_pair<T>(st.a[2], group * S + i, Stage::kRow, col), Q);
+        const float2 g = __fadd2_rn(read_pair<T>(st.a[2] + at, i, Stage::kRow, col), Q);
         R = join2(R, k[i]);
         Q = sub2(g, __fmul2_rn(k[i], g));
         if (slow.value && (resets >> i & 1)) {
@@ -603,13 +609,13 @@ __global__ void __launch_bounds__(32 * kWarps, kPerSm) scan_bwd_kernel(const Bwd
       T* oc = dcand + (t0 + S - 1) * p.lddc;
 #pragma unroll
       for (int i = S - 1; i >= 0; --i, og -= p.lddg, oc -= p.lddc) {
-        const float2 g = __fadd2_rn(read_pair<T>(st.a[2], group * S + i, Stage::kRow, col), v);
-        float2 before = read_pair<T>(st.a[3], group * S + i, Stage::kRow, col);
+        const float2 g = __fadd2_rn(read_pair<T>(st.a[2] + at, i, Stage::kRow, col), v);
+        float2 before = read_pair<T>(st.a[3] + at, i, Stage::kRow, col);
         const bool reset = slow.value && (resets >> i & 1);
         if (slow.value && t0 + i == 0) before = make_float2(start[0], start[1]);
         if (reset) before = none;
         const float2 dc = __fmul2_rn(k[i], g);
-        const float2 diff = sub2(before, read_pair<T>(st.a[1], group * S + i, Stage::kRow, col));
+        const float2 diff = sub2(before, read_pair<T>(st.a[1] + at, i, Stage::kRow, col));
         const float2 df = masked2(slope[i], __fmul2_rn(__fmul2_rn(g, slope[i]), diff));
         v = reset ? none : sub2(g, dc);
         if (live && (!slow.value || i < n)) {
@@ -682,8 +688,8 @@ constexpr double kNarrowGain = 1.2;
 
 // A launch: CTAs a cluster, and its estimated time in rounds of one CTA.  All
 // clusters of a wave walk their sequences side by side, `rows` steps a CTA and
-// round; a round that ends in an exchange across the cluster takes about 1.4
-// times one that does not.
+// round; a round that ends in an exchange across the cluster takes about 1.15
+// times one that does not, or 1.4 times where later waves keep the SMs full.
 struct Plan {
   int cluster;
   double cost;
@@ -699,7 +705,7 @@ Plan plan(int64_t tiles, int64_t length, int rows, int smem, int per_cta) {
     const int64_t full = tiles / n, left = tiles % n, rounds = (length + c * rows - 1) / (c * rows);
     // a last wave that is not full has the SMs more to itself
     const double waves = static_cast<double>(full) + (left ? 0.5 + 0.5 * left / n : 0.0);
-    const double cost = waves * rounds * (c > 1 ? 1.4 : 1.0);
+    const double cost = waves * rounds * (c == 1 ? 1.0 : waves <= 1.0 ? 1.15 : 1.4);
     if (best.cluster == 0 || cost < best.cost) best = {c, cost};
   }
   return best;
