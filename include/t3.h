@@ -377,7 +377,8 @@ enum { T3_ACT_NONE = 0, T3_ACT_RELU = 1, T3_ACT_RELU2 = 2, T3_ACT_SILU = 3, T3_A
  * row_scale [M], col_scale [N], bias [N] (float), residual [M][N] and pre
  * [M][N] (the output's type) may each be NULL: ones, ones, zeros, zeros, not
  * written.  pre is what t3_act_bwd takes.  out_kind: T3_OUT_F32 or T3_OUT_BF16.  K = 0
- * takes x = 0.  residual and pre must not be C's buffer (T3_EINVAL).  One
+ * takes x = 0.  C, residual and pre must be different buffers, and workspace
+ * another one than a bf16 C (T3_EINVAL).  One
  * kernel does it all for one or two rows (and up to eight when Wp is at most 4
  * MB), and for M > 32 where A, Wp, C, residual and pre have rows of whole 16-
  * byte pieces on 16-byte boundaries, K <= 65536 and the product is not one of

@@ -652,7 +652,9 @@ int t3_gemm_fwd_act(const int8_t* A, const uint8_t* Wp, void* C, int64_t M, int6
                     t3_stream_t stream) {
   if (bad_dims(M, N, K) || !valid_dtype(out_kind) || !valid_act(act)) return T3_EINVAL;
   if (M == 0 || N == 0) return T3_OK;
-  if (!C || (K > 0 && (!A || !Wp)) || C == residual || C == pre) return T3_EINVAL;
+  if (!C || (K > 0 && (!A || !Wp)) || C == residual || C == pre || (pre && pre == residual) ||
+      (out_kind == T3_OUT_BF16 && workspace == C))
+    return T3_EINVAL;
   if (K > kMaxTernaryReduction) return T3_EOVERFLOW;
   const EpilogueArgs e{row_scale, col_scale, bias, residual, pre, act};
   const DeviceInfo* dev = nullptr;

@@ -361,29 +361,43 @@ __device__ __forceinline__ void load_rows(uint8_t* slab, const T* base, int64_t 
   }
 }
 
-// This lane's pair of a row; `slab` is where its group's rows begin.
-template <class T>
-__device__ __forceinline__ float2 read_pair(const uint8_t* slab, int row, int rowbytes, int col) {
-  float f[2];
-  to_float(load<T, 2>(reinterpret_cast<const T*>(slab + row * rowbytes) + 2 * col), f);
-  return make_float2(f[0], f[1]);
-}
+// A lane's two channels of a tile: neighbours where rows are 16-byte pieces
+// (one access for both), else `col` and `col + LPR`, so that each access of a
+// warp covers neighbouring elements.
+template <int LPR, bool kPair> __device__ __forceinline__ int first_channel(int col) { return kPair ? 2 * col : col; }
+template <int LPR, bool kPair> constexpr int kApart = kPair ? 1 : LPR;
 
-// Two channels to memory: one store where pairs are aligned, else one each.
-template <class T, bool kPair>
-__device__ __forceinline__ void write_pair(T* p, float2 v, bool second) {
-  const float f[2] = {v.x, v.y};
+// This lane's pair of a row; `slab` is where its group's rows begin.
+template <class T, int LPR, bool kPair>
+__device__ __forceinline__ float2 read_pair(const uint8_t* slab, int row, int col) {
+  const T* p = reinterpret_cast<const T*>(slab) + row * (2 * LPR);
   if constexpr (kPair) {
-    store<T, 2>(p, from_float(f, T()));
+    float f[2];
+    to_float(load<T, 2>(p + 2 * col), f);
+    return make_float2(f[0], f[1]);
   } else {
-    const float lo[1] = {f[0]}, hi[1] = {f[1]};
-    store<T, 1>(p, from_float(lo, T()));
-    if (second) store<T, 1>(p + 1, from_float(hi, T()));
+    float x[1], y[1];
+    to_float(load<T, 1>(p + col), x);
+    to_float(load<T, 1>(p + col + LPR), y);
+    return make_float2(x[0], y[0]);
   }
 }
 
-// CH: bytes a copy (16: outputs are aligned to pairs too, else they go element by
-// element).  A launch without a cluster (size 1) executes no cluster instruction.
+// The pair to memory, p at its first channel.
+template <class T, int LPR, bool kPair>
+__device__ __forceinline__ void write_pair(T* p, float2 v, bool second) {
+  if constexpr (kPair) {
+    const float f[2] = {v.x, v.y};
+    store<T, 2>(p, from_float(f, T()));
+  } else {
+    const float lo[1] = {v.x}, hi[1] = {v.y};
+    store<T, 1>(p, from_float(lo, T()));
+    if (second) store<T, 1>(p + LPR, from_float(hi, T()));
+  }
+}
+
+// CH: bytes a copy (16: rows of whole 16-byte pieces, outputs on pairs).  A
+// launch without a cluster (size 1) executes no cluster instruction.
 template <class T, int LPR, int S, int CH>
 __global__ void __launch_bounds__(32 * kWarps, kPerSm) scan_fwd_kernel(const FwdArgs p) {
   using Stage = Slab<T, LPR, S, 2>;
@@ -393,8 +407,9 @@ __global__ void __launch_bounds__(32 * kWarps, kPerSm) scan_fwd_kernel(const Fwd
   const int col = lane % LPR, group = lane / LPR;
   const int size = static_cast<int>(cluster_size()), rank = static_cast<int>(cluster_rank());
   const int64_t tile = blockIdx.x / size;
-  const int64_t b = tile / p.tiles, ch0 = (tile - b * p.tiles) * (2 * LPR), ch = ch0 + 2 * col;
-  const bool live = ch < p.width, second = ch + 1 < p.width;
+  const int64_t b = tile / p.tiles, ch0 = (tile - b * p.tiles) * (2 * LPR), ch = ch0 + first_channel<LPR, CH == 16>(col);
+  constexpr int kNext = kApart<LPR, CH == 16>;  // to the lane's second channel
+  const bool live = ch < p.width, second = ch + kNext < p.width;
   const T* gate = static_cast<const T*>(p.gate) + b * p.length * p.ldg + ch0;
   const T* cand = static_cast<const T*>(p.cand) + b * p.length * p.ldc + ch0;
   T* out = static_cast<T*>(p.h) + b * p.length * p.ldh + ch;
@@ -413,7 +428,7 @@ __global__ void __launch_bounds__(32 * kWarps, kPerSm) scan_fwd_kernel(const Fwd
   issue(0, 0);
   if (p.h0 && live) {  // plain loads: h_last may be the same array
     carry[0] = p.h0[b * p.width + ch];
-    if (second) carry[1] = p.h0[b * p.width + ch + 1];
+    if (second) carry[1] = p.h0[b * p.width + ch + kNext];
   }
   if (size > 1) open_maps(maps);
   Waits waits{p.err, &maps.aborted, false};
@@ -439,9 +454,9 @@ __global__ void __launch_bounds__(32 * kWarps, kPerSm) scan_fwd_kernel(const Fwd
     if (!careful) {
 #pragma unroll
       for (int i = 0; i < S; ++i) {
-        k[i] = take2(read_pair<T>(sf, i, Stage::kRow, col));
+        k[i] = take2(read_pair<T, LPR, CH == 16>(sf, i, col));
         R = join2(R, k[i]);
-        H = step2(H, k[i], read_pair<T>(sc, i, Stage::kRow, col));
+        H = step2(H, k[i], read_pair<T, LPR, CH == 16>(sc, i, col));
       }
       careful = !(fabsf(H.x) + fabsf(H.y) < __int_as_float(0x7f800000));
     }
@@ -449,13 +464,13 @@ __global__ void __launch_bounds__(32 * kWarps, kPerSm) scan_fwd_kernel(const Fwd
       R = H = none;
 #pragma unroll
       for (int i = 0; i < S; ++i) {
-        k[i] = i < n ? take2(read_pair<T>(sf, i, Stage::kRow, col)) : none;
+        k[i] = i < n ? take2(read_pair<T, LPR, CH == 16>(sf, i, col)) : none;
         if (resets >> i & 1) {
           R = all;
           H = none;
         }
         R = join2(R, k[i]);
-        H = step2(H, k[i], masked2(k[i], read_pair<T>(sc, i, Stage::kRow, col)));
+        H = step2(H, k[i], masked2(k[i], read_pair<T, LPR, CH == 16>(sc, i, col)));
       }
     }
     h = exchange<LPR, false>(maps, cta_maps, round, size, rank, waits, R, H, carry);
@@ -463,15 +478,15 @@ __global__ void __launch_bounds__(32 * kWarps, kPerSm) scan_fwd_kernel(const Fwd
     if (!careful) {
 #pragma unroll
       for (int i = 0; i < S; ++i, o += p.ldh) {
-        h = step2(h, k[i], read_pair<T>(sc, i, Stage::kRow, col));
-        if (live) write_pair<T, (CH == 16)>(o, h, second);
+        h = step2(h, k[i], read_pair<T, LPR, CH == 16>(sc, i, col));
+        if (live) write_pair<T, LPR, CH == 16>(o, h, second);
       }
     } else {
 #pragma unroll
       for (int i = 0; i < S; ++i, o += p.ldh) {
         if (resets >> i & 1) h = none;
-        h = step2(h, k[i], masked2(k[i], read_pair<T>(sc, i, Stage::kRow, col)));
-        if (live && i < n) write_pair<T, (CH == 16)>(o, h, second);
+        h = step2(h, k[i], masked2(k[i], read_pair<T, LPR, CH == 16>(sc, i, col)));
+        if (live && i < n) write_pair<T, LPR, CH == 16>(o, h, second);
       }
     }
     __syncwarp();  // this stage is read: the next round copies into it
@@ -481,7 +496,7 @@ __global__ void __launch_bounds__(32 * kWarps, kPerSm) scan_fwd_kernel(const Fwd
   // the carried state is past the last step; every CTA has read h0 by now
   if (p.h_last && live && rank == 0 && warp == 0 && group == 0) {
     p.h_last[b * p.width + ch] = carry[0];
-    if (second) p.h_last[b * p.width + ch + 1] = carry[1];
+    if (second) p.h_last[b * p.width + ch + kNext] = carry[1];
   }
 }
 
@@ -528,8 +543,9 @@ __global__ void __launch_bounds__(32 * kWarps, kPerSm) scan_bwd_kernel(const Bwd
   const int col = lane % LPR, group = lane / LPR;
   const int size = static_cast<int>(cluster_size()), rank = static_cast<int>(cluster_rank());
   const int64_t tile = blockIdx.x / size;
-  const int64_t b = tile / p.tiles, ch0 = (tile - b * p.tiles) * (2 * LPR), ch = ch0 + 2 * col;
-  const bool live = ch < p.width, second = ch + 1 < p.width;
+  const int64_t b = tile / p.tiles, ch0 = (tile - b * p.tiles) * (2 * LPR), ch = ch0 + first_channel<LPR, CH == 16>(col);
+  constexpr int kNext = kApart<LPR, CH == 16>;  // to the lane's second channel
+  const bool live = ch < p.width, second = ch + kNext < p.width;
   const int64_t row0 = b * p.length;
   const T* gate = static_cast<const T*>(p.gate) + row0 * p.ldg + ch0;
   const T* cand = static_cast<const T*>(p.cand) + row0 * p.ldc + ch0;
@@ -558,11 +574,11 @@ __global__ void __launch_bounds__(32 * kWarps, kPerSm) scan_bwd_kernel(const Bwd
     const int64_t at = b * p.width + ch;
     if (p.dh_last) {
       carry[0] = p.dh_last[at];
-      if (second) carry[1] = p.dh_last[at + 1];
+      if (second) carry[1] = p.dh_last[at + kNext];
     }
     if (p.h0) {
       start[0] = p.h0[at];
-      if (second) start[1] = p.h0[at + 1];
+      if (second) start[1] = p.h0[at + kNext];
     }
   }
   if (size > 1) open_maps(maps);
@@ -588,9 +604,9 @@ __global__ void __launch_bounds__(32 * kWarps, kPerSm) scan_bwd_kernel(const Bwd
     auto fold = [&](auto slow) {
 #pragma unroll
       for (int i = S - 1; i >= 0; --i) {
-        k[i] = take2(read_pair<T>(st.a[0] + at, i, Stage::kRow, col), slope[i]);
+        k[i] = take2(read_pair<T, LPR, CH == 16>(st.a[0] + at, i, col), slope[i]);
         if (slow.value && i >= n) k[i] = none;
-        const float2 g = __fadd2_rn(read_pair<T>(st.a[2] + at, i, Stage::kRow, col), Q);
+        const float2 g = __fadd2_rn(read_pair<T, LPR, CH == 16>(st.a[2] + at, i, col), Q);
         R = join2(R, k[i]);
         Q = sub2(g, __fmul2_rn(k[i], g));
         if (slow.value && (resets >> i & 1)) {
@@ -609,18 +625,18 @@ __global__ void __launch_bounds__(32 * kWarps, kPerSm) scan_bwd_kernel(const Bwd
       T* oc = dcand + (t0 + S - 1) * p.lddc;
 #pragma unroll
       for (int i = S - 1; i >= 0; --i, og -= p.lddg, oc -= p.lddc) {
-        const float2 g = __fadd2_rn(read_pair<T>(st.a[2] + at, i, Stage::kRow, col), v);
-        float2 before = read_pair<T>(st.a[3] + at, i, Stage::kRow, col);
+        const float2 g = __fadd2_rn(read_pair<T, LPR, CH == 16>(st.a[2] + at, i, col), v);
+        float2 before = read_pair<T, LPR, CH == 16>(st.a[3] + at, i, col);
         const bool reset = slow.value && (resets >> i & 1);
         if (slow.value && t0 + i == 0) before = make_float2(start[0], start[1]);
         if (reset) before = none;
         const float2 dc = __fmul2_rn(k[i], g);
-        const float2 diff = sub2(before, read_pair<T>(st.a[1] + at, i, Stage::kRow, col));
+        const float2 diff = sub2(before, read_pair<T, LPR, CH == 16>(st.a[1] + at, i, col));
         const float2 df = masked2(slope[i], __fmul2_rn(__fmul2_rn(g, slope[i]), diff));
         v = reset ? none : sub2(g, dc);
         if (live && (!slow.value || i < n)) {
-          write_pair<T, (CH == 16)>(og, df, second);
-          write_pair<T, (CH == 16)>(oc, dc, second);
+          write_pair<T, LPR, CH == 16>(og, df, second);
+          write_pair<T, LPR, CH == 16>(oc, dc, second);
         }
       }
     };
@@ -634,7 +650,7 @@ __global__ void __launch_bounds__(32 * kWarps, kPerSm) scan_bwd_kernel(const Bwd
   if (size > 1) cluster_meet();  // nothing is on its way to a CTA that has left
   if (p.dh0 && live && rank == 0 && warp == 0 && group == 0) {
     p.dh0[b * p.width + ch] = carry[0];
-    if (second) p.dh0[b * p.width + ch + 1] = carry[1];
+    if (second) p.dh0[b * p.width + ch + kNext] = carry[1];
   }
 }
 

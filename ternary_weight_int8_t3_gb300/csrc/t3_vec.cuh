@@ -166,6 +166,7 @@ __device__ __forceinline__ float warp_max_nan(float v) {
 template <class... Params, class... Args>
 int launch(void (*fn)(Params...), int64_t grid, int threads, size_t smem, cudaStream_t s, int cluster,
            Args... args) {
+  if (grid < 1 || grid > 2147483647) return T3_EINVAL;  // more CTAs than a grid holds
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;

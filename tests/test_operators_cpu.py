@@ -93,6 +93,9 @@ def test_act_refusals(lib):
            dict(a=None), dict(wp=None), dict(c=None), dict(r=FAKE), dict(pre=FAKE)]
     for kw in bad:
         assert _act(lib, **kw) == t3.T3_EINVAL, kw
+    other = ctypes.c_void_p(8192)
+    assert _act(lib, r=other, pre=other) == t3.T3_EINVAL
+    assert _act(lib, kind=BF16, ws=FAKE) == t3.T3_EINVAL
     assert _act(lib, m=1, k=16777216) == t3.T3_EOVERFLOW
     assert _act(lib, m=0, a=None, wp=None, c=None) == t3.T3_OK
     assert _act(lib, n=0, a=None, wp=None, c=None) == t3.T3_OK
