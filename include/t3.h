@@ -378,14 +378,13 @@ enum { T3_ACT_NONE = 0, T3_ACT_RELU = 1, T3_ACT_RELU2 = 2, T3_ACT_SILU = 3, T3_A
  * [M][N] (the output's type) may each be NULL: ones, ones, zeros, zeros, not
  * written.  pre is what t3_act_bwd takes.  out_kind: T3_OUT_F32 or T3_OUT_BF16.  K = 0
  * takes x = 0.  C, residual and pre must be different buffers, and workspace
- * another one than a bf16 C (T3_EINVAL).  One
- * kernel does it all for one or two rows (and up to eight when Wp is at most 4
- * MB), and for M > 32 where A, Wp, C, residual and pre have rows of whole 16-
- * byte pieces on 16-byte boundaries, K <= 65536 and the product is not one of
- * the small ones that t3_gemm_fwd runs on the CUDA cores.  Otherwise the int32
- * product is taken first, into `workspace` (DEVICE int32 [M][N]) or, for
- * T3_OUT_F32 without one, into C; T3_OUT_BF16 returns T3_EINVAL there without
- * a workspace.  Sizes and overflow rules are those of t3_gemm_fwd_scaled.
+ * another one than a bf16 C (T3_EINVAL).  One kernel does it all for one or two
+ * rows (and up to eight when Wp is at most 4 MB), for M > 32 where A, Wp, C,
+ * residual and pre have rows of whole 16-byte pieces on 16-byte boundaries and K
+ * <= 65536, and for small products of many tiles.  Otherwise the int32 product
+ * is taken first, into `workspace` (DEVICE int32 [M][N]) or, for T3_OUT_F32
+ * without one, into C; T3_OUT_BF16 returns T3_EINVAL there without a
+ * workspace.  Sizes and overflow rules are those of t3_gemm_fwd_scaled.
  */
 int t3_gemm_fwd_act(const int8_t* A, const uint8_t* Wp, void* C, int64_t M, int64_t N, int64_t K,
                     const float* row_scale, const float* col_scale, const float* bias, int act,

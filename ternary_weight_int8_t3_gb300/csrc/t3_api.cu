@@ -661,12 +661,15 @@ int t3_gemm_fwd_act(const int8_t* A, const uint8_t* Wp, void* C, int64_t M, int6
   int st = device_info(&dev);
   if (st != T3_OK) return st;
   // the routes of t3_gemm_fwd; those that can end in this epilogue do
-  if (K > 0 && M <= kGemvM && gemv_rows(M, N, K)) {
-    st = launch_gemv_fwd_act(A, Wp, C, e, out_kind, M, N, K, dev->sms, stream);
-    if (st != T3_EINVAL) return st;
-  }
-  if (K > 0 && M > kSmallM && !small_product(M, N, K, word_rows(A, K) && word_rows(Wp, (K + 3) / 4))) {
-    st = run_tc2<kOpFwd>(A, Wp, C, M, N, K, stream, out_kind, row_scale, col_scale, &e);
+  if (K > 0) {
+    st = T3_EINVAL;
+    if (M <= kSmallM) {
+      if (gemv_rows(M, N, K)) st = launch_gemv_fwd_act(A, Wp, C, e, out_kind, M, N, K, dev->sms, stream);
+    } else if (small_product(M, N, K, word_rows(A, K) && word_rows(Wp, (K + 3) / 4))) {
+      st = launch_small_act(A, Wp, C, e, out_kind, M, N, K, dev->sms, stream);
+    } else {
+      st = run_tc2<kOpFwd>(A, Wp, C, M, N, K, stream, out_kind, row_scale, col_scale, &e);
+    }
     if (st != T3_EINVAL) return st;
   }
   int32_t* x = workspace ? workspace : (out_kind == T3_OUT_F32 ? static_cast<int32_t*>(C) : nullptr);

@@ -28,13 +28,12 @@
 // Launch: a programmatic dependent of whatever precedes it on the stream; it
 // reads A and Wp and writes C only after griddepcontrol.wait, and before the
 // wait asks its share of 16-byte aligned packed rows into L2.
-#include <cuda_bf16.h>
-
 #include <atomic>
 #include <cstdint>
 
 #include "t3.h"
 #include "t3_internal.h"
+#include "t3_out.cuh"
 
 namespace t3 {
 namespace gv {
@@ -54,46 +53,6 @@ __device__ __forceinline__ void decode16_s8(uint32_t x, uint32_t (&w)[4]) {
   w[2] = prmt(kWeightTable, 0u, od);
   w[3] = prmt(kWeightTable, 0u, od >> 16);
 }
-
-// Where a sum goes: the int32 output, or through a layer's epilogue into f32 or
-// bf16.  `ahead(m, n)` loads what the epilogue of C[m][n] needs before the sum
-// is taken, so that those loads are not on the end of the kernel.
-struct OutI32 {
-  int32_t* C;
-  struct Ahead {};
-  __device__ __forceinline__ Ahead ahead(int64_t, int64_t, int64_t) const { return {}; }
-  __device__ __forceinline__ void put(int64_t at, int32_t acc, const Ahead&) const { C[at] = acc; }
-};
-
-template <class T>
-struct OutAct {
-  T* C;
-  EpilogueArgs e;
-  struct Ahead {
-    float rs, cs, bias, res;
-  };
-  static __device__ __forceinline__ float value(const float* p) { return __ldg(p); }
-  static __device__ __forceinline__ float value(const __nv_bfloat16* p) { return __bfloat162float(*p); }
-  __device__ __forceinline__ Ahead ahead(int64_t m, int64_t n, int64_t N) const {
-    return {e.row_scale ? __ldg(e.row_scale + m) : 1.0f, e.col_scale ? __ldg(e.col_scale + n) : 1.0f,
-            e.bias ? __ldg(e.bias + n) : 0.0f,
-            e.residual ? value(static_cast<const T*>(e.residual) + m * N + n) : 0.0f};
-  }
-  static __device__ __forceinline__ void write(float* p, float y) { *p = y; }
-  static __device__ __forceinline__ void write(__nv_bfloat16* p, float y) { *p = __float2bfloat16_rn(y); }
-  __device__ __forceinline__ void put(int64_t at, int32_t acc, const Ahead& a) const {
-    float y = __fadd_rn(__fmul_rn(__fmul_rn(__int2float_rn(acc), a.rs), a.cs), a.bias);
-    if (e.pre) write(static_cast<T*>(e.pre) + at, y);
-    switch (e.act) {
-      case T3_ACT_RELU: y = vec::act<T3_ACT_RELU>(y); break;
-      case T3_ACT_RELU2: y = vec::act<T3_ACT_RELU2>(y); break;
-      case T3_ACT_SILU: y = vec::act<T3_ACT_SILU>(y); break;
-      case T3_ACT_GELU: y = vec::act<T3_ACT_GELU>(y); break;
-      default: break;
-    }
-    write(C + at, y + a.res);
-  }
-};
 
 // Each warp takes R weight rows at a time, so that one read of A's copy from
 // shared memory serves R rows.  kVec: packed rows of a multiple of 16 bytes
@@ -285,14 +244,14 @@ int launch_any(const int8_t* A, const uint8_t* Wp, const Out& out, int64_t M, in
 
 int launch_gemv_fwd(const int8_t* A, const uint8_t* Wp, int32_t* C, int64_t M, int64_t N,
                     int64_t K, int sms, cudaStream_t s) {
-  return gv::launch_any(A, Wp, gv::OutI32{C}, M, N, K, sms, s);
+  return gv::launch_any(A, Wp, OutI32{C}, M, N, K, sms, s);
 }
 
 int launch_gemv_fwd_act(const int8_t* A, const uint8_t* Wp, void* C, const EpilogueArgs& e, int kind,
                         int64_t M, int64_t N, int64_t K, int sms, cudaStream_t s) {
   if (kind == T3_OUT_BF16)
-    return gv::launch_any(A, Wp, gv::OutAct<__nv_bfloat16>{static_cast<__nv_bfloat16*>(C), e}, M, N, K, sms, s);
-  return gv::launch_any(A, Wp, gv::OutAct<float>{static_cast<float*>(C), e}, M, N, K, sms, s);
+    return gv::launch_any(A, Wp, OutAct<__nv_bfloat16>{static_cast<__nv_bfloat16*>(C), e}, M, N, K, sms, s);
+  return gv::launch_any(A, Wp, OutAct<float>{static_cast<float*>(C), e}, M, N, K, sms, s);
 }
 
 }  // namespace t3

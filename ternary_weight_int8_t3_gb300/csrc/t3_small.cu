@@ -32,6 +32,8 @@
 
 #include "t3.h"
 #include "t3_internal.h"
+#include "t3_out.cuh"
+#include "t3_vec.cuh"
 
 namespace t3 {
 namespace smp {
@@ -186,16 +188,13 @@ __device__ __forceinline__ void stage(const Params& p, int64_t row0, int64_t col
   }
 }
 
+// The sums of a tile's 4 x 4 block of this thread (rows ty + 16 i, columns
+// tx + 16 j) over chunks [c0, c1) of the reduction.
 template <int OP>
-__global__ void __launch_bounds__(kThreads) small_kernel(const Params p) {
-  __shared__ __align__(16) uint32_t xs[kTile][kPitch];
-  __shared__ __align__(16) uint32_t ys[kTile][kPitch];
-  const int t = threadIdx.x, ty = t >> 4, tx = t & 15;
-  const int64_t tile = static_cast<int64_t>(blockIdx.x) / p.split;
-  const int part = static_cast<int>(static_cast<int64_t>(blockIdx.x) % p.split);
-  const int64_t row0 = (tile / p.tiles_c) * kTile, col0 = (tile % p.tiles_c) * kTile;
-  const int64_t c0 = p.chunks * part / p.split, c1 = p.chunks * (part + 1) / p.split;
-  int32_t acc[4][4];
+__device__ __forceinline__ void tile_sums(const Params& p, int64_t row0, int64_t col0, int64_t c0, int64_t c1,
+                                          uint32_t (*xs)[kPitch], uint32_t (*ys)[kPitch], int t,
+                                          int32_t (&acc)[4][4]) {
+  const int ty = t >> 4, tx = t & 15;
 #pragma unroll
   for (int i = 0; i < 4; ++i)
 #pragma unroll
@@ -222,6 +221,19 @@ __global__ void __launch_bounds__(kThreads) small_kernel(const Params p) {
     }
     __syncthreads();
   }
+}
+
+template <int OP>
+__global__ void __launch_bounds__(kThreads) small_kernel(const Params p) {
+  __shared__ __align__(16) uint32_t xs[kTile][kPitch];
+  __shared__ __align__(16) uint32_t ys[kTile][kPitch];
+  const int t = threadIdx.x, ty = t >> 4, tx = t & 15;
+  const int64_t tile = static_cast<int64_t>(blockIdx.x) / p.split;
+  const int part = static_cast<int>(static_cast<int64_t>(blockIdx.x) % p.split);
+  const int64_t row0 = (tile / p.tiles_c) * kTile, col0 = (tile % p.tiles_c) * kTile;
+  const int64_t c0 = p.chunks * part / p.split, c1 = p.chunks * (part + 1) / p.split;
+  int32_t acc[4][4];
+  tile_sums<OP>(p, row0, col0, c0, c1, xs, ys, t, acc);
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const int64_t r = row0 + ty + 16 * i;
@@ -236,6 +248,31 @@ __global__ void __launch_bounds__(kThreads) small_kernel(const Params p) {
       else
         *dst = acc[i][j];
     }
+  }
+}
+
+// The forward with a layer's epilogue: one CTA takes a tile's whole reduction.
+template <class Out>
+__global__ void __launch_bounds__(kThreads) small_act_kernel(const Params p, const Out out) {
+  __shared__ __align__(16) uint32_t xs[kTile][kPitch];
+  __shared__ __align__(16) uint32_t ys[kTile][kPitch];
+  const int t = threadIdx.x, ty = t >> 4, tx = t & 15;
+  const int64_t row0 = (blockIdx.x / p.tiles_c) * kTile, col0 = (blockIdx.x % p.tiles_c) * kTile;
+  launch_dependents();
+  grid_dependency_wait();
+  int32_t acc[4][4];
+  tile_sums<kFwd>(p, row0, col0, 0, p.chunks, xs, ys, t, acc);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int64_t r = row0 + ty + 16 * i;
+    if (r >= p.rows) continue;
+    typename Out::Ahead a[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      if (col0 + tx + 16 * j < p.cols) a[j] = out.ahead(r, col0 + tx + 16 * j, p.cols);
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      if (col0 + tx + 16 * j < p.cols) out.put(r * p.cols + col0 + tx + 16 * j, acc[i][j], a[j]);
   }
 }
 
@@ -288,6 +325,35 @@ int launch_small(int op, const int8_t* x, const int8_t* y, const uint8_t* wp, in
   else
     smp::small_kernel<smp::kDw><<<grid, smp::kThreads, 0, s>>>(p);
   return cudaGetLastError() == cudaSuccess ? T3_OK : T3_ECUDA;
+}
+
+// With two tiles an SM one CTA takes a tile's whole sum and the epilogue with it
+// (1782 x 729 x 243: 17.1 us, against 21.7 split in two and with the epilogue behind).  Fewer
+// tiles are split over CTAs, which needs the int32 output in between (200 x 500
+// x 500: 8.2 us, against 16.9 unsplit).
+int launch_small_act(const int8_t* A, const uint8_t* Wp, void* C, const EpilogueArgs& e, int kind, int64_t M,
+                     int64_t N, int64_t K, int sms, cudaStream_t s) {
+  smp::Params p{};
+  p.x = A;
+  p.wp = Wp;
+  p.M = M;
+  p.N = N;
+  p.K = K;
+  p.KB = (K + 3) / 4;
+  p.rows = M;
+  p.cols = N;
+  p.red = K;
+  p.tiles_c = (N + smp::kTile - 1) / smp::kTile;
+  p.chunks = (K + smp::kChunk - 1) / smp::kChunk;
+  p.split = 1;
+  p.x_vec = (K % 16 == 0) && (reinterpret_cast<uintptr_t>(A) % 16 == 0);
+  const int64_t grid = (M + smp::kTile - 1) / smp::kTile * p.tiles_c;
+  if (grid < 2 * static_cast<int64_t>(sms)) return T3_EINVAL;
+  if (kind == T3_OUT_BF16)
+    return vec::launch(smp::small_act_kernel<OutAct<__nv_bfloat16>>, grid, smp::kThreads, 0, s, 1, p,
+                       OutAct<__nv_bfloat16>{static_cast<__nv_bfloat16*>(C), e});
+  return vec::launch(smp::small_act_kernel<OutAct<float>>, grid, smp::kThreads, 0, s, 1, p,
+                     OutAct<float>{static_cast<float*>(C), e});
 }
 
 }  // namespace t3
