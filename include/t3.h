@@ -384,12 +384,19 @@ enum { T3_ACT_NONE = 0, T3_ACT_RELU = 1, T3_ACT_RELU2 = 2, T3_ACT_SILU = 3, T3_A
  * <= 65536, and for small products of many tiles.  Otherwise the int32 product
  * is taken first, into `workspace` (DEVICE int32 [M][N]) or, for T3_OUT_F32
  * without one, into C; T3_OUT_BF16 returns T3_EINVAL there without a
- * workspace.  Sizes and overflow rules are those of t3_gemm_fwd_scaled.
+ * workspace.  scratch (DEVICE, 16-byte aligned, may be NULL) of at least
+ * t3_gemm_fwd_act_scratch(M, N, K) bytes makes products with M > 32 and odd
+ * rows several times faster: they are laid out aligned there first.
+ * Sizes and overflow rules are those of t3_gemm_fwd_scaled.
  */
 int t3_gemm_fwd_act(const int8_t* A, const uint8_t* Wp, void* C, int64_t M, int64_t N, int64_t K,
                     const float* row_scale, const float* col_scale, const float* bias, int act,
-                    const void* residual, void* pre, int out_kind, int32_t* workspace,
-                    t3_stream_t stream);
+                    const void* residual, void* pre, int out_kind, int32_t* workspace, void* scratch,
+                    int64_t scratch_bytes, t3_stream_t stream);
+
+/* Bytes of scratch that t3_gemm_fwd_act can use for a product of these sizes: 0
+ * where its rows are whole 16-byte pieces anyway. */
+int64_t t3_gemm_fwd_act_scratch(int64_t M, int64_t N, int64_t K);
 
 /*
  * t3_act_bwd -- the gradient of that epilogue: for dy, the gradient of C, and

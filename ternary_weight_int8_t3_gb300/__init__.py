@@ -102,11 +102,13 @@ def load():
                 ("t3_gated_scan_fwd", [p, i64, p, i64, p, p, p, i64, p, i64, i64, i64, i32, p]),
                 ("t3_gated_scan_bwd", [p, i64, p, i64, p, i64, p, i64, p, p, p, p, i64, p, i64, p,
                                        i64, i64, i64, i32, p]),
-                ("t3_gemm_fwd_act", [p, p, p, i64, i64, i64, p, p, p, i32, p, p, i32, p, p]),
+                ("t3_gemm_fwd_act", [p, p, p, i64, i64, i64, p, p, p, i32, p, p, i32, p, p, i64, p]),
                 ("t3_act_bwd", [p, p, i32, p, p, i64, i64, i32, p, p])):
             f = getattr(lib, name)
             f.argtypes = types
             f.restype = ctypes.c_int
+        lib.t3_gemm_fwd_act_scratch.argtypes = [i64, i64, i64]
+        lib.t3_gemm_fwd_act_scratch.restype = i64
         lib.t3_colsum_workspace.argtypes = [i64, i64]
         lib.t3_colsum_workspace.restype = i64
         lib.t3_version.argtypes = []
@@ -522,8 +524,16 @@ def _empty(shape, dtype, dev, stream):
         return torch.empty(shape, dtype=dtype, device=dev)
 
 
+_col_parts = None
+
+
 def _workspace(workspace, rows, cols, dev, stream):
-    n = load().t3_colsum_workspace(rows, cols)
+    """The column sums' partial rows: t3_colsum_workspace(rows, cols) floats, at
+    most a fixed number of rows."""
+    global _col_parts
+    if _col_parts is None:
+        _col_parts = load().t3_colsum_workspace((1 << 31) - 1, 1)
+    n = min(rows, _col_parts) * cols
     torch = _torch()
     if workspace is None:
         return _empty(n, torch.float32, dev, stream)
@@ -645,12 +655,17 @@ def t3_gated_scan_bwd(gate, cand, h, dh, h0=None, resets=None, dh_last=None, dga
     return dgate, dcand, dh0
 
 
+# Products up to the library's default limit run on the CUDA cores as they lie.
+_SMALL_MACS = 1 << 26
+
+
 def t3_gemm_fwd_act(A, Wp, K=None, row_scale=None, col_scale=None, bias=None, act=T3_ACT_NONE,
-                    residual=None, kind=T3_OUT_F32, C=None, pre=None, workspace=None, stream=None):
+                    residual=None, kind=T3_OUT_F32, C=None, pre=None, workspace=None, scratch=None, stream=None):
     """C = act(z) + residual with z = A . W scaled per row and column plus
     bias; `pre`, when given, receives z for t3_act_bwd.  kind: T3_OUT_F32 or
     T3_OUT_BF16, the type of C, residual and pre [M][N].  workspace: int32
-    [M][N], allocated when the call may need one and none is given."""
+    [M][N], and scratch: uint8 of t3_gemm_fwd_act_scratch(M, N, K), are allocated
+    when the call may need them and none is given."""
     torch = _torch()
     if not isinstance(A, torch.Tensor) or not A.is_cuda or A.dim() != 2 or Wp.dim() != 2:
         raise TypeError("A and Wp must be 2-D CUDA tensors")
@@ -667,11 +682,21 @@ def t3_gemm_fwd_act(A, Wp, K=None, row_scale=None, col_scale=None, bias=None, ac
         C = _empty(shape, dtype, dev, stream)
     if workspace is None and kind == T3_OUT_BF16:
         workspace = _empty(shape, torch.int32, dev, stream)
+    room = 0
+    if scratch is not None:
+        room = scratch.numel()
+        ps = _dense(scratch, torch.uint8, dev, (room,), "scratch")
+    elif M > 32 and (K % 64 or N % 8) and M * N * K > _SMALL_MACS:
+        room = load().t3_gemm_fwd_act_scratch(M, N, K)
+        scratch = _empty(room, torch.uint8, dev, stream)
+        ps = scratch.data_ptr()
+    else:
+        ps = None
     _launch("t3_gemm_fwd_act", dev, stream, _dense(A, torch.int8, dev, (M, K), "A"),
             _dense(Wp, torch.uint8, dev, (N, KB), "Wp"), _dense(C, dtype, dev, shape, "C"), M, N, K,
             _dense(row_scale, f32, dev, (M,), "row_scale"), _dense(col_scale, f32, dev, (N,), "col_scale"),
             _dense(bias, f32, dev, (N,), "bias"), act, _dense(residual, dtype, dev, shape, "residual"),
-            _dense(pre, dtype, dev, shape, "pre"), kind, _dense(workspace, torch.int32, dev, shape, "workspace"))
+            _dense(pre, dtype, dev, shape, "pre"), kind, _dense(workspace, torch.int32, dev, shape, "workspace"), ps, room)
     return C
 
 

@@ -394,6 +394,24 @@ bool bad_dims(int64_t M, int64_t N, int64_t K) {
   return M < 0 || N < 0 || K < 0 || M > kMaxDim || N > kMaxDim || K > kMaxDim;
 }
 
+// Where t3_gemm_fwd_act lays out operands whose rows are not 16-byte pieces:
+// A [M][K'] and Wp [N'][K' / 4] with K' = K rounded up to 64 and N' = N to 4, and an
+// int32 result [M][N'].
+struct AlignedLayout {
+  int64_t K, N;              // the padded sizes
+  int64_t a, w, x, bytes;    // byte offsets, and all of it
+};
+AlignedLayout aligned_layout(int64_t M, int64_t N, int64_t K) {
+  AlignedLayout l;
+  l.K = ceil_div(K, 64) * 64;
+  l.N = ceil_div(N, 4) * 4;
+  l.a = 0;
+  l.w = M * l.K;
+  l.x = l.w + l.N * (l.K / 4);
+  l.bytes = l.x + M * l.N * 4;
+  return l;
+}
+
 // Activations' element types are the output kinds that store them.
 bool valid_dtype(int dtype) { return dtype == T3_OUT_F32 || dtype == T3_OUT_BF16; }
 bool valid_act(int act) { return act >= T3_ACT_NONE && act <= T3_ACT_GELU; }
@@ -646,11 +664,16 @@ int t3_gated_scan_bwd(const void* gate, int64_t ldg, const void* cand, int64_t l
                          dh0, batch, length, width, dtype, dev->err_word, stream);
 }
 
+int64_t t3_gemm_fwd_act_scratch(int64_t M, int64_t N, int64_t K) {
+  if (bad_dims(M, N, K) || M <= kSmallM || N == 0 || K == 0 || (K % 64 == 0 && N % 8 == 0)) return 0;
+  return aligned_layout(M, N, K).bytes;
+}
+
 int t3_gemm_fwd_act(const int8_t* A, const uint8_t* Wp, void* C, int64_t M, int64_t N, int64_t K,
                     const float* row_scale, const float* col_scale, const float* bias, int act,
-                    const void* residual, void* pre, int out_kind, int32_t* workspace,
-                    t3_stream_t stream) {
-  if (bad_dims(M, N, K) || !valid_dtype(out_kind) || !valid_act(act)) return T3_EINVAL;
+                    const void* residual, void* pre, int out_kind, int32_t* workspace, void* scratch,
+                    int64_t scratch_bytes, t3_stream_t stream) {
+  if (bad_dims(M, N, K) || !valid_dtype(out_kind) || !valid_act(act) || scratch_bytes < 0) return T3_EINVAL;
   if (M == 0 || N == 0) return T3_OK;
   if (!C || (K > 0 && (!A || !Wp)) || C == residual || C == pre || (pre && pre == residual) ||
       (out_kind == T3_OUT_BF16 && workspace == C))
@@ -662,13 +685,35 @@ int t3_gemm_fwd_act(const int8_t* A, const uint8_t* Wp, void* C, int64_t M, int6
   if (st != T3_OK) return st;
   // the routes of t3_gemm_fwd; those that can end in this epilogue do
   if (K > 0) {
+    const int64_t KB = (K + 3) / 4;
+    const bool words = word_rows(A, K) && word_rows(Wp, KB);
+    const bool tma = K % 64 == 0 && reinterpret_cast<uintptr_t>(A) % 16 == 0 && reinterpret_cast<uintptr_t>(Wp) % 16 == 0;
+    const AlignedLayout lay = aligned_layout(M, N, K);
+    const bool room = scratch && scratch_bytes >= lay.bytes && reinterpret_cast<uintptr_t>(scratch) % 16 == 0;
     st = T3_EINVAL;
     if (M <= kSmallM) {
       if (gemv_rows(M, N, K)) st = launch_gemv_fwd_act(A, Wp, C, e, out_kind, M, N, K, dev->sms, stream);
-    } else if (small_product(M, N, K, word_rows(A, K) && word_rows(Wp, (K + 3) / 4))) {
+    } else if (small_product(M, N, K, words || room)) {
       st = launch_small_act(A, Wp, C, e, out_kind, M, N, K, dev->sms, stream);
     } else {
-      st = run_tc2<kOpFwd>(A, Wp, C, M, N, K, stream, out_kind, row_scale, col_scale, &e);
+      if (tma) st = run_tc2<kOpFwd>(A, Wp, C, M, N, K, stream, out_kind, row_scale, col_scale, &e);
+      if (st == T3_EINVAL && room) {
+        // rows that TMA cannot address cost the pipelines several times as much as
+        // laying them out once: operands padded with zeros to whole 64-element
+        // groups, and an int32 result of whole 16-byte rows where C, residual or pre are not
+        uint8_t* base = static_cast<uint8_t*>(scratch);
+        const int8_t* A2 = tma ? A : reinterpret_cast<int8_t*>(base + lay.a);
+        uint8_t* W2 = base + lay.w;
+        st = launch_align_rows(tma ? nullptr : reinterpret_cast<const uint8_t*>(A), M, K, base + lay.a, M, lay.K, Wp, N,
+                               KB, W2, lay.N, lay.K / 4, stream);
+        if (st != T3_OK) return st;
+        st = tma ? T3_EINVAL : run_tc2<kOpFwd>(A2, W2, C, M, N, lay.K, stream, out_kind, row_scale, col_scale, &e);
+        if (st == T3_EINVAL) {
+          int32_t* x = reinterpret_cast<int32_t*>(base + lay.x);
+          st = run_tc2<kOpFwd>(A2, W2, x, M, lay.N, lay.K, stream);
+          if (st == T3_OK) st = launch_epilogue(x, lay.N, C, e, M, N, out_kind, dev->sms, stream);
+        }
+      }
     }
     if (st != T3_EINVAL) return st;
   }
@@ -676,7 +721,7 @@ int t3_gemm_fwd_act(const int8_t* A, const uint8_t* Wp, void* C, int64_t M, int6
   if (!x) return T3_EINVAL;
   st = t3_gemm_fwd(A, Wp, x, M, N, K, stream);
   if (st != T3_OK) return st;
-  return launch_epilogue(x, C, e, M, N, out_kind, dev->sms, stream);
+  return launch_epilogue(x, N, C, e, M, N, out_kind, dev->sms, stream);
 }
 
 int t3_act_bwd(const void* dy, const void* z, int act, void* dz, float* dbias, int64_t rows,

@@ -25,52 +25,107 @@ using namespace vec;
 
 struct Args {
   const int32_t* x;
+  int64_t ldx;
   void* out;
   EpilogueArgs e;
-  int64_t rows, cols;
+  int64_t rows, cols, tiles;
 };
 
+// A thread holds VEC columns (their scales and biases in registers) and takes
+// every gridDim / tiles-th row.
 template <class T, int VEC, int ACT>
 __global__ void __launch_bounds__(256) epilogue_kernel(const Args p) {
-  const int64_t units = (p.cols + VEC - 1) / VEC, total = p.rows * units;
+  const int64_t c = (static_cast<int64_t>(blockIdx.x % p.tiles) * 256 + threadIdx.x) * VEC;
+  const int64_t step = gridDim.x / p.tiles;
   launch_dependents();
   grid_dependency_wait();
-  for (int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; i < total;
-       i += static_cast<int64_t>(gridDim.x) * blockDim.x) {
-    const int64_t r = i / units, c = (i - r * units) * VEC, at = r * p.cols + c;
+  if (c >= p.cols) return;
+  float cs[VEC], bias[VEC];
+#pragma unroll
+  for (int j = 0; j < VEC; ++j) {
+    cs[j] = 1.0f;
+    bias[j] = 0.0f;
+  }
+  if (p.e.col_scale) load_floats<VEC>(p.e.col_scale + c, cs);
+  if (p.e.bias) load_floats<VEC>(p.e.bias + c, bias);
+#pragma unroll 2
+  for (int64_t r = blockIdx.x / p.tiles; r < p.rows; r += step) {
+    const int64_t at = r * p.cols + c;
     const float rs = p.e.row_scale ? __ldg(p.e.row_scale + r) : 1.0f;
-    float y[VEC], t[VEC];
+    float y[VEC], t[VEC] = {};
     if constexpr (VEC == 4) {
-      const int4 v = *reinterpret_cast<const int4*>(p.x + at);
+      const int4 v = *reinterpret_cast<const int4*>(p.x + r * p.ldx + c);
       y[0] = __int2float_rn(v.x);
       y[1] = __int2float_rn(v.y);
       y[2] = __int2float_rn(v.z);
       y[3] = __int2float_rn(v.w);
     } else {
-      y[0] = __int2float_rn(p.x[at]);
+      y[0] = __int2float_rn(p.x[r * p.ldx + c]);
     }
+    if (p.e.residual) to_float(load<T, VEC>(static_cast<const T*>(p.e.residual) + at), t);
 #pragma unroll
-    for (int j = 0; j < VEC; ++j) y[j] = __fmul_rn(y[j], rs);
-    if (p.e.col_scale) {
-      load_floats<VEC>(p.e.col_scale + c, t);
-#pragma unroll
-      for (int j = 0; j < VEC; ++j) y[j] = __fmul_rn(y[j], t[j]);
-    }
-    if (p.e.bias) {
-      load_floats<VEC>(p.e.bias + c, t);
-#pragma unroll
-      for (int j = 0; j < VEC; ++j) y[j] = __fadd_rn(y[j], t[j]);
-    }
+    for (int j = 0; j < VEC; ++j) y[j] = __fadd_rn(__fmul_rn(__fmul_rn(y[j], rs), cs[j]), bias[j]);
     if (p.e.pre) store<T, VEC>(static_cast<T*>(p.e.pre) + at, from_float(y, T()));
 #pragma unroll
-    for (int j = 0; j < VEC; ++j) y[j] = act<ACT>(y[j]);
-    if (p.e.residual) {
-      to_float(load<T, VEC>(static_cast<const T*>(p.e.residual) + at), t);
-#pragma unroll
-      for (int j = 0; j < VEC; ++j) y[j] += t[j];
-    }
+    for (int j = 0; j < VEC; ++j) y[j] = __fadd_rn(act<ACT>(y[j]), t[j]);
     store<T, VEC>(static_cast<T*>(p.out) + at, from_float(y, T()));
   }
+}
+
+// Rows of `len` bytes, one after the other at any alignment, to rows of `pitch`
+// bytes (a multiple of 16), zeros behind each and in rows from `rows` to `rows2`.
+struct AlignArgs {
+  const uint8_t* src;
+  int64_t rows, len;
+  uint8_t* dst;
+  int64_t rows2, pitch;
+};
+
+// Bytes [at, at + 16) of the array [0, end): whole words where they lie inside.
+__device__ __forceinline__ uint4 gather16(const uint8_t* src, int64_t at, int64_t end) {
+  const uint64_t a = reinterpret_cast<uint64_t>(src) + at;
+  const int sh = static_cast<int>(a & 3) * 8;
+  const int64_t w = at - (sh >> 3);  // the aligned word's offset
+  uint32_t x[5];
+  if (w >= 0 && w + 20 <= end) {
+    const uint32_t* p = reinterpret_cast<const uint32_t*>(a & ~3ull);
+#pragma unroll
+    for (int i = 0; i < 5; ++i) x[i] = __ldg(p + i);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 5; ++i) {
+      x[i] = 0;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int64_t o = w + 4 * i + j;
+        if (o >= 0 && o < end) x[i] |= static_cast<uint32_t>(__ldg(src + o)) << (8 * j);
+      }
+    }
+  }
+  return make_uint4(__funnelshift_r(x[0], x[1], sh), __funnelshift_r(x[1], x[2], sh),
+                    __funnelshift_r(x[2], x[3], sh), __funnelshift_r(x[3], x[4], sh));
+}
+
+__global__ void __launch_bounds__(256) align_rows_kernel(const AlignArgs a, const AlignArgs b, int64_t blocks_a) {
+  const bool first = blockIdx.x < blocks_a;
+  const AlignArgs& p = first ? a : b;
+  launch_dependents();
+  grid_dependency_wait();
+  const int64_t i = (blockIdx.x - (first ? 0 : blocks_a)) * 256 + threadIdx.x;
+  const int64_t each = p.pitch / 16, r = i / each, c = (i - r * each) * 16;
+  if (r >= p.rows2) return;
+  uint4 v = make_uint4(0u, 0u, 0u, 0u);
+  if (r < p.rows && c < p.len) {
+    v = gather16(p.src, r * p.len + c, p.rows * p.len);
+    const int64_t left = p.len - c;  // bytes of this row
+    if (left < 16) {
+      uint32_t* w = reinterpret_cast<uint32_t*>(&v);
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        w[j] = left >= 4 * j + 4 ? w[j] : left <= 4 * j ? 0u : w[j] & (0xFFFFFFFFu >> (8 * (4 * j + 4 - left)));
+    }
+  }
+  *reinterpret_cast<uint4*>(p.dst + r * p.pitch + c) = v;
 }
 
 struct BwdArgs {
@@ -158,10 +213,12 @@ __global__ void __launch_bounds__(1024) col_finish_kernel(const float* partial, 
 }
 
 template <class T, int VEC>
-int epilogue_act(const Args& p, int sms, cudaStream_t s) {
-  const int64_t total = p.rows * ((p.cols + VEC - 1) / VEC);
-  int64_t grid = (total + 255) / 256;
-  if (grid > 16ll * sms) grid = 16ll * sms;
+int epilogue_act(Args p, int sms, cudaStream_t s) {
+  p.tiles = (p.cols + 256 * VEC - 1) / (256 * VEC);
+  // about eight CTAs an SM
+  int64_t groups = 8ll * sms / p.tiles > 1 ? 8ll * sms / p.tiles : 1;
+  if (groups > p.rows) groups = p.rows;
+  const int64_t grid = p.tiles * groups;
   switch (p.e.act) {
     case T3_ACT_RELU: return launch(epilogue_kernel<T, VEC, T3_ACT_RELU>, grid, 256, 0, s, 1, p);
     case T3_ACT_RELU2: return launch(epilogue_kernel<T, VEC, T3_ACT_RELU2>, grid, 256, 0, s, 1, p);
@@ -171,8 +228,9 @@ int epilogue_act(const Args& p, int sms, cudaStream_t s) {
   }
 }
 
+// One part writes the column sums themselves.
 template <class T, int VEC>
-int act_bwd_act(BwdArgs p, int act, int sms, int* parts, cudaStream_t s) {
+int act_bwd_act(BwdArgs p, int act, float* dbias, int sms, int* parts, cudaStream_t s) {
   const int64_t tiles = (p.cols + 32 * VEC - 1) / (32 * VEC);
   // at most four CTAs an SM (one wave: a few CTAs more would double the time),
   // each with at least one round of rows a warp
@@ -181,6 +239,7 @@ int act_bwd_act(BwdArgs p, int act, int sms, int* parts, cudaStream_t s) {
   if (n > most) n = most;
   if (n > kMaxColParts) n = kMaxColParts;
   p.parts = *parts = static_cast<int>(n);
+  if (n == 1 && dbias) p.partial = dbias;
   const int64_t grid = tiles * n;
   switch (act) {
     case T3_ACT_RELU: return launch(act_bwd_kernel<T, VEC, T3_ACT_RELU>, grid, 256, 0, s, 1, p);
@@ -193,11 +252,20 @@ int act_bwd_act(BwdArgs p, int act, int sms, int* parts, cudaStream_t s) {
 
 }  // namespace ep
 
-int launch_epilogue(const int32_t* x, void* out, const EpilogueArgs& e, int64_t rows, int64_t cols,
+int launch_align_rows(const uint8_t* a, int64_t rows_a, int64_t len_a, uint8_t* a2, int64_t rows_a2, int64_t pitch_a,
+                      const uint8_t* b, int64_t rows_b, int64_t len_b, uint8_t* b2, int64_t rows_b2, int64_t pitch_b,
+                      cudaStream_t s) {
+  const ep::AlignArgs x{a, rows_a, len_a, a2, a ? rows_a2 : 0, pitch_a}, y{b, rows_b, len_b, b2, rows_b2, pitch_b};
+  const int64_t blocks_a = a ? (rows_a2 * (pitch_a / 16) + 255) / 256 : 0;
+  const int64_t blocks_b = (rows_b2 * (pitch_b / 16) + 255) / 256;
+  return vec::launch(ep::align_rows_kernel, blocks_a + blocks_b, 256, 0, s, 1, x, y, blocks_a);
+}
+
+int launch_epilogue(const int32_t* x, int64_t ldx, void* out, const EpilogueArgs& e, int64_t rows, int64_t cols,
                     int kind, int sms, cudaStream_t s) {
-  const ep::Args p{x, out, e, rows, cols};
+  const ep::Args p{x, ldx, out, e, rows, cols, 0};
   const int64_t es = kind == T3_OUT_BF16 ? 8 : 16;
-  const bool vec4 = cols % 4 == 0 && vec::aligned(x, 16) && vec::aligned(out, es) &&
+  const bool vec4 = cols % 4 == 0 && ldx % 4 == 0 && vec::aligned(x, 16) && vec::aligned(out, es) &&
                     vec::aligned(e.pre, es) && vec::aligned(e.residual, es) &&
                     vec::aligned(e.col_scale, 16) && vec::aligned(e.bias, 16);
   if (kind == T3_OUT_BF16)
@@ -216,12 +284,12 @@ int launch_act_bwd(const void* dy, const void* z, int act, void* dz, float* dbia
   const bool vec = cols % v == 0 && vec::aligned(dy, 16) && vec::aligned(z, 16) && vec::aligned(dz, 16);
   int parts = 0, st;
   if (dtype == T3_OUT_BF16)
-    st = vec ? ep::act_bwd_act<vec::bf16, 8>(p, act, sms, &parts, s)
-             : ep::act_bwd_act<vec::bf16, 1>(p, act, sms, &parts, s);
+    st = vec ? ep::act_bwd_act<vec::bf16, 8>(p, act, dbias, sms, &parts, s)
+             : ep::act_bwd_act<vec::bf16, 1>(p, act, dbias, sms, &parts, s);
   else
-    st = vec ? ep::act_bwd_act<float, 4>(p, act, sms, &parts, s)
-             : ep::act_bwd_act<float, 1>(p, act, sms, &parts, s);
-  if (st != T3_OK || !dbias) return st;
+    st = vec ? ep::act_bwd_act<float, 4>(p, act, dbias, sms, &parts, s)
+             : ep::act_bwd_act<float, 1>(p, act, dbias, sms, &parts, s);
+  if (st != T3_OK || !dbias || parts == 1) return st;
   return launch_col_finish(workspace, parts, cols, dbias, s);
 }
 

@@ -120,10 +120,17 @@ int launch_scan_bwd(const void* gate, int64_t ldg, const void* cand, int64_t ldc
                     float* dh0, int64_t batch, int64_t length, int64_t width, int dtype, int* err,
                     cudaStream_t s);
 
-// What follows a product (EpilogueArgs) on its int32 result (t3_epilogue.cu);
-// x may be out's buffer for T3_OUT_F32.
-int launch_epilogue(const int32_t* x, void* out, const EpilogueArgs& e, int64_t rows, int64_t cols,
+// What follows a product (EpilogueArgs) on its int32 result x with row stride
+// ldx (t3_epilogue.cu); x may be out's buffer for T3_OUT_F32 (ldx = cols).
+int launch_epilogue(const int32_t* x, int64_t ldx, void* out, const EpilogueArgs& e, int64_t rows, int64_t cols,
                     int kind, int sms, cudaStream_t s);
+
+// Lays byte rows out 16-byte aligned: rows of len bytes (dense) to rows of pitch
+// bytes (a multiple of 16, so is the destination), zeros behind each row and in
+// rows rows .. rows2.  Two arrays in one launch; a may be null.
+int launch_align_rows(const uint8_t* a, int64_t rows_a, int64_t len_a, uint8_t* a2, int64_t rows_a2, int64_t pitch_a,
+                      const uint8_t* b, int64_t rows_b, int64_t len_b, uint8_t* b2, int64_t rows_b2, int64_t pitch_b,
+                      cudaStream_t s);
 
 // dz = dy act'(z) and its column sums.
 int launch_act_bwd(const void* dy, const void* z, int act, void* dz, float* dbias, int64_t rows,

@@ -469,7 +469,7 @@ int fwd_vec(const FwdArgs& p, int sms, cudaStream_t s) {
 // Backward: many rows take 8 elements a thread (more only where the row would not
 // fit a CTA).
 template <class T, int VEC, int MAXNV>
-int bwd_vec(BwdArgs p, int sms, int* parts, cudaStream_t s) {
+int bwd_vec(BwdArgs p, float* dgamma, int sms, int* parts, cudaStream_t s) {
   const bool many = p.rows >= 2 * static_cast<int64_t>(sms);
   int threads = 0;
   const int nv = pick<VEC, MAXNV>((p.cols + VEC - 1) / VEC, many ? 8 : 1, bwd_threads, &threads);
@@ -486,6 +486,7 @@ int bwd_vec(BwdArgs p, int sms, int* parts, cudaStream_t s) {
     if (grid > need) grid = need;
     if (grid > kMaxColParts) grid = kMaxColParts;
     *parts = static_cast<int>(grid);
+    if (grid == 1 && p.partial) p.partial = dgamma;  // one part is the sum itself
     if (!one)
       return launch(norm_bwd_kernel<T, VEC, 8 / VEC, false>, grid, threads * p.groups,
                     static_cast<size_t>(p.cols) * sizeof(float), s, 1, p);
@@ -497,6 +498,7 @@ int bwd_vec(BwdArgs p, int sms, int* parts, cudaStream_t s) {
     const int64_t tiles = (p.cols + 31) / 32;
     const int64_t n = (p.rows + 7) / 8 < 16 ? (p.rows + 7) / 8 : 16;
     *parts = static_cast<int>(n);
+    if (n == 1) p.partial = dgamma;
     const int st = launch(norm_dgamma_kernel<T>, tiles * n, 256, 0, s, 1, p, *parts);
     if (st != T3_OK) return st;
   }
@@ -535,12 +537,12 @@ int launch_norm_bwd(const void* dy, int64_t lddy, const void* x, int64_t lds, co
                    (!gamma || vec::aligned(gamma, 16));
   int parts = 0, st;
   if (dtype == T3_OUT_BF16)
-    st = vec ? nm::bwd_vec<vec::bf16, 8, 4>(p, sms, &parts, s)
-             : nm::bwd_vec<vec::bf16, 1, 32>(p, sms, &parts, s);
+    st = vec ? nm::bwd_vec<vec::bf16, 8, 4>(p, dgamma, sms, &parts, s)
+             : nm::bwd_vec<vec::bf16, 1, 32>(p, dgamma, sms, &parts, s);
   else
-    st = vec ? nm::bwd_vec<float, 4, 4>(p, sms, &parts, s)
-             : nm::bwd_vec<float, 1, 32>(p, sms, &parts, s);
-  if (st != T3_OK || !dgamma) return st;
+    st = vec ? nm::bwd_vec<float, 4, 4>(p, dgamma, sms, &parts, s)
+             : nm::bwd_vec<float, 1, 32>(p, dgamma, sms, &parts, s);
+  if (st != T3_OK || !dgamma || parts == 1) return st;
   return launch_col_finish(workspace, parts, cols, dgamma, s);
 }
 

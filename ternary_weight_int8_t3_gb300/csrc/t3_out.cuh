@@ -46,7 +46,7 @@ struct OutAct {
       case T3_ACT_GELU: y = vec::act<T3_ACT_GELU>(y); break;
       default: break;
     }
-    write(C + at, y + a.res);
+    write(C + at, __fadd_rn(y, a.res));  // the same bits on every route
   }
 };
 

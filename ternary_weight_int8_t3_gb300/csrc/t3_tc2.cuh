@@ -268,6 +268,8 @@ __device__ __forceinline__ uint8_t* act_piece(uint8_t* slot, int lane, int g, bo
   return slot + (bf16 ? lane * 64 + ((g ^ (lane >> 1)) & 3) * 16 : tc::sw128(lane, g));
 }
 
+// Additions of their own (no multiply-add with the activation's last product),
+// so that every route gives the same bits.
 __device__ __forceinline__ void add_slot(float (&y)[32], uint8_t* slot, int lane, bool bf16) {
   if (bf16) {
 #pragma unroll
@@ -276,18 +278,18 @@ __device__ __forceinline__ void add_slot(float (&y)[32], uint8_t* slot, int lane
       const uint32_t w[4] = {r.x, r.y, r.z, r.w};
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        y[8 * g + 2 * j] += __uint_as_float(w[j] << 16);
-        y[8 * g + 2 * j + 1] += __uint_as_float(w[j] & 0xFFFF0000u);
+        y[8 * g + 2 * j] = __fadd_rn(y[8 * g + 2 * j], __uint_as_float(w[j] << 16));
+        y[8 * g + 2 * j + 1] = __fadd_rn(y[8 * g + 2 * j + 1], __uint_as_float(w[j] & 0xFFFF0000u));
       }
     }
   } else {
 #pragma unroll
     for (int g = 0; g < 8; ++g) {
       const float4 r = *reinterpret_cast<const float4*>(act_piece(slot, lane, g, false));
-      y[4 * g] += r.x;
-      y[4 * g + 1] += r.y;
-      y[4 * g + 2] += r.z;
-      y[4 * g + 3] += r.w;
+      y[4 * g] = __fadd_rn(y[4 * g], r.x);
+      y[4 * g + 1] = __fadd_rn(y[4 * g + 1], r.y);
+      y[4 * g + 2] = __fadd_rn(y[4 * g + 2], r.z);
+      y[4 * g + 3] = __fadd_rn(y[4 * g + 3], r.w);
     }
   }
 }

@@ -187,7 +187,7 @@ def test_without_workspace():
     wp = torch.zeros((273, 64), dtype=torch.uint8, device="cuda")
     c = torch.zeros((300, 273), dtype=torch.bfloat16, device="cuda")
     args = [a.data_ptr(), wp.data_ptr(), c.data_ptr(), 300, 273, 256, None, None, None, 0, None, None]
-    assert f(*args, t3.T3_OUT_BF16, None, None) == t3.T3_EINVAL  # odd output rows
+    assert f(*args, t3.T3_OUT_BF16, None, None, 0, None) == t3.T3_EINVAL  # odd output rows
     with pytest.raises(ValueError):
         t3.t3_gemm_fwd_act(a, wp, kind=t3.T3_OUT_F32_ADD)
     with pytest.raises(ValueError):
@@ -196,6 +196,33 @@ def test_without_workspace():
         t3.t3_gemm_fwd_act(a, wp, act=9)
     with pytest.raises(t3.T3Error):
         t3.t3_gemm_fwd_act(a, wp, C=c, residual=c, kind=t3.T3_OUT_BF16)
+
+
+@pytest.mark.parametrize("dname", ["bf16", "f32"])
+@pytest.mark.parametrize("m,n,k", [(33, 193, 65), (300, 273, 96), (200, 256, 331), (129, 260, 4001), (64, 513, 1280),
+                                   (97, 8, 1030), (40, 100, 66_001)])
+def test_odd_rows_with_and_without_scratch(m, n, k, dname):
+    """Operands laid out aligned in scratch give the bits of those loaded as they lie."""
+    a, w, rs, cs, bias, res = _problem(m + n + k, m, n, k)
+    R = torch.from_numpy(res).to(DT[dname]).cuda()
+    A, Wp = _dev(a), _dev(oracle.pack(w))
+    outs = []
+    need = t3.load().t3_gemm_fwd_act_scratch(m, n, k)
+    assert need > 0
+    # none to speak of; too little; what it wants, one byte past it untouched
+    for room in (1, need - 1, need):
+        buf = torch.full((need + 16,), 0x5A, dtype=torch.uint8, device="cuda")
+        pre = torch.full((m, n), 7.0, dtype=DT[dname], device="cuda")
+        out = t3.t3_gemm_fwd_act(A, Wp, row_scale=_dev(rs), col_scale=_dev(cs), bias=_dev(bias), act=t3.T3_ACT_SILU,
+                                 residual=R, kind=KIND[dname], pre=pre, scratch=buf[:room])
+        outs.append((out, pre))
+        assert torch.all(buf[room:] == 0x5A)
+        if room < need:
+            assert torch.all(buf == 0x5A), "used a scratch that is too small"
+    x = a.astype(np.int64) @ w.astype(np.int64)
+    for out, pre in outs:
+        _check(out, pre, x, rs, cs, bias, _np(R), "silu", dname)
+        assert torch.equal(out, outs[0][0]) and torch.equal(pre, outs[0][1])
 
 
 # --------------------------------------------------------------- gradient ---

@@ -84,13 +84,13 @@ def test_scan_bwd_refusals(lib):
         assert _scan_bwd(lib, g=None, c=None, h=None, d=None, dg=None, dc=None, **kw) == t3.T3_OK, kw
 
 
-def _act(lib, a=FAKE, wp=FAKE, c=FAKE, m=4, n=8, k=8, act=0, r=None, pre=None, kind=F32, ws=None):
-    return lib.t3_gemm_fwd_act(a, wp, c, m, n, k, None, None, None, act, r, pre, kind, ws, None)
+def _act(lib, a=FAKE, wp=FAKE, c=FAKE, m=4, n=8, k=8, act=0, r=None, pre=None, kind=F32, ws=None, room=0):
+    return lib.t3_gemm_fwd_act(a, wp, c, m, n, k, None, None, None, act, r, pre, kind, ws, None, room, None)
 
 
 def test_act_refusals(lib):
     bad = [dict(m=-1), dict(n=-1), dict(k=-1), dict(m=BIG), dict(act=5), dict(act=-1), dict(kind=2), dict(kind=3),
-           dict(a=None), dict(wp=None), dict(c=None), dict(r=FAKE), dict(pre=FAKE)]
+           dict(a=None), dict(wp=None), dict(c=None), dict(r=FAKE), dict(pre=FAKE), dict(room=-1)]
     for kw in bad:
         assert _act(lib, **kw) == t3.T3_EINVAL, kw
     other = ctypes.c_void_p(8192)
@@ -99,6 +99,13 @@ def test_act_refusals(lib):
     assert _act(lib, m=1, k=16777216) == t3.T3_EOVERFLOW
     assert _act(lib, m=0, a=None, wp=None, c=None) == t3.T3_OK
     assert _act(lib, n=0, a=None, wp=None, c=None) == t3.T3_OK
+
+
+def test_act_scratch(lib):
+    f = lib.t3_gemm_fwd_act_scratch
+    assert f(32, 729, 243) == f(64, 728, 256) == f(64, 0, 3) == f(64, 3, 0) == f(-1, 3, 3) == 0
+    assert f(64, 729, 243) == 64 * 256 + 732 * 64 + 64 * 732 * 4  # A, packed weights, int32 result
+    assert f(64, 728, 243) > 0 and f(64, 729, 256) > 0
 
 
 def _act_bwd(lib, dy=FAKE, z=FAKE, act=1, dz=FAKE, db=None, rows=4, cols=8, dt=BF16, ws=None):
