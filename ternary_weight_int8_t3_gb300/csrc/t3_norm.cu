@@ -24,6 +24,11 @@
 // meet at barriers of their own.  dgamma: each CTA adds its groups' sums in turn,
 // writes one partial row, and a second small kernel adds the partial rows in a
 // fixed order.
+//
+// Measured (GB300, bf16 with residual; bytes of the formulas over the time, of
+// the measured 6784 GB/s): forward 16384 x 1280 25.7 us (84 %), 16384 x 3456
+// 62.6 us (93 %), 1 x 8192 2.6 us; backward 35 us (71 %) and 82.7 us (81 %).
+// Odd widths: 1782 x 729 float 4.8 us forward, 11.4 us backward.
 #include "t3_vec.cuh"
 
 namespace t3 {
