@@ -1135,23 +1135,39 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads(kMode), 1)
     const int nslots = bf16_out ? 4 : 2, slot_bytes = kWarpStage / nslots;
     const int uses = kMode == kModeAct && p.epi.pre ? 2 : 1;  // slots a block takes
     const bool has_res = kMode == kModeAct && p.epi.residual;
-    // room to load a tile's three residual blocks at once, or one block early
-    const bool res_all = nslots == 4 && uses == 1, res_ahead = !res_all && nslots >= 2 * uses;
-    uint32_t use = 0, res_par = 0;
+    // The residual runs ahead of the sums by so many blocks, across tiles, so that its way
+    // from memory is hidden; by none where a block takes all the slots.
+    const int lead = nslots / uses == 4 ? 2 : nslots / uses == 2 ? 1 : 0;
+    int use = 0, ahead = 0;  // ahead: residual blocks on their way or there, not yet added
+    uint32_t res_par = 0;
     bool res_ok = true;
-    auto fetch = [&](uint32_t n, int col, int row, int pending) {  // the residual into the slot of use n
+    int fetch_tile = pair - npairs, fetch_row = 0, fetch_col = 0, fetch_end = 0;  // the next block's place
+    auto fetch = [&](int c_use) {  // the next block into its slot; c_use: the use of the first block not added
       if constexpr (kMode == kModeAct) {
-        if (lane == 0) {
-          const int s = static_cast<int>(n) & (nslots - 1);
-          bulk_wait_read_upto(pending);
-          mbar_arrive_expect_tx(&res_bar[s], slot_bytes);
-          tma_load_2d(ring + s * slot_bytes, &more.res, &res_bar[s], col, row);
+        while (fetch_col >= fetch_end) {  // this warp's blocks of the tile end
+          if (fetch_tile + npairs >= num_tiles) return;
+          fetch_tile += npairs;
+          fetch_row = fetch_tile / p.tiles_c;
+          fetch_col = (fetch_tile - fetch_row * p.tiles_c) * BN;
+          fetch_end = min(fetch_col + cb1 * 32, static_cast<int>(p.out_cols));
+          fetch_col += cb0 * 32;
+          fetch_row = fetch_row * BMP + static_cast<int>(rank) * 128 + q * 32;
         }
+        if (lane == 0) {
+          const int n = c_use + ahead * uses, s = n & (nslots - 1);
+          bulk_wait_read_upto(use - 1 - (n - nslots));  // the stores behind the slot's last one may be in flight
+          mbar_arrive_expect_tx(&res_bar[s], slot_bytes);
+          tma_load_2d(ring + s * slot_bytes, &more.res, &res_bar[s], fetch_col, fetch_row);
+        }
+        ++ahead;
+        fetch_col += 32;
       }
     };
     if constexpr (kMode == kModeAct) {
       if (epi_tid == 0 && p.epi.pre) prefetch_tensormap(&more.pre);
       if (epi_tid == 0 && p.epi.residual) prefetch_tensormap(&more.res);
+      if (has_res)
+        for (int i = 0; i < lead; ++i) fetch(uses - 1);
     }
     // split schedule: the zeroing grid launched just before has finished
     // before the first output write
@@ -1172,22 +1188,25 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads(kMode), 1)
       const int64_t row = static_cast<int64_t>(row0) + srow;
       const float rs =
           (p.out_kind != kOutI32 && p.row_scale && row < p.out_rows) ? __ldg(p.row_scale + row) : 1.0f;
-      // kModeAct: the residual's first block or all, while the product is still
-      // computed
-      int fetched = 0;
-      if (has_res)
-        for (int cb = cb0; cb < (res_all ? cb1 : cb0 + 1); ++cb, ++fetched) {
-          if (static_cast<int64_t>(tcol) * BN + cb * 32 >= p.out_cols) break;
-          fetch(use + fetched + uses - 1, tcol * BN + cb * 32, row0 + q * 32, nslots - uses - fetched);
+      // kModeAct: the tile's scales and biases, a column a thread, while the
+      // product is still computed
+      float cs_next = 1.0f, bias_next = 0.0f;
+      if constexpr (kMode == kModeAct) {
+        static_assert(kEpiThreads >= BN, "a thread for each column");
+        const int64_t col = static_cast<int64_t>(tcol) * BN + epi_tid;
+        if (epi_tid < BN && col < p.out_cols) {
+          if (p.col_scale) cs_next = __ldg(p.col_scale + col);
+          if (p.epi.bias) bias_next = __ldg(p.epi.bias + col);
         }
+      }
       for (int64_t c0 = kb0, c1; c0 < kb1; c0 = c1) {
         c1 = kSplit ? chunk_end(static_cast<int>(c0), static_cast<int>(kb1))
                     : ((kb1 < c0 + kChunkStages) ? kb1 : c0 + kChunkStages);
         ok = mbar_wait(&acc_full[ab], aph, abort_flag, p.err, code_base | 4);
         ok = named_bar_and(kEpiBarrier, kEpiThreads, __all_sync(0xffffffffu, ok && res_ok));
         if (!ok)  // giving up: the copies in flight land before this CTA leaves
-          for (int i = 0; i < fetched; ++i) {
-            const int s = static_cast<int>(use + i + uses - 1) & (nslots - 1);
+          for (int i = 0; i < ahead; ++i) {
+            const int s = (use + uses - 1 + i * uses) & (nslots - 1);
             mbar_wait(&res_bar[s], (res_par >> s) & 1u, abort_flag, p.err, code_base | 4);
           }
         if (!ok) break;
@@ -1200,11 +1219,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads(kMode), 1)
         if (p.out_kind != kOutI32) {
           // the tile's column scales, once (the barrier above ends the previous
           // tile's reads of them)
-          for (int j = epi_tid; j < BN; j += kEpiThreads) {
-            const int64_t col = static_cast<int64_t>(tcol) * BN + j;
-            cs_tile[j] = p.col_scale ? (col < p.out_cols ? __ldg(p.col_scale + col) : 0.0f) : 1.0f;
-            if (kMode == kModeAct)
-              bias_tile[j] = p.epi.bias && col < p.out_cols ? __ldg(p.epi.bias + col) : 0.0f;
+          if constexpr (kMode == kModeAct) {
+            if (epi_tid < BN) {
+              cs_tile[epi_tid] = cs_next;
+              bias_tile[epi_tid] = bias_next;
+            }
+          } else {
+            for (int j = epi_tid; j < BN; j += kEpiThreads) {
+              const int64_t col = static_cast<int64_t>(tcol) * BN + j;
+              cs_tile[j] = p.col_scale ? (col < p.out_cols ? __ldg(p.col_scale + col) : 0.0f) : 1.0f;
+            }
           }
           named_bar_sync(kEpiBarrier, kEpiThreads);
         }
@@ -1219,20 +1243,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads(kMode), 1)
             // each warp stages and stores its own 32 rows: no barrier between
             // them within a tile
             const int row_w = row0 + q * 32, col = static_cast<int>(col0);
-            if (has_res) {
-              if (!res_all && !res_ahead && cb > cb0) fetch(use + uses - 1, col, row_w, nslots - uses);
-              if (res_ahead && cb + 1 < cb1 && col0 + 32 < p.out_cols)
-                fetch(use + 2 * uses - 1, col + 32, row_w, nslots - 2 * uses);
-            }
+            if (has_res && lead == 0) fetch(use + uses - 1);
             float y[32];
             scale_bias(y, v, rs, cs_tile + cb * 32, bias_tile + cb * 32);
             for (int pass = 2 - uses; pass < 2; ++pass, ++use) {
-              const int s = static_cast<int>(use) & (nslots - 1);
+              const int s = use & (nslots - 1);
               uint8_t* slot = ring + s * slot_bytes;
               if (pass == 1) act_row_any(y, p.epi.act);
               if (pass == 1 && has_res) {
+                if (lead > 0) fetch(use);
                 if (res_ok) res_ok = mbar_wait(&res_bar[s], (res_par >> s) & 1u, abort_flag, p.err, code_base | 4);
                 res_par ^= 1u << s;
+                --ahead;
                 add_slot(y, slot, lane, bf16_out);
               } else {
                 if (lane == 0) bulk_wait_read_upto(nslots - 1);
