@@ -490,24 +490,29 @@ def _dense(t, dtype, dev, shape, name):
 
 
 _fns = {}
-_raw_stream = None
+_raw_stream = _device = None
+
+
+def _bind(name):
+    """The library's function, and the current stream's handle and device without
+    the objects and checks around them."""
+    global _raw_stream, _device
+    torch = _torch()
+    _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
+                          lambda d: torch.cuda.current_stream(d).cuda_stream)
+    _device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+    fn = _fns[name] = getattr(load(), name)
+    return fn
 
 
 def _launch(name, dev, stream, *args):
     """Calls the library on device number `dev`, on its current stream unless one is given."""
-    global _raw_stream
-    fn = _fns.get(name)
-    if fn is None:
-        fn = _fns[name] = getattr(load(), name)
-        # the current stream's handle without a Stream object around it
-        _raw_stream = getattr(_torch()._C, "_cuda_getCurrentRawStream",
-                              lambda d: _torch().cuda.current_stream(d).cuda_stream)
+    fn = _fns.get(name) or _bind(name)
     s = _raw_stream(dev) if stream is None else stream.cuda_stream
-    cuda = _torch().cuda
-    if dev == cuda.current_device():
+    if dev == _device():
         rc = fn(*args, s)
     else:
-        with cuda.device(dev):
+        with _torch().cuda.device(dev):
             rc = fn(*args, s)
     if rc != T3_OK:
         raise T3Error(rc, name)

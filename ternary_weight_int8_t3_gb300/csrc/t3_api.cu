@@ -693,8 +693,11 @@ int t3_gemm_fwd_act(const int8_t* A, const uint8_t* Wp, void* C, int64_t M, int6
     st = T3_EINVAL;
     if (M <= kSmallM) {
       if (gemv_rows(M, N, K)) st = launch_gemv_fwd_act(A, Wp, C, e, out_kind, M, N, K, dev->sms, stream);
+      if (st == T3_EINVAL && small_product(M, N, K, false))
+        st = launch_few_act(A, Wp, C, e, out_kind, M, N, K, dev->sms, stream);
     } else if (small_product(M, N, K, words || room)) {
       st = launch_small_act(A, Wp, C, e, out_kind, M, N, K, dev->sms, stream);
+      if (st == T3_EINVAL) st = launch_few_act(A, Wp, C, e, out_kind, M, N, K, dev->sms, stream);
     } else {
       if (tma) st = run_tc2<kOpFwd>(A, Wp, C, M, N, K, stream, out_kind, row_scale, col_scale, &e);
       if (st == T3_EINVAL && room) {

@@ -85,9 +85,12 @@ int launch_small(int op, const int8_t* x, const int8_t* y, const uint8_t* wp, in
                  int64_t M, int64_t N, int64_t K, int sms, cudaStream_t s);
 
 // The forward of launch_small with the epilogue in its kernel; T3_EINVAL, with
-// nothing launched, where the tiles are so few that splitting the reduction is faster.
+// nothing launched, where the tiles are so few that splitting the reduction is faster;
+// launch_few_act splits it over a CTA's warps, T3_EINVAL where it is too long for that.
 int launch_small_act(const int8_t* A, const uint8_t* Wp, void* C, const EpilogueArgs& e, int kind, int64_t M,
                      int64_t N, int64_t K, int sms, cudaStream_t s);
+int launch_few_act(const int8_t* A, const uint8_t* Wp, void* C, const EpilogueArgs& e, int kind, int64_t M,
+                   int64_t N, int64_t K, int sms, cudaStream_t s);
 
 // Small-M forward (M <= 32) on the tensor cores.
 int launch_skinny_fwd(const int8_t* A, const uint8_t* Wp, int32_t* C, int64_t M, int64_t N,

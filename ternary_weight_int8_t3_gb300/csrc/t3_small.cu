@@ -60,6 +60,7 @@ struct Params {
   int split;           // CTAs per output tile (> 1: atomic adds onto zeros)
   int x_vec;           // fwd/dX: rows of x as 16-byte loads; dW: rows of A as words
   int y_vec;           // dW: rows of dY as words
+  int w_vec;           // rows of Wp as words (the kernel for few tiles)
 };
 
 // 16 bytes of row `row` (of `len` bytes, `nrows` rows) from column c; 0 past
@@ -276,6 +277,137 @@ __global__ void __launch_bounds__(kThreads) small_act_kernel(const Params p, con
   }
 }
 
+// The forward with a layer's epilogue where the tiles above are few: a CTA takes a
+// small tile, and its warps split the reduction and join in shared memory, so
+// that the sum ends in one launch and needs neither zeros nor an int32 output.
+// Each warp stages its own chunks: no barrier before the join.  What bounds it: reads of
+// shared memory (a lane's 4 x 4 block takes 8 of them for 64 dp4a) and, for
+// rows on odd boundaries, the loads' instructions.
+constexpr int kFewRows = 32, kFewCols = 16;  // output tile of a CTA
+constexpr int kFewChunk = 32;                // reduction elements a warp takes at once
+constexpr int kFewPitch = kFewChunk / 4 + 4; // words between staged rows (48 bytes): 8 rows on distinct banks
+constexpr int kFewWarps = 8;
+constexpr int64_t kFewLong = 1536;          // reductions up to which it is taken
+constexpr int kFewSlot = 40;                 // words between a warp's sums in the join: distinct banks
+
+// 16 bytes of a row from its column c; 0 past the row's end and where the row
+// does not exist.  Rows on any boundary: the aligned words around them, as far as those lie in
+// the matrix [base, base + total).
+__device__ __forceinline__ uint4 load16_words(const int8_t* base, int64_t total, int64_t at, int64_t left, int vec) {
+  uint32_t b[4] = {0u, 0u, 0u, 0u};
+  if (left > 0) {
+    const int8_t* p = base + at;
+    if (vec && left >= 16) return __ldg(reinterpret_cast<const uint4*>(p));
+    const int off = static_cast<int>(reinterpret_cast<uintptr_t>(p) & 3);
+    if (at >= off && at - off + 20 <= total) {
+      const uint32_t* w = reinterpret_cast<const uint32_t*>(p - off);
+      uint32_t v[5];
+#pragma unroll
+      for (int j = 0; j < 5; ++j) v[j] = __ldg(w + j);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        b[j] = __funnelshift_r(v[j], v[j + 1], 8 * off);
+        const int64_t n = left - 4 * j;  // of the row's bytes
+        if (n < 4) b[j] = n <= 0 ? 0u : b[j] & ((1u << (8 * n)) - 1u);
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < 16; ++j)
+        if (j < left) b[j >> 2] |= static_cast<uint32_t>(static_cast<uint8_t>(__ldg(p + j))) << (8 * (j & 3));
+    }
+  }
+  return make_uint4(b[0], b[1], b[2], b[3]);
+}
+
+template <class Out>
+__global__ void __launch_bounds__(32 * kFewWarps) few_act_kernel(const Params p, const Out out) {
+  __shared__ __align__(16) uint32_t stage[kFewWarps][kFewRows + kFewCols][kFewPitch];
+  __shared__ int32_t sums[kFewWarps][16 * kFewSlot];
+  const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
+  const int64_t tr = blockIdx.x / p.tiles_c;
+  const int64_t row0 = tr * kFewRows, col0 = (blockIdx.x - tr * p.tiles_c) * kFewCols;
+  launch_dependents();
+  grid_dependency_wait();
+  // this thread's outputs: rows t / 16 and t / 16 + 16, column t % 16
+  const int64_t col = col0 + (t & 15), r0 = row0 + (t >> 4);
+  typename Out::Ahead ahead[2];
+#pragma unroll
+  for (int u = 0; u < 2; ++u)
+    if (col < p.cols && r0 + 16 * u < p.rows) ahead[u] = out.ahead(r0 + 16 * u, col, p.cols);
+
+  uint32_t(*xs)[kFewPitch] = stage[warp];
+  uint32_t(*ys)[kFewPitch] = stage[warp] + kFewRows;
+  // a lane loads 16 elements of rows lane / 2 and lane / 2 + 16, and 16 codes of one
+  // of the 16 weight rows, a chunk of its warp ahead
+  const int lrow = lane >> 1, seg = lane & 1;
+  const int64_t total = p.M * p.K, n = col0 + lrow;
+  uint4 xv[2];
+  uint32_t code;
+  auto fetch = [&](int64_t c) {
+    const int64_t k = c * kFewChunk + 16 * seg, b = k / 4;
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      const int64_t m = row0 + lrow + 16 * u;
+      xv[u] = load16_words(p.x, total, m * p.K + k, m < p.M ? p.K - k : 0, p.x_vec);
+    }
+    if (p.w_vec)
+      code = n < p.N && b < p.KB ? __ldg(reinterpret_cast<const uint32_t*>(p.wp + n * p.KB + b)) : 0u;
+    else
+      code = load_codes4(p.wp, p.N, p.KB, n, b);
+  };
+  int32_t acc[4][4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) acc[i][j] = 0;
+  const int ty = lane >> 2, tx = lane & 3;  // rows ty + 8 i, columns tx + 4 j
+  if (warp < p.chunks) fetch(warp);
+  for (int64_t c = warp; c < p.chunks; c += kFewWarps) {
+#pragma unroll
+    for (int u = 0; u < 2; ++u)  // the decode's order: even elements, then odd
+      *reinterpret_cast<uint4*>(&xs[lrow + 16 * u][4 * seg]) =
+          make_uint4(prmt(xv[u].x, xv[u].y, 0x6420u), prmt(xv[u].z, xv[u].w, 0x6420u),
+                     prmt(xv[u].x, xv[u].y, 0x7531u), prmt(xv[u].z, xv[u].w, 0x7531u));
+    uint32_t d[4];
+    decode16_s8(code, d);
+    *reinterpret_cast<uint4*>(&ys[lrow][4 * seg]) = make_uint4(d[0], d[1], d[2], d[3]);
+    __syncwarp();
+    if (c + kFewWarps < p.chunks) fetch(c + kFewWarps);
+#pragma unroll
+    for (int g = 0; g < kFewChunk / 16; ++g) {
+      uint4 a[4], b[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) a[i] = *reinterpret_cast<const uint4*>(&xs[ty + 8 * i][4 * g]);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) b[j] = *reinterpret_cast<const uint4*>(&ys[tx + 4 * j][4 * g]);
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          acc[i][j] = __dp4a(static_cast<int>(a[i].x), static_cast<int>(b[j].x), acc[i][j]);
+          acc[i][j] = __dp4a(static_cast<int>(a[i].y), static_cast<int>(b[j].y), acc[i][j]);
+          acc[i][j] = __dp4a(static_cast<int>(a[i].z), static_cast<int>(b[j].z), acc[i][j]);
+          acc[i][j] = __dp4a(static_cast<int>(a[i].w), static_cast<int>(b[j].w), acc[i][j]);
+        }
+    }
+    __syncwarp();
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) sums[warp][(4 * i + j) * kFewSlot + lane] = acc[i][j];
+  __syncthreads();
+#pragma unroll
+  for (int u = 0; u < 2; ++u) {
+    const int r = (t >> 4) + 16 * u, c = t & 15;  // in the tile
+    const int at = (4 * (r >> 3) + (c >> 2)) * kFewSlot + 4 * (r & 7) + (c & 3);
+    int32_t sum = 0;
+#pragma unroll
+    for (int i = 0; i < kFewWarps; ++i) sum += sums[i][at];
+    if (col < p.cols && row0 + r < p.rows) out.put((row0 + r) * p.cols + col, sum, ahead[u]);
+  }
+}
+
 }  // namespace smp
 
 int launch_small(int op, const int8_t* x, const int8_t* y, const uint8_t* wp, int32_t* out,
@@ -327,13 +459,9 @@ int launch_small(int op, const int8_t* x, const int8_t* y, const uint8_t* wp, in
   return cudaGetLastError() == cudaSuccess ? T3_OK : T3_ECUDA;
 }
 
-// With two tiles an SM one CTA takes a tile's whole sum and the epilogue with it
-// (1782 x 729 x 243: 17.1 us, against 21.7 split in two and with the epilogue behind).  Fewer
-// tiles are split over CTAs, which needs the int32 output in between (200 x 500
-// x 500: 8.2 us, against 16.9 unsplit).
-int launch_small_act(const int8_t* A, const uint8_t* Wp, void* C, const EpilogueArgs& e, int kind, int64_t M,
-                     int64_t N, int64_t K, int sms, cudaStream_t s) {
-  smp::Params p{};
+namespace smp {
+Params act_params(const int8_t* A, const uint8_t* Wp, int64_t M, int64_t N, int64_t K) {
+  Params p{};
   p.x = A;
   p.wp = Wp;
   p.M = M;
@@ -343,16 +471,46 @@ int launch_small_act(const int8_t* A, const uint8_t* Wp, void* C, const Epilogue
   p.rows = M;
   p.cols = N;
   p.red = K;
-  p.tiles_c = (N + smp::kTile - 1) / smp::kTile;
-  p.chunks = (K + smp::kChunk - 1) / smp::kChunk;
   p.split = 1;
   p.x_vec = (K % 16 == 0) && (reinterpret_cast<uintptr_t>(A) % 16 == 0);
+  p.w_vec = (p.KB % 4 == 0) && (reinterpret_cast<uintptr_t>(Wp) % 4 == 0);
+  return p;
+}
+}  // namespace smp
+
+// With two tiles an SM one CTA takes a tile's whole sum and the epilogue with it
+// (1782 x 729 x 243: 17.1 us, against 21.7 split in two and with the epilogue behind).
+int launch_small_act(const int8_t* A, const uint8_t* Wp, void* C, const EpilogueArgs& e, int kind, int64_t M,
+                     int64_t N, int64_t K, int sms, cudaStream_t s) {
+  smp::Params p = smp::act_params(A, Wp, M, N, K);
+  p.tiles_c = (N + smp::kTile - 1) / smp::kTile;
+  p.chunks = (K + smp::kChunk - 1) / smp::kChunk;
   const int64_t grid = (M + smp::kTile - 1) / smp::kTile * p.tiles_c;
   if (grid < 2 * static_cast<int64_t>(sms)) return T3_EINVAL;
   if (kind == T3_OUT_BF16)
     return vec::launch(smp::small_act_kernel<OutAct<__nv_bfloat16>>, grid, smp::kThreads, 0, s, 1, p,
                        OutAct<__nv_bfloat16>{static_cast<__nv_bfloat16*>(C), e});
   return vec::launch(smp::small_act_kernel<OutAct<float>>, grid, smp::kThreads, 0, s, 1, p,
+                     OutAct<float>{static_cast<float*>(C), e});
+}
+
+// Short reductions over tiles that are resident at once (two CTAs an SM), or shorter
+// ones over several waves.  Measured against the int32 product and the epilogue
+// behind it: 27 x 729 x 243 3.2 us (7.0), 128 x 608 x 512 3.6 (7.5), 200 x 500 x 500
+// 5.7 (8.4), 27 x 2000 x 1501 9.7 (10.6), 1000 x 300 x 100 6.0 (7.2); beyond the limits
+// 27 x 1000 x 2001 12.1 (9.3), 32 x 2048 x 2048 10.3 (8.0) and, in two waves, 27 x 7296 x 512
+// 7.7 (6.0).
+int launch_few_act(const int8_t* A, const uint8_t* Wp, void* C, const EpilogueArgs& e, int kind, int64_t M,
+                   int64_t N, int64_t K, int sms, cudaStream_t s) {
+  smp::Params p = smp::act_params(A, Wp, M, N, K);
+  p.tiles_c = (N + smp::kFewCols - 1) / smp::kFewCols;
+  p.chunks = (K + smp::kFewChunk - 1) / smp::kFewChunk;
+  const int64_t grid = (M + smp::kFewRows - 1) / smp::kFewRows * p.tiles_c, wave = 2 * static_cast<int64_t>(sms);
+  if (K > smp::kFewLong || (grid > wave && (grid + wave - 1) / wave * K > smp::kFewLong / 2)) return T3_EINVAL;
+  if (kind == T3_OUT_BF16)
+    return vec::launch(smp::few_act_kernel<OutAct<__nv_bfloat16>>, grid, 32 * smp::kFewWarps, 0, s, 1, p,
+                       OutAct<__nv_bfloat16>{static_cast<__nv_bfloat16*>(C), e});
+  return vec::launch(smp::few_act_kernel<OutAct<float>>, grid, 32 * smp::kFewWarps, 0, s, 1, p,
                      OutAct<float>{static_cast<float*>(C), e});
 }
 

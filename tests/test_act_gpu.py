@@ -91,6 +91,24 @@ def test_product(m, n, k, dname):
     assert rc == t3.T3_OK, hex(detail)
 
 
+# reductions around the 16 codes a lane takes, the 32 and 256 elements a warp and a CTA take, and the
+# longest that stay in one CTA; tiles that end inside; operands on every byte boundary
+@pytest.mark.parametrize("k", [1, 4, 15, 16, 33, 64, 255, 256, 257, 511, 1535, 1536, 1537])
+@pytest.mark.parametrize("m,n", [(9, 17), (31, 200), (33, 15), (70, 48)])
+def test_short_reductions_of_few_tiles(m, n, k):
+    a, w, rs, cs, bias, res = _problem(m + n + k, m, n, k)
+    x = a.astype(np.int64) @ w.astype(np.int64)
+    packed = oracle.pack(w)
+    R = _dev(res)
+    for shift in range(4):
+        A = _dev(np.concatenate([np.full(shift, 77, np.int8), a.reshape(-1)]))[shift:].view(m, k)
+        Wp = _dev(np.concatenate([np.full(3 - shift, 255, np.uint8), packed.reshape(-1)]))[3 - shift:].view(packed.shape)
+        pre = torch.full((m, n), 7.0, device="cuda")
+        out = t3.t3_gemm_fwd_act(A, Wp, K=k, row_scale=_dev(rs), col_scale=_dev(cs), bias=_dev(bias),
+                                 act=t3.T3_ACT_GELU, residual=R, pre=pre)
+        _check(out, pre, x, rs, cs, bias, res, "gelu", "f32")
+
+
 @pytest.mark.parametrize("dname", ["bf16", "f32"])
 @pytest.mark.parametrize("m,n,k", [(1, 512, 256), (20, 512, 256), (300, 384, 256)])
 @pytest.mark.parametrize("act", ref.ACTS)
