@@ -185,12 +185,12 @@ __device__ __forceinline__ float2 take2(float2 f, float2& slope) {
   return k;
 }
 
-// Bit i of the result: whether a reset stands at step t0 + i (i < n <= 32).
-__device__ __forceinline__ uint32_t reset_bits(const uint8_t* resets, int64_t at, int64_t t0, int64_t length,
-                                               int n, int lane) {
-  if (!resets) return 0;
-  const bool r = lane < n && t0 + lane < length && resets[at + t0 + lane] != 0;
-  return __ballot_sync(0xffffffffu, r);
+// A lane's mark of a round: whether a reset stands at step t0 + lane (lane < n <= 32).
+// Loaded a round ahead, like the operands; the ballot of all lanes' is the
+// round's resets.
+__device__ __forceinline__ uint32_t reset_mark(const uint8_t* resets, int64_t at, int64_t t0, int64_t length, int n,
+                                               int lane) {
+  return resets && lane < n && t0 + lane < length ? resets[at + t0 + lane] : 0u;
 }
 
 // A map (R, H) applied to a state, and the map of first (a, b), then (R, H).
@@ -439,6 +439,7 @@ __global__ void __launch_bounds__(32 * kWarps, kPerSm) scan_fwd_kernel(const Fwd
     copy_commit();
   };
   issue(0, 0);
+  uint32_t mark = reset_mark(p.resets, b * p.length, mine, p.length, Stage::kRows, lane);
   if (p.h0 && live) {  // plain loads: h_last may be the same array
     carry[0] = p.h0[b * p.width + ch];
     if (second) carry[1] = p.h0[b * p.width + ch + kNext];
@@ -448,11 +449,13 @@ __global__ void __launch_bounds__(32 * kWarps, kPerSm) scan_fwd_kernel(const Fwd
   int round = 0;
   for (int64_t base = 0; base < p.length; base += span, ++round) {
     const int phase = round & 1;
-    if (base + span < p.length)
+    const uint32_t resets = __ballot_sync(0xffffffffu, mark != 0) >> (group * S);
+    if (base + span < p.length) {
       issue(base + span, phase ^ 1);
-    else
+      mark = reset_mark(p.resets, b * p.length, base + span + mine, p.length, Stage::kRows, lane);
+    } else {
       copy_commit();  // an empty group, so that waiting for all but one still means this stage
-    const uint32_t resets = reset_bits(p.resets, b * p.length, base + mine, p.length, Stage::kRows, lane) >> (group * S);
+    }
     copy_wait<1>();
     __syncwarp();
     const uint8_t* sf = stages[phase].a[0] + group * (S * Stage::kRow + Stage::kSkip);
@@ -583,6 +586,7 @@ __global__ void __launch_bounds__(32 * kWarps, kPerSm) scan_bwd_kernel(const Bwd
   };
   const int64_t last = p.length > 0 ? (p.length - 1) / span * span : 0;
   issue(last, 0);
+  uint32_t mark = reset_mark(p.resets, row0, last + mine, p.length, Stage::kRows, lane);
   if (live) {
     const int64_t at = b * p.width + ch;
     if (p.dh_last) {
@@ -599,11 +603,13 @@ __global__ void __launch_bounds__(32 * kWarps, kPerSm) scan_bwd_kernel(const Bwd
   int round = 0;
   for (int64_t base = last; base >= 0; base -= span, ++round) {
     const int phase = round & 1;
-    if (base > 0)
+    const uint32_t resets = __ballot_sync(0xffffffffu, mark != 0) >> (group * S);
+    if (base > 0) {
       issue(base - span, phase ^ 1);
-    else
+      mark = reset_mark(p.resets, row0, base - span + mine, p.length, Stage::kRows, lane);
+    } else {
       copy_commit();  // an empty group, so that waiting for all but one still means this stage
-    const uint32_t resets = reset_bits(p.resets, row0, base + mine, p.length, Stage::kRows, lane) >> (group * S);
+    }
     copy_wait<1>();
     __syncwarp();
     const Stage& st = stages[phase];
