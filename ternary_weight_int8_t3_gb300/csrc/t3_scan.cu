@@ -186,11 +186,12 @@ __device__ __forceinline__ float2 take2(float2 f, float2& slope) {
 }
 
 // A lane's mark of a round: whether a reset stands at step t0 + lane (lane < n <= 32).
-// Loaded a round ahead, like the operands; the ballot of all lanes' is the
-// round's resets.
+// Loaded a round ahead and in front of that round's copies, behind which it would
+// come back late (8 x 2048 x 3456 backward: 132 us, against 109); the ballot of all
+// lanes' is the round's resets.
 __device__ __forceinline__ uint32_t reset_mark(const uint8_t* resets, int64_t at, int64_t t0, int64_t length, int n,
                                                int lane) {
-  return resets && lane < n && t0 + lane < length ? resets[at + t0 + lane] : 0u;
+  return lane < n && t0 + lane < length ? resets[at + t0 + lane] : 0u;
 }
 
 // A map (R, H) applied to a state, and the map of first (a, b), then (R, H).
@@ -409,9 +410,15 @@ __device__ __forceinline__ void write_pair(T* p, float2 v, bool second) {
   }
 }
 
-// CH: bytes a copy (16: rows of whole 16-byte pieces, outputs on pairs).  A
-// launch without a cluster (size 1) executes no cluster instruction.
-template <class T, int LPR, int S, int CH>
+// What the steps of a lane's run have to look at.  Resets alone are common (a
+// packed batch) and cost a few predicated moves a step; with everything looked at, the one
+// slow warp in many rounds holds its CTA's others.
+enum { kPlain, kResets, kCareful };
+
+// CH: bytes a copy (16: rows of whole 16-byte pieces, outputs on pairs).  kMarks:
+// there are resets (looking whether there are costs a call without them 1 to 4 %).  A launch
+// without a cluster (size 1) executes no cluster instruction.
+template <class T, int LPR, int S, int CH, bool kMarks>
 __global__ void __launch_bounds__(32 * kWarps, kPerSm) scan_fwd_kernel(const FwdArgs p) {
   using Stage = Slab<T, LPR, S, 2>;
   extern __shared__ __align__(16) uint8_t smem[];
@@ -426,7 +433,7 @@ __global__ void __launch_bounds__(32 * kWarps, kPerSm) scan_fwd_kernel(const Fwd
   const T* gate = static_cast<const T*>(p.gate) + b * p.length * p.ldg + ch0;
   const T* cand = static_cast<const T*>(p.cand) + b * p.length * p.ldc + ch0;
   T* out = static_cast<T*>(p.h) + b * p.length * p.ldh + ch;
-  Stage* stages = reinterpret_cast<Stage*>(smem) + warp * 2;  // this warp's two
+  Stage* stages = reinterpret_cast<Stage*>(smem) + warp * 2;  // this warp's
   float4* cta_maps = reinterpret_cast<float4*>(smem + 2 * kWarps * sizeof(Stage));
   float carry[2] = {};
   launch_dependents();
@@ -439,7 +446,7 @@ __global__ void __launch_bounds__(32 * kWarps, kPerSm) scan_fwd_kernel(const Fwd
     copy_commit();
   };
   issue(0, 0);
-  uint32_t mark = reset_mark(p.resets, b * p.length, mine, p.length, Stage::kRows, lane);
+  uint32_t mark = kMarks ? reset_mark(p.resets, b * p.length, mine, p.length, Stage::kRows, lane) : 0u;
   if (p.h0 && live) {  // plain loads: h_last may be the same array
     carry[0] = p.h0[b * p.width + ch];
     if (second) carry[1] = p.h0[b * p.width + ch + kNext];
@@ -449,62 +456,66 @@ __global__ void __launch_bounds__(32 * kWarps, kPerSm) scan_fwd_kernel(const Fwd
   int round = 0;
   for (int64_t base = 0; base < p.length; base += span, ++round) {
     const int phase = round & 1;
-    const uint32_t resets = __ballot_sync(0xffffffffu, mark != 0) >> (group * S);
-    if (base + span < p.length) {
+    const uint32_t next_mark =
+        kMarks ? reset_mark(p.resets, b * p.length, base + span + mine, p.length, Stage::kRows, lane) : 0u;
+    if (base + span < p.length)
       issue(base + span, phase ^ 1);
-      mark = reset_mark(p.resets, b * p.length, base + span + mine, p.length, Stage::kRows, lane);
-    } else {
+    else
       copy_commit();  // an empty group, so that waiting for all but one still means this stage
-    }
     copy_wait<1>();
     __syncwarp();
+    const uint32_t resets = kMarks ? __ballot_sync(0xffffffffu, mark != 0) >> (group * S) : 0u;
+    mark = next_mark;
     const uint8_t* sf = stages[phase].a[0] + group * (S * Stage::kRow + Stage::kSkip);
     const uint8_t* sc = stages[phase].a[1] + group * (S * Stage::kRow + Stage::kSkip);
     const int64_t t0 = base + mine + group * S;
     const int n = p.length - t0 < S ? static_cast<int>(p.length - t0) : S;  // steps here (may be negative)
-    // Steps at the sequence's end, resets, and masked tokens (k = 0) whose
-    // candidate is not finite, which would show in H, take the careful form.
+    // A run is plain, or has resets; one that reaches past the sequence's end, or has masked
+    // tokens (k = 0) whose candidate is not finite, which would show in H, takes the
+    // careful form.
     const float2 none = make_float2(0.0f, 0.0f), all = make_float2(1.0f, 1.0f);
     float2 k[S], R = none, H = none, h;
-    bool careful = n < S || resets != 0;
-    if (!careful) {
-#pragma unroll
-      for (int i = 0; i < S; ++i) {
-        k[i] = take2(read_pair<T, LPR, CH == 16>(sf, i, col));
-        R = join2(R, k[i]);
-        H = step2(H, k[i], read_pair<T, LPR, CH == 16>(sc, i, col));
-      }
-      careful = !(fabsf(H.x) + fabsf(H.y) < __int_as_float(0x7f800000));
-    }
-    if (careful) {
+    int form = n < S ? kCareful : kMarks && resets != 0 ? kResets : kPlain;
+    auto first = [&](auto how) {
       R = H = none;
 #pragma unroll
       for (int i = 0; i < S; ++i) {
-        k[i] = i < n ? take2(read_pair<T, LPR, CH == 16>(sf, i, col)) : none;
-        if (resets >> i & 1) {
+        const float2 f = read_pair<T, LPR, CH == 16>(sf, i, col);
+        float2 c = read_pair<T, LPR, CH == 16>(sc, i, col);
+        k[i] = how.value < kCareful || i < n ? take2(f) : none;
+        if (how.value >= kResets && (resets >> i & 1)) {
           R = all;
           H = none;
         }
+        if (how.value == kCareful) c = masked2(k[i], c);
         R = join2(R, k[i]);
-        H = step2(H, k[i], masked2(k[i], read_pair<T, LPR, CH == 16>(sc, i, col)));
+        H = step2(H, k[i], c);
       }
-    }
+    };
+    if (form == kPlain)
+      first(std::integral_constant<int, kPlain>());
+    else if (kMarks && form == kResets)
+      first(std::integral_constant<int, kResets>());
+    if (!(fabsf(H.x) + fabsf(H.y) < __int_as_float(0x7f800000))) form = kCareful;
+    if (form == kCareful) first(std::integral_constant<int, kCareful>());
     h = exchange<LPR, false>(maps, cta_maps, round, size, rank, waits, R, H, carry);
     T* o = out + t0 * p.ldh;
-    if (!careful) {
+    auto second_pass = [&](auto how) {
 #pragma unroll
       for (int i = 0; i < S; ++i, o += p.ldh) {
-        h = step2(h, k[i], read_pair<T, LPR, CH == 16>(sc, i, col));
-        if (live) write_pair<T, LPR, CH == 16>(o, h, second);
+        float2 c = read_pair<T, LPR, CH == 16>(sc, i, col);
+        if (how.value >= kResets && (resets >> i & 1)) h = none;
+        if (how.value == kCareful) c = masked2(k[i], c);
+        h = step2(h, k[i], c);
+        if (live && (how.value < kCareful || i < n)) write_pair<T, LPR, CH == 16>(o, h, second);
       }
-    } else {
-#pragma unroll
-      for (int i = 0; i < S; ++i, o += p.ldh) {
-        if (resets >> i & 1) h = none;
-        h = step2(h, k[i], masked2(k[i], read_pair<T, LPR, CH == 16>(sc, i, col)));
-        if (live && i < n) write_pair<T, LPR, CH == 16>(o, h, second);
-      }
-    }
+    };
+    if (form == kPlain)
+      second_pass(std::integral_constant<int, kPlain>());
+    else if (kMarks && form == kResets)
+      second_pass(std::integral_constant<int, kResets>());
+    else
+      second_pass(std::integral_constant<int, kCareful>());
     __syncwarp();  // this stage is read: the next round copies into it
   }
   copy_wait<0>();
@@ -550,7 +561,7 @@ __global__ void __launch_bounds__(128) scan_fwd_short_kernel(const FwdArgs p) {
   }
 }
 
-template <class T, int LPR, int S, int CH>
+template <class T, int LPR, int S, int CH, bool kMarks>
 __global__ void __launch_bounds__(32 * kWarps, kPerSm) scan_bwd_kernel(const BwdArgs p) {
   using Stage = Slab<T, LPR, S, 4>;
   extern __shared__ __align__(16) uint8_t smem[];
@@ -586,7 +597,7 @@ __global__ void __launch_bounds__(32 * kWarps, kPerSm) scan_bwd_kernel(const Bwd
   };
   const int64_t last = p.length > 0 ? (p.length - 1) / span * span : 0;
   issue(last, 0);
-  uint32_t mark = reset_mark(p.resets, row0, last + mine, p.length, Stage::kRows, lane);
+  uint32_t mark = kMarks ? reset_mark(p.resets, row0, last + mine, p.length, Stage::kRows, lane) : 0u;
   if (live) {
     const int64_t at = b * p.width + ch;
     if (p.dh_last) {
@@ -603,66 +614,71 @@ __global__ void __launch_bounds__(32 * kWarps, kPerSm) scan_bwd_kernel(const Bwd
   int round = 0;
   for (int64_t base = last; base >= 0; base -= span, ++round) {
     const int phase = round & 1;
-    const uint32_t resets = __ballot_sync(0xffffffffu, mark != 0) >> (group * S);
-    if (base > 0) {
+    const uint32_t next_mark =
+        kMarks && base > 0 ? reset_mark(p.resets, row0, base - span + mine, p.length, Stage::kRows, lane) : 0u;
+    if (base > 0)
       issue(base - span, phase ^ 1);
-      mark = reset_mark(p.resets, row0, base - span + mine, p.length, Stage::kRows, lane);
-    } else {
+    else
       copy_commit();  // an empty group, so that waiting for all but one still means this stage
-    }
     copy_wait<1>();
     __syncwarp();
+    const uint32_t resets = kMarks ? __ballot_sync(0xffffffffu, mark != 0) >> (group * S) : 0u;
+    mark = next_mark;
     const Stage& st = stages[phase];
     const int at = group * (S * Stage::kRow + Stage::kSkip);
     const int64_t t0 = base + mine + group * S;
     const int n = p.length - t0 < S ? static_cast<int>(p.length - t0) : S;
     const float2 none = make_float2(0.0f, 0.0f), all = make_float2(1.0f, 1.0f);
     float2 k[S], slope[S], R = none, Q = none, v;
-    const bool careful = n < S || resets != 0 || t0 == 0;  // ends, resets
+    const int form = n < S || t0 == 0 ? kCareful : kMarks && resets != 0 ? kResets : kPlain;  // either end
     // the map of (1 - k) G past these steps to the same in front of them
-    auto fold = [&](auto slow) {
+    auto fold = [&](auto how) {
 #pragma unroll
       for (int i = S - 1; i >= 0; --i) {
         k[i] = take2(read_pair<T, LPR, CH == 16>(st.a[0] + at, i, col), slope[i]);
-        if (slow.value && i >= n) k[i] = none;
+        if (how.value == kCareful && i >= n) k[i] = none;
         const float2 g = __fadd2_rn(read_pair<T, LPR, CH == 16>(st.a[2] + at, i, col), Q);
         R = join2(R, k[i]);
         Q = sub2(g, __fmul2_rn(k[i], g));
-        if (slow.value && (resets >> i & 1)) {
+        if (how.value >= kResets && (resets >> i & 1)) {
           R = all;
           Q = none;
         }
       }
     };
-    if (careful)
-      fold(std::true_type());
+    if (form == kPlain)
+      fold(std::integral_constant<int, kPlain>());
+    else if (kMarks && form == kResets)
+      fold(std::integral_constant<int, kResets>());
     else
-      fold(std::false_type());
+      fold(std::integral_constant<int, kCareful>());
     v = exchange<LPR, true>(maps, cta_maps, round, size, rank, waits, R, Q, carry);
-    auto put = [&](auto slow) {
+    auto put = [&](auto how) {
       T* og = dgate + (t0 + S - 1) * p.lddg;
       T* oc = dcand + (t0 + S - 1) * p.lddc;
 #pragma unroll
       for (int i = S - 1; i >= 0; --i, og -= p.lddg, oc -= p.lddc) {
         const float2 g = __fadd2_rn(read_pair<T, LPR, CH == 16>(st.a[2] + at, i, col), v);
         float2 before = read_pair<T, LPR, CH == 16>(st.a[3] + at, i, col);
-        const bool reset = slow.value && (resets >> i & 1);
-        if (slow.value && t0 + i == 0) before = make_float2(start[0], start[1]);
+        const bool reset = how.value >= kResets && (resets >> i & 1);
+        if (how.value == kCareful && t0 + i == 0) before = make_float2(start[0], start[1]);
         if (reset) before = none;
         const float2 dc = __fmul2_rn(k[i], g);
         const float2 diff = sub2(before, read_pair<T, LPR, CH == 16>(st.a[1] + at, i, col));
         const float2 df = masked2(slope[i], __fmul2_rn(__fmul2_rn(g, slope[i]), diff));
         v = reset ? none : sub2(g, dc);
-        if (live && (!slow.value || i < n)) {
+        if (live && (how.value < kCareful || i < n)) {
           write_pair<T, LPR, CH == 16>(og, df, second);
           write_pair<T, LPR, CH == 16>(oc, dc, second);
         }
       }
     };
-    if (careful)
-      put(std::true_type());
+    if (form == kPlain)
+      put(std::integral_constant<int, kPlain>());
+    else if (kMarks && form == kResets)
+      put(std::integral_constant<int, kResets>());
     else
-      put(std::false_type());
+      put(std::integral_constant<int, kCareful>());
     __syncwarp();  // this stage is read: the next round copies into it
   }
   copy_wait<0>();
@@ -746,34 +762,34 @@ Plan plan(int64_t tiles, int64_t length, int rows, int smem, int per_cta) {
   return best;
 }
 
-template <class T, int CH>
+template <class T, int CH, bool kMarks>
 struct Fwd {
   template <int LPR> struct Kernel;
 };
-template <class T, int CH>
+template <class T, int CH, bool kMarks>
 struct Bwd {
   template <int LPR> struct Kernel;
 };
-template <class T, int CH>
+template <class T, int CH, bool kMarks>
 template <int LPR>
-struct Fwd<T, CH>::Kernel {
+struct Fwd<T, CH, kMarks>::Kernel {
   static constexpr int S = kFwdSteps<T>, rows = kWarps * (32 / LPR) * S;
   static constexpr int smem = 2 * kWarps * sizeof(Slab<T, LPR, S, 2>), per_cta = 2 * LPR * sizeof(float4);
-  static constexpr auto fn = scan_fwd_kernel<T, LPR, S, CH>;
+  static constexpr auto fn = scan_fwd_kernel<T, LPR, S, CH, kMarks>;
 };
-template <class T, int CH>
+template <class T, int CH, bool kMarks>
 template <int LPR>
-struct Bwd<T, CH>::Kernel {
+struct Bwd<T, CH, kMarks>::Kernel {
   static constexpr int S = kBwdSteps<T>, rows = kWarps * (32 / LPR) * S;
   static constexpr int smem = 2 * kWarps * sizeof(Slab<T, LPR, S, 4>), per_cta = 2 * LPR * sizeof(float4);
-  static constexpr auto fn = scan_bwd_kernel<T, LPR, S, CH>;
+  static constexpr auto fn = scan_bwd_kernel<T, LPR, S, CH, kMarks>;
 };
 
 template <class K, int LPR, class Args>
 int run_plan(Args p, int64_t batch, int cluster, cudaStream_t s) {
   p.tiles = (p.width + 2 * LPR - 1) / (2 * LPR);
-  return launch(K::fn, batch * p.tiles * cluster, 32 * kWarps, K::smem + (cluster > 1 ? cluster * K::per_cta : 0), s,
-                cluster, p);
+  return launch(K::fn, batch * p.tiles * cluster, 32 * kWarps,
+                K::smem + (cluster > 1 ? cluster * K::per_cta : 0), s, cluster, p);
 }
 
 // Tiles of 64 channels, or of 32 where that is estimated to be faster: few
@@ -794,18 +810,26 @@ int run(const Args& p, int64_t batch, cudaStream_t s) {
 
 // CH 16: rows of whole 16-byte pieces; otherwise pieces of 4 bytes, or of one
 // element where rows of 2-byte elements start on odd boundaries.
-template <class T>
-int fwd(const FwdArgs& p, int64_t batch, int ch, cudaStream_t s) {
-  if (ch == 16) return run<Fwd<T, 16>::template Kernel>(p, batch, s);
-  if (sizeof(T) == 4 || ch == 4) return run<Fwd<T, 4>::template Kernel>(p, batch, s);
-  return run<Fwd<T, sizeof(T) == 4 ? 4 : 2>::template Kernel>(p, batch, s);
+template <class T, bool kMarks, class Args>
+int run_rows(const Args& p, int64_t batch, int ch, cudaStream_t s) {
+  constexpr bool kFwd = std::is_same_v<Args, FwdArgs>;
+  constexpr int kOdd = sizeof(T) == 4 ? 4 : 2;
+  if constexpr (kFwd) {
+    if (ch == 16) return run<Fwd<T, 16, kMarks>::template Kernel>(p, batch, s);
+    if (ch == 4) return run<Fwd<T, 4, kMarks>::template Kernel>(p, batch, s);
+    return run<Fwd<T, kOdd, kMarks>::template Kernel>(p, batch, s);
+  } else {
+    if (ch == 16) return run<Bwd<T, 16, kMarks>::template Kernel>(p, batch, s);
+    if (ch == 4) return run<Bwd<T, 4, kMarks>::template Kernel>(p, batch, s);
+    return run<Bwd<T, kOdd, kMarks>::template Kernel>(p, batch, s);
+  }
 }
 
-template <class T>
-int bwd(const BwdArgs& p, int64_t batch, int ch, cudaStream_t s) {
-  if (ch == 16) return run<Bwd<T, 16>::template Kernel>(p, batch, s);
-  if (sizeof(T) == 4 || ch == 4) return run<Bwd<T, 4>::template Kernel>(p, batch, s);
-  return run<Bwd<T, sizeof(T) == 4 ? 4 : 2>::template Kernel>(p, batch, s);
+template <class Args>
+int run_any(const Args& p, int64_t batch, int ch, int dtype, cudaStream_t s) {
+  if (dtype == T3_OUT_BF16)
+    return p.resets ? run_rows<vec::bf16, true>(p, batch, ch, s) : run_rows<vec::bf16, false>(p, batch, ch, s);
+  return p.resets ? run_rows<float, true>(p, batch, ch, s) : run_rows<float, false>(p, batch, ch, s);
 }
 
 // Whether every row of `width` elements at `p` with stride ld starts and ends
@@ -832,7 +856,7 @@ int launch_scan_fwd(const void* gate, int64_t ldg, const void* cand, int64_t ldc
     return vec::launch(fn, (n + 127) / 128, 128, 0, s, 1, p);
   }
   const int ch = pair && on(16) ? 16 : on(4) ? 4 : 2;
-  return dtype == T3_OUT_BF16 ? sc::fwd<vec::bf16>(p, batch, ch, s) : sc::fwd<float>(p, batch, ch, s);
+  return sc::run_any(p, batch, ch, dtype, s);
 }
 
 int launch_scan_bwd(const void* gate, int64_t ldg, const void* cand, int64_t ldc, const void* h,
@@ -849,7 +873,7 @@ int launch_scan_bwd(const void* gate, int64_t ldg, const void* cand, int64_t ldc
   };
   const bool pair = sc::rows_on(dgate, lddg, width, es, 2 * es) && sc::rows_on(dcand, lddc, width, es, 2 * es);
   const int ch = pair && on(16) ? 16 : on(4) ? 4 : 2;
-  return dtype == T3_OUT_BF16 ? sc::bwd<vec::bf16>(p, batch, ch, s) : sc::bwd<float>(p, batch, ch, s);
+  return sc::run_any(p, batch, ch, dtype, s);
 }
 
 }  // namespace t3
