@@ -44,6 +44,7 @@
 // round trip between the CTAs of a cluster every 1536 tokens; 27 single tokens
 // of 8192 channels 1.9 us.  Rows that are not whole 16-byte pieces take 1.5 to
 // 1.9 times as long as aligned ones (3 x 1782 x 729 float: 17.1 and 28 us).
+#include <algorithm>
 #include <atomic>
 #include <type_traits>
 
@@ -69,7 +70,8 @@ struct FwdArgs {
   const uint8_t* resets;
   void* h;
   float* h_last;
-  int64_t length, width, tiles;
+  int64_t length, width, tiles;  // tiles: of a sequence
+  int64_t all_tiles;  // of all (shared tiles)
   int64_t channels;  // batch * width (short sequences)
   int* err;
 };
@@ -415,6 +417,64 @@ __device__ __forceinline__ void write_pair(T* p, float2 v, bool second) {
 // slow warp in many rounds holds its CTA's others.
 enum { kPlain, kResets, kCareful };
 
+// A round of this lane's steps: `stage` holds them, t0 is the first, o its output.
+template <class T, int LPR, int S, int CH, bool kMarks>
+__device__ __forceinline__ void forward_round(const Slab<T, LPR, S, 2>& stage, int64_t t0, int64_t length, uint32_t resets,
+                                              T* o, int64_t ldh, bool live, bool second, Maps<LPR>& maps,
+                                              float4* cta_maps, int round, int size, int rank, Waits& waits,
+                                              float (&carry)[2]) {
+  using Stage = Slab<T, LPR, S, 2>;
+  const int col = (threadIdx.x & 31) % LPR, group = (threadIdx.x & 31) / LPR;
+  const uint8_t* sf = stage.a[0] + group * (S * Stage::kRow + Stage::kSkip);
+  const uint8_t* sc = stage.a[1] + group * (S * Stage::kRow + Stage::kSkip);
+  const int n = length - t0 < S ? static_cast<int>(length - t0) : S;  // steps here (may be negative)
+  // A run is plain, or has resets; one that reaches past the sequence's end, or has masked
+  // tokens (k = 0) whose candidate is not finite, which would show in H, takes the
+  // careful form.
+  const float2 none = make_float2(0.0f, 0.0f), all = make_float2(1.0f, 1.0f);
+  float2 k[S], R = none, H = none, h;
+  int form = n < S ? kCareful : kMarks && resets != 0 ? kResets : kPlain;
+  auto first = [&](auto how) {
+    R = H = none;
+#pragma unroll
+    for (int i = 0; i < S; ++i) {
+      const float2 f = read_pair<T, LPR, CH == 16>(sf, i, col);
+      float2 c = read_pair<T, LPR, CH == 16>(sc, i, col);
+      k[i] = how.value < kCareful || i < n ? take2(f) : none;
+      if (how.value >= kResets && (resets >> i & 1)) {
+        R = all;
+        H = none;
+      }
+      if (how.value == kCareful) c = masked2(k[i], c);
+      R = join2(R, k[i]);
+      H = step2(H, k[i], c);
+    }
+  };
+  if (form == kPlain)
+    first(std::integral_constant<int, kPlain>());
+  else if (kMarks && form == kResets)
+    first(std::integral_constant<int, kResets>());
+  if (!(fabsf(H.x) + fabsf(H.y) < __int_as_float(0x7f800000))) form = kCareful;
+  if (form == kCareful) first(std::integral_constant<int, kCareful>());
+  h = exchange<LPR, false>(maps, cta_maps, round, size, rank, waits, R, H, carry);
+  auto second_pass = [&](auto how) {
+#pragma unroll
+    for (int i = 0; i < S; ++i, o += ldh) {
+      float2 c = read_pair<T, LPR, CH == 16>(sc, i, col);
+      if (how.value >= kResets && (resets >> i & 1)) h = none;
+      if (how.value == kCareful) c = masked2(k[i], c);
+      h = step2(h, k[i], c);
+      if (live && (how.value < kCareful || i < n)) write_pair<T, LPR, CH == 16>(o, h, second);
+    }
+  };
+  if (form == kPlain)
+    second_pass(std::integral_constant<int, kPlain>());
+  else if (kMarks && form == kResets)
+    second_pass(std::integral_constant<int, kResets>());
+  else
+    second_pass(std::integral_constant<int, kCareful>());
+}
+
 // CH: bytes a copy (16: rows of whole 16-byte pieces, outputs on pairs).  kMarks:
 // there are resets (looking whether there are costs a call without them 1 to 4 %).  A launch
 // without a cluster (size 1) executes no cluster instruction.
@@ -466,56 +526,9 @@ __global__ void __launch_bounds__(32 * kWarps, kPerSm) scan_fwd_kernel(const Fwd
     __syncwarp();
     const uint32_t resets = kMarks ? __ballot_sync(0xffffffffu, mark != 0) >> (group * S) : 0u;
     mark = next_mark;
-    const uint8_t* sf = stages[phase].a[0] + group * (S * Stage::kRow + Stage::kSkip);
-    const uint8_t* sc = stages[phase].a[1] + group * (S * Stage::kRow + Stage::kSkip);
     const int64_t t0 = base + mine + group * S;
-    const int n = p.length - t0 < S ? static_cast<int>(p.length - t0) : S;  // steps here (may be negative)
-    // A run is plain, or has resets; one that reaches past the sequence's end, or has masked
-    // tokens (k = 0) whose candidate is not finite, which would show in H, takes the
-    // careful form.
-    const float2 none = make_float2(0.0f, 0.0f), all = make_float2(1.0f, 1.0f);
-    float2 k[S], R = none, H = none, h;
-    int form = n < S ? kCareful : kMarks && resets != 0 ? kResets : kPlain;
-    auto first = [&](auto how) {
-      R = H = none;
-#pragma unroll
-      for (int i = 0; i < S; ++i) {
-        const float2 f = read_pair<T, LPR, CH == 16>(sf, i, col);
-        float2 c = read_pair<T, LPR, CH == 16>(sc, i, col);
-        k[i] = how.value < kCareful || i < n ? take2(f) : none;
-        if (how.value >= kResets && (resets >> i & 1)) {
-          R = all;
-          H = none;
-        }
-        if (how.value == kCareful) c = masked2(k[i], c);
-        R = join2(R, k[i]);
-        H = step2(H, k[i], c);
-      }
-    };
-    if (form == kPlain)
-      first(std::integral_constant<int, kPlain>());
-    else if (kMarks && form == kResets)
-      first(std::integral_constant<int, kResets>());
-    if (!(fabsf(H.x) + fabsf(H.y) < __int_as_float(0x7f800000))) form = kCareful;
-    if (form == kCareful) first(std::integral_constant<int, kCareful>());
-    h = exchange<LPR, false>(maps, cta_maps, round, size, rank, waits, R, H, carry);
-    T* o = out + t0 * p.ldh;
-    auto second_pass = [&](auto how) {
-#pragma unroll
-      for (int i = 0; i < S; ++i, o += p.ldh) {
-        float2 c = read_pair<T, LPR, CH == 16>(sc, i, col);
-        if (how.value >= kResets && (resets >> i & 1)) h = none;
-        if (how.value == kCareful) c = masked2(k[i], c);
-        h = step2(h, k[i], c);
-        if (live && (how.value < kCareful || i < n)) write_pair<T, LPR, CH == 16>(o, h, second);
-      }
-    };
-    if (form == kPlain)
-      second_pass(std::integral_constant<int, kPlain>());
-    else if (kMarks && form == kResets)
-      second_pass(std::integral_constant<int, kResets>());
-    else
-      second_pass(std::integral_constant<int, kCareful>());
+    forward_round<T, LPR, S, CH, kMarks>(stages[phase], t0, p.length, resets, out + t0 * p.ldh, p.ldh, live, second,
+                                         maps, cta_maps, round, size, rank, waits, carry);
     __syncwarp();  // this stage is read: the next round copies into it
   }
   copy_wait<0>();
@@ -525,6 +538,145 @@ __global__ void __launch_bounds__(32 * kWarps, kPerSm) scan_fwd_kernel(const Fwd
     p.h_last[b * p.width + ch] = carry[0];
     if (second) p.h_last[b * p.width + ch + kNext] = carry[1];
   }
+}
+
+// What a CTA works through: tiles `last` down to `first`, in rounds of a tile's
+// [0, rounds), where the last ends in front of round `to` and the first begins
+// with round `from`.
+struct Work {
+  int64_t first, last;
+  int from, to, rounds;
+};
+
+__device__ __forceinline__ Work work_of(int64_t tiles, int64_t length, int64_t span, int size, int rank) {
+  Work w;
+  w.rounds = static_cast<int>((length + span - 1) / span);
+  const int64_t cluster = blockIdx.x / size, clusters = gridDim.x / size;
+  const int64_t t0 = tiles * cluster / clusters, n = (tiles * (cluster + 1) / clusters - t0) * w.rounds;
+  const int64_t u0 = n * rank / size, u1 = n * (rank + 1) / size;
+  w.first = t0 + u0 / w.rounds;
+  w.last = t0 + (u1 - 1) / w.rounds;
+  w.from = static_cast<int>(u0 % w.rounds);
+  w.to = static_cast<int>((u1 - 1) % w.rounds) + 1;
+  return w;
+}
+
+// The state at the end of a CTA's first piece to the CTA behind it, and at the
+// beginning of its last piece from the one in front; warp 0, each lane its channels.
+template <int LPR>
+__device__ __forceinline__ void send_state(Maps<LPR>& m, float4* slots, int rank, const float (&carry)[2]) {
+  const int col = (threadIdx.x & 31) % LPR;
+  st_async_v4(peer(slots + col, rank + 1), __float_as_uint(carry[0]), __float_as_uint(carry[1]), 0u, 0u,
+              peer(&m.full[0], rank + 1));
+}
+template <int LPR>
+__device__ __forceinline__ void receive_state(Maps<LPR>& m, const float4* slots, Waits& waits, float (&carry)[2]) {
+  if ((threadIdx.x & 31) == 0) mbar_arrive_expect_tx(&m.full[0], LPR * 16);
+  __syncwarp();
+  wait_peers(&m.full[0], 0, waits);
+  const float4 v = slots[(threadIdx.x & 31) % LPR];
+  carry[0] = v.x;
+  carry[1] = v.y;
+}
+
+// For many tiles: a cluster takes consecutive tiles, at least as many as it has CTAs, and
+// each of its CTAs an equal part of all their rounds: the end of one tile, whole ones, the
+// beginning of another.  The beginning comes first, and its state travels once to
+// the next CTA, which needs it at its own end only: nobody waits, there is no
+// exchange in between, and no last wave in which most of the GPU idles (8 x 2048 x
+// 2560: 42.6 us, against 53.9 with a CTA a tile).  The backward, nearer to its limit of
+// instructions, loses by it (8 x 2048 x 3456: 131 us, against 108).
+template <class T, int S, bool kMarks>
+__global__ void __launch_bounds__(32 * kWarps, kPerSm) scan_fwd_shared_kernel(const FwdArgs p) {
+  constexpr int kLanes = 32;  // tiles of 64 channels, whole 16-byte pieces
+  using Stage = Slab<T, kLanes, S, 2>;
+  extern __shared__ __align__(16) uint8_t smem[];
+  __shared__ Maps<kLanes> maps;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int size = static_cast<int>(cluster_size()), rank = static_cast<int>(cluster_rank());
+  Stage* stages = reinterpret_cast<Stage*>(smem) + warp * 2;  // this warp's
+  float4* slots = reinterpret_cast<float4*>(smem + 2 * kWarps * sizeof(Stage));
+  constexpr int64_t span = kWarps * Stage::kRows;
+  const int64_t mine = warp * Stage::kRows;  // this warp's rows in a span
+  const Work w = work_of(p.all_tiles, p.length, span, size, rank);
+  int64_t b, ch0;  // of the tile
+  auto issue = [&](int64_t b, int64_t ch0, int64_t base, int st) {
+    const int64_t row0 = b * p.length;
+    load_rows<T, kLanes, S, 16>(stages[st].a[0], static_cast<const T*>(p.gate) + row0 * p.ldg + ch0, p.ldg, base + mine,
+                             p.length, ch0, p.width, lane);
+    load_rows<T, kLanes, S, 16>(stages[st].a[1], static_cast<const T*>(p.cand) + row0 * p.ldc + ch0, p.ldc, base + mine,
+                             p.length, ch0, p.width, lane);
+    copy_commit();
+  };
+  auto mark_of = [&](int64_t b, int64_t base) {
+    return kMarks ? reset_mark(p.resets, b * p.length, base + mine, p.length, Stage::kRows, lane) : 0u;
+  };
+  launch_dependents();
+  grid_dependency_wait();
+  int64_t tile = w.last;
+  b = tile / p.tiles;
+  ch0 = (tile - b * p.tiles) * (2 * kLanes);
+  int r = w.first == w.last ? w.from : 0, end = w.to;
+  uint32_t mark = mark_of(b, r * span);
+  issue(b, ch0, r * span, 0);
+  open_maps(maps);
+  Waits waits{p.err, &maps.aborted, false};
+  float carry[2] = {};
+  int round = 0;  // of all
+  for (;;) {  // a piece of a tile
+    const int64_t ch = ch0 + 2 * lane;
+    const bool live = ch < p.width, second = ch + 1 < p.width;
+    T* out = static_cast<T*>(p.h) + b * p.length * p.ldh + ch;
+    carry[0] = carry[1] = 0.0f;
+    if (r > 0) {
+      if (warp == 0) receive_state(maps, slots, waits, carry);
+    } else if (p.h0 && live) {  // plain loads: h_last may be the same array
+      carry[0] = p.h0[b * p.width + ch];
+      if (second) carry[1] = p.h0[b * p.width + ch + 1];
+    }
+    int64_t next_b = b, next_ch0 = ch0;
+    for (; r < end; ++r, ++round) {
+      const int phase = round & 1;
+      const int64_t base = r * span;
+      uint32_t next_mark = 0;
+      if (r + 1 < end) {
+        next_mark = mark_of(b, base + span);
+        issue(b, ch0, base + span, phase ^ 1);
+      } else if (tile != w.first) {
+        const bool first_of = ch0 == 0;  // of the sequence's tiles
+        next_b = first_of ? b - 1 : b;
+        next_ch0 = first_of ? (p.tiles - 1) * (2 * kLanes) : ch0 - 2 * kLanes;
+        const int64_t next = (tile - 1 == w.first ? w.from : 0) * span;
+        next_mark = mark_of(next_b, next);
+        issue(next_b, next_ch0, next, phase ^ 1);
+      } else {
+        copy_commit();  // an empty group, so that waiting for all but one still means this stage
+      }
+      copy_wait<1>();
+      __syncwarp();
+      const uint32_t resets = kMarks ? __ballot_sync(0xffffffffu, mark != 0) : 0u;
+      mark = next_mark;
+      const int64_t t0 = base + mine;
+      forward_round<T, kLanes, S, 16, kMarks>(stages[phase], t0, p.length, resets, out + t0 * p.ldh, p.ldh, live, second,
+                                              maps, slots, round, 1, rank, waits, carry);
+      __syncwarp();  // this stage is read: the next round copies into it
+    }
+    if (end < w.rounds) {
+      if (warp == 0) send_state(maps, slots, rank, carry);
+    } else if (p.h_last && live && warp == 0) {
+      // the carried state is past the last step, and h0 has been read
+      p.h_last[b * p.width + ch] = carry[0];
+      if (second) p.h_last[b * p.width + ch + 1] = carry[1];
+    }
+    if (tile == w.first) break;
+    --tile;
+    b = next_b;
+    ch0 = next_ch0;
+    r = tile == w.first ? w.from : 0;
+    end = w.rounds;
+  }
+  copy_wait<0>();
+  cluster_meet();  // nothing is on its way to a CTA that has left
 }
 
 // A few tokens per sequence: a thread takes CPL channels through all of them.
@@ -569,64 +721,70 @@ __global__ void __launch_bounds__(32 * kWarps, kPerSm) scan_bwd_kernel(const Bwd
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int col = lane % LPR, group = lane / LPR;
   const int size = static_cast<int>(cluster_size()), rank = static_cast<int>(cluster_rank());
-  const int64_t tile = blockIdx.x / size;
-  const int64_t b = tile / p.tiles, ch0 = (tile - b * p.tiles) * (2 * LPR), ch = ch0 + first_channel<LPR, CH == 16>(col);
   constexpr int kNext = kApart<LPR, CH == 16>;  // to the lane's second channel
-  const bool live = ch < p.width, second = ch + kNext < p.width;
-  const int64_t row0 = b * p.length;
-  const T* gate = static_cast<const T*>(p.gate) + row0 * p.ldg + ch0;
-  const T* cand = static_cast<const T*>(p.cand) + row0 * p.ldc + ch0;
-  const T* hs = static_cast<const T*>(p.h) + row0 * p.ldh + ch0;
-  const T* dh = static_cast<const T*>(p.dh) + row0 * p.lddh + ch0;
-  T* dgate = static_cast<T*>(p.dgate) + row0 * p.lddg + ch;
-  T* dcand = static_cast<T*>(p.dcand) + row0 * p.lddc + ch;
   Stage* stages = reinterpret_cast<Stage*>(smem) + warp * 2;
   float4* cta_maps = reinterpret_cast<float4*>(smem + 2 * kWarps * sizeof(Stage));
-  float carry[2] = {}, start[2] = {};
-  launch_dependents();
-  grid_dependency_wait();
   const int64_t span = static_cast<int64_t>(size) * kWarps * Stage::kRows;
   const int64_t mine = (rank * kWarps + warp) * Stage::kRows;
+  const int rounds = static_cast<int>((p.length + span - 1) / span);
+  const int64_t tile = blockIdx.x / size;
+  const int64_t b = tile / p.tiles, ch0 = (tile - b * p.tiles) * (2 * LPR), ch = ch0 + first_channel<LPR, CH == 16>(col);
+  const bool live = ch < p.width, second = ch + kNext < p.width;
   auto issue = [&](int64_t base, int st) {  // rows in front of the sequence: zeros
-    const int64_t t = base + mine;
-    load_rows<T, LPR, S, CH>(stages[st].a[0], gate, p.ldg, t, p.length, ch0, p.width, lane);
-    load_rows<T, LPR, S, CH>(stages[st].a[1], cand, p.ldc, t, p.length, ch0, p.width, lane);
-    load_rows<T, LPR, S, CH>(stages[st].a[2], dh, p.lddh, t, p.length, ch0, p.width, lane);
-    load_rows<T, LPR, S, CH>(stages[st].a[3], hs, p.ldh, t - 1, p.length, ch0, p.width, lane);
+    const int64_t t = base + mine, row0 = b * p.length;
+    load_rows<T, LPR, S, CH>(stages[st].a[0], static_cast<const T*>(p.gate) + row0 * p.ldg + ch0, p.ldg, t, p.length,
+                             ch0, p.width, lane);
+    load_rows<T, LPR, S, CH>(stages[st].a[1], static_cast<const T*>(p.cand) + row0 * p.ldc + ch0, p.ldc, t, p.length,
+                             ch0, p.width, lane);
+    load_rows<T, LPR, S, CH>(stages[st].a[2], static_cast<const T*>(p.dh) + row0 * p.lddh + ch0, p.lddh, t, p.length,
+                             ch0, p.width, lane);
+    load_rows<T, LPR, S, CH>(stages[st].a[3], static_cast<const T*>(p.h) + row0 * p.ldh + ch0, p.ldh, t - 1, p.length,
+                             ch0, p.width, lane);
     copy_commit();
   };
-  const int64_t last = p.length > 0 ? (p.length - 1) / span * span : 0;
-  issue(last, 0);
-  uint32_t mark = kMarks ? reset_mark(p.resets, row0, last + mine, p.length, Stage::kRows, lane) : 0u;
-  if (live) {
-    const int64_t at = b * p.width + ch;
-    if (p.dh_last) {
-      carry[0] = p.dh_last[at];
-      if (second) carry[1] = p.dh_last[at + kNext];
-    }
-    if (p.h0) {
-      start[0] = p.h0[at];
-      if (second) start[1] = p.h0[at + kNext];
-    }
+  auto mark_of = [&](int64_t base) {
+    return kMarks ? reset_mark(p.resets, b * p.length, base + mine, p.length, Stage::kRows, lane) : 0u;
+  };
+  launch_dependents();
+  grid_dependency_wait();
+  const int64_t last = (rounds - 1) * span;  // round r is the r-th from the sequence's end
+  uint32_t mark = 0;
+  if (rounds > 0) {
+    mark = mark_of(last);
+    issue(last, 0);
   }
   if (size > 1) open_maps(maps);
   Waits waits{p.err, &maps.aborted, false};
-  int round = 0;
-  for (int64_t base = last; base >= 0; base -= span, ++round) {
+  T* dgate = static_cast<T*>(p.dgate) + b * p.length * p.lddg + ch;
+  T* dcand = static_cast<T*>(p.dcand) + b * p.length * p.lddc + ch;
+  float carry[2] = {}, start[2] = {};
+  if (live) {
+    if (p.dh_last) {
+      carry[0] = p.dh_last[b * p.width + ch];
+      if (second) carry[1] = p.dh_last[b * p.width + ch + kNext];
+    }
+    if (p.h0) {
+      start[0] = p.h0[b * p.width + ch];
+      if (second) start[1] = p.h0[b * p.width + ch + kNext];
+    }
+  }
+  for (int round = 0; round < rounds; ++round) {
     const int phase = round & 1;
-    const uint32_t next_mark =
-        kMarks && base > 0 ? reset_mark(p.resets, row0, base - span + mine, p.length, Stage::kRows, lane) : 0u;
-    if (base > 0)
+    const int64_t base = last - round * span;
+    uint32_t next_mark = 0;
+    if (round + 1 < rounds) {
+      next_mark = mark_of(base - span);
       issue(base - span, phase ^ 1);
-    else
+    } else {
       copy_commit();  // an empty group, so that waiting for all but one still means this stage
+    }
     copy_wait<1>();
     __syncwarp();
     const uint32_t resets = kMarks ? __ballot_sync(0xffffffffu, mark != 0) >> (group * S) : 0u;
     mark = next_mark;
+    const int64_t t0 = base + mine + group * S;
     const Stage& st = stages[phase];
     const int at = group * (S * Stage::kRow + Stage::kSkip);
-    const int64_t t0 = base + mine + group * S;
     const int n = p.length - t0 < S ? static_cast<int>(p.length - t0) : S;
     const float2 none = make_float2(0.0f, 0.0f), all = make_float2(1.0f, 1.0f);
     float2 k[S], slope[S], R = none, Q = none, v;
@@ -744,6 +902,7 @@ constexpr double kNarrowGain = 1.2;
 struct Plan {
   int cluster;
   double cost;
+  int64_t clusters = 0;  // shared tiles: how many there are
 };
 
 template <auto Fn>
@@ -762,6 +921,20 @@ Plan plan(int64_t tiles, int64_t length, int rows, int smem, int per_cta) {
   return best;
 }
 
+// The same for shared tiles, each of whose CTAs has its part of the cluster's rounds.
+template <auto Fn>
+Plan plan_shared(int64_t tiles, int64_t length, int rows, int smem, int per_cta) {
+  Plan best{0, 0.0};
+  const int64_t rounds = (length + rows - 1) / rows;
+  for (int c = 2; c <= kMaxCluster; ++c) {
+    const int64_t n = std::min<int64_t>(max_clusters<Fn>(c, smem + c * per_cta), tiles / c);
+    if (n < 1) continue;
+    const double cost = static_cast<double>((tiles + n - 1) / n) * rounds / c;
+    if (best.cluster == 0 || cost < best.cost) best = {c, cost, n};
+  }
+  return best;
+}
+
 template <class T, int CH, bool kMarks>
 struct Fwd {
   template <int LPR> struct Kernel;
@@ -773,6 +946,8 @@ struct Bwd {
 template <class T, int CH, bool kMarks>
 template <int LPR>
 struct Fwd<T, CH, kMarks>::Kernel {
+  using Type = T;
+  static constexpr bool marks = kMarks;
   static constexpr int S = kFwdSteps<T>, rows = kWarps * (32 / LPR) * S;
   static constexpr int smem = 2 * kWarps * sizeof(Slab<T, LPR, S, 2>), per_cta = 2 * LPR * sizeof(float4);
   static constexpr auto fn = scan_fwd_kernel<T, LPR, S, CH, kMarks>;
@@ -794,7 +969,7 @@ int run_plan(Args p, int64_t batch, int cluster, cudaStream_t s) {
 
 // Tiles of 64 channels, or of 32 where that is estimated to be faster: few
 // channels leave the GPU short of CTAs.
-template <template <int> class K, class Args>
+template <template <int> class K, bool kTryShared, class Args>
 int run(const Args& p, int64_t batch, cudaStream_t s) {
   using Wide = K<32>;
   using Narrow = K<16>;
@@ -804,6 +979,17 @@ int run(const Args& p, int64_t batch, cudaStream_t s) {
   const Plan w = plan<Wide::fn>(batch * ((p.width + 63) / 64), p.length, Wide::rows, Wide::smem, Wide::per_cta);
   const Plan n = plan<Narrow::fn>(batch * ((p.width + 31) / 32), p.length, Narrow::rows, Narrow::smem, Narrow::per_cta);
   if (w.cluster == 0 && n.cluster == 0) return T3_ECUDA;
+  if constexpr (kTryShared) {
+    constexpr auto fn = scan_fwd_shared_kernel<typename Wide::Type, Wide::S, Wide::marks>;
+    st = allow_smem<fn>(Wide::smem + kMaxCluster * Wide::per_cta);
+    if (st != T3_OK) return st;
+    Args q = p;
+    q.tiles = (p.width + 63) / 64;
+    q.all_tiles = batch * q.tiles;
+    const Plan h = plan_shared<fn>(q.all_tiles, p.length, Wide::rows, Wide::smem, Wide::per_cta);
+    if (h.cluster > 0 && h.cost < std::min(w.cost, n.cost * kNarrowGain))
+      return launch(fn, h.clusters * h.cluster, 32 * kWarps, Wide::smem + h.cluster * Wide::per_cta, s, h.cluster, q);
+  }
   if (n.cluster == 0 || (w.cluster > 0 && w.cost <= kNarrowGain * n.cost)) return run_plan<Wide, 32>(p, batch, w.cluster, s);
   return run_plan<Narrow, 16>(p, batch, n.cluster, s);
 }
@@ -815,13 +1001,13 @@ int run_rows(const Args& p, int64_t batch, int ch, cudaStream_t s) {
   constexpr bool kFwd = std::is_same_v<Args, FwdArgs>;
   constexpr int kOdd = sizeof(T) == 4 ? 4 : 2;
   if constexpr (kFwd) {
-    if (ch == 16) return run<Fwd<T, 16, kMarks>::template Kernel>(p, batch, s);
-    if (ch == 4) return run<Fwd<T, 4, kMarks>::template Kernel>(p, batch, s);
-    return run<Fwd<T, kOdd, kMarks>::template Kernel>(p, batch, s);
+    if (ch == 16) return run<Fwd<T, 16, kMarks>::template Kernel, true>(p, batch, s);
+    if (ch == 4) return run<Fwd<T, 4, kMarks>::template Kernel, false>(p, batch, s);
+    return run<Fwd<T, kOdd, kMarks>::template Kernel, false>(p, batch, s);
   } else {
-    if (ch == 16) return run<Bwd<T, 16, kMarks>::template Kernel>(p, batch, s);
-    if (ch == 4) return run<Bwd<T, 4, kMarks>::template Kernel>(p, batch, s);
-    return run<Bwd<T, kOdd, kMarks>::template Kernel>(p, batch, s);
+    if (ch == 16) return run<Bwd<T, 16, kMarks>::template Kernel, false>(p, batch, s);
+    if (ch == 4) return run<Bwd<T, 4, kMarks>::template Kernel, false>(p, batch, s);
+    return run<Bwd<T, kOdd, kMarks>::template Kernel, false>(p, batch, s);
   }
 }
 
@@ -843,7 +1029,7 @@ bool rows_on(const void* p, int64_t ld, int64_t width, int es, int bytes) {
 int launch_scan_fwd(const void* gate, int64_t ldg, const void* cand, int64_t ldc, const float* h0,
                     const uint8_t* resets, void* h, int64_t ldh, float* h_last, int64_t batch,
                     int64_t length, int64_t width, int dtype, int* err, cudaStream_t s) {
-  const sc::FwdArgs p{gate, cand, ldg, ldc, ldh, h0, resets, h, h_last, length, width, 0, batch * width, err};
+  const sc::FwdArgs p{gate, cand, ldg, ldc, ldh, h0, resets, h, h_last, length, width, 0, 0, batch * width, err};
   const int es = dtype == T3_OUT_BF16 ? 2 : 4;
   auto on = [&](int n) { return sc::rows_on(gate, ldg, width, es, n) && sc::rows_on(cand, ldc, width, es, n); };
   const bool pair = sc::rows_on(h, ldh, width, es, 2 * es);

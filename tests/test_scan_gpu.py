@@ -91,6 +91,22 @@ def test_backward(b, t, d, dname):
     _check_backward(gate, cand, h, dh, None, None, None, t3.t3_gated_scan_bwd(gate, cand, h, dh), dname)
 
 
+# more tiles than are resident at once: CTAs take parts of several, whose states travel between them
+@pytest.mark.parametrize("dname", ["bf16", "f32"])
+@pytest.mark.parametrize("b,t,d", [(13, 210, 2056), (20, 600, 1024), (5, 500, 4104), (41, 129, 520)])
+def test_many_tiles(b, t, d, dname):
+    gate, cand, h0, r, dh, dl = _make(b * t, b, t, d, dname, fused=True, resets=True)
+    state = h0.clone()
+    got = t3.t3_gated_scan_fwd(gate, cand, state, r, h_last=state)
+    _check_forward(gate, cand, h0, r, got, dname)
+    _check_backward(gate, cand, got[0], dh, h0, r, dl, t3.t3_gated_scan_bwd(gate, cand, got[0], dh, h0, r, dl), dname)
+    got = t3.t3_gated_scan_fwd(gate, cand)
+    _check_forward(gate, cand, None, None, got, dname)
+    _check_backward(gate, cand, got[0], dh, None, None, None, t3.t3_gated_scan_bwd(gate, cand, got[0], dh), dname)
+    rc, detail = t3.t3_last_device_error()
+    assert rc == t3.T3_OK, hex(detail)
+
+
 def test_backward_against_differences_of_the_kernel():
     """Directional differences of the forward kernel itself.  loss is linear in
     the outputs; a central difference with step 2e-2 truncates at 1e-4 of the
