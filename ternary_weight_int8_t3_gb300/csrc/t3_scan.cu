@@ -377,17 +377,17 @@ __device__ __forceinline__ void load_rows(uint8_t* slab, const T* base, int64_t 
   }
 }
 
-// A lane's two channels of a tile: neighbours where rows are 16-byte pieces
-// (one access for both), else `col` and `col + LPR`, so that each access of a
-// warp covers neighbouring elements.
-template <int LPR, bool kPair> __device__ __forceinline__ int first_channel(int col) { return kPair ? 2 * col : col; }
-template <int LPR, bool kPair> constexpr int kApart = kPair ? 1 : LPR;
+// A lane's two channels of a tile: neighbours where one access takes both, else
+// `col` and `col + LPR`, so that each access of a warp covers neighbouring elements.
+template <class T, int CH> constexpr bool kPair = CH >= 2 * static_cast<int>(sizeof(T));
+template <int LPR, bool kTwo> __device__ __forceinline__ int first_channel(int col) { return kTwo ? 2 * col : col; }
+template <int LPR, bool kTwo> constexpr int kApart = kTwo ? 1 : LPR;
 
 // This lane's pair of a row; `slab` is where its group's rows begin.
-template <class T, int LPR, bool kPair>
+template <class T, int LPR, bool kTwo>
 __device__ __forceinline__ float2 read_pair(const uint8_t* slab, int row, int col) {
   const T* p = reinterpret_cast<const T*>(slab) + row * (2 * LPR);
-  if constexpr (kPair) {
+  if constexpr (kTwo) {
     float f[2];
     to_float(load<T, 2>(p + 2 * col), f);
     return make_float2(f[0], f[1]);
@@ -400,9 +400,9 @@ __device__ __forceinline__ float2 read_pair(const uint8_t* slab, int row, int co
 }
 
 // The pair to memory, p at its first channel.
-template <class T, int LPR, bool kPair>
+template <class T, int LPR, bool kTwo>
 __device__ __forceinline__ void write_pair(T* p, float2 v, bool second) {
-  if constexpr (kPair) {
+  if constexpr (kTwo) {
     const float f[2] = {v.x, v.y};
     store<T, 2>(p, from_float(f, T()));
   } else {
@@ -438,8 +438,8 @@ __device__ __forceinline__ void forward_round(const Slab<T, LPR, S, 2>& stage, i
     R = H = none;
 #pragma unroll
     for (int i = 0; i < S; ++i) {
-      const float2 f = read_pair<T, LPR, CH == 16>(sf, i, col);
-      float2 c = read_pair<T, LPR, CH == 16>(sc, i, col);
+      const float2 f = read_pair<T, LPR, kPair<T, CH>>(sf, i, col);
+      float2 c = read_pair<T, LPR, kPair<T, CH>>(sc, i, col);
       k[i] = how.value < kCareful || i < n ? take2(f) : none;
       if (how.value >= kResets && (resets >> i & 1)) {
         R = all;
@@ -460,11 +460,11 @@ __device__ __forceinline__ void forward_round(const Slab<T, LPR, S, 2>& stage, i
   auto second_pass = [&](auto how) {
 #pragma unroll
     for (int i = 0; i < S; ++i, o += ldh) {
-      float2 c = read_pair<T, LPR, CH == 16>(sc, i, col);
+      float2 c = read_pair<T, LPR, kPair<T, CH>>(sc, i, col);
       if (how.value >= kResets && (resets >> i & 1)) h = none;
       if (how.value == kCareful) c = masked2(k[i], c);
       h = step2(h, k[i], c);
-      if (live && (how.value < kCareful || i < n)) write_pair<T, LPR, CH == 16>(o, h, second);
+      if (live && (how.value < kCareful || i < n)) write_pair<T, LPR, kPair<T, CH>>(o, h, second);
     }
   };
   if (form == kPlain)
@@ -487,8 +487,8 @@ __global__ void __launch_bounds__(32 * kWarps, kPerSm) scan_fwd_kernel(const Fwd
   const int col = lane % LPR, group = lane / LPR;
   const int size = static_cast<int>(cluster_size()), rank = static_cast<int>(cluster_rank());
   const int64_t tile = blockIdx.x / size;
-  const int64_t b = tile / p.tiles, ch0 = (tile - b * p.tiles) * (2 * LPR), ch = ch0 + first_channel<LPR, CH == 16>(col);
-  constexpr int kNext = kApart<LPR, CH == 16>;  // to the lane's second channel
+  const int64_t b = tile / p.tiles, ch0 = (tile - b * p.tiles) * (2 * LPR), ch = ch0 + first_channel<LPR, kPair<T, CH>>(col);
+  constexpr int kNext = kApart<LPR, kPair<T, CH>>;  // to the lane's second channel
   const bool live = ch < p.width, second = ch + kNext < p.width;
   const T* gate = static_cast<const T*>(p.gate) + b * p.length * p.ldg + ch0;
   const T* cand = static_cast<const T*>(p.cand) + b * p.length * p.ldc + ch0;
@@ -721,14 +721,14 @@ __global__ void __launch_bounds__(32 * kWarps, kPerSm) scan_bwd_kernel(const Bwd
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int col = lane % LPR, group = lane / LPR;
   const int size = static_cast<int>(cluster_size()), rank = static_cast<int>(cluster_rank());
-  constexpr int kNext = kApart<LPR, CH == 16>;  // to the lane's second channel
+  constexpr int kNext = kApart<LPR, kPair<T, CH>>;  // to the lane's second channel
   Stage* stages = reinterpret_cast<Stage*>(smem) + warp * 2;
   float4* cta_maps = reinterpret_cast<float4*>(smem + 2 * kWarps * sizeof(Stage));
   const int64_t span = static_cast<int64_t>(size) * kWarps * Stage::kRows;
   const int64_t mine = (rank * kWarps + warp) * Stage::kRows;
   const int rounds = static_cast<int>((p.length + span - 1) / span);
   const int64_t tile = blockIdx.x / size;
-  const int64_t b = tile / p.tiles, ch0 = (tile - b * p.tiles) * (2 * LPR), ch = ch0 + first_channel<LPR, CH == 16>(col);
+  const int64_t b = tile / p.tiles, ch0 = (tile - b * p.tiles) * (2 * LPR), ch = ch0 + first_channel<LPR, kPair<T, CH>>(col);
   const bool live = ch < p.width, second = ch + kNext < p.width;
   auto issue = [&](int64_t base, int st) {  // rows in front of the sequence: zeros
     const int64_t t = base + mine, row0 = b * p.length;
@@ -793,9 +793,9 @@ __global__ void __launch_bounds__(32 * kWarps, kPerSm) scan_bwd_kernel(const Bwd
     auto fold = [&](auto how) {
 #pragma unroll
       for (int i = S - 1; i >= 0; --i) {
-        k[i] = take2(read_pair<T, LPR, CH == 16>(st.a[0] + at, i, col), slope[i]);
+        k[i] = take2(read_pair<T, LPR, kPair<T, CH>>(st.a[0] + at, i, col), slope[i]);
         if (how.value == kCareful && i >= n) k[i] = none;
-        const float2 g = __fadd2_rn(read_pair<T, LPR, CH == 16>(st.a[2] + at, i, col), Q);
+        const float2 g = __fadd2_rn(read_pair<T, LPR, kPair<T, CH>>(st.a[2] + at, i, col), Q);
         R = join2(R, k[i]);
         Q = sub2(g, __fmul2_rn(k[i], g));
         if (how.value >= kResets && (resets >> i & 1)) {
@@ -816,18 +816,18 @@ __global__ void __launch_bounds__(32 * kWarps, kPerSm) scan_bwd_kernel(const Bwd
       T* oc = dcand + (t0 + S - 1) * p.lddc;
 #pragma unroll
       for (int i = S - 1; i >= 0; --i, og -= p.lddg, oc -= p.lddc) {
-        const float2 g = __fadd2_rn(read_pair<T, LPR, CH == 16>(st.a[2] + at, i, col), v);
-        float2 before = read_pair<T, LPR, CH == 16>(st.a[3] + at, i, col);
+        const float2 g = __fadd2_rn(read_pair<T, LPR, kPair<T, CH>>(st.a[2] + at, i, col), v);
+        float2 before = read_pair<T, LPR, kPair<T, CH>>(st.a[3] + at, i, col);
         const bool reset = how.value >= kResets && (resets >> i & 1);
         if (how.value == kCareful && t0 + i == 0) before = make_float2(start[0], start[1]);
         if (reset) before = none;
         const float2 dc = __fmul2_rn(k[i], g);
-        const float2 diff = sub2(before, read_pair<T, LPR, CH == 16>(st.a[1] + at, i, col));
+        const float2 diff = sub2(before, read_pair<T, LPR, kPair<T, CH>>(st.a[1] + at, i, col));
         const float2 df = masked2(slope[i], __fmul2_rn(__fmul2_rn(g, slope[i]), diff));
         v = reset ? none : sub2(g, dc);
         if (live && (how.value < kCareful || i < n)) {
-          write_pair<T, LPR, CH == 16>(og, df, second);
-          write_pair<T, LPR, CH == 16>(oc, dc, second);
+          write_pair<T, LPR, kPair<T, CH>>(og, df, second);
+          write_pair<T, LPR, kPair<T, CH>>(oc, dc, second);
         }
       }
     };
@@ -892,8 +892,9 @@ int max_clusters(int c, size_t smem) {
 }
 
 // Rows of 32 channels fetch half as much with each access: they have to win by
-// this factor.
-constexpr double kNarrowGain = 1.2;
+// this factor (estimated at 1.18 to 1.2 they take 94 us for 102 in 8 x 2048 x 2560
+// backward, at 1.17 112 for 108 in 8 x 2048 x 3456).
+constexpr double kNarrowGain = 1.175;
 
 // A launch: CTAs a cluster, and its estimated time in rounds of one CTA.  All
 // clusters of a wave walk their sequences side by side, `rows` steps a CTA and
@@ -1041,7 +1042,7 @@ int launch_scan_fwd(const void* gate, int64_t ldg, const void* cand, int64_t ldc
                   : (two ? sc::scan_fwd_short_kernel<float, 2> : sc::scan_fwd_short_kernel<float, 1>);
     return vec::launch(fn, (n + 127) / 128, 128, 0, s, 1, p);
   }
-  const int ch = pair && on(16) ? 16 : on(4) ? 4 : 2;
+  const int ch = pair && on(16) ? 16 : (pair || es == 4) && on(4) ? 4 : 2;
   return sc::run_any(p, batch, ch, dtype, s);
 }
 
@@ -1058,7 +1059,7 @@ int launch_scan_bwd(const void* gate, int64_t ldg, const void* cand, int64_t ldc
            sc::rows_on(h, ldh, width, es, n) && sc::rows_on(dh, lddh, width, es, n);
   };
   const bool pair = sc::rows_on(dgate, lddg, width, es, 2 * es) && sc::rows_on(dcand, lddc, width, es, 2 * es);
-  const int ch = pair && on(16) ? 16 : on(4) ? 4 : 2;
+  const int ch = pair && on(16) ? 16 : (pair || es == 4) && on(4) ? 4 : 2;
   return sc::run_any(p, batch, ch, dtype, s);
 }
 
