@@ -40,6 +40,10 @@ using namespace vec;
 // elements a row forward (one float an element is kept) and 8192 backward (the
 // gain, the column sum and three operands), within 64 to 128 registers a thread.
 constexpr int fwd_threads(int ept) { return ept <= 16 ? 1024 : 16384 / ept; }
+// Columns from which vectors that begin inside a row pay (bf16, forward and
+// backward: 8000 x 1001 13.8 and 20.6 us, element by element 24.1 and 46.7; 16000 x 243
+// 11.0 and 12.7, 13.3 and 26.6).
+constexpr int64_t kOddCols = 64;
 constexpr int bwd_threads(int ept) { return ept <= 8 ? 1024 : 8192 / ept; }
 
 struct FwdArgs {
@@ -137,45 +141,83 @@ __device__ __forceinline__ float group_sum(float a, float* sm, int warp, int war
   return warp_sum(lane < warps ? sm[lane] : 0.0f);
 }
 
-template <class T, int VEC, int NV>
+// Rows that do not begin on 16-byte boundaries (kOdd): the vectors begin on the first
+// boundary in the row, and the few elements in front of them and behind them go one to
+// a thread.  A CTA's rows are a multiple of VEC apart in memory, so that a thread's columns
+// stay the same.
+template <class T, int VEC, bool kOdd>
+struct Columns {
+  int head = 0, end;  // the vectors' columns
+  int one = 0;        // this thread's single column
+  bool has = false;   // whether it has one
+  // a row begins `at` elements from p; `t` numbers the threads that share it
+  __device__ __forceinline__ Columns(const void* p, int64_t at, int cols, int t) : end(cols) {
+    if constexpr (kOdd) {
+      const uint64_t lead = (reinterpret_cast<uintptr_t>(p) / sizeof(T) + static_cast<uint64_t>(at)) % VEC;
+      head = min(static_cast<int>((VEC - lead) % VEC), cols);
+      end = head + (cols - head) / VEC * VEC;
+      one = t < head ? t : end + t - head;
+      has = one < cols;
+    }
+  }
+};
+
+template <class T, int VEC, int NV, bool kOdd>
 __global__ void __launch_bounds__(fwd_threads(NV * VEC)) norm_fwd_kernel(const FwdArgs p) {
   __shared__ float sm[2][64];
   const int lanes = blockDim.x, cols = static_cast<int>(p.cols);
+  const Columns<T, VEC, kOdd> at(p.x, blockIdx.x * p.ldx, cols, threadIdx.x);
   launch_dependents();
   grid_dependency_wait();
   // this thread's columns: their gains, and the next row's operands, which are on
   // their way while this row is reduced and written
   float g[NV][VEC];
+  float ge = 1.0f;
   Raw<T, VEC> xr[NV], rr[NV];
+  Raw<T, 1> xe = zero<T, 1>(), re = zero<T, 1>();
   auto fetch = [&](int64_t row) {
     const T* x = static_cast<const T*>(p.x) + row * p.ldx;
     const T* r = static_cast<const T*>(p.residual) + row * p.ldr;
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
-      const int k = (v * lanes + threadIdx.x) * VEC;
+      const int k = at.head + static_cast<int>(v * lanes + threadIdx.x) * VEC;
       xr[v] = zero<T, VEC>();
       rr[v] = zero<T, VEC>();
-      if (k < cols && row < p.rows) {
+      if (k < at.end && row < p.rows) {
         xr[v] = load<T, VEC>(x + k);
         if (p.residual) rr[v] = load<T, VEC>(r + k);
+      }
+    }
+    if constexpr (kOdd) {
+      if (at.has && row < p.rows) {
+        xe = load<T, 1>(x + at.one);
+        if (p.residual) re = load<T, 1>(r + at.one);
       }
     }
   };
   fetch(blockIdx.x);
 #pragma unroll
   for (int v = 0; v < NV; ++v) {
-    const int k = (v * lanes + threadIdx.x) * VEC;
+    const int k = at.head + static_cast<int>(v * lanes + threadIdx.x) * VEC;
 #pragma unroll
     for (int j = 0; j < VEC; ++j) g[v][j] = 1.0f;
-    if (p.gamma && k < cols) load_floats<VEC>(p.gamma + k, g[v]);
+    if (p.gamma && k < at.end) {
+      if constexpr (kOdd) {
+#pragma unroll
+        for (int j = 0; j < VEC; ++j) g[v][j] = __ldg(p.gamma + k + j);
+      } else {
+        load_floats<VEC>(p.gamma + k, g[v]);
+      }
+    }
   }
+  if (kOdd && p.gamma && at.has) ge = __ldg(p.gamma + at.one);
   int phase = 0;
   for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x, phase ^= 1) {
     T* so = static_cast<T*>(p.sum_out) + row * p.lds;
     float u[NV][VEC], ssq = 0.0f, amax = 0.0f;
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
-      const int k = (v * lanes + threadIdx.x) * VEC;
+      const int k = at.head + static_cast<int>(v * lanes + threadIdx.x) * VEC;
       float s[VEC], t[VEC];
       to_float(xr[v], s);
       if (p.residual) {
@@ -185,12 +227,29 @@ __global__ void __launch_bounds__(fwd_threads(NV * VEC)) norm_fwd_kernel(const F
       }
       const Raw<T, VEC> w = from_float(s, T());
       to_float(w, s);
-      if (p.sum_out && k < cols) store<T, VEC>(so + k, w);
+      if (p.sum_out && k < at.end) store<T, VEC>(so + k, w);
 #pragma unroll
       for (int j = 0; j < VEC; ++j) {
         ssq = fmaf(s[j], s[j], ssq);
         u[v][j] = __fmul_rn(s[j], g[v][j]);
         amax = max_nan(amax, fabsf(u[v][j]));
+      }
+    }
+    float ue = 0.0f;
+    if constexpr (kOdd) {
+      float se[1], te[1];
+      to_float(xe, se);
+      if (p.residual) {
+        to_float(re, te);
+        se[0] += te[0];
+      }
+      const Raw<T, 1> w = from_float(se, T());
+      to_float(w, se);
+      if (at.has) {
+        if (p.sum_out) store<T, 1>(so + at.one, w);
+        ssq = fmaf(se[0], se[0], ssq);
+        ue = __fmul_rn(se[0], ge);
+        amax = max_nan(amax, fabsf(ue));
       }
     }
     fetch(row + gridDim.x);
@@ -203,8 +262,8 @@ __global__ void __launch_bounds__(fwd_threads(NV * VEC)) norm_fwd_kernel(const F
     const bool plain = inv > 0.0f && inv < __int_as_float(0x7f800000);
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
-      const int k = (v * lanes + threadIdx.x) * VEC;
-      if (k >= cols) break;
+      const int k = at.head + static_cast<int>(v * lanes + threadIdx.x) * VEC;
+      if (k >= at.end) break;
       if constexpr (VEC == 1) {
         q[k] = static_cast<int8_t>(quant(u[v][0], inv));
       } else {
@@ -226,6 +285,7 @@ __global__ void __launch_bounds__(fwd_threads(NV * VEC)) norm_fwd_kernel(const F
           *reinterpret_cast<uint32_t*>(q + k) = w[0];
       }
     }
+    if (kOdd && at.has) q[at.one] = static_cast<int8_t>(quant(ue, inv));
   }
 }
 
@@ -303,7 +363,7 @@ __device__ __forceinline__ void add_floats(float* to, const float* from, bool ad
 }
 
 // kOne: the CTA is one group; else it has p.groups of them in 256 threads.
-template <class T, int VEC, int NV, bool kOne>
+template <class T, int VEC, int NV, bool kOne, bool kOdd>
 __global__ void __launch_bounds__(kOne ? bwd_threads(NV * VEC) : 256, kOne ? 1 : 3) norm_bwd_kernel(const BwdArgs p) {
   __shared__ float sm[2][32];
   extern __shared__ __align__(16) float sums[];  // [cols], with more than one group
@@ -311,11 +371,14 @@ __global__ void __launch_bounds__(kOne ? bwd_threads(NV * VEC) : 256, kOne ? 1 :
   const int lanes = blockDim.x / groups, cols = static_cast<int>(p.cols);
   const int group = kOne ? 0 : threadIdx.x / lanes, t = threadIdx.x - group * lanes, warps = lanes >> 5;
   const int64_t each = static_cast<int64_t>(gridDim.x) * groups;
+  const Columns<T, VEC, kOdd> at(p.dy, (static_cast<int64_t>(blockIdx.x) * groups + group) * p.lddy, cols, t);
   launch_dependents();
   grid_dependency_wait();
   // this thread's columns: gains, sums, and the next row's operands
   float g[NV][VEC], acc[NV][VEC], next_rstd = 0.0f;
+  float ge = 1.0f, acce = 0.0f;
   Raw<T, VEC> dyr[NV], sr[NV], dr[NV];
+  Raw<T, 1> dye = zero<T, 1>(), se = zero<T, 1>(), de = zero<T, 1>();
   auto fetch = [&](int64_t row) {
     const T* dy = static_cast<const T*>(p.dy) + row * p.lddy;
     const T* sp = static_cast<const T*>(p.s) + row * p.lds;
@@ -323,14 +386,21 @@ __global__ void __launch_bounds__(kOne ? bwd_threads(NV * VEC) : 256, kOne ? 1 :
     if (row < p.rows) next_rstd = p.rstd[row];
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
-      const int k = (v * lanes + t) * VEC;
+      const int k = at.head + (v * lanes + t) * VEC;
       dyr[v] = zero<T, VEC>();
       sr[v] = zero<T, VEC>();
       dr[v] = zero<T, VEC>();
-      if (k < cols && row < p.rows) {
+      if (k < at.end && row < p.rows) {
         dyr[v] = load<T, VEC>(dy + k);
         sr[v] = load<T, VEC>(sp + k);
         if (p.dsum) dr[v] = load<T, VEC>(ds + k);
+      }
+    }
+    if constexpr (kOdd) {
+      if (at.has && row < p.rows) {
+        dye = load<T, 1>(dy + at.one);
+        se = load<T, 1>(sp + at.one);
+        if (p.dsum) de = load<T, 1>(ds + at.one);
       }
     }
   };
@@ -338,14 +408,22 @@ __global__ void __launch_bounds__(kOne ? bwd_threads(NV * VEC) : 256, kOne ? 1 :
   fetch(first);
 #pragma unroll
   for (int v = 0; v < NV; ++v) {
-    const int k = (v * lanes + t) * VEC;
+    const int k = at.head + (v * lanes + t) * VEC;
 #pragma unroll
     for (int j = 0; j < VEC; ++j) {
       g[v][j] = 1.0f;
       acc[v][j] = 0.0f;
     }
-    if (p.gamma && k < cols) load_floats<VEC>(p.gamma + k, g[v]);
+    if (p.gamma && k < at.end) {
+      if constexpr (kOdd) {
+#pragma unroll
+        for (int j = 0; j < VEC; ++j) g[v][j] = __ldg(p.gamma + k + j);
+      } else {
+        load_floats<VEC>(p.gamma + k, g[v]);
+      }
+    }
   }
+  if (kOdd && p.gamma && at.has) ge = __ldg(p.gamma + at.one);
   const float inv_cols = 1.0f / static_cast<float>(p.cols);
   int phase = 0;
   for (int64_t row = first; row < p.rows; row += each, phase ^= 1) {
@@ -365,40 +443,71 @@ __global__ void __launch_bounds__(kOne ? bwd_threads(NV * VEC) : 256, kOne ? 1 :
         dot = fmaf(n[v][j], s[v][j], dot);
       }
     }
+    float ne[1] = {}, sse[1] = {}, ye[1] = {};
+    if constexpr (kOdd) {  // zeros where the thread has none
+      to_float(dye, ne);
+      to_float(se, sse);
+      to_float(de, ye);
+      sse[0] *= rstd;
+      acce = fmaf(ne[0], sse[0], acce);
+      ne[0] *= ge;
+      dot = fmaf(ne[0], sse[0], dot);
+    }
     fetch(row + each);
     dot = group_sum(dot, sm[phase] + group * warps, t >> 5, warps, 1 + group);
     const float c = dot * inv_cols;
     T* dx = static_cast<T*>(p.dx) + row * p.lddx;
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
-      const int k = (v * lanes + t) * VEC;
-      if (k >= cols) break;
+      const int k = at.head + (v * lanes + t) * VEC;
+      if (k >= at.end) break;
       float y[VEC];
       to_float(d[v], y);
 #pragma unroll
       for (int j = 0; j < VEC; ++j) y[j] = fmaf(rstd, fmaf(-c, s[v][j], n[v][j]), y[j]);
       store<T, VEC>(dx + k, from_float(y, T()));
     }
+    if (kOdd && at.has) {
+      ye[0] = fmaf(rstd, fmaf(-c, sse[0], ne[0]), ye[0]);
+      store<T, 1>(dx + at.one, from_float(ye, T()));
+    }
   }
   if (!p.partial) return;
   float* out = p.partial + static_cast<int64_t>(blockIdx.x) * p.cols;
-  // the groups add their sums in turn; the last one writes
-  for (int i = 0; i < groups - 1; ++i) {
-    if (group == i) {
+  if constexpr (kOdd) {  // element by element, and then in order
+    for (int i = 0; i < groups; ++i) {
+      if (group == i) {
 #pragma unroll
-      for (int v = 0; v < NV; ++v) {
-        const int k = (v * lanes + t) * VEC;
-        if (k < cols) add_floats<VEC>(sums + k, sums + k, i > 0, acc[v], true);
+        for (int v = 0; v < NV; ++v) {
+          const int k = at.head + (v * lanes + t) * VEC;
+#pragma unroll
+          for (int j = 0; j < VEC; ++j)
+            if (k < at.end) sums[k + j] = (i ? sums[k + j] : 0.0f) + acc[v][j];
+        }
+        if (at.has) sums[at.one] = (i ? sums[at.one] : 0.0f) + acce;
       }
+      __syncthreads();
     }
-    __syncthreads();
-  }
-  if (group != groups - 1) return;
-  const bool wide = (reinterpret_cast<uintptr_t>(out) & 15) == 0;
+    for (int k = threadIdx.x; k < cols; k += blockDim.x) out[k] = sums[k];
+  } else {
+    // the groups add their sums in turn; the last one writes
+    for (int i = 0; i < groups - 1; ++i) {
+      if (group == i) {
 #pragma unroll
-  for (int v = 0; v < NV; ++v) {
-    const int k = (v * lanes + t) * VEC;
-    if (k < cols) add_floats<VEC>(out + k, sums + k, groups > 1, acc[v], wide);
+        for (int v = 0; v < NV; ++v) {
+          const int k = at.head + (v * lanes + t) * VEC;
+          if (k < cols) add_floats<VEC>(sums + k, sums + k, i > 0, acc[v], true);
+        }
+      }
+      __syncthreads();
+    }
+    if (group != groups - 1) return;
+    const bool wide = (reinterpret_cast<uintptr_t>(out) & 15) == 0;
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+      const int k = at.head + (v * lanes + t) * VEC;
+      if (k < cols) add_floats<VEC>(out + k, sums + k, groups > 1, acc[v], wide);
+    }
   }
 }
 
@@ -485,24 +594,35 @@ int pick(int64_t units, int least, int (*max_threads)(int), int* threads) {
 }
 
 // Forward: few rows take the fewest elements a thread, many rows 16 or more.
-template <class T, int VEC, int MAXNV>
+// kOdd: as many CTAs as keep their rows' boundaries alike.
+template <int VEC>
+int64_t alike(int64_t grid, int64_t rows, int64_t ld, int groups) {
+  if (grid * groups >= rows) return grid;  // a row each
+  int64_t m = VEC;
+  for (int64_t step = ld * groups; m > 1 && step % 2 == 0; step /= 2) m /= 2;
+  return grid / m * m;
+}
+
+template <class T, int VEC, int MAXNV, bool kOdd>
 int fwd_vec(const FwdArgs& p, int sms, cudaStream_t s) {
   const bool many = p.rows >= 2 * static_cast<int64_t>(sms);
   int threads = 0;
-  const int nv = pick<VEC, MAXNV>((p.cols + VEC - 1) / VEC, many ? (VEC > 1 ? 16 : 8) : 1, fwd_threads, &threads);
+  const int nv = pick<VEC, MAXNV>((p.cols + VEC - 1) / VEC, many ? (VEC > 1 ? 16 : 8) : 1, fwd_threads,
+                                &threads);
   // one wave of resident CTAs (64 registers a thread)
   int64_t grid = static_cast<int64_t>(sms) * (threads > 512 ? 1 : 1024 / (threads > 0 ? threads : 1024));
   if (nv == 0) grid = 2ll * sms;
   if (grid > p.rows) grid = p.rows;
-  if (nv == MAXNV / 4) return launch(norm_fwd_kernel<T, VEC, MAXNV / 4>, grid, threads, 0, s, 1, p);
-  if (nv == MAXNV / 2) return launch(norm_fwd_kernel<T, VEC, MAXNV / 2>, grid, threads, 0, s, 1, p);
-  if (nv == MAXNV) return launch(norm_fwd_kernel<T, VEC, MAXNV>, grid, threads, 0, s, 1, p);
+  if (kOdd && nv) grid = alike<VEC>(grid, p.rows, p.ldx, 1);
+  if (nv == MAXNV / 4) return launch(norm_fwd_kernel<T, VEC, MAXNV / 4, kOdd>, grid, threads, 0, s, 1, p);
+  if (nv == MAXNV / 2) return launch(norm_fwd_kernel<T, VEC, MAXNV / 2, kOdd>, grid, threads, 0, s, 1, p);
+  if (nv == MAXNV) return launch(norm_fwd_kernel<T, VEC, MAXNV, kOdd>, grid, threads, 0, s, 1, p);
   return launch(norm_fwd_long_kernel<T>, grid, 1024, 0, s, 1, p);
 }
 
 // Backward: many rows take 8 elements a thread (more only where the row would not
 // fit a CTA).
-template <class T, int VEC, int MAXNV>
+template <class T, int VEC, int MAXNV, bool kOdd>
 int bwd_vec(BwdArgs p, float* dgamma, int sms, int* parts, cudaStream_t s) {
   const bool many = p.rows >= 2 * static_cast<int64_t>(sms);
   int threads = 0;
@@ -519,14 +639,15 @@ int bwd_vec(BwdArgs p, float* dgamma, int sms, int* parts, cudaStream_t s) {
     const int64_t need = (p.rows + p.groups - 1) / p.groups;
     if (grid > need) grid = need;
     if (grid > kMaxColParts) grid = kMaxColParts;
+    if (kOdd) grid = alike<VEC>(grid, p.rows, p.lddy, p.groups);
     *parts = static_cast<int>(grid);
     if (grid == 1 && p.partial) p.partial = dgamma;  // one part is the sum itself
+    const size_t sums = kOdd || !one ? static_cast<size_t>(p.cols) * sizeof(float) : 0;
     if (!one)
-      return launch(norm_bwd_kernel<T, VEC, 8 / VEC, false>, grid, threads * p.groups,
-                    static_cast<size_t>(p.cols) * sizeof(float), s, 1, p);
-    if (nv == MAXNV / 4) return launch(norm_bwd_kernel<T, VEC, MAXNV / 4, true>, grid, threads, 0, s, 1, p);
-    if (nv == MAXNV / 2) return launch(norm_bwd_kernel<T, VEC, MAXNV / 2, true>, grid, threads, 0, s, 1, p);
-    return launch(norm_bwd_kernel<T, VEC, MAXNV, true>, grid, threads, 0, s, 1, p);
+      return launch(norm_bwd_kernel<T, VEC, 8 / VEC, false, kOdd>, grid, threads * p.groups, sums, s, 1, p);
+    if (nv == MAXNV / 4) return launch(norm_bwd_kernel<T, VEC, MAXNV / 4, true, kOdd>, grid, threads, sums, s, 1, p);
+    if (nv == MAXNV / 2) return launch(norm_bwd_kernel<T, VEC, MAXNV / 2, true, kOdd>, grid, threads, sums, s, 1, p);
+    return launch(norm_bwd_kernel<T, VEC, MAXNV, true, kOdd>, grid, threads, sums, s, 1, p);
   }
   if (p.partial) {
     const int64_t tiles = (p.cols + 31) / 32;
@@ -544,6 +665,13 @@ bool vec_rows(const void* p, int64_t ld, int esize) {
   return !p || (aligned(p, 16) && (ld * esize) % 16 == 0);
 }
 
+// Whether the rows of `p` lie to 16-byte boundaries as those of `q` do (elements of
+// `esize` bytes, `v` of them in 16).
+bool alike_rows(const void* p, int64_t ld, const void* q, int64_t ldq, int esize, int v) {
+  const uintptr_t a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(q);
+  return !p || (a % esize == 0 && b % esize == 0 && (a - b) / esize % v == 0 && (ld - ldq) % v == 0);
+}
+
 }  // namespace nm
 
 int launch_norm_fwd(const void* x, int64_t ldx, const void* residual, int64_t ldr, const float* gamma,
@@ -554,9 +682,17 @@ int launch_norm_fwd(const void* x, int64_t ldx, const void* residual, int64_t ld
   const bool vec = cols % v == 0 && nm::vec_rows(x, ldx, es) && nm::vec_rows(residual, ldr, es) &&
                    nm::vec_rows(sum_out, lds, es) && vec::aligned(q, v) &&
                    (!gamma || vec::aligned(gamma, 16));
+  // rows that are alike; their codes, too, then lie to boundaries of v bytes as they do to v elements
+  const bool odd = !vec && cols >= nm::kOddCols && nm::alike_rows(residual, ldr, x, ldx, es, v) &&
+                   nm::alike_rows(sum_out, lds, x, ldx, es, v) && reinterpret_cast<uintptr_t>(x) % es == 0 &&
+                   (reinterpret_cast<uintptr_t>(x) / es - reinterpret_cast<uintptr_t>(q)) % v == 0 && (ldx - cols) % v == 0;
   if (dtype == T3_OUT_BF16)
-    return vec ? nm::fwd_vec<vec::bf16, 8, 4>(p, sms, s) : nm::fwd_vec<vec::bf16, 1, 32>(p, sms, s);
-  return vec ? nm::fwd_vec<float, 4, 4>(p, sms, s) : nm::fwd_vec<float, 1, 32>(p, sms, s);
+    return vec   ? nm::fwd_vec<vec::bf16, 8, 4, false>(p, sms, s)
+           : odd ? nm::fwd_vec<vec::bf16, 8, 4, true>(p, sms, s)
+                 : nm::fwd_vec<vec::bf16, 1, 32, false>(p, sms, s);
+  return vec   ? nm::fwd_vec<float, 4, 4, false>(p, sms, s)
+         : odd ? nm::fwd_vec<float, 4, 4, true>(p, sms, s)
+               : nm::fwd_vec<float, 1, 32, false>(p, sms, s);
 }
 
 int launch_norm_bwd(const void* dy, int64_t lddy, const void* x, int64_t lds, const float* rstd,
@@ -569,13 +705,17 @@ int launch_norm_bwd(const void* dy, int64_t lddy, const void* x, int64_t lds, co
   const bool vec = cols % v == 0 && nm::vec_rows(dy, lddy, es) && nm::vec_rows(x, lds, es) &&
                    nm::vec_rows(dsum, lddsum, es) && nm::vec_rows(dx, lddx, es) &&
                    (!gamma || vec::aligned(gamma, 16));
+  const bool odd = !vec && cols >= nm::kOddCols && nm::alike_rows(x, lds, dy, lddy, es, v) &&
+                   nm::alike_rows(dsum, lddsum, dy, lddy, es, v) && nm::alike_rows(dx, lddx, dy, lddy, es, v);
   int parts = 0, st;
   if (dtype == T3_OUT_BF16)
-    st = vec ? nm::bwd_vec<vec::bf16, 8, 4>(p, dgamma, sms, &parts, s)
-             : nm::bwd_vec<vec::bf16, 1, 32>(p, dgamma, sms, &parts, s);
+    st = vec   ? nm::bwd_vec<vec::bf16, 8, 4, false>(p, dgamma, sms, &parts, s)
+         : odd ? nm::bwd_vec<vec::bf16, 8, 4, true>(p, dgamma, sms, &parts, s)
+               : nm::bwd_vec<vec::bf16, 1, 32, false>(p, dgamma, sms, &parts, s);
   else
-    st = vec ? nm::bwd_vec<float, 4, 4>(p, dgamma, sms, &parts, s)
-             : nm::bwd_vec<float, 1, 32>(p, dgamma, sms, &parts, s);
+    st = vec   ? nm::bwd_vec<float, 4, 4, false>(p, dgamma, sms, &parts, s)
+         : odd ? nm::bwd_vec<float, 4, 4, true>(p, dgamma, sms, &parts, s)
+               : nm::bwd_vec<float, 1, 32, false>(p, dgamma, sms, &parts, s);
   if (st != T3_OK || !dgamma || parts == 1) return st;
   return launch_col_finish(workspace, parts, cols, dgamma, s);
 }

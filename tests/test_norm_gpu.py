@@ -188,6 +188,33 @@ def test_backward_strides_and_in_place(cols, pad):
     assert torch.equal(again[0], want[0]) and torch.equal(again[1], want[1]), "changes from call to call"
 
 
+# rows that begin on any boundary, all arrays alike: few columns and many, bases off the boundary too, CTAs of
+# several rows and of several groups of rows
+@pytest.mark.parametrize("dname", ["bf16", "f32"])
+@pytest.mark.parametrize("rows,cols,offset", [(3000, 65, 0), (2600, 67, 3), (5001, 243, 1), (2500, 514, 0), (700, 4099, 5),
+                                              (320, 8191, 0), (33, 1003, 7), (4000, 130, 2)])
+def test_odd_rows_alike(rows, cols, offset, dname):
+    g = _gen(rows + cols)
+    v = 8 if dname == "bf16" else 4
+
+    def alike(t):  # the rows one after another, `offset` elements off a boundary
+        flat = torch.zeros(t.numel() + 16, dtype=t.dtype, device="cuda")
+        out = flat[offset:offset + t.numel()].view(t.shape)
+        out.copy_(t)
+        return out
+
+    x, r, dy, ds = (alike(_rand(g, rows, cols, dtype=DT[dname])) for _ in range(4))
+    gamma = 1 + 0.3 * _rand(g, cols)
+    q = torch.zeros(rows * cols + 16, dtype=torch.int8, device="cuda")[offset % v:][:rows * cols].view(rows, cols)
+    s = (x.float() + r.float()).to(DT[dname])
+    got = t3.t3_rmsnorm_quant(x, gamma, r, EPS, q=q, sum_out=r)  # the stream in place
+    assert torch.equal(r, s)
+    _check_forward(s, gamma, (q, got[1], got[2], None), dname)
+    keep = dy.clone()
+    back = t3.t3_rmsnorm_bwd(dy, r, got[2], gamma, dsum=ds, dx=dy)  # dx over dy
+    _check_backward(keep, s, got[2], gamma, ds, back, dname)
+
+
 def test_one_row_repeated_as_input():
     """The gradient of a broadcast row (stride 0) counts it once a row."""
     g = _gen(5)
