@@ -18,7 +18,7 @@
 // row, so their gains (and, backward, their sums of dgamma) stay in registers, and the
 // next row's operands are loaded while this one is reduced and written.  Many
 // rows take 16 elements a thread forward and 8 backward (8 and 8 where rows
-// are not 16-byte vectors and go element by element), few rows as few as 1024 threads
+// go element by element: arrays whose rows lie differently to 16-byte boundaries), few rows as few as 1024 threads
 // allow, for the shortest time to one row; rows longer than the registers
 // hold are read twice.  Backward, narrow rows share a CTA in groups of warps that
 // meet at barriers of their own.  dgamma: each CTA adds its groups' sums in turn,
@@ -27,8 +27,9 @@
 //
 // Measured (GB300, bf16 with residual; bytes of the formulas over the time, of
 // the measured 6784 GB/s): forward 16384 x 1280 25.7 us (84 %), 16384 x 3456
-// 62.6 us (93 %), 1 x 8192 2.6 us; backward 35 us (71 %) and 82.7 us (81 %).
-// Odd widths: 1782 x 729 float 4.8 us forward, 11.4 us backward.
+// 62.6 us (93 %), 1 x 8192 2.6 us; backward 33 us (75 %) and 80.4 us (83 %).
+// Odd widths: 1782 x 729 float 5.5 us forward, 10.8 us backward; 5000 x 5003 bf16 32.9 us
+// (79 %) and 49 us (60 %).
 #include "t3_vec.cuh"
 
 namespace t3 {

@@ -21,8 +21,8 @@
 // and not 1 - R is what is kept: products of factors near 1 would lose the
 // same long memory), so:
 //   * a lane holds two channels over a run of S steps in registers (neighbours,
-//     worked on with packed instructions; half a tile apart where rows are not
-//     16-byte pieces), a warp 64 channels over S steps or 32 over 2 S, a CTA of 8
+//     worked on with packed instructions; half a tile apart where rows go element
+//     by element), a warp 64 channels over S steps or 32 over 2 S, a CTA of 8
 //     warps 8 times as many consecutive steps, a cluster up to 8 CTAs;
 //   * each lane composes its run's map; warp 0 composes the CTA's, which travel to
 //     the cluster's other CTAs by asynchronous stores that complete on the
@@ -30,6 +30,8 @@
 //     steps the carried state from warp to warp; each lane then runs its steps
 //     again from registers, this time from the true state;
 //   * the cluster walks along the sequence, a round at a time.
+// More tiles of channels than are resident at once need no split in time; forward, a
+// cluster's CTAs then share several tiles evenly (scan_fwd_shared_kernel).
 // Everything is read once and written once, in a fixed order: the result does
 // not change from call to call.  Sequences of a few tokens take one thread per
 // channel pair and no exchange.
@@ -39,11 +41,16 @@
 // read from the stage again.
 //
 // Measured (GB300, bf16; bytes of the formulas, of the measured 6784 GB/s):
-// 8 x 2048 x 3456 forward 55.4 us (90 %), backward 110 to 116 us (87 to 91 %);
-// 1 x 16384 x 1280 forward 33.1 us (56 %) and backward 64 us (58 %), bound by the
-// round trip between the CTAs of a cluster every 1536 tokens; 27 single tokens
-// of 8192 channels 1.9 us.  Rows that are not whole 16-byte pieces take 1.5 to
-// 1.9 times as long as aligned ones (3 x 1782 x 729 float: 17.1 and 28 us).
+// 8 x 2048 x 3456 forward 54 to 56 us (90 %), backward 108 to 111 us (92 %), with
+// resets the same; 8 x 2048 x 2560 forward 42.8 us (87 %); 1 x 16384 x 1280 forward
+// 32.6 us (57 %) and backward 62.5 us (59 %); 27 single tokens of 8192 channels 1.9 us.
+// Rows of 4-byte pieces take 1.2 to 1.5 times as long as aligned ones, odd rows of
+// 2-byte elements twice (3 x 1782 x 729 float with resets: 14.5 and 25.4 us).
+// The long sequence is held up by no one thing (left out one at a time, of 33 us: the
+// exchange 9, the first pass 7, the second 4.5, the copies 4): four warps a scheduler
+// do not overlap them all.  Trading the maps behind the next round's first pass, in a
+// warp of its own and with shorter runs, takes 35 us; runs of 8 and 12 steps in three or
+// four CTAs an SM 45 to 63; of 20 and 24 steps 34 and 42.
 #include <algorithm>
 #include <atomic>
 #include <type_traits>
@@ -59,8 +66,8 @@ constexpr int kWarps = 8;
 constexpr int kMaxCluster = 8;
 // CTAs that share an SM.  Their 64 KB of stages would let three; but the 16
 // steps a lane holds spill at the 80 registers that leaves, and two balance better over
-// the SMs (8 x 2048 x 3456 forward: 61 us with three, 55 with two; backward
-// 127 and 118).
+// the SMs (8 x 2048 x 3456 forward: 57 us with three and 12 steps, 55 with two and
+// 16; 1 x 16384 x 1280: 45 and 33).
 constexpr int kPerSm = 2;
 
 struct FwdArgs {
