@@ -457,6 +457,11 @@ def _rows(t, dtype, dev, shape, name, out=False):
         raise TypeError(f"{name} must be a {dtype} tensor on device {dev}")
     if t.shape != shape:
         raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+    return _spaced(t, shape, name, out)
+
+
+def _spaced(t, shape, name, out=False):
+    """The same for a tensor whose type, device and shape are the call's."""
     st = t.stride()
     cols = shape[-1]
     if st[-1] != 1 and cols > 1 and t.numel():
@@ -558,9 +563,9 @@ def t3_rmsnorm_quant(x, gamma=None, residual=None, eps=1e-5, q=None, row_scale=N
     without a residual and without sum_out; sum_out may be x or residual."""
     torch = _torch()
     dtype = _dtype_of(x, "x")
-    if x.dim() != 2:
-        raise TypeError("x must be 2-D [rows][cols]")
     shape, xt, dev, f32 = x.shape, x.dtype, x.get_device(), torch.float32
+    if len(shape) != 2:
+        raise TypeError("x must be 2-D [rows][cols]")
     rows, cols = shape
     if q is None:
         q = _empty(shape, torch.int8, dev, stream)
@@ -570,7 +575,7 @@ def t3_rmsnorm_quant(x, gamma=None, residual=None, eps=1e-5, q=None, row_scale=N
         rstd = _empty(rows, f32, dev, stream)
     if sum_out is None and residual is not None:
         sum_out = _empty(shape, xt, dev, stream)
-    px, ldx = _rows(x, xt, dev, shape, "x")
+    px, ldx = _spaced(x, shape, "x")
     pr, ldr = _rows(residual, xt, dev, shape, "residual")
     ps, lds = _rows(sum_out, xt, dev, shape, "sum_out", out=True)
     _launch("t3_rmsnorm_quant", dev, stream, px, ldx, pr, ldr, _dense(gamma, f32, dev, (cols,), "gamma"), eps,
@@ -594,7 +599,7 @@ def t3_rmsnorm_bwd(dy, s, rstd, gamma=None, dsum=None, dx=None, dgamma=None, wor
     if dgamma is None and gamma is not None:
         dgamma = _empty(cols, f32, dev, stream)
     ws = None if dgamma is None else _workspace(workspace, rows, cols, dev, stream)
-    pdy, lddy = _rows(dy, xt, dev, shape, "dy")
+    pdy, lddy = _spaced(dy, shape, "dy")
     ps, lds = _rows(s, xt, dev, shape, "s")
     pd, ldd = _rows(dsum, xt, dev, shape, "dsum")
     px, ldx = _rows(dx, xt, dev, shape, "dx", out=True)
@@ -612,15 +617,15 @@ def t3_gated_scan_fwd(gate, cand, h0=None, resets=None, h=None, h_last=None, str
     h_last (float32 [batch][width]) may be h0: the state advances in place."""
     torch = _torch()
     dtype = _dtype_of(gate, "gate")
-    if gate.dim() != 3:
-        raise TypeError("gate must be 3-D [batch][length][width]")
     shape, xt, dev, f32 = gate.shape, gate.dtype, gate.get_device(), torch.float32
+    if len(shape) != 3:
+        raise TypeError("gate must be 3-D [batch][length][width]")
     batch, length, width = shape
     if h is None:
         h = _empty(shape, xt, dev, stream)
     if h_last is None:
         h_last = _empty((batch, width), f32, dev, stream)
-    pg, ldg = _rows(gate, xt, dev, shape, "gate")
+    pg, ldg = _spaced(gate, shape, "gate")
     pc, ldc = _rows(cand, xt, dev, shape, "cand")
     ph, ldh = _rows(h, xt, dev, shape, "h", out=True)
     _launch("t3_gated_scan_fwd", dev, stream, pg, ldg, pc, ldc, _dense(h0, f32, dev, (batch, width), "h0"),
@@ -636,9 +641,9 @@ def t3_gated_scan_bwd(gate, cand, h, dh, h0=None, resets=None, dh_last=None, dga
     h_last; h is the forward's output."""
     torch = _torch()
     dtype = _dtype_of(gate, "gate")
-    if gate.dim() != 3:
-        raise TypeError("gate must be 3-D [batch][length][width]")
     shape, xt, dev, f32 = gate.shape, gate.dtype, gate.get_device(), torch.float32
+    if len(shape) != 3:
+        raise TypeError("gate must be 3-D [batch][length][width]")
     batch, length, width = shape
     if dgate is None:
         dgate = _empty(shape, xt, dev, stream)
@@ -646,7 +651,7 @@ def t3_gated_scan_bwd(gate, cand, h, dh, h0=None, resets=None, dh_last=None, dga
         dcand = _empty(shape, xt, dev, stream)
     if dh0 is None:
         dh0 = _empty((batch, width), f32, dev, stream)
-    pg, ldg = _rows(gate, xt, dev, shape, "gate")
+    pg, ldg = _spaced(gate, shape, "gate")
     pc, ldc = _rows(cand, xt, dev, shape, "cand")
     ph, ldh = _rows(h, xt, dev, shape, "h")
     pd, ldd = _rows(dh, xt, dev, shape, "dh")

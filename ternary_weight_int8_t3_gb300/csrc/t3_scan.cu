@@ -877,11 +877,8 @@ template <class T> constexpr int kBwdSteps = 16 / sizeof(T);
 
 // Dynamic shared memory of `Fn`, set once per device.
 template <auto Fn>
-int allow_smem(int bytes) {
+int allow_smem(int dev, int bytes) {
   static std::atomic<bool> done[64];
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess) return T3_ECUDA;
-  if (dev < 0 || dev >= 64) return T3_EDEVICE;
   if (!done[dev].load(std::memory_order_acquire)) {
     if (cudaFuncSetAttribute(Fn, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess) return T3_ECUDA;
     done[dev].store(true, std::memory_order_release);
@@ -891,10 +888,8 @@ int allow_smem(int bytes) {
 
 // How many clusters of c CTAs of `Fn` are resident at once (cached per device).
 template <auto Fn>
-int max_clusters(int c, size_t smem) {
+int max_clusters(int dev, int c, size_t smem) {
   static std::atomic<int> cache[64][kMaxCluster + 1];
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
   int n = cache[dev][c].load(std::memory_order_acquire);
   if (n > 0) return n;
   cudaLaunchAttribute attr[1];
@@ -929,11 +924,11 @@ struct Plan {
 };
 
 template <auto Fn>
-Plan plan(int64_t tiles, int64_t length, int rows, int smem, int per_cta) {
+Plan plan(int dev, int64_t tiles, int64_t length, int rows, int smem, int per_cta) {
   Plan best{0, 0.0};
   for (int c = 1; c <= kMaxCluster; ++c) {
     if (c > 1 && (c - 1) * static_cast<int64_t>(rows) >= length) break;  // CTAs without steps
-    const int n = max_clusters<Fn>(c, smem + (c > 1 ? c * per_cta : 0));
+    const int n = max_clusters<Fn>(dev, c, smem + (c > 1 ? c * per_cta : 0));
     if (n < 1) continue;
     const int64_t full = tiles / n, left = tiles % n, rounds = (length + c * rows - 1) / (c * rows);
     // a last wave that is not full has the SMs more to itself
@@ -946,11 +941,11 @@ Plan plan(int64_t tiles, int64_t length, int rows, int smem, int per_cta) {
 
 // The same for shared tiles, each of whose CTAs has its part of the cluster's rounds.
 template <auto Fn>
-Plan plan_shared(int64_t tiles, int64_t length, int rows, int smem, int per_cta) {
+Plan plan_shared(int dev, int64_t tiles, int64_t length, int rows, int smem, int per_cta) {
   Plan best{0, 0.0};
   const int64_t rounds = (length + rows - 1) / rows;
   for (int c = 2; c <= kMaxCluster; ++c) {
-    const int64_t n = std::min<int64_t>(max_clusters<Fn>(c, smem + c * per_cta), tiles / c);
+    const int64_t n = std::min<int64_t>(max_clusters<Fn>(dev, c, smem + c * per_cta), tiles / c);
     if (n < 1) continue;
     const double cost = static_cast<double>((tiles + n - 1) / n) * rounds / c;
     if (best.cluster == 0 || cost < best.cost) best = {c, cost, n};
@@ -996,20 +991,23 @@ template <template <int> class K, bool kTryShared, class Args>
 int run(const Args& p, int64_t batch, cudaStream_t s) {
   using Wide = K<32>;
   using Narrow = K<16>;
-  int st = allow_smem<Wide::fn>(Wide::smem + kMaxCluster * Wide::per_cta);
-  if (st == T3_OK) st = allow_smem<Narrow::fn>(Narrow::smem + kMaxCluster * Narrow::per_cta);
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return T3_ECUDA;
+  if (dev < 0 || dev >= 64) return T3_EDEVICE;
+  int st = allow_smem<Wide::fn>(dev, Wide::smem + kMaxCluster * Wide::per_cta);
+  if (st == T3_OK) st = allow_smem<Narrow::fn>(dev, Narrow::smem + kMaxCluster * Narrow::per_cta);
   if (st != T3_OK) return st;
-  const Plan w = plan<Wide::fn>(batch * ((p.width + 63) / 64), p.length, Wide::rows, Wide::smem, Wide::per_cta);
-  const Plan n = plan<Narrow::fn>(batch * ((p.width + 31) / 32), p.length, Narrow::rows, Narrow::smem, Narrow::per_cta);
+  const Plan w = plan<Wide::fn>(dev, batch * ((p.width + 63) / 64), p.length, Wide::rows, Wide::smem, Wide::per_cta);
+  const Plan n = plan<Narrow::fn>(dev, batch * ((p.width + 31) / 32), p.length, Narrow::rows, Narrow::smem, Narrow::per_cta);
   if (w.cluster == 0 && n.cluster == 0) return T3_ECUDA;
   if constexpr (kTryShared) {
     constexpr auto fn = scan_fwd_shared_kernel<typename Wide::Type, Wide::S, Wide::marks>;
-    st = allow_smem<fn>(Wide::smem + kMaxCluster * Wide::per_cta);
+    st = allow_smem<fn>(dev, Wide::smem + kMaxCluster * Wide::per_cta);
     if (st != T3_OK) return st;
     Args q = p;
     q.tiles = (p.width + 63) / 64;
     q.all_tiles = batch * q.tiles;
-    const Plan h = plan_shared<fn>(q.all_tiles, p.length, Wide::rows, Wide::smem, Wide::per_cta);
+    const Plan h = plan_shared<fn>(dev, q.all_tiles, p.length, Wide::rows, Wide::smem, Wide::per_cta);
     if (h.cluster > 0 && h.cost < std::min(w.cost, n.cost * kNarrowGain))
       return launch(fn, h.clusters * h.cluster, 32 * kWarps, Wide::smem + h.cluster * Wide::per_cta, s, h.cluster, q);
   }
