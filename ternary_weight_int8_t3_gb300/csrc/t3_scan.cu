@@ -451,10 +451,10 @@ __device__ __forceinline__ void forward_round(const Slab<T, LPR, S, 2>& stage, i
   const uint8_t* sc = stage.a[1] + group * (S * Stage::kRow + Stage::kSkip);
   const int n = length - t0 < S ? static_cast<int>(length - t0) : S;  // steps here (may be negative)
   // A run is plain, or has resets; one that reaches past the sequence's end, or has masked
-  // tokens (k = 0) whose candidate is not finite, which would show in H, takes the
-  // careful form.
+  // tokens (k = 0) whose candidate is not finite, takes the careful form.  Such a candidate
+  // shows in H, at the run's end or (`gone`, their sum) where a reset clears it.
   const float2 none = make_float2(0.0f, 0.0f), all = make_float2(1.0f, 1.0f);
-  float2 k[S], R = none, H = none, h;
+  float2 k[S], R = none, H = none, gone = none, h;
   int form = n < S ? kCareful : kMarks && resets != 0 ? kResets : kPlain;
   auto first = [&](auto how) {
     R = H = none;
@@ -464,6 +464,7 @@ __device__ __forceinline__ void forward_round(const Slab<T, LPR, S, 2>& stage, i
       float2 c = read_pair<T, LPR, kPair<T, CH>>(sc, i, col);
       k[i] = how.value < kCareful || i < n ? take2(f) : none;
       if (how.value >= kResets && (resets >> i & 1)) {
+        if (how.value == kResets) gone = __fadd2_rn(gone, H);
         R = all;
         H = none;
       }
@@ -476,7 +477,8 @@ __device__ __forceinline__ void forward_round(const Slab<T, LPR, S, 2>& stage, i
     first(std::integral_constant<int, kPlain>());
   else if (kMarks && form == kResets)
     first(std::integral_constant<int, kResets>());
-  if (!(fabsf(H.x) + fabsf(H.y) < __int_as_float(0x7f800000))) form = kCareful;
+  const float2 seen = __fadd2_rn(gone, H);
+  if (!(fabsf(seen.x) + fabsf(seen.y) < __int_as_float(0x7f800000))) form = kCareful;
   if (form == kCareful) first(std::integral_constant<int, kCareful>());
   h = exchange<LPR, false>(maps, cta_maps, round, size, rank, waits, R, H, carry);
   auto second_pass = [&](auto how) {

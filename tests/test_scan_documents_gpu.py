@@ -1,0 +1,81 @@
+"""GPU tests of documents packed into one sequence of the gated recurrence:
+masked tokens in front of a reset, values that are not finite on the other side
+of one, and the gradient that leaves the sequence.  The wanted values come from the
+64-bit forms of tests/operators_ref.py on data whose masked and poisoned
+entries are replaced by zeros: a document that is packed behind a reset does not
+depend on them, so everything outside them has to agree."""
+import numpy as np
+import pytest
+
+import operators_ref as ref
+import ternary_weight_int8_t3_gb300 as t3
+
+torch = pytest.importorskip("torch")
+pytestmark = pytest.mark.gpu
+
+DT = {"bf16": torch.bfloat16, "f32": torch.float32}
+INF, NAN = float("inf"), float("nan")
+
+
+def _np(t):
+    return t.detach().double().cpu().numpy()
+
+
+def _make(seed, b, t, d, dname):
+    g = torch.Generator(device="cuda")
+    g.manual_seed(seed)
+
+    def rand(*shape):
+        return torch.randn(shape, generator=g, device="cuda")
+    dt = DT[dname]
+    return ((rand(b, t, d) * 1.7 + 1.5).to(dt), rand(b, t, d).to(dt), rand(b, d), rand(b, t, d).to(dt), rand(b, d))
+
+
+def _resets(rng, b, t, every):
+    r = rng.random((b, t)) < 1 / every
+    return torch.from_numpy(r.astype(np.uint8)).cuda()
+
+
+def _within(got, want, err, ulp, where, name):
+    tol = ulp * np.abs(want) + err + 1e-30
+    off = np.abs(_np(got) - want)
+    bad = where & ~(off <= tol)  # NaN counts as off
+    assert not bad.any(), (name, int(bad.sum()), np.argwhere(bad)[:4].tolist())
+
+
+# widths whose rows are whole 16-byte pieces, whole words and odd; lengths that end in a
+# thread's loop, a lane's run, a warp, a CTA, a cluster and its next rounds; and more tiles than
+# are resident at once
+SHAPES = [(2, 7, 64), (3, 9, 64), (2, 40, 66), (3, 130, 63), (2, 300, 128), (1, 1300, 62), (1, 5000, 31), (20, 600, 1024)]
+
+
+@pytest.mark.parametrize("dname", ["bf16", "f32"])
+@pytest.mark.parametrize("b,t,d", SHAPES)
+def test_masked_tokens_in_front_of_a_reset(b, t, d, dname):
+    """Padding at the end of a document: gate +inf and any candidate, 1 to 15
+    tokens in front of the next one."""
+    gate, cand, h0, dh, dl = _make(b + t + d, b, t, d, dname)
+    rng = np.random.default_rng(t)
+    r = _resets(rng, b, t, 21)
+    mask = np.zeros((b, t), bool)
+    for s, at in np.argwhere(_np(r) != 0):
+        for back in rng.integers(1, 16, 3):
+            if at - back >= 0:
+                mask[s, at - back] = True
+    m = torch.from_numpy(mask).cuda()
+    fill = torch.tensor([NAN, INF, -INF, 3e38], device="cuda").to(DT[dname])
+    gate[m] = INF
+    dirty = cand.clone()
+    dirty[m] = fill[torch.arange(d, device="cuda") % 4].expand(int(mask.sum()), d)
+    cand[m] = 0
+    h, last = t3.t3_gated_scan_fwd(gate, dirty, h0, r)
+    want, prior, err = ref.scan(_np(gate), _np(cand), _np(h0), _np(r))
+    everywhere = np.ones((b, t, d), bool)
+    _within(h, want, err, ref.HALF_ULP[dname], everywhere, "h")
+    _within(last, want[:, -1], err[:, -1], ref.U, everywhere[:, 0], "h_last")
+    # what the masked candidates hold changes no bit of either direction
+    clean = t3.t3_gated_scan_fwd(gate, cand, h0, r)
+    assert torch.equal(h, clean[0]) and torch.equal(last, clean[1])
+    got = t3.t3_gated_scan_bwd(gate, dirty, h, dh, h0, r, dl)
+    for x, y in zip(got, t3.t3_gated_scan_bwd(gate, cand, h, dh, h0, r, dl)):
+        assert torch.equal(x, y)
