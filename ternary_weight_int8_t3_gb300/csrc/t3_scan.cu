@@ -481,6 +481,9 @@ __device__ __forceinline__ void forward_round(const Slab<T, LPR, S, 2>& stage, i
   if (!(fabsf(seen.x) + fabsf(seen.y) < __int_as_float(0x7f800000))) form = kCareful;
   if (form == kCareful) first(std::integral_constant<int, kCareful>());
   h = exchange<LPR, false>(maps, cta_maps, round, size, rank, waits, R, H, carry);
+  // a masked candidate near the float limit overflows c - h where h is large, which H (from a
+  // state of 0) did not show
+  if (!(fabsf(h.x) + fabsf(h.y) < 1e30f)) form = kCareful;
   auto second_pass = [&](auto how) {
 #pragma unroll
     for (int i = 0; i < S; ++i, o += ldh) {

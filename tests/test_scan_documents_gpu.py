@@ -79,3 +79,14 @@ def test_masked_tokens_in_front_of_a_reset(b, t, d, dname):
     got = t3.t3_gated_scan_bwd(gate, dirty, h, dh, h0, r, dl)
     for x, y in zip(got, t3.t3_gated_scan_bwd(gate, cand, h, dh, h0, r, dl)):
         assert torch.equal(x, y)
+
+
+@pytest.mark.parametrize("dname", ["bf16", "f32"])
+@pytest.mark.parametrize("t", [6, 9, 40, 300, 1300])
+def test_masked_tokens_keep_a_large_state(t, dname):
+    """A masked candidate at the other end of the float range, however large the state."""
+    gate, cand, h0, _, _ = _make(t, 2, t, 64, dname)
+    h0 = torch.full_like(h0, 2e38)
+    gate[:], cand[:] = INF, -3e38
+    h, last = t3.t3_gated_scan_fwd(gate, cand, h0)
+    assert torch.equal(last, h0) and torch.equal(h, h0.to(DT[dname])[:, None].expand_as(h))
