@@ -204,10 +204,22 @@ __device__ __forceinline__ uint32_t reset_mark(const uint8_t* resets, int64_t at
 }
 
 // A map (R, H) applied to a state, and the map of first (a, b), then (R, H).
-__device__ __forceinline__ float apply(float R, float H, float h) { return fmaf(-R, h, h) + H; }
+// kMarks: a run that holds a reset has R = NaN, which stays NaN through every
+// product and composition, and its map gives H whatever the state holds: R = 1 would
+// carry an infinite or NaN state of one document into the next (0 times it), and
+// is what a long run without a reset rounds to.  A gate of NaN makes H NaN too.
+template <bool kMarks>
+__device__ __forceinline__ float apply(float R, float H, float h) {
+  const float y = fmaf(-R, h, h) + H;
+  return kMarks && R != R ? H : y;
+}
+template <bool kMarks>
 __device__ __forceinline__ void compose(float R, float H, float& a, float& b) {
-  b = apply(R, H, b);
+  b = apply<kMarks>(R, H, b);
   a = fmaf(R, 1.0f - a, a);
+}
+__device__ __forceinline__ float2 forget() {
+  return make_float2(__int_as_float(0x7fffffff), __int_as_float(0x7fffffff));
 }
 
 // What a CTA's warps exchange, two channels an entry: their maps (R0, H0, R1,
@@ -244,7 +256,7 @@ __device__ __forceinline__ void open_maps(Maps<LPR>& m) {
 // becomes the state past them.  Warp 0 composes the CTA's maps, trades them
 // with the cluster and steps the state from warp to warp; the others only hand
 // their map in and take their state out.
-template <int LPR, bool kReverse>
+template <int LPR, bool kReverse, bool kMarks>
 __device__ __forceinline__ float2 exchange(Maps<LPR>& m, float4* cta, int round, int size, int rank, Waits& waits,
                                            float2 R2, float2 H2, float (&carry)[2]) {
   const float R[2] = {R2.x, R2.y}, H[2] = {H2.x, H2.y};
@@ -263,9 +275,9 @@ __device__ __forceinline__ float2 exchange(Maps<LPR>& m, float4* cta, int round,
         gh[j] = h2;
         tr[j] = r2;
         th[j] = h2;
-        compose(R[j], H[j], tr[j], th[j]);
+        compose<kMarks>(R[j], H[j], tr[j], th[j]);
       } else {
-        compose(r2, h2, tr[j], th[j]);
+        compose<kMarks>(r2, h2, tr[j], th[j]);
       }
     }
   }
@@ -280,8 +292,8 @@ __device__ __forceinline__ float2 exchange(Maps<LPR>& m, float4* cta, int round,
       float ar[2] = {}, ah[2] = {};
 #pragma unroll
       for (int i = 0; i < kWarps; ++i) {
-        compose(e[i].x, e[i].y, ar[0], ah[0]);
-        compose(e[i].z, e[i].w, ar[1], ah[1]);
+        compose<kMarks>(e[i].x, e[i].y, ar[0], ah[0]);
+        compose<kMarks>(e[i].z, e[i].w, ar[1], ah[1]);
       }
       if (lane == 0) mbar_arrive_expect_tx(&m.full[phase], size * LPR * 16);
       float4* slots = cta + phase * size * LPR + col;
@@ -305,15 +317,15 @@ __device__ __forceinline__ float2 exchange(Maps<LPR>& m, float4* cta, int round,
           s[0] = carry[0];
           s[1] = carry[1];
         }
-        carry[0] = apply(c[i].x, c[i].y, carry[0]);
-        carry[1] = apply(c[i].z, c[i].w, carry[1]);
+        carry[0] = apply<kMarks>(c[i].x, c[i].y, carry[0]);
+        carry[1] = apply<kMarks>(c[i].z, c[i].w, carry[1]);
       }
     }
 #pragma unroll
     for (int i = 0; i < kWarps; ++i) {
       if (lane < LPR) m.state[kReverse ? kWarps - 1 - i : i][col] = make_float2(s[0], s[1]);
-      s[0] = apply(e[i].x, e[i].y, s[0]);
-      s[1] = apply(e[i].z, e[i].w, s[1]);
+      s[0] = apply<kMarks>(e[i].x, e[i].y, s[0]);
+      s[1] = apply<kMarks>(e[i].z, e[i].w, s[1]);
     }
     if (size == 1) {
       carry[0] = s[0];
@@ -322,7 +334,7 @@ __device__ __forceinline__ float2 exchange(Maps<LPR>& m, float4* cta, int round,
   }
   __syncthreads();
   const float2 v = m.state[warp][col];
-  return make_float2(apply(gr[0], gh[0], v.x), apply(gr[1], gh[1], v.y));
+  return make_float2(apply<kMarks>(gr[0], gh[0], v.x), apply<kMarks>(gr[1], gh[1], v.y));
 }
 
 // v where the candidate or gradient of a taken token counts: 0 for k = 0.
@@ -453,7 +465,7 @@ __device__ __forceinline__ void forward_round(const Slab<T, LPR, S, 2>& stage, i
   // A run is plain, or has resets; one that reaches past the sequence's end, or has masked
   // tokens (k = 0) whose candidate is not finite, takes the careful form.  Such a candidate
   // shows in H, at the run's end or (`gone`, their sum) where a reset clears it.
-  const float2 none = make_float2(0.0f, 0.0f), all = make_float2(1.0f, 1.0f);
+  const float2 none = make_float2(0.0f, 0.0f);
   float2 k[S], R = none, H = none, gone = none, h;
   int form = n < S ? kCareful : kMarks && resets != 0 ? kResets : kPlain;
   auto first = [&](auto how) {
@@ -465,7 +477,7 @@ __device__ __forceinline__ void forward_round(const Slab<T, LPR, S, 2>& stage, i
       k[i] = how.value < kCareful || i < n ? take2(f) : none;
       if (how.value >= kResets && (resets >> i & 1)) {
         if (how.value == kResets) gone = __fadd2_rn(gone, H);
-        R = all;
+        R = forget();
         H = none;
       }
       if (how.value == kCareful) c = masked2(k[i], c);
@@ -480,7 +492,7 @@ __device__ __forceinline__ void forward_round(const Slab<T, LPR, S, 2>& stage, i
   const float2 seen = __fadd2_rn(gone, H);
   if (!(fabsf(seen.x) + fabsf(seen.y) < __int_as_float(0x7f800000))) form = kCareful;
   if (form == kCareful) first(std::integral_constant<int, kCareful>());
-  h = exchange<LPR, false>(maps, cta_maps, round, size, rank, waits, R, H, carry);
+  h = exchange<LPR, false, kMarks>(maps, cta_maps, round, size, rank, waits, R, H, carry);
   // a masked candidate near the float limit overflows c - h where h is large, which H (from a
   // state of 0) did not show
   if (!(fabsf(h.x) + fabsf(h.y) < 1e30f)) form = kCareful;
@@ -813,7 +825,7 @@ __global__ void __launch_bounds__(32 * kWarps, kPerSm) scan_bwd_kernel(const Bwd
     const Stage& st = stages[phase];
     const int at = group * (S * Stage::kRow + Stage::kSkip);
     const int n = p.length - t0 < S ? static_cast<int>(p.length - t0) : S;
-    const float2 none = make_float2(0.0f, 0.0f), all = make_float2(1.0f, 1.0f);
+    const float2 none = make_float2(0.0f, 0.0f);
     float2 k[S], slope[S], R = none, Q = none, v;
     const int form = n < S || t0 == 0 ? kCareful : kMarks && resets != 0 ? kResets : kPlain;  // either end
     // the map of (1 - k) G past these steps to the same in front of them
@@ -826,7 +838,7 @@ __global__ void __launch_bounds__(32 * kWarps, kPerSm) scan_bwd_kernel(const Bwd
         R = join2(R, k[i]);
         Q = sub2(g, __fmul2_rn(k[i], g));
         if (how.value >= kResets && (resets >> i & 1)) {
-          R = all;
+          R = forget();
           Q = none;
         }
       }
@@ -837,7 +849,7 @@ __global__ void __launch_bounds__(32 * kWarps, kPerSm) scan_bwd_kernel(const Bwd
       fold(std::integral_constant<int, kResets>());
     else
       fold(std::integral_constant<int, kCareful>());
-    v = exchange<LPR, true>(maps, cta_maps, round, size, rank, waits, R, Q, carry);
+    v = exchange<LPR, true, kMarks>(maps, cta_maps, round, size, rank, waits, R, Q, carry);
     auto put = [&](auto how) {
       T* og = dgate + (t0 + S - 1) * p.lddg;
       T* oc = dcand + (t0 + S - 1) * p.lddc;

@@ -90,3 +90,72 @@ def test_masked_tokens_keep_a_large_state(t, dname):
     gate[:], cand[:] = INF, -3e38
     h, last = t3.t3_gated_scan_fwd(gate, cand, h0)
     assert torch.equal(last, h0) and torch.equal(h, h0.to(DT[dname])[:, None].expand_as(h))
+
+
+def _documents(r):
+    """The document's number of each token."""
+    return np.cumsum(_np(r) != 0, 1)
+
+
+def _poison(rng, r):
+    """One token in every third document of each sequence, as (sequence, token, document)."""
+    docs, out = _documents(r), []
+    for s in range(docs.shape[0]):
+        for k in np.unique(docs[s]):
+            if rng.random() < 0.4:
+                out.append((s, int(rng.choice(np.flatnonzero(docs[s] == k))), k))
+    return docs, out
+
+
+@pytest.mark.parametrize("dname", ["bf16", "f32"])
+@pytest.mark.parametrize("b,t,d", SHAPES)
+@pytest.mark.parametrize("value", [NAN, INF])
+def test_a_reset_stops_a_state_that_is_not_finite(value, b, t, d, dname):
+    gate, cand, h0, _, _ = _make(b * t + d, b, t, d, dname)
+    rng = np.random.default_rng(t + d)
+    r = _resets(rng, b, t, 30)
+    r[:, 0] = 1  # h0 may be anything, too
+    r[-1, t - 1] = 1
+    docs, bad = _poison(rng, r)
+    dirty, h0d = cand.clone(), h0.clone()
+    h0d[:, ::2] = value
+    fine = np.ones((b, t, d), bool)
+    for s, at, k in bad:
+        dirty[s, at, ::3] = value
+        end = at + int((docs[s, at:] == k).sum())
+        fine[s, at:end, ::3] = False
+    h, last = t3.t3_gated_scan_fwd(gate, dirty, h0d, r)
+    want, _, err = ref.scan(_np(gate), _np(cand), _np(h0), _np(r))
+    _within(h, want, err, ref.HALF_ULP[dname], fine, "h")
+    _within(last, want[:, -1], err[:, -1], ref.U, fine[:, -1], "h_last")
+    for s, at, k in bad:  # and it shows in its own document
+        assert not torch.isfinite(h[s, at, ::3]).any()
+
+
+@pytest.mark.parametrize("dname", ["bf16", "f32"])
+@pytest.mark.parametrize("b,t,d", SHAPES)
+@pytest.mark.parametrize("value", [NAN, INF])
+def test_a_reset_stops_a_gradient_that_is_not_finite(value, b, t, d, dname):
+    gate, cand, h0, dh, dl = _make(b * t + d, b, t, d, dname)
+    rng = np.random.default_rng(t + d + 1)
+    r = _resets(rng, b, t, 30)
+    r[-1, t - 1] = 1
+    r[0, 0] = 1
+    docs, bad = _poison(rng, r)
+    h, _ = t3.t3_gated_scan_fwd(gate, cand, h0, r)
+    dirty, dld = dh.clone(), dl.clone()
+    fine = np.ones((b, t, d), bool)
+    for s, at, k in bad:
+        dirty[s, at, ::3] = value
+        fine[s, at + 1 - int((docs[s, :at + 1] == k).sum()):at + 1, ::3] = False
+    dld[-1, 1::3] = value  # a last document of one token
+    fine[-1, t - 1, 1::3] = False
+    got = t3.t3_gated_scan_bwd(gate, cand, h, dirty, h0, r, dld)
+    rs = _np(r)
+    prior = np.concatenate([_np(h0)[:, None], _np(h)[:, :-1]], 1) * (rs == 0)[..., None]
+    want, err = ref.scan_bwd(_np(gate), _np(cand), prior, _np(dh), rs, _np(dl))
+    for name, x, w, e in zip(("dgate", "dcand"), got, want, err):
+        _within(x, w, e, ref.HALF_ULP[dname], fine, name)
+    first = fine[:, 0] | (rs[:, :1] != 0)
+    _within(got[2], want[2], err[2], ref.U, first, "dh0")
+    assert torch.all(got[2][0] == 0)
