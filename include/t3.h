@@ -356,8 +356,8 @@ int t3_gated_scan_fwd(const void* gate, int64_t ldg, const void* cand, int64_t l
  *         dh_last joins at the last token),
  *   dcand_t = (1 - a_t) G_t,  dgate_t = G_t (h'_{t-1} - cand_t) a_t (1 - a_t),
  *   dh0 = a_0 G_0 (0 where token 0 resets; dh0 may be NULL).
- * dgate and dcand take strides as gate and cand do; a gate whose sigmoid is
- * exactly 0 or 1 gets dgate = 0.  length = 0 copies dh_last (or zeros) to dh0.
+ * From token to token a G is taken as G - (1 - a) G, off by a rounding of G however small a
+ * is; dh0 = a_0 G_0 keeps its own relative precision.
  */
 int t3_gated_scan_bwd(const void* gate, int64_t ldg, const void* cand, int64_t ldc, const void* h,
                       int64_t ldh, const void* dh, int64_t lddh, const float* h0,

@@ -170,6 +170,11 @@ __device__ __forceinline__ float below_inf(float e) {
 }
 __device__ __forceinline__ float take_of(float f) { return rcp_approx(1.0f + ex2_approx(1.4426950408889634f * f)); }
 
+// (1 - k) g, with slope = k (1 - k): to a few roundings however near k is to 1.
+__device__ __forceinline__ float past(float k, float slope, float g) {
+  return k < 0.5f ? fmaf(-k, g, g) : slope / k * g;
+}
+
 // One step of the state.
 __device__ __forceinline__ float step(float h, float k, float c) { return fmaf(k, c - h, h); }
 
@@ -864,6 +869,11 @@ __global__ void __launch_bounds__(32 * kWarps, kPerSm) scan_bwd_kernel(const Bwd
         const float2 diff = sub2(before, read_pair<T, LPR, kPair<T, CH>>(st.a[1] + at, i, col));
         const float2 df = masked2(slope[i], __fmul2_rn(__fmul2_rn(g, slope[i]), diff));
         v = reset ? none : sub2(g, dc);
+        if (how.value == kCareful && t0 + i == 0 && p.dh0 && live) {
+          // a G leaves the sequence: with a = slope / k where 1 - k would cancel
+          p.dh0[b * p.width + ch] = reset ? 0.0f : past(k[i].x, slope[i].x, g.x);
+          if (second) p.dh0[b * p.width + ch + kNext] = reset ? 0.0f : past(k[i].y, slope[i].y, g.y);
+        }
         if (live && (how.value < kCareful || i < n)) {
           write_pair<T, LPR, kPair<T, CH>>(og, df, second);
           write_pair<T, LPR, kPair<T, CH>>(oc, dc, second);
@@ -880,7 +890,7 @@ __global__ void __launch_bounds__(32 * kWarps, kPerSm) scan_bwd_kernel(const Bwd
   }
   copy_wait<0>();
   if (size > 1) cluster_meet();  // nothing is on its way to a CTA that has left
-  if (p.dh0 && live && rank == 0 && warp == 0 && group == 0) {
+  if (rounds == 0 && p.dh0 && live && rank == 0 && warp == 0 && group == 0) {  // no tokens
     p.dh0[b * p.width + ch] = carry[0];
     if (second) p.dh0[b * p.width + ch + kNext] = carry[1];
   }

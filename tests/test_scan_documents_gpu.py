@@ -159,3 +159,27 @@ def test_a_reset_stops_a_gradient_that_is_not_finite(value, b, t, d, dname):
     first = fine[:, 0] | (rs[:, :1] != 0)
     _within(got[2], want[2], err[2], ref.U, first, "dh0")
     assert torch.all(got[2][0] == 0)
+
+
+@pytest.mark.parametrize("dname", ["bf16", "f32"])
+@pytest.mark.parametrize("t", [1, 5, 9, 40, 300, 1300])
+@pytest.mark.parametrize("mean", [-8.0, -12.0, -20.0, 0.0, 9.0])
+def test_the_gradient_of_h0_keeps_its_relative_precision(mean, t, dname):
+    """dh0 = a_0 G_0 with a_0 far below 1: a_0's own relative error (the
+    logistic function's), two roundings, and a_0 times the error of G_0."""
+    gate, cand, h0, dh, dl = _make(t, 2, t, 66, dname)
+    gate = (gate * 0.1 + mean).to(DT[dname])
+    h, _ = t3.t3_gated_scan_fwd(gate, cand, h0)
+    got = t3.t3_gated_scan_bwd(gate, cand, h, dh, h0, None, dl)[2]
+    g, e = _np(dl), np.zeros((2, 66))
+    gt, dn = _np(gate), _np(dh)
+    for i in reversed(range(t)):
+        e = e + 3 * ref.U * (np.abs(g) + np.abs(dn[:, i]))
+        g = g + dn[:, i]
+        a, kerr = ref.sigmoid(gt[:, i]), ref.logistic_error(gt[:, i])
+        if i == 0:
+            e = a * (e + (kerr + 4 * ref.U) * np.abs(g))
+        else:
+            e = a * e + 3 * (kerr * (1 - a) + ref.U) * np.abs(g)
+        g = a * g
+    _within(got, g, e, ref.U, np.ones((2, 66), bool), "dh0")
