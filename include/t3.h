@@ -356,6 +356,8 @@ int t3_gated_scan_fwd(const void* gate, int64_t ldg, const void* cand, int64_t l
  *         dh_last joins at the last token),
  *   dcand_t = (1 - a_t) G_t,  dgate_t = G_t (h'_{t-1} - cand_t) a_t (1 - a_t),
  *   dh0 = a_0 G_0 (0 where token 0 resets; dh0 may be NULL).
+ * h'_{t-1} is read from h as it was stored (token 0's from h0): with bf16 rows its rounding adds up to
+ * 2^-8 |G_t h'_{t-1}| a_t (1 - a_t) to dgate, and nothing to dcand and dh0.
  * From token to token a G is taken as G - (1 - a) G, off by a rounding of G however small a
  * is; dh0 = a_0 G_0 keeps its own relative precision.
  */
