@@ -292,7 +292,8 @@ int t3_gemm_bwd_dw_scaled_noalloc(const int8_t* A, const int8_t* dY, void* dW, i
  *   rstd[r] = 1 / sqrt(mean_c(s^2) + eps),   y = s * rstd[r] * gamma[c],
  *   row_scale[r] = max_c |y| / 127,
  *   q = rint(u * (127 / max_c |u|)) with u = s * gamma (a float product), ties
- *   to even, clamped to [-127, 127]; y / row_scale up to rounding.
+ *   to even, clamped to [-127, 127]; y / row_scale up to rounding.  Where 127 /
+ *   max_c |u| would pass the float range (below 3.7e-37) u counts 2^64 times.
  * q [rows][cols] (dense) and row_scale are what the products take.  gamma [cols]
  * NULL stands for ones.  sum_out (stride lds) receives s, the residual stream, and may be
  * x's or residual's buffer with the same stride; rstd is kept for the

@@ -68,16 +68,22 @@ struct BwdArgs {
   int groups;      // row groups a CTA (norm_bwd_kernel)
 };
 
-__device__ __forceinline__ int quant(float u, float inv) {
-  const int q = __float2int_rn(__fmul_rn(u, inv));  // NaN (0 * inf) gives 0
+// Rows whose largest element is below kSmallRow are quantized 2^64 times larger, since 127 /
+// max|u| would pass the float range; a power of two changes no rounding.
+constexpr float kSmallRow = 7.888609e-31f;  // 2^-100
+constexpr float kSmallUp = 18446744073709551616.0f;
+
+__device__ __forceinline__ int quant(float u, float inv, float up) {
+  const int q = __float2int_rn(__fmul_rn(__fmul_rn(u, up), inv));  // NaN (of a row that is not finite) gives 0
   return q > 127 ? 127 : (q < -127 ? -127 : q);
 }
 
-// 127 / max|u|, or 0 for a row of zeros or one that is not finite: an element
+// 127 / max|u up|, or 0 for a row of zeros or one that is not finite: an element
 // of u is not, or the squares overflow their sum.
-__device__ __forceinline__ float inverse_of(float ssq, float amax) {
+__device__ __forceinline__ float inverse_of(float ssq, float amax, float& up) {
   const bool finite = ssq < __int_as_float(0x7f800000) && amax < __int_as_float(0x7f800000);
-  return finite && amax > 0.0f ? __fdiv_rn(127.0f, amax) : 0.0f;
+  up = amax < kSmallRow ? kSmallUp : 1.0f;
+  return finite && amax > 0.0f ? __fdiv_rn(127.0f, __fmul_rn(amax, up)) : 0.0f;
 }
 
 // One thread: the row's scale (NaN where it is not finite) and rstd.
@@ -255,18 +261,18 @@ __global__ void __launch_bounds__(fwd_threads(NV * VEC)) norm_fwd_kernel(const F
     }
     fetch(row + gridDim.x);
     cta_reduce(ssq, amax, sm[phase]);
-    const float inv = inverse_of(ssq, amax);
+    float up;
+    const float inv = inverse_of(ssq, amax, up);
     if (threadIdx.x == 0) put_scales(p, row, ssq, amax);
     int8_t* q = p.q + row * p.cols;
-    // u * inv within [-127, 127]: not for rows that are not finite (codes 0) nor
-    // for maxima so small that 127 / max overflows
-    const bool plain = inv > 0.0f && inv < __int_as_float(0x7f800000);
+    // u * inv within [-127, 127]: not for rows that are not finite (codes 0) nor small ones
+    const bool plain = inv > 0.0f && up == 1.0f;
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
       const int k = at.head + static_cast<int>(v * lanes + threadIdx.x) * VEC;
       if (k >= at.end) break;
       if constexpr (VEC == 1) {
-        q[k] = static_cast<int8_t>(quant(u[v][0], inv));
+        q[k] = static_cast<int8_t>(quant(u[v][0], inv, up));
       } else {
         uint32_t w[VEC / 4];
 #pragma unroll
@@ -277,7 +283,7 @@ __global__ void __launch_bounds__(fwd_threads(NV * VEC)) norm_fwd_kernel(const F
             w[j] = 0;
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-              w[j] |= static_cast<uint32_t>(quant(u[v][4 * j + i], inv) & 0xFF) << (8 * i);
+              w[j] |= static_cast<uint32_t>(quant(u[v][4 * j + i], inv, up) & 0xFF) << (8 * i);
           }
         }
         if constexpr (VEC == 8)
@@ -286,7 +292,7 @@ __global__ void __launch_bounds__(fwd_threads(NV * VEC)) norm_fwd_kernel(const F
           *reinterpret_cast<uint32_t*>(q + k) = w[0];
       }
     }
-    if (kOdd && at.has) q[at.one] = static_cast<int8_t>(quant(ue, inv));
+    if (kOdd && at.has) q[at.one] = static_cast<int8_t>(quant(ue, inv, up));
   }
 }
 
@@ -317,7 +323,8 @@ __global__ void __launch_bounds__(1024) norm_fwd_long_kernel(const FwdArgs p) {
       amax = max_nan(amax, fabsf(p.gamma ? __fmul_rn(s[0], __ldg(p.gamma + k)) : s[0]));
     }
     cta_reduce(ssq, amax, sm[phase]);
-    const float inv = inverse_of(ssq, amax);
+    float up;
+    const float inv = inverse_of(ssq, amax, up);
     if (threadIdx.x == 0) put_scales(p, row, ssq, amax);
     for (int64_t k = threadIdx.x; k < p.cols; k += blockDim.x) {
       float s[1];
@@ -326,7 +333,7 @@ __global__ void __launch_bounds__(1024) norm_fwd_long_kernel(const FwdArgs p) {
       else
         s[0] = sum_at(k);
       p.q[row * p.cols + k] =
-          static_cast<int8_t>(quant(p.gamma ? __fmul_rn(s[0], __ldg(p.gamma + k)) : s[0], inv));
+          static_cast<int8_t>(quant(p.gamma ? __fmul_rn(s[0], __ldg(p.gamma + k)) : s[0], inv, up));
     }
   }
 }

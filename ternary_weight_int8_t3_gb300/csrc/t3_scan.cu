@@ -10,7 +10,7 @@
 //   dc_t = k_t G_t,   df_t = G_t (h'_{t-1} - c_t) k_t (1 - k_t)
 //   dh0 = (1 - k_0) G_0.
 // Backward, h' comes from the forward's output: 2 bytes an element for bf16 rows, where a float
-// copy for the gradient would be written and read at 8 more on 18 (both directions).  The
+// copy for the gradient would add 6 to the 18 of both directions.  The
 // rounding costs dgate half of what its own costs (8 x 2048 x 3456, gates around 1.5:
 // relative norm 8.2e-4 for h', 1.66e-3 for dgate's bf16, 1.85e-3 together); a user who needs
 // more keeps gate, candidate and h in float.
