@@ -57,7 +57,6 @@
 // warp of its own and with shorter runs, takes 35 us; runs of 8 and 12 steps in three or
 // four CTAs an SM 45 to 63; of 20 and 24 steps 34 and 42.
 #include <algorithm>
-#include <atomic>
 #include <type_traits>
 
 #include "t3_vec.cuh"
@@ -68,7 +67,6 @@ namespace sc {
 using namespace vec;
 
 constexpr int kWarps = 8;
-constexpr int kMaxCluster = 8;
 // CTAs that share an SM.  Their 64 KB of stages would let three; but the 16
 // steps a lane holds spill at the 80 registers that leaves, and two balance better over
 // the SMs (8 x 2048 x 3456 forward: 57 us with three and 12 steps, 55 with two and
@@ -907,39 +905,6 @@ constexpr int64_t kShort = 8;  // tokens up to which a sequence is not split
 template <class T> constexpr int kFwdSteps = 32 / sizeof(T);
 template <class T> constexpr int kBwdSteps = 16 / sizeof(T);
 
-// Dynamic shared memory of `Fn`, set once per device.
-template <auto Fn>
-int allow_smem(int dev, int bytes) {
-  static std::atomic<bool> done[64];
-  if (!done[dev].load(std::memory_order_acquire)) {
-    if (cudaFuncSetAttribute(Fn, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess) return T3_ECUDA;
-    done[dev].store(true, std::memory_order_release);
-  }
-  return T3_OK;
-}
-
-// How many clusters of c CTAs of `Fn` are resident at once (cached per device).
-template <auto Fn>
-int max_clusters(int dev, int c, size_t smem) {
-  static std::atomic<int> cache[64][kMaxCluster + 1];
-  int n = cache[dev][c].load(std::memory_order_acquire);
-  if (n > 0) return n;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = static_cast<unsigned>(c);
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(c), 1, 1);
-  cfg.blockDim = dim3(32 * kWarps, 1, 1);
-  cfg.dynamicSmemBytes = smem;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  if (cudaOccupancyMaxActiveClusters(&n, Fn, &cfg) != cudaSuccess || n < 1) return 0;
-  cache[dev][c].store(n, std::memory_order_release);
-  return n;
-}
-
 // Rows of 32 channels fetch half as much with each access: they have to win by
 // this factor (estimated at 1.18 to 1.2 they take 94 us for 102 in 8 x 2048 x 2560
 // backward, at 1.17 112 for 108 in 8 x 2048 x 3456).
@@ -960,7 +925,7 @@ Plan plan(int dev, int64_t tiles, int64_t length, int rows, int smem, int per_ct
   Plan best{0, 0.0};
   for (int c = 1; c <= kMaxCluster; ++c) {
     if (c > 1 && (c - 1) * static_cast<int64_t>(rows) >= length) break;  // CTAs without steps
-    const int n = max_clusters<Fn>(dev, c, smem + (c > 1 ? c * per_cta : 0));
+    const int n = max_clusters<Fn>(dev, c, 32 * kWarps, smem + (c > 1 ? c * per_cta : 0));
     if (n < 1) continue;
     const int64_t full = tiles / n, left = tiles % n, rounds = (length + c * rows - 1) / (c * rows);
     // a last wave that is not full has the SMs more to itself
@@ -977,7 +942,7 @@ Plan plan_shared(int dev, int64_t tiles, int64_t length, int rows, int smem, int
   Plan best{0, 0.0};
   const int64_t rounds = (length + rows - 1) / rows;
   for (int c = 2; c <= kMaxCluster; ++c) {
-    const int64_t n = std::min<int64_t>(max_clusters<Fn>(dev, c, smem + c * per_cta), tiles / c);
+    const int64_t n = std::min<int64_t>(max_clusters<Fn>(dev, c, 32 * kWarps, smem + c * per_cta), tiles / c);
     if (n < 1) continue;
     const double cost = static_cast<double>((tiles + n - 1) / n) * rounds / c;
     if (best.cluster == 0 || cost < best.cost) best = {c, cost, n};

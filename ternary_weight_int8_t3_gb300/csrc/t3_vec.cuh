@@ -5,6 +5,7 @@
 #pragma once
 #include <cuda_bf16.h>
 
+#include <atomic>
 #include <cstdint>
 
 #include "t3.h"
@@ -186,6 +187,50 @@ int launch(void (*fn)(Params...), int64_t grid, int threads, size_t smem, cudaSt
     return T3_ECUDA;
   }
   return T3_OK;
+}
+
+constexpr int kMaxCluster = 8;  // CTAs a cluster, the portable limit
+
+// Host queries in front of a launch.  One that fails is not kept, and takes its
+// error out of the runtime's record: other calls end by looking there.
+
+// Dynamic shared memory of `Fn`, set once per device.
+template <auto Fn>
+int allow_smem(int dev, int bytes) {
+  static std::atomic<bool> done[64];
+  if (!done[dev].load(std::memory_order_acquire)) {
+    if (cudaFuncSetAttribute(Fn, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess) {
+      cudaGetLastError();
+      return T3_ECUDA;
+    }
+    done[dev].store(true, std::memory_order_release);
+  }
+  return T3_OK;
+}
+
+// How many clusters of c CTAs of `Fn` are resident at once, asked once per device.
+template <auto Fn>
+int max_clusters(int dev, int c, int threads, size_t smem) {
+  static std::atomic<int> cache[64][kMaxCluster + 1];  // the answer + 1
+  int n = cache[dev][c].load(std::memory_order_acquire);
+  if (n > 0) return n - 1;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = static_cast<unsigned>(c);
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(c), 1, 1);
+  cfg.blockDim = dim3(static_cast<unsigned>(threads), 1, 1);
+  cfg.dynamicSmemBytes = smem;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (cudaOccupancyMaxActiveClusters(&n, Fn, &cfg) != cudaSuccess) {
+    cudaGetLastError();
+    return 0;
+  }
+  cache[dev][c].store(n + 1, std::memory_order_release);
+  return n;
 }
 
 __host__ inline bool aligned(const void* p, int64_t bytes) {
