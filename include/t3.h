@@ -400,6 +400,9 @@ int t3_gemm_fwd_act(const int8_t* A, const uint8_t* Wp, void* C, int64_t M, int6
 /* Bytes of scratch that t3_gemm_fwd_act can use for a product of these sizes: 0
  * where its rows are whole 16-byte pieces anyway. */
 int64_t t3_gemm_fwd_act_scratch(int64_t M, int64_t N, int64_t K);
+/* The same under the present limit of small products (t3_set_small_product_limit):
+ * 0, too, for those, which the CUDA cores take as they lie. */
+int64_t t3_gemm_fwd_act_scratch_now(int64_t M, int64_t N, int64_t K);
 
 /*
  * t3_act_bwd -- the gradient of that epilogue: for dy, the gradient of C, and

@@ -107,8 +107,9 @@ def load():
             f = getattr(lib, name)
             f.argtypes = types
             f.restype = ctypes.c_int
-        lib.t3_gemm_fwd_act_scratch.argtypes = [i64, i64, i64]
-        lib.t3_gemm_fwd_act_scratch.restype = i64
+        for f in (lib.t3_gemm_fwd_act_scratch, lib.t3_gemm_fwd_act_scratch_now):
+            f.argtypes = [i64, i64, i64]
+            f.restype = i64
         lib.t3_colsum_workspace.argtypes = [i64, i64]
         lib.t3_colsum_workspace.restype = i64
         lib.t3_version.argtypes = []
@@ -665,16 +666,12 @@ def t3_gated_scan_bwd(gate, cand, h, dh, h0=None, resets=None, dh_last=None, dga
     return dgate, dcand, dh0
 
 
-# Products up to the library's default limit run on the CUDA cores as they lie.
-_SMALL_MACS = 1 << 26
-
-
 def t3_gemm_fwd_act(A, Wp, K=None, row_scale=None, col_scale=None, bias=None, act=T3_ACT_NONE,
                     residual=None, kind=T3_OUT_F32, C=None, pre=None, workspace=None, scratch=None, stream=None):
     """C = act(z) + residual with z = A . W scaled per row and column plus
     bias; `pre`, when given, receives z for t3_act_bwd.  kind: T3_OUT_F32 or
     T3_OUT_BF16, the type of C, residual and pre [M][N].  workspace: int32
-    [M][N], and scratch: uint8 of t3_gemm_fwd_act_scratch(M, N, K), are allocated
+    [M][N], and scratch: uint8 of t3_gemm_fwd_act_scratch_now(M, N, K), are allocated
     when the call may need them and none is given."""
     torch = _torch()
     if not isinstance(A, torch.Tensor) or not A.is_cuda or A.dim() != 2 or Wp.dim() != 2:
@@ -696,12 +693,13 @@ def t3_gemm_fwd_act(A, Wp, K=None, row_scale=None, col_scale=None, bias=None, ac
     if scratch is not None:
         room = scratch.numel()
         ps = _dense(scratch, torch.uint8, dev, (room,), "scratch")
-    elif M > 32 and (K % 64 or N % 8) and M * N * K > _SMALL_MACS:
-        room = load().t3_gemm_fwd_act_scratch(M, N, K)
-        scratch = _empty(room, torch.uint8, dev, stream)
-        ps = scratch.data_ptr()
     else:
         ps = None
+        if M > 32 and (K % 64 or N % 8):
+            room = load().t3_gemm_fwd_act_scratch_now(M, N, K)
+            if room:
+                scratch = _empty(room, torch.uint8, dev, stream)
+                ps = scratch.data_ptr()
     _launch("t3_gemm_fwd_act", dev, stream, _dense(A, torch.int8, dev, (M, K), "A"),
             _dense(Wp, torch.uint8, dev, (N, KB), "Wp"), _dense(C, dtype, dev, shape, "C"), M, N, K,
             _dense(row_scale, f32, dev, (M,), "row_scale"), _dense(col_scale, f32, dev, (N,), "col_scale"),

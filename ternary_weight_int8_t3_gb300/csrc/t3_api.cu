@@ -669,6 +669,11 @@ int64_t t3_gemm_fwd_act_scratch(int64_t M, int64_t N, int64_t K) {
   return aligned_layout(M, N, K).bytes;
 }
 
+int64_t t3_gemm_fwd_act_scratch_now(int64_t M, int64_t N, int64_t K) {
+  const int64_t bytes = t3_gemm_fwd_act_scratch(M, N, K);
+  return bytes > 0 && small_product(M, N, K, true) ? 0 : bytes;
+}
+
 int t3_gemm_fwd_act(const int8_t* A, const uint8_t* Wp, void* C, int64_t M, int64_t N, int64_t K,
                     const float* row_scale, const float* col_scale, const float* bias, int act,
                     const void* residual, void* pre, int out_kind, int32_t* workspace, void* scratch,
