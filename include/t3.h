@@ -387,7 +387,7 @@ enum { T3_ACT_NONE = 0, T3_ACT_RELU = 1, T3_ACT_RELU2 = 2, T3_ACT_SILU = 3, T3_A
  * <= 65536, and for small products of many tiles.  Otherwise the int32 product
  * is taken first, into `workspace` (DEVICE int32 [M][N]) or, for T3_OUT_F32
  * without one, into C; T3_OUT_BF16 returns T3_EINVAL there without a
- * workspace.  scratch (DEVICE, 16-byte aligned, may be NULL) of at least
+ * workspace (t3_gemm_fwd_act_workspace tells).  scratch (DEVICE, 16-byte aligned, may be NULL) of at least
  * t3_gemm_fwd_act_scratch(M, N, K) bytes makes products with M > 32 and odd
  * rows several times faster: they are laid out aligned there first.
  * Sizes and overflow rules are those of t3_gemm_fwd_scaled.
@@ -403,6 +403,12 @@ int64_t t3_gemm_fwd_act_scratch(int64_t M, int64_t N, int64_t K);
 /* The same under the present limit of small products (t3_set_small_product_limit):
  * 0, too, for those, which the CUDA cores take as they lie. */
 int64_t t3_gemm_fwd_act_scratch_now(int64_t M, int64_t N, int64_t K);
+/* int32 entries of workspace that t3_gemm_fwd_act takes for these arguments and this
+ * much scratch (16-byte aligned): M * N, or 0 where a call without one works; a
+ * negative status where the device cannot be asked. */
+int64_t t3_gemm_fwd_act_workspace(const int8_t* A, const uint8_t* Wp, const void* C, int64_t M, int64_t N,
+                                  int64_t K, const void* residual, const void* pre, int out_kind,
+                                  int64_t scratch_bytes);
 
 /*
  * t3_act_bwd -- the gradient of that epilogue: for dy, the gradient of C, and

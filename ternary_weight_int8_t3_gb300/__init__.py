@@ -110,6 +110,8 @@ def load():
         for f in (lib.t3_gemm_fwd_act_scratch, lib.t3_gemm_fwd_act_scratch_now):
             f.argtypes = [i64, i64, i64]
             f.restype = i64
+        lib.t3_gemm_fwd_act_workspace.argtypes = [p, p, p, i64, i64, i64, p, p, i32, i64]
+        lib.t3_gemm_fwd_act_workspace.restype = i64
         lib.t3_colsum_workspace.argtypes = [i64, i64]
         lib.t3_colsum_workspace.restype = i64
         lib.t3_version.argtypes = []
@@ -511,6 +513,15 @@ def _bind(name):
     return fn
 
 
+def _on(dev, name, *args):
+    """The library's answer on device number `dev`."""
+    fn = _fns.get(name) or _bind(name)
+    if dev == _device():
+        return fn(*args)
+    with _torch().cuda.device(dev):
+        return fn(*args)
+
+
 def _launch(name, dev, stream, *args):
     """Calls the library on device number `dev`, on its current stream unless one is given."""
     fn = _fns.get(name) or _bind(name)
@@ -671,8 +682,8 @@ def t3_gemm_fwd_act(A, Wp, K=None, row_scale=None, col_scale=None, bias=None, ac
     """C = act(z) + residual with z = A . W scaled per row and column plus
     bias; `pre`, when given, receives z for t3_act_bwd.  kind: T3_OUT_F32 or
     T3_OUT_BF16, the type of C, residual and pre [M][N].  workspace: int32
-    [M][N], and scratch: uint8 of t3_gemm_fwd_act_scratch_now(M, N, K), are allocated
-    when the call may need them and none is given."""
+    [M][N] where t3_gemm_fwd_act_workspace asks for one, and scratch: uint8 of t3_gemm_fwd_act_scratch_now(M, N, K), are allocated
+    where none is given."""
     torch = _torch()
     if not isinstance(A, torch.Tensor) or not A.is_cuda or A.dim() != 2 or Wp.dim() != 2:
         raise TypeError("A and Wp must be 2-D CUDA tensors")
@@ -687,12 +698,12 @@ def t3_gemm_fwd_act(A, Wp, K=None, row_scale=None, col_scale=None, bias=None, ac
     dtype = torch.bfloat16 if kind == T3_OUT_BF16 else f32
     if C is None:
         C = _empty(shape, dtype, dev, stream)
-    if workspace is None and kind == T3_OUT_BF16:
-        workspace = _empty(shape, torch.int32, dev, stream)
     room = 0
     if scratch is not None:
         room = scratch.numel()
         ps = _dense(scratch, torch.uint8, dev, (room,), "scratch")
+        if ps % 16:
+            room = 0  # the library does not use it either
     else:
         ps = None
         if M > 32 and (K % 64 or N % 8):
@@ -700,11 +711,18 @@ def t3_gemm_fwd_act(A, Wp, K=None, row_scale=None, col_scale=None, bias=None, ac
             if room:
                 scratch = _empty(room, torch.uint8, dev, stream)
                 ps = scratch.data_ptr()
-    _launch("t3_gemm_fwd_act", dev, stream, _dense(A, torch.int8, dev, (M, K), "A"),
-            _dense(Wp, torch.uint8, dev, (N, KB), "Wp"), _dense(C, dtype, dev, shape, "C"), M, N, K,
+    pa, pw, pc = _dense(A, torch.int8, dev, (M, K), "A"), _dense(Wp, torch.uint8, dev, (N, KB), "Wp"), _dense(C, dtype, dev, shape, "C")
+    pr, pp = _dense(residual, dtype, dev, shape, "residual"), _dense(pre, dtype, dev, shape, "pre")
+    if workspace is None and kind == T3_OUT_BF16:
+        n = _on(dev, "t3_gemm_fwd_act_workspace", pa, pw, pc, M, N, K, pr, pp, kind, room)
+        if n < 0:
+            raise T3Error(n, "t3_gemm_fwd_act_workspace")
+        if n:
+            workspace = _empty(shape, torch.int32, dev, stream)
+    _launch("t3_gemm_fwd_act", dev, stream, pa, pw, pc, M, N, K,
             _dense(row_scale, f32, dev, (M,), "row_scale"), _dense(col_scale, f32, dev, (N,), "col_scale"),
-            _dense(bias, f32, dev, (N,), "bias"), act, _dense(residual, dtype, dev, shape, "residual"),
-            _dense(pre, dtype, dev, shape, "pre"), kind, _dense(workspace, torch.int32, dev, shape, "workspace"), ps, room)
+            _dense(bias, f32, dev, (N,), "bias"), act, pr, pp, kind,
+            _dense(workspace, torch.int32, dev, shape, "workspace"), ps, room)
     return C
 
 

@@ -412,6 +412,31 @@ AlignedLayout aligned_layout(int64_t M, int64_t N, int64_t K) {
   return l;
 }
 
+// How t3_gemm_fwd_act takes a product: in one kernel of the routes of t3_gemm_fwd that
+// can end in its epilogue; on the CTA pairs behind a layout in scratch (`room`); or as the
+// int32 product in a workspace and the epilogue behind it.
+enum class ActRoute { kGemv, kSmall, kFew, kPairs, kAligned, kTwoKernels };
+
+ActRoute act_route(const int8_t* A, const uint8_t* Wp, const void* C, int64_t M, int64_t N, int64_t K,
+                   const void* residual, const void* pre, int out_kind, bool room, int sms) {
+  if (K == 0) return ActRoute::kTwoKernels;
+  if (M <= kSmallM) {
+    if (gemv_rows(M, N, K) && gemv_fits(M, N, K)) return ActRoute::kGemv;
+    return small_product(M, N, K, false) && few_act_fits(M, N, K, sms) ? ActRoute::kFew : ActRoute::kTwoKernels;
+  }
+  const bool words = word_rows(A, K) && word_rows(Wp, (K + 3) / 4);
+  if (small_product(M, N, K, words || room)) {
+    if (small_act_fits(M, N, sms)) return ActRoute::kSmall;
+    return few_act_fits(M, N, K, sms) ? ActRoute::kFew : ActRoute::kTwoKernels;
+  }
+  auto bulk = [](const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; };
+  const int64_t es = out_kind == T3_OUT_BF16 ? 2 : 4;
+  if (K % 64 == 0 && bulk(A) && bulk(Wp) && bulk(C) && bulk(residual) && bulk(pre) && N * es % 16 == 0 &&
+      ceil_div(K, tc2::BK) <= tc2::kChunkStages && ceil_div(M, tc2::BMP) * ceil_div(N, tc2::BN) <= kMaxDim)
+    return ActRoute::kPairs;
+  return room ? ActRoute::kAligned : ActRoute::kTwoKernels;
+}
+
 // Activations' element types are the output kinds that store them.
 bool valid_dtype(int dtype) { return dtype == T3_OUT_F32 || dtype == T3_OUT_BF16; }
 bool valid_act(int act) { return act >= T3_ACT_NONE && act <= T3_ACT_GELU; }
@@ -669,6 +694,17 @@ int64_t t3_gemm_fwd_act_scratch(int64_t M, int64_t N, int64_t K) {
   return aligned_layout(M, N, K).bytes;
 }
 
+int64_t t3_gemm_fwd_act_workspace(const int8_t* A, const uint8_t* Wp, const void* C, int64_t M, int64_t N,
+                                  int64_t K, const void* residual, const void* pre, int out_kind,
+                                  int64_t scratch_bytes) {
+  if (bad_dims(M, N, K) || M == 0 || N == 0 || out_kind != T3_OUT_BF16) return 0;
+  const DeviceInfo* dev = nullptr;
+  const int st = device_info(&dev);
+  if (st != T3_OK) return st;
+  const bool room = scratch_bytes >= aligned_layout(M, N, K).bytes;
+  return act_route(A, Wp, C, M, N, K, residual, pre, out_kind, room, dev->sms) == ActRoute::kTwoKernels ? M * N : 0;
+}
+
 int64_t t3_gemm_fwd_act_scratch_now(int64_t M, int64_t N, int64_t K) {
   const int64_t bytes = t3_gemm_fwd_act_scratch(M, N, K);
   return bytes > 0 && small_product(M, N, K, true) ? 0 : bytes;
@@ -688,43 +724,38 @@ int t3_gemm_fwd_act(const int8_t* A, const uint8_t* Wp, void* C, int64_t M, int6
   const DeviceInfo* dev = nullptr;
   int st = device_info(&dev);
   if (st != T3_OK) return st;
-  // the routes of t3_gemm_fwd; those that can end in this epilogue do
-  if (K > 0) {
-    const int64_t KB = (K + 3) / 4;
-    const bool words = word_rows(A, K) && word_rows(Wp, KB);
-    const bool tma = K % 64 == 0 && reinterpret_cast<uintptr_t>(A) % 16 == 0 && reinterpret_cast<uintptr_t>(Wp) % 16 == 0;
-    const AlignedLayout lay = aligned_layout(M, N, K);
-    const bool room = scratch && scratch_bytes >= lay.bytes && reinterpret_cast<uintptr_t>(scratch) % 16 == 0;
-    st = T3_EINVAL;
-    if (M <= kSmallM) {
-      if (gemv_rows(M, N, K)) st = launch_gemv_fwd_act(A, Wp, C, e, out_kind, M, N, K, dev->sms, stream);
-      if (st == T3_EINVAL && small_product(M, N, K, false))
-        st = launch_few_act(A, Wp, C, e, out_kind, M, N, K, dev->sms, stream);
-    } else if (small_product(M, N, K, words || room)) {
-      st = launch_small_act(A, Wp, C, e, out_kind, M, N, K, dev->sms, stream);
-      if (st == T3_EINVAL) st = launch_few_act(A, Wp, C, e, out_kind, M, N, K, dev->sms, stream);
-    } else {
-      if (tma) st = run_tc2<kOpFwd>(A, Wp, C, M, N, K, stream, out_kind, row_scale, col_scale, &e);
-      if (st == T3_EINVAL && room) {
-        // rows that TMA cannot address cost the pipelines several times as much as
-        // laying them out once: operands padded with zeros to whole 64-element
-        // groups, and an int32 result of whole 16-byte rows where C, residual or pre are not
-        uint8_t* base = static_cast<uint8_t*>(scratch);
-        const int8_t* A2 = tma ? A : reinterpret_cast<int8_t*>(base + lay.a);
-        uint8_t* W2 = base + lay.w;
-        st = launch_align_rows(tma ? nullptr : reinterpret_cast<const uint8_t*>(A), M, K, base + lay.a, M, lay.K, Wp, N,
-                               KB, W2, lay.N, lay.K / 4, stream);
-        if (st != T3_OK) return st;
-        st = tma ? T3_EINVAL : run_tc2<kOpFwd>(A2, W2, C, M, N, lay.K, stream, out_kind, row_scale, col_scale, &e);
-        if (st == T3_EINVAL) {
-          int32_t* x = reinterpret_cast<int32_t*>(base + lay.x);
-          st = run_tc2<kOpFwd>(A2, W2, x, M, lay.N, lay.K, stream);
-          if (st == T3_OK) st = launch_epilogue(x, lay.N, C, e, M, N, out_kind, dev->sms, stream);
-        }
+  const AlignedLayout lay = aligned_layout(M, N, K);
+  const bool room = scratch && scratch_bytes >= lay.bytes && reinterpret_cast<uintptr_t>(scratch) % 16 == 0;
+  st = T3_EINVAL;
+  switch (act_route(A, Wp, C, M, N, K, residual, pre, out_kind, room, dev->sms)) {
+    case ActRoute::kGemv: st = launch_gemv_fwd_act(A, Wp, C, e, out_kind, M, N, K, dev->sms, stream); break;
+    case ActRoute::kSmall: st = launch_small_act(A, Wp, C, e, out_kind, M, N, K, stream); break;
+    case ActRoute::kFew: st = launch_few_act(A, Wp, C, e, out_kind, M, N, K, stream); break;
+    case ActRoute::kPairs:
+      st = run_tc2<kOpFwd>(A, Wp, C, M, N, K, stream, out_kind, row_scale, col_scale, &e);
+      break;
+    case ActRoute::kAligned: {
+      // rows that TMA cannot address cost the pipelines several times as much as
+      // laying them out once: operands padded with zeros to whole 64-element
+      // groups, and an int32 result of whole 16-byte rows where C, residual or pre are not
+      const bool tma = K % 64 == 0 && reinterpret_cast<uintptr_t>(A) % 16 == 0 && reinterpret_cast<uintptr_t>(Wp) % 16 == 0;
+      uint8_t* base = static_cast<uint8_t*>(scratch);
+      const int8_t* A2 = tma ? A : reinterpret_cast<int8_t*>(base + lay.a);
+      uint8_t* W2 = base + lay.w;
+      st = launch_align_rows(tma ? nullptr : reinterpret_cast<const uint8_t*>(A), M, K, base + lay.a, M, lay.K, Wp, N,
+                             (K + 3) / 4, W2, lay.N, lay.K / 4, stream);
+      if (st != T3_OK) return st;
+      st = tma ? T3_EINVAL : run_tc2<kOpFwd>(A2, W2, C, M, N, lay.K, stream, out_kind, row_scale, col_scale, &e);
+      if (st == T3_EINVAL) {
+        int32_t* x = reinterpret_cast<int32_t*>(base + lay.x);
+        st = run_tc2<kOpFwd>(A2, W2, x, M, lay.N, lay.K, stream);
+        if (st == T3_OK) st = launch_epilogue(x, lay.N, C, e, M, N, out_kind, dev->sms, stream);
       }
+      break;
     }
-    if (st != T3_EINVAL) return st;
+    case ActRoute::kTwoKernels: break;
   }
+  if (st != T3_EINVAL) return st;
   int32_t* x = workspace ? workspace : (out_kind == T3_OUT_F32 ? static_cast<int32_t*>(C) : nullptr);
   if (!x) return T3_EINVAL;
   st = t3_gemm_fwd(A, Wp, x, M, N, K, stream);

@@ -207,15 +207,18 @@ int launch_mr(const int8_t* A, const uint8_t* Wp, const Out& out, int M, int N, 
   return cudaGetLastError() == cudaSuccess ? T3_OK : T3_ECUDA;
 }
 
+// A's copy: 16-k groups, padded to whole 16-byte chunks of codes (64 k)
+int64_t k_groups(int64_t K) { return (K + 63) / 64 * 4; }
+int padded_rows(int64_t M) { return M <= 1 ? 1 : M <= 2 ? 2 : M <= 4 ? 4 : 8; }
+int64_t copy_bytes(int64_t M, int64_t K) { return padded_rows(M) * k_groups(K) * 16; }
+
 template <class Out>
 int launch_any(const int8_t* A, const uint8_t* Wp, const Out& out, int64_t M, int64_t N, int64_t K, int sms,
                cudaStream_t s) {
   const int64_t KB = (K + 3) / 4;
-  // 16-k groups, padded to whole 16-byte chunks of codes (64 k)
-  const int64_t groups = (K + 63) / 64 * 4;
-  const int mr = M <= 1 ? 1 : M <= 2 ? 2 : M <= 4 ? 4 : 8;
-  const int64_t smem = static_cast<int64_t>(mr) * groups * 16;
-  if (M < 1 || M > 8 || smem > kMaxSmem || N > 2147483647LL) return T3_EINVAL;
+  if (!gemv_fits(M, N, K)) return T3_EINVAL;
+  const int64_t groups = k_groups(K), smem = copy_bytes(M, K);
+  const int mr = padded_rows(M);
   const bool vec = (KB % 16 == 0) && (reinterpret_cast<uintptr_t>(Wp) % 16 == 0);
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return T3_ECUDA;
@@ -241,6 +244,10 @@ int launch_any(const int8_t* A, const uint8_t* Wp, const Out& out, int64_t M, in
 }
 
 }  // namespace gv
+
+bool gemv_fits(int64_t M, int64_t N, int64_t K) {
+  return M >= 1 && M <= 8 && gv::copy_bytes(M, K) <= gv::kMaxSmem && N <= 2147483647LL;
+}
 
 int launch_gemv_fwd(const int8_t* A, const uint8_t* Wp, int32_t* C, int64_t M, int64_t N,
                     int64_t K, int sms, cudaStream_t s) {

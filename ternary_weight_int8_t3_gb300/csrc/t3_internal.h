@@ -73,6 +73,8 @@ int launch_dequant(const int32_t* x, void* out, int64_t rows, int64_t cols, cons
 // launched, when A's copy would not fit its shared-memory budget.
 int launch_gemv_fwd(const int8_t* A, const uint8_t* Wp, int32_t* C, int64_t M, int64_t N,
                     int64_t K, int sms, cudaStream_t s);
+// Whether it takes these rows.
+bool gemv_fits(int64_t M, int64_t N, int64_t K);
 // The same with the epilogue in the kernel that ends each sum.
 int launch_gemv_fwd_act(const int8_t* A, const uint8_t* Wp, void* C, const EpilogueArgs& e, int kind,
                         int64_t M, int64_t N, int64_t K, int sms, cudaStream_t s);
@@ -84,13 +86,15 @@ int launch_gemv_fwd_act(const int8_t* A, const uint8_t* Wp, void* C, const Epilo
 int launch_small(int op, const int8_t* x, const int8_t* y, const uint8_t* wp, int32_t* out,
                  int64_t M, int64_t N, int64_t K, int sms, cudaStream_t s);
 
-// The forward of launch_small with the epilogue in its kernel; T3_EINVAL, with
-// nothing launched, where the tiles are so few that splitting the reduction is faster;
-// launch_few_act splits it over a CTA's warps, T3_EINVAL where it is too long for that.
+// The forward of launch_small with the epilogue in its kernel; not where the tiles
+// are so few that splitting the reduction is faster (small_act_fits).  launch_few_act
+// splits it over a CTA's warps, unless it is too long for that (few_act_fits).
+bool small_act_fits(int64_t M, int64_t N, int sms);
+bool few_act_fits(int64_t M, int64_t N, int64_t K, int sms);
 int launch_small_act(const int8_t* A, const uint8_t* Wp, void* C, const EpilogueArgs& e, int kind, int64_t M,
-                     int64_t N, int64_t K, int sms, cudaStream_t s);
+                     int64_t N, int64_t K, cudaStream_t s);
 int launch_few_act(const int8_t* A, const uint8_t* Wp, void* C, const EpilogueArgs& e, int kind, int64_t M,
-                   int64_t N, int64_t K, int sms, cudaStream_t s);
+                   int64_t N, int64_t K, cudaStream_t s);
 
 // Small-M forward (M <= 32) on the tensor cores.
 int launch_skinny_fwd(const int8_t* A, const uint8_t* Wp, int32_t* C, int64_t M, int64_t N,

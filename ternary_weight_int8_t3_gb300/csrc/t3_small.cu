@@ -480,13 +480,16 @@ Params act_params(const int8_t* A, const uint8_t* Wp, int64_t M, int64_t N, int6
 
 // With two tiles an SM one CTA takes a tile's whole sum and the epilogue with it
 // (1782 x 729 x 243: 17.1 us, against 21.7 split in two and with the epilogue behind).
+bool small_act_fits(int64_t M, int64_t N, int sms) {
+  return (M + smp::kTile - 1) / smp::kTile * ((N + smp::kTile - 1) / smp::kTile) >= 2 * static_cast<int64_t>(sms);
+}
+
 int launch_small_act(const int8_t* A, const uint8_t* Wp, void* C, const EpilogueArgs& e, int kind, int64_t M,
-                     int64_t N, int64_t K, int sms, cudaStream_t s) {
+                     int64_t N, int64_t K, cudaStream_t s) {
   smp::Params p = smp::act_params(A, Wp, M, N, K);
   p.tiles_c = (N + smp::kTile - 1) / smp::kTile;
   p.chunks = (K + smp::kChunk - 1) / smp::kChunk;
   const int64_t grid = (M + smp::kTile - 1) / smp::kTile * p.tiles_c;
-  if (grid < 2 * static_cast<int64_t>(sms)) return T3_EINVAL;
   if (kind == T3_OUT_BF16)
     return vec::launch(smp::small_act_kernel<OutAct<__nv_bfloat16>>, grid, smp::kThreads, 0, s, 1, p,
                        OutAct<__nv_bfloat16>{static_cast<__nv_bfloat16*>(C), e});
@@ -500,13 +503,18 @@ int launch_small_act(const int8_t* A, const uint8_t* Wp, void* C, const Epilogue
 // 5.7 (8.4), 27 x 2000 x 1501 9.7 (10.6), 1000 x 300 x 100 6.0 (7.2); beyond the limits
 // 27 x 1000 x 2001 12.1 (9.3), 32 x 2048 x 2048 10.3 (8.0) and, in two waves, 27 x 7296 x 512
 // 7.7 (6.0).
+bool few_act_fits(int64_t M, int64_t N, int64_t K, int sms) {
+  const int64_t grid = (M + smp::kFewRows - 1) / smp::kFewRows * ((N + smp::kFewCols - 1) / smp::kFewCols);
+  const int64_t wave = 2 * static_cast<int64_t>(sms);
+  return K <= smp::kFewLong && (grid <= wave || (grid + wave - 1) / wave * K <= smp::kFewLong / 2);
+}
+
 int launch_few_act(const int8_t* A, const uint8_t* Wp, void* C, const EpilogueArgs& e, int kind, int64_t M,
-                   int64_t N, int64_t K, int sms, cudaStream_t s) {
+                   int64_t N, int64_t K, cudaStream_t s) {
   smp::Params p = smp::act_params(A, Wp, M, N, K);
   p.tiles_c = (N + smp::kFewCols - 1) / smp::kFewCols;
   p.chunks = (K + smp::kFewChunk - 1) / smp::kFewChunk;
-  const int64_t grid = (M + smp::kFewRows - 1) / smp::kFewRows * p.tiles_c, wave = 2 * static_cast<int64_t>(sms);
-  if (K > smp::kFewLong || (grid > wave && (grid + wave - 1) / wave * K > smp::kFewLong / 2)) return T3_EINVAL;
+  const int64_t grid = (M + smp::kFewRows - 1) / smp::kFewRows * p.tiles_c;
   if (kind == T3_OUT_BF16)
     return vec::launch(smp::few_act_kernel<OutAct<__nv_bfloat16>>, grid, 32 * smp::kFewWarps, 0, s, 1, p,
                        OutAct<__nv_bfloat16>{static_cast<__nv_bfloat16*>(C), e});
