@@ -497,6 +497,14 @@ def _dense(t, dtype, dev, shape, name):
     return t.data_ptr()
 
 
+def _marks(resets, dev, shape):
+    """Address of the resets, uint8 or bool (what a comparison gives)."""
+    torch = _torch()
+    if resets is not None and resets.dtype is torch.bool:
+        resets = resets.view(torch.uint8)
+    return _dense(resets, torch.uint8, dev, shape, "resets")
+
+
 _fns = {}
 _raw_stream = _device = None
 
@@ -624,8 +632,8 @@ def t3_rmsnorm_bwd(dy, s, rstd, gamma=None, dsum=None, dx=None, dgamma=None, wor
 def t3_gated_scan_fwd(gate, cand, h0=None, resets=None, h=None, h_last=None, stream=None):
     """(h, h_last): h_t = a_t h_(t-1) + (1 - a_t) cand_t with a_t =
     sigmoid(gate_t) over [batch][length][width], from the float state h0
-    [batch][width] (None: zeros); resets uint8 [batch][length] marks tokens
-    that start from zero.  gate and cand may be slices of one wider tensor.
+    [batch][width] (None: zeros); resets uint8 or bool [batch][length] marks
+    tokens that start from zero.  gate and cand may be slices of one wider tensor.
     h_last (float32 [batch][width]) may be h0: the state advances in place."""
     torch = _torch()
     dtype = _dtype_of(gate, "gate")
@@ -641,7 +649,7 @@ def t3_gated_scan_fwd(gate, cand, h0=None, resets=None, h=None, h_last=None, str
     pc, ldc = _rows(cand, xt, dev, shape, "cand")
     ph, ldh = _rows(h, xt, dev, shape, "h", out=True)
     _launch("t3_gated_scan_fwd", dev, stream, pg, ldg, pc, ldc, _dense(h0, f32, dev, (batch, width), "h0"),
-            _dense(resets, torch.uint8, dev, (batch, length), "resets"), ph, ldh,
+            _marks(resets, dev, (batch, length)), ph, ldh,
             _dense(h_last, f32, dev, (batch, width), "h_last"), batch, length, width, dtype)
     return h, h_last
 
@@ -671,7 +679,7 @@ def t3_gated_scan_bwd(gate, cand, h, dh, h0=None, resets=None, dh_last=None, dga
     pdc, lddc = _rows(dcand, xt, dev, shape, "dcand", out=True)
     _launch("t3_gated_scan_bwd", dev, stream, pg, ldg, pc, ldc, ph, ldh, pd, ldd,
             _dense(h0, f32, dev, (batch, width), "h0"),
-            _dense(resets, torch.uint8, dev, (batch, length), "resets"),
+            _marks(resets, dev, (batch, length)),
             _dense(dh_last, f32, dev, (batch, width), "dh_last"), pdg, lddg, pdc, lddc,
             _dense(dh0, f32, dev, (batch, width), "dh0"), batch, length, width, dtype)
     return dgate, dcand, dh0

@@ -183,3 +183,17 @@ def test_the_gradient_of_h0_keeps_its_relative_precision(mean, t, dname):
             e = a * e + 3 * (kerr * (1 - a) + ref.U) * np.abs(g)
         g = a * g
     _within(got, g, e, ref.U, np.ones((2, 66), bool), "dh0")
+
+
+def test_resets_from_a_comparison():
+    """resets as torch makes them: bool, the same bytes as uint8."""
+    gate, cand, h0, dh, dl = _make(4, 2, 60, 64, "bf16")
+    ids = torch.arange(60, device="cuda").expand(2, 60) // 13
+    marks = ids != torch.roll(ids, 1, 1)
+    r = marks.to(torch.uint8)
+    got, want = t3.t3_gated_scan_fwd(gate, cand, h0, marks), t3.t3_gated_scan_fwd(gate, cand, h0, r)
+    assert all(torch.equal(x, y) for x, y in zip(got, want))
+    got = t3.t3_gated_scan_bwd(gate, cand, want[0], dh, h0, marks, dl)
+    assert all(torch.equal(x, y) for x, y in zip(got, t3.t3_gated_scan_bwd(gate, cand, want[0], dh, h0, r, dl)))
+    with pytest.raises(ValueError):
+        t3.t3_gated_scan_fwd(gate, cand, h0, marks[:, :-1])
