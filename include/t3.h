@@ -468,6 +468,9 @@ int64_t t3_set_small_product_limit(int64_t macs);
  * T3_EINVAL; asynchronous on `stream`.
  */
 int t3_selftest_wait_timeout(int64_t limit_ns, t3_stream_t stream);
+/* The same for the wait of the recurrence's CTAs on their cluster, which records
+ * (11 << 8) | 7. */
+int t3_selftest_scan_wait_timeout(int64_t limit_ns, t3_stream_t stream);
 
 /* Library version as major*10000 + minor*100 + patch. */
 int t3_version(void);

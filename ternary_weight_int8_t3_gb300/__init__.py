@@ -91,8 +91,9 @@ def load():
         lib.t3_status_string.restype = ctypes.c_char_p
         lib.t3_last_device_error.argtypes = [p, ctypes.POINTER(ctypes.c_int32)]
         lib.t3_last_device_error.restype = ctypes.c_int
-        lib.t3_selftest_wait_timeout.argtypes = [i64, p]
-        lib.t3_selftest_wait_timeout.restype = ctypes.c_int
+        for f in (lib.t3_selftest_wait_timeout, lib.t3_selftest_scan_wait_timeout):
+            f.argtypes = [i64, p]
+            f.restype = ctypes.c_int
         lib.t3_set_small_product_limit.argtypes = [i64]
         lib.t3_set_small_product_limit.restype = i64
         i32 = ctypes.c_int
@@ -781,6 +782,14 @@ def t3_selftest_wait_timeout(limit_ns: int, stream=None):
     s = stream if stream is not None else torch.cuda.current_stream()
     _check(load().t3_selftest_wait_timeout(int(limit_ns), ctypes.c_void_p(s.cuda_stream)),
            "t3_selftest_wait_timeout")
+
+
+def t3_selftest_scan_wait_timeout(limit_ns: int, stream=None):
+    """The same for the recurrence's wait on the other CTAs of a cluster."""
+    torch = _torch()
+    s = stream if stream is not None else torch.cuda.current_stream()
+    _check(load().t3_selftest_scan_wait_timeout(int(limit_ns), ctypes.c_void_p(s.cuda_stream)),
+           "t3_selftest_scan_wait_timeout")
 
 
 def t3_version() -> int:

@@ -876,6 +876,14 @@ int t3_gemm_fwd_bf16(const void* X, const uint8_t* Wp, int32_t* C, float* row_sc
   return launch_tc2_fwd_bf16(p, ma, mw, mo, static_cast<int>(2 * pairs), stream);
 }
 
+int t3_selftest_scan_wait_timeout(int64_t limit_ns, t3_stream_t stream) {
+  if (limit_ns < 1000 || limit_ns > static_cast<int64_t>(kWaitLimitNs)) return T3_EINVAL;
+  const DeviceInfo* dev = nullptr;
+  const int st = device_info(&dev);
+  if (st != T3_OK) return st;
+  return launch_scan_wait_selftest(dev->err_word, static_cast<uint64_t>(limit_ns), stream);
+}
+
 int t3_selftest_wait_timeout(int64_t limit_ns, t3_stream_t stream) {
   if (limit_ns < 1000 || limit_ns > static_cast<int64_t>(kWaitLimitNs)) return T3_EINVAL;
   const DeviceInfo* dev = nullptr;

@@ -143,4 +143,7 @@ int launch_align_rows(const uint8_t* a, int64_t rows_a, int64_t len_a, uint8_t* 
 int launch_act_bwd(const void* dy, const void* z, int act, void* dz, float* dbias, int64_t rows,
                    int64_t cols, int dtype, float* workspace, int sms, cudaStream_t s);
 
+// The recurrence's wait between CTAs, run out on purpose (t3_selftest_scan_wait_timeout).
+int launch_scan_wait_selftest(int* err, uint64_t limit_ns, cudaStream_t s);
+
 }  // namespace t3

@@ -131,7 +131,8 @@ constexpr int kWaitCode = (11 << 8) | 7;
 
 // Waits for a phase of `bar` that peers complete with st.async; bounded like
 // mbar_wait, with the acquire at cluster scope.
-__device__ __forceinline__ void wait_peers(uint64_t* bar, uint32_t parity, Waits& w) {
+__device__ __forceinline__ void wait_peers(uint64_t* bar, uint32_t parity, Waits& w,
+                                           uint64_t limit_ns = kWaitLimitNs) {
   if (w.failed) return;
   uint64_t t0 = 0;
   for (uint32_t spin = 0;; ++spin) {
@@ -145,13 +146,29 @@ __device__ __forceinline__ void wait_peers(uint64_t* bar, uint32_t parity, Waits
         : "memory");
     if (ok) return;
     if (spin == 0) t0 = global_timer_ns();
-    if (*w.abort_flag || global_timer_ns() - t0 > kWaitLimitNs) {
+    if (*w.abort_flag || global_timer_ns() - t0 > limit_ns) {
       atomicCAS(w.err, 0, kWaitCode);
       *w.abort_flag = 1;
       w.failed = true;
       return;
     }
   }
+}
+
+// One CTA waits for peers that it does not have: the wait gives up, and so does the
+// next one at once.
+__global__ void wait_peers_selftest_kernel(int* err, uint64_t limit_ns) {
+  __shared__ uint64_t bar;
+  __shared__ int aborted;
+  if (threadIdx.x == 0) {
+    mbar_init(&bar, 1);
+    aborted = 0;
+    fence_mbarrier_init();
+  }
+  __syncthreads();
+  Waits waits{err, &aborted, false};
+  wait_peers(&bar, 0, waits, limit_ns);
+  wait_peers(&bar, 0, waits, limit_ns);
 }
 
 // k = sigmoid(-f) = 1 / (1 + e) with e = exp(f), 0 once e is infinite.  Both ways
@@ -1043,6 +1060,11 @@ bool rows_on(const void* p, int64_t ld, int64_t width, int es, int bytes) {
 }
 
 }  // namespace sc
+
+int launch_scan_wait_selftest(int* err, uint64_t limit_ns, cudaStream_t s) {
+  sc::wait_peers_selftest_kernel<<<1, 32, 0, s>>>(err, limit_ns);
+  return cudaGetLastError() == cudaSuccess ? T3_OK : T3_ECUDA;
+}
 
 int launch_scan_fwd(const void* gate, int64_t ldg, const void* cand, int64_t ldc, const float* h0,
                     const uint8_t* resets, void* h, int64_t ldh, float* h_last, int64_t batch,
