@@ -922,10 +922,16 @@ constexpr int64_t kShort = 8;  // tokens up to which a sequence is not split
 template <class T> constexpr int kFwdSteps = 32 / sizeof(T);
 template <class T> constexpr int kBwdSteps = 16 / sizeof(T);
 
-// Rows of 32 channels fetch half as much with each access: they have to win by
-// this factor (estimated at 1.18 to 1.2 they take 94 us for 102 in 8 x 2048 x 2560
-// backward, at 1.17 112 for 108 in 8 x 2048 x 3456).
-constexpr double kNarrowGain = 1.175;
+// By how much an estimate has to win before its kernel is taken, from 728 measurements of all
+// that could run (150 sizes of 2 to 60 million elements, most drawn at random, 1 to 64 sequences of 64 to 16384
+// tokens, both directions and types; a third of them again in odd rows).  Tiles of 32 channels
+// fetch rows half as long, which costs most where those are 64 bytes of 16-byte copies: the
+// mean time lost against the best choice is 1.8 to 2.0 % for any factor from 1.16 to 1.2
+// there (4.6 % at 1, 2.7 at 1.3), and elsewhere least at 1.03 to 1.12 (1.1 %; 2.2 at 1, 3.8 at 1.3).
+// Shared tiles, whose pieces depend on one another, lose 2.3 % at 1 (12 x 967 x 3464: 74 us
+// for 50), 0.8 at 1.2 and 1.0 where they are never taken.
+template <class T, int CH> constexpr double kNarrowGain = sizeof(T) == 2 && CH == 16 ? 1.18 : 1.08;
+constexpr double kSharedGain = 1.2;
 
 // A launch: CTAs a cluster, and its estimated time in rounds of one CTA.  All
 // clusters of a wave walk their sequences side by side, `rows` steps a CTA and
@@ -980,6 +986,7 @@ template <int LPR>
 struct Fwd<T, CH, kMarks>::Kernel {
   using Type = T;
   static constexpr bool marks = kMarks;
+  static constexpr double gain = kNarrowGain<T, CH>;
   static constexpr int S = kFwdSteps<T>, rows = kWarps * (32 / LPR) * S;
   static constexpr int smem = 2 * kWarps * sizeof(Slab<T, LPR, S, 2>), per_cta = 2 * LPR * sizeof(float4);
   static constexpr auto fn = scan_fwd_kernel<T, LPR, S, CH, kMarks>;
@@ -987,6 +994,7 @@ struct Fwd<T, CH, kMarks>::Kernel {
 template <class T, int CH, bool kMarks>
 template <int LPR>
 struct Bwd<T, CH, kMarks>::Kernel {
+  static constexpr double gain = kNarrowGain<T, CH>;
   static constexpr int S = kBwdSteps<T>, rows = kWarps * (32 / LPR) * S;
   static constexpr int smem = 2 * kWarps * sizeof(Slab<T, LPR, S, 4>), per_cta = 2 * LPR * sizeof(float4);
   static constexpr auto fn = scan_bwd_kernel<T, LPR, S, CH, kMarks>;
@@ -1022,10 +1030,10 @@ int run(const Args& p, int64_t batch, cudaStream_t s) {
     q.tiles = (p.width + 63) / 64;
     q.all_tiles = batch * q.tiles;
     const Plan h = plan_shared<fn>(dev, q.all_tiles, p.length, Wide::rows, Wide::smem, Wide::per_cta);
-    if (h.cluster > 0 && h.cost < std::min(w.cost, n.cost * kNarrowGain))
+    if (h.cluster > 0 && h.cost * kSharedGain < std::min(w.cost, n.cost * Wide::gain))
       return launch(fn, h.clusters * h.cluster, 32 * kWarps, Wide::smem + h.cluster * Wide::per_cta, s, h.cluster, q);
   }
-  if (n.cluster == 0 || (w.cluster > 0 && w.cost <= kNarrowGain * n.cost)) return run_plan<Wide, 32>(p, batch, w.cluster, s);
+  if (n.cluster == 0 || (w.cluster > 0 && w.cost <= Wide::gain * n.cost)) return run_plan<Wide, 32>(p, batch, w.cluster, s);
   return run_plan<Narrow, 16>(p, batch, n.cluster, s);
 }
 
