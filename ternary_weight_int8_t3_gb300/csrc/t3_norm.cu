@@ -25,11 +25,16 @@
 // writes one partial row, and a second small kernel adds the partial rows in a
 // fixed order.
 //
-// Measured (GB300, bf16 with residual; bytes of the formulas over the time, of
-// the measured 6784 GB/s): forward 16384 x 1280 25.7 us (84 %), 16384 x 3456
-// 62.6 us (93 %), 1 x 8192 2.6 us; backward 33 us (75 %) and 80.4 us (83 %).
-// Odd widths: 1782 x 729 float 5.5 us forward, 10.8 us backward; 5000 x 5003 bf16 32.9 us
-// (79 %) and 49 us (60 %).
+// Measured (GB300, with residual; bytes of the formulas over the time, of the measured
+// 6784 GB/s): bf16 forward 16384 x 1280 26.3 us (82 %), 16384 x 3456 63 us (92 %), 1 x
+// 8192 2.9 us; backward 33 us (75 %) and 82 us (82 %).  Float 16384 x 1280 49 us (82 %)
+// and 60 us (83 %), 16384 x 3456 121 us (90 %) and 152 us (88 %), although every float
+// instantiation of the backward and the widest of the forward spill 28 to 136 bytes a thread.
+// Odd widths: 1782 x 729 float 5.8 us forward, 10.9 us backward; 8000 x 729 bf16 without
+// residual 11.3 and 14.6 us, forward 16.3 where the codes lie differently to the rows.
+// Wide rows (bf16 without residual): 4096 x 16384 forward 56 us, 16392 columns 312 us;
+// backward 8192 columns 46 us, 12288 285 us: past the registers every element is a
+// load of its own, and dy and s are read three times.
 #include "t3_vec.cuh"
 
 namespace t3 {

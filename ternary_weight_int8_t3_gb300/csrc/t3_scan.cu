@@ -37,20 +37,23 @@
 //   * the cluster walks along the sequence, a round at a time.
 // More tiles of channels than are resident at once need no split in time; forward, a
 // cluster's CTAs then share several tiles evenly (scan_fwd_shared_kernel).
-// Everything is read once and written once, in a fixed order: the result does
-// not change from call to call.  Sequences of a few tokens take one thread per
+// Each direction reads its operands once (the backward gate, candidate and h anew) and
+// writes once, in a fixed order: the result does not change from call to call.  Sequences of a few tokens take one thread per
 // channel pair and no exchange.
 //
 // Operands arrive by asynchronous copies, a round ahead, in a stage of the warp's
 // own; k stays in registers between the two passes over a run, the candidate is
 // read from the stage again.
 //
-// Measured (GB300, bf16; bytes of the formulas, of the measured 6784 GB/s):
-// 8 x 2048 x 3456 forward 54 to 56 us (90 %), backward 108 to 111 us (92 %), with
-// resets the same; 8 x 2048 x 2560 forward 42.8 us (87 %); 1 x 16384 x 1280 forward
-// 32.6 us (57 %) and backward 62.5 us (59 %); 27 single tokens of 8192 channels 1.9 us.
+// Measured (GB300; bytes of the formulas, of the measured 6784 GB/s): bf16 8 x 2048 x
+// 3456 forward 55 to 56 us (90 %), with resets 57; backward 109 us (92 %) to 129, by how the
+// arrays happen to lie in memory, with resets 111; 8 x 2048 x 2560 forward 42.5 us (87 %),
+// backward 96 (77 %); 1 x 16384 x 1280 forward 33 us (57 %) and backward 64 us (58 %),
+// with resets 37 and 70; 27 single tokens of 8192 channels 2 us.  Float 6 x 1000 x 4096
+// 48 us (91 %) and 91 us (95 %), with resets 49 and 93.
 // Rows of 4-byte pieces take 1.2 to 1.5 times as long as aligned ones, odd rows of
-// 2-byte elements twice (3 x 1782 x 729 float with resets: 14.5 and 25.4 us).
+// 2-byte elements, copied one by one, twice (11 x 1500 x 1101 bf16: 52 and 101 us;
+// 3 x 1782 x 729 float with resets 12.8 and 21.8).
 // The long sequence is held up by no one thing (left out one at a time, of 33 us: the
 // exchange 9, the first pass 7, the second 4.5, the copies 4): four warps a scheduler
 // do not overlap them all.  Trading the maps behind the next round's first pass, in a
@@ -935,8 +938,9 @@ constexpr double kSharedGain = 1.2;
 
 // A launch: CTAs a cluster, and its estimated time in rounds of one CTA.  All
 // clusters of a wave walk their sequences side by side, `rows` steps a CTA and
-// round; a round that ends in an exchange across the cluster takes about 1.15
-// times one that does not, or 1.4 times where later waves keep the SMs full.
+// round; a round that ends in an exchange across the cluster is counted 1.15
+// times one that does not, or 1.4 times where later waves keep the SMs full: how far
+// the choice is off with these is said at kNarrowGain.
 struct Plan {
   int cluster;
   double cost;
