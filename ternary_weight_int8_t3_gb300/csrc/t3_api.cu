@@ -408,7 +408,8 @@ AlignedLayout aligned_layout(int64_t M, int64_t N, int64_t K) {
   l.a = 0;
   l.w = M * l.K;
   l.x = l.w + l.N * (l.K / 4);
-  l.bytes = l.x + M * l.N * 4;
+  const __int128 bytes = static_cast<__int128>(l.x) + static_cast<__int128>(M) * l.N * 4;
+  l.bytes = bytes > INT64_MAX ? INT64_MAX : static_cast<int64_t>(bytes);  // never fits, instead of a negative count
   return l;
 }
 

@@ -47,6 +47,15 @@ def test_scratch_follows_the_limit_of_small_products():
     assert now(32, 729, 243) == now(64, 728, 256) == now(64, 0, 3) == now(-1, 3, 3) == 0
 
 
+def test_scratch_of_sizes_past_64_bits():
+    """Sizes that the checks of arguments let through, whose bytes pass 64 bits: the largest count there is, not a
+    negative one that any scratch would satisfy."""
+    big = (1 << 31) - 1
+    for m, n, k in [(big, big, 3), (big, big, big), (big, big - 4, 61)]:
+        assert t3.load().t3_gemm_fwd_act_scratch(m, n, k) == (1 << 63) - 1
+    assert t3.load().t3_gemm_fwd_act_scratch(big, 3, 61) == big * 64 + 4 * 16 + big * 16
+
+
 @pytest.mark.gpu
 @pytest.mark.parametrize("limit", [0, 8 * 100 * 243 * 731, 1 << 40])
 def test_binding_gives_scratch_where_the_library_takes_it(limit, allocations):
