@@ -332,6 +332,43 @@ int t3_rmsnorm_bwd(const void* dy, int64_t lddy, const void* s, int64_t lds, con
                    float* dgamma, int64_t rows, int64_t cols, int dtype, float* workspace,
                    t3_stream_t stream);
 
+/*
+ * t3_layernorm_quant -- the same with the layer norm in place of the root mean square:
+ *   s = x + residual, rounded to `dtype` (s = x when residual is NULL),
+ *   mean[r] = mean_c(s),   rstd[r] = 1 / sqrt(mean_c((s - mean)^2) + eps),
+ *   y = (s - mean) * rstd[r] * gamma[c] + beta[c],
+ *   row_scale[r] = max_c |y| / 127,
+ *   q = rint(y * (127 / max_c |y|)), ties to even, clamped to [-127, 127].  Where 127 /
+ *   max_c |y| would pass the float range (below 3.7e-37) y counts 2^64 times.
+ * beta [cols] NULL stands for zeros; mean and rstd are kept for the gradient, and may each
+ * be NULL.  The squares are of differences from a mean, so a row far from zero keeps its
+ * deviation.  A row with y = 0 everywhere (equal elements without beta, whose deviations are rounding errors
+ * of the mean at most) gives q = 0 and row_scale = 0; a row with an element of y that is
+ * not finite, or whose squares overflow a float sum, row_scale = NaN and q = 0.  Everything else (gamma, sum_out, lengths of rows, alignment,
+ * errors) is as in t3_rmsnorm_quant; longer rows than the registers hold are read five
+ * times.  cols = 0 writes row_scale = 0, mean = 0 and rstd = 1 / sqrt(eps).
+ */
+int t3_layernorm_quant(const void* x, int64_t ldx, const void* residual, int64_t ldr,
+                       const float* gamma, const float* beta, float eps, int8_t* q,
+                       float* row_scale, float* mean, float* rstd, void* sum_out, int64_t lds,
+                       int64_t rows, int64_t cols, int dtype, t3_stream_t stream);
+
+/*
+ * t3_layernorm_bwd -- its gradient, with the rounding to int8 passed straight through.  dy is
+ * the gradient of y, dsum (may be NULL) that of s itself:
+ *   h = (s - mean) * rstd,   n = dy * gamma,
+ *   dx = rstd * (n - mean_c(n) - h * mean_c(n * h)) + dsum,
+ *   dgamma[c] = sum_r dy * h,   dbeta[c] = sum_r dy     (each skipped when NULL).
+ * s, mean and rstd are the forward's.  dx may be dy's or dsum's buffer with the same
+ * stride.  workspace: DEVICE floats, at least t3_colsum_workspace(rows, cols) of them for
+ * one of dgamma and dbeta, t3_colsum_workspace(rows, 2 * cols) for both (not zeroed).
+ * rows = 0 writes dgamma = 0 and dbeta = 0.
+ */
+int t3_layernorm_bwd(const void* dy, int64_t lddy, const void* s, int64_t lds, const float* mean,
+                     const float* rstd, const float* gamma, const void* dsum, int64_t lddsum,
+                     void* dx, int64_t lddx, float* dgamma, float* dbeta, int64_t rows,
+                     int64_t cols, int dtype, float* workspace, t3_stream_t stream);
+
 /* Floats of workspace the column sums over [rows][cols] need (0 for empty or
  * invalid sizes); the same on every device. */
 int64_t t3_colsum_workspace(int64_t rows, int64_t cols);

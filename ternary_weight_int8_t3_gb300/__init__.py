@@ -18,6 +18,8 @@ Function names follow the C ABI:
                                            the products with that output
   t3_rmsnorm_quant(x, gamma, residual)     residual add, norm, int8 rows with scales
   t3_rmsnorm_bwd(dy, s, rstd, gamma)       its gradient
+  t3_layernorm_quant(x, gamma, beta)       the same with the layer norm
+  t3_layernorm_bwd(dy, s, mean, rstd)      its gradient
   t3_gated_scan_fwd(gate, cand, h0)        the gated linear recurrence (sequences, tokens)
   t3_gated_scan_bwd(gate, cand, h, dh)     its gradient
   t3_gemm_fwd_act(A, Wp, bias=, act=)      the forward with bias, activation, residual
@@ -100,6 +102,8 @@ def load():
         for name, types in (
                 ("t3_rmsnorm_quant", [p, i64, p, i64, p, ctypes.c_float, p, p, p, p, i64, i64, i64, i32, p]),
                 ("t3_rmsnorm_bwd", [p, i64, p, i64, p, p, p, i64, p, i64, p, i64, i64, i32, p, p]),
+                ("t3_layernorm_quant", [p, i64, p, i64, p, p, ctypes.c_float, p, p, p, p, p, i64, i64, i64, i32, p]),
+                ("t3_layernorm_bwd", [p, i64, p, i64, p, p, p, p, i64, p, i64, p, p, i64, i64, i32, p, p]),
                 ("t3_gated_scan_fwd", [p, i64, p, i64, p, p, p, i64, p, i64, i64, i64, i32, p]),
                 ("t3_gated_scan_bwd", [p, i64, p, i64, p, i64, p, i64, p, p, p, p, i64, p, i64, p,
                                        i64, i64, i64, i32, p]),
@@ -628,6 +632,68 @@ def t3_rmsnorm_bwd(dy, s, rstd, gamma=None, dsum=None, dx=None, dgamma=None, wor
             _dense(gamma, f32, dev, (cols,), "gamma"), pd, ldd, px, ldx,
             _dense(dgamma, f32, dev, (cols,), "dgamma"), rows, cols, dtype, None if ws is None else ws.data_ptr())
     return dx, dgamma
+
+
+def t3_layernorm_quant(x, gamma=None, beta=None, residual=None, eps=1e-5, q=None, row_scale=None, mean=None,
+                       rstd=None, sum_out=None, stream=None):
+    """(q, row_scale, mean, rstd, s): s = x + residual in x's type, less its mean and over its
+    deviation, times gamma plus beta, as int8 rows with one scale each; mean, rstd and s
+    are what t3_layernorm_bwd takes (see include/t3.h).  x [rows][cols] bfloat16
+    or float32, rows evenly spaced; gamma and beta float32 [cols].  s is x itself
+    without a residual and without sum_out; sum_out may be x or residual."""
+    torch = _torch()
+    dtype = _dtype_of(x, "x")
+    shape, xt, dev, f32 = x.shape, x.dtype, x.get_device(), torch.float32
+    if len(shape) != 2:
+        raise TypeError("x must be 2-D [rows][cols]")
+    rows, cols = shape
+    if q is None:
+        q = _empty(shape, torch.int8, dev, stream)
+    if row_scale is None:
+        row_scale = _empty(rows, f32, dev, stream)
+    if mean is None:
+        mean = _empty(rows, f32, dev, stream)
+    if rstd is None:
+        rstd = _empty(rows, f32, dev, stream)
+    if sum_out is None and residual is not None:
+        sum_out = _empty(shape, xt, dev, stream)
+    px, ldx = _spaced(x, shape, "x")
+    pr, ldr = _rows(residual, xt, dev, shape, "residual")
+    ps, lds = _rows(sum_out, xt, dev, shape, "sum_out", out=True)
+    _launch("t3_layernorm_quant", dev, stream, px, ldx, pr, ldr, _dense(gamma, f32, dev, (cols,), "gamma"),
+            _dense(beta, f32, dev, (cols,), "beta"), eps, _dense(q, torch.int8, dev, shape, "q"),
+            _dense(row_scale, f32, dev, (rows,), "row_scale"), _dense(mean, f32, dev, (rows,), "mean"),
+            _dense(rstd, f32, dev, (rows,), "rstd"), ps, lds, rows, cols, dtype)
+    return q, row_scale, mean, rstd, x if sum_out is None else sum_out
+
+
+def t3_layernorm_bwd(dy, s, mean, rstd, gamma=None, dsum=None, dx=None, dgamma=None, dbeta=None, workspace=None,
+                     stream=None):
+    """(dx, dgamma, dbeta): the gradient of t3_layernorm_quant for dy, the gradient of
+    the normalized rows, and dsum, that of s itself; s, mean and rstd are the
+    forward's.  dgamma is allocated where gamma is given and none is passed; dbeta is
+    computed where one is passed (float32 [cols]).  dx may be dy or dsum."""
+    torch = _torch()
+    dtype = _dtype_of(dy, "dy")
+    if dy.dim() != 2:
+        raise TypeError("dy must be 2-D [rows][cols]")
+    shape, xt, dev, f32 = dy.shape, dy.dtype, dy.get_device(), torch.float32
+    rows, cols = shape
+    if dx is None:
+        dx = _empty(shape, xt, dev, stream)
+    if dgamma is None and gamma is not None:
+        dgamma = _empty(cols, f32, dev, stream)
+    sums = (dgamma is not None) + (dbeta is not None)
+    ws = _workspace(workspace, rows, sums * cols, dev, stream) if sums else None
+    pdy, lddy = _spaced(dy, shape, "dy")
+    ps, lds = _rows(s, xt, dev, shape, "s")
+    pd, ldd = _rows(dsum, xt, dev, shape, "dsum")
+    px, ldx = _rows(dx, xt, dev, shape, "dx", out=True)
+    _launch("t3_layernorm_bwd", dev, stream, pdy, lddy, ps, lds, _dense(mean, f32, dev, (rows,), "mean"),
+            _dense(rstd, f32, dev, (rows,), "rstd"), _dense(gamma, f32, dev, (cols,), "gamma"), pd, ldd, px, ldx,
+            _dense(dgamma, f32, dev, (cols,), "dgamma"), _dense(dbeta, f32, dev, (cols,), "dbeta"), rows, cols, dtype,
+            None if ws is None else ws.data_ptr())
+    return dx, dgamma, dbeta
 
 
 def t3_gated_scan_fwd(gate, cand, h0=None, resets=None, h=None, h_last=None, stream=None):

@@ -656,6 +656,40 @@ int t3_rmsnorm_bwd(const void* dy, int64_t lddy, const void* s, int64_t lds, con
                          workspace, dev->sms, stream);
 }
 
+int t3_layernorm_quant(const void* x, int64_t ldx, const void* residual, int64_t ldr, const float* gamma,
+                       const float* beta, float eps, int8_t* q, float* row_scale, float* mean, float* rstd,
+                       void* sum_out, int64_t lds, int64_t rows, int64_t cols, int dtype, t3_stream_t stream) {
+  if (bad_dims(rows, cols, 0) || !valid_dtype(dtype) || bad_ld(ldx) || (residual && bad_ld(ldr)) ||
+      (sum_out && (bad_ld(lds) || lds < cols)) || !(eps > 0.0f) || !(eps <= 3.4028234e38f))
+    return T3_EINVAL;
+  if (rows == 0) return T3_OK;
+  if (!row_scale || (cols > 0 && (!x || !q))) return T3_EINVAL;
+  const DeviceInfo* dev = nullptr;
+  const int st = device_info(&dev);
+  if (st != T3_OK) return st;
+  return launch_layernorm_fwd(x, ldx, residual, ldr, gamma, beta, eps, q, row_scale, mean, rstd, sum_out, lds, rows,
+                              cols, dtype, dev->sms, stream);
+}
+
+int t3_layernorm_bwd(const void* dy, int64_t lddy, const void* s, int64_t lds, const float* mean, const float* rstd,
+                     const float* gamma, const void* dsum, int64_t lddsum, void* dx, int64_t lddx, float* dgamma,
+                     float* dbeta, int64_t rows, int64_t cols, int dtype, float* workspace, t3_stream_t stream) {
+  if (bad_dims(rows, cols, 0) || !valid_dtype(dtype) || bad_ld(lddy) || bad_ld(lds) ||
+      (dsum && bad_ld(lddsum)) || bad_ld(lddx) || (rows > 1 && lddx < cols) || (dgamma && dgamma == dbeta))
+    return T3_EINVAL;
+  if (cols == 0) return T3_OK;
+  if (rows == 0) {
+    const int st = dgamma ? zero_fill(reinterpret_cast<int32_t*>(dgamma), 1, cols, stream) : T3_OK;
+    return st == T3_OK && dbeta ? zero_fill(reinterpret_cast<int32_t*>(dbeta), 1, cols, stream) : st;
+  }
+  if (!dy || !s || !mean || !rstd || !dx || ((dgamma || dbeta) && !workspace)) return T3_EINVAL;
+  const DeviceInfo* dev = nullptr;
+  const int st = device_info(&dev);
+  if (st != T3_OK) return st;
+  return launch_layernorm_bwd(dy, lddy, s, lds, mean, rstd, gamma, dsum, lddsum, dx, lddx, dgamma, dbeta, rows, cols,
+                              dtype, workspace, dev->sms, stream);
+}
+
 int t3_gated_scan_fwd(const void* gate, int64_t ldg, const void* cand, int64_t ldc,
                       const float* h0, const uint8_t* resets, void* h, int64_t ldh, float* h_last,
                       int64_t batch, int64_t length, int64_t width, int dtype, t3_stream_t stream) {

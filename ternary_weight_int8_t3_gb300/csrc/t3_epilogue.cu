@@ -196,9 +196,10 @@ __global__ void __launch_bounds__(256) act_bwd_kernel(const BwdArgs p) {
   }
 }
 
-// 32 columns a CTA, its 32 warps take the partial rows in turn.
+// 32 columns a CTA, its 32 warps take the partial rows in turn.  The columns from `split`
+// on go to out2.
 __global__ void __launch_bounds__(1024) col_finish_kernel(const float* partial, int parts, int64_t cols,
-                                                          float* out) {
+                                                          float* out, int64_t split, float* out2) {
   __shared__ float sm[32][33];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int64_t c = static_cast<int64_t>(blockIdx.x) * 32 + lane;
@@ -213,7 +214,7 @@ __global__ void __launch_bounds__(1024) col_finish_kernel(const float* partial, 
   __syncthreads();
   const float t = warp_sum(sm[lane][warp]);  // warp w: column w's 32 sums
   const int64_t col = static_cast<int64_t>(blockIdx.x) * 32 + warp;
-  if (lane == 0 && col < cols) out[col] = t;
+  if (lane == 0 && col < cols) (col < split ? out : out2 - split)[col] = t;
 }
 
 template <class T, int VEC>
@@ -278,7 +279,12 @@ int launch_epilogue(const int32_t* x, int64_t ldx, void* out, const EpilogueArgs
 }
 
 int launch_col_finish(const float* partial, int parts, int64_t cols, float* out, cudaStream_t s) {
-  return vec::launch(ep::col_finish_kernel, (cols + 31) / 32, 1024, 0, s, 1, partial, parts, cols, out);
+  return vec::launch(ep::col_finish_kernel, (cols + 31) / 32, 1024, 0, s, 1, partial, parts, cols, out, cols, out);
+}
+
+int launch_col_finish2(const float* partial, int parts, int64_t cols, float* out, float* out2, cudaStream_t s) {
+  return vec::launch(ep::col_finish_kernel, (2 * cols + 31) / 32, 1024, 0, s, 1, partial, parts, 2 * cols, out, cols,
+                     out2);
 }
 
 int launch_act_bwd(const void* dy, const void* z, int act, void* dz, float* dbias, int64_t rows,

@@ -106,6 +106,8 @@ constexpr int kMaxColParts = 1216;
 
 // out[c] = the sum of partial[0 .. parts)[c], added in a fixed order, on `s`.
 int launch_col_finish(const float* partial, int parts, int64_t cols, float* out, cudaStream_t s);
+// The same over partial rows of 2 cols floats: the first cols sums to out, the others to out2.
+int launch_col_finish2(const float* partial, int parts, int64_t cols, float* out, float* out2, cudaStream_t s);
 
 // Residual add, root-mean-square norm, int8 rows with a scale each, and its
 // gradient (t3_norm.cu); dtype T3_OUT_F32 or T3_OUT_BF16.
@@ -116,6 +118,16 @@ int launch_norm_bwd(const void* dy, int64_t lddy, const void* x, int64_t lds, co
                     const float* gamma, const void* dsum, int64_t lddsum, void* dx, int64_t lddx,
                     float* dgamma, int64_t rows, int64_t cols, int dtype, float* workspace, int sms,
                     cudaStream_t s);
+
+// The same for the layer norm (t3_layernorm.cu).
+int launch_layernorm_fwd(const void* x, int64_t ldx, const void* residual, int64_t ldr, const float* gamma,
+                         const float* beta, float eps, int8_t* q, float* row_scale, float* mean, float* rstd,
+                         void* sum_out, int64_t lds, int64_t rows, int64_t cols, int dtype, int sms,
+                         cudaStream_t s);
+int launch_layernorm_bwd(const void* dy, int64_t lddy, const void* x, int64_t lds, const float* mean,
+                         const float* rstd, const float* gamma, const void* dsum, int64_t lddsum, void* dx,
+                         int64_t lddx, float* dgamma, float* dbeta, int64_t rows, int64_t cols, int dtype,
+                         float* workspace, int sms, cudaStream_t s);
 
 // The gated recurrence over sequences and its gradient (t3_scan.cu).
 int launch_scan_fwd(const void* gate, int64_t ldg, const void* cand, int64_t ldc, const float* h0,
