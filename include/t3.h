@@ -469,6 +469,50 @@ int64_t t3_gemm_fwd_act_workspace(const int8_t* A, const uint8_t* Wp, const void
 int t3_act_bwd(const void* dy, const void* z, int act, void* dz, float* dbias, int64_t rows,
                int64_t cols, int dtype, float* workspace, t3_stream_t stream);
 
+/*
+ * t3_gemm_fwd_glu -- the first half of a gated feed-forward block in one call: two ternary
+ * products over the same A, the activation of the one and the product of both.  For the
+ * exact int32 x_g = A . Wg and x_u = A . Wu of t3_gemm_fwd:
+ *   zg = (x_g * row_scale[m]) * gate_scale[n] + gate_bias[n],
+ *   zu = (x_u * row_scale[m]) * up_scale[n] + up_bias[n],
+ *   C = act(zg) * zu,   pre_gate = zg,   pre_up = zu.
+ * Wg and Wu [N][ceil(K/4)]; row_scale [M], the other scales and biases [N] (float) and the
+ * pre-activations [M][N] (the output's type, dense) may each be NULL: ones, zeros, not
+ * written.  The pre-activations are what t3_glu_bwd takes.  out_kind: T3_OUT_F32 or T3_OUT_BF16.
+ * K = 0 takes x = 0.  C, pre_gate, pre_up and workspace must be different buffers.  One kernel does
+ * it all for one or two rows (and up to eight when both weights are at most 4 MB), for M
+ * > 32 where A, Wg, Wu, C and the pre-activations have rows of whole 16-byte pieces on
+ * 16-byte boundaries and K <= 65536, and for small products.  workspace (DEVICE, 16-byte aligned) of at
+ * least t3_gemm_fwd_glu_workspace bytes holds operands laid out aligned and int32
+ * results otherwise: T3_EINVAL where it is missing or too small, with nothing launched.  Every
+ * route gives the same bits.  Sizes and overflow rules are those of t3_gemm_fwd_scaled.
+ */
+int t3_gemm_fwd_glu(const int8_t* A, const uint8_t* Wg, const uint8_t* Wu, void* C, int64_t M,
+                    int64_t N, int64_t K, const float* row_scale, const float* gate_scale,
+                    const float* up_scale, const float* gate_bias, const float* up_bias, int act,
+                    void* pre_gate, void* pre_up, int out_kind, void* workspace,
+                    int64_t workspace_bytes, t3_stream_t stream);
+
+/* Bytes of workspace that t3_gemm_fwd_glu takes for these arguments (0: none), under the
+ * present limit of small products; a negative status where the device cannot be asked. */
+int64_t t3_gemm_fwd_glu_workspace(const int8_t* A, const uint8_t* Wg, const uint8_t* Wu, const void* C,
+                                  int64_t M, int64_t N, int64_t K, const void* pre_gate,
+                                  const void* pre_up, int out_kind);
+
+/*
+ * t3_glu_bwd -- the gradient of what t3_gemm_fwd_glu does behind its products: for dy, the gradient of
+ * C, and the pre-activations gate and up, all dense [rows][cols] of `dtype`:
+ *   dgate = dy * up * act'(gate),   dup = dy * act(gate),
+ *   dgate_bias[c] = sum_r dgate,   dup_bias[c] = sum_r dup     (before the rounding).
+ * Each output may be NULL; dgate and dup may be dy's, gate's or up's buffer, not the same one.
+ * They are what t3_quantize_rows_bf16 and the backward products take.  workspace: at
+ * least t3_colsum_workspace(rows, cols) floats for one of the sums, (rows, 2 * cols) for both.
+ * rows = 0 writes zero sums.
+ */
+int t3_glu_bwd(const void* dy, const void* gate, const void* up, int act, void* dgate, void* dup,
+               float* dgate_bias, float* dup_bias, int64_t rows, int64_t cols, int dtype,
+               float* workspace, t3_stream_t stream);
+
 /* A static, human-readable name for a status code (never NULL). */
 const char* t3_status_string(int status);
 

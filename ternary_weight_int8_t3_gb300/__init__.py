@@ -24,6 +24,8 @@ Function names follow the C ABI:
   t3_gated_scan_bwd(gate, cand, h, dh)     its gradient
   t3_gemm_fwd_act(A, Wp, bias=, act=)      the forward with bias, activation, residual
   t3_act_bwd(dy, z, act)                   that epilogue's gradient
+  t3_gemm_fwd_glu(A, Wg, Wu, act=)         two forwards, an activation and their product
+  t3_glu_bwd(dy, gate, up, act)            its gradient
 """
 from __future__ import annotations
 
@@ -108,7 +110,9 @@ def load():
                 ("t3_gated_scan_bwd", [p, i64, p, i64, p, i64, p, i64, p, p, p, p, i64, p, i64, p,
                                        i64, i64, i64, i32, p]),
                 ("t3_gemm_fwd_act", [p, p, p, i64, i64, i64, p, p, p, i32, p, p, i32, p, p, i64, p]),
-                ("t3_act_bwd", [p, p, i32, p, p, i64, i64, i32, p, p])):
+                ("t3_act_bwd", [p, p, i32, p, p, i64, i64, i32, p, p]),
+                ("t3_gemm_fwd_glu", [p, p, p, p, i64, i64, i64, p, p, p, p, p, i32, p, p, i32, p, i64, p]),
+                ("t3_glu_bwd", [p, p, p, i32, p, p, p, p, i64, i64, i32, p, p])):
             f = getattr(lib, name)
             f.argtypes = types
             f.restype = ctypes.c_int
@@ -117,6 +121,8 @@ def load():
             f.restype = i64
         lib.t3_gemm_fwd_act_workspace.argtypes = [p, p, p, i64, i64, i64, p, p, i32, i64]
         lib.t3_gemm_fwd_act_workspace.restype = i64
+        lib.t3_gemm_fwd_glu_workspace.argtypes = [p, p, p, p, i64, i64, i64, p, p, i32]
+        lib.t3_gemm_fwd_glu_workspace.restype = i64
         lib.t3_colsum_workspace.argtypes = [i64, i64]
         lib.t3_colsum_workspace.restype = i64
         lib.t3_version.argtypes = []
@@ -820,6 +826,67 @@ def t3_act_bwd(dy, z, act, dz=None, dbias=None, workspace=None, stream=None):
             _dense(dz, xt, dev, shape, "dz"), _dense(dbias, torch.float32, dev, (cols,), "dbias"), rows, cols, dtype,
             None if ws is None else ws.data_ptr())
     return dz, dbias
+
+
+def t3_gemm_fwd_glu(A, Wg, Wu, K=None, row_scale=None, gate_scale=None, up_scale=None, gate_bias=None, up_bias=None,
+                    act=T3_ACT_SILU, kind=T3_OUT_F32, C=None, pre_gate=None, pre_up=None, workspace=None, stream=None):
+    """C = act(zg) * zu with zg = A . Wg and zu = A . Wu, each scaled per row and column plus its
+    bias; pre_gate and pre_up, when given, receive zg and zu for t3_glu_bwd.  kind: T3_OUT_F32
+    or T3_OUT_BF16, the type of C and the pre-activations [M][N].  workspace: uint8 of
+    t3_gemm_fwd_glu_workspace bytes, allocated where none is given."""
+    torch = _torch()
+    if not isinstance(A, torch.Tensor) or not A.is_cuda or A.dim() != 2 or Wg.dim() != 2:
+        raise TypeError("A, Wg and Wu must be 2-D CUDA tensors")
+    M, Ka = A.shape
+    N, KB = Wg.shape
+    K = Ka if K is None else K
+    if Ka != K or KB != (K + 3) // 4:
+        raise ValueError("A must be [M][K], Wg and Wu [N][ceil(K/4)]")
+    if kind not in (T3_OUT_F32, T3_OUT_BF16):
+        raise ValueError(f"unknown output kind {kind}")
+    dev, f32, shape = A.get_device(), torch.float32, (M, N)
+    dtype = torch.bfloat16 if kind == T3_OUT_BF16 else f32
+    if C is None:
+        C = _empty(shape, dtype, dev, stream)
+    pa, pc = _dense(A, torch.int8, dev, (M, K), "A"), _dense(C, dtype, dev, shape, "C")
+    pg, pu = _dense(Wg, torch.uint8, dev, (N, KB), "Wg"), _dense(Wu, torch.uint8, dev, (N, KB), "Wu")
+    qg, qu = _dense(pre_gate, dtype, dev, shape, "pre_gate"), _dense(pre_up, dtype, dev, shape, "pre_up")
+    if workspace is None:
+        room = _on(dev, "t3_gemm_fwd_glu_workspace", pa, pg, pu, pc, M, N, K, qg, qu, kind)
+        if room < 0:
+            raise T3Error(room, "t3_gemm_fwd_glu_workspace")
+        if room:
+            workspace = _empty(room, torch.uint8, dev, stream)
+    else:
+        room = workspace.numel()
+    _launch("t3_gemm_fwd_glu", dev, stream, pa, pg, pu, pc, M, N, K, _dense(row_scale, f32, dev, (M,), "row_scale"),
+            _dense(gate_scale, f32, dev, (N,), "gate_scale"), _dense(up_scale, f32, dev, (N,), "up_scale"),
+            _dense(gate_bias, f32, dev, (N,), "gate_bias"), _dense(up_bias, f32, dev, (N,), "up_bias"), act, qg, qu,
+            kind, _dense(workspace, torch.uint8, dev, (room,), "workspace"), room)
+    return C
+
+
+def t3_glu_bwd(dy, gate, up, act, dgate=None, dup=None, dgate_bias=None, dup_bias=None, workspace=None, stream=None):
+    """(dgate, dup, dgate_bias, dup_bias): the gradient of act(gate) * up for dy and, into
+    the bias gradients that are given (float32 [cols]), the column sums; gate and up are
+    t3_gemm_fwd_glu's pre-activations.  dgate and dup may be dy, gate or up."""
+    torch = _torch()
+    dtype = _dtype_of(dy, "dy")
+    if dy.dim() != 2:
+        raise TypeError("dy must be 2-D [rows][cols]")
+    shape, xt, dev, f32 = dy.shape, dy.dtype, dy.get_device(), torch.float32
+    rows, cols = shape
+    if dgate is None:
+        dgate = _empty(shape, xt, dev, stream)
+    if dup is None:
+        dup = _empty(shape, xt, dev, stream)
+    sums = (dgate_bias is not None) + (dup_bias is not None)
+    ws = _workspace(workspace, rows, sums * cols, dev, stream) if sums else None
+    _launch("t3_glu_bwd", dev, stream, _dense(dy, xt, dev, shape, "dy"), _dense(gate, xt, dev, shape, "gate"),
+            _dense(up, xt, dev, shape, "up"), act, _dense(dgate, xt, dev, shape, "dgate"),
+            _dense(dup, xt, dev, shape, "dup"), _dense(dgate_bias, f32, dev, (cols,), "dgate_bias"),
+            _dense(dup_bias, f32, dev, (cols,), "dup_bias"), rows, cols, dtype, None if ws is None else ws.data_ptr())
+    return dgate, dup, dgate_bias, dup_bias
 
 
 def t3_last_device_error(stream=None):

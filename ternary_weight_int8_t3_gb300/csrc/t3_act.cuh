@@ -16,6 +16,15 @@ struct EpilogueArgs {
   int act;
 };
 
+// Two products over one A (0: the gate's, 1: the other's): z_i = (x_i row_scale) scale_i +
+// bias_i, pre_i = z_i, out = act(z_0) z_1; any pointer may be null.
+struct GluArgs {
+  const float* row_scale;
+  const float *scale[2], *bias[2];
+  void* pre[2];
+  int act;
+};
+
 namespace vec {
 
 // The logistic function from one exponential that cannot overflow, with
@@ -62,6 +71,16 @@ __device__ __forceinline__ float act(float z) {
   if constexpr (ACT == T3_ACT_SILU) return z * sigmoid_scaled(-kLog2e * z);
   if constexpr (ACT == T3_ACT_GELU) return z * sigmoid_scaled(z * fmaf(-kLog2e * kGeluC * kGeluA, z * z, -kLog2e * kGeluC));
   return z;
+}
+
+__device__ __forceinline__ float act_any(float z, int kind) {
+  switch (kind) {
+    case T3_ACT_RELU: return act<T3_ACT_RELU>(z);
+    case T3_ACT_RELU2: return act<T3_ACT_RELU2>(z);
+    case T3_ACT_SILU: return act<T3_ACT_SILU>(z);
+    case T3_ACT_GELU: return act<T3_ACT_GELU>(z);
+    default: return z;
+  }
 }
 
 template <int ACT>

@@ -92,8 +92,10 @@ bool make_u16_map_tiled(CUtensorMap* map, const void* base, int64_t rows, int64_
 // in the 128-byte swizzle, bf16 rows (64 bytes) unswizzled.
 // per_warp: boxes of 32 x 32 as a layer's epilogue takes them, bf16 rows in the
 // 64-byte swizzle (no int32 there).
+// box_cols 16: boxes of 16 x 32 for two products' epilogue, float rows in the 64-byte swizzle,
+// bf16 rows in the 32-byte one.
 bool make_out_map(CUtensorMap* map, const void* base, int64_t rows, int64_t cols, int kind,
-                  bool per_warp = false) {
+                  bool per_warp = false, uint32_t box_cols = 32) {
   if (kind == tc2::kOutI32) return make_i32_map_tiled(map, base, rows, cols, 128, 32, true);
   std::memset(map, 0, sizeof(*map));
   const int64_t esize = (kind == T3_OUT_BF16) ? 2 : 4;
@@ -102,12 +104,13 @@ bool make_out_map(CUtensorMap* map, const void* base, int64_t rows, int64_t cols
   if (!fn) return false;
   cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
   cuuint64_t strides[1] = {static_cast<cuuint64_t>(cols * esize)};
-  cuuint32_t box[2] = {32, per_warp ? 32u : 128u};
+  cuuint32_t box[2] = {box_cols, per_warp ? 32u : 128u};
   cuuint32_t estr[2] = {1, 1};
   CUresult r = fn(map,
                   kind == T3_OUT_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32,
                   2, const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                  kind != T3_OUT_BF16 ? CU_TENSOR_MAP_SWIZZLE_128B
+                  box_cols == 16      ? (kind != T3_OUT_BF16 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_32B)
+                  : kind != T3_OUT_BF16 ? CU_TENSOR_MAP_SWIZZLE_128B
                   : per_warp          ? CU_TENSOR_MAP_SWIZZLE_64B
                                       : CU_TENSOR_MAP_SWIZZLE_NONE,
                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
@@ -292,6 +295,46 @@ int run_tc2(const int8_t* act, const uint8_t* Wp, void* out, int64_t M, int64_t 
                         : launch_tc2_dx(p, ma, mw, mo, grid, stream);
 }
 
+// Two forwards with their product in the epilogue on the CTA pairs (tc2::kModeGlu), for
+// operands and outputs that TMA can address; T3_EINVAL, with nothing launched, for others.
+int run_tc2_glu(const int8_t* A, const uint8_t* Wg, const uint8_t* Wu, void* C, int64_t M, int64_t N, int64_t K,
+                const GluArgs& e, int out_kind, const DeviceInfo* dev, cudaStream_t stream) {
+  const int64_t KB = (K + 3) / 4;
+  const int64_t tiles_r = ceil_div(M, tc2::BMP), tiles_c = ceil_div(N, tc2::BNH), tiles = tiles_r * tiles_c;
+  if (ceil_div(K, tc2::BK) > tc2::kChunkStages || tiles > kMaxDim) return T3_EINVAL;
+  CUtensorMap ma, mw, mo;
+  tc2::GluMaps more;
+  if (!make_u8_map_tiled(&ma, A, M, K, K, 128, tc2::BK, true) ||
+      !make_u8_map_tiled(&mw, Wg, N, KB, KB, tc2::BNH, tc2::BK / 4) ||
+      !make_u8_map_tiled(&more.w2, Wu, N, KB, KB, tc2::BNH, tc2::BK / 4) ||
+      !make_out_map(&mo, C, M, N, out_kind, true, 16))
+    return T3_EINVAL;
+  for (int i = 0; i < 2; ++i) {
+    more.pre[i] = mo;  // an unused copy: any initialised map
+    if (e.pre[i] && !make_out_map(&more.pre[i], e.pre[i], M, N, out_kind, true, 16)) return T3_EINVAL;
+  }
+  tc2::Params p{};
+  p.M = M;
+  p.N = N;
+  p.K = K;
+  p.out_rows = M;
+  p.out_cols = N;
+  p.num_stages = ceil_div(K, tc2::BK);
+  p.tiles_r = static_cast<int>(tiles_r);
+  p.tiles_c = static_cast<int>(tiles_c);
+  p.use_tma_out = 1;
+  p.out_kind = out_kind;
+  p.row_scale = e.row_scale;
+  p.w_tma = 1;
+  p.a_tma = 1;
+  p.mode = tc2::kModeGlu;
+  p.dp_tiles = static_cast<int>(tiles);
+  p.glu = e;
+  p.err = dev->err_word;
+  const int64_t pairs = std::min<int64_t>(tiles, std::max(dev->sms / 2, 1));
+  return launch_tc2_fwd_glu(p, ma, mw, mo, more, static_cast<int>(2 * pairs), stream);
+}
+
 // The CTA-pair dW pipeline, for operands and output of any alignment.
 int run_dw2(const int8_t* A, const int8_t* dY, int32_t* dW, int64_t M, int64_t N, int64_t K,
             cudaStream_t stream) {
@@ -436,6 +479,76 @@ ActRoute act_route(const int8_t* A, const uint8_t* Wp, const void* C, int64_t M,
       ceil_div(K, tc2::BK) <= tc2::kChunkStages && ceil_div(M, tc2::BMP) * ceil_div(N, tc2::BN) <= kMaxDim)
     return ActRoute::kPairs;
   return room ? ActRoute::kAligned : ActRoute::kTwoKernels;
+}
+
+// How t3_gemm_fwd_glu takes a product, and where its workspace holds what: operands laid out aligned
+// (A [M][K'] and both weights [N'][K' / 4], K' = K rounded up to 64 and N' = N to 4) and
+// the int32 results [M][N'].  An offset below 0: as the caller has it, or not needed.
+struct GluPlan {
+  enum Route { kGemv, kSmall, kFew, kPairs, kTwoKernels } route;
+  bool aligned = false;           // kPairs: operands laid out first
+  int64_t K = 0, N = 0;           // the padded sizes (kTwoKernels: the caller's)
+  int64_t a = -1, w[2] = {-1, -1}, x[2] = {-1, -1};
+  int64_t bytes = 0;
+};
+
+GluPlan glu_plan(const int8_t* A, const uint8_t* Wg, const uint8_t* Wu, const void* C, int64_t M, int64_t N, int64_t K,
+                 const void* pre_gate, const void* pre_up, int out_kind, int sms) {
+  GluPlan p;
+  p.K = K;
+  p.N = N;
+  auto take = [&p](int64_t rows, int64_t pitch) {
+    const int64_t at = p.bytes;
+    const __int128 end = static_cast<__int128>(rows) * pitch + at + 255;
+    p.bytes = end > INT64_MAX ? INT64_MAX : static_cast<int64_t>(end) / 256 * 256;  // never fits, instead of a negative count
+    return at;
+  };
+  auto results = [&] {
+    for (int i = 0; i < 2; ++i) p.x[i] = take(M, p.N * 4);
+  };
+  auto bulk = [](const void* q) { return reinterpret_cast<uintptr_t>(q) % 16 == 0; };
+  const int64_t twice = 2 * N;  // columns of both products
+  p.route = GluPlan::kTwoKernels;
+  if (K == 0) {
+    results();
+    return p;
+  }
+  if (M <= kSmallM) {
+    if (gemv_rows(M, twice, K) && gemv_fits(M, N, K))
+      p.route = GluPlan::kGemv;
+    else if (small_product(M, twice, K, false) && few_act_fits(M, twice, K, sms))
+      p.route = GluPlan::kFew;
+    else
+      results();
+    return p;
+  }
+  const int64_t KB = (K + 3) / 4, es = out_kind == T3_OUT_BF16 ? 2 : 4;
+  const bool a_ok = K % 16 == 0 && bulk(A), w_ok = KB % 16 == 0 && bulk(Wg) && bulk(Wu);
+  const bool out_ok = bulk(C) && bulk(pre_gate) && bulk(pre_up) && N * es % 16 == 0;
+  const bool one_chunk = ceil_div(K, tc2::BK) <= tc2::kChunkStages;
+  if (small_product(M, twice, K, true)) {
+    if (small_act_fits(M, twice, sms)) {
+      p.route = GluPlan::kSmall;
+      return p;
+    }
+    if (few_act_fits(M, twice, K, sms))
+      p.route = GluPlan::kFew;
+    else
+      results();
+    return p;
+  }
+  // rows that TMA cannot address cost the pipelines several times as much as
+  // laying them out once
+  p.route = GluPlan::kPairs;
+  p.aligned = !a_ok || !w_ok || !out_ok || !one_chunk;
+  if (!p.aligned) return p;
+  if (!a_ok || !w_ok) p.K = ceil_div(K, 64) * 64;
+  p.N = ceil_div(N, 4) * 4;
+  if (!a_ok || p.K != K) p.a = take(M, p.K);
+  if (!w_ok || p.K != K)
+    for (int i = 0; i < 2; ++i) p.w[i] = take(p.N, p.K / 4);
+  if (!out_ok || !one_chunk) results();
+  return p;
 }
 
 // Activations' element types are the output kinds that store them.
@@ -808,6 +921,85 @@ int t3_act_bwd(const void* dy, const void* z, int act, void* dz, float* dbias, i
   const int st = device_info(&dev);
   if (st != T3_OK) return st;
   return launch_act_bwd(dy, z, act, dz, dbias, rows, cols, dtype, workspace, dev->sms, stream);
+}
+
+int64_t t3_gemm_fwd_glu_workspace(const int8_t* A, const uint8_t* Wg, const uint8_t* Wu, const void* C, int64_t M,
+                                  int64_t N, int64_t K, const void* pre_gate, const void* pre_up, int out_kind) {
+  if (bad_dims(M, N, K) || M == 0 || N == 0 || !valid_dtype(out_kind)) return 0;
+  const DeviceInfo* dev = nullptr;
+  const int st = device_info(&dev);
+  if (st != T3_OK) return st;
+  return glu_plan(A, Wg, Wu, C, M, N, K, pre_gate, pre_up, out_kind, dev->sms).bytes;
+}
+
+int t3_gemm_fwd_glu(const int8_t* A, const uint8_t* Wg, const uint8_t* Wu, void* C, int64_t M, int64_t N, int64_t K,
+                    const float* row_scale, const float* gate_scale, const float* up_scale, const float* gate_bias,
+                    const float* up_bias, int act, void* pre_gate, void* pre_up, int out_kind, void* workspace,
+                    int64_t workspace_bytes, t3_stream_t stream) {
+  if (bad_dims(M, N, K) || !valid_dtype(out_kind) || !valid_act(act) || workspace_bytes < 0) return T3_EINVAL;
+  if (M == 0 || N == 0) return T3_OK;
+  if (!C || (K > 0 && (!A || !Wg || !Wu)) || C == pre_gate || C == pre_up || (pre_gate && pre_gate == pre_up) ||
+      (workspace && (workspace == C || workspace == pre_gate || workspace == pre_up)))
+    return T3_EINVAL;
+  if (K > kMaxTernaryReduction) return T3_EOVERFLOW;
+  const GluArgs e{row_scale, {gate_scale, up_scale}, {gate_bias, up_bias}, {pre_gate, pre_up}, act};
+  const DeviceInfo* dev = nullptr;
+  int st = device_info(&dev);
+  if (st != T3_OK) return st;
+  const GluPlan p = glu_plan(A, Wg, Wu, C, M, N, K, pre_gate, pre_up, out_kind, dev->sms);
+  if (p.bytes > 0 && (!workspace || workspace_bytes < p.bytes || reinterpret_cast<uintptr_t>(workspace) % 16 != 0))
+    return T3_EINVAL;
+  uint8_t* base = static_cast<uint8_t*>(workspace);
+  int32_t* x[2] = {nullptr, nullptr};
+  for (int i = 0; i < 2; ++i)
+    if (p.x[i] >= 0) x[i] = reinterpret_cast<int32_t*>(base + p.x[i]);
+  switch (p.route) {
+    case GluPlan::kGemv: return launch_gemv_fwd_glu(A, Wg, Wu, C, e, out_kind, M, N, K, dev->sms, stream);
+    case GluPlan::kSmall: return launch_small_glu(A, Wg, Wu, C, e, out_kind, M, N, K, stream);
+    case GluPlan::kFew: return launch_few_glu(A, Wg, Wu, C, e, out_kind, M, N, K, stream);
+    case GluPlan::kPairs: {
+      const int8_t* A2 = p.a >= 0 ? reinterpret_cast<const int8_t*>(base + p.a) : A;
+      const uint8_t* w[2] = {p.w[0] >= 0 ? base + p.w[0] : Wg, p.w[1] >= 0 ? base + p.w[1] : Wu};
+      if (p.w[0] >= 0) {
+        const int64_t KB = (K + 3) / 4;
+        st = launch_align_rows(p.a >= 0 ? reinterpret_cast<const uint8_t*>(A) : nullptr, M, K, base + p.a, M, p.K, Wg,
+                               N, KB, base + p.w[0], p.N, p.K / 4, stream);
+        if (st == T3_OK)
+          st = launch_align_rows(nullptr, 0, 0, nullptr, 0, 16, Wu, N, KB, base + p.w[1], p.N, p.K / 4, stream);
+      } else if (p.a >= 0) {
+        st = launch_align_rows(nullptr, 0, 0, nullptr, 0, 16, reinterpret_cast<const uint8_t*>(A), M, K, base + p.a, M,
+                               p.K, stream);
+      }
+      if (st != T3_OK) return st;
+      if (!x[0]) return run_tc2_glu(A2, w[0], w[1], C, M, N, p.K, e, out_kind, dev, stream);
+      // weights laid out have rows of zeros up to N'; the caller's have N
+      const int64_t n = p.w[0] >= 0 ? p.N : N;
+      for (int i = 0; i < 2 && st == T3_OK; ++i) st = run_tc2<kOpFwd>(A2, w[i], x[i], M, n, p.K, stream);
+      return st != T3_OK ? st : launch_glu_epilogue(x[0], x[1], n, C, e, M, N, out_kind, dev->sms, stream);
+    }
+    case GluPlan::kTwoKernels: break;
+  }
+  st = t3_gemm_fwd(A, Wg, x[0], M, N, K, stream);
+  if (st == T3_OK) st = t3_gemm_fwd(A, Wu, x[1], M, N, K, stream);
+  return st != T3_OK ? st : launch_glu_epilogue(x[0], x[1], N, C, e, M, N, out_kind, dev->sms, stream);
+}
+
+int t3_glu_bwd(const void* dy, const void* gate, const void* up, int act, void* dgate, void* dup, float* dgate_bias,
+               float* dup_bias, int64_t rows, int64_t cols, int dtype, float* workspace, t3_stream_t stream) {
+  if (bad_dims(rows, cols, 0) || !valid_dtype(dtype) || !valid_act(act) || (dgate && dgate == dup) ||
+      (dgate_bias && dgate_bias == dup_bias))
+    return T3_EINVAL;
+  if (cols == 0 || (!dgate && !dup && !dgate_bias && !dup_bias)) return T3_OK;
+  if (rows == 0) {
+    const int st = dgate_bias ? zero_fill(reinterpret_cast<int32_t*>(dgate_bias), 1, cols, stream) : T3_OK;
+    return st == T3_OK && dup_bias ? zero_fill(reinterpret_cast<int32_t*>(dup_bias), 1, cols, stream) : st;
+  }
+  if (!dy || !gate || !up || ((dgate_bias || dup_bias) && !workspace)) return T3_EINVAL;
+  const DeviceInfo* dev = nullptr;
+  const int st = device_info(&dev);
+  if (st != T3_OK) return st;
+  return launch_glu_bwd(dy, gate, up, act, dgate, dup, dgate_bias, dup_bias, rows, cols, dtype, workspace, dev->sms,
+                        stream);
 }
 
 int64_t t3_set_small_product_limit(int64_t macs) {

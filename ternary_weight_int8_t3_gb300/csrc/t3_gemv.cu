@@ -58,11 +58,13 @@ __device__ __forceinline__ void decode16_s8(uint32_t x, uint32_t (&w)[4]) {
 // shared memory serves R rows.  kVec: packed rows of a multiple of 16 bytes
 // at a 16-byte aligned base (16-byte loads); else the chunks are assembled
 // from single bytes.
-template <int MR, bool kVec, class Out>
+// kTwo: two weights over one A (Wp and Wp2), half of a warp's rows of each.
+template <int MR, bool kVec, bool kTwo, class Out>
 __global__ void __launch_bounds__(32 * kWarps, 1)
-    gemv_kernel(const int8_t* __restrict__ A, const uint8_t* __restrict__ Wp,
+    gemv_kernel(const int8_t* __restrict__ A, const uint8_t* __restrict__ Wp, const uint8_t* __restrict__ Wp2,
                 const Out out, int M, int N, int K, int64_t KB, int groups) {
   constexpr int R = MR <= 4 ? 4 : 2;
+  constexpr int RN = kTwo ? R / 2 : R;  // columns of the output a warp takes at once
   // A's copy, [MR][4][chunks]: entry (m, q, j) holds the 16 activations of
   // 16-k group 4 j + q in the decode's order, so that consecutive lanes (chunks
   // j) read consecutive 16-byte entries
@@ -78,13 +80,15 @@ __global__ void __launch_bounds__(32 * kWarps, 1)
     // the share's packed rows are contiguous: ask them into L2 while the grid
     // before is still running (a hint only; the loads come after the wait)
     int64_t bytes = (ne - nb) * KB;
-    const int64_t cap = kPrefetchBytes / gridDim.x / 16 * 16;
+    const int64_t cap = kPrefetchBytes / (kTwo ? 2 : 1) / gridDim.x / 16 * 16;
     if (bytes > cap) bytes = cap;
     const uint8_t* base = Wp + nb * KB;
     for (int64_t off = static_cast<int64_t>(tid) * kPrefetchPiece; off < bytes;
-         off += static_cast<int64_t>(32 * kWarps) * kPrefetchPiece)
-      bulk_prefetch_l2(base + off, static_cast<uint32_t>(bytes - off < kPrefetchPiece ? bytes - off
-                                                                                      : kPrefetchPiece));
+         off += static_cast<int64_t>(32 * kWarps) * kPrefetchPiece) {
+      const uint32_t piece = static_cast<uint32_t>(bytes - off < kPrefetchPiece ? bytes - off : kPrefetchPiece);
+      bulk_prefetch_l2(base + off, piece);
+      if (kTwo) bulk_prefetch_l2(Wp2 + nb * KB + off, piece);
+    }
   }
   grid_dependency_wait();  // A and Wp exist, and C is no longer read by the grid before
   // rows of A in 16-byte pieces where they allow (K a multiple of 16, aligned)
@@ -113,21 +117,21 @@ __global__ void __launch_bounds__(32 * kWarps, 1)
   }
   __syncthreads();
   const int64_t chunks = (KB + 15) / 16;
-  for (int64_t n0 = nb + static_cast<int64_t>(warp) * R; n0 < ne; n0 += kWarps * R) {
+  for (int64_t n0 = nb + static_cast<int64_t>(warp) * RN; n0 < ne; n0 += kWarps * RN) {
     int32_t acc[R][MR];
 #pragma unroll
     for (int r = 0; r < R; ++r)
 #pragma unroll
       for (int m = 0; m < MR; ++m) acc[r][m] = 0;
     typename Out::Ahead ahead{};
-    if (lane < R * MR && lane % MR < M && n0 + lane / MR < ne) ahead = out.ahead(lane % MR, n0 + lane / MR, N);
+    if (lane < RN * MR && lane % MR < M && n0 + lane / MR < ne) ahead = out.ahead(lane % MR, n0 + lane / MR, N);
 #pragma unroll 2
     for (int64_t j = lane; j < chunks; j += 32) {
       uint32_t c[R][4];
 #pragma unroll
       for (int r = 0; r < R; ++r) {
-        const int64_t n = n0 + r < ne ? n0 + r : n0;  // rows past the share repeat row n0, unused
-        const uint8_t* wrow = Wp + n * KB;
+        const int64_t n = n0 + r % RN < ne ? n0 + r % RN : n0;  // rows past the share repeat row n0, unused
+        const uint8_t* wrow = (r < RN ? Wp : Wp2) + n * KB;
         if (kVec) {
           const uint4 v = __ldg(reinterpret_cast<const uint4*>(wrow) + j);
           c[r][0] = v.x;
@@ -171,28 +175,32 @@ __global__ void __launch_bounds__(32 * kWarps, 1)
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) acc[r][m] += __shfl_xor_sync(0xffffffffu, acc[r][m], o);
 #pragma unroll
-    for (int r = 0; r < R; ++r)
+    for (int r = 0; r < RN; ++r)
 #pragma unroll
       for (int m = 0; m < MR; ++m)
-        if (lane == r * MR + m && m < M && n0 + r < ne)
-          out.put(static_cast<int64_t>(m) * N + n0 + r, acc[r][m], ahead);
+        if (lane == r * MR + m && m < M && n0 + r < ne) {
+          if constexpr (kTwo)
+            out.put(static_cast<int64_t>(m) * N + n0 + r, acc[r][m], acc[RN + r][m], ahead);
+          else
+            out.put(static_cast<int64_t>(m) * N + n0 + r, acc[r][m], ahead);
+        }
   }
 }
 
-template <int MR, class Out>
+template <int MR, bool kTwo, class Out>
 int set_attrs() {
-  return (cudaFuncSetAttribute(gemv_kernel<MR, true, Out>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+  return (cudaFuncSetAttribute(gemv_kernel<MR, true, kTwo, Out>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                static_cast<int>(kMaxSmem)) == cudaSuccess &&
-          cudaFuncSetAttribute(gemv_kernel<MR, false, Out>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+          cudaFuncSetAttribute(gemv_kernel<MR, false, kTwo, Out>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                static_cast<int>(kMaxSmem)) == cudaSuccess)
              ? T3_OK
              : T3_ECUDA;
 }
 
-template <int MR, class Out>
-int launch_mr(const int8_t* A, const uint8_t* Wp, const Out& out, int M, int N, int K, int64_t KB,
+template <int MR, bool kTwo, class Out>
+int launch_mr(const int8_t* A, const uint8_t* Wp, const uint8_t* Wp2, const Out& out, int M, int N, int K, int64_t KB,
               int groups, int64_t smem, int grid, bool vec, cudaStream_t s) {
-  auto fn = vec ? gemv_kernel<MR, true, Out> : gemv_kernel<MR, false, Out>;
+  auto fn = vec ? gemv_kernel<MR, true, kTwo, Out> : gemv_kernel<MR, false, kTwo, Out>;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
@@ -203,7 +211,7 @@ int launch_mr(const int8_t* A, const uint8_t* Wp, const Out& out, int M, int N, 
   cfg.stream = s;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  if (cudaLaunchKernelEx(&cfg, fn, A, Wp, out, M, N, K, KB, groups) != cudaSuccess) return T3_ECUDA;
+  if (cudaLaunchKernelEx(&cfg, fn, A, Wp, Wp2, out, M, N, K, KB, groups) != cudaSuccess) return T3_ECUDA;
   return cudaGetLastError() == cudaSuccess ? T3_OK : T3_ECUDA;
 }
 
@@ -212,21 +220,22 @@ int64_t k_groups(int64_t K) { return (K + 63) / 64 * 4; }
 int padded_rows(int64_t M) { return M <= 1 ? 1 : M <= 2 ? 2 : M <= 4 ? 4 : 8; }
 int64_t copy_bytes(int64_t M, int64_t K) { return padded_rows(M) * k_groups(K) * 16; }
 
-template <class Out>
-int launch_any(const int8_t* A, const uint8_t* Wp, const Out& out, int64_t M, int64_t N, int64_t K, int sms,
+template <bool kTwo, class Out>
+int launch_any(const int8_t* A, const uint8_t* Wp, const uint8_t* Wp2, const Out& out, int64_t M, int64_t N, int64_t K, int sms,
                cudaStream_t s) {
   const int64_t KB = (K + 3) / 4;
   if (!gemv_fits(M, N, K)) return T3_EINVAL;
   const int64_t groups = k_groups(K), smem = copy_bytes(M, K);
   const int mr = padded_rows(M);
-  const bool vec = (KB % 16 == 0) && (reinterpret_cast<uintptr_t>(Wp) % 16 == 0);
+  const bool vec = (KB % 16 == 0) && (reinterpret_cast<uintptr_t>(Wp) % 16 == 0) &&
+                   (!kTwo || reinterpret_cast<uintptr_t>(Wp2) % 16 == 0);
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return T3_ECUDA;
   static std::atomic<bool> attr_done[64];
   if (dev < 0 || dev >= 64) return T3_EDEVICE;
   if (!attr_done[dev].load(std::memory_order_acquire)) {
-    if (set_attrs<1, Out>() != T3_OK || set_attrs<2, Out>() != T3_OK || set_attrs<4, Out>() != T3_OK ||
-        set_attrs<8, Out>() != T3_OK)
+    if (set_attrs<1, kTwo, Out>() != T3_OK || set_attrs<2, kTwo, Out>() != T3_OK ||
+        set_attrs<4, kTwo, Out>() != T3_OK || set_attrs<8, kTwo, Out>() != T3_OK)
       return T3_ECUDA;
     attr_done[dev].store(true, std::memory_order_release);
   }
@@ -236,10 +245,10 @@ int launch_any(const int8_t* A, const uint8_t* Wp, const Out& out, int64_t M, in
   const int m = static_cast<int>(M), n = static_cast<int>(N), k = static_cast<int>(K);
   const int gr = static_cast<int>(groups);
   switch (mr) {
-    case 1: return launch_mr<1>(A, Wp, out, m, n, k, KB, gr, smem, grid, vec, s);
-    case 2: return launch_mr<2>(A, Wp, out, m, n, k, KB, gr, smem, grid, vec, s);
-    case 4: return launch_mr<4>(A, Wp, out, m, n, k, KB, gr, smem, grid, vec, s);
-    default: return launch_mr<8>(A, Wp, out, m, n, k, KB, gr, smem, grid, vec, s);
+    case 1: return launch_mr<1, kTwo>(A, Wp, Wp2, out, m, n, k, KB, gr, smem, grid, vec, s);
+    case 2: return launch_mr<2, kTwo>(A, Wp, Wp2, out, m, n, k, KB, gr, smem, grid, vec, s);
+    case 4: return launch_mr<4, kTwo>(A, Wp, Wp2, out, m, n, k, KB, gr, smem, grid, vec, s);
+    default: return launch_mr<8, kTwo>(A, Wp, Wp2, out, m, n, k, KB, gr, smem, grid, vec, s);
   }
 }
 
@@ -251,14 +260,21 @@ bool gemv_fits(int64_t M, int64_t N, int64_t K) {
 
 int launch_gemv_fwd(const int8_t* A, const uint8_t* Wp, int32_t* C, int64_t M, int64_t N,
                     int64_t K, int sms, cudaStream_t s) {
-  return gv::launch_any(A, Wp, OutI32{C}, M, N, K, sms, s);
+  return gv::launch_any<false>(A, Wp, nullptr, OutI32{C}, M, N, K, sms, s);
 }
 
 int launch_gemv_fwd_act(const int8_t* A, const uint8_t* Wp, void* C, const EpilogueArgs& e, int kind,
                         int64_t M, int64_t N, int64_t K, int sms, cudaStream_t s) {
   if (kind == T3_OUT_BF16)
-    return gv::launch_any(A, Wp, OutAct<__nv_bfloat16>{static_cast<__nv_bfloat16*>(C), e}, M, N, K, sms, s);
-  return gv::launch_any(A, Wp, OutAct<float>{static_cast<float*>(C), e}, M, N, K, sms, s);
+    return gv::launch_any<false>(A, Wp, nullptr, OutAct<__nv_bfloat16>{static_cast<__nv_bfloat16*>(C), e}, M, N, K, sms, s);
+  return gv::launch_any<false>(A, Wp, nullptr, OutAct<float>{static_cast<float*>(C), e}, M, N, K, sms, s);
+}
+
+int launch_gemv_fwd_glu(const int8_t* A, const uint8_t* Wg, const uint8_t* Wu, void* C, const GluArgs& e, int kind,
+                        int64_t M, int64_t N, int64_t K, int sms, cudaStream_t s) {
+  if (kind == T3_OUT_BF16)
+    return gv::launch_any<true>(A, Wg, Wu, OutGlu<__nv_bfloat16>{static_cast<__nv_bfloat16*>(C), e}, M, N, K, sms, s);
+  return gv::launch_any<true>(A, Wg, Wu, OutGlu<float>{static_cast<float*>(C), e}, M, N, K, sms, s);
 }
 
 }  // namespace t3

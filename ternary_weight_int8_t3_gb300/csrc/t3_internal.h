@@ -41,6 +41,11 @@ int launch_tc2_fwd_bf16(const tc2::Params& p, const CUtensorMap& ma, const CUten
 int launch_tc2_fwd_act(const tc2::Params& p, const CUtensorMap& ma, const CUtensorMap& mw,
                        const CUtensorMap& mo, const tc2::ActMaps& more, int grid, cudaStream_t s);
 
+// Two forwards with their product in the epilogue (tc2::kModeGlu; p.glu): mw maps the gate's weights,
+// `more` the other's and p.glu.pre where those are set.
+int launch_tc2_fwd_glu(const tc2::Params& p, const CUtensorMap& ma, const CUtensorMap& mw,
+                       const CUtensorMap& mo, const tc2::GluMaps& more, int grid, cudaStream_t s);
+
 // Zeroes out[0, n) on `s` as a programmatic dependent of the work before it:
 // it waits for that work to complete, then lets the next grid launch early.
 int launch_zero_pdl(int32_t* out, int64_t n, int sms, cudaStream_t s);
@@ -79,6 +84,10 @@ bool gemv_fits(int64_t M, int64_t N, int64_t K);
 int launch_gemv_fwd_act(const int8_t* A, const uint8_t* Wp, void* C, const EpilogueArgs& e, int kind,
                         int64_t M, int64_t N, int64_t K, int sms, cudaStream_t s);
 
+// The same with two weights over one A.
+int launch_gemv_fwd_glu(const int8_t* A, const uint8_t* Wg, const uint8_t* Wu, void* C, const GluArgs& e, int kind,
+                        int64_t M, int64_t N, int64_t K, int sms, cudaStream_t s);
+
 // The three products on the CUDA cores for small problems, any alignment
 // (t3_small.cu): op 1 C = A.W (x = A, wp = Wp), 2 dX = dY.Wᵀ (x = dY, wp = Wp),
 // 3 dW = Aᵀ.dY (x = A, y = dY); int32 output, written whole (zeroed first
@@ -95,6 +104,12 @@ int launch_small_act(const int8_t* A, const uint8_t* Wp, void* C, const Epilogue
                      int64_t N, int64_t K, cudaStream_t s);
 int launch_few_act(const int8_t* A, const uint8_t* Wp, void* C, const EpilogueArgs& e, int kind, int64_t M,
                    int64_t N, int64_t K, cudaStream_t s);
+
+// The same two with two weights over one A; the fits take twice the columns.
+int launch_small_glu(const int8_t* A, const uint8_t* Wg, const uint8_t* Wu, void* C, const GluArgs& e, int kind,
+                     int64_t M, int64_t N, int64_t K, cudaStream_t s);
+int launch_few_glu(const int8_t* A, const uint8_t* Wg, const uint8_t* Wu, void* C, const GluArgs& e, int kind,
+                   int64_t M, int64_t N, int64_t K, cudaStream_t s);
 
 // Small-M forward (M <= 32) on the tensor cores.
 int launch_skinny_fwd(const int8_t* A, const uint8_t* Wp, int32_t* C, int64_t M, int64_t N,
@@ -154,6 +169,16 @@ int launch_align_rows(const uint8_t* a, int64_t rows_a, int64_t len_a, uint8_t* 
 // dz = dy act'(z) and its column sums.
 int launch_act_bwd(const void* dy, const void* z, int act, void* dz, float* dbias, int64_t rows,
                    int64_t cols, int dtype, float* workspace, int sms, cudaStream_t s);
+
+// What follows two products (GluArgs) on their int32 results, with row stride ldx
+// (t3_glu.cu).
+int launch_glu_epilogue(const int32_t* gate, const int32_t* up, int64_t ldx, void* out, const GluArgs& e, int64_t rows,
+                        int64_t cols, int kind, int sms, cudaStream_t s);
+
+// dgate = dy up act'(gate), dup = dy act(gate), and their column sums.
+int launch_glu_bwd(const void* dy, const void* gate, const void* up, int act, void* dgate, void* dup,
+                   float* dgate_bias, float* dup_bias, int64_t rows, int64_t cols, int dtype, float* workspace,
+                   int sms, cudaStream_t s);
 
 // The recurrence's wait between CTAs, run out on purpose (t3_selftest_scan_wait_timeout).
 int launch_scan_wait_selftest(int* err, uint64_t limit_ns, cudaStream_t s);

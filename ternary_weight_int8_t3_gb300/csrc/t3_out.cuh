@@ -50,4 +50,31 @@ struct OutAct {
   }
 };
 
+// Two sums at once, of the gate's and the other's weights.
+template <class T>
+struct OutGlu {
+  T* C;
+  GluArgs e;
+  struct Ahead {
+    float rs, scale[2], bias[2];
+  };
+  __device__ __forceinline__ Ahead ahead(int64_t m, int64_t n, int64_t) const {
+    Ahead a;
+    a.rs = e.row_scale ? __ldg(e.row_scale + m) : 1.0f;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      a.scale[i] = e.scale[i] ? __ldg(e.scale[i] + n) : 1.0f;
+      a.bias[i] = e.bias[i] ? __ldg(e.bias[i] + n) : 0.0f;
+    }
+    return a;
+  }
+  __device__ __forceinline__ void put(int64_t at, int32_t gate, int32_t up, const Ahead& a) const {
+    const float zg = __fadd_rn(__fmul_rn(__fmul_rn(__int2float_rn(gate), a.rs), a.scale[0]), a.bias[0]);
+    const float zu = __fadd_rn(__fmul_rn(__fmul_rn(__int2float_rn(up), a.rs), a.scale[1]), a.bias[1]);
+    if (e.pre[0]) OutAct<T>::write(static_cast<T*>(e.pre[0]) + at, zg);
+    if (e.pre[1]) OutAct<T>::write(static_cast<T*>(e.pre[1]) + at, zu);
+    OutAct<T>::write(C + at, __fmul_rn(vec::act_any(zg, e.act), zu));  // the same bits on every route
+  }
+};
+
 }  // namespace t3

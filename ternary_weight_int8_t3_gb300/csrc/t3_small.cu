@@ -51,6 +51,7 @@ struct Params {
   const int8_t* x;     // fwd: A [M][K]; dX: dY [M][N]; dW: A [M][K]
   const int8_t* y;     // dW: dY [M][N]
   const uint8_t* wp;   // fwd, dX: Wp [N][KB]
+  const uint8_t* wp2;  // the second weights of a product with two
   int32_t* out;        // fwd: C [M][N]; dX: dX [M][K]; dW: dW [K][N]
   int64_t M, N, K, KB;
   int64_t rows, cols;  // the output's shape
@@ -136,7 +137,7 @@ __device__ __forceinline__ void decode16_s8(uint32_t x, uint32_t (&w)[4]) {
 
 // Stages chunk [r0, r0 + 64) of the reduction for output rows [row0, +64) (X)
 // and columns [col0, +64) (Y).
-template <int OP>
+template <int OP, bool kTwo>
 __device__ __forceinline__ void stage(const Params& p, int64_t row0, int64_t col0, int64_t r0,
                                       uint32_t (*xs)[kPitch], uint32_t (*ys)[kPitch], int t) {
   if constexpr (OP == kFwd || OP == kDx) {
@@ -152,10 +153,12 @@ __device__ __forceinline__ void stage(const Params& p, int64_t row0, int64_t col
       *dst = v;
   }
   if constexpr (OP == kFwd) {
-    // Y: weight row col0 + t/4, its codes for k in [r0 + 16 (t % 4), +16)
+    // Y: weight row col0 + t/4, its codes for k in [r0 + 16 (t % 4), +16); with two weights
+    // the lower half of the rows is the first's, the upper half the second's
     const int row = t >> 2, seg = t & 3;
     uint32_t w[4];
-    decode16_s8(load_codes4(p.wp, p.N, p.KB, col0 + row, r0 / 4 + 4 * seg), w);
+    const bool second = kTwo && row >= kTile / 2;
+    decode16_s8(load_codes4(second ? p.wp2 : p.wp, p.N, p.KB, col0 + row - (second ? kTile / 2 : 0), r0 / 4 + 4 * seg), w);
     *reinterpret_cast<uint4*>(&ys[row][4 * seg]) = make_uint4(w[0], w[1], w[2], w[3]);
   } else if constexpr (OP == kDx) {
     // Y: k in [col0, +64) as rows, n along the words: packed rows n0 + 4 g .. +3,
@@ -191,7 +194,7 @@ __device__ __forceinline__ void stage(const Params& p, int64_t row0, int64_t col
 
 // The sums of a tile's 4 x 4 block of this thread (rows ty + 16 i, columns
 // tx + 16 j) over chunks [c0, c1) of the reduction.
-template <int OP>
+template <int OP, bool kTwo = false>
 __device__ __forceinline__ void tile_sums(const Params& p, int64_t row0, int64_t col0, int64_t c0, int64_t c1,
                                           uint32_t (*xs)[kPitch], uint32_t (*ys)[kPitch], int t,
                                           int32_t (&acc)[4][4]) {
@@ -201,7 +204,7 @@ __device__ __forceinline__ void tile_sums(const Params& p, int64_t row0, int64_t
 #pragma unroll
     for (int j = 0; j < 4; ++j) acc[i][j] = 0;
   for (int64_t c = c0; c < c1; ++c) {
-    stage<OP>(p, row0, col0, c * kChunk, xs, ys, t);
+    stage<OP, kTwo>(p, row0, col0, c * kChunk, xs, ys, t);
     __syncthreads();
 #pragma unroll
     for (int w4 = 0; w4 < kWords / 4; ++w4) {
@@ -277,6 +280,34 @@ __global__ void __launch_bounds__(kThreads) small_act_kernel(const Params p, con
   }
 }
 
+// The forward with two weights: a tile's columns are kTile / 2 of each, so that a thread's
+// columns j and j + 2 are the two sums of one output.
+constexpr int kTwoCols = kTile / 2;
+
+template <class Out>
+__global__ void __launch_bounds__(kThreads) small_glu_kernel(const Params p, const Out out) {
+  __shared__ __align__(16) uint32_t xs[kTile][kPitch];
+  __shared__ __align__(16) uint32_t ys[kTile][kPitch];
+  const int t = threadIdx.x, ty = t >> 4, tx = t & 15;
+  const int64_t row0 = (blockIdx.x / p.tiles_c) * kTile, col0 = (blockIdx.x % p.tiles_c) * kTwoCols;
+  launch_dependents();
+  grid_dependency_wait();
+  int32_t acc[4][4];
+  tile_sums<kFwd, true>(p, row0, col0, 0, p.chunks, xs, ys, t, acc);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int64_t r = row0 + ty + 16 * i;
+    if (r >= p.rows) continue;
+    typename Out::Ahead a[2];
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+      if (col0 + tx + 16 * j < p.cols) a[j] = out.ahead(r, col0 + tx + 16 * j, p.cols);
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+      if (col0 + tx + 16 * j < p.cols) out.put(r * p.cols + col0 + tx + 16 * j, acc[i][j], acc[i][j + 2], a[j]);
+  }
+}
+
 // The forward with a layer's epilogue where the tiles above are few: a CTA takes a
 // small tile, and its warps split the reduction and join in shared memory, so
 // that the sum ends in one launch and needs neither zeros nor an int32 output.
@@ -319,20 +350,24 @@ __device__ __forceinline__ uint4 load16_words(const int8_t* base, int64_t total,
   return make_uint4(b[0], b[1], b[2], b[3]);
 }
 
-template <class Out>
+// kTwo: two weights, half of the tile's columns of each.
+template <bool kTwo, class Out>
 __global__ void __launch_bounds__(32 * kFewWarps) few_act_kernel(const Params p, const Out out) {
+  constexpr int kCols = kTwo ? kFewCols / 2 : kFewCols;  // of the output
   __shared__ __align__(16) uint32_t stage[kFewWarps][kFewRows + kFewCols][kFewPitch];
   __shared__ int32_t sums[kFewWarps][16 * kFewSlot];
   const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
   const int64_t tr = blockIdx.x / p.tiles_c;
-  const int64_t row0 = tr * kFewRows, col0 = (blockIdx.x - tr * p.tiles_c) * kFewCols;
+  const int64_t row0 = tr * kFewRows, col0 = (blockIdx.x - tr * p.tiles_c) * kCols;
   launch_dependents();
   grid_dependency_wait();
-  // this thread's outputs: rows t / 16 and t / 16 + 16, column t % 16
-  const int64_t col = col0 + (t & 15), r0 = row0 + (t >> 4);
-  typename Out::Ahead ahead[2];
+  // this thread's outputs: rows t / 16 and t / 16 + 16, column t % 16; with two weights
+  // row t / 8, column t % 8
+  const int64_t col = col0 + t % kCols, r0 = row0 + t / kCols;
+  constexpr int kOuts = kTwo ? 1 : 2;
+  typename Out::Ahead ahead[kOuts];
 #pragma unroll
-  for (int u = 0; u < 2; ++u)
+  for (int u = 0; u < kOuts; ++u)
     if (col < p.cols && r0 + 16 * u < p.rows) ahead[u] = out.ahead(r0 + 16 * u, col, p.cols);
 
   uint32_t(*xs)[kFewPitch] = stage[warp];
@@ -340,7 +375,8 @@ __global__ void __launch_bounds__(32 * kFewWarps) few_act_kernel(const Params p,
   // a lane loads 16 elements of rows lane / 2 and lane / 2 + 16, and 16 codes of one
   // of the 16 weight rows, a chunk of its warp ahead
   const int lrow = lane >> 1, seg = lane & 1;
-  const int64_t total = p.M * p.K, n = col0 + lrow;
+  const int64_t total = p.M * p.K, n = col0 + lrow % kCols;
+  const uint8_t* wp = lrow < kCols ? p.wp : p.wp2;
   uint4 xv[2];
   uint32_t code;
   auto fetch = [&](int64_t c) {
@@ -351,9 +387,9 @@ __global__ void __launch_bounds__(32 * kFewWarps) few_act_kernel(const Params p,
       xv[u] = load16_words(p.x, total, m * p.K + k, m < p.M ? p.K - k : 0, p.x_vec);
     }
     if (p.w_vec)
-      code = n < p.N && b < p.KB ? __ldg(reinterpret_cast<const uint32_t*>(p.wp + n * p.KB + b)) : 0u;
+      code = n < p.N && b < p.KB ? __ldg(reinterpret_cast<const uint32_t*>(wp + n * p.KB + b)) : 0u;
     else
-      code = load_codes4(p.wp, p.N, p.KB, n, b);
+      code = load_codes4(wp, p.N, p.KB, n, b);
   };
   int32_t acc[4][4];
 #pragma unroll
@@ -397,14 +433,24 @@ __global__ void __launch_bounds__(32 * kFewWarps) few_act_kernel(const Params p,
 #pragma unroll
     for (int j = 0; j < 4; ++j) sums[warp][(4 * i + j) * kFewSlot + lane] = acc[i][j];
   __syncthreads();
-#pragma unroll
-  for (int u = 0; u < 2; ++u) {
-    const int r = (t >> 4) + 16 * u, c = t & 15;  // in the tile
+  auto joined = [&](int r, int c) {  // row r, column c of the tile
     const int at = (4 * (r >> 3) + (c >> 2)) * kFewSlot + 4 * (r & 7) + (c & 3);
     int32_t sum = 0;
 #pragma unroll
     for (int i = 0; i < kFewWarps; ++i) sum += sums[i][at];
-    if (col < p.cols && row0 + r < p.rows) out.put((row0 + r) * p.cols + col, sum, ahead[u]);
+    return sum;
+  };
+  if constexpr (kTwo) {
+    const int r = t / kCols, c = t % kCols;
+    const int32_t gate = joined(r, c), up = joined(r, c + kCols);
+    if (col < p.cols && row0 + r < p.rows) out.put((row0 + r) * p.cols + col, gate, up, ahead[0]);
+  } else {
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      const int r = (t >> 4) + 16 * u;
+      const int32_t sum = joined(r, t & 15);
+      if (col < p.cols && row0 + r < p.rows) out.put((row0 + r) * p.cols + col, sum, ahead[u]);
+    }
   }
 }
 
@@ -516,10 +562,45 @@ int launch_few_act(const int8_t* A, const uint8_t* Wp, void* C, const EpilogueAr
   p.chunks = (K + smp::kFewChunk - 1) / smp::kFewChunk;
   const int64_t grid = (M + smp::kFewRows - 1) / smp::kFewRows * p.tiles_c;
   if (kind == T3_OUT_BF16)
-    return vec::launch(smp::few_act_kernel<OutAct<__nv_bfloat16>>, grid, 32 * smp::kFewWarps, 0, s, 1, p,
+    return vec::launch(smp::few_act_kernel<false, OutAct<__nv_bfloat16>>, grid, 32 * smp::kFewWarps, 0, s, 1, p,
                        OutAct<__nv_bfloat16>{static_cast<__nv_bfloat16*>(C), e});
-  return vec::launch(smp::few_act_kernel<OutAct<float>>, grid, 32 * smp::kFewWarps, 0, s, 1, p,
+  return vec::launch(smp::few_act_kernel<false, OutAct<float>>, grid, 32 * smp::kFewWarps, 0, s, 1, p,
                      OutAct<float>{static_cast<float*>(C), e});
+}
+
+namespace smp {
+Params glu_params(const int8_t* A, const uint8_t* Wg, const uint8_t* Wu, int64_t M, int64_t N, int64_t K) {
+  Params p = act_params(A, Wg, M, N, K);
+  p.wp2 = Wu;
+  p.w_vec = p.w_vec && reinterpret_cast<uintptr_t>(Wu) % 4 == 0;
+  return p;
+}
+}  // namespace smp
+
+int launch_small_glu(const int8_t* A, const uint8_t* Wg, const uint8_t* Wu, void* C, const GluArgs& e, int kind,
+                     int64_t M, int64_t N, int64_t K, cudaStream_t s) {
+  smp::Params p = smp::glu_params(A, Wg, Wu, M, N, K);
+  p.tiles_c = (N + smp::kTwoCols - 1) / smp::kTwoCols;
+  p.chunks = (K + smp::kChunk - 1) / smp::kChunk;
+  const int64_t grid = (M + smp::kTile - 1) / smp::kTile * p.tiles_c;
+  if (kind == T3_OUT_BF16)
+    return vec::launch(smp::small_glu_kernel<OutGlu<__nv_bfloat16>>, grid, smp::kThreads, 0, s, 1, p,
+                       OutGlu<__nv_bfloat16>{static_cast<__nv_bfloat16*>(C), e});
+  return vec::launch(smp::small_glu_kernel<OutGlu<float>>, grid, smp::kThreads, 0, s, 1, p,
+                     OutGlu<float>{static_cast<float*>(C), e});
+}
+
+int launch_few_glu(const int8_t* A, const uint8_t* Wg, const uint8_t* Wu, void* C, const GluArgs& e, int kind,
+                   int64_t M, int64_t N, int64_t K, cudaStream_t s) {
+  smp::Params p = smp::glu_params(A, Wg, Wu, M, N, K);
+  p.tiles_c = (N + smp::kFewCols / 2 - 1) / (smp::kFewCols / 2);
+  p.chunks = (K + smp::kFewChunk - 1) / smp::kFewChunk;
+  const int64_t grid = (M + smp::kFewRows - 1) / smp::kFewRows * p.tiles_c;
+  if (kind == T3_OUT_BF16)
+    return vec::launch(smp::few_act_kernel<true, OutGlu<__nv_bfloat16>>, grid, 32 * smp::kFewWarps, 0, s, 1, p,
+                       OutGlu<__nv_bfloat16>{static_cast<__nv_bfloat16*>(C), e});
+  return vec::launch(smp::few_act_kernel<true, OutGlu<float>>, grid, 32 * smp::kFewWarps, 0, s, 1, p,
+                     OutGlu<float>{static_cast<float*>(C), e});
 }
 
 }  // namespace t3

@@ -134,6 +134,8 @@ struct Params {
   const float* row_inv;
   // kModeAct: what the epilogue adds to the scales
   EpilogueArgs epi;
+  // kModeGlu: both products' epilogue
+  GluArgs glu;
   int* err;
 };
 
@@ -199,6 +201,13 @@ constexpr int kModeBf16 = 3;
 // shares its SM's issue slots and shared memory with the converters, so what it
 // adds is not free as in a kernel that the tensor pipe alone bounds.
 constexpr int kModeAct = 4;
+// Two forwards over one A with their product in the epilogue (operands by TMA, whole tiles, f32 or
+// bf16 output): the even CTA of a pair decodes 96 rows of the gate's weights and the odd
+// CTA the same 96 of the other's, so that a tile's accumulator holds both sums of 96 output columns
+// (the gate's in columns 0 to 95, the other's behind) and the main loop is the forward's own.
+constexpr int kModeGlu = 5;
+// Instantiations with a layer's epilogue.
+__host__ __device__ constexpr bool layer_epilogue(int mode) { return mode == kModeAct || mode == kModeGlu; }
 
 // Stages 32 floats of row `srow` for a bulk store: float (128-byte-swizzled rows
 // of 32 words, like the int32 path) or bf16 ([128][64 B], unswizzled).
@@ -314,6 +323,59 @@ __device__ __forceinline__ void stage_slot(uint8_t* slot, int lane, const float 
     for (int g = 0; g < 8; ++g)
       sts128(act_piece(slot, lane, g, false), __float_as_uint(y[4 * g]), __float_as_uint(y[4 * g + 1]),
              __float_as_uint(y[4 * g + 2]), __float_as_uint(y[4 * g + 3]));
+  }
+}
+
+// The same for kModeGlu's blocks of 16 columns: rows of 16 floats in the 64-byte swizzle
+// (16-byte piece g of row r at g ^ (r / 2) % 4), or of 16 bf16 in the 32-byte one (at g ^ (r / 4) % 2).
+__device__ __forceinline__ void scale_bias16(float (&y)[16], const uint32_t (&v)[16], float rs, const float* cs,
+                                             const float* bias) {
+#pragma unroll
+  for (int g = 0; g < 4; ++g) {
+    const float4 c = *reinterpret_cast<const float4*>(cs + 4 * g), b = *reinterpret_cast<const float4*>(bias + 4 * g);
+    y[4 * g] = __fadd_rn(__fmul_rn(__fmul_rn(__uint_as_float(v[4 * g]), rs), c.x), b.x);
+    y[4 * g + 1] = __fadd_rn(__fmul_rn(__fmul_rn(__uint_as_float(v[4 * g + 1]), rs), c.y), b.y);
+    y[4 * g + 2] = __fadd_rn(__fmul_rn(__fmul_rn(__uint_as_float(v[4 * g + 2]), rs), c.z), b.z);
+    y[4 * g + 3] = __fadd_rn(__fmul_rn(__fmul_rn(__uint_as_float(v[4 * g + 3]), rs), c.w), b.w);
+  }
+}
+
+constexpr int kGluSlot = 32 * 16 * 4;  // bytes of a slot
+
+__device__ __forceinline__ void stage_slot16(uint8_t* slot, int lane, const float (&y)[16], bool bf16) {
+  if (bf16) {
+#pragma unroll
+    for (int g = 0; g < 2; ++g) {
+      uint32_t w[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const __nv_bfloat162 b = __floats2bfloat162_rn(y[8 * g + 2 * j], y[8 * g + 2 * j + 1]);
+        w[j] = *reinterpret_cast<const uint32_t*>(&b);
+      }
+      sts128(slot + lane * 32 + ((g ^ (lane >> 2)) & 1) * 16, w[0], w[1], w[2], w[3]);
+    }
+  } else {
+#pragma unroll
+    for (int g = 0; g < 4; ++g)
+      sts128(slot + lane * 64 + ((g ^ (lane >> 1)) & 3) * 16, __float_as_uint(y[4 * g]), __float_as_uint(y[4 * g + 1]),
+             __float_as_uint(y[4 * g + 2]), __float_as_uint(y[4 * g + 3]));
+  }
+}
+
+// g = act(g) u, a product of its own.
+template <int ACT>
+__device__ __forceinline__ void glu_row(float (&g)[16], const float (&u)[16]) {
+#pragma unroll
+  for (int e = 0; e < 16; ++e) g[e] = __fmul_rn(vec::act<ACT>(g[e]), u[e]);
+}
+
+__device__ __forceinline__ void glu_row_any(float (&g)[16], const float (&u)[16], int act) {
+  switch (act) {
+    case T3_ACT_RELU: return glu_row<T3_ACT_RELU>(g, u);
+    case T3_ACT_RELU2: return glu_row<T3_ACT_RELU2>(g, u);
+    case T3_ACT_SILU: return glu_row<T3_ACT_SILU>(g, u);
+    case T3_ACT_GELU: return glu_row<T3_ACT_GELU>(g, u);
+    default: return glu_row<T3_ACT_NONE>(g, u);
   }
 }
 
@@ -755,6 +817,7 @@ __device__ __forceinline__ int64_t pair_stage_count(const Params& p, int pair, i
 // floats, or four of bf16.
 constexpr int kWarpStage = 2 * 32 * 32 * 4;
 static_assert(4 * kWarpStage <= 2 * Layout<kOpFwd>::stage_out, "four warps' slots fit the staging buffers");
+static_assert(4 * kGluSlot <= kWarpStage, "four slots of kModeGlu a warp");
 
 // kModeAct's further maps: the pre-activation's and the residual's.
 struct NoMap {};
@@ -763,13 +826,18 @@ struct ActMaps {
 };
 template <int kMode> struct MoreMapsOf { using type = NoMap; };
 template <> struct MoreMapsOf<kModeAct> { using type = ActMaps; };
+// kModeGlu's: the second weights and both pre-activations.
+struct GluMaps {
+  CUtensorMap w2, pre[2];
+};
+template <> struct MoreMapsOf<kModeGlu> { using type = GluMaps; };
 template <int kMode> using MoreMaps = typename MoreMapsOf<kMode>::type;
 
 // kSplit: the split schedule (operands by TMA only); without it every pair
 // takes whole tiles and the loops below reduce to plain tile loops.
 // Epilogue warps and threads of an instantiation: a layer's epilogue has about
 // three times the instructions of the others, and takes twice the warps.
-__host__ __device__ constexpr int epi_warps(int mode) { return mode == kModeAct ? 8 : 4; }
+__host__ __device__ constexpr int epi_warps(int mode) { return layer_epilogue(mode) ? 8 : 4; }
 __host__ __device__ constexpr int threads(int mode) { return 32 * (kConvWarps + 2 + epi_warps(mode)); }
 static_assert(threads(kModeTma) == kThreads, "four epilogue warps elsewhere");
 
@@ -780,7 +848,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads(kMode), 1)
                const __grid_constant__ CUtensorMap map_out,
                const __grid_constant__ MoreMaps<kMode> more) {
   static_assert(!kSplit || kMode == kModeTma, "the split schedule takes TMA operands");
-  static_assert(kMode != kModeAct || (OP == kOpFwd && !kSplit), "the layer epilogue: forward, whole tiles");
+  static_assert(!layer_epilogue(kMode) || (OP == kOpFwd && !kSplit), "the layer epilogue: forward, whole tiles");
   static_assert(kMode != kModeBf16 || (OP == kOpFwd && !kSplit), "bf16 activations: forward, whole tiles");
   using L = Layout<OP, kMode == kModeBf16 ? 2 : 1>;
   extern __shared__ uint8_t smem_raw[];
@@ -814,7 +882,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads(kMode), 1)
       // without weight TMA only the activation warps read the raw stages
       // the warps that read the raw stages release them
       const int readers = (p.a_tma ? kActWarps : 0) + (p.w_tma ? kWWarps : 0);
-      mbar_init(&raw_empty[s], (kMode == kModeTma || kMode == kModeBf16 || kMode == kModeAct) ? kConvWarps
+      mbar_init(&raw_empty[s], (kMode == kModeTma || kMode == kModeBf16 || layer_epilogue(kMode)) ? kConvWarps
                                : kMode == kModeWGlobal ? kActWarps
                                : (readers > 0 ? readers : 1));
     }
@@ -968,6 +1036,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads(kMode), 1)
     if (lane == 0 && !idle) {
       if (!ag_p) prefetch_tensormap(&map_a);
       if (!wg_p) prefetch_tensormap(&map_w);
+      if constexpr (kMode == kModeGlu) prefetch_tensormap(&more.w2);
     }
     uint32_t stage = 0, phase = 0, issued_mask = 0, issued_phase = 0;
     bool ok = true;
@@ -985,7 +1054,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads(kMode), 1)
       const int tr = tile / p.tiles_c, tcol = tile % p.tiles_c;
       const int ay = tr * BMP + static_cast<int>(rank) * 128;
       int wx, wy;  // weight box origin and its per-stage step
-      if (OP == kOpFwd) {
+      if (kMode == kModeGlu) {
+        wx = 0;
+        wy = tcol * BNH;
+      } else if (OP == kOpFwd) {
         wx = 0;
         wy = tcol * BN + static_cast<int>(rank) * BNH;
       } else {
@@ -1008,8 +1080,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads(kMode), 1)
             tma_load_2d(dst, &map_a, &raw_full[stage], static_cast<int>(kb * BK), ay);
           }
           if (!wg_p) {
+            const CUtensorMap* w_from = &map_w;
+            if constexpr (kMode == kModeGlu)
+              if (rank) w_from = &more.w2;
             if (OP == kOpFwd)
-              tma_load_2d(dst + L::raw_a, &map_w, &raw_full[stage], static_cast<int>(kb * (BK / 4)), wy);
+              tma_load_2d(dst + L::raw_a, w_from, &raw_full[stage], static_cast<int>(kb * (BK / 4)), wy);
             else
               tma_load_2d(dst + L::raw_a, &map_w, &raw_full[stage], wx, static_cast<int>(kb * BK));
           }
@@ -1122,7 +1197,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads(kMode), 1)
     if (p.use_tma_out && epi_tid == 0) prefetch_tensormap(&map_out);
     constexpr int kEpiThreads = 32 * epi_warps(kMode);
     // kModeAct: warps 4 to 7 of the epilogue take the tile's upper 96 columns
-    const int half = kMode == kModeAct ? (warp - kEpiWarp0) >> 2 : 0;
+    const int half = layer_epilogue(kMode) ? (warp - kEpiWarp0) >> 2 : 0;
     const int cb0 = half * (BN / 64), cb1 = kMode == kModeAct ? cb0 + BN / 64 : BN / 32;
     // kModeAct: the biases' tile, and this warp's ring of slots.  Each output of
     // a block (the pre-activation, where one is wanted, then C) takes the next
@@ -1169,6 +1244,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads(kMode), 1)
       if (has_res)
         for (int i = 0; i < lead; ++i) fetch(uses - 1);
     }
+    if constexpr (kMode == kModeGlu) {
+      for (int i = 0; i < 2; ++i)
+        if (epi_tid == 0 && p.glu.pre[i]) prefetch_tensormap(&more.pre[i]);
+    }
     // split schedule: the zeroing grid launched just before has finished
     // before the first output write
     if (kSplit) grid_dependency_wait();
@@ -1199,6 +1278,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads(kMode), 1)
           if (p.epi.bias) bias_next = __ldg(p.epi.bias + col);
         }
       }
+      if constexpr (kMode == kModeGlu) {  // the gate's 96 columns, then the other's
+        const int which = epi_tid >= BNH, c = epi_tid - which * BNH;
+        const int64_t col = static_cast<int64_t>(tcol) * BNH + c;
+        if (epi_tid < BN && col < p.out_cols) {
+          if (p.glu.scale[which]) cs_next = __ldg(p.glu.scale[which] + col);
+          if (p.glu.bias[which]) bias_next = __ldg(p.glu.bias[which] + col);
+        }
+      }
       for (int64_t c0 = kb0, c1; c0 < kb1; c0 = c1) {
         c1 = kSplit ? chunk_end(static_cast<int>(c0), static_cast<int>(kb1))
                     : ((kb1 < c0 + kChunkStages) ? kb1 : c0 + kChunkStages);
@@ -1219,7 +1306,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads(kMode), 1)
         if (p.out_kind != kOutI32) {
           // the tile's column scales, once (the barrier above ends the previous
           // tile's reads of them)
-          if constexpr (kMode == kModeAct) {
+          if constexpr (layer_epilogue(kMode)) {
             if (epi_tid < BN) {
               cs_tile[epi_tid] = cs_next;
               bias_tile[epi_tid] = bias_next;
@@ -1232,7 +1319,42 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads(kMode), 1)
           }
           named_bar_sync(kEpiBarrier, kEpiThreads);
         }
-        for (int cb = cb0; cb < cb1; ++cb) {
+        if constexpr (kMode == kModeGlu) {
+          // this warp's 32 rows and 48 of the tile's output columns, 16 at a time: each
+          // output (both pre-activations where they are wanted, then the product) takes the
+          // next of four slots
+          const int row_w = row0 + q * 32;
+          for (int b = 0; b < BNH / 32; ++b) {
+            const int c = half * (BNH / 2) + 16 * b, col0 = tcol * BNH + c;
+            if (col0 >= p.out_cols) break;
+            uint32_t vg[16], vu[16];
+            const uint32_t at = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + kAccCol + ab * BN + c;
+            tmem_ld_32x32b_x16(at, vg);
+            tmem_ld_32x32b_x16(at + BNH, vu);
+            tmem_wait_ld();
+            float zg[16], zu[16];
+            scale_bias16(zg, vg, rs, cs_tile + c, bias_tile + c);
+            scale_bias16(zu, vu, rs, cs_tile + BNH + c, bias_tile + BNH + c);
+            auto emit = [&](const float(&y)[16], const CUtensorMap* map) {
+              uint8_t* slot = ring + (slab & 3) * kGluSlot;
+              if (lane == 0) bulk_wait_group_read<3>();
+              __syncwarp();
+              stage_slot16(slot, lane, y, bf16_out);
+              fence_proxy_async_smem();
+              __syncwarp();
+              if (lane == 0) {
+                if (row_w < p.out_rows) tma_store_2d(map, slot, col0, row_w);
+                bulk_commit_group();
+              }
+              ++slab;
+            };
+            if (p.glu.pre[0]) emit(zg, &more.pre[0]);
+            if (p.glu.pre[1]) emit(zu, &more.pre[1]);
+            glu_row_any(zg, zu, p.glu.act);
+            emit(zg, &map_out);
+          }
+        }
+        for (int cb = cb0; kMode != kModeGlu && cb < cb1; ++cb) {
           const int64_t col0 = static_cast<int64_t>(tcol) * BN + cb * 32;
           if (col0 >= p.out_cols) break;
           uint32_t v[32];
@@ -1309,7 +1431,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads(kMode), 1)
         if (++ab == ACC_BUFS) { ab = 0; aph ^= 1u; }
       }
     }
-    if (kMode == kModeAct ? lane == 0 : p.use_tma_out && epi_tid == 0) bulk_wait_group<0>();
+    if (layer_epilogue(kMode) ? lane == 0 : p.use_tma_out && epi_tid == 0) bulk_wait_group<0>();
   }
 
   tc_fence_before();

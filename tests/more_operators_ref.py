@@ -41,3 +41,59 @@ def layer_norm_bwd(dy, s, mean, rstd, gamma, dsum):
     dx = r * (n - n.mean(1, keepdims=True) - h * (n * h).mean(1, keepdims=True)) + dsum
     mag = r * (np.abs(n) + np.abs(n).mean(1, keepdims=True) + np.abs(h) * np.abs(n * h).mean(1, keepdims=True))
     return dx, (dy * h).sum(0), dy.sum(0), mag + np.abs(dsum), np.abs(dy * h).sum(0), np.abs(dy).sum(0)
+
+
+# ------------------------------------------------- gated feed-forward ------
+
+ACTS = ("none", "relu", "relu2", "silu", "gelu")
+
+
+def _logistic_error(x):
+    """Bound on sigmoid(x) from an exponential of 2 ulp whose argument, a product of at most
+    three roundings, is off by 4 U of itself, one addition and a reciprocal of 1 ulp."""
+    return (4 + 2 + 2 + 4 * 1.45 * np.minimum(np.abs(x), 128.0)) * 2 * U
+
+
+def act(z, kind):
+    """(act(z), act'(z), bounds of a float computation of each, absolute)."""
+    zero = np.zeros_like(z)
+    if kind == "none":
+        return z, zero + 1, zero, zero
+    if kind == "relu":
+        return np.maximum(z, 0), (z > 0) * 1.0, zero, zero
+    if kind == "relu2":
+        p = np.maximum(z, 0)
+        return p * p, 2 * p, 2 * U * p * p, 2 * U * p
+    with np.errstate(over="ignore"):
+        if kind == "silu":
+            x, dx = z, zero + 1
+        else:  # z sigmoid(2 u): (1 + tanh u) / 2 = sigmoid(2 u)
+            c = 2 * np.sqrt(2 / np.pi)
+            x, dx = c * (z + 0.044715 * z ** 3), c * (1 + 3 * 0.044715 * z * z)
+        e = np.exp(-np.abs(x))
+        s = np.where(x >= 0, 1, e) / (1 + e)
+        flat = e / (1 + e) ** 2
+    rel = _logistic_error(x)
+    y, slope = z * s, s + z * flat * dx
+    # the exponential flushes results below 2^-126 to 0: s and flat, each at most the exponential, are
+    # off by as much, y by |z| of it and the slope by (1 + |z dx|) of it
+    flush = 2.0 ** -126
+    return (y, slope, (rel + 4 * U) * np.abs(y) + flush * np.abs(z),
+            (2 * rel + 8 * U) * (s + np.abs(z * flat * dx)) + flush * (1 + np.abs(z * dx)))
+
+
+def glu_z(x, rs, cs, bias):
+    """z in float32, rounding by rounding, from the exact integer product."""
+    z = x.astype(np.float32)
+    if rs is not None:
+        z = z * rs[:, None]
+    if cs is not None:
+        z = z * cs
+    return z + bias if bias is not None else z
+
+
+def glu_bwd(dy, gate, up, kind):
+    """(dgate, dup, their bounds before the rounding)."""
+    y, slope, ey, es = act(gate, kind)
+    dgate, dup = dy * up * slope, dy * y
+    return dgate, dup, np.abs(dy * up) * es + 4 * U * np.abs(dgate), np.abs(dy) * ey + 4 * U * np.abs(dup)

@@ -43,3 +43,39 @@ def test_layer_norm_bwd_refusals(lib):
         assert _norm_bwd(lib, **kw) == t3.T3_EINVAL, kw
     assert _norm_bwd(lib, cols=0, lddx=0, dy=None, s=None, mean=None, rstd=None, dx=None) == t3.T3_OK
     assert _norm_bwd(lib, rows=0, dy=None, s=None, mean=None, rstd=None, dx=None) == t3.T3_OK
+
+
+def _glu(lib, a=FAKE, g=FAKE, u=FAKE, c=FAKE, m=4, n=8, k=8, act=0, pg=None, pu=None, kind=F32, ws=None, room=0):
+    return lib.t3_gemm_fwd_glu(a, g, u, c, m, n, k, None, None, None, None, None, act, pg, pu, kind, ws, room, None)
+
+
+def test_glu_refusals(lib):
+    bad = [dict(m=-1), dict(n=-1), dict(k=-1), dict(m=BIG), dict(n=BIG), dict(act=5), dict(act=-1), dict(kind=2),
+           dict(kind=3), dict(a=None), dict(g=None), dict(u=None), dict(c=None), dict(pg=FAKE), dict(pu=FAKE),
+           dict(room=-1), dict(ws=FAKE, room=1)]
+    for kw in bad:
+        assert _glu(lib, **kw) == t3.T3_EINVAL, kw
+    other = ctypes.c_void_p(8192)
+    assert _glu(lib, pg=other, pu=other) == t3.T3_EINVAL
+    assert _glu(lib, pg=other, ws=other, room=64) == t3.T3_EINVAL
+    assert _glu(lib, m=1, k=16777216) == t3.T3_EOVERFLOW
+    assert _glu(lib, m=0, a=None, g=None, u=None, c=None) == t3.T3_OK
+    assert _glu(lib, n=0, a=None, g=None, u=None, c=None) == t3.T3_OK
+    f = lib.t3_gemm_fwd_glu_workspace
+    assert f(FAKE, FAKE, FAKE, FAKE, 0, 8, 8, None, None, F32) == 0
+    assert f(FAKE, FAKE, FAKE, FAKE, -1, 8, 8, None, None, F32) == 0
+    assert f(FAKE, FAKE, FAKE, FAKE, 8, 8, 8, None, None, 2) == 0
+
+
+def _glu_bwd(lib, dy=FAKE, gate=FAKE, up=FAKE, act=0, dg=FAKE, du=None, gb=None, ub=None, rows=4, cols=8, dt=BF16, ws=None):
+    return lib.t3_glu_bwd(dy, gate, up, act, dg, du, gb, ub, rows, cols, dt, ws, None)
+
+
+def test_glu_bwd_refusals(lib):
+    bad = [dict(rows=-1), dict(cols=-1), dict(rows=BIG), dict(cols=BIG), dict(act=5), dict(dt=2), dict(dy=None),
+           dict(gate=None), dict(up=None), dict(du=FAKE), dict(gb=FAKE), dict(ub=FAKE), dict(gb=FAKE, ub=FAKE, ws=FAKE)]
+    for kw in bad:
+        assert _glu_bwd(lib, **kw) == t3.T3_EINVAL, kw
+    assert _glu_bwd(lib, dg=None) == t3.T3_OK
+    assert _glu_bwd(lib, cols=0, dy=None, gate=None, up=None) == t3.T3_OK
+    assert _glu_bwd(lib, rows=0, dy=None, gate=None, up=None) == t3.T3_OK
