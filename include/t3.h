@@ -414,6 +414,57 @@ int t3_gated_scan_bwd(const void* gate, int64_t ldg, const void* cand, int64_t l
                       void* dcand, int64_t lddc, float* dh0, int64_t batch, int64_t length,
                       int64_t width, int dtype, t3_stream_t stream);
 
+/*
+ * t3_linear_attn_fwd -- linear attention with a decay for each head, over `batch` sequences of
+ * `length` tokens and `heads` heads; a head's state S is a float matrix [dk][dv]:
+ *   S_t = exp(log_decay[h]) * S'_{t-1} + k_t v_t^T,   o_t = scale * S_t^T q_t,
+ *   S'_{t-1} = S_{t-1}, or 0 where resets[b][t] is not 0 (a document starts);
+ *   S_{-1} = state (NULL: zeros).
+ * q, k: token t of sequence b is row b * length + t of a matrix with the given stride, head h
+ * its columns from h * dk on; v and o the same with dv.  dk and dv are 128 at most.  log_decay
+ * float [heads], a constant of the model (no gradient is taken of it): 0 forgets nothing, -inf everything;
+ * above 0 states grow.  state, state_last float [batch][heads][dk][dv]; resets uint8 [batch][length] or
+ * NULL.  state_last (may be NULL, may be state's buffer) receives the state after the last
+ * token, so single tokens (length = 1) advance a state in place; length = 0 copies it.
+ * workspace: DEVICE floats, t3_linear_attn_workspace of them (not zeroed), with which few long
+ * sequences fill the GPU; NULL takes every sequence and head as a whole.
+ * bf16 rows of more than 16 tokens whose bases, strides and heads are whole 16-byte pieces run on the tensor cores,
+ * 128 tokens at a time: products inside such a chunk and the state it begins with are rounded to bf16 where they meet
+ * q and v (o is off by about a rounding more than its own), what is added to the state is not (2^-17 of each
+ * term).  A value of q, k or v that is not finite spoils its chunk in its head, tokens in front of it included.
+ * Everything else is float, token by token.
+ * T3_EINVAL: negative sizes or strides, sizes above 2^31 - 1 or heads above 128 elements, batch * heads above
+ * 2^31 - 1, ldo < heads * dv, a null q, k, v, o or log_decay with a non-empty shape, an unknown dtype.
+ */
+int t3_linear_attn_fwd(const void* q, int64_t ldq, const void* k, int64_t ldk, const void* v,
+                       int64_t ldv, const float* log_decay, const float* state,
+                       const uint8_t* resets, float scale, void* o, int64_t ldo, float* state_last,
+                       int64_t batch, int64_t length, int64_t heads, int64_t dk, int64_t dv,
+                       int dtype, float* workspace, t3_stream_t stream);
+
+/*
+ * t3_linear_attn_bwd -- the gradient of t3_linear_attn_fwd.  dout is the gradient of o,
+ * dstate_last (may be NULL) that of state_last:
+ *   G_t = scale * q_t dout_t^T + exp(log_decay[h]) * G_{t+1} (without the second term where
+ *         t + 1 resets; dstate_last joins at the last token),
+ *   dq_t = scale * S_t dout_t,   dk_t = G_t v_t,   dv_t = G_t^T k_t,
+ *   dstate = exp(log_decay[h]) * G_0 (0 where token 0 resets; may be NULL, may be dstate_last's buffer).
+ * The S_t are taken again from state, k and v: nothing of the forward is kept.  dq, dk and dv are
+ * laid out like q, k and v, with strides of their own, and overlap none of the inputs.  Each is a pass of the
+ * forward's kernels over other operands, with the forward's roundings and workspace.
+ */
+int t3_linear_attn_bwd(const void* q, int64_t ldq, const void* k, int64_t ldk, const void* v,
+                       int64_t ldv, const void* dout, int64_t lddo, const float* log_decay,
+                       const float* state, const uint8_t* resets, float scale,
+                       const float* dstate_last, void* dq, int64_t lddq, void* dk_out, int64_t lddk,
+                       void* dv_out, int64_t lddv, float* dstate, int64_t batch, int64_t length,
+                       int64_t heads, int64_t dk, int64_t dv, int dtype, float* workspace,
+                       t3_stream_t stream);
+
+/* Floats of workspace those two take (0 for short sequences and for empty or invalid sizes); the
+ * same on every device. */
+int64_t t3_linear_attn_workspace(int64_t batch, int64_t length, int64_t heads, int64_t dk, int64_t dv);
+
 /* Activations: T3_ACT_RELU2 is max(z, 0)^2, T3_ACT_SILU z sigmoid(z), T3_ACT_GELU
  * the tanh form z (1 + tanh(sqrt(2/pi) (z + 0.044715 z^3))) / 2. */
 enum { T3_ACT_NONE = 0, T3_ACT_RELU = 1, T3_ACT_RELU2 = 2, T3_ACT_SILU = 3, T3_ACT_GELU = 4 };

@@ -22,6 +22,8 @@ Function names follow the C ABI:
   t3_layernorm_bwd(dy, s, mean, rstd)      its gradient
   t3_gated_scan_fwd(gate, cand, h0)        the gated linear recurrence (sequences, tokens)
   t3_gated_scan_bwd(gate, cand, h, dh)     its gradient
+  t3_linear_attn_fwd(q, k, v, log_decay)   linear attention with a decay for each head
+  t3_linear_attn_bwd(q, k, v, log_decay, do)   its gradient
   t3_gemm_fwd_act(A, Wp, bias=, act=)      the forward with bias, activation, residual
   t3_act_bwd(dy, z, act)                   that epilogue's gradient
   t3_gemm_fwd_glu(A, Wg, Wu, act=)         two forwards, an activation and their product
@@ -109,6 +111,10 @@ def load():
                 ("t3_gated_scan_fwd", [p, i64, p, i64, p, p, p, i64, p, i64, i64, i64, i32, p]),
                 ("t3_gated_scan_bwd", [p, i64, p, i64, p, i64, p, i64, p, p, p, p, i64, p, i64, p,
                                        i64, i64, i64, i32, p]),
+                ("t3_linear_attn_fwd", [p, i64, p, i64, p, i64, p, p, p, ctypes.c_float, p, i64, p, i64, i64, i64, i64, i64,
+                                        i32, p, p]),
+                ("t3_linear_attn_bwd", [p, i64, p, i64, p, i64, p, i64, p, p, p, ctypes.c_float, p, p, i64, p, i64, p, i64, p,
+                                        i64, i64, i64, i64, i64, i32, p, p]),
                 ("t3_gemm_fwd_act", [p, p, p, i64, i64, i64, p, p, p, i32, p, p, i32, p, p, i64, p]),
                 ("t3_act_bwd", [p, p, i32, p, p, i64, i64, i32, p, p]),
                 ("t3_gemm_fwd_glu", [p, p, p, p, i64, i64, i64, p, p, p, p, p, i32, p, p, i32, p, i64, p]),
@@ -123,6 +129,8 @@ def load():
         lib.t3_gemm_fwd_act_workspace.restype = i64
         lib.t3_gemm_fwd_glu_workspace.argtypes = [p, p, p, p, i64, i64, i64, p, p, i32]
         lib.t3_gemm_fwd_glu_workspace.restype = i64
+        lib.t3_linear_attn_workspace.argtypes = [i64, i64, i64, i64, i64]
+        lib.t3_linear_attn_workspace.restype = i64
         lib.t3_colsum_workspace.argtypes = [i64, i64]
         lib.t3_colsum_workspace.restype = i64
         lib.t3_version.argtypes = []
@@ -756,6 +764,113 @@ def t3_gated_scan_bwd(gate, cand, h, dh, h0=None, resets=None, dh_last=None, dga
             _dense(dh_last, f32, dev, (batch, width), "dh_last"), pdg, lddg, pdc, lddc,
             _dense(dh0, f32, dev, (batch, width), "dh0"), batch, length, width, dtype)
     return dgate, dcand, dh0
+
+
+def _heads(t, dtype, dev, shape, name, out=False):
+    """(address, stride from token to token) of a tensor [batch][length][heads][d] on
+    device number `dev` whose tokens are evenly spaced and whose heads are adjacent."""
+    if t.dtype is not dtype or t.get_device() != dev:
+        raise TypeError(f"{name} must be a {dtype} tensor on device {dev}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+    batch, length, heads, d = shape
+    st = t.stride()
+    if not t.numel():
+        return t.data_ptr(), heads * d
+    if (d > 1 and st[3] != 1) or (heads > 1 and st[2] != d):
+        raise ValueError(f"{name}: the heads of a token must be adjacent")
+    ld = st[1] if length > 1 else st[0] if batch > 1 else heads * d
+    if batch > 1 and length > 1 and st[0] != length * ld:
+        raise ValueError(f"{name}: sequences must be evenly spaced (stride {st[0]}, not {length * ld})")
+    if out and ld < heads * d:
+        raise ValueError(f"{name}: output rows must not overlap")
+    return t.data_ptr(), ld
+
+
+def _linear_workspace(workspace, shape, dk, dev, stream):
+    """Floats that linear attention over v's shape takes to fill the GPU with few sequences."""
+    batch, length, heads, dv = shape
+    if workspace is not None:
+        n = load().t3_linear_attn_workspace(batch, length, heads, dk, dv)
+        if workspace.dtype is not _torch().float32 or workspace.get_device() != dev or not workspace.is_contiguous():
+            raise TypeError(f"workspace must be a contiguous float32 tensor on device {dev}")
+        if workspace.numel() < n:
+            raise ValueError(f"workspace needs {n} floats, has {workspace.numel()}")
+        return workspace.data_ptr(), workspace
+    if length <= 32:
+        return None, None
+    n = load().t3_linear_attn_workspace(batch, length, heads, dk, dv)
+    if not n:
+        return None, None
+    workspace = _empty(n, _torch().float32, dev, stream)
+    return workspace.data_ptr(), workspace
+
+
+def _linear_shapes(q, v):
+    if len(q.shape) != 4 or len(v.shape) != 4 or q.shape[:3] != v.shape[:3]:
+        raise TypeError("q and k must be [batch][length][heads][dk], v [batch][length][heads][dv]")
+    return q.shape, v.shape
+
+
+def t3_linear_attn_fwd(q, k, v, log_decay, state=None, resets=None, scale=1.0, o=None, state_last=None,
+                       workspace=None, stream=None):
+    """(o, state_last): S_t = exp(log_decay) S_(t-1) + k_t v_t^T, o_t = scale S_t^T q_t for every
+    sequence and head of q, k [batch][length][heads][dk] and v [batch][length][heads][dv], from the float
+    state [batch][heads][dk][dv] (None: zeros); log_decay float32 [heads]; resets uint8 or
+    bool [batch][length] marks tokens that start from zero.  q, k and v may be slices of one wider
+    tensor.  state_last may be state: the state advances in place."""
+    torch = _torch()
+    dtype = _dtype_of(q, "q")
+    qs, vs = _linear_shapes(q, v)
+    xt, dev, f32 = q.dtype, q.get_device(), torch.float32
+    batch, length, heads, dv = vs
+    ss = (batch, heads, qs[3], dv)
+    if o is None:
+        o = _empty(vs, xt, dev, stream)
+    if state_last is None:
+        state_last = _empty(ss, f32, dev, stream)
+    pq, ldq = _heads(q, xt, dev, qs, "q")
+    pk, ldk = _heads(k, xt, dev, qs, "k")
+    pv, ldv = _heads(v, xt, dev, vs, "v")
+    po, ldo = _heads(o, xt, dev, vs, "o", out=True)
+    pw, workspace = _linear_workspace(workspace, vs, qs[3], dev, stream)
+    _launch("t3_linear_attn_fwd", dev, stream, pq, ldq, pk, ldk, pv, ldv, _dense(log_decay, f32, dev, (heads,), "log_decay"),
+            _dense(state, f32, dev, ss, "state"), _marks(resets, dev, (batch, length)), scale, po, ldo,
+            _dense(state_last, f32, dev, ss, "state_last"), batch, length, heads, qs[3], dv, dtype, pw)
+    return o, state_last
+
+
+def t3_linear_attn_bwd(q, k, v, log_decay, do, state=None, resets=None, scale=1.0, dstate_last=None, dq=None, dk=None,
+                       dv=None, dstate=None, workspace=None, stream=None):
+    """(dq, dk, dv, dstate): the gradient of t3_linear_attn_fwd for do, the gradient of o, and
+    dstate_last (float32 [batch][heads][dk][dv] or None), that of state_last."""
+    torch = _torch()
+    dtype = _dtype_of(q, "q")
+    qs, vs = _linear_shapes(q, v)
+    xt, dev, f32 = q.dtype, q.get_device(), torch.float32
+    batch, length, heads, d = vs
+    ss = (batch, heads, qs[3], d)
+    if dq is None:
+        dq = _empty(qs, xt, dev, stream)
+    if dk is None:
+        dk = _empty(qs, xt, dev, stream)
+    if dv is None:
+        dv = _empty(vs, xt, dev, stream)
+    if dstate is None:
+        dstate = _empty(ss, f32, dev, stream)
+    pq, ldq = _heads(q, xt, dev, qs, "q")
+    pk, ldk = _heads(k, xt, dev, qs, "k")
+    pv, ldv = _heads(v, xt, dev, vs, "v")
+    pd, lddo = _heads(do, xt, dev, vs, "do")
+    gq, lddq = _heads(dq, xt, dev, qs, "dq", out=True)
+    gk, lddk = _heads(dk, xt, dev, qs, "dk", out=True)
+    gv, lddv = _heads(dv, xt, dev, vs, "dv", out=True)
+    pw, workspace = _linear_workspace(workspace, vs, qs[3], dev, stream)
+    _launch("t3_linear_attn_bwd", dev, stream, pq, ldq, pk, ldk, pv, ldv, pd, lddo,
+            _dense(log_decay, f32, dev, (heads,), "log_decay"), _dense(state, f32, dev, ss, "state"),
+            _marks(resets, dev, (batch, length)), scale, _dense(dstate_last, f32, dev, ss, "dstate_last"), gq, lddq, gk, lddk,
+            gv, lddv, _dense(dstate, f32, dev, ss, "dstate"), batch, length, heads, qs[3], d, dtype, pw)
+    return dq, dk, dv, dstate
 
 
 def t3_gemm_fwd_act(A, Wp, K=None, row_scale=None, col_scale=None, bias=None, act=T3_ACT_NONE,

@@ -9,6 +9,7 @@
 
 #include "t3.h"
 #include "t3_internal.h"
+#include "t3_linear.cuh"
 
 namespace t3 {
 
@@ -557,6 +558,19 @@ bool valid_act(int act) { return act >= T3_ACT_NONE && act <= T3_ACT_GELU; }
 // Row strides so large that a row's offset in bytes could pass 63 bits.
 bool bad_ld(int64_t ld) { return ld < 0 || ld > kMaxDim; }
 
+// Sizes of linear attention: heads of 1 to kMaxHead elements, tokens of all heads countable.
+bool bad_linear(int64_t batch, int64_t length, int64_t heads, int64_t dk, int64_t dv, int dtype) {
+  return bad_dims(batch, length, heads) || !valid_dtype(dtype) || dk < 1 || dv < 1 || dk > lin::kMaxHead ||
+         dv > lin::kMaxHead || static_cast<__int128>(batch) * heads > kMaxDim ||
+         static_cast<__int128>(batch) * heads * length > static_cast<__int128>(1) << 50;
+}
+
+// One pass of the recurrence on the kernels that take it.
+int linear_pass(const lin::Args& p, bool reverse, int dtype, float* workspace, const DeviceInfo* dev, cudaStream_t s) {
+  if (linear_tc_fits(p, dtype)) return launch_linear_tc(p, reverse, workspace, dev->sms, dev->err_word, s);
+  return launch_linear_tokens(p, reverse, dtype, workspace, dev->sms, s);
+}
+
 // Empty reduction: the output is all zeros.
 int zero_fill(int32_t* out, int64_t rows, int64_t cols, cudaStream_t s) {
   if (!out) return T3_EINVAL;
@@ -1000,6 +1014,90 @@ int t3_glu_bwd(const void* dy, const void* gate, const void* up, int act, void* 
   if (st != T3_OK) return st;
   return launch_glu_bwd(dy, gate, up, act, dgate, dup, dgate_bias, dup_bias, rows, cols, dtype, workspace, dev->sms,
                         stream);
+}
+
+int64_t t3_linear_attn_workspace(int64_t batch, int64_t length, int64_t heads, int64_t dk, int64_t dv) {
+  return bad_linear(batch, length, heads, dk, dv, T3_OUT_BF16) ? 0 : linear_workspace(batch * heads, length, dk, dv);
+}
+
+int t3_linear_attn_fwd(const void* q, int64_t ldq, const void* k, int64_t ldk, const void* v, int64_t ldv,
+                       const float* log_decay, const float* state, const uint8_t* resets, float scale, void* o,
+                       int64_t ldo, float* state_last, int64_t batch, int64_t length, int64_t heads, int64_t dk,
+                       int64_t dv, int dtype, float* workspace, t3_stream_t stream) {
+  if (bad_linear(batch, length, heads, dk, dv, dtype) || bad_ld(ldq) || bad_ld(ldk) || bad_ld(ldv) || bad_ld(ldo) ||
+      ldo < heads * dv)
+    return T3_EINVAL;
+  if (batch == 0 || heads == 0) return T3_OK;
+  const int64_t state_bytes = batch * heads * dk * dv * static_cast<int64_t>(sizeof(float));
+  if (length > 0 && (!q || !k || !v || !o || !log_decay)) return T3_EINVAL;
+  const DeviceInfo* dev = nullptr;
+  const int st = device_info(&dev);
+  if (st != T3_OK) return st;
+  if (length == 0) {  // the state stays
+    if (!state_last || state_last == state) return T3_OK;
+    const cudaError_t e = state ? cudaMemcpyAsync(state_last, state, state_bytes, cudaMemcpyDeviceToDevice, stream)
+                                : cudaMemsetAsync(state_last, 0, state_bytes, stream);
+    return e == cudaSuccess ? T3_OK : T3_ECUDA;
+  }
+  lin::Args p{};
+  p.q = q, p.k = k, p.v = v, p.o = o;
+  p.ldq = ldq, p.ldk = ldk, p.ldv = ldv, p.ldo = ldo;
+  p.log_decay = log_decay;
+  p.init = state;
+  p.resets = resets;
+  p.in_scale = 1.0f, p.out_scale = scale;
+  p.last = state_last;
+  p.length = length, p.heads = heads, p.pairs = batch * heads;
+  p.dk = static_cast<int>(dk), p.dv = static_cast<int>(dv);
+  return linear_pass(p, false, dtype, workspace, dev, stream);
+}
+
+int t3_linear_attn_bwd(const void* q, int64_t ldq, const void* k, int64_t ldk, const void* v, int64_t ldv,
+                       const void* dout, int64_t lddo, const float* log_decay, const float* state,
+                       const uint8_t* resets, float scale, const float* dstate_last, void* dq, int64_t lddq, void* dk_out,
+                       int64_t lddk, void* dv_out, int64_t lddv, float* dstate, int64_t batch, int64_t length,
+                       int64_t heads, int64_t dk, int64_t dv, int dtype, float* workspace, t3_stream_t stream) {
+  if (bad_linear(batch, length, heads, dk, dv, dtype) || bad_ld(ldq) || bad_ld(ldk) || bad_ld(ldv) || bad_ld(lddo) ||
+      bad_ld(lddq) || bad_ld(lddk) || bad_ld(lddv) || lddq < heads * dk || lddk < heads * dk || lddv < heads * dv)
+    return T3_EINVAL;
+  if (batch == 0 || heads == 0) return T3_OK;
+  if (length > 0 && (!q || !k || !v || !dout || !log_decay || !dq || !dk_out || !dv_out)) return T3_EINVAL;
+  const DeviceInfo* dev = nullptr;
+  int st = device_info(&dev);
+  if (st != T3_OK) return st;
+  const int64_t state_bytes = batch * heads * dk * dv * static_cast<int64_t>(sizeof(float));
+  if (length == 0) {
+    if (!dstate || dstate == dstate_last) return T3_OK;
+    const cudaError_t e = dstate_last ? cudaMemcpyAsync(dstate, dstate_last, state_bytes, cudaMemcpyDeviceToDevice, stream)
+                                      : cudaMemsetAsync(dstate, 0, state_bytes, stream);
+    return e == cudaSuccess ? T3_OK : T3_ECUDA;
+  }
+  lin::Args p{};
+  p.log_decay = log_decay;
+  p.resets = resets;
+  p.length = length, p.heads = heads, p.pairs = batch * heads;
+  lin::Args a = p;  // dq: in time, from the state transposed
+  a.q = dout, a.k = v, a.v = k, a.o = dq;
+  a.ldq = lddo, a.ldk = ldv, a.ldv = ldk, a.ldo = lddq;
+  a.init = state, a.init_transposed = 1;
+  a.in_scale = 1.0f, a.out_scale = scale;
+  a.dk = static_cast<int>(dv), a.dv = static_cast<int>(dk);
+  st = linear_pass(a, false, dtype, workspace, dev, stream);
+  if (st != T3_OK) return st;
+  a.q = v, a.k = dout, a.v = q, a.o = dk_out;  // dk: against time, from dstate_last transposed
+  a.ldq = ldv, a.ldk = lddo, a.ldv = ldq, a.ldo = lddk;
+  a.init = dstate_last;
+  a.in_scale = scale, a.out_scale = 1.0f;
+  st = linear_pass(a, true, dtype, workspace, dev, stream);
+  if (st != T3_OK) return st;
+  // dv, and dstate, which may lie over dstate_last: the last to read it
+  p.q = k, p.k = q, p.v = dout, p.o = dv_out;
+  p.ldq = ldk, p.ldk = ldq, p.ldv = lddo, p.ldo = lddv;
+  p.init = dstate_last;
+  p.in_scale = scale, p.out_scale = 1.0f;
+  p.last = dstate;
+  p.dk = static_cast<int>(dk), p.dv = static_cast<int>(dv);
+  return linear_pass(p, true, dtype, workspace, dev, stream);
 }
 
 int64_t t3_set_small_product_limit(int64_t macs) {

@@ -1,0 +1,251 @@
+// t3_linear.cu -- linear attention with a decay for each head, token by token: single
+// tokens, float rows, short sequences, heads and strides of any size.
+//
+// What it computes: the recurrence of t3_linear.cuh.
+//
+// What bounds it: a single token reads and writes its state, dk dv floats each way: memory. Longer
+// sequences, three packed instructions for two elements of the state a token.  A CTA holds
+// 32 columns of a state in registers, 16 rows of a column a thread, so that S stays where it is from
+// token to token; a block of tokens' rows is staged in shared memory as floats, where a warp reads
+// q and k as broadcasts, and o is summed over the rows by the warps, each leaving its part in
+// shared memory until the block ends.
+#include "t3_linear.cuh"
+
+namespace t3 {
+namespace lin {
+
+constexpr int kCols = 32;   // columns of a state a CTA holds, one a lane
+constexpr int kRows = 16;   // rows of it a warp
+constexpr int kTokens = 32; // tokens of a block
+
+__device__ __forceinline__ float load1(const float* p) { return *p; }
+__device__ __forceinline__ float load1(const bf16* p) { return __bfloat162float(*p); }
+__device__ __forceinline__ void store1(float* p, float x) { *p = x; }
+__device__ __forceinline__ void store1(bf16* p, float x) { *p = __float2bfloat16_rn(x); }
+
+constexpr int padded(int d) { return (d + kRows - 1) / kRows * kRows; }
+constexpr int smem_floats(int tokens, int dk) {
+  return tokens * (2 * padded(dk) + kCols + 1) + padded(dk) / kRows * tokens * kCols;
+}
+
+// kStates: only what each part's last piece adds to the state (Args::local).
+template <class T, bool kReverse, bool kStates>
+__global__ void __launch_bounds__(kMaxHead / kRows * 32) linear_tokens_kernel(const Args p, int col_blocks) {
+  extern __shared__ __align__(16) float sm[];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5, threads = blockDim.x;
+  const int part = blockIdx.x / col_blocks, col = (blockIdx.x - part * col_blocks) * kCols + lane;
+  const int rows = warps * kRows;
+  const int tokens = p.length < kTokens ? static_cast<int>(p.length) : kTokens;
+  float* qs = sm;                         // [tokens][rows]
+  float* ks = qs + tokens * rows;         // [tokens][rows]
+  float* vs = ks + tokens * rows;         // [tokens][kCols]
+  float* os = vs + tokens * kCols;        // [warps][tokens][kCols]
+  float* cs = os + warps * tokens * kCols;  // [tokens]
+  launch_dependents();
+  grid_dependency_wait();
+  int64_t at = part_begin(p, part), end = part_begin(p, part + 1);
+  if (kStates) {
+    int64_t pair, b0, b1;
+    if (!cut_piece(p, part, pair, b0, b1)) return;
+    at = pair * p.blocks + b0;
+  }
+  const bool has_col = col < p.dv;
+  float2 S[kRows / 2];
+  bool fresh = true;  // the state is still to be loaded
+  float passed = 1.0f;
+  for (; at < end; ++at) {
+    const int64_t pair = at / p.blocks, head = pair % p.heads, batch = pair / p.heads;
+    const int64_t block = at - pair * p.blocks, tb = kReverse ? p.blocks - 1 - block : block;
+    const int64_t t0 = tb * kTokens;
+    const int n = static_cast<int>(p.length - t0 < kTokens ? p.length - t0 : kTokens);
+    const float decay = exp2f(p.log_decay[head] * kLog2e);
+    const int64_t state_at = pair * p.dk * p.dv;
+    if (fresh || block == 0) {
+      fresh = false;
+      const bool inside = block > 0 && !kStates;  // behind a cut
+      const float* from = inside ? p.local + static_cast<int64_t>(part) * p.dk * p.dv : p.init ? p.init + state_at : nullptr;
+      const bool transposed = !inside && p.init_transposed;
+      const bool there = from && has_col && !kStates;
+#pragma unroll
+      for (int i = 0; i < kRows; ++i) {
+        const int r = warp * kRows + i;
+        const float x = there && r < p.dk ? from[transposed ? col * p.dk + r : r * p.dv + col] : 0.0f;
+        if (i & 1)
+          S[i / 2].y = x;
+        else
+          S[i / 2].x = x;
+      }
+    }
+    // the block's rows, in the order they are taken
+    const int64_t row0 = batch * p.length + t0;
+    for (int i = threadIdx.x; i < n * rows; i += threads) {
+      const int j = i / rows, r = i - j * rows;
+      const int64_t row = row0 + (kReverse ? n - 1 - j : j);
+      const bool in = r < p.dk;
+      ks[i] = in ? p.in_scale * load1(static_cast<const T*>(p.k) + row * p.ldk + head * p.dk + r) : 0.0f;
+      if (!kStates) qs[i] = in ? load1(static_cast<const T*>(p.q) + row * p.ldq + head * p.dk + r) : 0.0f;
+    }
+    for (int i = threadIdx.x; i < n * kCols; i += threads) {
+      const int j = i / kCols, c = col - lane + i % kCols;
+      const int64_t row = row0 + (kReverse ? n - 1 - j : j);
+      vs[i] = c < p.dv ? load1(static_cast<const T*>(p.v) + row * p.ldv + head * p.dv + c) : 0.0f;
+    }
+    for (int j = threadIdx.x; j < n; j += threads) {
+      const int64_t t = t0 + (kReverse ? n - 1 - j : j);
+      // what cuts a token off from the one taken before it: in time its own mark, against time
+      // that of the token taken before it, which is the next one
+      const int64_t mark = kReverse ? t + 1 : t;
+      const bool cut = p.resets && mark < p.length && p.resets[batch * p.length + mark] != 0;
+      cs[j] = cut ? 0.0f : kReverse && t + 1 == p.length ? 1.0f : decay;
+    }
+    __syncthreads();
+    for (int j = 0; j < n; ++j) {
+      const float c = cs[j], v = vs[j * kCols + lane];
+      if (kStates) passed *= c;
+      const float2 c2 = make_float2(c, c), v2 = make_float2(v, v);
+      const float4* kp = reinterpret_cast<const float4*>(ks + j * rows + warp * kRows);
+      const float4* qp = reinterpret_cast<const float4*>(qs + j * rows + warp * kRows);
+      if (c == 0.0f) {  // whatever the state held
+#pragma unroll
+        for (int i = 0; i < kRows / 2; ++i) S[i] = make_float2(0.0f, 0.0f);
+      }
+      float2 sum = make_float2(0.0f, 0.0f), sum2 = sum;
+#pragma unroll
+      for (int i = 0; i < kRows / 4; ++i) {
+        const float4 k4 = kp[i];
+        S[2 * i] = __ffma2_rn(make_float2(k4.x, k4.y), v2, __fmul2_rn(S[2 * i], c2));
+        S[2 * i + 1] = __ffma2_rn(make_float2(k4.z, k4.w), v2, __fmul2_rn(S[2 * i + 1], c2));
+        if (!kStates) {
+          const float4 q4 = qp[i];
+          sum = __ffma2_rn(make_float2(q4.x, q4.y), S[2 * i], sum);
+          sum2 = __ffma2_rn(make_float2(q4.z, q4.w), S[2 * i + 1], sum2);
+        }
+      }
+      if (!kStates) os[(warp * tokens + j) * kCols + lane] = (sum.x + sum.y) + (sum2.x + sum2.y);
+    }
+    __syncthreads();
+    if (!kStates)
+      for (int i = threadIdx.x; i < n * kCols; i += threads) {
+        const int j = i / kCols, c = col - lane + i % kCols;
+        if (c >= p.dv) continue;
+        float x = 0.0f;
+        for (int w = 0; w < warps; ++w) x += os[w * tokens * kCols + i];
+        const int64_t row = row0 + (kReverse ? n - 1 - j : j);
+        store1(static_cast<T*>(p.o) + row * p.ldo + head * p.dv + c, p.out_scale * x);
+      }
+    const bool behind = !kStates && block + 1 == p.blocks && p.last;  // the sequence ends
+    if ((behind || (kStates && at + 1 == end)) && has_col) {
+      float* to = kStates ? p.local + static_cast<int64_t>(part + 1) * p.dk * p.dv : p.last + state_at;
+      // against time what is left is the gradient of the state in front of the first token
+      const bool cut = kReverse && behind && p.resets && p.resets[batch * p.length] != 0;
+      const float f = kReverse && behind ? decay : 1.0f;
+#pragma unroll
+      for (int i = 0; i < kRows; ++i) {
+        const int r = warp * kRows + i;
+        const float x = i & 1 ? S[i / 2].y : S[i / 2].x;
+        if (r < p.dk) to[r * p.dv + col] = cut || f == 0.0f ? 0.0f : f * x;
+      }
+    }
+  }
+  if (kStates && threadIdx.x == 0 && col == 0) p.pass[part + 1] = passed;
+}
+
+// The states in front of the ranges that begin inside a sequence: what the piece before adds, plus what is left
+// of the state in front of that.  A CTA takes 1024 elements of the states of one sequence and head.
+__global__ void __launch_bounds__(256) linear_join_kernel(const Args p, int element_blocks) {
+  const int64_t pair = blockIdx.x / element_blocks;
+  const int e0 = static_cast<int>(blockIdx.x - pair * element_blocks) * 1024 + threadIdx.x, size = p.dk * p.dv;
+  launch_dependents();
+  grid_dependency_wait();
+  const int64_t total = p.pairs * p.blocks, first = pair * p.blocks;
+  // the first range that begins behind the sequence's first block
+  int64_t j = (first * p.parts + total - 1) / total;
+  while (part_begin(p, j) <= first) ++j;
+  if (j >= p.parts || part_begin(p, j) >= first + p.blocks) return;
+  float x[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int e = e0 + 256 * i, r = e / p.dv, c = e - r * p.dv;
+    x[i] = p.init && e < size ? p.init[pair * size + (p.init_transposed ? c * p.dk + r : e)] : 0.0f;
+  }
+  for (; j < p.parts && part_begin(p, j) < first + p.blocks; ++j) {
+    const float pass = p.pass[j];
+    float* at = p.local + j * size;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int e = e0 + 256 * i;
+      if (e < size) {
+        x[i] = pass == 0.0f ? at[e] : fmaf(pass, x[i], at[e]);
+        at[e] = x[i];
+      }
+    }
+  }
+}
+
+int cut(Args* p, int64_t parts, float* workspace, cudaStream_t s) {
+  const int64_t total = p->pairs * p->blocks;
+  auto set = [&](int64_t n) {
+    p->parts = static_cast<int>(n);
+    p->each = total / n;
+    p->rest = total % n;
+    return T3_OK;
+  };
+  const bool in_place = p->init && p->last == p->init;
+  p->local = p->pass = nullptr;
+  parts = std::min(parts, total);
+  if (p->pairs % parts == 0) return set(parts);  // they end with sequences
+  if (!workspace || parts > kMaxLinearParts || (in_place && p->pairs >= kMaxLinearParts)) return set(p->pairs);
+  const int64_t size = static_cast<int64_t>(p->dk) * p->dv;
+  p->local = workspace;
+  p->pass = workspace + kMaxLinearParts * size;
+  if (in_place) {  // one range may end a sequence before another has begun it
+    float* copy = workspace + kMaxLinearParts * (size + 1);
+    if (cudaMemcpyAsync(copy, p->init, p->pairs * size * sizeof(float), cudaMemcpyDeviceToDevice, s) != cudaSuccess)
+      return T3_ECUDA;
+    p->init = copy;
+  }
+  return set(parts);
+}
+
+int launch_join(const Args& p, cudaStream_t s) {
+  const int blocks = (p.dk * p.dv + 1023) / 1024;
+  return launch(linear_join_kernel, p.pairs * blocks, 256, 0, s, 1, p, blocks);
+}
+
+template <class T, bool kReverse>
+int run(const Args& p, cudaStream_t s) {
+  const int col_blocks = (p.dv + kCols - 1) / kCols, threads = padded(p.dk) / kRows * 32;
+  const int tokens = p.length < kTokens ? static_cast<int>(p.length) : kTokens;
+  const size_t smem = smem_floats(tokens, p.dk) * sizeof(float);
+  int dev = 0, st;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return T3_EDEVICE;
+  constexpr int kMost = smem_floats(kTokens, kMaxHead) * 4;
+  if ((st = allow_smem<linear_tokens_kernel<T, kReverse, false>>(dev, kMost)) != T3_OK) return st;
+  if (p.local) {
+    if ((st = allow_smem<linear_tokens_kernel<T, kReverse, true>>(dev, kMost)) != T3_OK) return st;
+    st = launch(linear_tokens_kernel<T, kReverse, true>, static_cast<int64_t>(p.parts) * col_blocks, threads, smem, s, 1, p,
+                col_blocks);
+    if (st == T3_OK) st = launch_join(p, s);
+    if (st != T3_OK) return st;
+  }
+  return launch(linear_tokens_kernel<T, kReverse, false>, static_cast<int64_t>(p.parts) * col_blocks, threads, smem, s, 1,
+                p, col_blocks);
+}
+
+}  // namespace lin
+
+bool linear_tc_fits(const lin::Args&, int) { return false; }
+int launch_linear_tc(lin::Args, bool, float*, int, int*, cudaStream_t) { return T3_EINVAL; }
+
+int launch_linear_tokens(lin::Args p, bool reverse, int dtype, float* workspace, int sms, cudaStream_t s) {
+  p.blocks = (p.length + lin::kTokens - 1) / lin::kTokens;
+  // about two CTAs an SM: whole sequences where there are as many, else cuts
+  const int64_t col_blocks = (p.dv + lin::kCols - 1) / lin::kCols, want = (2 * sms + col_blocks - 1) / col_blocks;
+  const int st = lin::cut(&p, p.pairs < want ? std::min<int64_t>(want, kMaxLinearParts) : p.pairs, workspace, s);
+  if (st != T3_OK) return st;
+  if (dtype == T3_OUT_BF16)
+    return reverse ? lin::run<vec::bf16, true>(p, s) : lin::run<vec::bf16, false>(p, s);
+  return reverse ? lin::run<float, true>(p, s) : lin::run<float, false>(p, s);
+}
+
+}  // namespace t3

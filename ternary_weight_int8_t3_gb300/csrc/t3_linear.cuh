@@ -1,0 +1,91 @@
+// t3_linear.cuh -- what the kernels of linear attention share (t3_linear.cu token by token,
+// t3_linear_tc.cu by chunks on the tensor cores).
+//
+// One recurrence serves the forward and all of the gradient.  For a head with decay g = exp(log_decay),
+// rows q_t, k_t of dk and v_t of dv elements, in the order the tokens are taken:
+//   S = c_t S + in_scale k_t v_t^T,   o_t = out_scale S^T q_t
+// with c_t = g, or 0 where the token in front is cut off (a reset), or 1 at the first token of a
+// reversed pass.  With G_t = dL/dS_t the gradients are the same recurrence over other operands:
+//   o  = (q, k, v)    in time, in_scale 1, out_scale scale, from the state
+//   dq = (do, v, k)   in time, the same scales, from the state transposed
+//   dv = (k, q, do)   against time, in_scale scale, out_scale 1, from dstate_last; leaves G_0
+//   dk = (v, do, q)   the same, from dstate_last transposed
+//
+// Parts.  Every sequence and head is `blocks` blocks of tokens in the order they are taken, and all
+// of them together, one after the other, are cut into `parts` equal ranges, one for each CTA (or
+// group of CTAs that share a state's columns), so that few long sequences fill the GPU as many short ones
+// do.  Where a cut falls inside a sequence, a first kernel takes the state that the range in front of the cut
+// adds, a second joins those along the sequence, and the ranges then begin with the state they need.
+#pragma once
+#include <algorithm>
+
+#include "t3_vec.cuh"
+
+namespace t3 {
+namespace lin {
+
+using namespace vec;
+
+constexpr int kMaxHead = 128;   // elements of a head's row
+
+struct Args {
+  const void *q, *k, *v;
+  int64_t ldq, ldk, ldv;  // elements from token to token; heads lie one after the other
+  void* o;
+  int64_t ldo;
+  const float* log_decay;  // [heads]
+  const float* init;       // [batch][heads] states [dk][dv], or [dv][dk] (init_transposed); null: zeros
+  int init_transposed;
+  const uint8_t* resets;   // [batch][length] or null
+  float in_scale, out_scale;
+  float* last;             // the state behind the last token, [dk][dv]; null: not wanted
+  int64_t length, heads, pairs;  // pairs: batch * heads
+  int dk, dv;
+  int64_t blocks;          // blocks of tokens a sequence
+  int parts;
+  int64_t each, rest;      // blocks in all over parts, and what is left
+  float* local;            // [parts][dk * dv]: the state in front of each range that begins inside a sequence
+  float* pass;             // [parts]: what is left of a state across the piece in front of such a range
+};
+
+__host__ __device__ __forceinline__ int64_t part_begin(const Args& p, int64_t i) { return p.each * i + p.rest * i / p.parts; }
+
+// exp(log_decay n), and 1 for n = 0 whatever the decay.
+__device__ __forceinline__ float decay_power(float log2_decay, int n) {
+  return n == 0 ? 1.0f : exp2f(log2_decay * static_cast<float>(n));
+}
+
+// A sequence's first block of the piece that part i computes last, and the end of it; false
+// where the part ends with a sequence.
+__device__ __forceinline__ bool cut_piece(const Args& p, int part, int64_t& pair, int64_t& b0, int64_t& b1) {
+  const int64_t begin = part_begin(p, part), end = part_begin(p, part + 1);
+  pair = end / p.blocks;
+  b1 = end - pair * p.blocks;
+  b0 = begin > pair * p.blocks ? begin - pair * p.blocks : 0;
+  return b1 > 0;
+}
+
+// Sets the ranges: so many, where there is a workspace for their states or they end with sequences anyway;
+// else one for each sequence and head.  A pass that replaces the states it begins with takes a copy of them.
+int cut(Args* p, int64_t parts, float* workspace, cudaStream_t s);
+int launch_join(const Args& p, cudaStream_t s);
+
+}  // namespace lin
+
+// Ranges a pass is cut into at most: a workspace's size does not depend on the device.
+constexpr int kMaxLinearParts = 304;
+// Floats of workspace for a pass: `local` and `pass` of the ranges, and a copy of the first states for a
+// pass that replaces them (few sequences: kMaxLinearParts at most; more are not cut then).
+inline int64_t linear_workspace(int64_t pairs, int64_t length, int64_t dk, int64_t dv) {
+  if (pairs <= 0 || length <= 32 || dk <= 0 || dv <= 0) return 0;
+  return kMaxLinearParts * (dk * dv + 1) + std::min<int64_t>(pairs, kMaxLinearParts) * dk * dv;
+}
+
+// One pass of the recurrence above, by chunks on the tensor cores (bf16, rows of 16-byte
+// pieces, t3_linear_tc.cu) and token by token (t3_linear.cu).  workspace: floats for
+// linear_parts() states and passes.
+bool linear_tc_fits(const lin::Args& p, int dtype);
+int launch_linear_tc(lin::Args p, bool reverse, float* workspace, int sms, int* err, cudaStream_t s);
+int launch_linear_tokens(lin::Args p, bool reverse, int dtype, float* workspace, int sms, cudaStream_t s);
+
+}  // namespace t3

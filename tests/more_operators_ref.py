@@ -97,3 +97,56 @@ def glu_bwd(dy, gate, up, kind):
     y, slope, ey, es = act(gate, kind)
     dgate, dup = dy * up * slope, dy * y
     return dgate, dup, np.abs(dy * up) * es + 4 * U * np.abs(dgate), np.abs(dy) * ey + 4 * U * np.abs(dup)
+
+
+# --------------------------------------------------------- linear attention ---
+
+def linear_attend(q, k, v, log_decay, state, resets, scale, reverse=False, chunks=False):
+    """The recurrence of linear attention over [batch][length][heads][d], token by token in 64 bits, and
+    bounds of its float computation.  reverse: against time, a mark cutting a token off from the
+    one behind it, and the first token taken undecayed.  Returns (o, last state, bound of
+    o before its rounding, bound of the state).
+
+    With A the recurrence of magnitudes, a state is off by E: the decay's relative error (its
+    argument's rounding and an exponential of 2 ulp) and three roundings a step; o by q E and a float
+    sum's roundings.  Parts joined along a sequence repeat at most each of these once.
+    chunks: q k^T and the state are rounded to bf16 on their way to o, 2^-8 each, and what is added
+    to the state to 2^-16 (two bf16 terms)."""
+    batch, length, heads, dk = q.shape
+    decay = np.exp(log_decay)[None, :, None, None]
+    with np.errstate(invalid="ignore"):
+        err = np.where(np.isinf(log_decay), 0, 6 + 3 * np.abs(np.where(np.isinf(log_decay), 0, log_decay)))[None, :, None, None] * U
+    order = range(length - 1, -1, -1) if reverse else range(length)
+    S = np.zeros((batch, heads, dk, v.shape[3])) if state is None else state.copy()
+    A, E = np.abs(S), np.zeros_like(S)
+    o = np.empty((batch, length, heads, v.shape[3]))
+    eo = np.empty_like(o)
+    add = (2.0 ** -16 if chunks else 0) + 4 * U
+    meet = 2.0 ** -8 if chunks else 0
+    for t in order:
+        mark = t + 1 if reverse else t
+        if resets is not None and mark < length:
+            live = (resets[:, mark] == 0)[:, None, None, None]
+            S, A, E = np.where(live, S, 0), np.where(live, A, 0), np.where(live, E, 0)
+        c = 1.0 if reverse and t == length - 1 else decay
+        kv = k[:, t, :, :, None] * v[:, t, :, None, :]
+        E = c * (E + (err + 3 * U) * A) + add * np.abs(kv)
+        S, A = c * S + kv, c * A + np.abs(kv)
+        qt = q[:, t, :, None, :]
+        o[:, t] = scale * (qt @ S)[:, :, 0]
+        eo[:, t] = abs(scale) * (np.abs(qt) @ (2 * E + (meet + (dk + 16) * U) * A))[:, :, 0]
+    return o, S, eo, 2 * E + 4 * U * np.abs(S)
+
+
+def linear_attend_bwd(q, k, v, log_decay, do, state, resets, scale, dlast, chunks=False):
+    """{name: (gradient, bound before its rounding)} of q, k, v and the state."""
+    t = (0, 1, 3, 2)
+    swap = lambda s: None if s is None else s.transpose(t)  # noqa: E731
+    dq, _, eq, _ = linear_attend(do, v, k, log_decay, swap(state), resets, scale, chunks=chunks)
+    dv, ds, ev, es = linear_attend(k, scale * q, do, log_decay, dlast, resets, 1.0, True, chunks)
+    dk, _, ek, _ = linear_attend(v, do, scale * q, log_decay, swap(dlast), resets, 1.0, True, chunks)
+    decay = np.exp(log_decay)[None, :, None, None]
+    live = 1.0 if resets is None else (resets[:, 0] == 0)[:, None, None, None]
+    ds = np.where(live, ds * decay, 0)
+    es = np.where(live, es * decay + np.abs(ds) * (8 + 3 * np.abs(np.where(np.isinf(log_decay), 0, log_decay)))[None, :, None, None] * U, 0)
+    return {"q": (dq, eq), "k": (dk, ek), "v": (dv, ev), "state": (ds, es)}

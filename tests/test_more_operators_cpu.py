@@ -79,3 +79,38 @@ def test_glu_bwd_refusals(lib):
     assert _glu_bwd(lib, dg=None) == t3.T3_OK
     assert _glu_bwd(lib, cols=0, dy=None, gate=None, up=None) == t3.T3_OK
     assert _glu_bwd(lib, rows=0, dy=None, gate=None, up=None) == t3.T3_OK
+
+
+def _lin(lib, q=FAKE, k=FAKE, v=FAKE, o=FAKE, ld=FAKE, ldq=48, ldk=48, ldv=48, ldo=48, b=2, t=3, h=3, dk=16, dv=16, dt=BF16,
+         last=None):
+    return lib.t3_linear_attn_fwd(q, ldq, k, ldk, v, ldv, ld, None, None, 1.0, o, ldo, last, b, t, h, dk, dv, dt, None, None)
+
+
+def test_linear_refusals(lib):
+    bad = [dict(b=-1), dict(t=-1), dict(h=-1), dict(dk=0), dict(dv=0), dict(dk=129), dict(dv=129), dict(b=BIG), dict(t=BIG),
+           dict(h=BIG), dict(b=1 << 20, h=1 << 20), dict(ldq=-1), dict(ldk=BIG), dict(ldv=-1), dict(ldo=47), dict(dt=2),
+           dict(q=None), dict(k=None), dict(v=None), dict(o=None), dict(ld=None)]
+    for kw in bad:
+        assert _lin(lib, **kw) == t3.T3_EINVAL, kw
+    for kw in (dict(b=0), dict(h=0)):
+        assert _lin(lib, q=None, k=None, v=None, o=None, ld=None, **kw) == t3.T3_OK, kw
+
+
+def _lin_bwd(lib, q=FAKE, k=FAKE, v=FAKE, do=FAKE, ld=FAKE, dq=FAKE, dk_=FAKE, dv_=FAKE, s=48, sq=48, sk=48, sv=48, b=2, t=3,
+             h=3, dk=16, dv=16, dt=BF16):
+    return lib.t3_linear_attn_bwd(q, s, k, s, v, s, do, s, ld, None, None, 1.0, None, dq, sq, dk_, sk, dv_, sv, None, b, t, h,
+                                  dk, dv, dt, None, None)
+
+
+def test_linear_bwd_refusals(lib):
+    bad = [dict(b=-1), dict(t=-1), dict(h=-1), dict(dk=0), dict(dv=129), dict(s=-1), dict(sq=47), dict(sk=47), dict(sv=47),
+           dict(dt=2)] + [{n: None} for n in ("q", "k", "v", "do", "ld", "dq", "dk_", "dv_")]
+    for kw in bad:
+        assert _lin_bwd(lib, **kw) == t3.T3_EINVAL, kw
+    assert _lin_bwd(lib, b=0, q=None, k=None, v=None, do=None, ld=None, dq=None, dk_=None, dv_=None) == t3.T3_OK
+
+
+def test_linear_workspace(lib):
+    f = lib.t3_linear_attn_workspace
+    assert f(0, 100, 3, 64, 64) == f(2, 32, 3, 64, 64) == f(2, 100, 3, 0, 64) == f(2, 100, 3, 64, 129) == 0
+    assert 0 < f(1, 33, 1, 64, 64) <= f(400, 100, 1, 64, 64) <= 610 * 64 * 64
