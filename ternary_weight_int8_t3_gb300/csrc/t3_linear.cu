@@ -8,7 +8,9 @@
 // 32 columns of a state in registers, 16 rows of a column a thread, so that S stays where it is from
 // token to token; a block of tokens' rows is staged in shared memory as floats, where a warp reads
 // q and k as broadcasts, and o is summed over the rows by the warps, each leaving its part in
-// shared memory until the block ends.
+// shared memory until the block ends.  A step with g above a half is taken as S + (g - 1) S + k v^T with g - 1 =
+// expm1(log_decay): g itself, rounded, would be off by as much at every step, and a memory of n tokens by n
+// times that (512 tokens: the state 2e-4).  Below, g S keeps its own relative precision.
 #include "t3_linear.cuh"
 
 namespace t3 {
@@ -17,6 +19,7 @@ namespace lin {
 constexpr int kCols = 32;   // columns of a state a CTA holds, one a lane
 constexpr int kRows = 16;   // rows of it a warp
 constexpr int kTokens = 32; // tokens of a block
+constexpr float kLn2 = 0.69314718f;
 
 __device__ __forceinline__ float load1(const float* p) { return *p; }
 __device__ __forceinline__ float load1(const bf16* p) { return __bfloat162float(*p); }
@@ -26,6 +29,33 @@ __device__ __forceinline__ void store1(bf16* p, float x) { *p = __float2bfloat16
 constexpr int padded(int d) { return (d + kRows - 1) / kRows * kRows; }
 constexpr int smem_floats(int tokens, int dk) {
   return tokens * (2 * padded(dk) + kCols + 1) + padded(dk) / kRows * tokens * kCols;
+}
+
+constexpr float kCut = 2.0f;  // a token whose state starts anew, among the factors
+
+// One token: S = S + c S (kSlow) or c S, plus k v^T, and this warp's part of S^T q.
+template <bool kSlow, bool kStates>
+__device__ __forceinline__ float token(float2 (&S)[kRows / 2], float c, float v, const float4* k, const float4* q) {
+  if (c == kCut) {  // whatever the state held
+    c = 0.0f;
+#pragma unroll
+    for (int i = 0; i < kRows / 2; ++i) S[i] = make_float2(0.0f, 0.0f);
+  }
+  const float2 c2 = make_float2(c, c), v2 = make_float2(v, v);
+  float2 sum = make_float2(0.0f, 0.0f), sum2 = sum;
+#pragma unroll
+  for (int i = 0; i < kRows / 4; ++i) {
+    const float4 k4 = k[i];
+    float2 &a = S[2 * i], &b = S[2 * i + 1];
+    a = __ffma2_rn(make_float2(k4.x, k4.y), v2, kSlow ? __ffma2_rn(a, c2, a) : __fmul2_rn(a, c2));
+    b = __ffma2_rn(make_float2(k4.z, k4.w), v2, kSlow ? __ffma2_rn(b, c2, b) : __fmul2_rn(b, c2));
+    if (!kStates) {
+      const float4 q4 = q[i];
+      sum = __ffma2_rn(make_float2(q4.x, q4.y), a, sum);
+      sum2 = __ffma2_rn(make_float2(q4.z, q4.w), b, sum2);
+    }
+  }
+  return (sum.x + sum.y) + (sum2.x + sum2.y);
 }
 
 // kStates: only what each part's last piece adds to the state (Args::local).
@@ -52,13 +82,17 @@ __global__ void __launch_bounds__(kMaxHead / kRows * 32) linear_tokens_kernel(co
   const bool has_col = col < p.dv;
   float2 S[kRows / 2];
   bool fresh = true;  // the state is still to be loaded
-  float passed = 1.0f;
+  int64_t decays = 0;  // of a state that passes this piece, and whether something cuts it off
+  bool cut_off = false;
   for (; at < end; ++at) {
     const int64_t pair = at / p.blocks, head = pair % p.heads, batch = pair / p.heads;
     const int64_t block = at - pair * p.blocks, tb = kReverse ? p.blocks - 1 - block : block;
     const int64_t t0 = tb * kTokens;
     const int n = static_cast<int>(p.length - t0 < kTokens ? p.length - t0 : kTokens);
-    const float decay = exp2f(p.log_decay[head] * kLog2e);
+    const float log_decay = p.log_decay[head];
+    const bool slow = log_decay > -kLn2;
+    // of the state from token to token, and where it comes from behind the last token
+    const float factor = slow ? expm1f(log_decay) : expf(log_decay), whole = slow ? 0.0f : 1.0f;
     const int64_t state_at = pair * p.dk * p.dv;
     if (fresh || block == 0) {
       fresh = false;
@@ -96,32 +130,19 @@ __global__ void __launch_bounds__(kMaxHead / kRows * 32) linear_tokens_kernel(co
       // that of the token taken before it, which is the next one
       const int64_t mark = kReverse ? t + 1 : t;
       const bool cut = p.resets && mark < p.length && p.resets[batch * p.length + mark] != 0;
-      cs[j] = cut ? 0.0f : kReverse && t + 1 == p.length ? 1.0f : decay;
+      cs[j] = cut ? kCut : kReverse && t + 1 == p.length ? whole : factor;
     }
     __syncthreads();
     for (int j = 0; j < n; ++j) {
       const float c = cs[j], v = vs[j * kCols + lane];
-      if (kStates) passed *= c;
-      const float2 c2 = make_float2(c, c), v2 = make_float2(v, v);
+      if (kStates) {
+        decays += c != whole;
+        cut_off |= c == kCut;
+      }
       const float4* kp = reinterpret_cast<const float4*>(ks + j * rows + warp * kRows);
       const float4* qp = reinterpret_cast<const float4*>(qs + j * rows + warp * kRows);
-      if (c == 0.0f) {  // whatever the state held
-#pragma unroll
-        for (int i = 0; i < kRows / 2; ++i) S[i] = make_float2(0.0f, 0.0f);
-      }
-      float2 sum = make_float2(0.0f, 0.0f), sum2 = sum;
-#pragma unroll
-      for (int i = 0; i < kRows / 4; ++i) {
-        const float4 k4 = kp[i];
-        S[2 * i] = __ffma2_rn(make_float2(k4.x, k4.y), v2, __fmul2_rn(S[2 * i], c2));
-        S[2 * i + 1] = __ffma2_rn(make_float2(k4.z, k4.w), v2, __fmul2_rn(S[2 * i + 1], c2));
-        if (!kStates) {
-          const float4 q4 = qp[i];
-          sum = __ffma2_rn(make_float2(q4.x, q4.y), S[2 * i], sum);
-          sum2 = __ffma2_rn(make_float2(q4.z, q4.w), S[2 * i + 1], sum2);
-        }
-      }
-      if (!kStates) os[(warp * tokens + j) * kCols + lane] = (sum.x + sum.y) + (sum2.x + sum2.y);
+      const float x = slow ? token<true, kStates>(S, c, v, kp, qp) : token<false, kStates>(S, c, v, kp, qp);
+      if (!kStates) os[(warp * tokens + j) * kCols + lane] = x;
     }
     __syncthreads();
     if (!kStates)
@@ -138,16 +159,17 @@ __global__ void __launch_bounds__(kMaxHead / kRows * 32) linear_tokens_kernel(co
       float* to = kStates ? p.local + static_cast<int64_t>(part + 1) * p.dk * p.dv : p.last + state_at;
       // against time what is left is the gradient of the state in front of the first token
       const bool cut = kReverse && behind && p.resets && p.resets[batch * p.length] != 0;
-      const float f = kReverse && behind ? decay : 1.0f;
+      const float f = kReverse && behind ? expf(log_decay) : 1.0f;
 #pragma unroll
       for (int i = 0; i < kRows; ++i) {
         const int r = warp * kRows + i;
         const float x = i & 1 ? S[i / 2].y : S[i / 2].x;
         if (r < p.dk) to[r * p.dv + col] = cut || f == 0.0f ? 0.0f : f * x;
       }
+      if (kStates && threadIdx.x == 0 && col == 0)
+        p.pass[part + 1] = cut_off ? 0.0f : decays == 0 ? 1.0f : expf(log_decay * static_cast<float>(decays));
     }
   }
-  if (kStates && threadIdx.x == 0 && col == 0) p.pass[part + 1] = passed;
 }
 
 // The states in front of the ranges that begin inside a sequence: what the piece before adds, plus what is left
@@ -193,7 +215,7 @@ int cut(Args* p, int64_t parts, float* workspace, cudaStream_t s) {
   const bool in_place = p->init && p->last == p->init;
   p->local = p->pass = nullptr;
   parts = std::min(parts, total);
-  if (p->pairs % parts == 0) return set(parts);  // they end with sequences
+  if (p->pairs % parts == 0 || p->blocks == 1) return set(parts);  // they end with sequences
   if (!workspace || parts > kMaxLinearParts || (in_place && p->pairs >= kMaxLinearParts)) return set(p->pairs);
   const int64_t size = static_cast<int64_t>(p->dk) * p->dv;
   p->local = workspace;
@@ -233,9 +255,6 @@ int run(const Args& p, cudaStream_t s) {
 }
 
 }  // namespace lin
-
-bool linear_tc_fits(const lin::Args&, int) { return false; }
-int launch_linear_tc(lin::Args, bool, float*, int, int*, cudaStream_t) { return T3_EINVAL; }
 
 int launch_linear_tokens(lin::Args p, bool reverse, int dtype, float* workspace, int sms, cudaStream_t s) {
   p.blocks = (p.length + lin::kTokens - 1) / lin::kTokens;

@@ -50,11 +50,6 @@ struct Args {
 
 __host__ __device__ __forceinline__ int64_t part_begin(const Args& p, int64_t i) { return p.each * i + p.rest * i / p.parts; }
 
-// exp(log_decay n), and 1 for n = 0 whatever the decay.
-__device__ __forceinline__ float decay_power(float log2_decay, int n) {
-  return n == 0 ? 1.0f : exp2f(log2_decay * static_cast<float>(n));
-}
-
 // A sequence's first block of the piece that part i computes last, and the end of it; false
 // where the part ends with a sequence.
 __device__ __forceinline__ bool cut_piece(const Args& p, int part, int64_t& pair, int64_t& b0, int64_t& b1) {
