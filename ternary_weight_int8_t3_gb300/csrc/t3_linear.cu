@@ -173,26 +173,25 @@ __global__ void __launch_bounds__(kMaxHead / kRows * 32) linear_tokens_kernel(co
 }
 
 // The states in front of the ranges that begin inside a sequence: what the piece before adds, plus what is left
-// of the state in front of that.  A CTA takes 1024 elements of the states of one sequence and head.
+// of the state in front of that.  A CTA takes 1024 elements of one sequence's states: it goes with the
+// first range that begins inside the sequence.
 __global__ void __launch_bounds__(256) linear_join_kernel(const Args p, int element_blocks) {
-  const int64_t pair = blockIdx.x / element_blocks;
-  const int e0 = static_cast<int>(blockIdx.x - pair * element_blocks) * 1024 + threadIdx.x, size = p.dk * p.dv;
+  int j = blockIdx.x / element_blocks + 1;
+  const int size = p.dk * p.dv, e0 = (blockIdx.x - (j - 1) * element_blocks) * 1024 + threadIdx.x;
+  const int64_t begin = part_begin(p, j), pair = begin / p.blocks, first = pair * p.blocks;
   launch_dependents();
   grid_dependency_wait();
-  const int64_t total = p.pairs * p.blocks, first = pair * p.blocks;
-  // the first range that begins behind the sequence's first block
-  int64_t j = (first * p.parts + total - 1) / total;
-  while (part_begin(p, j) <= first) ++j;
-  if (j >= p.parts || part_begin(p, j) >= first + p.blocks) return;
+  if (begin == first || part_begin(p, j - 1) > first) return;
   float x[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const int e = e0 + 256 * i, r = e / p.dv, c = e - r * p.dv;
-    x[i] = p.init && e < size ? p.init[pair * size + (p.init_transposed ? c * p.dk + r : e)] : 0.0f;
+    const int e = e0 + 256 * i;
+    x[i] = 0.0f;
+    if (p.init && e < size) x[i] = p.init[pair * size + (p.init_transposed ? e % p.dv * p.dk + e / p.dv : e)];
   }
   for (; j < p.parts && part_begin(p, j) < first + p.blocks; ++j) {
     const float pass = p.pass[j];
-    float* at = p.local + j * size;
+    float* at = p.local + static_cast<int64_t>(j) * size;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int e = e0 + 256 * i;
@@ -231,7 +230,7 @@ int cut(Args* p, int64_t parts, float* workspace, cudaStream_t s) {
 
 int launch_join(const Args& p, cudaStream_t s) {
   const int blocks = (p.dk * p.dv + 1023) / 1024;
-  return launch(linear_join_kernel, p.pairs * blocks, 256, 0, s, 1, p, blocks);
+  return launch(linear_join_kernel, static_cast<int64_t>(p.parts - 1) * blocks, 256, 0, s, 1, p, blocks);
 }
 
 template <class T, bool kReverse>

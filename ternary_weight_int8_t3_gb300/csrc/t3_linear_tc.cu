@@ -13,14 +13,15 @@
 // What bounds it: memory, q, k, v in and o out once.  A chunk of a head of 128 moves 128 KB, some 5600 clocks of an
 // SM's share of the memory's rate; its five products take 1300 of the tensor pipe.  The rest is latency: P
 // waits for Q K^T, the state for the product before.  So every step has warps of its own, handing over through
-// mbarriers, K and V come two chunks ahead and Q one:
-//   warp 0 TMA; warp 1 issues the products; warps 4-7 P; 8-11 K'; 12-15 the state; 16-19 o.
+// mbarriers, and the two chains have an issuer each; K and V come two chunks ahead and Q one:
+//   warp 0 TMA; warp 1 issues Q K^T and P V, warp 2 Q S and K'^T V; warps 4-7 P; 8-11 K'; 12-15 the state; 16-19 o.
 // Each group's thread owns a TMEM lane: a token's row of P and o, a row of the state (dk), and for K' a
 // token's row in shared memory.  TMEM columns: Q K^T 128, with P over its first 64; P V; Q S; the state.
 //
 // Decays.  A thread of P has one row; in a block of 32 columns next to it the coefficient is a power of its own
 // times one of a table of 32 that all rows share, and where the block meets the diagonal the
-// table read at the distance: two products an element, no exponential, and none of them above 1.
+// table read at the distance, zeros where it is negative: no exponential an element, and no coefficient above 1.
+// The pass for the states alone takes K' decayed to the end of the piece, so that it is one long product.
 #include <cudaTypedefs.h>
 
 #include <cstring>
@@ -40,19 +41,20 @@ constexpr int kWarpP = 4, kWarpK = 8, kWarpS = 12, kWarpO = 16;
 constexpr int kTcThreads = 32 * 20;
 constexpr int kColS = 0, kColPV = 128, kColQS = 256, kColState = 384;  // TMEM columns
 constexpr int kCode = 12 << 8;
+constexpr int kTable = 96;  // floats: 32 zeros, g^0 .. g^31 (times in_scale), and those backwards
 
 template <int DK, int DV> struct Smem {
   static constexpr int half = kChunk * 128;  // a tile's 64 columns
   static constexpr int tile_k = DK / 64 * half, tile_v = DV / 64 * half;
   static constexpr int state = DK * DV * 2;
-  static constexpr int q = 0;
+  static constexpr int q = 0;                  // for the states alone a second k_low
   static constexpr int k = q + tile_k;         // two
   static constexpr int v = k + 2 * tile_k;     // two
   static constexpr int k_low = v + 2 * tile_v; // what K' leaves behind its first bf16
   static constexpr int s = k_low + tile_k;     // the state as bf16, [DK][64] halves
-  static constexpr int tables = s + state;     // a warp of P each: g^0 .. g^31, and backwards
-  static constexpr int bars = tables + 4 * 2 * 32 * 4;
-  static constexpr int n_bars = 2 + 8 + 7;
+  static constexpr int tables = s + state;     // a warp of P each: see kTable
+  static constexpr int bars = tables + 4 * kTable * 4;
+  static constexpr int n_bars = 22;
   static constexpr int misc = bars + 8 * n_bars;
   static constexpr int bytes = misc + 16 + 1024;
   static_assert(bytes <= 227 * 1024, "shared memory budget");
@@ -110,67 +112,67 @@ __device__ __forceinline__ float power(float log2_decay, int n) {
 
 // A CTA's chunks, in the order they are taken.  Every role walks the same ones.
 struct Walk {
-  int64_t at, end;
-  int64_t pair, block;
-  int count = 0;  // chunks taken before this one
+  int left;              // chunks still to take
+  int count = 0;         // and taken
+  int pair, head, batch;
+  int block;             // in the sequence
   __device__ __forceinline__ void next(const Args& p) {
-    ++at;
+    --left;
     ++count;
-    if (++block == p.blocks) {
+    if (++block == static_cast<int>(p.blocks)) {
       block = 0;
       ++pair;
+      if (++head == static_cast<int>(p.heads)) {
+        head = 0;
+        ++batch;
+      }
     }
   }
-  __device__ __forceinline__ bool more() const { return at < end; }
+  __device__ __forceinline__ bool more() const { return left > 0; }
   __device__ __forceinline__ uint32_t parity() const { return count & 1; }
 };
 
-template <bool kReverse, bool kStates>
+template <bool kStates>
 __device__ __forceinline__ Walk walk(const Args& p) {
   Walk w;
-  w.at = part_begin(p, blockIdx.x);
-  w.end = part_begin(p, blockIdx.x + 1);
+  int64_t pair, b0, b1;
   if (kStates) {
-    int64_t b0, b1;
-    if (!cut_piece(p, blockIdx.x, w.pair, b0, b1)) {
-      w.at = w.end;
-      return w;
-    }
-    w.block = b0;
-    w.at = w.end - (b1 - b0);
+    w.left = cut_piece(p, blockIdx.x, pair, b0, b1) ? static_cast<int>(b1 - b0) : 0;
   } else {
-    w.pair = w.at / p.blocks;
-    w.block = w.at - w.pair * p.blocks;
+    const int64_t at = part_begin(p, blockIdx.x);
+    w.left = static_cast<int>(part_begin(p, blockIdx.x + 1) - at);
+    pair = at / p.blocks;
+    b0 = at - pair * p.blocks;
   }
+  if (w.left == 0) pair = b0 = 0;
+  w.pair = static_cast<int>(pair);
+  w.block = static_cast<int>(b0);
+  w.batch = w.pair / static_cast<int>(p.heads);
+  w.head = w.pair - w.batch * static_cast<int>(p.heads);
   return w;
 }
 
 // A chunk: its first token, tokens, and whether it begins a reversed pass.
 struct Chunk {
-  int64_t t0;
-  int n, e;
-  template <bool kReverse>
-  static __device__ __forceinline__ Chunk of(const Args& p, int64_t block) {
-    Chunk c;
-    c.t0 = (kReverse ? p.blocks - 1 - block : block) * kChunk;
-    c.n = static_cast<int>(p.length - c.t0 < kChunk ? p.length - c.t0 : kChunk);
-    c.e = kReverse && block == 0 ? 0 : 1;
-    return c;
-  }
+  int t0, n, e;
 };
+template <bool kReverse>
+__device__ __forceinline__ Chunk chunk(const Args& p, int block) {
+  Chunk c;
+  c.t0 = (kReverse ? static_cast<int>(p.blocks) - 1 - block : block) * kChunk;
+  c.n = min(static_cast<int>(p.length) - c.t0, kChunk);
+  c.e = kReverse && block == 0 ? 0 : 1;
+  return c;
+}
 
 // The marks of a chunk's tokens, a bit each; the whole warp calls.
 struct Marks {
   uint32_t w[4];
-  __device__ __forceinline__ Marks(const Args& p, int64_t batch, const Chunk& c) {
-    const int lane = threadIdx.x & 31;
+  __device__ __forceinline__ Marks(const Args& p, int batch, const Chunk& c) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      w[i] = 0u;
-      if (p.resets) {
-        const int j = 32 * i + lane;
-        w[i] = __ballot_sync(0xffffffffu, j < c.n && p.resets[batch * p.length + c.t0 + j] != 0);
-      }
+      const int j = 32 * i + (threadIdx.x & 31);
+      w[i] = __ballot_sync(0xffffffffu, j < c.n && p.resets[batch * p.length + c.t0 + j] != 0);
     }
   }
   __device__ __forceinline__ bool any() const { return (w[0] | w[1] | w[2] | w[3]) != 0u; }
@@ -206,18 +208,18 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + (((smem_addr(smem_raw) + 1023u) & ~1023u) - smem_addr(smem_raw));
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::bars);
-  uint64_t *q_full = bars, *q_empty = bars + 1, *k_full = bars + 2, *k_empty = bars + 4, *v_full = bars + 6,
-           *v_empty = bars + 8, *s_full = bars + 10, *p_full = bars + 11, *kp_full = bars + 12, *st_full = bars + 13,
-           *upd_done = bars + 14, *o_full = bars + 15, *o_empty = bars + 16;
+  uint64_t *q_full = bars, *k_full = bars + 1, *v_full = bars + 3, *k_empty = bars + 5, *s_full = bars + 7,
+           *pv_done = bars + 8, *upd_done = bars + 9, *end_bar = bars + 10;  // one arrival each
+  uint64_t *q_empty = bars + 11, *v_empty = bars + 12, *o_full = bars + 14;  // both issuers
+  uint64_t *p_full = bars + 15, *kp_full = bars + 16, *st_full = bars + 18, *o_empty = bars + 19;  // a group's warps
+  uint64_t* drain = bars + 20;  // one for each issuer
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(smem + L::misc);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::misc + 4);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) {
-    for (int i = 0; i < L::n_bars; ++i) {
-      const uint64_t* b = bars + i;
-      mbar_init(bars + i, b == p_full || b == kp_full || b == st_full || b == o_empty ? kGroup : 1);
-    }
+    for (int i = 0; i < L::n_bars; ++i)
+      mbar_init(bars + i, i < 11 ? 1 : i < 15 ? (kStates ? 1 : 2) : i < 20 ? kGroup : 1);
     *abort_flag = 0;
     fence_mbarrier_init();
   }
@@ -232,7 +234,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   launch_dependents();
   grid_dependency_wait();
 
-  Walk w = walk<kReverse, kStates>(p);
+  Walk w = walk<kStates>(p);
   bool ok = true;
   if (warp == 0) {
     // ---------------------------------------------------------------- loads
@@ -240,30 +242,28 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       prefetch_tensormap(&map_k);
       prefetch_tensormap(&map_v);
       if (!kStates) prefetch_tensormap(&map_q);
-      int q_loads = 0, kv_loads = 0, v_loads = 0;
+      int q_loads = 0, k_loads = 0, v_loads = 0;
       for (; ok && w.more(); w.next(p)) {
-        const Chunk c = Chunk::of<kReverse>(p, w.block);
-        const int head = static_cast<int>(w.pair % p.heads), batch = static_cast<int>(w.pair / p.heads);
-        const int slot = w.count & 1, t0 = static_cast<int>(c.t0);
+        const int t0 = chunk<kReverse>(p, w.block).t0, slot = w.count & 1;
         const uint32_t free = ((w.count >> 1) & 1) ^ 1u;
         ok = mbar_wait(&k_empty[slot], free, abort_flag, err, kCode | 1);
         if (!ok) break;
         mbar_arrive_expect_tx(&k_full[slot], L::tile_k);
         for (int h = 0; h < DK / 64; ++h)
-          tma_load_4d(smem + L::k + slot * L::tile_k + h * L::half, &map_k, &k_full[slot], 64 * h, head, t0, batch);
-        ++kv_loads;
+          tma_load_4d(smem + L::k + slot * L::tile_k + h * L::half, &map_k, &k_full[slot], 64 * h, w.head, t0, w.batch);
+        ++k_loads;
         ok = mbar_wait(&v_empty[slot], free, abort_flag, err, kCode | 1);
         if (!ok) break;
         mbar_arrive_expect_tx(&v_full[slot], L::tile_v);
         for (int h = 0; h < DV / 64; ++h)
-          tma_load_4d(smem + L::v + slot * L::tile_v + h * L::half, &map_v, &v_full[slot], 64 * h, head, t0, batch);
+          tma_load_4d(smem + L::v + slot * L::tile_v + h * L::half, &map_v, &v_full[slot], 64 * h, w.head, t0, w.batch);
         ++v_loads;
         if (kStates) continue;
         ok = mbar_wait(q_empty, w.parity() ^ 1u, abort_flag, err, kCode | 1);
         if (!ok) break;
         mbar_arrive_expect_tx(q_full, L::tile_k);
         for (int h = 0; h < DK / 64; ++h)
-          tma_load_4d(smem + L::q + h * L::half, &map_q, q_full, 64 * h, head, t0, batch);
+          tma_load_4d(smem + L::q + h * L::half, &map_q, q_full, 64 * h, w.head, t0, w.batch);
         ++q_loads;
       }
       if (!ok) {  // giving up: the copies in flight land before this CTA leaves
@@ -274,85 +274,99 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             }
         };
         for (int s = 0; s < 2; ++s) {
-          landed(&k_full[s], (kv_loads + 1 - s) / 2);
+          landed(&k_full[s], (k_loads + 1 - s) / 2);
           landed(&v_full[s], (v_loads + 1 - s) / 2);
         }
         landed(q_full, q_loads);
       }
     }
     __syncwarp();
-  } else if (warp == 1) {
+  } else if (warp == 1 || warp == 2) {
     // ------------------------------------------------------------- products
     if (lane == 0) {
       const uint32_t base = smem_addr(smem);
+      const uint64_t q_rows = smem_desc_k_sw128(base + L::q), k_rows = smem_desc_k_sw128(base + L::k);
+      const uint64_t k_cols = smem_desc_mn_sw128(base + L::k, L::half, 1024), v_cols = smem_desc_mn_sw128(base + L::v, L::half, 1024);
+      const uint64_t low_cols = smem_desc_mn_sw128(base + L::k_low, L::half, 1024);
+      const uint64_t q_as_low = smem_desc_mn_sw128(base + L::q, L::half, 1024);
+      const uint64_t s_cols = smem_desc_mn_sw128(base + L::s, DK * 128, 1024);
+      // step j of 16 along a product's sum: rows of 128 bytes hold 64 of it, 32 bytes a step; columns
+      // go on by two groups of eight rows
+      auto along = [](int j) { return static_cast<uint64_t>((j >> 2) * L::half + 32 * (j & 3)) >> 4; };
+      auto down = [](int j) { return static_cast<uint64_t>(2048 * j) >> 4; };
       bool issued = false;
       for (; ok && w.more(); w.next(p)) {
         const int slot = w.count & 1;
         const uint32_t par = w.parity(), par2 = (w.count >> 1) & 1;
-        const uint32_t q = base + L::q, k = base + L::k + slot * L::tile_k, v = base + L::v + slot * L::tile_v;
-        if (!kStates) {
-          // Q K^T, over the columns that the product before reads P from
-          if (w.count > 0) ok = mbar_wait(o_full, par ^ 1u, abort_flag, err, kCode | 3);
+        const uint64_t k_at = static_cast<uint64_t>(slot * L::tile_k) >> 4, v_at = static_cast<uint64_t>(slot * L::tile_v) >> 4;
+        if (warp == 1) {
+          if (kStates) break;
+          // Q K^T, over the columns that the product before reads P from, and not before the warps of K' have seen
+          // that one's end: a barrier that moves on twice is missed
+          if (w.count > 0) {
+            ok = mbar_wait(pv_done, par ^ 1u, abort_flag, err, kCode | 3) &&
+                 mbar_wait(&kp_full[slot ^ 1], ((w.count - 1) >> 1) & 1, abort_flag, err, kCode | 3);
+          }
           ok = ok && mbar_wait(q_full, par, abort_flag, err, kCode | 3);
           ok = ok && mbar_wait(&k_full[slot], par2, abort_flag, err, kCode | 3);
           if (!ok) break;
           tc_fence_after();
 #pragma unroll
           for (int j = 0; j < DK / 16; ++j)
-            mma_ss(tmem + kColS, smem_desc_k_sw128(q + (j >> 2) * L::half + 32 * (j & 3)),
-                   smem_desc_k_sw128(k + (j >> 2) * L::half + 32 * (j & 3)), idesc_bf16(128, false, false), j > 0);
+            mma_ss(tmem + kColS, q_rows + along(j), k_rows + k_at + along(j), idesc_bf16(128, false, false), j > 0);
           issued = true;
           mma_commit(s_full);
-        }
-        ok = mbar_wait(st_full, par, abort_flag, err, kCode | 3);
-        if (!kStates && ok) {
-          // Q S
-          ok = w.count == 0 || mbar_wait(o_empty, par ^ 1u, abort_flag, err, kCode | 3);
+          mma_commit(q_empty);
+          // P V
+          ok = mbar_wait(&v_full[slot], par2, abort_flag, err, kCode | 3);
+          ok = ok && (w.count == 0 || mbar_wait(o_empty, par ^ 1u, abort_flag, err, kCode | 3));
+          ok = ok && mbar_wait(p_full, par, abort_flag, err, kCode | 3);
           if (!ok) break;
           tc_fence_after();
 #pragma unroll
-          for (int j = 0; j < DK / 16; ++j)
-            mma_ss(tmem + kColQS, smem_desc_k_sw128(q + (j >> 2) * L::half + 32 * (j & 3)),
-                   smem_desc_mn_sw128(base + L::s + j * 2048, DK * 128, 1024), idesc_bf16(DV, false, true), j > 0);
-          mma_commit(q_empty);
-        }
-        // S += K'^T V
-        ok = ok && mbar_wait(kp_full, par, abort_flag, err, kCode | 3);
-        ok = ok && mbar_wait(&v_full[slot], par2, abort_flag, err, kCode | 3);
-        if (!ok) break;
-        tc_fence_after();
-#pragma unroll
-        for (int j = 0; j < kChunk / 16; ++j) {
-          const uint64_t vd = smem_desc_mn_sw128(v + j * 2048, L::half, 1024);
-          mma_ss(tmem + kColState, smem_desc_mn_sw128(k + j * 2048, L::half, 1024), vd, idesc_bf16(DV, true, true), 1u);
-          mma_ss(tmem + kColState, smem_desc_mn_sw128(base + L::k_low + j * 2048, L::half, 1024), vd,
-                 idesc_bf16(DV, true, true), 1u);
-        }
-        issued = true;
-        mma_commit(upd_done);
-        mma_commit(&k_empty[slot]);
-        if (kStates) {
+          for (int j = 0; j < kChunk / 16; ++j)
+            mma_ts(tmem + kColPV, tmem + kColS + 8 * j, v_cols + v_at + down(j), idesc_bf16(DV, false, true), j > 0);
+          mma_commit(pv_done);
+          mma_commit(o_full);
           mma_commit(&v_empty[slot]);
-          continue;
-        }
-        // P V
-        ok = mbar_wait(p_full, par, abort_flag, err, kCode | 3);
-        if (!ok) break;
-        tc_fence_after();
+        } else {
+          if (!kStates) {
+            // Q S
+            ok = mbar_wait(q_full, par, abort_flag, err, kCode | 3);
+            ok = ok && (w.count == 0 || mbar_wait(o_empty, par ^ 1u, abort_flag, err, kCode | 3));
+            ok = ok && mbar_wait(st_full, par, abort_flag, err, kCode | 3);
+            if (!ok) break;
+            tc_fence_after();
 #pragma unroll
-        for (int j = 0; j < kChunk / 16; ++j)
-          mma_ts(tmem + kColPV, tmem + kColS + 8 * j, smem_desc_mn_sw128(v + j * 2048, L::half, 1024),
-                 idesc_bf16(DV, false, true), j > 0);
-        mma_commit(o_full);
-        mma_commit(&v_empty[slot]);
+            for (int j = 0; j < DK / 16; ++j)
+              mma_ss(tmem + kColQS, q_rows + along(j), s_cols + down(j), idesc_bf16(DV, false, true), j > 0);
+            issued = true;
+            mma_commit(q_empty);
+            mma_commit(o_full);
+          }
+          // S += K'^T V
+          ok = mbar_wait(&v_full[slot], par2, abort_flag, err, kCode | 3);
+          ok = ok && mbar_wait(&kp_full[slot], par2, abort_flag, err, kCode | 3);
+          if (!ok) break;
+          tc_fence_after();
+          const uint64_t low = kStates && slot ? q_as_low : low_cols;
+#pragma unroll
+          for (int j = 0; j < kChunk / 16; ++j) {
+            mma_ss(tmem + kColState, k_cols + k_at + down(j), v_cols + v_at + down(j), idesc_bf16(DV, true, true),
+                   !kStates || j > 0 || w.count > 0);
+            mma_ss(tmem + kColState, low + down(j), v_cols + v_at + down(j), idesc_bf16(DV, true, true), 1u);
+          }
+          issued = true;
+          if (!kStates) mma_commit(upd_done);
+          mma_commit(&k_empty[slot]);
+          mma_commit(&v_empty[slot]);
+        }
       }
+      if (kStates && warp == 2 && ok && issued) mma_commit(end_bar);
       if (!ok && issued) {  // the products in flight end before their operands go
-        uint64_t* drain = reinterpret_cast<uint64_t*>(smem + L::tables);
-        mbar_init(drain, 1);
-        fence_mbarrier_init();
-        mma_commit(drain);
+        mma_commit(drain + warp - 1);
         const uint64_t t = global_timer_ns();
-        while (!mbar_try_wait(drain, 0) && global_timer_ns() - t < kWaitLimitNs) {
+        while (!mbar_try_wait(drain + warp - 1, 0) && global_timer_ns() - t < kWaitLimitNs) {
         }
       }
     }
@@ -361,25 +375,32 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     // --------------------------------------------------------------------- P
     const int q = warp - kWarpP, row = 32 * q + lane;
     const uint32_t at = tmem + (static_cast<uint32_t>(32 * q) << 16) + kColS;
-    float* up = reinterpret_cast<float*>(smem + L::tables) + q * 64;  // g^t
-    float* down = up + 32;                                             // g^(31 - t)
-    int64_t head_of_table = -1;
+    float* up = reinterpret_cast<float*>(smem + L::tables) + q * kTable + 32;  // g^t, zeros for t < 0
+    float* back = up + 32;                                                      // g^(31 - t)
+    const float* mine = kReverse ? up - lane : up + lane;  // g^distance at [t] against time, at [-t] in time
+    int head_of_table = -1;
     float log2_decay = 0.0f;
     for (; !kStates && w.more(); w.next(p)) {
-      const Chunk c = Chunk::of<kReverse>(p, w.block);
-      const int64_t head = w.pair % p.heads;
-      if (head != head_of_table) {
-        head_of_table = head;
-        log2_decay = p.log_decay[head] * kLog2e;
+      if (w.head != head_of_table) {
+        head_of_table = w.head;
+        log2_decay = p.log_decay[w.head] * kLog2e;
         __syncwarp();
-        up[lane] = power(log2_decay, lane);
-        down[lane] = power(log2_decay, 31 - lane);
+        up[lane - 32] = 0.0f;
+        up[lane] = p.in_scale * power(log2_decay, lane);
+        back[lane] = p.in_scale * power(log2_decay, 31 - lane);
         __syncwarp();
       }
-      const Marks marks(p, w.pair / p.heads, c);
       // the columns that count: in time lo .. row, against it row .. hi
-      const int lo = kReverse ? row : max(marks.last(row), 0), hi = kReverse ? marks.first(row + 1) - 1 : row;
-      const bool marked = marks.any();
+      int lo = 0, hi = kChunk - 1;
+      bool marked = false;
+      if (p.resets) {
+        const Marks marks(p, w.batch, chunk<kReverse>(p, w.block));
+        marked = marks.any();
+        if (kReverse)
+          hi = marks.first(row + 1) - 1;
+        else
+          lo = max(marks.last(row), 0);
+      }
       ok = mbar_wait(s_full, w.parity(), abort_flag, err, kCode | 2);
       if (!__all_sync(0xffffffffu, ok)) break;
       tc_fence_after();
@@ -391,30 +412,28 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           for (int i = 0; i < 16; ++i) out[i] = 0u;
         } else {
           uint32_t s[32];
-          tmem_ld_32x32b_x32(at + 32 * b, s);
-          tmem_wait_ld();
           float2 x[16];
+          __syncwarp();
+          tmem_ld_32x32b_x32(at + 32 * b, s);
           if (b == q) {
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              const int d0 = kReverse ? 2 * i - lane : lane - 2 * i, d1 = kReverse ? 2 * i + 1 - lane : lane - 2 * i - 1;
-              x[i].x = d0 >= 0 ? up[d0] * p.in_scale * __uint_as_float(s[2 * i]) : 0.0f;
-              x[i].y = d1 >= 0 ? up[d1] * p.in_scale * __uint_as_float(s[2 * i + 1]) : 0.0f;
-            }
+            for (int i = 0; i < 16; ++i)
+              x[i] = make_float2(mine[kReverse ? 2 * i : -2 * i], mine[kReverse ? 2 * i + 1 : -2 * i - 1]);
           } else {
             // in time g^(row - 32 b - 31) g^(31 - t), against it g^(32 b - row) g^t
-            const float f = p.in_scale * power(log2_decay, kReverse ? 32 * b - row : row - 32 * b - 31);
-            const float4* table = reinterpret_cast<const float4*>(kReverse ? up : down);
+            const float f = power(log2_decay, kReverse ? 32 * b - row : row - 32 * b - 31);
+            const float4* table = reinterpret_cast<const float4*>(kReverse ? up : back);
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
               const float4 t = table[i];
-              const float2 f2 = make_float2(f, f);
-              x[2 * i] = __fmul2_rn(make_float2(__uint_as_float(s[4 * i]), __uint_as_float(s[4 * i + 1])),
-                                    __fmul2_rn(make_float2(t.x, t.y), f2));
-              x[2 * i + 1] = __fmul2_rn(make_float2(__uint_as_float(s[4 * i + 2]), __uint_as_float(s[4 * i + 3])),
-                                        __fmul2_rn(make_float2(t.z, t.w), f2));
+              x[2 * i] = __fmul2_rn(make_float2(t.x, t.y), make_float2(f, f));
+              x[2 * i + 1] = __fmul2_rn(make_float2(t.z, t.w), make_float2(f, f));
             }
           }
+          tmem_wait_ld();
+#pragma unroll
+          for (int i = 0; i < 16; ++i)
+            x[i] = __fmul2_rn(x[i], make_float2(__uint_as_float(s[2 * i]), __uint_as_float(s[2 * i + 1])));
           if (marked) {
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
@@ -426,6 +445,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 #pragma unroll
           for (int i = 0; i < 16; ++i) out[i] = pack(x[i].x, x[i].y);
         }
+        __syncwarp();
         tmem_st_x16(at + 16 * b, out);  // over columns that this row's thread has read
       }
       tc2::tmem_wait_st();
@@ -436,36 +456,59 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   } else if (warp >= kWarpK && warp < kWarpS) {
     // -------------------------------------------------------------------- K'
     const int row = 32 * (warp - kWarpK) + lane;
+    // kStates: decayed to the end of the piece, tokens of which those from `edge` on count (against
+    // time those in front of it); the others are cut off by a mark behind them
+    int behind = 0, edge = kReverse ? 0x7FFFFFFF : -1;
+    if (kStates && w.more()) {
+      const Chunk first = chunk<kReverse>(p, w.block), end = chunk<kReverse>(p, w.block + w.left - 1);
+      const int t0 = kReverse ? end.t0 : first.t0, t1 = kReverse ? first.t0 + first.n : end.t0 + end.n;
+      behind = t1 - t0;
+      if (p.resets) {
+        for (int t = t0 + lane; t < t1; t += 32)
+          if (p.resets[w.batch * p.length + t] != 0) edge = kReverse ? min(edge, t) : max(edge, t);
+        edge = kReverse ? __reduce_min_sync(0xffffffffu, edge) : __reduce_max_sync(0xffffffffu, edge);
+      }
+    }
     for (; w.more(); w.next(p)) {
-      const Chunk c = Chunk::of<kReverse>(p, w.block);
-      const Marks marks(p, w.pair / p.heads, c);
-      // whether this token's row is still in the state when the chunk ends
-      const bool alive = row < c.n && (kReverse ? marks.first(0) > row : marks.last(127) <= row);
-      const float f = alive ? p.in_scale * power(p.log_decay[w.pair % p.heads] * kLog2e, kReverse ? row : c.n - 1 - row) : 0.0f;
+      const Chunk c = chunk<kReverse>(p, w.block);
+      // whether this token's row is still in the state in the end, and behind how many tokens
+      bool alive = row < c.n;
+      int away = kReverse ? row : c.n - 1 - row;
+      if (kStates) {
+        behind -= c.n;
+        away += behind;
+        alive = alive && (kReverse ? c.t0 + row < edge : c.t0 + row >= edge);
+      } else if (p.resets) {
+        const Marks marks(p, w.batch, c);
+        alive = alive && (kReverse ? marks.first(0) > row : marks.last(kChunk - 1) <= row);
+      }
+      const float f = alive ? p.in_scale * power(p.log_decay[w.head] * kLog2e, away) : 0.0f;
+      const uint32_t keep = f == 0.0f ? 0u : 0xFFFFFFFFu;  // whatever a row that is cut off holds
+      const float2 f2 = make_float2(f, f);
       const int slot = w.count & 1;
       ok = mbar_wait(&k_full[slot], (w.count >> 1) & 1, abort_flag, err, kCode | 2);
       if (!kStates && ok) ok = mbar_wait(s_full, w.parity(), abort_flag, err, kCode | 2);  // K has been read as it came
-      if (w.count > 0 && ok) ok = mbar_wait(upd_done, w.parity() ^ 1u, abort_flag, err, kCode | 2);
+      if (!kStates && w.count > 0 && ok) ok = mbar_wait(upd_done, w.parity() ^ 1u, abort_flag, err, kCode | 2);
       if (!__all_sync(0xffffffffu, ok)) break;
-      uint8_t* high = smem + L::k + slot * L::tile_k;
-      uint8_t* low = smem + L::k_low;
+      uint8_t* high = smem + L::k + slot * L::tile_k + row * 128;
+      uint8_t* low = smem + (kStates && slot ? L::q : L::k_low) + row * 128;
 #pragma unroll
       for (int h = 0; h < DK / 64; ++h) {
 #pragma unroll 4
         for (int g = 0; g < 8; ++g) {
-          const int o = h * L::half + tc::sw128(row, g);
+          const int o = h * L::half + ((g ^ (row & 7)) << 4);  // the 128-byte swizzle
           const uint4 x = *reinterpret_cast<const uint4*>(high + o);
-          const uint32_t in[4] = {x.x, x.y, x.z, x.w};
+          const uint32_t in[4] = {x.x & keep, x.y & keep, x.z & keep, x.w & keep};
           uint32_t a[4], b[4];
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            float u0, u1, h0, h1;
-            unpack(in[i], u0, u1);
-            u0 = f == 0.0f ? 0.0f : u0 * f;
-            u1 = f == 0.0f ? 0.0f : u1 * f;
-            a[i] = pack(u0, u1);
-            unpack(a[i], h0, h1);
-            b[i] = pack(u0 - h0, u1 - h1);
+            float2 u, t;
+            unpack(in[i], u.x, u.y);
+            u = __fmul2_rn(u, f2);
+            a[i] = pack(u.x, u.y);
+            unpack(a[i], t.x, t.y);
+            u = __ffma2_rn(t, make_float2(-1.0f, -1.0f), u);
+            b[i] = pack(u.x, u.y);
           }
           sts128(high + o, a[0], a[1], a[2], a[3]);
           sts128(low + o, b[0], b[1], b[2], b[3]);
@@ -473,7 +516,17 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       }
       fence_proxy_async_smem();
       __syncwarp();
-      if (lane == 0) mbar_arrive(kp_full);
+      if (lane == 0) mbar_arrive(&kp_full[slot]);
+    }
+    if (kStates && w.count > 0 && threadIdx.x == 32 * kWarpK) {
+      // what a state in front of the piece has left behind it; the first token of a reversed pass takes it whole
+      const bool cut = kReverse ? edge != 0x7FFFFFFF : edge >= 0;
+      const int head = (w.block == 0 ? w.pair - 1 : w.pair) % static_cast<int>(p.heads);
+      const int begun = w.block == 0 ? static_cast<int>(p.blocks) - w.count : w.block - w.count;  // its first block
+      int tokens = 0;
+      for (int i = 0; i < w.count; ++i) tokens += chunk<kReverse>(p, begun + i).n;
+      if (kReverse && begun == 0) --tokens;
+      p.pass[blockIdx.x + 1] = cut ? 0.0f : tokens == 0 ? 1.0f : expf(p.log_decay[head] * static_cast<float>(tokens));
     }
   } else if (warp >= kWarpS && warp < kWarpO) {
     // ------------------------------------------------------------- the state
@@ -481,10 +534,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     const uint32_t at = tmem + (static_cast<uint32_t>(32 * q) << 16) + kColState;
     const bool mine = 32 * q < DK;  // this warp has rows of it
     const int64_t size = static_cast<int64_t>(p.dk) * p.dv;
-    int64_t decays = 0;
-    bool cut_off = false;
     // the state behind a piece, to the caller or to the next part
-    auto put = [&](int64_t pair, float* to, float f) {
+    auto put = [&](float* to, float f) {
       if (!mine) return;
       const bool wide = (reinterpret_cast<uintptr_t>(to) & 15) == 0;  // rows are multiples of 32 bytes
 #pragma unroll 1
@@ -510,36 +561,31 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         }
       }
     };
-    auto ended = [&](int64_t pair) {  // a sequence has
-      if (kStates || !p.last) return;
-      const bool cut = kReverse && p.resets && p.resets[pair / p.heads * p.length] != 0;
-      put(pair, p.last + pair * size, cut ? 0.0f : kReverse ? expf(p.log_decay[pair % p.heads]) : 1.0f);
+    // a sequence has ended, the one in front of the chunk that the walk is at
+    auto ended = [&]() {
+      if (!p.last) return;
+      const int pair = w.pair - 1, batch = pair / static_cast<int>(p.heads), head = pair - batch * static_cast<int>(p.heads);
+      const bool cut = kReverse && p.resets && p.resets[batch * p.length] != 0;
+      put(p.last + pair * size, cut ? 0.0f : kReverse ? expf(p.log_decay[head]) : 1.0f);
     };
-    for (; w.more(); w.next(p)) {
-      const Chunk c = Chunk::of<kReverse>(p, w.block);
-      const Marks marks(p, w.pair / p.heads, c);
-      const float log_decay = p.log_decay[w.pair % p.heads];
-      __syncwarp();
-      const float f = marks.any() ? 0.0f : power(log_decay * kLog2e, c.n - 1 + c.e);
-      decays += c.n - 1 + c.e;
-      cut_off |= marks.any();
+    for (; !kStates && w.more(); w.next(p)) {
+      const Chunk c = chunk<kReverse>(p, w.block);
+      const bool cut = p.resets && Marks(p, w.batch, c).any();
+      const float f = cut ? 0.0f : power(p.log_decay[w.head] * kLog2e, c.n - 1 + c.e);
       if (w.count > 0) {
         ok = mbar_wait(upd_done, w.parity() ^ 1u, abort_flag, err, kCode | 4);
         if (!__all_sync(0xffffffffu, ok)) break;
         tc_fence_after();
-        if (w.block == 0) ended(w.pair - 1);
+        if (w.block == 0) ended();
       }
       const bool fresh = w.block == 0 || w.count == 0;
-      const float* from = nullptr;
-      bool transposed = false;
-      if (fresh && !kStates) {
-        from = w.block > 0 ? p.local + blockIdx.x * size : p.init ? p.init + w.pair * size : nullptr;
-        transposed = w.block == 0 && p.init_transposed;
-      }
+      const bool transposed = w.block == 0 && p.init_transposed;
+      const float* from = w.block > 0 ? p.local + blockIdx.x * size : p.init ? p.init + w.pair * size : nullptr;
       if (mine) {
 #pragma unroll 1
         for (int b = 0; b < DV / 32; ++b) {
           uint32_t s[32];
+          __syncwarp();
           if (fresh) {
 #pragma unroll
             for (int i = 0; i < 32; ++i) {
@@ -549,66 +595,75 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 x = from[transposed ? static_cast<int64_t>(col) * p.dk + row : static_cast<int64_t>(row) * p.dv + col];
               s[i] = __float_as_uint(x);
             }
+            __syncwarp();
           } else {
             tmem_ld_32x32b_x32(at + 32 * b, s);
             tmem_wait_ld();
           }
-          if (!kStates) {
-            uint8_t* to = smem + L::s + (b >> 1) * DK * 128;
+          uint8_t* to = smem + L::s + (b >> 1) * DK * 128;
 #pragma unroll
-            for (int g = 0; g < 4; ++g) {
-              uint32_t o[4];
+          for (int g = 0; g < 4; ++g) {
+            uint32_t o[4];
 #pragma unroll
-              for (int i = 0; i < 4; ++i) o[i] = pack(__uint_as_float(s[8 * g + 2 * i]), __uint_as_float(s[8 * g + 2 * i + 1]));
-              sts128(to + tc::sw128(row, 4 * (b & 1) + g), o[0], o[1], o[2], o[3]);
+            for (int i = 0; i < 4; ++i) o[i] = pack(__uint_as_float(s[8 * g + 2 * i]), __uint_as_float(s[8 * g + 2 * i + 1]));
+            sts128(to + tc::sw128(row, 4 * (b & 1) + g), o[0], o[1], o[2], o[3]);
+          }
+          if (f == 0.0f) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) s[i] = 0u;
+          } else {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              const float2 x = __fmul2_rn(make_float2(__uint_as_float(s[2 * i]), __uint_as_float(s[2 * i + 1])), make_float2(f, f));
+              s[2 * i] = __float_as_uint(x.x);
+              s[2 * i + 1] = __float_as_uint(x.y);
             }
           }
-#pragma unroll
-          for (int i = 0; i < 32; ++i) s[i] = f == 0.0f ? 0u : __float_as_uint(f * __uint_as_float(s[i]));
           __syncwarp();
           tc2::tmem_st_32x32b_x32(at + 32 * b, s);
         }
+        tc2::tmem_wait_st();
       }
-      tc2::tmem_wait_st();
       fence_proxy_async_smem();
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(st_full);
     }
-    if (ok && w.count > 0) {
+    if (kStates && w.more()) {
+      ok = mbar_wait(end_bar, 0, abort_flag, err, kCode | 4);
+      if (__all_sync(0xffffffffu, ok)) {
+        tc_fence_after();
+        put(p.local + (blockIdx.x + 1) * size, 1.0f);
+      }
+    } else if (!kStates && ok && w.count > 0) {
       ok = mbar_wait(upd_done, w.parity() ^ 1u, abort_flag, err, kCode | 4);
       if (__all_sync(0xffffffffu, ok)) {
         tc_fence_after();
-        if (kStates) {
-          put(w.pair, p.local + (blockIdx.x + 1) * size, 1.0f);
-          if (threadIdx.x == 32 * kWarpS) {
-            const float g = p.log_decay[(w.at - 1) / p.blocks % p.heads];
-            p.pass[blockIdx.x + 1] = cut_off ? 0.0f : decays == 0 ? 1.0f : expf(g * static_cast<float>(decays));
-          }
-        } else if (w.block == 0) {
-          ended(w.pair - 1);
-        }
+        if (w.block == 0) ended();
       }
     }
   } else if (warp >= kWarpO) {
     // --------------------------------------------------------------------- o
     const int q = warp - kWarpO, row = 32 * q + lane;
     const uint32_t at = tmem + (static_cast<uint32_t>(32 * q) << 16);
+    const bool wide = ((reinterpret_cast<uintptr_t>(p.o) | (p.ldo * 2) | (p.dv * 2)) & 31) == 0;
     for (; !kStates && w.more(); w.next(p)) {
-      const Chunk c = Chunk::of<kReverse>(p, w.block);
-      const int64_t head = w.pair % p.heads, batch = w.pair / p.heads;
-      const Marks marks(p, batch, c);
+      const Chunk c = chunk<kReverse>(p, w.block);
       // what the state that the chunk begins with has left at this token
-      const bool alive = kReverse ? marks.first(row + 1) >= 128 : marks.last(row) < 0;
       const int pos = kReverse ? c.n - 1 - row : row;
-      const float f = alive && pos >= 0 ? p.out_scale * power(p.log_decay[head] * kLog2e, pos + c.e) : 0.0f;
-      bf16* out = static_cast<bf16*>(p.o) + (batch * p.length + c.t0 + row) * p.ldo + head * p.dv;
+      bool alive = pos >= 0;
+      if (p.resets) {
+        const Marks marks(p, w.batch, c);
+        alive = alive && (kReverse ? marks.first(row + 1) >= kChunk : marks.last(row) < 0);
+      }
+      const float f = alive ? p.out_scale * power(p.log_decay[w.head] * kLog2e, pos + c.e) : 0.0f;
+      bf16* out = static_cast<bf16*>(p.o) + (w.batch * p.length + c.t0 + row) * p.ldo + w.head * p.dv;
       ok = mbar_wait(o_full, w.parity(), abort_flag, err, kCode | 4);
       if (!__all_sync(0xffffffffu, ok)) break;
       tc_fence_after();
 #pragma unroll 1
       for (int b = 0; b < DV / 32; ++b) {
-        uint32_t x[32], y[32];
+        uint32_t x[32], y[32], o[16];
         __syncwarp();
         tmem_ld_32x32b_x32(at + kColPV + 32 * b, x);
         tmem_ld_32x32b_x32(at + kColQS + 32 * b, y);
@@ -619,22 +674,27 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           if (lane == 0) mbar_arrive(o_empty);
         }
 #pragma unroll
-        for (int g = 0; g < 4; ++g) {
-          const int col = 32 * b + 8 * g;
-          if (row >= c.n || col >= p.dv) break;
-          uint32_t o[4];
+        for (int i = 0; i < 16; ++i) {
+          float2 z = __fmul2_rn(make_float2(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1])), make_float2(p.out_scale, p.out_scale));
+          const float2 t = __ffma2_rn(make_float2(__uint_as_float(y[2 * i]), __uint_as_float(y[2 * i + 1])), make_float2(f, f), z);
+          if (f != 0.0f) z = t;  // whatever a state that is cut off holds
+          o[i] = pack(z.x, z.y);
+        }
+        if (row < c.n) {
+          if (wide) {
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int j = 8 * g + 2 * i;
-            float z[2];
+            for (int g = 0; g < 2; ++g)
+              if (32 * b + 16 * g < p.dv)
+                asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(out + 32 * b + 16 * g),
+                             "r"(o[8 * g]), "r"(o[8 * g + 1]), "r"(o[8 * g + 2]), "r"(o[8 * g + 3]), "r"(o[8 * g + 4]),
+                             "r"(o[8 * g + 5]), "r"(o[8 * g + 6]), "r"(o[8 * g + 7])
+                             : "memory");
+          } else {
 #pragma unroll
-            for (int k = 0; k < 2; ++k) {
-              const float s = p.out_scale * __uint_as_float(x[j + k]);
-              z[k] = f == 0.0f ? s : fmaf(f, __uint_as_float(y[j + k]), s);
-            }
-            o[i] = pack(z[0], z[1]);
+            for (int g = 0; g < 4; ++g)
+              if (32 * b + 8 * g < p.dv)
+                *reinterpret_cast<uint4*>(out + 32 * b + 8 * g) = make_uint4(o[4 * g], o[4 * g + 1], o[4 * g + 2], o[4 * g + 3]);
           }
-          *reinterpret_cast<uint4*>(out + col) = make_uint4(o[0], o[1], o[2], o[3]);
         }
       }
     }
