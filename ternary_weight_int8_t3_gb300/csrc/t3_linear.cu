@@ -78,6 +78,9 @@ __global__ void __launch_bounds__(kMaxHead / kRows * 32) linear_tokens_kernel(co
     int64_t pair, b0, b1;
     if (!cut_piece(p, part, pair, b0, b1)) return;
     at = pair * p.blocks + b0;
+  } else if (p.whole > 0) {  // whole sequences: then there are no others
+    at = static_cast<int64_t>(part) * p.whole * p.blocks;
+    end = at + p.whole * p.blocks;
   }
   const bool has_col = col < p.dv;
   float2 S[kRows / 2];
@@ -173,49 +176,61 @@ __global__ void __launch_bounds__(kMaxHead / kRows * 32) linear_tokens_kernel(co
 }
 
 // The states in front of the ranges that begin inside a sequence: what the piece before adds, plus what is left
-// of the state in front of that.  A CTA takes 1024 elements of one sequence's states: it goes with the
-// first range that begins inside the sequence.
+// of the state in front of that.  A CTA takes 256 elements of one sequence's states, and goes with the
+// first range that begins inside the sequence; eight ranges' pieces are on their way at a time.
 __global__ void __launch_bounds__(256) linear_join_kernel(const Args p, int element_blocks) {
-  int j = blockIdx.x / element_blocks + 1;
-  const int size = p.dk * p.dv, e0 = (blockIdx.x - (j - 1) * element_blocks) * 1024 + threadIdx.x;
+  constexpr int kAhead = 8;
+  const int slot = blockIdx.x / element_blocks, size = p.dk * p.dv;
+  const int e = (blockIdx.x - slot * element_blocks) * 256 + threadIdx.x;
+  int j = slot + 1;
   const int64_t begin = part_begin(p, j), pair = begin / p.blocks, first = pair * p.blocks;
   launch_dependents();
+  if (begin == first || part_begin(p, j - 1) > first || e >= size) return;
+  int end = j + 1;
+  while (end < p.ranges && part_begin(p, end) < first + p.blocks) ++end;
   grid_dependency_wait();
-  if (begin == first || part_begin(p, j - 1) > first) return;
-  float x[4];
+  float x = 0.0f;
+  if (p.init) x = p.init[pair * size + (p.init_transposed ? e % p.dv * p.dk + e / p.dv : e)];
+  float* at = p.local + static_cast<int64_t>(j) * size + e;
+  for (; j < end; j += kAhead) {
+    float piece[kAhead], pass[kAhead];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int e = e0 + 256 * i;
-    x[i] = 0.0f;
-    if (p.init && e < size) x[i] = p.init[pair * size + (p.init_transposed ? e % p.dv * p.dk + e / p.dv : e)];
-  }
-  for (; j < p.parts && part_begin(p, j) < first + p.blocks; ++j) {
-    const float pass = p.pass[j];
-    float* at = p.local + static_cast<int64_t>(j) * size;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int e = e0 + 256 * i;
-      if (e < size) {
-        x[i] = pass == 0.0f ? at[e] : fmaf(pass, x[i], at[e]);
-        at[e] = x[i];
-      }
+    for (int i = 0; i < kAhead; ++i) {
+      const bool there = j + i < end;
+      piece[i] = there ? at[static_cast<int64_t>(i) * size] : 0.0f;
+      pass[i] = there ? p.pass[j + i] : 0.0f;
     }
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      x = pass[i] == 0.0f ? piece[i] : fmaf(pass[i], x, piece[i]);
+      if (j + i < end) at[static_cast<int64_t>(i) * size] = x;
+    }
+    at += static_cast<int64_t>(kAhead) * size;
   }
 }
 
 int cut(Args* p, int64_t parts, float* workspace, cudaStream_t s) {
   const int64_t total = p->pairs * p->blocks;
-  auto set = [&](int64_t n) {
-    p->parts = static_cast<int>(n);
-    p->each = total / n;
-    p->rest = total % n;
-    return T3_OK;
-  };
   const bool in_place = p->init && p->last == p->init;
   p->local = p->pass = nullptr;
-  parts = std::min(parts, total);
-  if (p->pairs % parts == 0 || p->blocks == 1) return set(parts);  // they end with sequences
-  if (!workspace || parts > kMaxLinearParts || (in_place && p->pairs >= kMaxLinearParts)) return set(p->pairs);
+  auto deal = [&](int64_t n) {
+    p->parts = static_cast<int>(n);
+    p->whole = static_cast<int>(p->pairs / n);
+    p->first = p->whole * n * p->blocks;
+    const int64_t left = total - p->first;
+    p->ranges = static_cast<int>(std::min(left, n));
+    p->each = left > 0 ? left / p->ranges : 0;
+    p->rest = left > 0 ? left % p->ranges : 0;
+  };
+  deal(std::min(parts, total));
+  if (p->first == total || p->blocks == 1) return T3_OK;  // nothing is cut
+  // tenths of a block's time
+  const int64_t longest = p->each + (p->rest > 0 ? 1 : 0);
+  const bool pays = 10 * p->whole * p->blocks + 16 * longest + 30 < 10 * (p->whole + 1) * p->blocks;
+  if (!workspace || !pays || p->parts > kMaxLinearParts || (in_place && p->pairs >= kMaxLinearParts)) {
+    deal(p->pairs);
+    return T3_OK;
+  }
   const int64_t size = static_cast<int64_t>(p->dk) * p->dv;
   p->local = workspace;
   p->pass = workspace + kMaxLinearParts * size;
@@ -225,12 +240,12 @@ int cut(Args* p, int64_t parts, float* workspace, cudaStream_t s) {
       return T3_ECUDA;
     p->init = copy;
   }
-  return set(parts);
+  return T3_OK;
 }
 
 int launch_join(const Args& p, cudaStream_t s) {
-  const int blocks = (p.dk * p.dv + 1023) / 1024;
-  return launch(linear_join_kernel, static_cast<int64_t>(p.parts - 1) * blocks, 256, 0, s, 1, p, blocks);
+  const int blocks = (p.dk * p.dv + 255) / 256;
+  return launch(linear_join_kernel, static_cast<int64_t>(p.ranges - 1) * blocks, 256, 0, s, 1, p, blocks);
 }
 
 template <class T, bool kReverse>

@@ -11,10 +11,10 @@
 //   dv = (k, q, do)   against time, in_scale scale, out_scale 1, from dstate_last; leaves G_0
 //   dk = (v, do, q)   the same, from dstate_last transposed
 //
-// Parts.  Every sequence and head is `blocks` blocks of tokens in the order they are taken, and all
-// of them together, one after the other, are cut into `parts` equal ranges, one for each CTA (or
-// group of CTAs that share a state's columns), so that few long sequences fill the GPU as many short ones
-// do.  Where a cut falls inside a sequence, a first kernel takes the state that the range in front of the cut
+// Parts.  Every sequence and head is `blocks` blocks of tokens in the order they are taken.  Each of `parts` CTAs
+// (or groups of CTAs that share a state's columns) takes as many whole sequences as there are for all of them; the
+// blocks of the sequences left, one after the other, are cut into equal ranges, one for each, so that few long
+// sequences fill the GPU as many short ones do.  Where a cut falls inside a sequence, a first kernel takes the state that the range in front of the cut
 // adds, a second joins those along the sequence, and the ranges then begin with the state they need.
 #pragma once
 #include <algorithm>
@@ -43,12 +43,17 @@ struct Args {
   int dk, dv;
   int64_t blocks;          // blocks of tokens a sequence
   int parts;
-  int64_t each, rest;      // blocks in all over parts, and what is left
+  int whole;               // sequences a part takes as wholes
+  int64_t first;           // the first block of the others; so many over parts, and what is left of that
+  int64_t each, rest;
+  int ranges;              // parts that have some of them
   float* local;            // [parts][dk * dv]: the state in front of each range that begins inside a sequence
   float* pass;             // [parts]: what is left of a state across the piece in front of such a range
 };
 
-__host__ __device__ __forceinline__ int64_t part_begin(const Args& p, int64_t i) { return p.each * i + p.rest * i / p.parts; }
+__host__ __device__ __forceinline__ int64_t part_begin(const Args& p, int64_t i) {
+  return i >= p.ranges ? p.pairs * p.blocks : p.first + p.each * i + p.rest * i / p.ranges;
+}
 
 // A sequence's first block of the piece that part i computes last, and the end of it; false
 // where the part ends with a sequence.
@@ -60,8 +65,9 @@ __device__ __forceinline__ bool cut_piece(const Args& p, int part, int64_t& pair
   return b1 > 0;
 }
 
-// Sets the ranges: so many, where there is a workspace for their states or they end with sequences anyway;
-// else one for each sequence and head.  A pass that replaces the states it begins with takes a copy of them.
+// Deals the sequences to so many parts at most, cutting those left over into ranges where there is a workspace for
+// their states and it pays: a range's blocks are taken once more for the states, at 0.6 of the time, and
+// two more kernels cost some three blocks' time.  Else a part for each sequence and head.  A pass that replaces the states it begins with takes a copy of them.
 int cut(Args* p, int64_t parts, float* workspace, cudaStream_t s);
 int launch_join(const Args& p, cudaStream_t s);
 

@@ -14,8 +14,8 @@
 // SM's share of the memory's rate; its five products take 1300 of the tensor pipe.  The rest is latency: P
 // waits for Q K^T, the state for the product before.  So every step has warps of its own, handing over through
 // mbarriers, and the two chains have an issuer each; K and V come two chunks ahead and Q one:
-//   warp 0 TMA; warp 1 issues Q K^T and P V, warp 2 Q S and K'^T V; warps 4-7 P; 8-11 K'; 12-15 the state; 16-19 o.
-// Each group's thread owns a TMEM lane: a token's row of P and o, a row of the state (dk), and for K' a
+//   warp 0 TMA; warp 1 issues Q K^T, Q S and P V, warp 2 K'^T V; warps 4-7 P; 8-15 K'; 16-23 the state; 24-27 o.
+// Each group's thread owns a TMEM lane: a token's row of P and o, half a row of the state (dk), and for K' half a
 // token's row in shared memory.  TMEM columns: Q K^T 128, with P over its first 64; P V; Q S; the state.
 //
 // Decays.  A thread of P has one row; in a block of 32 columns next to it the coefficient is a power of its own
@@ -36,9 +36,8 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn();
 namespace lin {
 
 constexpr int kChunk = 128;
-constexpr int kGroup = 4;  // warps of a group
-constexpr int kWarpP = 4, kWarpK = 8, kWarpS = 12, kWarpO = 16;
-constexpr int kTcThreads = 32 * 20;
+constexpr int kWarpP = 4, kWarpK = 8, kWarpS = 16, kWarpO = 24;
+constexpr int kTcThreads = 32 * 28;
 constexpr int kColS = 0, kColPV = 128, kColQS = 256, kColState = 384;  // TMEM columns
 constexpr int kCode = 12 << 8;
 constexpr int kTable = 96;  // floats: 32 zeros, g^0 .. g^31 (times in_scale), and those backwards
@@ -68,23 +67,28 @@ __device__ __forceinline__ uint32_t idesc_bf16(int n, bool a_mn, bool b_mn) {
          (static_cast<uint32_t>(n >> 3) << 17) | (128u >> 4 << 24);
 }
 
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t add) {
+// Issued by the thread whose `lead` is set; the whole warp comes here, so that descriptors stay in uniform
+// registers (issued from a branch of one thread, a product took 110 clocks instead of the tensor pipe's 64).
+__device__ __forceinline__ void mma_ss(uint32_t lead, uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t add) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"(add)
+      "{\n\t.reg .pred p, l;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 l, %5, 0;\n\t"
+      "@l tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(add), "r"(lead)
       : "memory");
 }
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t add) {
+__device__ __forceinline__ void mma_ts(uint32_t lead, uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t add) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-      "r"(a), "l"(b), "r"(idesc), "r"(add)
+      "{\n\t.reg .pred p, l;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 l, %5, 0;\n\t"
+      "@l tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"(add), "r"(lead)
       : "memory");
 }
-__device__ __forceinline__ void mma_commit(uint64_t* bar) {
-  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_addr(bar))
-               : "memory");
+__device__ __forceinline__ void mma_commit(uint32_t lead, uint64_t* bar) {
+  asm volatile(
+      "{\n\t.reg .pred l;\n\tsetp.ne.b32 l, %1, 0;\n\t"
+      "@l tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_addr(bar)),
+      "r"(lead)
+      : "memory");
 }
 
 __device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* map, uint64_t* bar, int x, int head, int token,
@@ -96,6 +100,12 @@ __device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* map, u
       : "memory");
 }
 
+__device__ __forceinline__ void tmem_st_x8(uint32_t taddr, const uint32_t (&v)[8]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr), "r"(v[0]),
+               "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+               : "memory");
+}
+
 __device__ __forceinline__ void tmem_st_x16(uint32_t taddr, const uint32_t (&v)[16]) {
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
@@ -105,21 +115,33 @@ __device__ __forceinline__ void tmem_st_x16(uint32_t taddr, const uint32_t (&v)[
       : "memory");
 }
 
+// The loads so far are in; what was loaded cannot be used in front of this.
+__device__ __forceinline__ void loaded(uint32_t (&v)[16]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(v[0]), "+r"(v[1]), "+r"(v[2]), "+r"(v[3]), "+r"(v[4]), "+r"(v[5]), "+r"(v[6]), "+r"(v[7]), "+r"(v[8]),
+                 "+r"(v[9]), "+r"(v[10]), "+r"(v[11]), "+r"(v[12]), "+r"(v[13]), "+r"(v[14]), "+r"(v[15])::"memory");
+}
+
 // g^n from log2 g, 1 for n = 0 whatever g.
 __device__ __forceinline__ float power(float log2_decay, int n) {
   return n == 0 ? 1.0f : exp2f(log2_decay * static_cast<float>(n));
 }
 
-// A CTA's chunks, in the order they are taken.  Every role walks the same ones.
+// A CTA's chunks, in the order they are taken: those of its whole sequences, then those of its range of the
+// others.  Every role walks the same ones.
 struct Walk {
   int left;              // chunks still to take
+  int turn = -1;         // of which so many are of the second kind, which begins at
+  int64_t then = 0;      // this block
   int count = 0;         // and taken
   int pair, head, batch;
   int block;             // in the sequence
   __device__ __forceinline__ void next(const Args& p) {
     --left;
     ++count;
-    if (++block == static_cast<int>(p.blocks)) {
+    if (left == turn) {
+      go(p, then);
+    } else if (++block == static_cast<int>(p.blocks)) {
       block = 0;
       ++pair;
       if (++head == static_cast<int>(p.heads)) {
@@ -128,6 +150,13 @@ struct Walk {
       }
     }
   }
+  // to a block among those of all sequences
+  __device__ __forceinline__ void go(const Args& p, int64_t at) {
+    pair = static_cast<int>(at / p.blocks);
+    block = static_cast<int>(at - pair * p.blocks);
+    batch = pair / static_cast<int>(p.heads);
+    head = pair - batch * static_cast<int>(p.heads);
+  }
   __device__ __forceinline__ bool more() const { return left > 0; }
   __device__ __forceinline__ uint32_t parity() const { return count & 1; }
 };
@@ -135,20 +164,19 @@ struct Walk {
 template <bool kStates>
 __device__ __forceinline__ Walk walk(const Args& p) {
   Walk w;
-  int64_t pair, b0, b1;
+  int64_t at = 0;
   if (kStates) {
+    int64_t pair, b0, b1;
     w.left = cut_piece(p, blockIdx.x, pair, b0, b1) ? static_cast<int>(b1 - b0) : 0;
+    if (w.left > 0) at = pair * p.blocks + b0;
   } else {
-    const int64_t at = part_begin(p, blockIdx.x);
-    w.left = static_cast<int>(part_begin(p, blockIdx.x + 1) - at);
-    pair = at / p.blocks;
-    b0 = at - pair * p.blocks;
+    w.then = part_begin(p, blockIdx.x);
+    w.turn = static_cast<int>(part_begin(p, blockIdx.x + 1) - w.then);
+    w.left = p.whole * static_cast<int>(p.blocks) + w.turn;
+    at = p.whole > 0 ? static_cast<int64_t>(blockIdx.x) * p.whole * p.blocks : w.then;
+    if (w.turn == 0 || p.whole == 0) w.turn = -1;
   }
-  if (w.left == 0) pair = b0 = 0;
-  w.pair = static_cast<int>(pair);
-  w.block = static_cast<int>(b0);
-  w.batch = w.pair / static_cast<int>(p.heads);
-  w.head = w.pair - w.batch * static_cast<int>(p.heads);
+  w.go(p, w.left > 0 ? at : 0);
   return w;
 }
 
@@ -209,17 +237,19 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   uint8_t* smem = smem_raw + (((smem_addr(smem_raw) + 1023u) & ~1023u) - smem_addr(smem_raw));
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::bars);
   uint64_t *q_full = bars, *k_full = bars + 1, *v_full = bars + 3, *k_empty = bars + 5, *s_full = bars + 7,
-           *pv_done = bars + 8, *upd_done = bars + 9, *end_bar = bars + 10;  // one arrival each
-  uint64_t *q_empty = bars + 11, *v_empty = bars + 12, *o_full = bars + 14;  // both issuers
-  uint64_t *p_full = bars + 15, *kp_full = bars + 16, *st_full = bars + 18, *o_empty = bars + 19;  // a group's warps
-  uint64_t* drain = bars + 20;  // one for each issuer
+           *pv_done = bars + 8, *upd_done = bars + 9, *end_bar = bars + 10, *q_empty = bars + 11,
+           *o_full = bars + 12;                                           // one arrival each
+  uint64_t* v_empty = bars + 13;                                          // both issuers
+  uint64_t *p_full = bars + 15, *o_empty = bars + 16;                     // a group's four warps
+  uint64_t *kp_full = bars + 17, *st_full = bars + 19;                    // or eight
+  uint64_t* drain = bars + 20;                                            // one for each issuer
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(smem + L::misc);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::misc + 4);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < L::n_bars; ++i)
-      mbar_init(bars + i, i < 11 ? 1 : i < 15 ? (kStates ? 1 : 2) : i < 20 ? kGroup : 1);
+      mbar_init(bars + i, i < 13 ? 1 : i < 15 ? (kStates ? 1 : 2) : i < 17 ? 4 : i < 20 ? 8 : 1);
     *abort_flag = 0;
     fence_mbarrier_init();
   }
@@ -283,91 +313,87 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     __syncwarp();
   } else if (warp == 1 || warp == 2) {
     // ------------------------------------------------------------- products
-    if (lane == 0) {
-      const uint32_t base = smem_addr(smem);
-      const uint64_t q_rows = smem_desc_k_sw128(base + L::q), k_rows = smem_desc_k_sw128(base + L::k);
-      const uint64_t k_cols = smem_desc_mn_sw128(base + L::k, L::half, 1024), v_cols = smem_desc_mn_sw128(base + L::v, L::half, 1024);
-      const uint64_t low_cols = smem_desc_mn_sw128(base + L::k_low, L::half, 1024);
-      const uint64_t q_as_low = smem_desc_mn_sw128(base + L::q, L::half, 1024);
-      const uint64_t s_cols = smem_desc_mn_sw128(base + L::s, DK * 128, 1024);
-      // step j of 16 along a product's sum: rows of 128 bytes hold 64 of it, 32 bytes a step; columns
-      // go on by two groups of eight rows
-      auto along = [](int j) { return static_cast<uint64_t>((j >> 2) * L::half + 32 * (j & 3)) >> 4; };
-      auto down = [](int j) { return static_cast<uint64_t>(2048 * j) >> 4; };
-      bool issued = false;
-      for (; ok && w.more(); w.next(p)) {
-        const int slot = w.count & 1;
-        const uint32_t par = w.parity(), par2 = (w.count >> 1) & 1;
-        const uint64_t k_at = static_cast<uint64_t>(slot * L::tile_k) >> 4, v_at = static_cast<uint64_t>(slot * L::tile_v) >> 4;
-        if (warp == 1) {
-          if (kStates) break;
-          // Q K^T, over the columns that the product before reads P from, and not before the warps of K' have seen
-          // that one's end: a barrier that moves on twice is missed
-          if (w.count > 0) {
-            ok = mbar_wait(pv_done, par ^ 1u, abort_flag, err, kCode | 3) &&
-                 mbar_wait(&kp_full[slot ^ 1], ((w.count - 1) >> 1) & 1, abort_flag, err, kCode | 3);
-          }
-          ok = ok && mbar_wait(q_full, par, abort_flag, err, kCode | 3);
-          ok = ok && mbar_wait(&k_full[slot], par2, abort_flag, err, kCode | 3);
-          if (!ok) break;
-          tc_fence_after();
-#pragma unroll
-          for (int j = 0; j < DK / 16; ++j)
-            mma_ss(tmem + kColS, q_rows + along(j), k_rows + k_at + along(j), idesc_bf16(128, false, false), j > 0);
-          issued = true;
-          mma_commit(s_full);
-          mma_commit(q_empty);
-          // P V
-          ok = mbar_wait(&v_full[slot], par2, abort_flag, err, kCode | 3);
-          ok = ok && (w.count == 0 || mbar_wait(o_empty, par ^ 1u, abort_flag, err, kCode | 3));
-          ok = ok && mbar_wait(p_full, par, abort_flag, err, kCode | 3);
-          if (!ok) break;
-          tc_fence_after();
-#pragma unroll
-          for (int j = 0; j < kChunk / 16; ++j)
-            mma_ts(tmem + kColPV, tmem + kColS + 8 * j, v_cols + v_at + down(j), idesc_bf16(DV, false, true), j > 0);
-          mma_commit(pv_done);
-          mma_commit(o_full);
-          mma_commit(&v_empty[slot]);
-        } else {
-          if (!kStates) {
-            // Q S
-            ok = mbar_wait(q_full, par, abort_flag, err, kCode | 3);
-            ok = ok && (w.count == 0 || mbar_wait(o_empty, par ^ 1u, abort_flag, err, kCode | 3));
-            ok = ok && mbar_wait(st_full, par, abort_flag, err, kCode | 3);
-            if (!ok) break;
-            tc_fence_after();
-#pragma unroll
-            for (int j = 0; j < DK / 16; ++j)
-              mma_ss(tmem + kColQS, q_rows + along(j), s_cols + down(j), idesc_bf16(DV, false, true), j > 0);
-            issued = true;
-            mma_commit(q_empty);
-            mma_commit(o_full);
-          }
-          // S += K'^T V
-          ok = mbar_wait(&v_full[slot], par2, abort_flag, err, kCode | 3);
-          ok = ok && mbar_wait(&kp_full[slot], par2, abort_flag, err, kCode | 3);
-          if (!ok) break;
-          tc_fence_after();
-          const uint64_t low = kStates && slot ? q_as_low : low_cols;
-#pragma unroll
-          for (int j = 0; j < kChunk / 16; ++j) {
-            mma_ss(tmem + kColState, k_cols + k_at + down(j), v_cols + v_at + down(j), idesc_bf16(DV, true, true),
-                   !kStates || j > 0 || w.count > 0);
-            mma_ss(tmem + kColState, low + down(j), v_cols + v_at + down(j), idesc_bf16(DV, true, true), 1u);
-          }
-          issued = true;
-          if (!kStates) mma_commit(upd_done);
-          mma_commit(&k_empty[slot]);
-          mma_commit(&v_empty[slot]);
+    const uint32_t lead = lane == 0;
+    const uint32_t base = smem_addr(smem);
+    const uint64_t q_rows = smem_desc_k_sw128(base + L::q), k_rows = smem_desc_k_sw128(base + L::k);
+    const uint64_t k_cols = smem_desc_mn_sw128(base + L::k, L::half, 1024), v_cols = smem_desc_mn_sw128(base + L::v, L::half, 1024);
+    const uint64_t low_cols = smem_desc_mn_sw128(base + L::k_low, L::half, 1024);
+    const uint64_t q_as_low = smem_desc_mn_sw128(base + L::q, L::half, 1024);
+    const uint64_t s_cols = smem_desc_mn_sw128(base + L::s, DK * 128, 1024);
+    // step j of 16 along a product's sum: rows of 128 bytes hold 64 of it, 32 bytes a step; columns
+    // go on by two groups of eight rows
+    auto along = [](int j) { return static_cast<uint64_t>((j >> 2) * L::half + 32 * (j & 3)) >> 4; };
+    auto down = [](int j) { return static_cast<uint64_t>(2048 * j) >> 4; };
+    bool issued = false;
+    auto seen = [&](uint64_t* bar, uint32_t parity) {
+      ok = ok && mbar_wait(bar, parity, abort_flag, err, kCode | 3);
+    };
+    for (; w.more(); w.next(p)) {
+      const int slot = w.count & 1;
+      const uint32_t par = w.parity(), par2 = (w.count >> 1) & 1;
+      const uint64_t k_at = static_cast<uint64_t>(slot * L::tile_k) >> 4, v_at = static_cast<uint64_t>(slot * L::tile_v) >> 4;
+      if (warp == 1) {
+        if (kStates) break;
+        // Q K^T, over the columns that the product before reads P from, and not before the warps of K' have seen
+        // that one's end: a barrier that moves on twice is missed
+        if (w.count > 0) {
+          seen(pv_done, par ^ 1u);
+          seen(&kp_full[slot ^ 1], ((w.count - 1) >> 1) & 1);
         }
+        seen(q_full, par);
+        seen(&k_full[slot], par2);
+        if (!__all_sync(0xffffffffu, ok)) break;
+        tc_fence_after();
+#pragma unroll
+        for (int j = 0; j < DK / 16; ++j)
+          mma_ss(lead, tmem + kColS, q_rows + along(j), k_rows + k_at + along(j), idesc_bf16(128, false, false), j > 0);
+        issued = true;
+        mma_commit(lead, s_full);
+        // Q S
+        if (w.count > 0) seen(o_empty, par ^ 1u);
+        seen(st_full, par);
+        if (!__all_sync(0xffffffffu, ok)) break;
+        tc_fence_after();
+#pragma unroll
+        for (int j = 0; j < DK / 16; ++j)
+          mma_ss(lead, tmem + kColQS, q_rows + along(j), s_cols + down(j), idesc_bf16(DV, false, true), j > 0);
+        mma_commit(lead, q_empty);
+        // P V
+        seen(&v_full[slot], par2);
+        seen(p_full, par);
+        if (!__all_sync(0xffffffffu, ok)) break;
+        tc_fence_after();
+#pragma unroll
+        for (int j = 0; j < kChunk / 16; ++j)
+          mma_ts(lead, tmem + kColPV, tmem + kColS + 8 * j, v_cols + v_at + down(j), idesc_bf16(DV, false, true), j > 0);
+        mma_commit(lead, pv_done);
+        mma_commit(lead, o_full);
+        mma_commit(lead, &v_empty[slot]);
+      } else {
+        // S += K'^T V
+        if (!kStates) seen(st_full, par);
+        seen(&v_full[slot], par2);
+        seen(&kp_full[slot], par2);
+        if (!__all_sync(0xffffffffu, ok)) break;
+        tc_fence_after();
+        const uint64_t low = kStates && slot ? q_as_low : low_cols;
+#pragma unroll
+        for (int j = 0; j < kChunk / 16; ++j) {
+          mma_ss(lead, tmem + kColState, k_cols + k_at + down(j), v_cols + v_at + down(j), idesc_bf16(DV, true, true),
+                 !kStates || j > 0 || w.count > 0);
+          mma_ss(lead, tmem + kColState, low + down(j), v_cols + v_at + down(j), idesc_bf16(DV, true, true), 1u);
+        }
+        issued = true;
+        if (!kStates) mma_commit(lead, upd_done);
+        mma_commit(lead, &k_empty[slot]);
+        mma_commit(lead, &v_empty[slot]);
       }
-      if (kStates && warp == 2 && ok && issued) mma_commit(end_bar);
-      if (!ok && issued) {  // the products in flight end before their operands go
-        mma_commit(drain + warp - 1);
-        const uint64_t t = global_timer_ns();
-        while (!mbar_try_wait(drain + warp - 1, 0) && global_timer_ns() - t < kWaitLimitNs) {
-        }
+    }
+    if (kStates && warp == 2 && ok && issued) mma_commit(lead, end_bar);
+    if (!__all_sync(0xffffffffu, ok) && issued && lead) {  // the products in flight end before their operands go
+      mma_commit(1u, drain + warp - 1);
+      const uint64_t t = global_timer_ns();
+      while (!mbar_try_wait(drain + warp - 1, 0) && global_timer_ns() - t < kWaitLimitNs) {
       }
     }
     __syncwarp();
@@ -404,50 +430,52 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       ok = mbar_wait(s_full, w.parity(), abort_flag, err, kCode | 2);
       if (!__all_sync(0xffffffffu, ok)) break;
       tc_fence_after();
+      // 16 columns at a time: units 0 .. 2 q + 1 in time, 2 q .. 7 against it; the next one's on their way
+      const int u0 = kReverse ? 2 * q : 0, u1 = kReverse ? 8 : 2 * q + 2;
+      uint32_t s[16];
+      tmem_ld_32x32b_x16(at + 16 * u0, s);
 #pragma unroll 1
-      for (int b = 0; b < 4; ++b) {
-        uint32_t out[16];
-        if (kReverse ? b < q : b > q) {
+      for (int u = u0; u < u1; ++u) {
+        const int b = u >> 1;
+        float2 x[8];
+        if (b == q) {
+          const float* m = mine + (kReverse ? 16 : -16) * (u & 1);
 #pragma unroll
-          for (int i = 0; i < 16; ++i) out[i] = 0u;
+          for (int i = 0; i < 8; ++i) x[i] = make_float2(m[kReverse ? 2 * i : -2 * i], m[kReverse ? 2 * i + 1 : -2 * i - 1]);
         } else {
-          uint32_t s[32];
-          float2 x[16];
-          __syncwarp();
-          tmem_ld_32x32b_x32(at + 32 * b, s);
-          if (b == q) {
+          // in time g^(row - 32 b - 31) g^(31 - t), against it g^(32 b - row) g^t
+          const float f = power(log2_decay, kReverse ? 32 * b - row : row - 32 * b - 31);
+          const float4* table = reinterpret_cast<const float4*>((kReverse ? up : back) + 16 * (u & 1));
 #pragma unroll
-            for (int i = 0; i < 16; ++i)
-              x[i] = make_float2(mine[kReverse ? 2 * i : -2 * i], mine[kReverse ? 2 * i + 1 : -2 * i - 1]);
-          } else {
-            // in time g^(row - 32 b - 31) g^(31 - t), against it g^(32 b - row) g^t
-            const float f = power(log2_decay, kReverse ? 32 * b - row : row - 32 * b - 31);
-            const float4* table = reinterpret_cast<const float4*>(kReverse ? up : back);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              const float4 t = table[i];
-              x[2 * i] = __fmul2_rn(make_float2(t.x, t.y), make_float2(f, f));
-              x[2 * i + 1] = __fmul2_rn(make_float2(t.z, t.w), make_float2(f, f));
-            }
+          for (int i = 0; i < 4; ++i) {
+            const float4 t = table[i];
+            x[2 * i] = __fmul2_rn(make_float2(t.x, t.y), make_float2(f, f));
+            x[2 * i + 1] = __fmul2_rn(make_float2(t.z, t.w), make_float2(f, f));
           }
-          tmem_wait_ld();
-#pragma unroll
-          for (int i = 0; i < 16; ++i)
-            x[i] = __fmul2_rn(x[i], make_float2(__uint_as_float(s[2 * i]), __uint_as_float(s[2 * i + 1])));
-          if (marked) {
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              const int j = 32 * b + 2 * i;
-              if (j < lo || j > hi) x[i].x = 0.0f;
-              if (j + 1 < lo || j + 1 > hi) x[i].y = 0.0f;
-            }
-          }
-#pragma unroll
-          for (int i = 0; i < 16; ++i) out[i] = pack(x[i].x, x[i].y);
         }
+        loaded(s);
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          x[i] = __fmul2_rn(x[i], make_float2(__uint_as_float(s[2 * i]), __uint_as_float(s[2 * i + 1])));
         __syncwarp();
-        tmem_st_x16(at + 16 * b, out);  // over columns that this row's thread has read
+        if (u + 1 < u1) tmem_ld_32x32b_x16(at + 16 * (u + 1), s);
+        if (marked) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const int j = 16 * u + 2 * i;
+            if (j < lo || j > hi) x[i].x = 0.0f;
+            if (j + 1 < lo || j + 1 > hi) x[i].y = 0.0f;
+          }
+        }
+        uint32_t out[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) out[i] = pack(x[i].x, x[i].y);
+        __syncwarp();
+        tmem_st_x8(at + 8 * u, out);  // over columns that this row's thread has read
       }
+      const uint32_t none[8] = {};
+      for (int u = 0; u < 8; ++u)
+        if (u < u0 || u >= u1) tmem_st_x8(at + 8 * u, none);
       tc2::tmem_wait_st();
       tc_fence_before();
       __syncwarp();
@@ -455,7 +483,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     }
   } else if (warp >= kWarpK && warp < kWarpS) {
     // -------------------------------------------------------------------- K'
-    const int row = 32 * (warp - kWarpK) + lane;
+    const int row = 32 * (warp & 3) + lane, part = (warp - kWarpK) >> 2;  // half of the row's 16-byte pieces
     // kStates: decayed to the end of the piece, tokens of which those from `edge` on count (against
     // time those in front of it); the others are cut off by a mark behind them
     int behind = 0, edge = kReverse ? 0x7FFFFFFF : -1;
@@ -492,27 +520,25 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       if (!__all_sync(0xffffffffu, ok)) break;
       uint8_t* high = smem + L::k + slot * L::tile_k + row * 128;
       uint8_t* low = smem + (kStates && slot ? L::q : L::k_low) + row * 128;
-#pragma unroll
-      for (int h = 0; h < DK / 64; ++h) {
 #pragma unroll 4
-        for (int g = 0; g < 8; ++g) {
-          const int o = h * L::half + ((g ^ (row & 7)) << 4);  // the 128-byte swizzle
-          const uint4 x = *reinterpret_cast<const uint4*>(high + o);
-          const uint32_t in[4] = {x.x & keep, x.y & keep, x.z & keep, x.w & keep};
-          uint32_t a[4], b[4];
+      for (int i0 = 0; i0 < DK / 16; ++i0) {
+        const int g = part * (DK / 16) + i0;
+        const int o = (g >> 3) * L::half + (((g ^ row) & 7) << 4);  // the 128-byte swizzle
+        const uint4 x = *reinterpret_cast<const uint4*>(high + o);
+        const uint32_t in[4] = {x.x & keep, x.y & keep, x.z & keep, x.w & keep};
+        uint32_t a[4], b[4];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            float2 u, t;
-            unpack(in[i], u.x, u.y);
-            u = __fmul2_rn(u, f2);
-            a[i] = pack(u.x, u.y);
-            unpack(a[i], t.x, t.y);
-            u = __ffma2_rn(t, make_float2(-1.0f, -1.0f), u);
-            b[i] = pack(u.x, u.y);
-          }
-          sts128(high + o, a[0], a[1], a[2], a[3]);
-          sts128(low + o, b[0], b[1], b[2], b[3]);
+        for (int i = 0; i < 4; ++i) {
+          float2 u, t;
+          unpack(in[i], u.x, u.y);
+          u = __fmul2_rn(u, f2);
+          a[i] = pack(u.x, u.y);
+          unpack(a[i], t.x, t.y);
+          u = __ffma2_rn(t, make_float2(-1.0f, -1.0f), u);
+          b[i] = pack(u.x, u.y);
         }
+        sts128(high + o, a[0], a[1], a[2], a[3]);
+        sts128(low + o, b[0], b[1], b[2], b[3]);
       }
       fence_proxy_async_smem();
       __syncwarp();
@@ -521,17 +547,17 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     if (kStates && w.count > 0 && threadIdx.x == 32 * kWarpK) {
       // what a state in front of the piece has left behind it; the first token of a reversed pass takes it whole
       const bool cut = kReverse ? edge != 0x7FFFFFFF : edge >= 0;
-      const int head = (w.block == 0 ? w.pair - 1 : w.pair) % static_cast<int>(p.heads);
-      const int begun = w.block == 0 ? static_cast<int>(p.blocks) - w.count : w.block - w.count;  // its first block
+      const int begun = w.block - w.count;  // its first block: the piece ends inside the sequence
       int tokens = 0;
       for (int i = 0; i < w.count; ++i) tokens += chunk<kReverse>(p, begun + i).n;
       if (kReverse && begun == 0) --tokens;
-      p.pass[blockIdx.x + 1] = cut ? 0.0f : tokens == 0 ? 1.0f : expf(p.log_decay[head] * static_cast<float>(tokens));
+      p.pass[blockIdx.x + 1] = cut ? 0.0f : tokens == 0 ? 1.0f : expf(p.log_decay[w.head] * static_cast<float>(tokens));
     }
   } else if (warp >= kWarpS && warp < kWarpO) {
     // ------------------------------------------------------------- the state
-    const int q = warp - kWarpS, row = 32 * q + lane;
-    const uint32_t at = tmem + (static_cast<uint32_t>(32 * q) << 16) + kColState;
+    const int q = warp & 3, row = 32 * q + lane;
+    const int col0 = ((warp - kWarpS) >> 2) * (DV / 2);  // half of the columns
+    const uint32_t at = tmem + (static_cast<uint32_t>(32 * q) << 16) + kColState + col0;
     const bool mine = 32 * q < DK;  // this warp has rows of it
     const int64_t size = static_cast<int64_t>(p.dk) * p.dv;
     // the state behind a piece, to the caller or to the next part
@@ -540,13 +566,13 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       const bool wide = (reinterpret_cast<uintptr_t>(to) & 15) == 0;  // rows are multiples of 32 bytes
 #pragma unroll 1
       for (int b = 0; b < DV / 32; ++b) {
-        uint32_t s[32];
+        uint32_t s[16];
         __syncwarp();
-        tmem_ld_32x32b_x32(at + 32 * b, s);
-        tmem_wait_ld();
+        tmem_ld_32x32b_x16(at + 16 * b, s);
+        loaded(s);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const int col = 32 * b + 4 * i;
+        for (int i = 0; i < 4; ++i) {
+          const int col = col0 + 16 * b + 4 * i;
           if (row >= p.dk || col >= p.dv) break;
           float x[4];
 #pragma unroll
@@ -561,10 +587,13 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         }
       }
     };
-    // a sequence has ended, the one in front of the chunk that the walk is at
+    // the sequence that the chunk before was the last of has ended
+    int last_pair = -1;
     auto ended = [&]() {
-      if (!p.last) return;
-      const int pair = w.pair - 1, batch = pair / static_cast<int>(p.heads), head = pair - batch * static_cast<int>(p.heads);
+      const int pair = last_pair;
+      last_pair = -1;
+      if (pair < 0 || !p.last) return;
+      const int batch = pair / static_cast<int>(p.heads), head = pair - batch * static_cast<int>(p.heads);
       const bool cut = kReverse && p.resets && p.resets[batch * p.length] != 0;
       put(p.last + pair * size, cut ? 0.0f : kReverse ? expf(p.log_decay[head]) : 1.0f);
     };
@@ -576,51 +605,58 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         ok = mbar_wait(upd_done, w.parity() ^ 1u, abort_flag, err, kCode | 4);
         if (!__all_sync(0xffffffffu, ok)) break;
         tc_fence_after();
-        if (w.block == 0) ended();
+        ended();
       }
-      const bool fresh = w.block == 0 || w.count == 0;
+      const bool fresh = w.block == 0 || w.count == 0 || w.left == w.turn;
+      if (w.block + 1 == static_cast<int>(p.blocks)) last_pair = w.pair;
       const bool transposed = w.block == 0 && p.init_transposed;
       const float* from = w.block > 0 ? p.local + blockIdx.x * size : p.init ? p.init + w.pair * size : nullptr;
       if (mine) {
 #pragma unroll 1
         for (int b = 0; b < DV / 32; ++b) {
-          uint32_t s[32];
+          const int col = col0 + 16 * b;
+          uint32_t s[16];
           __syncwarp();
           if (fresh) {
+            const bool wide = !transposed && (reinterpret_cast<uintptr_t>(from) & 15) == 0;
 #pragma unroll
-            for (int i = 0; i < 32; ++i) {
-              const int col = 32 * b + i;
-              float x = 0.0f;
-              if (from && row < p.dk && col < p.dv)
-                x = from[transposed ? static_cast<int64_t>(col) * p.dk + row : static_cast<int64_t>(row) * p.dv + col];
-              s[i] = __float_as_uint(x);
+            for (int i = 0; i < 4; ++i) {
+              float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+              const int c4 = col + 4 * i;
+              if (from && row < p.dk && c4 < p.dv) {
+                const int step = transposed ? p.dk : 1;
+                const float* f4 = from + (transposed ? c4 * p.dk + row : row * p.dv + c4);
+                if (wide)
+                  x = *reinterpret_cast<const float4*>(f4);
+                else
+                  x = make_float4(f4[0], f4[step], f4[2 * step], f4[3 * step]);
+              }
+              s[4 * i] = __float_as_uint(x.x);
+              s[4 * i + 1] = __float_as_uint(x.y);
+              s[4 * i + 2] = __float_as_uint(x.z);
+              s[4 * i + 3] = __float_as_uint(x.w);
             }
             __syncwarp();
           } else {
-            tmem_ld_32x32b_x32(at + 32 * b, s);
-            tmem_wait_ld();
+            tmem_ld_32x32b_x16(at + 16 * b, s);
+            loaded(s);
           }
-          uint8_t* to = smem + L::s + (b >> 1) * DK * 128;
+          uint8_t* to = smem + L::s + (col >> 6) * DK * 128;
 #pragma unroll
-          for (int g = 0; g < 4; ++g) {
+          for (int g = 0; g < 2; ++g) {
             uint32_t o[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) o[i] = pack(__uint_as_float(s[8 * g + 2 * i]), __uint_as_float(s[8 * g + 2 * i + 1]));
-            sts128(to + tc::sw128(row, 4 * (b & 1) + g), o[0], o[1], o[2], o[3]);
+            sts128(to + tc::sw128(row, (col >> 3 & 7) + g), o[0], o[1], o[2], o[3]);
           }
-          if (f == 0.0f) {
 #pragma unroll
-            for (int i = 0; i < 32; ++i) s[i] = 0u;
-          } else {
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              const float2 x = __fmul2_rn(make_float2(__uint_as_float(s[2 * i]), __uint_as_float(s[2 * i + 1])), make_float2(f, f));
-              s[2 * i] = __float_as_uint(x.x);
-              s[2 * i + 1] = __float_as_uint(x.y);
-            }
+          for (int i = 0; i < 8; ++i) {
+            const float2 x = __fmul2_rn(make_float2(__uint_as_float(s[2 * i]), __uint_as_float(s[2 * i + 1])), make_float2(f, f));
+            s[2 * i] = f == 0.0f ? 0u : __float_as_uint(x.x);
+            s[2 * i + 1] = f == 0.0f ? 0u : __float_as_uint(x.y);
           }
           __syncwarp();
-          tc2::tmem_st_32x32b_x32(at + 32 * b, s);
+          tmem_st_x16(at + 16 * b, s);
         }
         tc2::tmem_wait_st();
       }
@@ -639,7 +675,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       ok = mbar_wait(upd_done, w.parity() ^ 1u, abort_flag, err, kCode | 4);
       if (__all_sync(0xffffffffu, ok)) {
         tc_fence_after();
-        if (w.block == 0) ended();
+        ended();
       }
     }
   } else if (warp >= kWarpO) {
@@ -662,38 +698,33 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       if (!__all_sync(0xffffffffu, ok)) break;
       tc_fence_after();
 #pragma unroll 1
-      for (int b = 0; b < DV / 32; ++b) {
-        uint32_t x[32], y[32], o[16];
+      for (int b = 0; b < DV / 16; ++b) {
+        uint32_t x[16], y[16], o[8];
         __syncwarp();
-        tmem_ld_32x32b_x32(at + kColPV + 32 * b, x);
-        tmem_ld_32x32b_x32(at + kColQS + 32 * b, y);
-        tmem_wait_ld();
-        if (b + 1 == DV / 32) {
+        tmem_ld_32x32b_x16(at + kColPV + 16 * b, x);
+        tmem_ld_32x32b_x16(at + kColQS + 16 * b, y);
+        loaded(x);
+        loaded(y);
+        if (b + 1 == DV / 16) {
           tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive(o_empty);
         }
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
+        for (int i = 0; i < 8; ++i) {
           float2 z = __fmul2_rn(make_float2(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1])), make_float2(p.out_scale, p.out_scale));
           const float2 t = __ffma2_rn(make_float2(__uint_as_float(y[2 * i]), __uint_as_float(y[2 * i + 1])), make_float2(f, f), z);
           if (f != 0.0f) z = t;  // whatever a state that is cut off holds
           o[i] = pack(z.x, z.y);
         }
-        if (row < c.n) {
+        if (row < c.n && 16 * b < p.dv) {
           if (wide) {
-#pragma unroll
-            for (int g = 0; g < 2; ++g)
-              if (32 * b + 16 * g < p.dv)
-                asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(out + 32 * b + 16 * g),
-                             "r"(o[8 * g]), "r"(o[8 * g + 1]), "r"(o[8 * g + 2]), "r"(o[8 * g + 3]), "r"(o[8 * g + 4]),
-                             "r"(o[8 * g + 5]), "r"(o[8 * g + 6]), "r"(o[8 * g + 7])
-                             : "memory");
+            asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(out + 16 * b), "r"(o[0]), "r"(o[1]),
+                         "r"(o[2]), "r"(o[3]), "r"(o[4]), "r"(o[5]), "r"(o[6]), "r"(o[7])
+                         : "memory");
           } else {
-#pragma unroll
-            for (int g = 0; g < 4; ++g)
-              if (32 * b + 8 * g < p.dv)
-                *reinterpret_cast<uint4*>(out + 32 * b + 8 * g) = make_uint4(o[4 * g], o[4 * g + 1], o[4 * g + 2], o[4 * g + 3]);
+            *reinterpret_cast<uint4*>(out + 16 * b) = make_uint4(o[0], o[1], o[2], o[3]);
+            if (16 * b + 8 < p.dv) *reinterpret_cast<uint4*>(out + 16 * b + 8) = make_uint4(o[4], o[5], o[6], o[7]);
           }
         }
       }
