@@ -73,14 +73,15 @@ __global__ void __launch_bounds__(kMaxHead / kRows * 32) linear_tokens_kernel(co
   float* cs = os + warps * tokens * kCols;  // [tokens]
   launch_dependents();
   grid_dependency_wait();
-  int64_t at = part_begin(p, part), end = part_begin(p, part + 1);
+  const int blocks = static_cast<int>(p.blocks);
+  int at = part_begin(p, part), end = part_begin(p, part + 1);
   if (kStates) {
-    int64_t pair, b0, b1;
+    int pair, b0, b1;
     if (!cut_piece(p, part, pair, b0, b1)) return;
-    at = pair * p.blocks + b0;
+    at = pair * blocks + b0;
   } else if (p.whole > 0) {  // whole sequences: then there are no others
-    at = static_cast<int64_t>(part) * p.whole * p.blocks;
-    end = at + p.whole * p.blocks;
+    at = part * p.whole * blocks;
+    end = at + p.whole * blocks;
   }
   const bool has_col = col < p.dv;
   float2 S[kRows / 2];
@@ -88,15 +89,14 @@ __global__ void __launch_bounds__(kMaxHead / kRows * 32) linear_tokens_kernel(co
   int64_t decays = 0;  // of a state that passes this piece, and whether something cuts it off
   bool cut_off = false;
   for (; at < end; ++at) {
-    const int64_t pair = at / p.blocks, head = pair % p.heads, batch = pair / p.heads;
-    const int64_t block = at - pair * p.blocks, tb = kReverse ? p.blocks - 1 - block : block;
-    const int64_t t0 = tb * kTokens;
+    const int pair = at / blocks, block = at - pair * blocks, tb = kReverse ? blocks - 1 - block : block;
+    const int64_t batch = pair / static_cast<int>(p.heads), head = pair - batch * p.heads, t0 = static_cast<int64_t>(tb) * kTokens;
     const int n = static_cast<int>(p.length - t0 < kTokens ? p.length - t0 : kTokens);
     const float log_decay = p.log_decay[head];
     const bool slow = log_decay > -kLn2;
     // of the state from token to token, and where it comes from behind the last token
     const float factor = slow ? expm1f(log_decay) : expf(log_decay), whole = slow ? 0.0f : 1.0f;
-    const int64_t state_at = pair * p.dk * p.dv;
+    const int64_t state_at = static_cast<int64_t>(pair) * p.dk * p.dv;
     if (fresh || block == 0) {
       fresh = false;
       const bool inside = block > 0 && !kStates;  // behind a cut
@@ -157,7 +157,7 @@ __global__ void __launch_bounds__(kMaxHead / kRows * 32) linear_tokens_kernel(co
         const int64_t row = row0 + (kReverse ? n - 1 - j : j);
         store1(static_cast<T*>(p.o) + row * p.ldo + head * p.dv + c, p.out_scale * x);
       }
-    const bool behind = !kStates && block + 1 == p.blocks && p.last;  // the sequence ends
+    const bool behind = !kStates && block + 1 == blocks && p.last;  // the sequence ends
     if ((behind || (kStates && at + 1 == end)) && has_col) {
       float* to = kStates ? p.local + static_cast<int64_t>(part + 1) * p.dk * p.dv : p.last + state_at;
       // against time what is left is the gradient of the state in front of the first token
@@ -176,36 +176,43 @@ __global__ void __launch_bounds__(kMaxHead / kRows * 32) linear_tokens_kernel(co
 }
 
 // The states in front of the ranges that begin inside a sequence: what the piece before adds, plus what is left
-// of the state in front of that.  A CTA takes 256 elements of one sequence's states, and goes with the
-// first range that begins inside the sequence; eight ranges' pieces are on their way at a time.
+// of the state in front of that.  A CTA takes 1024 elements of one sequence's states, and goes with the
+// first range that begins inside the sequence; four ranges' pieces are on their way at a time.
 __global__ void __launch_bounds__(256) linear_join_kernel(const Args p, int element_blocks) {
-  constexpr int kAhead = 8;
-  const int slot = blockIdx.x / element_blocks, size = p.dk * p.dv;
-  const int e = (blockIdx.x - slot * element_blocks) * 256 + threadIdx.x;
+  constexpr int kAhead = 4, kEach = 4;
+  const int slot = blockIdx.x / element_blocks, size = p.dk * p.dv, blocks = static_cast<int>(p.blocks);
+  const int e0 = (blockIdx.x - slot * element_blocks) * 1024 + threadIdx.x;
   int j = slot + 1;
-  const int64_t begin = part_begin(p, j), pair = begin / p.blocks, first = pair * p.blocks;
+  const int begin = part_begin(p, j), pair = begin / blocks, first = pair * blocks;
   launch_dependents();
-  if (begin == first || part_begin(p, j - 1) > first || e >= size) return;
+  if (begin == first || part_begin(p, j - 1) > first) return;
   int end = j + 1;
-  while (end < p.ranges && part_begin(p, end) < first + p.blocks) ++end;
+  while (end < p.ranges && part_begin(p, end) < first + blocks) ++end;
   grid_dependency_wait();
-  float x = 0.0f;
-  if (p.init) x = p.init[pair * size + (p.init_transposed ? e % p.dv * p.dk + e / p.dv : e)];
-  float* at = p.local + static_cast<int64_t>(j) * size + e;
+  float x[kEach];
+#pragma unroll
+  for (int k = 0; k < kEach; ++k) {
+    const int e = e0 + 256 * k;
+    x[k] = 0.0f;
+    if (p.init && e < size) x[k] = p.init[static_cast<int64_t>(pair) * size + (p.init_transposed ? e % p.dv * p.dk + e / p.dv : e)];
+  }
   for (; j < end; j += kAhead) {
-    float piece[kAhead], pass[kAhead];
+    float* at = p.local + static_cast<int64_t>(j) * size + e0;
+    float piece[kAhead][kEach], pass[kAhead];
 #pragma unroll
     for (int i = 0; i < kAhead; ++i) {
-      const bool there = j + i < end;
-      piece[i] = there ? at[static_cast<int64_t>(i) * size] : 0.0f;
-      pass[i] = there ? p.pass[j + i] : 0.0f;
+      pass[i] = j + i < end ? p.pass[j + i] : 0.0f;
+#pragma unroll
+      for (int k = 0; k < kEach; ++k)
+        piece[i][k] = j + i < end && e0 + 256 * k < size ? at[static_cast<int64_t>(i) * size + 256 * k] : 0.0f;
     }
 #pragma unroll
-    for (int i = 0; i < kAhead; ++i) {
-      x = pass[i] == 0.0f ? piece[i] : fmaf(pass[i], x, piece[i]);
-      if (j + i < end) at[static_cast<int64_t>(i) * size] = x;
-    }
-    at += static_cast<int64_t>(kAhead) * size;
+    for (int i = 0; i < kAhead; ++i)
+#pragma unroll
+      for (int k = 0; k < kEach; ++k) {
+        x[k] = pass[i] == 0.0f ? piece[i][k] : fmaf(pass[i], x[k], piece[i][k]);
+        if (j + i < end && e0 + 256 * k < size) at[static_cast<int64_t>(i) * size + 256 * k] = x[k];
+      }
   }
 }
 
@@ -216,11 +223,11 @@ int cut(Args* p, int64_t parts, float* workspace, cudaStream_t s) {
   auto deal = [&](int64_t n) {
     p->parts = static_cast<int>(n);
     p->whole = static_cast<int>(p->pairs / n);
-    p->first = p->whole * n * p->blocks;
+    p->first = static_cast<int>(p->whole * n * p->blocks);
     const int64_t left = total - p->first;
     p->ranges = static_cast<int>(std::min(left, n));
-    p->each = left > 0 ? left / p->ranges : 0;
-    p->rest = left > 0 ? left % p->ranges : 0;
+    p->each = left > 0 ? static_cast<int>(left / p->ranges) : 0;
+    p->rest = left > 0 ? static_cast<int>(left % p->ranges) : 0;
   };
   deal(std::min(parts, total));
   if (p->first == total || p->blocks == 1) return T3_OK;  // nothing is cut
@@ -244,7 +251,7 @@ int cut(Args* p, int64_t parts, float* workspace, cudaStream_t s) {
 }
 
 int launch_join(const Args& p, cudaStream_t s) {
-  const int blocks = (p.dk * p.dv + 255) / 256;
+  const int blocks = (p.dk * p.dv + 1023) / 1024;
   return launch(linear_join_kernel, static_cast<int64_t>(p.ranges - 1) * blocks, 256, 0, s, 1, p, blocks);
 }
 

@@ -44,24 +44,26 @@ struct Args {
   int64_t blocks;          // blocks of tokens a sequence
   int parts;
   int whole;               // sequences a part takes as wholes
-  int64_t first;           // the first block of the others; so many over parts, and what is left of that
-  int64_t each, rest;
-  int ranges;              // parts that have some of them
+  int first;               // the first block of the others
+  int ranges;              // parts that have some of them: so many each, and one more for some
+  int each, rest;
   float* local;            // [parts][dk * dv]: the state in front of each range that begins inside a sequence
   float* pass;             // [parts]: what is left of a state across the piece in front of such a range
 };
 
-__host__ __device__ __forceinline__ int64_t part_begin(const Args& p, int64_t i) {
-  return i >= p.ranges ? p.pairs * p.blocks : p.first + p.each * i + p.rest * i / p.ranges;
+// Blocks are counted in 32 bits (2^36 tokens of all heads would not fit the memory).
+__host__ __device__ __forceinline__ int part_begin(const Args& p, int i) {
+  return i >= p.ranges ? static_cast<int>(p.pairs * p.blocks)
+                       : p.first + p.each * i + static_cast<int>(static_cast<uint32_t>(p.rest * i) / static_cast<uint32_t>(p.ranges));
 }
 
 // A sequence's first block of the piece that part i computes last, and the end of it; false
 // where the part ends with a sequence.
-__device__ __forceinline__ bool cut_piece(const Args& p, int part, int64_t& pair, int64_t& b0, int64_t& b1) {
-  const int64_t begin = part_begin(p, part), end = part_begin(p, part + 1);
-  pair = end / p.blocks;
-  b1 = end - pair * p.blocks;
-  b0 = begin > pair * p.blocks ? begin - pair * p.blocks : 0;
+__device__ __forceinline__ bool cut_piece(const Args& p, int part, int& pair, int& b0, int& b1) {
+  const int begin = part_begin(p, part), end = part_begin(p, part + 1), blocks = static_cast<int>(p.blocks);
+  pair = end / blocks;
+  b1 = end - pair * blocks;
+  b0 = begin > pair * blocks ? begin - pair * blocks : 0;
   return b1 > 0;
 }
 

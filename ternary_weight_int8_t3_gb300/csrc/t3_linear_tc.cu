@@ -13,7 +13,7 @@
 // What bounds it: memory, q, k, v in and o out once.  A chunk of a head of 128 moves 128 KB, some 5600 clocks of an
 // SM's share of the memory's rate; its five products take 1300 of the tensor pipe.  The rest is latency: P
 // waits for Q K^T, the state for the product before.  So every step has warps of its own, handing over through
-// mbarriers, and the two chains have an issuer each; K and V come two chunks ahead and Q one:
+// mbarriers, and the two chains have an issuer each; Q and K, which a chunk begins with, come a chunk ahead:
 //   warp 0 TMA; warp 1 issues Q K^T, Q S and P V, warp 2 K'^T V; warps 4-7 P; 8-15 K'; 16-23 the state; 24-27 o.
 // Each group's thread owns a TMEM lane: a token's row of P and o, half a row of the state (dk), and for K' half a
 // token's row in shared memory.  TMEM columns: Q K^T 128, with P over its first 64; P V; Q S; the state.
@@ -40,26 +40,27 @@ constexpr int kWarpP = 4, kWarpK = 8, kWarpS = 16, kWarpO = 24;
 constexpr int kTcThreads = 32 * 28;
 constexpr int kColS = 0, kColPV = 128, kColQS = 256, kColState = 384;  // TMEM columns
 constexpr int kCode = 12 << 8;
-constexpr int kTable = 96;  // floats: 32 zeros, g^0 .. g^31 (times in_scale), and those backwards
+constexpr int kTable = 96;  // floats: 32 zeros, g^0 .. g^31 (times both scales), and those backwards
 
 template <int DK, int DV> struct Smem {
   static constexpr int half = kChunk * 128;  // a tile's 64 columns
   static constexpr int tile_k = DK / 64 * half, tile_v = DV / 64 * half;
   static constexpr int state = DK * DV * 2;
-  static constexpr int q = 0;                  // for the states alone a second k_low
-  static constexpr int k = q + tile_k;         // two
-  static constexpr int v = k + 2 * tile_k;     // two
-  static constexpr int k_low = v + 2 * tile_v; // what K' leaves behind its first bf16
-  static constexpr int s = k_low + tile_k;     // the state as bf16, [DK][64] halves
+  static constexpr int k = 0;                  // two
+  static constexpr int v = k + 2 * tile_k;
+  static constexpr int k_low = v + tile_v;     // what K' leaves behind its first bf16
+  static constexpr int q = k_low + tile_k;     // two; for the states alone a second k_low and V
+  static constexpr int s = q + 2 * tile_k;     // the state as bf16, [DK][64] halves
   static constexpr int tables = s + state;     // a warp of P each: see kTable
   static constexpr int bars = tables + 4 * kTable * 4;
-  static constexpr int n_bars = 22;
+  static constexpr int n_bars = 26;
   static constexpr int misc = bars + 8 * n_bars;
   static constexpr int bytes = misc + 16 + 1024;
   static_assert(bytes <= 227 * 1024, "shared memory budget");
   // 64 rows of the state: its product is taken with 128, of which the upper half reads whatever lies
   // 64 columns on
-  static_assert(k_low + tile_k + half <= tables || DK == 128, "inside the buffers");
+  static_assert(q + 2 * tile_k + half <= tables + (DK == 128 ? half : 0), "inside the buffers");
+  static_assert(tile_k + tile_v <= 2 * tile_k + state, "the states' second V");
 };
 
 __device__ __forceinline__ uint32_t idesc_bf16(int n, bool a_mn, bool b_mn) {
@@ -132,7 +133,7 @@ __device__ __forceinline__ float power(float log2_decay, int n) {
 struct Walk {
   int left;              // chunks still to take
   int turn = -1;         // of which so many are of the second kind, which begins at
-  int64_t then = 0;      // this block
+  int then = 0;          // this block
   int count = 0;         // and taken
   int pair, head, batch;
   int block;             // in the sequence
@@ -151,9 +152,9 @@ struct Walk {
     }
   }
   // to a block among those of all sequences
-  __device__ __forceinline__ void go(const Args& p, int64_t at) {
-    pair = static_cast<int>(at / p.blocks);
-    block = static_cast<int>(at - pair * p.blocks);
+  __device__ __forceinline__ void go(const Args& p, int at) {
+    pair = at / static_cast<int>(p.blocks);
+    block = at - pair * static_cast<int>(p.blocks);
     batch = pair / static_cast<int>(p.heads);
     head = pair - batch * static_cast<int>(p.heads);
   }
@@ -164,16 +165,16 @@ struct Walk {
 template <bool kStates>
 __device__ __forceinline__ Walk walk(const Args& p) {
   Walk w;
-  int64_t at = 0;
+  int at = 0;
   if (kStates) {
-    int64_t pair, b0, b1;
-    w.left = cut_piece(p, blockIdx.x, pair, b0, b1) ? static_cast<int>(b1 - b0) : 0;
-    if (w.left > 0) at = pair * p.blocks + b0;
+    int pair, b0, b1;
+    w.left = cut_piece(p, blockIdx.x, pair, b0, b1) ? b1 - b0 : 0;
+    if (w.left > 0) at = pair * static_cast<int>(p.blocks) + b0;
   } else {
     w.then = part_begin(p, blockIdx.x);
-    w.turn = static_cast<int>(part_begin(p, blockIdx.x + 1) - w.then);
+    w.turn = part_begin(p, blockIdx.x + 1) - w.then;
     w.left = p.whole * static_cast<int>(p.blocks) + w.turn;
-    at = p.whole > 0 ? static_cast<int64_t>(blockIdx.x) * p.whole * p.blocks : w.then;
+    at = p.whole > 0 ? static_cast<int>(blockIdx.x) * p.whole * static_cast<int>(p.blocks) : w.then;
     if (w.turn == 0 || p.whole == 0) w.turn = -1;
   }
   w.go(p, w.left > 0 ? at : 0);
@@ -236,13 +237,14 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + (((smem_addr(smem_raw) + 1023u) & ~1023u) - smem_addr(smem_raw));
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::bars);
-  uint64_t *q_full = bars, *k_full = bars + 1, *v_full = bars + 3, *k_empty = bars + 5, *s_full = bars + 7,
-           *pv_done = bars + 8, *upd_done = bars + 9, *end_bar = bars + 10, *q_empty = bars + 11,
+  uint64_t *k_full = bars + 1, *v_full = bars + 3, *k_empty = bars + 5, *s_full = bars + 7,
+           *pv_done = bars + 8, *upd_done = bars + 9, *end_bar = bars + 10,
            *o_full = bars + 12;                                           // one arrival each
-  uint64_t* v_empty = bars + 13;                                          // both issuers
+  uint64_t* v_empty = bars + 13;                                          // both issuers; two, of which without kStates one is used
   uint64_t *p_full = bars + 15, *o_empty = bars + 16;                     // a group's four warps
   uint64_t *kp_full = bars + 17, *st_full = bars + 19;                    // or eight
   uint64_t* drain = bars + 20;                                            // one for each issuer
+  uint64_t *q_full = bars + 22, *q_empty = bars + 24;                     // one arrival, two of each
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(smem + L::misc);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::misc + 4);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -273,28 +275,56 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       prefetch_tensormap(&map_v);
       if (!kStates) prefetch_tensormap(&map_q);
       int q_loads = 0, k_loads = 0, v_loads = 0;
-      for (; ok && w.more(); w.next(p)) {
-        const int t0 = chunk<kReverse>(p, w.block).t0, slot = w.count & 1;
-        const uint32_t free = ((w.count >> 1) & 1) ^ 1u;
-        ok = mbar_wait(&k_empty[slot], free, abort_flag, err, kCode | 1);
-        if (!ok) break;
+      auto load_q = [&](const Walk& at) {
+        const int slot = at.count & 1;
+        ok = mbar_wait(&q_empty[slot], ((at.count >> 1) & 1) ^ 1u, abort_flag, err, kCode | 1);
+        if (!ok) return;
+        mbar_arrive_expect_tx(&q_full[slot], L::tile_k);
+        for (int h = 0; h < DK / 64; ++h)
+          tma_load_4d(smem + L::q + slot * L::tile_k + h * L::half, &map_q, &q_full[slot], 64 * h, at.head,
+                      chunk<kReverse>(p, at.block).t0, at.batch);
+        ++q_loads;
+      };
+      auto load_k = [&](const Walk& at) {
+        const int slot = at.count & 1;
+        ok = mbar_wait(&k_empty[slot], ((at.count >> 1) & 1) ^ 1u, abort_flag, err, kCode | 1);
+        if (!ok) return;
         mbar_arrive_expect_tx(&k_full[slot], L::tile_k);
         for (int h = 0; h < DK / 64; ++h)
-          tma_load_4d(smem + L::k + slot * L::tile_k + h * L::half, &map_k, &k_full[slot], 64 * h, w.head, t0, w.batch);
+          tma_load_4d(smem + L::k + slot * L::tile_k + h * L::half, &map_k, &k_full[slot], 64 * h, at.head,
+                      chunk<kReverse>(p, at.block).t0, at.batch);
         ++k_loads;
-        ok = mbar_wait(&v_empty[slot], free, abort_flag, err, kCode | 1);
-        if (!ok) break;
+      };
+      auto load_v = [&](const Walk& at) {
+        const int slot = kStates ? at.count & 1 : 0;
+        const uint32_t round = kStates ? at.count >> 1 : at.count;
+        ok = mbar_wait(&v_empty[slot], (round & 1) ^ 1u, abort_flag, err, kCode | 1);
+        if (!ok) return;
         mbar_arrive_expect_tx(&v_full[slot], L::tile_v);
         for (int h = 0; h < DV / 64; ++h)
-          tma_load_4d(smem + L::v + slot * L::tile_v + h * L::half, &map_v, &v_full[slot], 64 * h, w.head, t0, w.batch);
+          tma_load_4d(smem + (slot ? L::q + L::tile_k : L::v) + h * L::half, &map_v, &v_full[slot], 64 * h, at.head,
+                      chunk<kReverse>(p, at.block).t0, at.batch);
         ++v_loads;
-        if (kStates) continue;
-        ok = mbar_wait(q_empty, w.parity() ^ 1u, abort_flag, err, kCode | 1);
-        if (!ok) break;
-        mbar_arrive_expect_tx(q_full, L::tile_k);
-        for (int h = 0; h < DK / 64; ++h)
-          tma_load_4d(smem + L::q + h * L::half, &map_q, q_full, 64 * h, w.head, t0, w.batch);
-        ++q_loads;
+      };
+      if (kStates) {
+        for (; ok && w.more(); w.next(p)) {
+          load_k(w);
+          if (ok) load_v(w);
+        }
+      } else if (w.more()) {
+        // Q and K of a chunk in front of V of the one before: V's place is free later
+        load_q(w);
+        if (ok) load_k(w);
+        while (ok) {
+          const Walk now = w;
+          w.next(p);
+          if (w.more()) {
+            load_q(w);
+            if (ok) load_k(w);
+          }
+          if (ok) load_v(now);
+          if (!w.more()) break;
+        }
       }
       if (!ok) {  // giving up: the copies in flight land before this CTA leaves
         const uint64_t t = global_timer_ns();
@@ -305,9 +335,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         };
         for (int s = 0; s < 2; ++s) {
           landed(&k_full[s], (k_loads + 1 - s) / 2);
-          landed(&v_full[s], (v_loads + 1 - s) / 2);
+          landed(&q_full[s], (q_loads + 1 - s) / 2);
+          landed(&v_full[s], kStates ? (v_loads + 1 - s) / 2 : s ? 0 : v_loads);
         }
-        landed(q_full, q_loads);
       }
     }
     __syncwarp();
@@ -316,9 +346,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     const uint32_t lead = lane == 0;
     const uint32_t base = smem_addr(smem);
     const uint64_t q_rows = smem_desc_k_sw128(base + L::q), k_rows = smem_desc_k_sw128(base + L::k);
-    const uint64_t k_cols = smem_desc_mn_sw128(base + L::k, L::half, 1024), v_cols = smem_desc_mn_sw128(base + L::v, L::half, 1024);
+    const uint64_t k_cols = smem_desc_mn_sw128(base + L::k, L::half, 1024), v1_cols = smem_desc_mn_sw128(base + L::v, L::half, 1024);
     const uint64_t low_cols = smem_desc_mn_sw128(base + L::k_low, L::half, 1024);
-    const uint64_t q_as_low = smem_desc_mn_sw128(base + L::q, L::half, 1024);
+    const uint64_t low2_cols = smem_desc_mn_sw128(base + L::q, L::half, 1024);
+    const uint64_t v2_cols = smem_desc_mn_sw128(base + L::q + L::tile_k, L::half, 1024);
     const uint64_t s_cols = smem_desc_mn_sw128(base + L::s, DK * 128, 1024);
     // step j of 16 along a product's sum: rows of 128 bytes hold 64 of it, 32 bytes a step; columns
     // go on by two groups of eight rows
@@ -331,7 +362,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     for (; w.more(); w.next(p)) {
       const int slot = w.count & 1;
       const uint32_t par = w.parity(), par2 = (w.count >> 1) & 1;
-      const uint64_t k_at = static_cast<uint64_t>(slot * L::tile_k) >> 4, v_at = static_cast<uint64_t>(slot * L::tile_v) >> 4;
+      const uint64_t k_at = static_cast<uint64_t>(slot * L::tile_k) >> 4;  // of Q's and K's slot
+      const int v_slot = kStates ? slot : 0;
+      const uint32_t v_par = kStates ? par2 : par;
+      const uint64_t v_cols = v_slot ? v2_cols : v1_cols;
       if (warp == 1) {
         if (kStates) break;
         // Q K^T, over the columns that the product before reads P from, and not before the warps of K' have seen
@@ -340,13 +374,13 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           seen(pv_done, par ^ 1u);
           seen(&kp_full[slot ^ 1], ((w.count - 1) >> 1) & 1);
         }
-        seen(q_full, par);
+        seen(&q_full[slot], par2);
         seen(&k_full[slot], par2);
         if (!__all_sync(0xffffffffu, ok)) break;
         tc_fence_after();
 #pragma unroll
         for (int j = 0; j < DK / 16; ++j)
-          mma_ss(lead, tmem + kColS, q_rows + along(j), k_rows + k_at + along(j), idesc_bf16(128, false, false), j > 0);
+          mma_ss(lead, tmem + kColS, q_rows + k_at + along(j), k_rows + k_at + along(j), idesc_bf16(128, false, false), j > 0);
         issued = true;
         mma_commit(lead, s_full);
         // Q S
@@ -356,37 +390,37 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         tc_fence_after();
 #pragma unroll
         for (int j = 0; j < DK / 16; ++j)
-          mma_ss(lead, tmem + kColQS, q_rows + along(j), s_cols + down(j), idesc_bf16(DV, false, true), j > 0);
-        mma_commit(lead, q_empty);
+          mma_ss(lead, tmem + kColQS, q_rows + k_at + along(j), s_cols + down(j), idesc_bf16(DV, false, true), j > 0);
+        mma_commit(lead, &q_empty[slot]);
         // P V
-        seen(&v_full[slot], par2);
+        seen(&v_full[v_slot], v_par);
         seen(p_full, par);
         if (!__all_sync(0xffffffffu, ok)) break;
         tc_fence_after();
 #pragma unroll
         for (int j = 0; j < kChunk / 16; ++j)
-          mma_ts(lead, tmem + kColPV, tmem + kColS + 8 * j, v_cols + v_at + down(j), idesc_bf16(DV, false, true), j > 0);
+          mma_ts(lead, tmem + kColPV, tmem + kColS + 8 * j, v_cols + down(j), idesc_bf16(DV, false, true), j > 0);
         mma_commit(lead, pv_done);
         mma_commit(lead, o_full);
-        mma_commit(lead, &v_empty[slot]);
+        mma_commit(lead, &v_empty[v_slot]);
       } else {
         // S += K'^T V
         if (!kStates) seen(st_full, par);
-        seen(&v_full[slot], par2);
+        seen(&v_full[v_slot], v_par);
         seen(&kp_full[slot], par2);
         if (!__all_sync(0xffffffffu, ok)) break;
         tc_fence_after();
-        const uint64_t low = kStates && slot ? q_as_low : low_cols;
+        const uint64_t low = kStates && slot ? low2_cols : low_cols;
 #pragma unroll
         for (int j = 0; j < kChunk / 16; ++j) {
-          mma_ss(lead, tmem + kColState, k_cols + k_at + down(j), v_cols + v_at + down(j), idesc_bf16(DV, true, true),
+          mma_ss(lead, tmem + kColState, k_cols + k_at + down(j), v_cols + down(j), idesc_bf16(DV, true, true),
                  !kStates || j > 0 || w.count > 0);
-          mma_ss(lead, tmem + kColState, low + down(j), v_cols + v_at + down(j), idesc_bf16(DV, true, true), 1u);
+          mma_ss(lead, tmem + kColState, low + down(j), v_cols + down(j), idesc_bf16(DV, true, true), 1u);
         }
         issued = true;
         if (!kStates) mma_commit(lead, upd_done);
         mma_commit(lead, &k_empty[slot]);
-        mma_commit(lead, &v_empty[slot]);
+        mma_commit(lead, &v_empty[v_slot]);
       }
     }
     if (kStates && warp == 2 && ok && issued) mma_commit(lead, end_bar);
@@ -412,8 +446,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         log2_decay = p.log_decay[w.head] * kLog2e;
         __syncwarp();
         up[lane - 32] = 0.0f;
-        up[lane] = p.in_scale * power(log2_decay, lane);
-        back[lane] = p.in_scale * power(log2_decay, 31 - lane);
+        up[lane] = p.in_scale * p.out_scale * power(log2_decay, lane);
+        back[lane] = p.in_scale * p.out_scale * power(log2_decay, 31 - lane);
         __syncwarp();
       }
       // the columns that count: in time lo .. row, against it row .. hi
@@ -712,7 +746,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         }
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          float2 z = __fmul2_rn(make_float2(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1])), make_float2(p.out_scale, p.out_scale));
+          float2 z = make_float2(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1]));  // P has out_scale in it
           const float2 t = __ffma2_rn(make_float2(__uint_as_float(y[2 * i]), __uint_as_float(y[2 * i + 1])), make_float2(f, f), z);
           if (f != 0.0f) z = t;  // whatever a state that is cut off holds
           o[i] = pack(z.x, z.y);
