@@ -18,7 +18,8 @@ BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libt3.so")
 
 SOURCES = ["t3_api.cu", "t3_tc_fwd.cu", "t3_tc_dx.cu", "t3_tc_dw.cu", "t3_skinny.cu", "t3_pack.cu", "t3_dequant.cu", "t3_quant.cu",
-           "t3_noalloc.cu", "t3_gemv.cu", "t3_small.cu", "t3_norm.cu", "t3_layernorm.cu", "t3_scan.cu", "t3_epilogue.cu", "t3_glu.cu", "t3_linear.cu", "t3_linear_tc.cu"]
+           "t3_noalloc.cu", "t3_gemv.cu", "t3_small.cu", "t3_norm.cu", "t3_layernorm.cu", "t3_scan.cu", "t3_epilogue.cu", "t3_glu.cu", "t3_linear.cu", "t3_linear_tc.cu",
+           "t3_linear_tc_128_128.cu", "t3_linear_tc_64_64.cu", "t3_linear_tc_64_128.cu", "t3_linear_tc_128_64.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC,-O2", "-Xptxas", "-v",
          "-I", os.path.join(ROOT, "include")]
