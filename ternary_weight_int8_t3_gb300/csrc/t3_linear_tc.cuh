@@ -138,6 +138,18 @@ __device__ __forceinline__ float power(float log2_decay, int n) {
   return n == 0 ? 1.0f : exp2f(log2_decay * static_cast<float>(n));
 }
 
+// log2 of the decay of the head at hand.
+struct Decay {
+  int head = -1;
+  float log2 = 0.0f;
+  __device__ __forceinline__ bool go(const Args& p, int to) {
+    if (to == head) return false;
+    head = to;
+    log2 = p.log_decay[to] * kLog2e;
+    return true;
+  }
+};
+
 // A CTA's chunks, in the order they are taken: those of its whole sequences, then those of its range of the
 // others.  Every role walks the same ones.
 struct Walk {
@@ -448,16 +460,16 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     float* up = reinterpret_cast<float*>(smem + L::tables) + q * kTable + 32;  // g^t, zeros for t < 0
     float* back = up + 32;                                                      // g^(31 - t)
     const float* mine = kReverse ? up - lane : up + lane;  // g^distance at [t] against time, at [-t] in time
-    int head_of_table = -1;
-    float log2_decay = 0.0f;
+    Decay decay;
+    float near = 0.0f, over32 = 0.0f;  // a row's power for the next block, and from block to block
     for (; !kStates && w.more(); w.next(p)) {
-      if (w.head != head_of_table) {
-        head_of_table = w.head;
-        log2_decay = p.log_decay[w.head] * kLog2e;
+      if (decay.go(p, w.head)) {
         __syncwarp();
         up[lane - 32] = 0.0f;
-        up[lane] = p.in_scale * p.out_scale * power(log2_decay, lane);
-        back[lane] = p.in_scale * p.out_scale * power(log2_decay, 31 - lane);
+        up[lane] = p.in_scale * p.out_scale * power(decay.log2, lane);
+        back[lane] = p.in_scale * p.out_scale * power(decay.log2, 31 - lane);
+        near = power(decay.log2, kReverse ? 32 - lane : lane + 1);
+        over32 = power(decay.log2, 32);
         __syncwarp();
       }
       // the columns that count: in time lo .. row, against it row .. hi
@@ -488,7 +500,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           for (int i = 0; i < 8; ++i) x[i] = make_float2(m[kReverse ? 2 * i : -2 * i], m[kReverse ? 2 * i + 1 : -2 * i - 1]);
         } else {
           // in time g^(row - 32 b - 31) g^(31 - t), against it g^(32 b - row) g^t
-          const float f = power(log2_decay, kReverse ? 32 * b - row : row - 32 * b - 31);
+          const int blocks = kReverse ? b - q : q - b;
+          float f = blocks > 2 ? near * over32 : near;
+          if (blocks > 1) f *= over32;
           const float4* table = reinterpret_cast<const float4*>((kReverse ? up : back) + 16 * (u & 1));
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
@@ -531,6 +545,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     // kStates: decayed to the end of the piece, tokens of which those from `edge` on count (against
     // time those in front of it); the others are cut off by a mark behind them
     int behind = 0, edge = kReverse ? 0x7FFFFFFF : -1;
+    Decay decay;
     if (kStates && w.more()) {
       const Chunk first = chunk<kReverse>(p, w.block), end = chunk<kReverse>(p, w.block + w.left - 1);
       const int t0 = kReverse ? end.t0 : first.t0, t1 = kReverse ? first.t0 + first.n : end.t0 + end.n;
@@ -554,7 +569,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         const Marks marks(p, w.batch, c);
         alive = alive && (kReverse ? marks.first(0) > row : marks.last(kChunk - 1) <= row);
       }
-      const float f = alive ? p.in_scale * power(p.log_decay[w.head] * kLog2e, away) : 0.0f;
+      decay.go(p, w.head);
+      const float f = alive ? p.in_scale * power(decay.log2, away) : 0.0f;
       const uint32_t keep = f == 0.0f ? 0u : 0xFFFFFFFFu;  // whatever a row that is cut off holds
       const float2 f2 = make_float2(f, f);
       const int slot = w.count & 1;
@@ -603,6 +619,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     const int col0 = ((warp - kWarpS) >> 2) * (DV / 2);  // half of the columns
     const uint32_t at = tmem + (static_cast<uint32_t>(32 * q) << 16) + kColState + col0;
     const bool mine = 32 * q < DK;  // this warp has rows of it
+    Decay decay;
     const int64_t size = static_cast<int64_t>(p.dk) * p.dv;
     // the state behind a piece, to the caller or to the next part
     auto put = [&](float* to, float f) {
@@ -643,7 +660,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     for (; !kStates && w.more(); w.next(p)) {
       const Chunk c = chunk<kReverse>(p, w.block);
       const bool cut = p.resets && Marks(p, w.batch, c).any();
-      const float f = cut ? 0.0f : power(p.log_decay[w.head] * kLog2e, c.n - 1 + c.e);
+      decay.go(p, w.head);
+      const float f = cut ? 0.0f : power(decay.log2, c.n - 1 + c.e);
       // a state that comes from memory, 16 columns ahead
       const bool fresh = w.block == 0 || w.count == 0 || w.left == w.turn;
       const bool transposed = w.block == 0 && p.init_transposed;
@@ -698,11 +716,16 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             for (int i = 0; i < 4; ++i) o[i] = pack(__uint_as_float(s[8 * g + 2 * i]), __uint_as_float(s[8 * g + 2 * i + 1]));
             sts128(to + tc::sw128(row, (col >> 3 & 7) + g), o[0], o[1], o[2], o[3]);
           }
+          if (f == 0.0f) {  // whatever it holds
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const float2 x = __fmul2_rn(make_float2(__uint_as_float(s[2 * i]), __uint_as_float(s[2 * i + 1])), make_float2(f, f));
-            s[2 * i] = f == 0.0f ? 0u : __float_as_uint(x.x);
-            s[2 * i + 1] = f == 0.0f ? 0u : __float_as_uint(x.y);
+            for (int i = 0; i < 16; ++i) s[i] = 0u;
+          } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const float2 x = __fmul2_rn(make_float2(__uint_as_float(s[2 * i]), __uint_as_float(s[2 * i + 1])), make_float2(f, f));
+              s[2 * i] = __float_as_uint(x.x);
+              s[2 * i + 1] = __float_as_uint(x.y);
+            }
           }
           __syncwarp();
           tmem_st_x16(at + 16 * b, s);
@@ -731,17 +754,20 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     // --------------------------------------------------------------------- o
     const int q = warp - kWarpO, row = 32 * q + lane;
     const uint32_t at = tmem + (static_cast<uint32_t>(32 * q) << 16);
+    Decay decay;
     const bool wide = ((reinterpret_cast<uintptr_t>(p.o) | (p.ldo * 2) | (p.dv * 2)) & 31) == 0;
     for (; !kStates && w.more(); w.next(p)) {
       const Chunk c = chunk<kReverse>(p, w.block);
       // what the state that the chunk begins with has left at this token
       const int pos = kReverse ? c.n - 1 - row : row;
-      bool alive = pos >= 0;
+      bool alive = pos >= 0, marked = false;
       if (p.resets) {
         const Marks marks(p, w.batch, c);
+        marked = marks.any();
         alive = alive && (kReverse ? marks.first(row + 1) >= kChunk : marks.last(row) < 0);
       }
-      const float f = alive ? p.out_scale * power(p.log_decay[w.head] * kLog2e, pos + c.e) : 0.0f;
+      decay.go(p, w.head);
+      const float f = alive ? p.out_scale * power(decay.log2, pos + c.e) : 0.0f;
       bf16* out = static_cast<bf16*>(p.o) + (w.batch * p.length + c.t0 + row) * p.ldo + w.head * p.dv;
       ok = mbar_wait(o_full, w.parity(), abort_flag, err, kCode | 4);
       if (!__all_sync(0xffffffffu, ok)) break;
@@ -761,10 +787,14 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         }
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          float2 z = make_float2(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1]));  // P has out_scale in it
-          const float2 t = __ffma2_rn(make_float2(__uint_as_float(y[2 * i]), __uint_as_float(y[2 * i + 1])), make_float2(f, f), z);
-          if (f != 0.0f) z = t;  // whatever a state that is cut off holds
+          // P has out_scale in it
+          const float2 z = __ffma2_rn(make_float2(__uint_as_float(y[2 * i]), __uint_as_float(y[2 * i + 1])), make_float2(f, f),
+                                      make_float2(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1])));
           o[i] = pack(z.x, z.y);
+        }
+        if (marked && !alive) {  // whatever a state that is cut off holds
+#pragma unroll
+          for (int i = 0; i < 8; ++i) o[i] = pack(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1]));
         }
         if (row < c.n && 16 * b < p.dv) {
           if (wide) {
