@@ -562,7 +562,7 @@ bool bad_ld(int64_t ld) { return ld < 0 || ld > kMaxDim; }
 bool bad_linear(int64_t batch, int64_t length, int64_t heads, int64_t dk, int64_t dv, int dtype) {
   return bad_dims(batch, length, heads) || !valid_dtype(dtype) || dk < 1 || dv < 1 || dk > lin::kMaxHead ||
          dv > lin::kMaxHead || static_cast<__int128>(batch) * heads > kMaxDim ||
-         static_cast<__int128>(batch) * heads * ceil_div(length, 32) > kMaxDim;
+         static_cast<__int128>(batch) * heads * ceil_div(length, 16) > kMaxDim;
 }
 
 // One pass of the recurrence on the kernels that take it.

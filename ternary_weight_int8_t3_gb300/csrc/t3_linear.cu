@@ -11,6 +11,8 @@
 // shared memory until the block ends.  A step with g above a half is taken as S + (g - 1) S + k v^T with g - 1 =
 // expm1(log_decay): g itself, rounded, would be off by as much at every step, and a memory of n tokens by n
 // times that (512 tokens: the state 2e-4).  Below, g S keeps its own relative precision.
+#include <type_traits>
+
 #include "t3_linear.cuh"
 
 namespace t3 {
@@ -18,17 +20,18 @@ namespace lin {
 
 constexpr int kCols = 32;   // columns of a state a CTA holds, one a lane
 constexpr int kRows = 16;   // rows of it a warp
-constexpr int kTokens = 32; // tokens of a block
+constexpr int kTokens = 16; // tokens of a block
 constexpr float kLn2 = 0.69314718f;
 
-__device__ __forceinline__ float load1(const float* p) { return *p; }
-__device__ __forceinline__ float load1(const bf16* p) { return __bfloat162float(*p); }
+__device__ __forceinline__ float as_float(float x) { return x; }
+__device__ __forceinline__ float as_float(bf16 x) { return __bfloat162float(x); }
 __device__ __forceinline__ void store1(float* p, float x) { *p = x; }
 __device__ __forceinline__ void store1(bf16* p, float x) { *p = __float2bfloat16_rn(x); }
 
-constexpr int padded(int d) { return (d + kRows - 1) / kRows * kRows; }
-constexpr int smem_floats(int tokens, int dk) {
-  return tokens * (2 * padded(dk) + kCols + 1) + padded(dk) / kRows * tokens * kCols;
+// Rows a CTA holds: whole warps, two at least (so that a thread fetches half a block's v at most).
+constexpr int padded(int d) { return d <= 2 * kRows ? 2 * kRows : (d + kRows - 1) / kRows * kRows; }
+constexpr int smem_floats(int dk) {
+  return 2 * kTokens * (2 * padded(dk) + kCols + 1) + 2 * padded(dk) / kRows * kTokens * kCols;
 }
 
 constexpr float kCut = 2.0f;  // a token whose state starts anew, among the factors
@@ -58,19 +61,71 @@ __device__ __forceinline__ float token(float2 (&S)[kRows / 2], float c, float v,
   return (sum.x + sum.y) + (sum2.x + sum2.y);
 }
 
+// A block of a sequence's tokens.
+struct Where {
+  int pair, block;
+  int64_t batch, head, t0;
+  int n;
+};
+
+template <bool kReverse>
+__device__ __forceinline__ Where locate(const Args& p, int pair, int block) {
+  Where w;
+  w.pair = pair, w.block = block;
+  w.batch = pair / static_cast<int>(p.heads), w.head = pair - w.batch * p.heads;
+  w.t0 = static_cast<int64_t>(kReverse ? static_cast<int>(p.blocks) - 1 - block : block) * kTokens;
+  w.n = static_cast<int>(p.length - w.t0 < kTokens ? p.length - w.t0 : kTokens);
+  return w;
+}
+
+// A block's rows on their way, in the order the tokens are taken: half the CTA's threads hold an element
+// of each k, the others of each q; each warp every `warps`th v.
+template <class T>
+struct Rows {
+  T kq[kTokens], v[kTokens / 2];
+  uint8_t mark;
+};
+
+template <class T, bool kReverse, bool kStates>
+__device__ __forceinline__ void fetch(const Args& p, const Where& w, int rows, int col, Rows<T>& x) {
+  const int warp = threadIdx.x >> 5, warps = rows / kRows, tid = threadIdx.x;
+  const bool is_q = tid >= rows;
+  const int r = is_q ? tid - rows : tid;
+  const int64_t ld = is_q ? p.ldq : p.ldk, row0 = w.batch * p.length + w.t0 + (kReverse ? w.n - 1 : 0);
+  const T zero = T(0.0f);
+  if (!(kStates && is_q)) {
+    const T* from = static_cast<const T*>(is_q ? p.q : p.k) + row0 * ld + w.head * p.dk + r;
+#pragma unroll
+    for (int j = 0; j < kTokens; ++j) {
+      x.kq[j] = j < w.n && r < p.dk ? *from : zero;
+      from += kReverse ? -ld : ld;
+    }
+  }
+  const T* from = static_cast<const T*>(p.v) + (row0 + (kReverse ? -warp : warp)) * p.ldv + w.head * p.dv + col;
+#pragma unroll
+  for (int i = 0; i < kTokens / 2; ++i) {
+    x.v[i] = i * warps + warp < w.n && col < p.dv ? *from : zero;
+    from += (kReverse ? -warps : warps) * p.ldv;
+  }
+  x.mark = 0;
+  if (p.resets && tid < w.n) {
+    // what cuts a token off from the one taken before it: in time its own mark, against time
+    // that of the token taken before it, which is the next one
+    const int64_t mark = kReverse ? w.t0 + w.n - tid : w.t0 + tid;
+    if (mark < p.length) x.mark = p.resets[w.batch * p.length + mark];
+  }
+}
+
 // kStates: only what each part's last piece adds to the state (Args::local).
 template <class T, bool kReverse, bool kStates>
-__global__ void __launch_bounds__(kMaxHead / kRows * 32) linear_tokens_kernel(const Args p, int col_blocks) {
+__global__ void __launch_bounds__(kMaxHead / kRows * 32, 2) linear_tokens_kernel(const Args p, int col_blocks) {
   extern __shared__ __align__(16) float sm[];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5, threads = blockDim.x;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
   const int part = blockIdx.x / col_blocks, col = (blockIdx.x - part * col_blocks) * kCols + lane;
   const int rows = warps * kRows;
-  const int tokens = p.length < kTokens ? static_cast<int>(p.length) : kTokens;
-  float* qs = sm;                         // [tokens][rows]
-  float* ks = qs + tokens * rows;         // [tokens][rows]
-  float* vs = ks + tokens * rows;         // [tokens][kCols]
-  float* os = vs + tokens * kCols;        // [warps][tokens][kCols]
-  float* cs = os + warps * tokens * kCols;  // [tokens]
+  // twice: k and q [tokens][rows], v [tokens][kCols], the factors [tokens]; then the sums [warps][tokens][kCols]
+  const int block_floats = kTokens * (2 * rows + kCols + 1);
+  float* sums = sm + 2 * block_floats;
   launch_dependents();
   grid_dependency_wait();
   const int blocks = static_cast<int>(p.blocks);
@@ -83,96 +138,178 @@ __global__ void __launch_bounds__(kMaxHead / kRows * 32) linear_tokens_kernel(co
     at = part * p.whole * blocks;
     end = at + p.whole * blocks;
   }
+  if (at >= end) return;
   const bool has_col = col < p.dv;
   float2 S[kRows / 2];
   bool fresh = true;  // the state is still to be loaded
-  int64_t decays = 0;  // of a state that passes this piece, and whether something cuts it off
+  int decays = 0;  // of a state that passes this piece, and whether something cuts it off
   bool cut_off = false;
-  for (; at < end; ++at) {
-    const int pair = at / blocks, block = at - pair * blocks, tb = kReverse ? blocks - 1 - block : block;
-    const int64_t batch = pair / static_cast<int>(p.heads), head = pair - batch * p.heads, t0 = static_cast<int64_t>(tb) * kTokens;
-    const int n = static_cast<int>(p.length - t0 < kTokens ? p.length - t0 : kTokens);
-    const float log_decay = p.log_decay[head];
+
+  Where w = locate<kReverse>(p, at / blocks, at % blocks), next = w;
+  Rows<T> x;
+  float log_decay = 0.0f;
+  auto put = [&](float* to) {
     const bool slow = log_decay > -kLn2;
-    // of the state from token to token, and where it comes from behind the last token
-    const float factor = slow ? expm1f(log_decay) : expf(log_decay), whole = slow ? 0.0f : 1.0f;
-    const int64_t state_at = static_cast<int64_t>(pair) * p.dk * p.dv;
-    if (fresh || block == 0) {
+    const int r = threadIdx.x;  // k's rows, then q's
+    if (!(kStates && r >= rows)) {
+      float* kq = to + (r >= rows ? kTokens * rows + r - rows : r);
+#pragma unroll
+      for (int j = 0; j < kTokens; ++j) kq[j * rows] = as_float(x.kq[j]);
+    }
+    float* vs = to + 2 * kTokens * rows;
+#pragma unroll
+    for (int i = 0; i < kTokens / 2; ++i)
+      if (i * warps + warp < kTokens) vs[(i * warps + warp) * kCols + lane] = p.in_scale * as_float(x.v[i]);
+    if (threadIdx.x < kTokens)  // of the state from token to token, and where it comes from behind the last token
+      vs[kTokens * kCols + threadIdx.x] = x.mark ? kCut
+                                          : kReverse && next.t0 + next.n - threadIdx.x == p.length ? (slow ? 0.0f : 1.0f)
+                                          : slow ? expm1f(log_decay) : expf(log_decay);
+  };
+  fetch<T, kReverse, kStates>(p, w, rows, col, x);
+  log_decay = p.log_decay[w.head];
+  put(sm);
+  __syncthreads();
+  for (int turn = 0; at < end; ++at, turn ^= 1) {
+    const bool slow = log_decay > -kLn2;
+    const float this_decay = log_decay;
+    if (at + 1 < end) {
+      const bool ends = w.block + 1 == blocks;
+      next = locate<kReverse>(p, ends ? w.pair + 1 : w.pair, ends ? 0 : w.block + 1);
+      fetch<T, kReverse, kStates>(p, next, rows, col, x);
+      log_decay = p.log_decay[next.head];
+    }
+    const int64_t state_at = static_cast<int64_t>(w.pair) * p.dk * p.dv;
+    if (fresh || w.block == 0) {
       fresh = false;
-      const bool inside = block > 0 && !kStates;  // behind a cut
+      const bool inside = w.block > 0 && !kStates;  // behind a cut
       const float* from = inside ? p.local + static_cast<int64_t>(part) * p.dk * p.dv : p.init ? p.init + state_at : nullptr;
       const bool transposed = !inside && p.init_transposed;
       const bool there = from && has_col && !kStates;
 #pragma unroll
       for (int i = 0; i < kRows; ++i) {
         const int r = warp * kRows + i;
-        const float x = there && r < p.dk ? from[transposed ? col * p.dk + r : r * p.dv + col] : 0.0f;
+        const float y = there && r < p.dk ? from[transposed ? col * p.dk + r : r * p.dv + col] : 0.0f;
         if (i & 1)
-          S[i / 2].y = x;
+          S[i / 2].y = y;
         else
-          S[i / 2].x = x;
+          S[i / 2].x = y;
       }
     }
-    // the block's rows, in the order they are taken
-    const int64_t row0 = batch * p.length + t0;
-    for (int i = threadIdx.x; i < n * rows; i += threads) {
-      const int j = i / rows, r = i - j * rows;
-      const int64_t row = row0 + (kReverse ? n - 1 - j : j);
-      const bool in = r < p.dk;
-      ks[i] = in ? p.in_scale * load1(static_cast<const T*>(p.k) + row * p.ldk + head * p.dk + r) : 0.0f;
-      if (!kStates) qs[i] = in ? load1(static_cast<const T*>(p.q) + row * p.ldq + head * p.dk + r) : 0.0f;
-    }
-    for (int i = threadIdx.x; i < n * kCols; i += threads) {
-      const int j = i / kCols, c = col - lane + i % kCols;
-      const int64_t row = row0 + (kReverse ? n - 1 - j : j);
-      vs[i] = c < p.dv ? load1(static_cast<const T*>(p.v) + row * p.ldv + head * p.dv + c) : 0.0f;
-    }
-    for (int j = threadIdx.x; j < n; j += threads) {
-      const int64_t t = t0 + (kReverse ? n - 1 - j : j);
-      // what cuts a token off from the one taken before it: in time its own mark, against time
-      // that of the token taken before it, which is the next one
-      const int64_t mark = kReverse ? t + 1 : t;
-      const bool cut = p.resets && mark < p.length && p.resets[batch * p.length + mark] != 0;
-      cs[j] = cut ? kCut : kReverse && t + 1 == p.length ? whole : factor;
-    }
+    const float* ks = sm + turn * block_floats;
+    const float* vs = ks + 2 * kTokens * rows + lane;
+    const float* cs = ks + 2 * kTokens * rows + kTokens * kCols;
+    const float4* kp = reinterpret_cast<const float4*>(ks + warp * kRows);
+    const float4* qp = reinterpret_cast<const float4*>(ks + kTokens * rows + warp * kRows);
+    float* os = sums + (turn * warps + warp) * kTokens * kCols + lane;
+    auto take = [&](auto is_slow) {
+      constexpr bool kSlow = decltype(is_slow)::value;
+#pragma unroll 2
+      for (int j = 0; j < w.n; ++j) {
+        const float c = cs[j];
+        if (kStates) {
+          decays += c != (kSlow ? 0.0f : 1.0f);
+          cut_off |= c == kCut;
+        }
+        const float y = token<kSlow, kStates>(S, c, vs[j * kCols], kp + j * (rows / 4), qp + j * (rows / 4));
+        if (!kStates) os[j * kCols] = y;
+      }
+    };
+    if (slow)
+      take(std::true_type());
+    else
+      take(std::false_type());
+    if (at + 1 < end) put(sm + (turn ^ 1) * block_floats);
     __syncthreads();
-    for (int j = 0; j < n; ++j) {
-      const float c = cs[j], v = vs[j * kCols + lane];
-      if (kStates) {
-        decays += c != whole;
-        cut_off |= c == kCut;
+    if (!kStates && has_col) {
+      const float* from = sums + turn * warps * kTokens * kCols + lane;
+      for (int j = warp; j < w.n; j += warps) {
+        float y = 0.0f;
+        for (int u = 0; u < warps; ++u) y += from[(u * kTokens + j) * kCols];
+        const int64_t row = w.batch * p.length + w.t0 + (kReverse ? w.n - 1 - j : j);
+        store1(static_cast<T*>(p.o) + row * p.ldo + w.head * p.dv + col, p.out_scale * y);
       }
-      const float4* kp = reinterpret_cast<const float4*>(ks + j * rows + warp * kRows);
-      const float4* qp = reinterpret_cast<const float4*>(qs + j * rows + warp * kRows);
-      const float x = slow ? token<true, kStates>(S, c, v, kp, qp) : token<false, kStates>(S, c, v, kp, qp);
-      if (!kStates) os[(warp * tokens + j) * kCols + lane] = x;
     }
-    __syncthreads();
-    if (!kStates)
-      for (int i = threadIdx.x; i < n * kCols; i += threads) {
-        const int j = i / kCols, c = col - lane + i % kCols;
-        if (c >= p.dv) continue;
-        float x = 0.0f;
-        for (int w = 0; w < warps; ++w) x += os[w * tokens * kCols + i];
-        const int64_t row = row0 + (kReverse ? n - 1 - j : j);
-        store1(static_cast<T*>(p.o) + row * p.ldo + head * p.dv + c, p.out_scale * x);
-      }
-    const bool behind = !kStates && block + 1 == blocks && p.last;  // the sequence ends
+    const bool behind = !kStates && w.block + 1 == blocks && p.last;  // the sequence ends
     if ((behind || (kStates && at + 1 == end)) && has_col) {
       float* to = kStates ? p.local + static_cast<int64_t>(part + 1) * p.dk * p.dv : p.last + state_at;
       // against time what is left is the gradient of the state in front of the first token
-      const bool cut = kReverse && behind && p.resets && p.resets[batch * p.length] != 0;
-      const float f = kReverse && behind ? expf(log_decay) : 1.0f;
+      const bool cut = kReverse && behind && p.resets && p.resets[w.batch * p.length] != 0;
+      const float f = kReverse && behind ? expf(this_decay) : 1.0f;
 #pragma unroll
       for (int i = 0; i < kRows; ++i) {
         const int r = warp * kRows + i;
-        const float x = i & 1 ? S[i / 2].y : S[i / 2].x;
-        if (r < p.dk) to[r * p.dv + col] = cut || f == 0.0f ? 0.0f : f * x;
+        const float y = i & 1 ? S[i / 2].y : S[i / 2].x;
+        if (r < p.dk) to[r * p.dv + col] = cut || f == 0.0f ? 0.0f : f * y;
       }
       if (kStates && threadIdx.x == 0 && col == 0)
-        p.pass[part + 1] = cut_off ? 0.0f : decays == 0 ? 1.0f : expf(log_decay * static_cast<float>(decays));
+        p.pass[part + 1] = cut_off ? 0.0f : decays == 0 ? 1.0f : expf(this_decay * static_cast<float>(decays));
     }
+    w = next;
   }
+}
+
+// One token a sequence, its state read once and written once, 16 bytes a thread and row, all of a thread's 16 rows on
+// their way at a time.  A CTA takes `cols` columns of a state; `lanes` lanes (a power of two, 4 columns each) share a row.
+constexpr int kStepRows = 16;
+
+template <class T>
+__global__ void __launch_bounds__(kMaxHead / kStepRows * 32, 2) linear_step_kernel(const Args p, int cols, int lanes, int col_blocks) {
+  __shared__ float4 sums[kMaxHead / kStepRows][32];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+  const int pair = blockIdx.x / col_blocks, col0 = (blockIdx.x - pair * col_blocks) * cols;
+  const int sub = lane / lanes, c = (lane - sub * lanes) * 4, col = col0 + c, step = 32 / lanes;
+  const int row0 = warp * kStepRows * step + sub;
+  const bool has_col = c < cols && col < p.dv;
+  const int64_t batch = pair / static_cast<int>(p.heads), head = pair - batch * p.heads;
+  const int64_t at = static_cast<int64_t>(pair) * p.dk * p.dv + static_cast<int64_t>(row0) * p.dv + col;
+  launch_dependents();
+  grid_dependency_wait();
+  float4 S[kStepRows];
+#pragma unroll
+  for (int i = 0; i < kStepRows; ++i)
+    S[i] = p.init && has_col && row0 + i * step < p.dk ? *reinterpret_cast<const float4*>(p.init + at + i * step * p.dv)
+                                                       : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  const float log_decay = p.log_decay[head];
+  const bool cut = p.resets && p.resets[batch] != 0, slow = log_decay > -kLn2;
+  const float f = cut ? 0.0f : slow ? expm1f(log_decay) : expf(log_decay);
+  float v[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    v[i] = has_col ? p.in_scale * as_float(static_cast<const T*>(p.v)[batch * p.ldv + head * p.dv + col + i]) : 0.0f;
+  const T* kp = static_cast<const T*>(p.k) + batch * p.ldk + head * p.dk + row0;
+  const T* qp = static_cast<const T*>(p.q) + batch * p.ldq + head * p.dk + row0;
+  float4 sum = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+  for (int i = 0; i < kStepRows; ++i) {
+    const bool in = row0 + i * step < p.dk;
+    const float k = in ? as_float(kp[i * step]) : 0.0f, q = in ? as_float(qp[i * step]) : 0.0f;
+    auto one = [&](float s, float x) {
+      return fmaf(k, x, cut ? 0.0f : slow ? fmaf(s, f, s) : s * f);
+    };
+    S[i] = make_float4(one(S[i].x, v[0]), one(S[i].y, v[1]), one(S[i].z, v[2]), one(S[i].w, v[3]));
+    sum = make_float4(fmaf(q, S[i].x, sum.x), fmaf(q, S[i].y, sum.y), fmaf(q, S[i].z, sum.z), fmaf(q, S[i].w, sum.w));
+    if (p.last && has_col && in) *reinterpret_cast<float4*>(p.last + at + i * step * p.dv) = S[i];
+  }
+  sums[warp][lane] = sum;
+  __syncthreads();
+  // o: over the warps and the rows of each
+  for (int i = threadIdx.x; i < cols; i += blockDim.x) {
+    if (col0 + i >= p.dv) break;
+    float y = 0.0f;
+    for (int w = 0; w < warps; ++w)
+      for (int u = 0; u < step; ++u) y += reinterpret_cast<const float*>(&sums[w][u * lanes])[i];
+    store1(static_cast<T*>(p.o) + batch * p.ldo + head * p.dv + col0 + i, p.out_scale * y);
+  }
+}
+
+template <class T>
+int run_step(const Args& p, int sms, cudaStream_t s) {
+  // A state's columns go to CTAs of 32 each while that leaves none of the SMs with two
+  const int cols = p.pairs * ((p.dv + 31) / 32) <= 2 * sms ? 32 : (p.dv + 3) / 4 * 4;
+  int lanes = 1;
+  while (4 * lanes < cols && 4 * lanes < p.dv) lanes *= 2;
+  const int rows = kStepRows * (32 / lanes), warps = (p.dk + rows - 1) / rows, col_blocks = (p.dv + cols - 1) / cols;
+  return launch(linear_step_kernel<T>, p.pairs * col_blocks, warps * 32, 0, s, 1, p, cols, lanes, col_blocks);
 }
 
 // The states in front of the ranges that begin inside a sequence: what the piece before adds, plus what is left
@@ -258,11 +395,10 @@ int launch_join(const Args& p, cudaStream_t s) {
 template <class T, bool kReverse>
 int run(const Args& p, cudaStream_t s) {
   const int col_blocks = (p.dv + kCols - 1) / kCols, threads = padded(p.dk) / kRows * 32;
-  const int tokens = p.length < kTokens ? static_cast<int>(p.length) : kTokens;
-  const size_t smem = smem_floats(tokens, p.dk) * sizeof(float);
+  const size_t smem = smem_floats(p.dk) * sizeof(float);
   int dev = 0, st;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return T3_EDEVICE;
-  constexpr int kMost = smem_floats(kTokens, kMaxHead) * 4;
+  constexpr int kMost = smem_floats(kMaxHead) * 4;
   if ((st = allow_smem<linear_tokens_kernel<T, kReverse, false>>(dev, kMost)) != T3_OK) return st;
   if (p.local) {
     if ((st = allow_smem<linear_tokens_kernel<T, kReverse, true>>(dev, kMost)) != T3_OK) return st;
@@ -278,6 +414,9 @@ int run(const Args& p, cudaStream_t s) {
 }  // namespace lin
 
 int launch_linear_tokens(lin::Args p, bool reverse, int dtype, float* workspace, int sms, cudaStream_t s) {
+  const auto aligned = [](const void* x) { return reinterpret_cast<uintptr_t>(x) % 16 == 0; };
+  if (p.length == 1 && !reverse && !p.init_transposed && p.dv % 4 == 0 && aligned(p.init) && aligned(p.last))
+    return dtype == T3_OUT_BF16 ? lin::run_step<vec::bf16>(p, sms, s) : lin::run_step<float>(p, sms, s);
   p.blocks = (p.length + lin::kTokens - 1) / lin::kTokens;
   // about two CTAs an SM: whole sequences where there are as many, else cuts
   const int64_t col_blocks = (p.dv + lin::kCols - 1) / lin::kCols, want = (2 * sms + col_blocks - 1) / col_blocks;
