@@ -133,6 +133,16 @@ __device__ __forceinline__ void loaded(uint32_t (&v)[16]) {
                  "+r"(v[9]), "+r"(v[10]), "+r"(v[11]), "+r"(v[12]), "+r"(v[13]), "+r"(v[14]), "+r"(v[15])::"memory");
 }
 
+// What a wait does when its barrier keeps it, once in the code: the roles together would not fit the
+// instruction cache with a copy at each wait.
+static __device__ __noinline__ bool keep_waiting(uint64_t* bar, uint32_t parity, volatile int* abort_flag, int* err, int code) {
+  return mbar_wait(bar, parity, abort_flag, err, code);
+}
+__device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag, int* err, int code) {
+  return mbar_try_wait(bar, parity) || keep_waiting(bar, parity, abort_flag, err, code);
+}
+static __device__ __noinline__ int quotient(int a, int b) { return static_cast<int>(static_cast<uint32_t>(a) / static_cast<uint32_t>(b)); }
+
 // g^n from log2 g, 1 for n = 0 whatever g.
 __device__ __forceinline__ float power(float log2_decay, int n) {
   return n == 0 ? 1.0f : exp2f(log2_decay * static_cast<float>(n));
@@ -175,9 +185,9 @@ struct Walk {
   }
   // to a block among those of all sequences
   __device__ __forceinline__ void go(const Args& p, int at) {
-    pair = at / static_cast<int>(p.blocks);
+    pair = quotient(at, static_cast<int>(p.blocks));
     block = at - pair * static_cast<int>(p.blocks);
-    batch = pair / static_cast<int>(p.heads);
+    batch = quotient(pair, static_cast<int>(p.heads));
     head = pair - batch * static_cast<int>(p.heads);
   }
   __device__ __forceinline__ bool more() const { return left > 0; }
@@ -216,38 +226,47 @@ __device__ __forceinline__ Chunk chunk(const Args& p, int block) {
   return c;
 }
 
-// The marks of a chunk's tokens, a bit each; the whole warp calls.
-struct Marks {
+// The marks of n tokens, a bit each; the whole warp calls.
+static __device__ __noinline__ uint4 read_marks(const uint8_t* resets, int n) {
   uint32_t w[4];
-  __device__ __forceinline__ Marks(const Args& p, int batch, const Chunk& c) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int j = 32 * i + (threadIdx.x & 31);
-      w[i] = __ballot_sync(0xffffffffu, j < c.n && p.resets[batch * p.length + c.t0 + j] != 0);
-    }
+  for (int i = 0; i < 4; ++i) {
+    const int j = 32 * i + (threadIdx.x & 31);
+    w[i] = __ballot_sync(0xffffffffu, j < n && resets[j] != 0);
   }
-  __device__ __forceinline__ bool any() const { return (w[0] | w[1] | w[2] | w[3]) != 0u; }
-  // the last mark at or in front of token i, -1 if none; the first at or behind it, 128 if none
-  __device__ __forceinline__ int last(int i) const {
-    int r = -1;
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+// The last mark at or in front of token i, -1 if none.
+static __device__ __noinline__ int last_mark(uint4 marks, int i) {
+  const uint32_t w[4] = {marks.x, marks.y, marks.z, marks.w};
+  int r = -1;
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const int in = i - 32 * k;  // bits 0 .. in count
-      const uint32_t m = in < 0 ? 0u : in >= 31 ? w[k] : w[k] & ((2u << in) - 1u);
-      if (m) r = 32 * k + 31 - __clz(m);
-    }
-    return r;
+  for (int k = 0; k < 4; ++k) {
+    const int in = i - 32 * k;  // bits 0 .. in count
+    const uint32_t m = in < 0 ? 0u : in >= 31 ? w[k] : w[k] & ((2u << in) - 1u);
+    if (m) r = 32 * k + 31 - __clz(m);
   }
-  __device__ __forceinline__ int first(int i) const {
-    int r = 128;
+  return r;
+}
+// The first mark at or behind token i, 128 if none.
+static __device__ __noinline__ int first_mark(uint4 marks, int i) {
+  const uint32_t w[4] = {marks.x, marks.y, marks.z, marks.w};
+  int r = 128;
 #pragma unroll
-    for (int k = 3; k >= 0; --k) {
-      const int from = i - 32 * k;  // bits from .. 31 count
-      const uint32_t m = from > 31 ? 0u : from <= 0 ? w[k] : w[k] & (0xFFFFFFFFu << from);
-      if (m) r = 32 * k + __ffs(m) - 1;
-    }
-    return r;
+  for (int k = 3; k >= 0; --k) {
+    const int from = i - 32 * k;  // bits from .. 31 count
+    const uint32_t m = from > 31 ? 0u : from <= 0 ? w[k] : w[k] & (0xFFFFFFFFu << from);
+    if (m) r = 32 * k + __ffs(m) - 1;
   }
+  return r;
+}
+
+struct Marks {
+  uint4 w;
+  __device__ __forceinline__ Marks(const Args& p, int batch, const Chunk& c) : w(read_marks(p.resets + batch * p.length + c.t0, c.n)) {}
+  __device__ __forceinline__ bool any() const { return (w.x | w.y | w.z | w.w) != 0u; }
+  __device__ __forceinline__ int last(int i) const { return last_mark(w, i); }
+  __device__ __forceinline__ int first(int i) const { return first_mark(w, i); }
 };
 
 // kStates: only what each part's last piece adds to the state (Args::local).
@@ -299,7 +318,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       int q_loads = 0, k_loads = 0, v_loads = 0;
       auto load_q = [&](const Walk& at) {
         const int slot = at.count & 1;
-        ok = mbar_wait(&q_empty[slot], ((at.count >> 1) & 1) ^ 1u, abort_flag, err, kCode | 1);
+        ok = wait(&q_empty[slot], ((at.count >> 1) & 1) ^ 1u, abort_flag, err, kCode | 1);
         if (!ok) return;
         mbar_arrive_expect_tx(&q_full[slot], L::tile_k);
         for (int h = 0; h < DK / 64; ++h)
@@ -309,7 +328,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       };
       auto load_k = [&](const Walk& at) {
         const int slot = at.count & 1;
-        ok = mbar_wait(&k_empty[slot], ((at.count >> 1) & 1) ^ 1u, abort_flag, err, kCode | 1);
+        ok = wait(&k_empty[slot], ((at.count >> 1) & 1) ^ 1u, abort_flag, err, kCode | 1);
         if (!ok) return;
         mbar_arrive_expect_tx(&k_full[slot], L::tile_k);
         for (int h = 0; h < DK / 64; ++h)
@@ -320,7 +339,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       auto load_v = [&](const Walk& at) {
         const int slot = kStates ? at.count & 1 : 0;
         const uint32_t round = kStates ? at.count >> 1 : at.count;
-        ok = mbar_wait(&v_empty[slot], (round & 1) ^ 1u, abort_flag, err, kCode | 1);
+        ok = wait(&v_empty[slot], (round & 1) ^ 1u, abort_flag, err, kCode | 1);
         if (!ok) return;
         mbar_arrive_expect_tx(&v_full[slot], L::tile_v);
         for (int h = 0; h < DV / 64; ++h)
@@ -333,19 +352,19 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           load_k(w);
           if (ok) load_v(w);
         }
-      } else if (w.more()) {
+      } else {
         // Q and K of a chunk in front of V of the one before: V's place is free later
-        load_q(w);
-        if (ok) load_k(w);
+        Walk before = w;
         while (ok) {
-          const Walk now = w;
-          w.next(p);
-          if (w.more()) {
+          const bool more = w.more();
+          if (more) {
             load_q(w);
             if (ok) load_k(w);
           }
-          if (ok) load_v(now);
-          if (!w.more()) break;
+          if (ok && w.count > 0) load_v(before);
+          if (!more) break;
+          before = w;
+          w.next(p);
         }
       }
       if (!ok) {  // giving up: the copies in flight land before this CTA leaves
@@ -379,7 +398,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     auto down = [](int j) { return static_cast<uint64_t>(2048 * j) >> 4; };
     bool issued = false;
     auto seen = [&](uint64_t* bar, uint32_t parity) {
-      ok = ok && mbar_wait(bar, parity, abort_flag, err, kCode | 3);
+      ok = ok && wait(bar, parity, abort_flag, err, kCode | 3);
     };
     for (; w.more(); w.next(p)) {
       const int slot = w.count & 1;
@@ -400,7 +419,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         seen(&k_full[slot], par2);
         if (!__all_sync(0xffffffffu, ok)) break;
         tc_fence_after();
-#pragma unroll
+#pragma unroll 2
         for (int j = 0; j < DK / 16; ++j)
           mma_ss(lead, tmem + kColS, q_rows + k_at + along(j), k_rows + k_at + along(j), idesc_bf16(128, false, false), j > 0);
         issued = true;
@@ -410,7 +429,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         seen(st_full, par);
         if (!__all_sync(0xffffffffu, ok)) break;
         tc_fence_after();
-#pragma unroll
+#pragma unroll 2
         for (int j = 0; j < DK / 16; ++j)
           mma_ss(lead, tmem + kColQS, q_rows + k_at + along(j), s_cols + down(j), idesc_bf16(DV, false, true), j > 0);
         mma_commit(lead, &q_empty[slot]);
@@ -419,7 +438,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         seen(p_full, par);
         if (!__all_sync(0xffffffffu, ok)) break;
         tc_fence_after();
-#pragma unroll
+#pragma unroll 2
         for (int j = 0; j < kChunk / 16; ++j)
           mma_ts(lead, tmem + kColPV, tmem + kColS + 8 * j, v_cols + down(j), idesc_bf16(DV, false, true), j > 0);
         mma_commit(lead, pv_done);
@@ -433,7 +452,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         if (!__all_sync(0xffffffffu, ok)) break;
         tc_fence_after();
         const uint64_t low = kStates && slot ? low2_cols : low_cols;
-#pragma unroll
+#pragma unroll 2
         for (int j = 0; j < kChunk / 16; ++j) {
           mma_ss(lead, tmem + kColState, k_cols + k_at + down(j), v_cols + down(j), idesc_bf16(DV, true, true),
                  !kStates || j > 0 || w.count > 0);
@@ -483,7 +502,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         else
           lo = max(marks.last(row), 0);
       }
-      ok = mbar_wait(s_full, w.parity(), abort_flag, err, kCode | 2);
+      ok = wait(s_full, w.parity(), abort_flag, err, kCode | 2);
       if (!__all_sync(0xffffffffu, ok)) break;
       tc_fence_after();
       // 16 columns at a time: units 0 .. 2 q + 1 in time, 2 q .. 7 against it; the next one's on their way
@@ -574,9 +593,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       const uint32_t keep = f == 0.0f ? 0u : 0xFFFFFFFFu;  // whatever a row that is cut off holds
       const float2 f2 = make_float2(f, f);
       const int slot = w.count & 1;
-      ok = mbar_wait(&k_full[slot], (w.count >> 1) & 1, abort_flag, err, kCode | 2);
-      if (!kStates && ok) ok = mbar_wait(s_full, w.parity(), abort_flag, err, kCode | 2);  // K has been read as it came
-      if (!kStates && w.count > 0 && ok) ok = mbar_wait(upd_done, w.parity() ^ 1u, abort_flag, err, kCode | 2);
+      ok = wait(&k_full[slot], (w.count >> 1) & 1, abort_flag, err, kCode | 2);
+      if (!kStates && ok) ok = wait(s_full, w.parity(), abort_flag, err, kCode | 2);  // K has been read as it came
+      if (!kStates && w.count > 0 && ok) ok = wait(upd_done, w.parity() ^ 1u, abort_flag, err, kCode | 2);
       if (!__all_sync(0xffffffffu, ok)) break;
       uint8_t* high = smem + L::k + slot * L::tile_k + row * 128;
       uint8_t* low = smem + (kStates && slot ? L::q : L::k_low) + row * 128;
@@ -653,101 +672,101 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       const int pair = last_pair;
       last_pair = -1;
       if (pair < 0 || !p.last) return;
-      const int batch = pair / static_cast<int>(p.heads), head = pair - batch * static_cast<int>(p.heads);
+      const int batch = quotient(pair, static_cast<int>(p.heads)), head = pair - batch * static_cast<int>(p.heads);
       const bool cut = kReverse && p.resets && p.resets[batch * p.length] != 0;
       put(p.last + pair * size, cut ? 0.0f : kReverse ? expf(p.log_decay[head]) : 1.0f);
     };
-    for (; !kStates && w.more(); w.next(p)) {
-      const Chunk c = chunk<kReverse>(p, w.block);
-      const bool cut = p.resets && Marks(p, w.batch, c).any();
-      decay.go(p, w.head);
-      const float f = cut ? 0.0f : power(decay.log2, c.n - 1 + c.e);
+    // one turn behind the last chunk, for the state behind it
+    for (; !kStates; w.next(p)) {
+      const bool more = w.more();
+      float f = 0.0f;
+      if (more) {
+        const Chunk c = chunk<kReverse>(p, w.block);
+        decay.go(p, w.head);
+        if (!(p.resets && Marks(p, w.batch, c).any())) f = power(decay.log2, c.n - 1 + c.e);
+      }
       // a state that comes from memory, 16 columns ahead
-      const bool fresh = w.block == 0 || w.count == 0 || w.left == w.turn;
+      const bool fresh = more && (w.block == 0 || w.count == 0 || w.left == w.turn);
       const bool transposed = w.block == 0 && p.init_transposed;
       const float* from = w.block > 0 ? p.local + blockIdx.x * size : p.init ? p.init + w.pair * size : nullptr;
       const bool wide = !transposed && (reinterpret_cast<uintptr_t>(from) & 31) == 0;
       uint32_t next[16];
-      auto fetch = [&](int b) {
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const int col = col0 + 16 * b + 8 * i;
-#pragma unroll
-          for (int j = 0; j < 8; ++j) next[8 * i + j] = 0u;
-          if (!from || row >= p.dk || col >= p.dv) continue;
-          if (wide) {
-            load8(from + row * p.dv + col, next + 8 * i);
-          } else {
-            const int step = transposed ? p.dk : 1;
-            const float* at8 = from + (transposed ? col * p.dk + row : row * p.dv + col);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) next[8 * i + j] = __float_as_uint(at8[j * step]);
-          }
-        }
-      };
-      if (fresh && mine) fetch(0);
-      if (w.count > 0) {
-        ok = mbar_wait(upd_done, w.parity() ^ 1u, abort_flag, err, kCode | 4);
-        if (!__all_sync(0xffffffffu, ok)) break;
-        tc_fence_after();
-        ended();
-      }
-      if (w.block + 1 == static_cast<int>(p.blocks)) last_pair = w.pair;
-      if (mine) {
 #pragma unroll 1
-        for (int b = 0; b < DV / 32; ++b) {
-          const int col = col0 + 16 * b;
-          uint32_t s[16];
-          __syncwarp();
-          if (fresh) {
-#pragma unroll
-            for (int i = 0; i < 16; ++i) s[i] = next[i];
-            if (b + 1 < DV / 32) fetch(b + 1);
-            __syncwarp();
-          } else {
-            tmem_ld_32x32b_x16(at + 16 * b, s);
-            loaded(s);
+      for (int b = fresh ? -1 : 0; b < DV / 32; ++b) {
+        if (b == 0) {
+          if (w.count > 0) {
+            ok = wait(upd_done, w.parity() ^ 1u, abort_flag, err, kCode | 4);
+            if (!__all_sync(0xffffffffu, ok)) break;
+            tc_fence_after();
+            ended();
           }
-          uint8_t* to = smem + L::s + (col >> 6) * DK * 128;
+          if (!more) break;
+          if (w.block + 1 == static_cast<int>(p.blocks)) last_pair = w.pair;
+        }
+        if (!mine) continue;
+        uint32_t s[16];
+        __syncwarp();
+        if (fresh) {
 #pragma unroll
-          for (int g = 0; g < 2; ++g) {
-            uint32_t o[4];
+          for (int i = 0; i < 16; ++i) s[i] = next[i];
+          if (b + 1 < DV / 32) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) o[i] = pack(__uint_as_float(s[8 * g + 2 * i]), __uint_as_float(s[8 * g + 2 * i + 1]));
-            sts128(to + tc::sw128(row, (col >> 3 & 7) + g), o[0], o[1], o[2], o[3]);
-          }
-          if (f == 0.0f) {  // whatever it holds
+            for (int i = 0; i < 2; ++i) {
+              const int col = col0 + 16 * (b + 1) + 8 * i;
 #pragma unroll
-            for (int i = 0; i < 16; ++i) s[i] = 0u;
-          } else {
+              for (int j = 0; j < 8; ++j) next[8 * i + j] = 0u;
+              if (!from || row >= p.dk || col >= p.dv) continue;
+              if (wide) {
+                load8(from + row * p.dv + col, next + 8 * i);
+              } else {
+                const int step = transposed ? p.dk : 1;
+                const float* at8 = from + (transposed ? col * p.dk + row : row * p.dv + col);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              const float2 x = __fmul2_rn(make_float2(__uint_as_float(s[2 * i]), __uint_as_float(s[2 * i + 1])), make_float2(f, f));
-              s[2 * i] = __float_as_uint(x.x);
-              s[2 * i + 1] = __float_as_uint(x.y);
+                for (int j = 0; j < 8; ++j) next[8 * i + j] = __float_as_uint(at8[j * step]);
+              }
             }
           }
+          if (b < 0) continue;
           __syncwarp();
-          tmem_st_x16(at + 16 * b, s);
+        } else {
+          tmem_ld_32x32b_x16(at + 16 * b, s);
+          loaded(s);
         }
-        tc2::tmem_wait_st();
+        const int col = col0 + 16 * b;
+        uint8_t* to = smem + L::s + (col >> 6) * DK * 128;
+#pragma unroll
+        for (int g = 0; g < 2; ++g) {
+          uint32_t o[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) o[i] = pack(__uint_as_float(s[8 * g + 2 * i]), __uint_as_float(s[8 * g + 2 * i + 1]));
+          sts128(to + tc::sw128(row, (col >> 3 & 7) + g), o[0], o[1], o[2], o[3]);
+        }
+        if (f == 0.0f) {  // whatever it holds
+#pragma unroll
+          for (int i = 0; i < 16; ++i) s[i] = 0u;
+        } else {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const float2 x = __fmul2_rn(make_float2(__uint_as_float(s[2 * i]), __uint_as_float(s[2 * i + 1])), make_float2(f, f));
+            s[2 * i] = __float_as_uint(x.x);
+            s[2 * i + 1] = __float_as_uint(x.y);
+          }
+        }
+        __syncwarp();
+        tmem_st_x16(at + 16 * b, s);
       }
+      if (!__all_sync(0xffffffffu, ok) || !more) break;
+      tc2::tmem_wait_st();
       fence_proxy_async_smem();
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(st_full);
     }
     if (kStates && w.more()) {
-      ok = mbar_wait(end_bar, 0, abort_flag, err, kCode | 4);
+      ok = wait(end_bar, 0, abort_flag, err, kCode | 4);
       if (__all_sync(0xffffffffu, ok)) {
         tc_fence_after();
         put(p.local + (blockIdx.x + 1) * size, 1.0f);
-      }
-    } else if (!kStates && ok && w.count > 0) {
-      ok = mbar_wait(upd_done, w.parity() ^ 1u, abort_flag, err, kCode | 4);
-      if (__all_sync(0xffffffffu, ok)) {
-        tc_fence_after();
-        ended();
       }
     }
   } else if (warp >= kWarpO) {
@@ -769,7 +788,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       decay.go(p, w.head);
       const float f = alive ? p.out_scale * power(decay.log2, pos + c.e) : 0.0f;
       bf16* out = static_cast<bf16*>(p.o) + (w.batch * p.length + c.t0 + row) * p.ldo + w.head * p.dv;
-      ok = mbar_wait(o_full, w.parity(), abort_flag, err, kCode | 4);
+      ok = wait(o_full, w.parity(), abort_flag, err, kCode | 4);
       if (!__all_sync(0xffffffffu, ok)) break;
       tc_fence_after();
 #pragma unroll 1
