@@ -113,6 +113,11 @@ __device__ __forceinline__ void tmem_st_x16(uint32_t taddr, const uint32_t (&v)[
       : "memory");
 }
 
+// `bytes` of memory on their way to L2, multiples of 16 at a multiple of 16.
+__device__ __forceinline__ void prefetch_l2(const void* p, int bytes) {
+  asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p), "r"(bytes) : "memory");
+}
+
 // 32 bytes at once: a row a lane, so that each takes a whole sector.
 __device__ __forceinline__ void load8(const float* p, uint32_t* v) {
   asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
@@ -190,6 +195,8 @@ struct Walk {
     batch = quotient(pair, static_cast<int>(p.heads));
     head = pair - batch * static_cast<int>(p.heads);
   }
+  // The state comes from memory: at a sequence's begin, and at that of the range
+  __device__ __forceinline__ bool fresh() const { return block == 0 || count == 0 || left == turn; }
   __device__ __forceinline__ bool more() const { return left > 0; }
   __device__ __forceinline__ uint32_t parity() const { return count & 1; }
 };
@@ -211,6 +218,12 @@ __device__ __forceinline__ Walk walk(const Args& p) {
   }
   w.go(p, w.left > 0 ? at : 0);
   return w;
+}
+
+// The state that a walk's chunk takes from memory; null: zeros.
+__device__ __forceinline__ const float* state_from(const Args& p, const Walk& w) {
+  const int64_t size = static_cast<int64_t>(p.dk) * p.dv;
+  return w.block > 0 ? p.local + blockIdx.x * size : p.init ? p.init + w.pair * size : nullptr;
 }
 
 // A chunk: its first token, tokens, and whether it begins a reversed pass.
@@ -360,6 +373,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           if (more) {
             load_q(w);
             if (ok) load_k(w);
+            const float* state = state_from(p, w);
+            if (w.fresh() && w.count > 0 && (reinterpret_cast<uintptr_t>(state) & 15) == 0 && state)
+              prefetch_l2(state, p.dk * p.dv * 4);
           }
           if (ok && w.count > 0) load_v(before);
           if (!more) break;
@@ -686,9 +702,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         if (!(p.resets && Marks(p, w.batch, c).any())) f = power(decay.log2, c.n - 1 + c.e);
       }
       // a state that comes from memory, 16 columns ahead
-      const bool fresh = more && (w.block == 0 || w.count == 0 || w.left == w.turn);
+      const bool fresh = more && w.fresh();
       const bool transposed = w.block == 0 && p.init_transposed;
-      const float* from = w.block > 0 ? p.local + blockIdx.x * size : p.init ? p.init + w.pair * size : nullptr;
+      const float* from = state_from(p, w);
       const bool wide = !transposed && (reinterpret_cast<uintptr_t>(from) & 31) == 0;
       uint32_t next[16];
 #pragma unroll 1
