@@ -435,7 +435,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         seen(&k_full[slot], par2);
         if (!__all_sync(0xffffffffu, ok)) break;
         tc_fence_after();
-#pragma unroll 2
+#pragma unroll 4
         for (int j = 0; j < DK / 16; ++j)
           mma_ss(lead, tmem + kColS, q_rows + k_at + along(j), k_rows + k_at + along(j), idesc_bf16(128, false, false), j > 0);
         issued = true;
@@ -445,7 +445,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         seen(st_full, par);
         if (!__all_sync(0xffffffffu, ok)) break;
         tc_fence_after();
-#pragma unroll 2
+#pragma unroll 4
         for (int j = 0; j < DK / 16; ++j)
           mma_ss(lead, tmem + kColQS, q_rows + k_at + along(j), s_cols + down(j), idesc_bf16(DV, false, true), j > 0);
         mma_commit(lead, &q_empty[slot]);
@@ -454,7 +454,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         seen(p_full, par);
         if (!__all_sync(0xffffffffu, ok)) break;
         tc_fence_after();
-#pragma unroll 2
+#pragma unroll 4
         for (int j = 0; j < kChunk / 16; ++j)
           mma_ts(lead, tmem + kColPV, tmem + kColS + 8 * j, v_cols + down(j), idesc_bf16(DV, false, true), j > 0);
         mma_commit(lead, pv_done);
@@ -468,7 +468,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         if (!__all_sync(0xffffffffu, ok)) break;
         tc_fence_after();
         const uint64_t low = kStates && slot ? low2_cols : low_cols;
-#pragma unroll 2
+#pragma unroll 4
         for (int j = 0; j < kChunk / 16; ++j) {
           mma_ss(lead, tmem + kColState, k_cols + k_at + down(j), v_cols + down(j), idesc_bf16(DV, true, true),
                  !kStates || j > 0 || w.count > 0);
