@@ -36,10 +36,14 @@ constexpr int smem_floats(int dk) {
 
 constexpr float kCut = 2.0f;  // a token whose state starts anew, among the factors
 
-// One token: S = S + c S (kSlow) or c S, plus k v^T, and this warp's part of S^T q.
-template <bool kSlow, bool kStates>
+// How a token is taken: S = S + c S + k v^T, or S = c S + k v^T; for the states alone S = S + k v^T, with
+// the decays up to the end in v.
+enum Take { kSlow, kFast, kStates };
+
+// One token, and this warp's part of S^T q.
+template <Take kTake>
 __device__ __forceinline__ float token(float2 (&S)[kRows / 2], float c, float v, const float4* k, const float4* q) {
-  if (c == kCut) {  // whatever the state held
+  if (kTake != kStates && c == kCut) {  // whatever the state held
     c = 0.0f;
 #pragma unroll
     for (int i = 0; i < kRows / 2; ++i) S[i] = make_float2(0.0f, 0.0f);
@@ -50,9 +54,9 @@ __device__ __forceinline__ float token(float2 (&S)[kRows / 2], float c, float v,
   for (int i = 0; i < kRows / 4; ++i) {
     const float4 k4 = k[i];
     float2 &a = S[2 * i], &b = S[2 * i + 1];
-    a = __ffma2_rn(make_float2(k4.x, k4.y), v2, kSlow ? __ffma2_rn(a, c2, a) : __fmul2_rn(a, c2));
-    b = __ffma2_rn(make_float2(k4.z, k4.w), v2, kSlow ? __ffma2_rn(b, c2, b) : __fmul2_rn(b, c2));
-    if (!kStates) {
+    a = __ffma2_rn(make_float2(k4.x, k4.y), v2, kTake == kSlow ? __ffma2_rn(a, c2, a) : kTake == kFast ? __fmul2_rn(a, c2) : a);
+    b = __ffma2_rn(make_float2(k4.z, k4.w), v2, kTake == kSlow ? __ffma2_rn(b, c2, b) : kTake == kFast ? __fmul2_rn(b, c2) : b);
+    if (kTake != kStates) {
       const float4 q4 = q[i];
       sum = __ffma2_rn(make_float2(q4.x, q4.y), a, sum);
       sum2 = __ffma2_rn(make_float2(q4.z, q4.w), b, sum2);
@@ -116,21 +120,21 @@ __device__ __forceinline__ void fetch(const Args& p, const Where& w, int rows, i
   }
 }
 
-// kStates: only what each part's last piece adds to the state (Args::local).
-template <class T, bool kReverse, bool kStates>
+// kAlone: only what each part's last piece adds to the state (Args::local).
+template <class T, bool kReverse, bool kAlone>
 __global__ void __launch_bounds__(kMaxHead / kRows * 32, 2) linear_tokens_kernel(const Args p, int col_blocks) {
   extern __shared__ __align__(16) float sm[];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
   const int part = blockIdx.x / col_blocks, col = (blockIdx.x - part * col_blocks) * kCols + lane;
   const int rows = warps * kRows;
-  // twice: k and q [tokens][rows], v [tokens][kCols], the factors [tokens]; then the sums [warps][tokens][kCols]
+  // twice: k and q [tokens][rows], v [tokens][kCols], the factors [tokens]; twice the sums [warps][tokens][kCols]
   const int block_floats = kTokens * (2 * rows + kCols + 1);
   float* sums = sm + 2 * block_floats;
   launch_dependents();
   grid_dependency_wait();
   const int blocks = static_cast<int>(p.blocks);
   int at = part_begin(p, part), end = part_begin(p, part + 1);
-  if (kStates) {
+  if (kAlone) {
     int pair, b0, b1;
     if (!cut_piece(p, part, pair, b0, b1)) return;
     at = pair * blocks + b0;
@@ -142,49 +146,69 @@ __global__ void __launch_bounds__(kMaxHead / kRows * 32, 2) linear_tokens_kernel
   const bool has_col = col < p.dv;
   float2 S[kRows / 2];
   bool fresh = true;  // the state is still to be loaded
-  int decays = 0;  // of a state that passes this piece, and whether something cuts it off
-  bool cut_off = false;
 
   Where w = locate<kReverse>(p, at / blocks, at % blocks), next = w;
+  // kAlone: the piece's tokens, counted in the order they are taken, and the last one of them that is cut off from the one
+  // in front: those in front of it are not in the state
+  int tau0 = 0, tau1 = 0, edge = -1;
+  auto tau = [&](const Where& x) { return static_cast<int>(kReverse ? p.length - x.t0 - x.n : x.t0); };
+  if (kAlone) {
+    const Where last = locate<kReverse>(p, w.pair, w.block + (end - at) - 1);
+    tau0 = tau(w);
+    tau1 = tau(last) + last.n;
+    if (p.resets) {
+      const uint8_t* marks = p.resets + w.batch * p.length;
+      for (int i = tau0 + lane; i < tau1; i += 32)
+        if (kReverse ? i > 0 && marks[p.length - i] != 0 : marks[i] != 0) edge = max(edge, i);
+      edge = __reduce_max_sync(0xffffffffu, edge);
+    }
+  }
   Rows<T> x;
   float log_decay = 0.0f;
   auto put = [&](float* to) {
     const bool slow = log_decay > -kLn2;
     const int r = threadIdx.x;  // k's rows, then q's
-    if (!(kStates && r >= rows)) {
+    const int dead = kAlone ? edge - tau(next) : 0;  // so many of the block's first tokens
+    if (!(kAlone && r >= rows)) {
       float* kq = to + (r >= rows ? kTokens * rows + r - rows : r);
 #pragma unroll
-      for (int j = 0; j < kTokens; ++j) kq[j * rows] = as_float(x.kq[j]);
+      for (int j = 0; j < kTokens; ++j) kq[j * rows] = kAlone && j < dead ? 0.0f : as_float(x.kq[j]);
     }
     float* vs = to + 2 * kTokens * rows;
+    const int behind = tau1 - 1 - tau(next);
 #pragma unroll
-    for (int i = 0; i < kTokens / 2; ++i)
-      if (i * warps + warp < kTokens) vs[(i * warps + warp) * kCols + lane] = p.in_scale * as_float(x.v[i]);
-    if (threadIdx.x < kTokens)  // of the state from token to token, and where it comes from behind the last token
+    for (int i = 0; i < kTokens / 2; ++i) {
+      const int j = i * warps + warp;
+      if (j >= kTokens) break;
+      float f = p.in_scale;
+      if (kAlone && j < behind) f *= expf(log_decay * static_cast<float>(behind - j));
+      vs[j * kCols + lane] = kAlone && j < dead ? 0.0f : f * as_float(x.v[i]);
+    }
+    if (!kAlone && threadIdx.x < kTokens)  // of the state from token to token, and where it comes from behind the last token
       vs[kTokens * kCols + threadIdx.x] = x.mark ? kCut
                                           : kReverse && next.t0 + next.n - threadIdx.x == p.length ? (slow ? 0.0f : 1.0f)
                                           : slow ? expm1f(log_decay) : expf(log_decay);
   };
-  fetch<T, kReverse, kStates>(p, w, rows, col, x);
+  fetch<T, kReverse, kAlone>(p, w, rows, col, x);
   log_decay = p.log_decay[w.head];
   put(sm);
   __syncthreads();
   for (int turn = 0; at < end; ++at, turn ^= 1) {
     const bool slow = log_decay > -kLn2;
-    const float this_decay = log_decay;
+    const float log_decay_now = log_decay;
     if (at + 1 < end) {
       const bool ends = w.block + 1 == blocks;
       next = locate<kReverse>(p, ends ? w.pair + 1 : w.pair, ends ? 0 : w.block + 1);
-      fetch<T, kReverse, kStates>(p, next, rows, col, x);
+      fetch<T, kReverse, kAlone>(p, next, rows, col, x);
       log_decay = p.log_decay[next.head];
     }
     const int64_t state_at = static_cast<int64_t>(w.pair) * p.dk * p.dv;
     if (fresh || w.block == 0) {
       fresh = false;
-      const bool inside = w.block > 0 && !kStates;  // behind a cut
+      const bool inside = w.block > 0 && !kAlone;  // behind a cut
       const float* from = inside ? p.local + static_cast<int64_t>(part) * p.dk * p.dv : p.init ? p.init + state_at : nullptr;
       const bool transposed = !inside && p.init_transposed;
-      const bool there = from && has_col && !kStates;
+      const bool there = from && has_col && !kAlone;
 #pragma unroll
       for (int i = 0; i < kRows; ++i) {
         const int r = warp * kRows + i;
@@ -201,26 +225,24 @@ __global__ void __launch_bounds__(kMaxHead / kRows * 32, 2) linear_tokens_kernel
     const float4* kp = reinterpret_cast<const float4*>(ks + warp * kRows);
     const float4* qp = reinterpret_cast<const float4*>(ks + kTokens * rows + warp * kRows);
     float* os = sums + (turn * warps + warp) * kTokens * kCols + lane;
-    auto take = [&](auto is_slow) {
-      constexpr bool kSlow = decltype(is_slow)::value;
+    auto take = [&](auto how) {
+      constexpr Take kTake = decltype(how)::value;
 #pragma unroll 2
       for (int j = 0; j < w.n; ++j) {
-        const float c = cs[j];
-        if (kStates) {
-          decays += c != (kSlow ? 0.0f : 1.0f);
-          cut_off |= c == kCut;
-        }
-        const float y = token<kSlow, kStates>(S, c, vs[j * kCols], kp + j * (rows / 4), qp + j * (rows / 4));
-        if (!kStates) os[j * kCols] = y;
+        const float y = token<kTake>(S, kTake == kStates ? 0.0f : cs[j], vs[j * kCols], kp + j * (rows / 4), qp + j * (rows / 4));
+        if (kTake != kStates) os[j * kCols] = y;
       }
     };
-    if (slow)
-      take(std::true_type());
-    else
-      take(std::false_type());
+    if (kAlone) {
+      take(std::integral_constant<Take, kStates>());
+    } else if (slow) {
+      take(std::integral_constant<Take, kSlow>());
+    } else {
+      take(std::integral_constant<Take, kFast>());
+    }
     if (at + 1 < end) put(sm + (turn ^ 1) * block_floats);
     __syncthreads();
-    if (!kStates && has_col) {
+    if (!kAlone && has_col) {
       const float* from = sums + turn * warps * kTokens * kCols + lane;
       for (int j = warp; j < w.n; j += warps) {
         float y = 0.0f;
@@ -229,20 +251,22 @@ __global__ void __launch_bounds__(kMaxHead / kRows * 32, 2) linear_tokens_kernel
         store1(static_cast<T*>(p.o) + row * p.ldo + w.head * p.dv + col, p.out_scale * y);
       }
     }
-    const bool behind = !kStates && w.block + 1 == blocks && p.last;  // the sequence ends
-    if ((behind || (kStates && at + 1 == end)) && has_col) {
-      float* to = kStates ? p.local + static_cast<int64_t>(part + 1) * p.dk * p.dv : p.last + state_at;
+    const bool behind = !kAlone && w.block + 1 == blocks && p.last;  // the sequence ends
+    if ((behind || (kAlone && at + 1 == end)) && has_col) {
+      float* to = kAlone ? p.local + static_cast<int64_t>(part + 1) * p.dk * p.dv : p.last + state_at;
       // against time what is left is the gradient of the state in front of the first token
       const bool cut = kReverse && behind && p.resets && p.resets[w.batch * p.length] != 0;
-      const float f = kReverse && behind ? expf(this_decay) : 1.0f;
+      const float f = kReverse && behind ? expf(log_decay_now) : 1.0f;
 #pragma unroll
       for (int i = 0; i < kRows; ++i) {
         const int r = warp * kRows + i;
         const float y = i & 1 ? S[i / 2].y : S[i / 2].x;
         if (r < p.dk) to[r * p.dv + col] = cut || f == 0.0f ? 0.0f : f * y;
       }
-      if (kStates && threadIdx.x == 0 && col == 0)
-        p.pass[part + 1] = cut_off ? 0.0f : decays == 0 ? 1.0f : expf(this_decay * static_cast<float>(decays));
+      if (kAlone && threadIdx.x == 0 && col == 0) {
+        const int decays = tau1 - tau0 - (kReverse && tau0 == 0 ? 1 : 0);
+        p.pass[part + 1] = edge >= 0 ? 0.0f : decays == 0 ? 1.0f : expf(log_decay_now * static_cast<float>(decays));
+      }
     }
     w = next;
   }
@@ -440,9 +464,10 @@ int launch_linear_tokens(lin::Args p, bool reverse, int dtype, float* workspace,
   if (p.length == 1 && !reverse && !p.init_transposed && p.dv % 4 == 0 && aligned(p.init) && aligned(p.last))
     return dtype == T3_OUT_BF16 ? lin::run_step<vec::bf16>(p, sms, s) : lin::run_step<float>(p, sms, s);
   p.blocks = (p.length + lin::kTokens - 1) / lin::kTokens;
-  // about two CTAs an SM: whole sequences where there are as many, else cuts
-  const int64_t col_blocks = (p.dv + lin::kCols - 1) / lin::kCols, want = (2 * sms + col_blocks - 1) / col_blocks;
-  const int st = lin::cut(&p, p.pairs < want ? std::min<int64_t>(want, kMaxLinearParts) : p.pairs, workspace, s);
+  // as many CTAs as run at once (16 warps an SM): whole sequences where there are as many, else cuts
+  const int64_t col_blocks = (p.dv + lin::kCols - 1) / lin::kCols, warps = lin::padded(p.dk) / lin::kRows;
+  const int64_t want = std::min<int64_t>(sms * (16 / warps) / col_blocks, kMaxLinearParts);
+  const int st = lin::cut(&p, std::max(p.pairs, want), workspace, s);
   if (st != T3_OK) return st;
   if (dtype == T3_OUT_BF16)
     return reverse ? lin::run<vec::bf16, true>(p, s) : lin::run<vec::bf16, false>(p, s);
