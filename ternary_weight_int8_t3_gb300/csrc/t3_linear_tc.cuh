@@ -371,11 +371,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         while (ok) {
           const bool more = w.more();
           if (more) {
+            const float* state = state_from(p, w);
+            if (w.fresh() && (reinterpret_cast<uintptr_t>(state) & 15) == 0 && state) prefetch_l2(state, p.dk * p.dv * 4);
             load_q(w);
             if (ok) load_k(w);
-            const float* state = state_from(p, w);
-            if (w.fresh() && w.count > 0 && (reinterpret_cast<uintptr_t>(state) & 15) == 0 && state)
-              prefetch_l2(state, p.dk * p.dv * 4);
           }
           if (ok && w.count > 0) load_v(before);
           if (!more) break;
@@ -712,6 +711,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         if (b == 0) {
           if (w.count > 0) {
             ok = wait(upd_done, w.parity() ^ 1u, abort_flag, err, kCode | 4);
+            // and Q S has read the bf16 state: the two products have an issuer each, and it may be the later one
+            ok = ok && wait(&q_empty[(w.count - 1) & 1], ((w.count - 1) >> 1) & 1, abort_flag, err, kCode | 4);
             if (!__all_sync(0xffffffffu, ok)) break;
             tc_fence_after();
             ended();
