@@ -344,9 +344,11 @@ int t3_rmsnorm_bwd(const void* dy, int64_t lddy, const void* s, int64_t lds, con
  * be NULL.  The squares are of differences from a mean, so a row far from zero keeps its
  * deviation.  A row with y = 0 everywhere (equal elements without beta, whose deviations are rounding errors
  * of the mean at most) gives q = 0 and row_scale = 0; a row with an element of y that is
- * not finite, or whose squares overflow a float sum, row_scale = NaN and q = 0.  Everything else (gamma, sum_out, lengths of rows, alignment,
- * errors) is as in t3_rmsnorm_quant; longer rows than the registers hold are read five
- * times.  cols = 0 writes row_scale = 0, mean = 0 and rstd = 1 / sqrt(eps).
+ * not finite, or whose squares overflow a float sum, row_scale = NaN and q = 0.  gamma, sum_out and the
+ * errors are as in t3_rmsnorm_quant.  Rows that are 16-byte vectors alike in all arrays and have up to 16384
+ * columns (floats 12288; 8192 for the gradient) are read once; all others element by element, from memory
+ * again for every pass over a row (four, two for the gradient).  Odd rows that lie alike keep their vectors, as there.
+ * cols = 0 writes row_scale = 0, mean = 0 and rstd = 1 / sqrt(eps).
  */
 int t3_layernorm_quant(const void* x, int64_t ldx, const void* residual, int64_t ldr,
                        const float* gamma, const float* beta, float eps, int8_t* q,
@@ -433,8 +435,8 @@ int t3_gated_scan_bwd(const void* gate, int64_t ldg, const void* cand, int64_t l
  * q and v (o is off by about a rounding more than its own), what is added to the state is not (2^-17 of each
  * term).  A value of q, k or v that is not finite spoils its chunk in its head, tokens in front of it included.
  * Everything else is float, token by token.
- * T3_EINVAL: negative sizes or strides, sizes above 2^31 - 1 or heads above 128 elements, batch * heads above
- * 2^31 - 1, ldo < heads * dv, a null q, k, v, o or log_decay with a non-empty shape, an unknown dtype.
+ * T3_EINVAL: negative sizes or strides, sizes above 2^31 - 1 or heads above 128 elements, batch * heads *
+ * ceil(length / 16) above 2^31 - 1, ldo < heads * dv, a null q, k, v, o or log_decay with a non-empty shape, an unknown dtype.
  */
 int t3_linear_attn_fwd(const void* q, int64_t ldq, const void* k, int64_t ldk, const void* v,
                        int64_t ldv, const float* log_decay, const float* state,
@@ -579,7 +581,7 @@ const char* t3_status_string(int status);
  * 5 pair forwarder gave up; 6 an input value was invalid; 7 a CTA gave up
  * waiting for its cluster), bits 8-15 the kernel (4 small-M fwd;
  * 5 fwd, 6 dX, 7 dW on CTA pairs; 9 the device packer; 10 the wait self-test
- * below; 11 the gated recurrence).
+ * below; 11 the gated recurrence; 12 linear attention by chunks).
  */
 int t3_last_device_error(t3_stream_t stream, int32_t* detail);
 

@@ -14,7 +14,8 @@
 // reads and two writes).  Backward, a lane holds eight neighbouring columns (four floats, or one
 // where rows are not 16-byte vectors) and a CTA's eight warps take rows in turn, so that the
 // column sums stay in registers over all rows of the CTA; the CTA writes one partial
-// row, and a second kernel adds the partial rows in a fixed order.
+// row, and a second kernel adds the partial rows in a fixed order.  Measured, bf16: backward 16384 x 3456 107 us
+// (5.3 TB/s), 4096 x 3456 27.5; forward behind the two products of 27 x 8192 x 8192 2 of 26 us.
 #include <algorithm>
 
 #include "t3_vec.cuh"

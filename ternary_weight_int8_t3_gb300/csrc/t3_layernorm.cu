@@ -23,6 +23,10 @@
 // alone, so that it needs no barrier.  Operands whose rows lie differently to 16-byte boundaries, and
 // rows longer than a CTA holds, go element by element and are read again from memory for every
 // pass.  Column sums as in t3_norm.cu: partial rows, added in a fixed order.
+//
+// Measured (replays of a graph).  bf16 with residual and shift: 16384 x 1280 forward 28 us (5.8 TB/s), 16384 x 3456 68 (5.8)
+// and 99 backward (5.0: 311 instructions a warp and row, half of the issue slots), 4096 x 8192 45 and 64, 1 x
+// 8192 4.6.  float: 16384 x 1280 50 and 57, 8192 x 3456 65 and 75, 1782 x 729 5.8 and 14.
 #include <algorithm>
 
 #include "t3_norm.cuh"

@@ -204,7 +204,9 @@ constexpr int kModeAct = 4;
 // Two forwards over one A with their product in the epilogue (operands by TMA, whole tiles, f32 or
 // bf16 output): the even CTA of a pair decodes 96 rows of the gate's weights and the odd
 // CTA the same 96 of the other's, so that a tile's accumulator holds both sums of 96 output columns
-// (the gate's in columns 0 to 95, the other's behind) and the main loop is the forward's own.
+// (the gate's in columns 0 to 95, the other's behind) and the main loop is the forward's own.  16384 x 3456 x
+// 1280 in bf16 with SiLU: 222 us, 1304 TFLOP/s, where the int32 product alone takes 117 for each of the two; with GELU, biases and both
+// pre-activations 235.
 constexpr int kModeGlu = 5;
 // Instantiations with a layer's epilogue.
 __host__ __device__ constexpr bool layer_epilogue(int mode) { return mode == kModeAct || mode == kModeGlu; }
