@@ -19,8 +19,8 @@
 // Measured: that case 167 us forward and 500 backward (twelve warps an SM that read q and k four rows at a time: shared memory
 // is in use 60 % of the time, the float units 50 %); 2 x 2048 of 8 float heads of 128 175 and 532.  Decays kept out of the inner
 // loop, in v and o, as for the states alone: 1.05 times as fast in parts of sequences, 0.93 in whole ones.
-// One token of 27 sequences and 64 heads of 128 x 128: 48.5 us, 4.7 TB/s (two CTAs an SM, 16 rows of 16 bytes a
-// thread on their way; one element a thread and row took 77).
+// One token of 27 sequences and 64 heads of 128 x 128: 40.7 us, 5.6 TB/s (eight CTAs an SM, 8 rows of 16 bytes a
+// thread on their way; whole states a CTA and 16 rows a thread 48, 4 rows 59, one element a thread and row 77).
 #include <type_traits>
 
 #include "t3_linear.cuh"
@@ -282,18 +282,19 @@ __global__ void __launch_bounds__(kMaxHead / kRows * 32, 2) linear_tokens_kernel
   }
 }
 
-// One token a sequence, its state read once and written once, 16 bytes a thread and row, all of a thread's 16 rows on
-// their way at a time.  A CTA takes `cols` columns of a state; `lanes` lanes (a power of two, 4 columns each) share a row.
-constexpr int kStepRows = 16;
+// One token a sequence, its state read once and written once, 16 bytes a thread and row, all of a thread's 8 rows on
+// their way at a time.  A CTA takes 32 columns of a state; `lanes` lanes (a power of two, 4 columns each) share a row.
+constexpr int kStepRows = 8, kStepCols = 32;
+constexpr int kStepWarps = kMaxHead / (kStepRows * 32 / (kStepCols / 4));
 
 template <class T>
-__global__ void __launch_bounds__(kMaxHead / kStepRows * 32, 2) linear_step_kernel(const Args p, int cols, int lanes, int col_blocks) {
-  __shared__ float4 sums[kMaxHead / kStepRows][32];
+__global__ void __launch_bounds__(kStepWarps * 32, 8) linear_step_kernel(const Args p, int lanes, int col_blocks) {
+  __shared__ float4 sums[kStepWarps][32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
-  const int pair = blockIdx.x / col_blocks, col0 = (blockIdx.x - pair * col_blocks) * cols;
+  const int pair = blockIdx.x / col_blocks, col0 = (blockIdx.x - pair * col_blocks) * kStepCols;
   const int sub = lane / lanes, c = (lane - sub * lanes) * 4, col = col0 + c, step = 32 / lanes;
   const int row0 = warp * kStepRows * step + sub;
-  const bool has_col = c < cols && col < p.dv;
+  const bool has_col = col < p.dv;
   const int64_t batch = pair / static_cast<int>(p.heads), head = pair - batch * p.heads;
   const int64_t at = static_cast<int64_t>(pair) * p.dk * p.dv + static_cast<int64_t>(row0) * p.dv + col;
   launch_dependents();
@@ -327,8 +328,7 @@ __global__ void __launch_bounds__(kMaxHead / kStepRows * 32, 2) linear_step_kern
   sums[warp][lane] = sum;
   __syncthreads();
   // o: over the warps and the rows of each
-  for (int i = threadIdx.x; i < cols; i += blockDim.x) {
-    if (col0 + i >= p.dv) break;
+  for (int i = threadIdx.x; i < kStepCols && col0 + i < p.dv; i += blockDim.x) {
     float y = 0.0f;
     for (int w = 0; w < warps; ++w)
       for (int u = 0; u < step; ++u) y += reinterpret_cast<const float*>(&sums[w][u * lanes])[i];
@@ -337,13 +337,11 @@ __global__ void __launch_bounds__(kMaxHead / kStepRows * 32, 2) linear_step_kern
 }
 
 template <class T>
-int run_step(const Args& p, int sms, cudaStream_t s) {
-  // A state's columns go to CTAs of 32 each while that leaves none of the SMs with two
-  const int cols = p.pairs * ((p.dv + 31) / 32) <= 2 * sms ? 32 : (p.dv + 3) / 4 * 4;
+int run_step(const Args& p, cudaStream_t s) {
   int lanes = 1;
-  while (4 * lanes < cols && 4 * lanes < p.dv) lanes *= 2;
-  const int rows = kStepRows * (32 / lanes), warps = (p.dk + rows - 1) / rows, col_blocks = (p.dv + cols - 1) / cols;
-  return launch(linear_step_kernel<T>, p.pairs * col_blocks, warps * 32, 0, s, 1, p, cols, lanes, col_blocks);
+  while (4 * lanes < kStepCols && 4 * lanes < p.dv) lanes *= 2;
+  const int rows = kStepRows * (32 / lanes), warps = (p.dk + rows - 1) / rows, col_blocks = (p.dv + kStepCols - 1) / kStepCols;
+  return launch(linear_step_kernel<T>, p.pairs * col_blocks, warps * 32, 0, s, 1, p, lanes, col_blocks);
 }
 
 // The states in front of the ranges that begin inside a sequence: what the piece before adds, plus what is left
@@ -472,7 +470,7 @@ int run(const Args& p, cudaStream_t s) {
 int launch_linear_tokens(lin::Args p, bool reverse, int dtype, float* workspace, int sms, cudaStream_t s) {
   const auto aligned = [](const void* x) { return reinterpret_cast<uintptr_t>(x) % 16 == 0; };
   if (p.length == 1 && !reverse && !p.init_transposed && p.dv % 4 == 0 && aligned(p.init) && aligned(p.last))
-    return dtype == T3_OUT_BF16 ? lin::run_step<vec::bf16>(p, sms, s) : lin::run_step<float>(p, sms, s);
+    return dtype == T3_OUT_BF16 ? lin::run_step<vec::bf16>(p, s) : lin::run_step<float>(p, s);
   p.blocks = (p.length + lin::kTokens - 1) / lin::kTokens;
   // as many CTAs as run at once (16 warps an SM): whole sequences where there are as many, else cuts
   const int64_t col_blocks = (p.dv + lin::kCols - 1) / lin::kCols, warps = lin::padded(p.dk) / lin::kRows;
