@@ -522,10 +522,12 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       if (p.resets) {
         const Marks marks(p, w.batch, chunk<kReverse>(p, w.block));
         marked = marks.any();
-        if (kReverse)
-          hi = marks.first(row + 1) - 1;
-        else
-          lo = max(marks.last(row), 0);
+        if (marked) {
+          if (kReverse)
+            hi = marks.first(row + 1) - 1;
+          else
+            lo = max(marks.last(row), 0);
+        }
       }
       ok = wait(s_full, w.parity(), abort_flag, err, kCode | 2);
       if (!__all_sync(0xffffffffu, ok)) break;
@@ -611,7 +613,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         alive = alive && (kReverse ? c.t0 + row < edge : c.t0 + row >= edge);
       } else if (p.resets) {
         const Marks marks(p, w.batch, c);
-        alive = alive && (kReverse ? marks.first(0) > row : marks.last(kChunk - 1) <= row);
+        if (marks.any()) alive = alive && (kReverse ? marks.first(0) > row : marks.last(kChunk - 1) <= row);
       }
       decay.go(p, w.head);
       const float f = alive ? p.in_scale * power(decay.log2, away) : 0.0f;
@@ -810,7 +812,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       if (p.resets) {
         const Marks marks(p, w.batch, c);
         marked = marks.any();
-        alive = alive && (kReverse ? marks.first(row + 1) >= kChunk : marks.last(row) < 0);
+        if (marked) alive = alive && (kReverse ? marks.first(row + 1) >= kChunk : marks.last(row) < 0);
       }
       decay.go(p, w.head);
       const float f = alive ? p.out_scale * power(decay.log2, pos + c.e) : 0.0f;
