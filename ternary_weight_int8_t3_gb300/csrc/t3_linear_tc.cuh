@@ -23,15 +23,20 @@
 // table read at the distance, zeros where it is negative: no exponential an element, and no coefficient above 1.
 // The pass for the states alone takes K' decayed to the end of the piece, so that it is one long product.
 //
-// Measured (bf16, replays of a graph).  8 x 2048 tokens of 27 heads of 128: forward 126 us, 3.8 TB/s: 101 us of it this kernel, 19
+// Measured (bf16, replays of a graph).  8 x 2048 tokens of 27 heads of 128: forward 125 us, 3.8 TB/s: 100 us of it this kernel, 19
 // the states of the ranges that the last 64 of 216 sequences are cut into, the rest joining those;
-// gradient 370, three such passes.  54 heads of 64: 142 and 428.  1 x 16384 of 10 heads of 128: 74 (states 23, join 8, this 47)
+// gradient 369, three such passes.  54 heads of 64: 132 and 394.  1 x 16384 of 10 heads of 128: 73 (states 23, join 8, this 47)
 // and 213.  In the middle of a sequence a chunk takes 6500 clocks, where memory's rate allows 6000; what is
 // lost lies at the ends: a sequence's begin and end cost 4000 to 10000 clocks more, a kernel's begin
 // as much.  A state on its way through shared memory in whole lines instead of a row a lane took 5 % longer,
 // and so did P by eight warps (K' by four), 32 warps with 64 registers 15 %.
 // The roles' code together is more than the instruction cache next to a scheduler holds: with every wait, mark and division
-// written out at its place and the products' loops unrolled (82 KB instead of 54) the first case took 148 us.
+// written out at its place and the products' loops unrolled (82 KB instead of 51) the first case took 148 us.
+//
+// Marks.  Where a chunk has any, documents meet in it, and zero times a value that is not finite would pass from one to
+// another: P is masked by selection, K' by bits, and rows of V are looked through (by the warps of K') and cleared,
+// with NaN in P and K' in their place.  Documents of 300 tokens on average: the first case 170 us (139 without the look at V, which waits for
+// V's one place) and gradient 511.
 //
 // Heads are taken as 64 or 128 elements, zeros behind their own (DK, DV; a file for each pair of them, so that they compile
 // in parallel).
@@ -60,9 +65,10 @@ template <int DK, int DV> struct Smem {
   static constexpr int s = q + 2 * tile_k;     // the state as bf16, [DK][64] halves
   static constexpr int tables = s + state;     // a warp of P each: see kTable
   static constexpr int bars = tables + 4 * kTable * 4;
-  static constexpr int n_bars = 26;
+  static constexpr int n_bars = 27;
   static constexpr int misc = bars + 8 * n_bars;
-  static constexpr int bytes = misc + 16 + 1024;
+  static constexpr int bad = (misc + 8 + 15) / 16 * 16;  // a bit a token, for each half of its row of V; one marked chunk's and the next's
+  static constexpr int bytes = bad + 64 + 1024;
   static_assert(bytes <= 227 * 1024, "shared memory budget");
   // 64 rows of the state: its product is taken with 128, of which the upper half reads whatever lies
   // 64 columns on
@@ -292,8 +298,25 @@ struct Marks {
   __device__ __forceinline__ int first(int i) const { return first_mark(w, i); }
 };
 
-// kStates: only what each part's last piece adds to the state (Args::local).
-template <int DK, int DV, bool kReverse, bool kStates>
+// Whether `pieces` of 16 bytes of a row of V hold a value that is not finite; they are cleared then.  Zero times it would be
+// NaN in the rows of other documents: what it spoils of its own is marked in P and K' instead.
+static __device__ __noinline__ bool clear_bad(uint8_t* row, int pieces) {
+  bool bad = false;
+#pragma unroll 4
+  for (int g = 0; g < pieces; ++g) {
+    const uint4 x = *reinterpret_cast<const uint4*>(row + 16 * g);
+    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) bad |= (w[i] & 0x7F80u) == 0x7F80u || (w[i] & 0x7F800000u) == 0x7F800000u;
+  }
+  if (bad)
+    for (int g = 0; g < pieces; ++g) *reinterpret_cast<uint4*>(row + 16 * g) = make_uint4(0u, 0u, 0u, 0u);
+  return bad;
+}
+
+// kStates: only what each part's last piece adds to the state (Args::local).  kMarks: with resets, whose code the others
+// are faster without (8 x 2048 tokens of 54 heads of 64 132 us for 148).
+template <int DK, int DV, bool kReverse, bool kStates, bool kMarks>
 __global__ void __launch_bounds__(kTcThreads, 1)
     linear_tc_kernel(const Args p, const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
                      const __grid_constant__ CUtensorMap map_v, int* err) {
@@ -309,13 +332,16 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   uint64_t *kp_full = bars + 17, *st_full = bars + 19;                    // or eight
   uint64_t* drain = bars + 20;                                            // one for each issuer
   uint64_t *q_full = bars + 22, *q_empty = bars + 24;                     // one arrival, two of each
+  uint64_t* v_seen = bars + 26;                                           // the warps of K', where a chunk has marks
+  uint32_t* bad = reinterpret_cast<uint32_t*>(smem + L::bad);
+  int marked_chunks = 0;                                                  // so far
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(smem + L::misc);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::misc + 4);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < L::n_bars; ++i)
-      mbar_init(bars + i, i < 13 ? 1 : i < 15 ? (kStates ? 1 : 2) : i < 17 ? 4 : i < 20 ? 8 : 1);
+      mbar_init(bars + i, i < 13 ? 1 : i < 15 ? (kStates ? 1 : 2) : i < 17 ? 4 : i < 20 ? 8 : i == 26 ? 8 : 1);
     *abort_flag = 0;
     fence_mbarrier_init();
   }
@@ -516,17 +542,17 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         over32 = power(decay.log2, 32);
         __syncwarp();
       }
-      // the columns that count: in time lo .. row, against it row .. hi
+      // the columns that count where there are marks (where there are none, zeros in the table leave out the others)
       int lo = 0, hi = kChunk - 1;
       bool marked = false;
-      if (p.resets) {
+      if (kMarks) {
         const Marks marks(p, w.batch, chunk<kReverse>(p, w.block));
         marked = marks.any();
         if (marked) {
           if (kReverse)
-            hi = marks.first(row + 1) - 1;
+            lo = row, hi = marks.first(row + 1) - 1;
           else
-            lo = max(marks.last(row), 0);
+            lo = max(marks.last(row), 0), hi = row;
         }
       }
       ok = wait(s_full, w.parity(), abort_flag, err, kCode | 2);
@@ -581,6 +607,30 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       for (int u = 0; u < 8; ++u)
         if (u < u0 || u >= u1) tmem_st_x8(at + 8 * u, none);
       tc2::tmem_wait_st();
+      if (marked) {  // what V holds that is not finite spoils the rows of its document
+        ok = wait(v_seen, marked_chunks & 1, abort_flag, err, kCode | 2);
+        if (!__all_sync(0xffffffffu, ok)) break;
+        const uint32_t* words = bad + 8 * (marked_chunks & 1);
+        ++marked_chunks;
+#pragma unroll 1
+        for (int b = 0; b < 4; ++b) {
+          const uint32_t spoilt = words[b] | words[4 + b];
+          if (spoilt == 0u) continue;
+          uint32_t v[16];
+          __syncwarp();
+          tmem_ld_32x32b_x16(at + 16 * b, v);
+          loaded(v);
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            const int j = 32 * b + 2 * i;
+            if (spoilt >> (2 * i) & 1 && j >= lo && j <= hi) v[i] |= 0x7FFFu;
+            if (spoilt >> (2 * i + 1) & 1 && j + 1 >= lo && j + 1 <= hi) v[i] |= 0x7FFF0000u;
+          }
+          __syncwarp();
+          tmem_st_x16(at + 16 * b, v);
+        }
+        tc2::tmem_wait_st();
+      }
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(p_full);
@@ -596,7 +646,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       const Chunk first = chunk<kReverse>(p, w.block), end = chunk<kReverse>(p, w.block + w.left - 1);
       const int t0 = kReverse ? end.t0 : first.t0, t1 = kReverse ? first.t0 + first.n : end.t0 + end.n;
       behind = t1 - t0;
-      if (p.resets) {
+      if (kMarks) {
         for (int t = t0 + lane; t < t1; t += 32)
           if (p.resets[w.batch * p.length + t] != 0) edge = kReverse ? min(edge, t) : max(edge, t);
         edge = kReverse ? __reduce_min_sync(0xffffffffu, edge) : __reduce_max_sync(0xffffffffu, edge);
@@ -605,15 +655,16 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     for (; w.more(); w.next(p)) {
       const Chunk c = chunk<kReverse>(p, w.block);
       // whether this token's row is still in the state in the end, and behind how many tokens
-      bool alive = row < c.n;
+      bool alive = row < c.n, marked = false;
       int away = kReverse ? row : c.n - 1 - row;
       if (kStates) {
         behind -= c.n;
         away += behind;
         alive = alive && (kReverse ? c.t0 + row < edge : c.t0 + row >= edge);
-      } else if (p.resets) {
+      } else if (kMarks) {
         const Marks marks(p, w.batch, c);
-        if (marks.any()) alive = alive && (kReverse ? marks.first(0) > row : marks.last(kChunk - 1) <= row);
+        marked = marks.any();
+        if (marked) alive = alive && (kReverse ? marks.first(0) > row : marks.last(kChunk - 1) <= row);
       }
       decay.go(p, w.head);
       const float f = alive ? p.in_scale * power(decay.log2, away) : 0.0f;
@@ -623,6 +674,13 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       ok = wait(&k_full[slot], (w.count >> 1) & 1, abort_flag, err, kCode | 2);
       if (!kStates && ok) ok = wait(s_full, w.parity(), abort_flag, err, kCode | 2);  // K has been read as it came
       if (!kStates && w.count > 0 && ok) ok = wait(upd_done, w.parity() ^ 1u, abort_flag, err, kCode | 2);
+      if (kStates && (kReverse ? c.t0 + c.n > edge : c.t0 < edge)) {  // nor may what V holds in rows that are cut off count
+        ok = ok && wait(&v_full[slot], (w.count >> 1) & 1, abort_flag, err, kCode | 2);
+        if (ok && !alive)
+          for (int i = part * (DV / 16); i < (part + 1) * (DV / 16); ++i)
+            *reinterpret_cast<uint4*>(smem + (slot ? L::q + L::tile_k : L::v) + (i >> 3) * L::half + row * 128 + 16 * (i & 7)) =
+                make_uint4(0u, 0u, 0u, 0u);
+      }
       if (!__all_sync(0xffffffffu, ok)) break;
       uint8_t* high = smem + L::k + slot * L::tile_k + row * 128;
       uint8_t* low = smem + (kStates && slot ? L::q : L::k_low) + row * 128;
@@ -645,6 +703,23 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         }
         sts128(high + o, a[0], a[1], a[2], a[3]);
         sts128(low + o, b[0], b[1], b[2], b[3]);
+      }
+      if (!kStates && marked) {
+        ok = wait(v_full, w.parity(), abort_flag, err, kCode | 2);
+        if (!__all_sync(0xffffffffu, ok)) break;
+        const uint32_t found = __ballot_sync(
+            0xffffffffu, clear_bad(smem + L::v + (DV == 128 ? part * L::half : part * 64) + row * 128, DV / 16));
+        uint32_t* words = bad + 8 * (marked_chunks & 1) + (warp & 3);
+        if (lane == 0) words[4 * part] = found;
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(v_seen);
+        ok = wait(v_seen, marked_chunks & 1, abort_flag, err, kCode | 2);
+        if (!__all_sync(0xffffffffu, ok)) break;
+        ++marked_chunks;
+        if (alive && (words[0] | words[4]) >> lane & 1)
+          for (int g = part * (DK / 16); g < (part + 1) * (DK / 16); ++g)
+            sts128(high + (g >> 3) * L::half + ((g & 7) << 4), 0x7FFF7FFFu, 0x7FFF7FFFu, 0x7FFF7FFFu, 0x7FFF7FFFu);
       }
       fence_proxy_async_smem();
       __syncwarp();
@@ -700,7 +775,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       last_pair = -1;
       if (pair < 0 || !p.last) return;
       const int batch = quotient(pair, static_cast<int>(p.heads)), head = pair - batch * static_cast<int>(p.heads);
-      const bool cut = kReverse && p.resets && p.resets[batch * p.length] != 0;
+      const bool cut = kReverse && kMarks && p.resets[batch * p.length] != 0;
       put(p.last + pair * size, cut ? 0.0f : kReverse ? expf(p.log_decay[head]) : 1.0f);
     };
     // one turn behind the last chunk, for the state behind it
@@ -710,7 +785,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       if (more) {
         const Chunk c = chunk<kReverse>(p, w.block);
         decay.go(p, w.head);
-        if (!(p.resets && Marks(p, w.batch, c).any())) f = power(decay.log2, c.n - 1 + c.e);
+        if (!(kMarks && Marks(p, w.batch, c).any())) f = power(decay.log2, c.n - 1 + c.e);
       }
       // a state that comes from memory, 16 columns ahead
       const bool fresh = more && w.fresh();
@@ -809,7 +884,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       // what the state that the chunk begins with has left at this token
       const int pos = kReverse ? c.n - 1 - row : row;
       bool alive = pos >= 0, marked = false;
-      if (p.resets) {
+      if (kMarks) {
         const Marks marks(p, w.batch, c);
         marked = marks.any();
         if (marked) alive = alive && (kReverse ? marks.first(row + 1) >= kChunk : marks.last(row) < 0);
@@ -862,25 +937,27 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   if (warp == 1) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
 }
 
-template <int DK, int DV, bool kReverse>
+template <int DK, int DV, bool kReverse, bool kMarks>
 int run_tc(const Args& p, const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv, int* err, cudaStream_t s) {
   int dev = 0, st;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return T3_EDEVICE;
   constexpr int kBytes = Smem<DK, DV>::bytes;
-  if ((st = allow_smem<linear_tc_kernel<DK, DV, kReverse, false>>(dev, kBytes)) != T3_OK) return st;
+  if ((st = allow_smem<linear_tc_kernel<DK, DV, kReverse, false, kMarks>>(dev, kBytes)) != T3_OK) return st;
   if (p.local) {
-    if ((st = allow_smem<linear_tc_kernel<DK, DV, kReverse, true>>(dev, kBytes)) != T3_OK) return st;
-    st = launch(linear_tc_kernel<DK, DV, kReverse, true>, p.parts, kTcThreads, kBytes, s, 1, p, mq, mk, mv, err);
+    if ((st = allow_smem<linear_tc_kernel<DK, DV, kReverse, true, kMarks>>(dev, kBytes)) != T3_OK) return st;
+    st = launch(linear_tc_kernel<DK, DV, kReverse, true, kMarks>, p.parts, kTcThreads, kBytes, s, 1, p, mq, mk, mv, err);
     if (st == T3_OK) st = launch_join(p, s);
     if (st != T3_OK) return st;
   }
-  return launch(linear_tc_kernel<DK, DV, kReverse, false>, p.parts, kTcThreads, kBytes, s, 1, p, mq, mk, mv, err);
+  return launch(linear_tc_kernel<DK, DV, kReverse, false, kMarks>, p.parts, kTcThreads, kBytes, s, 1, p, mq, mk, mv, err);
 }
 
 template <int DK, int DV>
 int run_tc(const Args& p, bool reverse, const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv, int* err,
            cudaStream_t s) {
-  return reverse ? run_tc<DK, DV, true>(p, mq, mk, mv, err, s) : run_tc<DK, DV, false>(p, mq, mk, mv, err, s);
+  if (p.resets)
+    return reverse ? run_tc<DK, DV, true, true>(p, mq, mk, mv, err, s) : run_tc<DK, DV, false, true>(p, mq, mk, mv, err, s);
+  return reverse ? run_tc<DK, DV, true, false>(p, mq, mk, mv, err, s) : run_tc<DK, DV, false, false>(p, mq, mk, mv, err, s);
 }
 
 // One pass for heads of up to DK and DV elements.

@@ -234,6 +234,34 @@ def test_documents_do_not_see_each_other():
                 _close(got[i][:, a:b], *back[n], dname, False)
 
 
+@pytest.mark.parametrize("dname,length,dk,dv", [("bf16", 400, 64, 64), ("bf16", 400, 128, 128), ("bf16", 3000, 128, 64),
+                                                ("bf16", 14, 32, 32), ("f32", 400, 40, 33), ("bf16", 200, 27, 27)])
+def test_values_that_are_not_finite_stay_in_their_document(dname, length, dk, dv):
+    """A document that holds NaN and infinities, and a state in front of the first that does: the others' outputs and
+    gradients are, bit for bit, those beside a finite one."""
+    p = _problem(dk + length, 2, length, 2, dk, dv, dname)
+    at = sorted([0, length // 4, length // 4 + 9, length // 2, length - 3])
+    r = torch.zeros((2, length), dtype=torch.bool, device="cuda")
+    r[:, at] = True
+
+    def run(q, k, v, do, state):
+        o, last = t3.t3_linear_attn_fwd(q, k, v, p["log_decay"], state, r, p["scale"])
+        return [o, *t3.t3_linear_attn_bwd(q, k, v, p["log_decay"], do, state, r, p["scale"], p["dstate_last"])[:3]], last
+    want, last = run(*(p[n] for n in ("q", "k", "v", "do", "state")))
+    nan, inf = float("nan"), float("inf")
+    for begin, end in zip(at[:-1], at[1:]):
+        bad = {n: p[n].clone() for n in ("q", "k", "v", "do")}
+        middle = (begin + end) // 2
+        bad["q"][0, middle, 0, 3], bad["k"][0, middle, 0, 1], bad["v"][0, end - 1, 0, 2] = nan, inf, nan
+        bad["v"][0, begin, 1], bad["do"][0, middle, 0, 4], bad["do"][0, begin, 1, 0] = -inf, nan, inf
+        got, end_state = run(*bad.values(), torch.full_like(p["state"], nan))
+        for g, w in zip(got, want):
+            assert torch.equal(g[1], w[1])
+            assert torch.equal(g[0, :begin], w[0, :begin]) and torch.equal(g[0, end:], w[0, end:])
+            assert not torch.isfinite(g[0, begin:end]).all()
+        assert torch.equal(end_state, last)
+
+
 def test_gradient_against_differences():
     """dq, dk, dv and dstate against central differences of the 64-bit recurrence."""
     p = _problem(11, 1, 6, 2, 3, 2, "f32", 0.2)
