@@ -68,8 +68,9 @@ __device__ __forceinline__ bool cut_piece(const Args& p, int part, int& pair, in
 }
 
 // Deals the sequences to so many parts at most, cutting those left over into ranges where there is a workspace for
-// their states and it pays: a range's blocks are taken once more for the states, at 0.6 of the time, and
-// two more kernels cost some three blocks' time.  Else a part for each sequence and head.  A pass that replaces the states it begins with takes a copy of them.
+// their states and it pays: a range's blocks are taken once more for the states, at 0.6 of the time (by chunks;
+// 0.5 token by token), and two more kernels cost some three blocks' time.  Else a part for each sequence and
+// head.  A pass that replaces the states it begins with takes a copy of them.
 int cut(Args* p, int64_t parts, float* workspace, cudaStream_t s);
 int launch_join(const Args& p, cudaStream_t s);
 
@@ -85,8 +86,8 @@ inline int64_t linear_workspace(int64_t pairs, int64_t length, int64_t dk, int64
 }
 
 // One pass of the recurrence above, by chunks on the tensor cores (bf16, rows of 16-byte
-// pieces, t3_linear_tc.cu) and token by token (t3_linear.cu).  workspace: floats for
-// linear_parts() states and passes.
+// pieces, t3_linear_tc.cu) and token by token (t3_linear.cu).  workspace: linear_workspace()
+// floats, or null.
 bool linear_tc_fits(const lin::Args& p, int dtype);
 int launch_linear_tc(lin::Args p, bool reverse, float* workspace, int sms, int* err, cudaStream_t s);
 int launch_linear_tokens(lin::Args p, bool reverse, int dtype, float* workspace, int sms, cudaStream_t s);
