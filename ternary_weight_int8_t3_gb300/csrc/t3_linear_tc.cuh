@@ -15,6 +15,8 @@
 // waits for Q K^T, the state for the product before.  So every step has warps of its own, handing over through
 // mbarriers, and the two chains have an issuer each; Q and K, which a chunk begins with, come a chunk ahead:
 //   warp 0 TMA; warp 1 issues Q K^T, Q S and P V, warp 2 K'^T V; warps 4-7 P; 8-15 K'; 16-23 the state; 24-27 o.
+// Where rows of K have 64 elements warps 4-11 take P and 12-15 K': a chunk waits for P longest (132 us -> 127; with 128, where K'
+// is as long, 125 -> 128).
 // Each group's thread owns a TMEM lane: a token's row of P and o, half a row of the state (dk), and for K' half a
 // token's row in shared memory.  TMEM columns: Q K^T 128, with P over its first 64; P V; Q S; the state.
 //
@@ -25,7 +27,7 @@
 //
 // Measured (bf16, replays of a graph).  8 x 2048 tokens of 27 heads of 128: forward 125 us, 3.8 TB/s: 100 us of it this kernel, 19
 // the states of the ranges that the last 64 of 216 sequences are cut into, the rest joining those;
-// gradient 369, three such passes.  54 heads of 64: 132 and 394.  1 x 16384 of 10 heads of 128: 73 (states 23, join 8, this 47)
+// gradient 369, three such passes.  54 heads of 64: 127 and 381.  1 x 16384 of 10 heads of 128: 73 (states 23, join 8, this 47)
 // and 213.  In the middle of a sequence a chunk takes 6500 clocks, where memory's rate allows 6000; what is
 // lost lies at the ends: a sequence's begin and end cost 4000 to 10000 clocks more, a kernel's begin
 // as much.  A state on its way through shared memory in whole lines instead of a row a lane took 5 % longer,
@@ -48,7 +50,7 @@ namespace t3 {
 namespace lin {
 
 constexpr int kChunk = 128;
-constexpr int kWarpP = 4, kWarpK = 8, kWarpS = 16, kWarpO = 24;
+constexpr int kWarpP = 4, kWarpS = 16, kWarpO = 24;
 constexpr int kTcThreads = 32 * 28;
 constexpr int kColS = 0, kColPV = 128, kColQS = 256, kColState = 384;  // TMEM columns
 constexpr int kCode = 12 << 8;
@@ -63,8 +65,9 @@ template <int DK, int DV> struct Smem {
   static constexpr int k_low = v + tile_v;     // what K' leaves behind its first bf16
   static constexpr int q = k_low + tile_k;     // two; for the states alone a second k_low and V
   static constexpr int s = q + 2 * tile_k;     // the state as bf16, [DK][64] halves
+  static constexpr int warps_p = DK == 64 ? 8 : 4;  // half the row's terms of K' leave warps to P
   static constexpr int tables = s + state;     // a warp of P each: see kTable
-  static constexpr int bars = tables + 4 * kTable * 4;
+  static constexpr int bars = tables + warps_p * kTable * 4;
   static constexpr int n_bars = 27;
   static constexpr int misc = bars + 8 * n_bars;
   static constexpr int bad = (misc + 8 + 15) / 16 * 16;  // a bit a token, for each half of its row of V; one marked chunk's and the next's
@@ -315,7 +318,7 @@ static __device__ __noinline__ bool clear_bad(uint8_t* row, int pieces) {
 }
 
 // kStates: only what each part's last piece adds to the state (Args::local).  kMarks: with resets, whose code the others
-// are faster without (8 x 2048 tokens of 54 heads of 64 132 us for 148).
+// are faster without (8 x 2048 tokens of 54 heads of 64 11 % so).
 template <int DK, int DV, bool kReverse, bool kStates, bool kMarks>
 __global__ void __launch_bounds__(kTcThreads, 1)
     linear_tc_kernel(const Args p, const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
@@ -328,8 +331,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
            *pv_done = bars + 8, *upd_done = bars + 9, *end_bar = bars + 10,
            *o_full = bars + 12;                                           // one arrival each
   uint64_t* v_empty = bars + 13;                                          // both issuers; two, of which without kStates one is used
-  uint64_t *p_full = bars + 15, *o_empty = bars + 16;                     // a group's four warps
-  uint64_t *kp_full = bars + 17, *st_full = bars + 19;                    // or eight
+  uint64_t *p_full = bars + 15, *o_empty = bars + 16, *kp_full = bars + 17, *st_full = bars + 19;  // a group's warps, kp_full two
   uint64_t* drain = bars + 20;                                            // one for each issuer
   uint64_t *q_full = bars + 22, *q_empty = bars + 24;                     // one arrival, two of each
   uint64_t* v_seen = bars + 26;                                           // the warps of K', where a chunk has marks
@@ -338,10 +340,13 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(smem + L::misc);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::misc + 4);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  // the first warp of K'; how many warps share a row of P (by halves of its columns) and of K' (by halves of it)
+  constexpr int kWarpK = kStates ? 8 : kWarpP + L::warps_p, kShareP = (kWarpK - kWarpP) / 4, kShareK = (kWarpS - kWarpK) / 4;
+  constexpr int kGapP = kShareP == 2 ? 32 : 0;  // between the halves of P, each of which lies over its own half of Q K^T
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < L::n_bars; ++i)
-      mbar_init(bars + i, i < 13 ? 1 : i < 15 ? (kStates ? 1 : 2) : i < 17 ? 4 : i < 20 ? 8 : i == 26 ? 8 : 1);
+      mbar_init(bars + i, i < 13 ? 1 : i < 15 ? (kStates ? 1 : 2) : i == 15 ? 4 * kShareP : i == 16 ? 4 : i < 19 || i == 26 ? 4 * kShareK : i == 19 ? 8 : 1);
     *abort_flag = 0;
     fence_mbarrier_init();
   }
@@ -491,7 +496,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         tc_fence_after();
 #pragma unroll 4
         for (int j = 0; j < kChunk / 16; ++j)
-          mma_ts(lead, tmem + kColPV, tmem + kColS + 8 * j, v_cols + down(j), idesc_bf16(DV, false, true), j > 0);
+          mma_ts(lead, tmem + kColPV, tmem + kColS + 8 * j + kGapP * (j >> 2), v_cols + down(j), idesc_bf16(DV, false, true), j > 0);
         mma_commit(lead, pv_done);
         mma_commit(lead, o_full);
         mma_commit(lead, &v_empty[v_slot]);
@@ -525,9 +530,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     __syncwarp();
   } else if (warp >= kWarpP && warp < kWarpK) {
     // --------------------------------------------------------------------- P
-    const int q = warp - kWarpP, row = 32 * q + lane;
+    const int q = warp & 3, row = 32 * q + lane, group = (warp - kWarpP) >> 2;
     const uint32_t at = tmem + (static_cast<uint32_t>(32 * q) << 16) + kColS;
-    float* up = reinterpret_cast<float*>(smem + L::tables) + q * kTable + 32;  // g^t, zeros for t < 0
+    const uint32_t to = at + kGapP * group;
+    float* up = reinterpret_cast<float*>(smem + L::tables) + (warp - kWarpP) * kTable + 32;  // g^t, zeros for t < 0
     float* back = up + 32;                                                      // g^(31 - t)
     const float* mine = kReverse ? up - lane : up + lane;  // g^distance at [t] against time, at [-t] in time
     Decay decay;
@@ -559,9 +565,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       if (!__all_sync(0xffffffffu, ok)) break;
       tc_fence_after();
       // 16 columns at a time: units 0 .. 2 q + 1 in time, 2 q .. 7 against it; the next one's on their way
-      const int u0 = kReverse ? 2 * q : 0, u1 = kReverse ? 8 : 2 * q + 2;
+      const int first = 8 / kShareP * group, end = first + 8 / kShareP;  // this warp's
+      const int u0 = max(kReverse ? 2 * q : 0, first), u1 = min(kReverse ? 8 : 2 * q + 2, end);
       uint32_t s[16];
-      tmem_ld_32x32b_x16(at + 16 * u0, s);
+      if (u0 < u1) tmem_ld_32x32b_x16(at + 16 * u0, s);
 #pragma unroll 1
       for (int u = u0; u < u1; ++u) {
         const int b = u >> 1;
@@ -601,11 +608,11 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 #pragma unroll
         for (int i = 0; i < 8; ++i) out[i] = pack(x[i].x, x[i].y);
         __syncwarp();
-        tmem_st_x8(at + 8 * u, out);  // over columns that this row's thread has read
+        tmem_st_x8(to + 8 * u, out);  // over columns that this thread has read
       }
       const uint32_t none[8] = {};
-      for (int u = 0; u < 8; ++u)
-        if (u < u0 || u >= u1) tmem_st_x8(at + 8 * u, none);
+      for (int u = first; u < end; ++u)
+        if (u < u0 || u >= u1) tmem_st_x8(to + 8 * u, none);
       tc2::tmem_wait_st();
       if (marked) {  // what V holds that is not finite spoils the rows of its document
         ok = wait(v_seen, marked_chunks & 1, abort_flag, err, kCode | 2);
@@ -613,12 +620,12 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         const uint32_t* words = bad + 8 * (marked_chunks & 1);
         ++marked_chunks;
 #pragma unroll 1
-        for (int b = 0; b < 4; ++b) {
+        for (int b = first / 2; b < end / 2; ++b) {
           const uint32_t spoilt = words[b] | words[4 + b];
           if (spoilt == 0u) continue;
           uint32_t v[16];
           __syncwarp();
-          tmem_ld_32x32b_x16(at + 16 * b, v);
+          tmem_ld_32x32b_x16(to + 16 * b, v);
           loaded(v);
 #pragma unroll
           for (int i = 0; i < 16; ++i) {
@@ -627,7 +634,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             if (spoilt >> (2 * i + 1) & 1 && j + 1 >= lo && j + 1 <= hi) v[i] |= 0x7FFF0000u;
           }
           __syncwarp();
-          tmem_st_x16(at + 16 * b, v);
+          tmem_st_x16(to + 16 * b, v);
         }
         tc2::tmem_wait_st();
       }
@@ -637,7 +644,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     }
   } else if (warp >= kWarpK && warp < kWarpS) {
     // -------------------------------------------------------------------- K'
-    const int row = 32 * (warp & 3) + lane, part = (warp - kWarpK) >> 2;  // half of the row's 16-byte pieces
+    const int row = 32 * (warp & 3) + lane, part = (warp - kWarpK) >> 2;  // of the row's 16-byte pieces
+    constexpr int kPieces = DK / 8 / kShareK;
     // kStates: decayed to the end of the piece, tokens of which those from `edge` on count (against
     // time those in front of it); the others are cut off by a mark behind them
     int behind = 0, edge = kReverse ? 0x7FFFFFFF : -1;
@@ -685,8 +693,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       uint8_t* high = smem + L::k + slot * L::tile_k + row * 128;
       uint8_t* low = smem + (kStates && slot ? L::q : L::k_low) + row * 128;
 #pragma unroll 4
-      for (int i0 = 0; i0 < DK / 16; ++i0) {
-        const int g = part * (DK / 16) + i0;
+      for (int i0 = 0; i0 < kPieces; ++i0) {
+        const int g = part * kPieces + i0;
         const int o = (g >> 3) * L::half + (((g ^ row) & 7) << 4);  // the 128-byte swizzle
         const uint4 x = *reinterpret_cast<const uint4*>(high + o);
         const uint32_t in[4] = {x.x & keep, x.y & keep, x.z & keep, x.w & keep};
@@ -707,10 +715,12 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       if (!kStates && marked) {
         ok = wait(v_full, w.parity(), abort_flag, err, kCode | 2);
         if (!__all_sync(0xffffffffu, ok)) break;
-        const uint32_t found = __ballot_sync(
-            0xffffffffu, clear_bad(smem + L::v + (DV == 128 ? part * L::half : part * 64) + row * 128, DV / 16));
         uint32_t* words = bad + 8 * (marked_chunks & 1) + (warp & 3);
-        if (lane == 0) words[4 * part] = found;
+        for (int h = part; h < 2; h += kShareK) {  // by halves of the row
+          const uint32_t found = __ballot_sync(
+              0xffffffffu, clear_bad(smem + L::v + (DV == 128 ? h * L::half : h * 64) + row * 128, DV / 16));
+          if (lane == 0) words[4 * h] = found;
+        }
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(v_seen);
@@ -718,7 +728,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         if (!__all_sync(0xffffffffu, ok)) break;
         ++marked_chunks;
         if (alive && (words[0] | words[4]) >> lane & 1)
-          for (int g = part * (DK / 16); g < (part + 1) * (DK / 16); ++g)
+          for (int g = part * kPieces; g < (part + 1) * kPieces; ++g)
             sts128(high + (g >> 3) * L::half + ((g & 7) << 4), 0x7FFF7FFFu, 0x7FFF7FFFu, 0x7FFF7FFFu, 0x7FFF7FFFu);
       }
       fence_proxy_async_smem();
