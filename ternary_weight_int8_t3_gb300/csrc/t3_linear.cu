@@ -44,7 +44,8 @@ constexpr int smem_floats(int dk) {
   return 2 * kTokens * (2 * padded(dk) + kCols + 1) + 2 * padded(dk) / kRows * kTokens * kCols;
 }
 
-constexpr float kCut = 2.0f;  // a token whose state starts anew, among the factors
+// A token whose state starts anew, among the factors: expm1 and exp of a decay are -1 and 0 at least.
+constexpr float kCut = -2.0f;
 
 // How a token is taken: S = S + c S + k v^T, or S = c S + k v^T; for the states alone S = S + k v^T, with
 // the decays up to the end in v.
