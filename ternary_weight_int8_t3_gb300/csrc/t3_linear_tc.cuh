@@ -548,15 +548,21 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         over32 = power(decay.log2, 32);
         __syncwarp();
       }
-      // the columns that count where there are marks (where there are none, zeros in the table leave out the others)
+      // the columns that count where not all do that the table leaves (zeros there for those on the row's other side)
       int lo = 0, hi = kChunk - 1;
-      bool marked = false;
+      bool marked = false, some = false;
+      if (kReverse) {  // none lies behind the sequence's end, where a power of a growing state may be infinite
+        const int n = chunk<kReverse>(p, w.block).n;
+        some = n < kChunk;
+        hi = n - 1;
+      }
       if (kMarks) {
         const Marks marks(p, w.batch, chunk<kReverse>(p, w.block));
         marked = marks.any();
         if (marked) {
+          some = true;
           if (kReverse)
-            lo = row, hi = marks.first(row + 1) - 1;
+            lo = row, hi = min(hi, marks.first(row + 1) - 1);
           else
             lo = max(marks.last(row), 0), hi = row;
         }
@@ -596,7 +602,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           x[i] = __fmul2_rn(x[i], make_float2(__uint_as_float(s[2 * i]), __uint_as_float(s[2 * i + 1])));
         __syncwarp();
         if (u + 1 < u1) tmem_ld_32x32b_x16(at + 16 * (u + 1), s);
-        if (marked) {
+        if (some) {
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
             const int j = 16 * u + 2 * i;

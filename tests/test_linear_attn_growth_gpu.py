@@ -71,6 +71,13 @@ def test_growing_states_of_long_sequences(dname, length, dk, dv):
     _check(1, length, dk, dv, dname, [60.0 / length, 1.0 / length, 0.0], False)
 
 
+@pytest.mark.parametrize("marks", [False, True])
+@pytest.mark.parametrize("batch,length,dk,dv", [(2, 17, 64, 64), (2, 24, 24, 40), (1, 40, 64, 128), (2, 60, 128, 32), (1, 60, 128, 128)])
+def test_growing_states_by_chunks(batch, length, dk, dv, marks):
+    """Sequences shorter than a chunk whose growth is a float: what the chunk's other rows would have grown to, 3^127, is none."""
+    _check(batch, length, dk, dv, "bf16", GROWTH, marks)
+
+
 @pytest.mark.parametrize("dname", ["bf16", "f32"])
 def test_a_factor_of_any_value_is_a_factor(dname):
     """The floats next to log 3, where a step adds twice the state: the state after two tokens of
