@@ -342,8 +342,9 @@ int t3_rmsnorm_bwd(const void* dy, int64_t lddy, const void* s, int64_t lds, con
  *   max_c |y| would pass the float range (below 3.7e-37) y counts 2^64 times.
  * beta [cols] NULL stands for zeros; mean and rstd are kept for the gradient, and may each
  * be NULL.  The squares are of differences from a mean, so a row far from zero keeps its
- * deviation.  A row with y = 0 everywhere (equal elements without beta, whose deviations are rounding errors
- * of the mean at most) gives q = 0 and row_scale = 0; a row with an element of y that is
+ * deviation, and the mean is corrected by the sum of those differences: it is the float next to the right one, but for the
+ * rounding errors of the deviations' own sum.  A row with y = 0 everywhere (equal elements without beta) gives q = 0 and
+ * row_scale = 0; a row with an element of y that is
  * not finite, or whose squares overflow a float sum, row_scale = NaN and q = 0.  gamma, sum_out and the
  * errors are as in t3_rmsnorm_quant.  Rows that are 16-byte vectors alike in all arrays and have up to 16384
  * columns (floats 12288; 8192 for the gradient) are read once; all others element by element, from memory

@@ -7,8 +7,10 @@
 //   y = (s - mean) rstd gamma + beta
 //   row_scale = max|y| / 127,   q = rint(y * (127 / max|y|)) in [-127, 127]
 // The squares are taken of differences from a mean, never as sum(s^2) - mean^2, so that a row
-// far from zero keeps its deviation: each warp takes its own mean and its squares from that, and
-// the warps' moments join exactly (cta_moments).  With a shift, max|y| needs the
+// far from zero keeps its deviation: each warp takes its own mean and its squares from that, with the sum of
+// the differences themselves, which tells how far that mean is from the right one.  So the warps' moments
+// join without the error of a float sum over the row (cta_moments): the mean is rounded once at its own size,
+// and a row of equal elements has no deviation.  With a shift, max|y| needs the
 // deviation first, so a row is reduced twice, with a barrier each.  Backward, with the rounding passed
 // straight through, h = (s - mean) rstd and n = dy gamma:
 //   dx = rstd (n - mean(n) - h mean(n h)) + dsum
@@ -24,9 +26,9 @@
 // rows longer than a CTA holds, go element by element and are read again from memory for every
 // pass.  Column sums as in t3_norm.cu: partial rows, added in a fixed order.
 //
-// Measured (replays of a graph).  bf16 with residual and shift: 16384 x 1280 forward 28 us (5.8 TB/s), 16384 x 3456 68 (5.8)
-// and 99 backward (5.0: 311 instructions a warp and row, half of the issue slots), 4096 x 8192 45 and 64, 1 x
-// 8192 4.6.  float: 16384 x 1280 50 and 57, 8192 x 3456 65 and 75, 1782 x 729 5.8 and 14.
+// Measured (replays of a graph, the kernel's own bytes).  bf16 with residual and shift: 16384 x 1280 forward 28 us (5.3 TB/s),
+// 16384 x 3456 66 (6.0) and 99 backward (4.6: two thirds of the issue slots and of the memory's rate), 4096 x 8192 43 and 64, 4096 x
+// 16384 87, 1 x 8192 4.8.  float: 16384 x 1280 52 and 57, 8192 x 3456 64 and 75, 1782 x 729 5.8 and 14.
 #include <algorithm>
 
 #include "t3_norm.cuh"
@@ -180,22 +182,41 @@ struct Counts {
   }
 };
 
-// A row's mean and sum of squared deviations from the warps' own (mean m of n elements,
-// sum m2 of squared deviations from m), with one barrier: the deviations of the whole are
-// m2 plus n (m - mean)^2 of every warp, and no square is taken of anything but a difference from a
-// mean.  n: the count of warp `lane`; sm holds 64 floats that no one reads any more.
+// The sum of n squared differences from a mean that lies `off` from some value near it, from the sum m2 of the
+// squared differences from that value and `rest` of the differences themselves: m2 - 2 off rest + n off^2.
+__device__ __forceinline__ float about(float m2, float rest, float n, float off) {
+  return fmaf(off, fmaf(n, off, -2.0f * rest), m2);
+}
+// A sum of squares is not below zero for its roundings (a NaN stays).
+__device__ __forceinline__ float no_less(float m2) { return max_nan(m2, 0.0f); }
+
+// Two sums over a warp at the shuffles of one: a's in lanes 0 to 15, b's in the others.
+__device__ __forceinline__ float warp_sum_halves(float a, float b) {
+  const bool upper = threadIdx.x & 16;
+  float x = (upper ? b : a) + __shfl_xor_sync(0xffffffffu, upper ? a : b, 16);
+#pragma unroll
+  for (int i = 8; i > 0; i >>= 1) x += __shfl_xor_sync(0xffffffffu, x, i);
+  return x;
+}
+
+// A row's mean and sum of squared deviations from the warps' own (a mean m of n elements as a float sum has
+// it, and the sum m2 of squared differences from it), with one barrier.  The means are added as
+// differences from the first one and with how far each is from the right one, so that only the last addition rounds at
+// their own size; no square is taken of anything but a difference from a mean.  n: the count of warp
+// `lane`; sm holds 96 floats that no one reads any more, the last 32 of them by now the sums of each warp's
+// differences from its mean.
 __device__ __forceinline__ void cta_moments(float& m, float& m2, float n, float inv_cols, float* sm) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
-  if (warps == 1) return;
   if (lane == 0) {
     sm[warp] = m;
     sm[32 + warp] = m2;
   }
   __syncthreads();
-  const float own = lane < warps ? sm[lane] : 0.0f, own2 = lane < warps ? sm[32 + lane] : 0.0f;
-  m = warp_sum(n * own) * inv_cols;
-  const float d = own - m;
-  m2 = warp_sum(fmaf(n * d, d, own2));  // n is 0 behind the last warp
+  const bool has = lane < warps;
+  const float own = has ? sm[lane] : 0.0f, own2 = has ? sm[32 + lane] : 0.0f, rest = has ? sm[64 + lane] : 0.0f;
+  const float first = sm[0];
+  m = fmaf(warp_sum(fmaf(n, own - first, rest)), inv_cols, first);  // n is 0 behind the last warp
+  m2 = no_less(warp_sum(about(own2, rest, n, m - own)));
 }
 
 // Two sums over a group of `warps` warps, which meets at barrier `bar`; `sm` holds two floats
@@ -334,7 +355,7 @@ constexpr int front_threads(int ept) { return ept <= 8 ? 1024 : ept <= 16 ? 768 
 template <class T, int VEC, int NV, bool kOdd>
 __global__ void __launch_bounds__(front_threads(NV * VEC)) layer_fwd_kernel(const FwdArgs p) {
   extern __shared__ __align__(16) uint4 ring[];
-  __shared__ float sm[3][32];
+  __shared__ float sm[4][32], count[2][32];
   constexpr int P = VEC / 2;
   const int cols = static_cast<int>(p.cols), tid = threadIdx.x, lanes = blockDim.x;
   Rows<T, VEC, NV, kOdd, 2> rows(p.from, p.ld, p.rows, blockIdx.x, gridDim.x, cols, tid, lanes,
@@ -365,9 +386,13 @@ __global__ void __launch_bounds__(front_threads(NV * VEC)) layer_fwd_kernel(cons
   }
   const Counts counts{at.head, at.end, cols, lanes};
   const int lane = tid & 31;
-  const float of_lane = lane < lanes >> 5 ? counts.of<VEC, NV>(lane) : 0.0f;
-  const float own = counts.of<VEC, NV>(tid >> 5);
-  const float inv_own = own > 0.0f ? __fdiv_rn(1.0f, own) : 0.0f;
+  // the warps' counts and their reciprocals (in registers they cost spills)
+  if (tid < 32) {
+    const float n = lane < lanes >> 5 ? counts.of<VEC, NV>(lane) : 0.0f;
+    count[0][lane] = n;
+    count[1][lane] = n > 0.0f ? __fdiv_rn(1.0f, n) : 0.0f;
+  }
+  __syncthreads();
   const float inv_cols = cols > 0 ? __fdiv_rn(1.0f, static_cast<float>(cols)) : 0.0f;
   T* so = static_cast<T*>(p.sum_out) + blockIdx.x * p.lds + rows.column0;
   int8_t* q = p.q + blockIdx.x * p.cols + rows.column0;
@@ -395,8 +420,13 @@ __global__ void __launch_bounds__(front_threads(NV * VEC)) layer_fwd_kernel(cons
         first += ue;
       }
     }
-    float mean = warp_sum(first) * inv_own;  // the warp's own
-    float2 square = both(0.0f);
+    // How far a warp's mean is from the right one: the sum of the differences from it.  bf16 elements that are alike
+    // enough for it to matter have few bits in common units, so that their float sum is exact and tells.
+    constexpr bool kSums = sizeof(T) == 2;
+    first = warp_sum(first);
+    float mean = first * count[1][tid >> 5];  // the warp's own
+    if (kSums && lane == 0) sm[2][tid >> 5] = fmaf(-count[0][tid >> 5], mean, first);
+    float2 square = both(0.0f), diff = both(0.0f);
 #pragma unroll
     for (int v = 0; v < NV; ++v)
       if (rows.column(v) < rows.end) {
@@ -404,12 +434,22 @@ __global__ void __launch_bounds__(front_threads(NV * VEC)) layer_fwd_kernel(cons
         for (int j = 0; j < P; ++j) {
           const float2 d = __fadd2_rn(u[v][j], both(-mean));
           square = __ffma2_rn(d, d, square);
+          if (!kSums) diff = __fadd2_rn(diff, d);
         }
       }
-    float m2 = square.x + square.y;
-    if (kOdd && at.has) m2 = fmaf(ue - mean, ue - mean, m2);
-    m2 = warp_sum(m2);
-    cta_moments(mean, m2, of_lane, inv_cols, sm[0]);
+    float m2 = square.x + square.y, rest = diff.x + diff.y;
+    if (kOdd && at.has) {
+      m2 = fmaf(ue - mean, ue - mean, m2);
+      if (!kSums) rest += ue - mean;
+    }
+    if (kSums) {
+      m2 = warp_sum(m2);
+    } else {
+      m2 = warp_sum_halves(m2, rest);
+      if (lane == 16) sm[2][tid >> 5] = m2;
+      m2 = __shfl_sync(0xffffffffu, m2, 0);
+    }
+    cta_moments(mean, m2, count[0][lane], inv_cols, sm[0]);
     const float rstd = deviation(p, m2, inv_cols);
     float amax = 0.0f;
 #pragma unroll
@@ -425,7 +465,7 @@ __global__ void __launch_bounds__(front_threads(NV * VEC)) layer_fwd_kernel(cons
       ue = fmaf(__fmul_rn(ue - mean, rstd), ge, be);
       amax = absmax(amax, make_float2(ue, 0.0f));
     }
-    amax = cta_absmax(amax, sm[2]);
+    amax = cta_absmax(amax, sm[3]);
     if (tid == 0) put_row(p, row, mean, m2, rstd, amax);
     float up;
     const float inv = inverse_row(m2, amax, up);
@@ -475,7 +515,7 @@ __device__ __forceinline__ float cta_sum(float a, float* sm) {
 // the first from sum_out where it is written.
 template <class T>
 __global__ void __launch_bounds__(1024) layer_fwd_long_kernel(const FwdArgs p) {
-  __shared__ float sm[3][32];
+  __shared__ float sm[4][32];
   launch_dependents();
   grid_dependency_wait();
   for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x) {
@@ -495,19 +535,23 @@ __global__ void __launch_bounds__(1024) layer_fwd_long_kernel(const FwdArgs p) {
       to_float(load<T, 1>(so + k), s);
       return s[0];
     };
-    float total = 0.0f, m2 = 0.0f, amax = 0.0f;
+    float total = 0.0f, rest = 0.0f, m2 = 0.0f, amax = 0.0f;
     for (int64_t k = threadIdx.x; k < p.cols; k += blockDim.x) {
       const float s[1] = {sum_at(k)};
       if (p.sum_out) store<T, 1>(so + k, from_float(s, T()));
       total += s[0];
     }
     const float inv_cols = __fdiv_rn(1.0f, static_cast<float>(p.cols));
-    const float mean = cta_sum(total, sm[0]) * inv_cols;
+    const float near = cta_sum(total, sm[0]) * inv_cols;  // the mean but for its sum's roundings
     for (int64_t k = threadIdx.x; k < p.cols; k += blockDim.x) {
-      const float d = again(k) - mean;
+      const float d = again(k) - near;
+      rest += d;
       m2 = fmaf(d, d, m2);
     }
+    rest = cta_sum(rest, sm[3]);
     m2 = cta_sum(m2, sm[1]);
+    const float mean = fmaf(rest, inv_cols, near);
+    m2 = no_less(about(m2, rest, static_cast<float>(p.cols), mean - near));
     const float rstd = deviation(p, m2, inv_cols);
     auto y_at = [&](int64_t k) {
       return fmaf(__fmul_rn(again(k) - mean, rstd), p.gamma ? __ldg(p.gamma + k) : 1.0f,
