@@ -426,7 +426,8 @@ int t3_gated_scan_bwd(const void* gate, int64_t ldg, const void* cand, int64_t l
  * q, k: token t of sequence b is row b * length + t of a matrix with the given stride, head h
  * its columns from h * dk on; v and o the same with dv.  dk and dv are 128 at most.  log_decay
  * float [heads], a constant of the model (no gradient is taken of it): 0 forgets nothing, -inf everything;
- * above 0 states grow, and exp(length * log_decay) has to be a float.  state, state_last float [batch][heads][dk][dv]; resets uint8 [batch][length] or
+ * above 0 states grow, and exp(length * log_decay) has to be a float.  A state that is not finite stays so (0 times it is
+ * NaN) until a reset, behind which it is nothing.  state, state_last float [batch][heads][dk][dv]; resets uint8 [batch][length] or
  * NULL.  state_last (may be NULL, may be state's buffer) receives the state after the last
  * token, so single tokens (length = 1) advance a state in place; length = 0 copies it.
  * workspace: DEVICE floats, t3_linear_attn_workspace of them (not zeroed), with which few long

@@ -272,11 +272,11 @@ __global__ void __launch_bounds__(kMaxHead / kRows * 32, 2) linear_tokens_kernel
       for (int i = 0; i < kRows; ++i) {
         const int r = warp * kRows + i;
         const float y = i & 1 ? S[i / 2].y : S[i / 2].x;
-        if (r < p.dk) to[r * p.dv + col] = cut || f == 0.0f ? 0.0f : f * y;
+        if (r < p.dk) to[r * p.dv + col] = cut ? 0.0f : f * y;
       }
       if (kAlone && threadIdx.x == 0 && col == 0) {
         const int decays = tau1 - tau0 - (kReverse && tau0 == 0 ? 1 : 0);
-        p.pass[part + 1] = edge >= 0 ? 0.0f : decays == 0 ? 1.0f : expf(log_decay_now * static_cast<float>(decays));
+        p.pass[part + 1] = edge >= 0 ? kCutOff : decays == 0 ? 1.0f : expf(log_decay_now * static_cast<float>(decays));
       }
     }
     w = next;
@@ -397,7 +397,7 @@ __global__ void __launch_bounds__(256) linear_join_kernel(const Args p, int elem
       for (int i = 0; i < kAhead; ++i)
 #pragma unroll
         for (int k = 0; k < kEach; ++k) {
-          x[k] = pass[i] == 0.0f ? piece[i][k] : fmaf(pass[i], x[k], piece[i][k]);
+          x[k] = pass[i] == kCutOff ? piece[i][k] : fmaf(pass[i], x[k], piece[i][k]);
           if (j + i < end && e0 + 256 * k < size) at[static_cast<int64_t>(i) * size + 256 * k] = x[k];
         }
     }

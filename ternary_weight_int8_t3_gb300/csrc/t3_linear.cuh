@@ -48,8 +48,10 @@ struct Args {
   int ranges;              // parts that have some of them: so many each, and one more for some
   int each, rest;
   float* local;            // [parts][dk * dv]: the state in front of each range that begins inside a sequence
-  float* pass;             // [parts]: what is left of a state across the piece in front of such a range
+  float* pass;             // [parts]: what is left of a state across the piece in front of such a range, or kCutOff
 };
+// A mark lies in between: nothing, whatever the state holds (a decay of 0 times what is not finite is NaN).
+constexpr float kCutOff = -1.0f;
 
 // Blocks are counted in 32 bits (2^36 tokens of all heads would not fit the memory).
 __host__ __device__ __forceinline__ int part_begin(const Args& p, int i) {

@@ -682,7 +682,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       }
       decay.go(p, w.head);
       const float f = alive ? p.in_scale * power(decay.log2, away) : 0.0f;
-      const uint32_t keep = f == 0.0f ? 0u : 0xFFFFFFFFu;  // whatever a row that is cut off holds
+      const uint32_t keep = alive ? 0xFFFFFFFFu : 0u;  // whatever a row that is cut off holds
       const float2 f2 = make_float2(f, f);
       const int slot = w.count & 1;
       ok = wait(&k_full[slot], (w.count >> 1) & 1, abort_flag, err, kCode | 2);
@@ -748,7 +748,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       int tokens = 0;
       for (int i = 0; i < w.count; ++i) tokens += chunk<kReverse>(p, begun + i).n;
       if (kReverse && begun == 0) --tokens;
-      p.pass[blockIdx.x + 1] = cut ? 0.0f : tokens == 0 ? 1.0f : expf(p.log_decay[w.head] * static_cast<float>(tokens));
+      p.pass[blockIdx.x + 1] = cut ? kCutOff : tokens == 0 ? 1.0f : expf(p.log_decay[w.head] * static_cast<float>(tokens));
     }
   } else if (warp >= kWarpS && warp < kWarpO) {
     // ------------------------------------------------------------- the state
@@ -759,7 +759,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     Decay decay;
     const int64_t size = static_cast<int64_t>(p.dk) * p.dv;
     // the state behind a piece, to the caller or to the next part
-    auto put = [&](float* to, float f) {
+    auto put = [&](float* to, bool cut, float f) {
       if (!mine) return;
       const bool wide = (reinterpret_cast<uintptr_t>(to) & 31) == 0;  // rows are multiples of 32 bytes
 #pragma unroll 1
@@ -769,7 +769,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         tmem_ld_32x32b_x16(at + 16 * b, s);
         loaded(s);
 #pragma unroll
-        for (int i = 0; i < 16; ++i) s[i] = f == 0.0f ? 0u : __float_as_uint(f * __uint_as_float(s[i]));
+        for (int i = 0; i < 16; ++i) s[i] = cut ? 0u : __float_as_uint(f * __uint_as_float(s[i]));
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
           const int col = col0 + 16 * b + 8 * i;
@@ -792,16 +792,18 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       if (pair < 0 || !p.last) return;
       const int batch = quotient(pair, static_cast<int>(p.heads)), head = pair - batch * static_cast<int>(p.heads);
       const bool cut = kReverse && kMarks && p.resets[batch * p.length] != 0;
-      put(p.last + pair * size, cut ? 0.0f : kReverse ? expf(p.log_decay[head]) : 1.0f);
+      put(p.last + pair * size, cut, kReverse ? expf(p.log_decay[head]) : 1.0f);
     };
     // one turn behind the last chunk, for the state behind it
     for (; !kStates; w.next(p)) {
       const bool more = w.more();
       float f = 0.0f;
+      bool cut = false;
       if (more) {
         const Chunk c = chunk<kReverse>(p, w.block);
         decay.go(p, w.head);
-        if (!(kMarks && Marks(p, w.batch, c).any())) f = power(decay.log2, c.n - 1 + c.e);
+        f = power(decay.log2, c.n - 1 + c.e);
+        if (kMarks) cut = Marks(p, w.batch, c).any();
       }
       // a state that comes from memory, 16 columns ahead
       const bool fresh = more && w.fresh();
@@ -861,7 +863,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           for (int i = 0; i < 4; ++i) o[i] = pack(__uint_as_float(s[8 * g + 2 * i]), __uint_as_float(s[8 * g + 2 * i + 1]));
           sts128(to + tc::sw128(row, (col >> 3 & 7) + g), o[0], o[1], o[2], o[3]);
         }
-        if (f == 0.0f) {  // whatever it holds
+        if (kMarks && cut) {  // whatever it holds
 #pragma unroll
           for (int i = 0; i < 16; ++i) s[i] = 0u;
         } else {
@@ -886,7 +888,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       ok = wait(end_bar, 0, abort_flag, err, kCode | 4);
       if (__all_sync(0xffffffffu, ok)) {
         tc_fence_after();
-        put(p.local + (blockIdx.x + 1) * size, 1.0f);
+        put(p.local + (blockIdx.x + 1) * size, false, 1.0f);
       }
     }
   } else if (warp >= kWarpO) {
