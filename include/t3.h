@@ -435,8 +435,9 @@ int t3_gated_scan_bwd(const void* gate, int64_t ldg, const void* cand, int64_t l
  * bf16 rows of more than 16 tokens whose bases, strides and heads are whole 16-byte pieces run on the tensor cores,
  * 128 tokens at a time: products inside such a chunk and the state it begins with are rounded to bf16 where they meet
  * q and v (o is off by about a rounding more than its own), what is added to the state is not (2^-17 of each
- * term).  A value of q, k or v that is not finite spoils its document's tokens of the chunk, those in front of it
- * included, and the state from there on.  On no path does it pass a reset, in either direction.
+ * term).  A value of q, k or v that is not finite shows in the outputs that the recurrence takes it to, in none
+ * in front of it (for the gradient's passes against time, behind it) and on no path beyond a reset; in 128 tokens with a reset among them
+ * it spoils all columns of its token's outputs and of the state, not its own alone.
  * Everything else is float, token by token.
  * T3_EINVAL: negative sizes or strides, sizes above 2^31 - 1 or heads above 128 elements, batch * heads *
  * ceil(length / 16) above 2^31 - 1, ldo < heads * dv, a null q, k, v, o or log_decay with a non-empty shape, an unknown dtype.

@@ -40,6 +40,10 @@
 // with NaN in P and K' in their place.  Documents of 300 tokens on average: the first case 170 us (139 without the look at V, which waits for
 // V's one place) and gradient 511.
 //
+// Without marks a value that is not finite meets P's zeros in the rows in front of it: the warps of o look whether P V is finite
+// and take such rows again (take_again).  Without ever being run this costs up to 3 % (54 heads of 64 127 us -> 131, 27 of 128 none); as a
+// call, or with more loads on their way, 3 to 6 %.
+//
 // Heads are taken as 64 or 128 elements, zeros behind their own (DK, DV; a file for each pair of them, so that they compile
 // in parallel).
 #pragma once
@@ -54,6 +58,7 @@ constexpr int kWarpP = 4, kWarpS = 16, kWarpO = 24;
 constexpr int kTcThreads = 32 * 28;
 constexpr int kColS = 0, kColPV = 128, kColQS = 256, kColState = 384;  // TMEM columns
 constexpr int kCode = 12 << 8;
+constexpr float kInfinity = __builtin_huge_valf();
 constexpr int kTable = 96;  // floats: 32 zeros, g^0 .. g^31 (times both scales), and those backwards
 
 template <int DK, int DV> struct Smem {
@@ -129,6 +134,23 @@ __device__ __forceinline__ void tmem_st_x16(uint32_t taddr, const uint32_t (&v)[
       "%16};" ::"r"(taddr),
       "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
       "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
+      : "memory");
+}
+
+// One column, and eight, of the rows' own; loaded on return.
+__device__ __forceinline__ void tmem_st_x1(uint32_t taddr, float v) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x1.b32 [%0], {%1};" ::"r"(taddr), "r"(__float_as_uint(v)) : "memory");
+}
+__device__ __forceinline__ float tmem_ld_x1(uint32_t taddr) {
+  uint32_t v;
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];\n\ttcgen05.wait::ld.sync.aligned;" : "=r"(v) : "r"(taddr) : "memory");
+  return __uint_as_float(v);
+}
+__device__ __forceinline__ void tmem_ld_x8(uint32_t taddr, uint32_t (&v)[8]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];\n\ttcgen05.wait::ld.sync.aligned;"
+      : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7])
+      : "r"(taddr)
       : "memory");
 }
 
@@ -315,6 +337,75 @@ static __device__ __noinline__ bool clear_bad(uint8_t* row, int pieces) {
   if (bad)
     for (int g = 0; g < pieces; ++g) *reinterpret_cast<uint4*>(row + 16 * g) = make_uint4(0u, 0u, 0u, 0u);
   return bad;
+}
+
+// Rows of o that P V left not finite, taken again from memory over their own tokens alone: P's zeros on the other side of a
+// row's place leave out what is finite, but zero times a value that is not is NaN.  Written small, since the roles' code has to fit: 0.7 ms a chunk that has one.
+struct Again {
+  const bf16 *q, *k, *v;  // the row's q, the chunk's first k and v
+  int64_t ldk, ldv;
+  bf16* out;
+  int dk, dv, n, row;
+  uint32_t at;            // this lane's TMEM
+  float state, scale, log2;  // coefficients of Q S and of P, and the decay's logarithm
+  bool bad;               // this row is one of them; the whole warp calls
+};
+template <bool kReverse>
+__device__ __forceinline__ void take_again(const Again a) {
+  auto dot8 = [](const bf16* x, const bf16* y, float sum) {
+    const uint4 u = *reinterpret_cast<const uint4*>(x), t = *reinterpret_cast<const uint4*>(y);
+    const uint32_t us[4] = {u.x, u.y, u.z, u.w}, ts[4] = {t.x, t.y, t.z, t.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      float2 c, d;
+      unpack(us[i], c.x, c.y);
+      unpack(ts[i], d.x, d.y);
+      sum = fmaf(c.x, d.x, fmaf(c.y, d.y, sum));
+    }
+    return sum;
+  };
+  auto counts = [&](int j) { return a.bad && (kReverse ? j >= a.row : j <= a.row); };
+  // the row of P over that of P V
+#pragma unroll 1
+  for (int j = 0; j < a.n; ++j) {
+    float x = 0.0f;
+    if (counts(j)) {
+#pragma unroll 1
+      for (int d = 0; d < a.dk; d += 8) x = dot8(a.q + d, a.k + j * a.ldk + d, x);
+      x *= a.scale * power(a.log2, kReverse ? j - a.row : a.row - j);
+    }
+    __syncwarp();
+    tmem_st_x1(a.at + kColPV + j, x);
+  }
+  tc2::tmem_wait_st();
+#pragma unroll 1
+  for (int b = 0; b < a.dv; b += 8) {
+    uint32_t y[8], o[4];
+    float z[8];
+    __syncwarp();
+    tmem_ld_x8(a.at + kColQS + b, y);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) z[i] = a.state * __uint_as_float(y[i]);
+#pragma unroll 1
+    for (int j = 0; j < a.n; ++j) {
+      __syncwarp();
+      const float x = tmem_ld_x1(a.at + kColPV + j);
+      if (!counts(j)) continue;
+      const uint4 v = *reinterpret_cast<const uint4*>(a.v + j * a.ldv + b);
+      const uint32_t vs[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        float2 t;
+        unpack(vs[i], t.x, t.y);
+        z[2 * i] = fmaf(x, t.x, z[2 * i]);
+        z[2 * i + 1] = fmaf(x, t.y, z[2 * i + 1]);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) o[i] = pack(z[2 * i], z[2 * i + 1]);
+    if (a.bad) *reinterpret_cast<uint4*>(a.out + b) = make_uint4(o[0], o[1], o[2], o[3]);
+  }
+  __syncwarp();
 }
 
 // kStates: only what each part's last piece adds to the state (Args::local).  kMarks: with resets, whose code the others
@@ -913,6 +1004,13 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       ok = wait(o_full, w.parity(), abort_flag, err, kCode | 4);
       if (!__all_sync(0xffffffffu, ok)) break;
       tc_fence_after();
+      float top = 0.0f;  // of P V, or NaN
+      bool again = false;
+      auto release = [&]() {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(o_empty);
+      };
 #pragma unroll 1
       for (int b = 0; b < DV / 16; ++b) {
         uint32_t x[16], y[16], o[8];
@@ -921,10 +1019,12 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         tmem_ld_32x32b_x16(at + kColQS + 16 * b, y);
         loaded(x);
         loaded(y);
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          asm("max.NaN.abs.f32 %0, %0, %1, %2;" : "+f"(top) : "f"(__uint_as_float(x[2 * i])), "f"(__uint_as_float(x[2 * i + 1])));
         if (b + 1 == DV / 16) {
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(o_empty);
+          again = !marked && __any_sync(0xffffffffu, row < c.n && !(top < kInfinity));
+          if (__builtin_expect(!again, 1)) release();
         }
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
@@ -945,6 +1045,14 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             if (16 * b + 8 < p.dv) *reinterpret_cast<uint4*>(out + 16 * b + 8) = make_uint4(o[4], o[5], o[6], o[7]);
           }
         }
+      }
+      if (__builtin_expect(again, 0)) {
+        const int64_t first = w.batch * p.length + c.t0;
+        take_again<kReverse>({static_cast<const bf16*>(p.q) + (first + row) * p.ldq + w.head * p.dk,
+                              static_cast<const bf16*>(p.k) + first * p.ldk + w.head * p.dk,
+                              static_cast<const bf16*>(p.v) + first * p.ldv + w.head * p.dv, p.ldk, p.ldv, out, p.dk, p.dv, c.n, row,
+                              at, f, p.in_scale * p.out_scale, decay.log2, row < c.n && !(top < kInfinity)});
+        release();
       }
     }
   }
