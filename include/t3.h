@@ -424,7 +424,8 @@ int t3_gated_scan_bwd(const void* gate, int64_t ldg, const void* cand, int64_t l
  *   S'_{t-1} = S_{t-1}, or 0 where resets[b][t] is not 0 (a document starts);
  *   S_{-1} = state (NULL: zeros).
  * q, k: token t of sequence b is row b * length + t of a matrix with the given stride, head h
- * its columns from h * dk on; v and o the same with dv.  dk and dv are 128 at most.  log_decay
+ * its columns from h * dk on; v and o the same with dv, and o overlaps none of q, k and v (which are read while others of its
+ * columns are written).  dk and dv are 128 at most.  log_decay
  * float [heads], a constant of the model (no gradient is taken of it): 0 forgets nothing, -inf everything;
  * above 0 states grow, and exp(length * log_decay) has to be a float.  A state that is not finite stays so (0 times it is
  * NaN) until a reset, behind which it is nothing.  state, state_last float [batch][heads][dk][dv]; resets uint8 [batch][length] or
@@ -440,7 +441,8 @@ int t3_gated_scan_bwd(const void* gate, int64_t ldg, const void* cand, int64_t l
  * it spoils all columns of its token's outputs and of the state, not its own alone.
  * Everything else is float, token by token.
  * T3_EINVAL: negative sizes or strides, sizes above 2^31 - 1 or heads above 128 elements, batch * heads *
- * ceil(length / 16) above 2^31 - 1, ldo < heads * dv, a null q, k, v, o or log_decay with a non-empty shape, an unknown dtype.
+ * ceil(length / 16) above 2^31 - 1, ldo < heads * dv, a null q, k, v, o or log_decay with a non-empty shape, an o that is q,
+ * k or v, an unknown dtype.
  */
 int t3_linear_attn_fwd(const void* q, int64_t ldq, const void* k, int64_t ldk, const void* v,
                        int64_t ldv, const float* log_decay, const float* state,
@@ -456,7 +458,8 @@ int t3_linear_attn_fwd(const void* q, int64_t ldq, const void* k, int64_t ldk, c
  *   dq_t = scale * S_t dout_t,   dk_t = G_t v_t,   dv_t = G_t^T k_t,
  *   dstate = exp(log_decay[h]) * G_0 (0 where token 0 resets; may be NULL, may be dstate_last's buffer).
  * The S_t are taken again from state, k and v: nothing of the forward is kept.  dq, dk and dv are
- * laid out like q, k and v, with strides of their own, and overlap none of the inputs.  Each is a pass of the
+ * laid out like q, k and v, with strides of their own, and overlap none of the inputs nor each other (T3_EINVAL where two are the
+ * same).  Each is a pass of the
  * forward's kernels over other operands, with the forward's roundings and workspace.
  */
 int t3_linear_attn_bwd(const void* q, int64_t ldq, const void* k, int64_t ldk, const void* v,

@@ -818,7 +818,7 @@ def t3_linear_attn_fwd(q, k, v, log_decay, state=None, resets=None, scale=1.0, o
     sequence and head of q, k [batch][length][heads][dk] and v [batch][length][heads][dv], from the float
     state [batch][heads][dk][dv] (None: zeros); log_decay float32 [heads]; resets uint8 or
     bool [batch][length] marks tokens that start from zero.  q, k and v may be slices of one wider
-    tensor.  state_last may be state: the state advances in place."""
+    tensor; o overlaps none of them.  state_last may be state: the state advances in place."""
     torch = _torch()
     dtype = _dtype_of(q, "q")
     qs, vs = _linear_shapes(q, v)
@@ -843,7 +843,8 @@ def t3_linear_attn_fwd(q, k, v, log_decay, state=None, resets=None, scale=1.0, o
 def t3_linear_attn_bwd(q, k, v, log_decay, do, state=None, resets=None, scale=1.0, dstate_last=None, dq=None, dk=None,
                        dv=None, dstate=None, workspace=None, stream=None):
     """(dq, dk, dv, dstate): the gradient of t3_linear_attn_fwd for do, the gradient of o, and
-    dstate_last (float32 [batch][heads][dk][dv] or None), that of state_last."""
+    dstate_last (float32 [batch][heads][dk][dv] or None), that of state_last; dstate may be dstate_last, the other
+    outputs overlap no input."""
     torch = _torch()
     dtype = _dtype_of(q, "q")
     qs, vs = _linear_shapes(q, v)

@@ -1029,7 +1029,7 @@ int t3_linear_attn_fwd(const void* q, int64_t ldq, const void* k, int64_t ldk, c
     return T3_EINVAL;
   if (batch == 0 || heads == 0) return T3_OK;
   const int64_t state_bytes = batch * heads * dk * dv * static_cast<int64_t>(sizeof(float));
-  if (length > 0 && (!q || !k || !v || !o || !log_decay)) return T3_EINVAL;
+  if (length > 0 && (!q || !k || !v || !o || !log_decay || o == q || o == k || o == v)) return T3_EINVAL;
   const DeviceInfo* dev = nullptr;
   const int st = device_info(&dev);
   if (st != T3_OK) return st;
@@ -1061,7 +1061,12 @@ int t3_linear_attn_bwd(const void* q, int64_t ldq, const void* k, int64_t ldk, c
       bad_ld(lddq) || bad_ld(lddk) || bad_ld(lddv) || lddq < heads * dk || lddk < heads * dk || lddv < heads * dv)
     return T3_EINVAL;
   if (batch == 0 || heads == 0) return T3_OK;
-  if (length > 0 && (!q || !k || !v || !dout || !log_decay || !dq || !dk_out || !dv_out)) return T3_EINVAL;
+  if (length > 0) {
+    if (!q || !k || !v || !dout || !log_decay || !dq || !dk_out || !dv_out) return T3_EINVAL;
+    for (const void* g : {dq, dk_out, dv_out})  // each pass reads what another one's gradient would lie over
+      if (g == q || g == k || g == v || g == dout) return T3_EINVAL;
+    if (dq == dk_out || dq == dv_out || dk_out == dv_out) return T3_EINVAL;
+  }
   const DeviceInfo* dev = nullptr;
   int st = device_info(&dev);
   if (st != T3_OK) return st;
