@@ -539,7 +539,8 @@ GluPlan glu_plan(const int8_t* A, const uint8_t* Wg, const uint8_t* Wu, const vo
     return p;
   }
   // rows that TMA cannot address cost the pipelines several times as much as
-  // laying them out once
+  // laying them out once (4096 x 3456 x 1281 75 us, with K = 1280 64).  Few tiles over a long reduction are better off
+  // as two split products (40 x 1280 x 16384 85 us here, 21 each), which this plan does not know.
   p.route = GluPlan::kPairs;
   p.aligned = !a_ok || !w_ok || !out_ok || !one_chunk;
   if (!p.aligned) return p;

@@ -791,7 +791,7 @@ constexpr int kSmemSm = 216 << 10;  // of an SM's shared memory, what rings may 
 constexpr int kSmemCta = 200 << 10;
 
 // Bytes of a ring over a CTA's rows of `row` bytes, and how far ahead it runs: not further than the
-// CTA has rows, nor than its shared memory holds (16384 floats and their residual: one row, none ahead).
+// CTA has rows, nor than its shared memory holds (12288 floats and their residual: one row ahead).
 int ring_of(int row, int64_t rows_each, int* ahead) {
   *ahead = kAhead;
   while (*ahead > 0 && (*ahead >= rows_each || (*ahead + 1) * row > kSmemCta)) --*ahead;

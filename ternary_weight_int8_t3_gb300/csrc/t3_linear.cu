@@ -19,8 +19,9 @@
 // Measured: that case 167 us forward and 500 backward (twelve warps an SM that read q and k four rows at a time: shared memory
 // is in use 60 % of the time, the float units 50 %); 2 x 2048 of 8 float heads of 128 175 and 532.  Decays kept out of the inner
 // loop, in v and o, as for the states alone: 1.05 times as fast in parts of sequences, 0.93 in whole ones.
-// One token of 27 sequences and 64 heads of 128 x 128: 40.7 us, 5.6 TB/s (eight CTAs an SM, 8 rows of 16 bytes a
-// thread on their way; whole states a CTA and 16 rows a thread 48, 4 rows 59, one element a thread and row 77).
+// One token of 27 sequences and 64 heads of 128 x 128: 40.6 us, 5.6 TB/s (eight CTAs an SM, 8 rows of 16 bytes a
+// thread on their way; whole states a CTA and 16 rows a thread 48, 4 rows 59, one element a thread and row 77).  Where rows of a
+// state are no 16-byte pieces (dv off multiples of 4) the blocks' kernel takes it: 128 x 126 94 us.
 #include <type_traits>
 
 #include "t3_linear.cuh"

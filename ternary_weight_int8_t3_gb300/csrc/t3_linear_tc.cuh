@@ -25,9 +25,9 @@
 // table read at the distance, zeros where it is negative: no exponential an element, and no coefficient above 1.
 // The pass for the states alone takes K' decayed to the end of the piece, so that it is one long product.
 //
-// Measured (bf16, replays of a graph).  8 x 2048 tokens of 27 heads of 128: forward 125 us, 3.8 TB/s: 100 us of it this kernel, 19
+// Measured (bf16, replays of a graph).  8 x 2048 tokens of 27 heads of 128: forward 127 us, 3.8 TB/s: 100 us of it this kernel, 19
 // the states of the ranges that the last 64 of 216 sequences are cut into, the rest joining those;
-// gradient 369, three such passes.  54 heads of 64: 127 and 381.  1 x 16384 of 10 heads of 128: 73 (states 23, join 8, this 47)
+// gradient 371, three such passes.  54 heads of 64: 130 and 395.  1 x 16384 of 10 heads of 128: 74 (states 23, join 8, this 47)
 // and 213.  In the middle of a sequence a chunk takes 6500 clocks, where memory's rate allows 6000; what is
 // lost lies at the ends: a sequence's begin and end cost 4000 to 10000 clocks more, a kernel's begin
 // as much.  A state on its way through shared memory in whole lines instead of a row a lane took 5 % longer,
@@ -37,8 +37,8 @@
 //
 // Marks.  Where a chunk has any, documents meet in it, and zero times a value that is not finite would pass from one to
 // another: P is masked by selection, K' by bits, and rows of V are looked through (by the warps of K') and cleared,
-// with NaN in P and K' in their place.  Documents of 300 tokens on average: the first case 170 us (139 without the look at V, which waits for
-// V's one place) and gradient 511.
+// with NaN in P and K' in their place.  Documents of 300 tokens on average: the first case 168 us (139 without the look at V, which waits for
+// V's one place) and gradient 508, heads of 64 186 and 551.
 //
 // Without marks a value that is not finite meets P's zeros in the rows in front of it: the warps of o look whether P V is finite
 // and take such rows again (take_again).  Without ever being run this costs up to 3 % (54 heads of 64 127 us -> 131, 27 of 128 none); as a
