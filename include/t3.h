@@ -436,7 +436,7 @@ int t3_gated_scan_bwd(const void* gate, int64_t ldg, const void* cand, int64_t l
  * bf16 rows of more than 16 tokens whose bases, strides and heads are whole 16-byte pieces run on the tensor cores,
  * 128 tokens at a time: products inside such a chunk and the state it begins with are rounded to bf16 where they meet
  * q and v (o is off by about a rounding more than its own), what is added to the state is not (2^-17 of each
- * term).  A caller who wants both in float precision from bf16 rows hands them over as floats.  A value of q, k or v that is not finite shows in the outputs that the recurrence takes it to, in none
+ * term; state_last is off by some 2.5e-6 of itself).  A caller who wants both in float precision from bf16 rows hands them over as floats.  A value of q, k or v that is not finite shows in the outputs that the recurrence takes it to, in none
  * in front of it (for the gradient's passes against time, behind it) and on no path beyond a reset; in 128 tokens with a reset among them
  * it spoils all columns of its token's outputs and of the state, not its own alone.
  * Everything else is float, token by token.
